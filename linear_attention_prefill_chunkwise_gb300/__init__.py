@@ -1,10 +1,13 @@
-"""GB300 (sm_103a) Lightning Attention chunkwise prefill and speculative-decoding ops.
+"""GB300 (sm_103a) Lightning Attention chunkwise prefill and speculative-decoding ops, and the
+gated linear recurrence and RMS norm beside them.
 
 ``la_prefill_fwd`` (include/la_prefill.h), ``la_prefill_bwd`` (include/la_backward.h),
 ``la_prefill_fwd_segmented``,
 ``la_prefill_fwd_segmented_static`` and ``la_prefill_segmented_workspace``
 (include/la_segment.h) and ``la_decode_mtp``,
-``la_verify``, ``la_commit`` (include/la_decode.h) are thin ctypes bindings of the C
+``la_verify``, ``la_commit`` (include/la_decode.h), ``la_gated_scan_fwd``, ``la_gated_scan_bwd``,
+``la_gated_decode``, ``la_gated_verify``, ``la_gated_commit`` (include/la_gated.h) and
+``la_rms_norm_fwd``, ``la_rms_norm_fwd_fp8``, ``la_rms_norm_bwd`` (include/la_norm.h) are thin ctypes bindings of the C
 entry points of the same names: they check dtypes and shapes of torch tensors, pass their device
 pointers and the current CUDA stream, and raise on a non-OK status.  Every step of the
 computation runs in the library's CUDA kernels; there is no other implementation in
@@ -13,6 +16,7 @@ this package and no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -21,7 +25,10 @@ from . import build as _build
 __all__ = ["la_prefill_fwd", "la_prefill_fwd_segmented", "la_prefill_fwd_segmented_static", "la_prefill_bwd",
            "la_prefill_bwd_workspace", "la_prefill_fwd_d256", "la_prefill_d256_workspace",
            "la_prefill_fwd_d256_segmented", "la_prefill_d256_segmented_workspace",
-           "la_prefill_segmented_workspace", "la_decode_mtp", "la_verify", "la_commit", "LaError", "load_library", "SCHEDULES", "DEV_ERR_BAD_SEQLENS",
+           "la_prefill_segmented_workspace", "la_decode_mtp", "la_verify", "la_commit",
+           "la_gated_scan_fwd", "la_gated_scan_bwd", "la_gated_scan_workspace", "la_gated_decode", "la_gated_verify",
+           "la_gated_commit", "la_rms_norm_fwd", "la_rms_norm_fwd_fp8", "la_rms_norm_bwd", "la_rms_norm_bwd_workspace",
+           "LaError", "load_library", "SCHEDULES", "DEV_ERR_BAD_SEQLENS",
            "DEV_ERR_BAD_INDEX", "DEV_ERR_TIMEOUT", "EXPORTED_SYMBOLS"]
 
 SCHEDULES = {"auto": 0, "persistent": 1, "non_persistent": 2}
@@ -33,7 +40,9 @@ EXPORTED_SYMBOLS = ("la_prefill_fwd", "la_status_string", "la_last_error", "la_p
                     "la_commit", "la_prefill_segmented_workspace", "la_prefill_fwd_segmented",
                     "la_prefill_fwd_segmented_static", "la_prefill_bwd_workspace", "la_prefill_bwd",
                     "la_prefill_d256_workspace", "la_prefill_fwd_d256", "la_prefill_d256_segmented_workspace",
-                    "la_prefill_fwd_d256_segmented")
+                    "la_prefill_fwd_d256_segmented", "la_gated_scan_workspace", "la_gated_scan_fwd", "la_gated_scan_bwd",
+                    "la_gated_decode", "la_gated_verify", "la_gated_commit", "la_rms_norm_fwd", "la_rms_norm_fwd_fp8",
+                    "la_rms_norm_bwd_workspace", "la_rms_norm_bwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -99,6 +108,22 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
             lib.la_prefill_fwd_d256_segmented.argtypes = [vp, vp, vp, fp, ctypes.c_float, fp, i32p, i32p, vp, fp] + \
                 [ctypes.c_int] * 9 + [vp, ctypes.c_size_t, vp, vp]
             lib.la_prefill_fwd_d256_segmented.restype = ctypes.c_int
+            i64, i32 = ctypes.c_int64, ctypes.c_int
+            lib.la_gated_scan_workspace.argtypes = [i32] * 7 + [vp]
+            lib.la_gated_scan_fwd.argtypes = [vp] * 9 + [i64] * 4 + [i32] * 6 + [vp, ctypes.c_size_t, vp, vp]
+            lib.la_gated_scan_bwd.argtypes = [vp] * 15 + [i64] * 8 + [i32] * 6 + [vp, ctypes.c_size_t, vp, vp]
+            lib.la_gated_decode.argtypes = [vp] * 7 + [i64] * 4 + [i32] * 5 + [vp, vp]
+            lib.la_gated_verify.argtypes = [vp] * 7 + [i64] * 4 + [i32] * 5 + [vp, vp]
+            lib.la_gated_commit.argtypes = [vp] * 7 + [i64] * 3 + [i32] * 5 + [vp, vp]
+            lib.la_rms_norm_fwd.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 2 + [i64] * 4 + [i32] * 3 + [vp]
+            lib.la_rms_norm_fwd_fp8.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 3 + [i64] * 4 + [i32] * 4 + [vp]
+            lib.la_rms_norm_bwd_workspace.argtypes = [i32] * 2 + [vp]
+            lib.la_rms_norm_bwd.argtypes = [vp] * 2 + [ctypes.c_float] + [vp] * 4 + [i64] * 4 + [i32] * 3 + \
+                [vp, ctypes.c_size_t, vp]
+            for fn in ("la_gated_scan_workspace", "la_gated_scan_fwd", "la_gated_scan_bwd", "la_gated_decode",
+                       "la_gated_verify", "la_gated_commit", "la_rms_norm_fwd", "la_rms_norm_fwd_fp8",
+                       "la_rms_norm_bwd_workspace", "la_rms_norm_bwd"):
+                getattr(lib, fn).restype = ctypes.c_int
             _lib = lib
         return _lib
 
@@ -471,6 +496,354 @@ def la_commit(state, kbuf, vbuf, accepted_len, slopes, state_indices=None, dev_e
     _raise(lib, lib.la_commit(_ptr(state), _ptr(state_indices), _ptr(kbuf), _ptr(vbuf), _ptr(accepted_len),
                               _ptr(slopes), B, T, H, HV, D, V, P, _ptr(dev_error), ctypes.c_void_p(stream)))
     return state
+
+
+# ---- rows of channels: the gated recurrence (include/la_gated.h) and the RMS norm (include/la_norm.h)
+
+def _matrix(t, name):
+    """Checks of a call's leading activation matrix; returns (la_dtype, rows, C, row stride)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is torch.bfloat16:
+        code = 0
+    elif t.dtype is torch.float32:
+        code = 1
+    else:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    rows, C = t.shape
+    if C < 1:
+        raise ValueError(f"{name} must have at least one column")
+    return code, rows, C, _row_stride(t, name, rows, C)
+
+
+def _row_stride(t, name, rows, C):
+    s0, s1 = t.stride()
+    if s1 != 1 and C > 1 and rows > 0:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    if rows <= 1:
+        return C
+    if s0 < C:
+        raise ValueError(f"the row stride of {name} must be at least its {C} columns, got {s0}")
+    return s0
+
+
+def _rows_like(t, name, like, dtype=None):
+    """Checks a matrix of the leading one's shape, type and device; returns its row stride."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not (dtype or like.dtype):
+        raise TypeError(f"{name} must be {dtype or like.dtype}, got {t.dtype}")
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return _row_stride(t, name, *t.shape)
+
+
+def _on_device(t, name, dtype, shape, like):
+    """Checks an optional contiguous tensor; a None in ``shape`` stands for any size."""
+    if t is None:
+        return
+    _check(t, name, dtype, len(shape))
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    for have, want in zip(t.shape, shape):
+        if want is not None and have != want:
+            raise ValueError(f"{name} must have shape {['any' if w is None else w for w in shape]}, "
+                             f"got {tuple(t.shape)}")
+
+
+def _empty(shape, dtype, like, stream):
+    """A new tensor whose memory belongs to the stream that the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream, like), device=like.device)):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _stream(stream, like):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(like.device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _call(fn, like, *args):
+    """Call a C entry point with ``like``'s device current; raise on a non-OK status."""
+    import torch
+    if like.device.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(like.device):
+            st = fn(*args)
+    if st != 0:
+        _raise(load_library(), st)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _gated_sequences(x, state_indices, cu_seqlens, seq_len, pools):
+    """Batch mode of a gated scan; returns (B, T, N, pool size)."""
+    import torch
+    tokens, C = x.shape
+    if cu_seqlens is not None:
+        _on_device(cu_seqlens, "cu_seqlens", torch.int32, (None,), x)
+        N = cu_seqlens.shape[0] - 1
+        if N < 0:
+            raise ValueError("cu_seqlens must have N + 1 entries")
+        B, T = 1, tokens
+    else:
+        if seq_len is None:
+            raise ValueError("fixed-length mode needs seq_len")
+        T = int(seq_len)
+        if T < 1:
+            raise ValueError("seq_len must be positive in fixed-length mode")
+        if tokens % T:
+            raise ValueError("tokens must be a multiple of seq_len")
+        B = N = tokens // T
+    pool = None
+    for t, name in pools:
+        if t is not None:
+            _on_device(t, name, torch.float32, (pool, C), x)
+            pool = t.shape[0]
+    _on_device(state_indices, "state_indices", torch.int32, (N,), x)
+    return B, T, N, pool or 0
+
+
+@functools.lru_cache(maxsize=1024)
+def la_gated_scan_workspace(B, T, N, C, packed, dtype, backward):
+    """Bytes of device workspace la_gated_scan_fwd / la_gated_scan_bwd (``backward``) needs for
+    these sizes; dtype is torch.bfloat16 or torch.float32."""
+    import torch
+    lib = load_library()
+    nbytes = ctypes.c_size_t(0)
+    st = lib.la_gated_scan_workspace(int(B), int(T), int(N), int(C), int(bool(packed)),
+                                     {torch.bfloat16: 0, torch.float32: 1}[dtype], int(bool(backward)),
+                                     ctypes.byref(nbytes))
+    if st != 0:
+        _raise(lib, st)
+    return nbytes.value
+
+
+def _scan_workspace(workspace, x, B, T, N, C, packed, backward, stream):
+    import torch
+    if workspace is None:
+        nbytes = la_gated_scan_workspace(B, T, N, C, packed, x.dtype, backward)
+        return (None, 0) if nbytes == 0 else (_empty((nbytes,), torch.uint8, x, stream), nbytes)
+    _on_device(workspace, "workspace", torch.uint8, (None,), x)
+    return workspace, workspace.numel()
+
+
+def la_gated_scan_fwd(x, r, g, slopes, h0=None, state_indices=None, cu_seqlens=None, o=None, h_final=None,
+                      seq_len=None, workspace=None, dev_error=None, stream=None):
+    """Gated linear recurrence over every sequence: with u = slopes * sigmoid(r),
+    h_t = exp(-u_t) h_{t-1} + sqrt(1 - exp(-2 u_t)) sigmoid(g_t) x_t and o_t = h_t.
+
+    x, r, g: bf16 or fp32 [tokens, C], columns contiguous, any row stride (column ranges of one
+    projection's output work in place); slopes: fp32 [C]; h0 / h_final: fp32 [P, C] or None
+    (h_final may be h0); state_indices: int32 [N] or None (negative = padded sequence);
+    cu_seqlens: int32 [N + 1] or None (then ``seq_len`` tokens per sequence).  ``o`` is allocated
+    when not given; rows of padded sequences are not written.  ``workspace``: CUDA uint8, at least
+    la_gated_scan_workspace(...) bytes, allocated here when None.  Returns ``o``."""
+    import torch
+    lib = load_library()
+    code, tokens, C, ldx = _matrix(x, "x")
+    ldr, ldg = _rows_like(r, "r", x), _rows_like(g, "g", x)
+    _on_device(slopes, "slopes", torch.float32, (C,), x)
+    B, T, N, pool = _gated_sequences(x, state_indices, cu_seqlens, seq_len, ((h0, "h0"), (h_final, "h_final")))
+    if o is None:
+        o = _empty((tokens, C), x.dtype, x, stream)
+    ldo = _rows_like(o, "o", x)
+    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
+    workspace, nbytes = _scan_workspace(workspace, x, B, T, N, C, cu_seqlens is not None, False, stream)
+    _call(lib.la_gated_scan_fwd, x, x.data_ptr(), r.data_ptr(), g.data_ptr(), _p(slopes), _p(h0), _p(state_indices),
+          _p(cu_seqlens), o.data_ptr(), _p(h_final), ldx, ldr, ldg, ldo, B, T, N, C, pool, code, _p(workspace), nbytes,
+          _p(dev_error), _stream(stream, x))
+    return o
+
+
+def la_gated_scan_bwd(x, r, g, slopes, o, dout, h0=None, dh_final=None, state_indices=None, cu_seqlens=None, dx=None,
+                      dr=None, dg=None, dslopes=None, dh0=None, seq_len=None, workspace=None, dev_error=None,
+                      stream=None):
+    """Gradients of la_gated_scan_fwd: given its output ``o``, dout = dL/do and dh_final =
+    dL/dh_final (fp32 [P, C] or None), returns (dx, dr, dg, dslopes, dh0); dh0 (fp32 [P, C]) only
+    when a tensor is passed in.  dx, dr, dg may be column ranges of one matrix.  Rows of padded
+    sequences and unselected slots are not written.  The other arguments as la_gated_scan_fwd."""
+    import torch
+    lib = load_library()
+    code, tokens, C, ldx = _matrix(x, "x")
+    lds = [_rows_like(t, n, x) for t, n in ((r, "r"), (g, "g"), (o, "o"), (dout, "dout"))]
+    _on_device(slopes, "slopes", torch.float32, (C,), x)
+    B, T, N, pool = _gated_sequences(x, state_indices, cu_seqlens, seq_len,
+                                     ((h0, "h0"), (dh_final, "dh_final"), (dh0, "dh0")))
+    dx, dr, dg = (_empty((tokens, C), x.dtype, x, stream) if t is None else t for t in (dx, dr, dg))
+    lds += [_rows_like(t, n, x) for t, n in ((dx, "dx"), (dr, "dr"), (dg, "dg"))]
+    if dslopes is None:
+        dslopes = _empty((C,), torch.float32, x, stream)
+    _on_device(dslopes, "dslopes", torch.float32, (C,), x)
+    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
+    workspace, nbytes = _scan_workspace(workspace, x, B, T, N, C, cu_seqlens is not None, True, stream)
+    _call(lib.la_gated_scan_bwd, x, x.data_ptr(), r.data_ptr(), g.data_ptr(), _p(slopes), _p(h0), o.data_ptr(),
+          dout.data_ptr(), _p(dh_final), _p(state_indices), _p(cu_seqlens), dx.data_ptr(), dr.data_ptr(),
+          dg.data_ptr(), dslopes.data_ptr(), _p(dh0), ldx, *lds, B, T, N, C, pool, code, _p(workspace), nbytes,
+          _p(dev_error), _stream(stream, x))
+    return dx, dr, dg, dslopes, dh0
+
+
+def _gated_requests(x, r, g, slopes, state, T, state_indices, dev_error):
+    """Checks shared by the gated speculative-decoding ops; returns (code, B, C, ldx, ldr, ldg, P)."""
+    import torch
+    code, tokens, C, ldx = _matrix(x, "x")
+    ldr, ldg = _rows_like(r, "r", x), _rows_like(g, "g", x)
+    if T < 1 or tokens % T:
+        raise ValueError("T must be >= 1 and x must have B*T rows")
+    B = tokens // T
+    _on_device(slopes, "slopes", torch.float32, (C,), x)
+    if state is None:
+        raise TypeError("state must be a torch.Tensor")
+    _on_device(state, "state", torch.float32, (None, C), x)
+    _on_device(state_indices, "state_indices", torch.int32, (B,), x)
+    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
+    return code, B, C, ldx, ldr, ldg, state.shape[0]
+
+
+def _gated_outputs(fn, x, r, g, slopes, state, T, state_indices, o, dev_error, stream):
+    T = int(T)
+    code, B, C, ldx, ldr, ldg, P = _gated_requests(x, r, g, slopes, state, T, state_indices, dev_error)
+    if o is None:
+        o = _empty(x.shape, x.dtype, x, stream)
+    ldo = _rows_like(o, "o", x)
+    _call(fn, x, x.data_ptr(), r.data_ptr(), g.data_ptr(), _p(slopes), state.data_ptr(), _p(state_indices),
+          o.data_ptr(), ldx, ldr, ldg, ldo, B, T, C, P, code, _p(dev_error), _stream(stream, x))
+    return o
+
+
+def la_gated_decode(x, r, g, slopes, state, T, state_indices=None, o=None, dev_error=None, stream=None):
+    """Gated recurrence over each request's T tokens (x, r, g [B*T, C]) from its pooled state
+    (fp32 [P, C]), which advances in place.  Returns the outputs o (x's type)."""
+    return _gated_outputs(load_library().la_gated_decode, x, r, g, slopes, state, T, state_indices, o, dev_error,
+                          stream)
+
+
+def la_gated_verify(x, r, g, slopes, state, T, state_indices=None, o=None, dev_error=None, stream=None):
+    """la_gated_decode's outputs (bitwise), the pooled states left untouched."""
+    return _gated_outputs(load_library().la_gated_verify, x, r, g, slopes, state, T, state_indices, o, dev_error,
+                          stream)
+
+
+def la_gated_commit(x, r, g, slopes, state, T, accepted_len, state_indices=None, dev_error=None, stream=None):
+    """Advance each request's pooled state (in place) over the first accepted_len (int32 [B]) of
+    its T tokens; 0 = untouched, T = bitwise what la_gated_decode leaves.  Returns ``state``."""
+    import torch
+    T = int(T)
+    code, B, C, ldx, ldr, ldg, P = _gated_requests(x, r, g, slopes, state, T, state_indices, dev_error)
+    if accepted_len is None:
+        raise TypeError("accepted_len must be a torch.Tensor")
+    _on_device(accepted_len, "accepted_len", torch.int32, (B,), x)
+    _call(load_library().la_gated_commit, x, x.data_ptr(), r.data_ptr(), g.data_ptr(), _p(slopes), state.data_ptr(),
+          _p(state_indices), accepted_len.data_ptr(), ldx, ldr, ldg, B, T, C, P, code, _p(dev_error),
+          _stream(stream, x))
+    return state
+
+
+def _norm_inputs(x, weight, residual, residual_out, stream):
+    """Checks shared by the norm's forwards; returns (code, rows, C, residual_out, ldx, ldres, ldres_out)."""
+    import torch
+    code, rows, C, ldx = _matrix(x, "x")
+    _on_device(weight, "weight", torch.float32, (C,), x)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return code, rows, C, None, ldx, 0, 0
+    ldres = _rows_like(residual, "residual", x)
+    if residual_out is None:
+        residual_out = _empty((rows, C), x.dtype, x, stream)
+    return code, rows, C, residual_out, ldx, ldres, _rows_like(residual_out, "residual_out", x)
+
+
+def la_rms_norm_fwd(x, weight, eps, residual=None, y=None, residual_out=None, stream=None):
+    """RMS norm of s = x + residual over the columns: y = s / sqrt(mean(s^2) + eps) * weight.
+
+    x, residual, y, residual_out: bf16 or fp32 [rows, C] (C <= 16384), columns contiguous, any row
+    stride; weight: fp32 [C].  residual_out receives s rounded to x's type and may be the residual
+    itself.  Returns (y, residual_out); residual_out is None without a residual."""
+    lib = load_library()
+    code, rows, C, residual_out, ldx, ldres, ldro = _norm_inputs(x, weight, residual, residual_out, stream)
+    if y is None:
+        y = _empty((rows, C), x.dtype, x, stream)
+    ldy = _rows_like(y, "y", x)
+    _call(lib.la_rms_norm_fwd, x, x.data_ptr(), _p(residual), _p(weight), eps, y.data_ptr(), _p(residual_out), ldx,
+          ldres, ldy, ldro, rows, C, code, _stream(stream, x))
+    return y, residual_out
+
+
+def la_rms_norm_fwd_fp8(x, weight, eps, residual=None, group=0, y=None, scales=None, residual_out=None, stream=None):
+    """la_rms_norm_fwd with an 8-bit output: y (torch.float8_e4m3fn [rows, C]) and FP32 scales, the
+    norm's value being y * scale; one scale per row (group = 0: scales [rows, 1]) or per 128
+    columns (group = 128: scales [rows, ceil(C / 128)]).  Returns (y, scales, residual_out)."""
+    import torch
+    lib = load_library()
+    code, rows, C, residual_out, ldx, ldres, ldro = _norm_inputs(x, weight, residual, residual_out, stream)
+    if group not in (0, 128):
+        raise ValueError(f"group must be 0 or 128, got {group}")
+    if y is None:
+        y = _empty((rows, C), torch.float8_e4m3fn, x, stream)
+    ldy = _rows_like(y, "y", x, torch.float8_e4m3fn)
+    groups = -(-C // 128) if group else 1
+    if scales is None:
+        scales = _empty((rows, groups), torch.float32, x, stream)
+    _on_device(scales, "scales", torch.float32, (rows, groups), x)
+    _call(lib.la_rms_norm_fwd_fp8, x, x.data_ptr(), _p(residual), _p(weight), eps, y.data_ptr(), _p(scales),
+          _p(residual_out), ldx, ldres, ldy, ldro, rows, C, group, code, _stream(stream, x))
+    return y, scales, residual_out
+
+
+@functools.lru_cache(maxsize=1024)
+def la_rms_norm_bwd_workspace(rows, C):
+    """Bytes of device workspace la_rms_norm_bwd needs for these sizes."""
+    lib = load_library()
+    nbytes = ctypes.c_size_t(0)
+    st = lib.la_rms_norm_bwd_workspace(int(rows), int(C), ctypes.byref(nbytes))
+    if st != 0:
+        _raise(lib, st)
+    return nbytes.value
+
+
+def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradients of the norm of s (la_rms_norm_fwd's residual_out, or its x without a residual):
+    given dy = dL/dy and dres (the gradient reaching residual_out from later layers, or None),
+    returns (dx, dweight); dx is dL/dx and dL/dresidual alike, dweight fp32 [C].  ``workspace``:
+    CUDA uint8, at least la_rms_norm_bwd_workspace(...) bytes, allocated here when None."""
+    import torch
+    lib = load_library()
+    code, rows, C, lds = _matrix(s, "s")
+    _on_device(weight, "weight", torch.float32, (C,), s)
+    lddy = _rows_like(dy, "dy", s)
+    lddres = 0 if dres is None else _rows_like(dres, "dres", s)
+    if dx is None:
+        dx = _empty((rows, C), s.dtype, s, stream)
+    lddx = _rows_like(dx, "dx", s)
+    if dweight is None:
+        dweight = _empty((C,), torch.float32, s, stream)
+    _on_device(dweight, "dweight", torch.float32, (C,), s)
+    if workspace is None:
+        nbytes = la_rms_norm_bwd_workspace(rows, C)
+        workspace = _empty((nbytes,), torch.uint8, s, stream) if nbytes else None
+    else:
+        _on_device(workspace, "workspace", torch.uint8, (None,), s)
+        nbytes = workspace.numel()
+    _call(lib.la_rms_norm_bwd, s, s.data_ptr(), _p(weight), eps, dy.data_ptr(), _p(dres), dx.data_ptr(),
+          dweight.data_ptr(), lds, lddy, lddres, lddx, rows, C, code, _p(workspace), nbytes, _stream(stream, s))
+    return dx, dweight
 
 
 def la_prefill_fwd_raw(*args):
