@@ -17,18 +17,45 @@ using la_host::RowSpan;
 
 la_host::DeviceState g_dev[la_host::kMaxDevices];
 
-// The device workspace of a scan: the result of the cu_seqlens check, and for the gradients one
-// row of partial sums of dslopes per sequence.
-struct Workspace {
-  size_t flag, part, bytes;
+// How a scan is cut, and its device workspace: the ticket, the sequences of each tile (packed),
+// the published runs and states, and for the gradients one row of partial sums of dslopes per tile.
+struct Plan {
+  int tiles = 0, columns = 0, stride = 0, group = 0;
+  bool waits = false;  // tickets and published states are needed
+  size_t first_seq = 0, runs = 0, words = 0, before = 0, part = 0, bytes = 0;
 };
 
-Workspace workspace_of(int N, int C, bool packed, bool backward) {
-  Workspace w{};
-  if (packed) w.bytes += 256;
-  w.part = w.bytes;
-  if (backward) w.bytes += la_host::align256(static_cast<size_t>(N) * C * sizeof(float));
-  return w;
+// Tiles of a group: each composes half a group of published runs on average, and a scan is a
+// chain of one step per group.
+constexpr int kGroup = 16;
+
+Plan plan_of(int B, int T, int N, int C, bool packed, la_dtype dtype, bool backward) {
+  Plan q;
+  if (N == 0) return q;
+  const int most = dtype == LA_DTYPE_BF16
+                       ? (backward ? lag::tile_rows<__nv_bfloat16, true>() : lag::tile_rows<__nv_bfloat16, false>())
+                       : (backward ? lag::tile_rows<float, true>() : lag::tile_rows<float, false>());
+  const int64_t rows = static_cast<int64_t>(B) * T;
+  // short sequences of one length: tiles of whole sequences wait for nothing
+  const bool whole = !packed && T > 0 && T <= most;
+  q.stride = whole ? most / T * T : most;
+  q.waits = !whole;
+  q.tiles = static_cast<int>((rows + q.stride - 1) / q.stride);
+  if (q.tiles == 0) q.tiles = 1;  // empty sequences alone
+  q.columns = (C + lag::kCols - 1) / lag::kCols;
+  q.group = kGroup;
+  if (q.waits) {
+    const size_t width = static_cast<size_t>(q.columns) * lag::kCols;
+    const size_t groups = (q.tiles + q.group - 1) / q.group;
+    q.first_seq = 256;
+    q.runs = q.first_seq + (packed ? la_host::align256((static_cast<size_t>(q.tiles) + 1) * 4) : 0);
+    q.before = q.runs + q.tiles * width * 8;
+    q.words = q.tiles * width * 2 + groups * width;
+    q.bytes = q.runs + q.words * 4;
+  }
+  q.part = q.bytes;
+  if (backward) q.bytes += la_host::align256(static_cast<size_t>(q.tiles) * C * 4);
+  return q;
 }
 
 la_status check_sizes(int B, int T, int N, int C, bool packed, la_dtype dtype) {
@@ -42,6 +69,9 @@ la_status check_sizes(int B, int T, int N, int C, bool packed, la_dtype dtype) {
   }
   if (static_cast<int64_t>(B) * T > la_host::kMaxRows)
     return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)B * T);
+  // tiles of at least 32 rows and 64 channels, numbered below 2^30 (more than any memory holds)
+  if ((static_cast<int64_t>(B) * T / 32 + 1) * ((C + 63) / 64) >= int64_t(1) << 30)
+    return fail(LA_ERR_UNSUPPORTED, "B*T*C too large");
   if (static_cast<int64_t>(N) * ((C + 63) / 64) > INT32_MAX) return fail(LA_ERR_UNSUPPORTED, "N*C too large");
   return LA_OK;
 }
@@ -66,30 +96,53 @@ la_status device(la_host::DeviceState** ds) {
   return la_host::current_device(g_dev, ds, [] { return cudaSuccess; });
 }
 
-la_status launched() {
-  const cudaError_t ce = cudaGetLastError();
+template <typename E>
+void set_plan(lag::Params<E>* p, const Plan& q, void* workspace) {
+  char* ws = static_cast<char*>(workspace);
+  p->tiles = q.tiles;
+  p->columns = q.columns;
+  p->stride = q.stride;
+  p->group = q.group;
+  if (q.waits) {
+    p->ticket = reinterpret_cast<int*>(ws);
+    p->first_seq = reinterpret_cast<int32_t*>(ws + q.first_seq);
+    p->runs = reinterpret_cast<float2*>(ws + q.runs);
+    p->before = reinterpret_cast<float*>(ws + q.before);
+  }
+  p->part = reinterpret_cast<float*>(ws + q.part);
+}
+
+// Whether a lane may load two neighbouring elements at once from rows of this stride.
+template <typename E>
+bool paired(const void* p, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % (2 * sizeof(E)) == 0 && ld % 2 == 0;
+}
+
+template <typename E>
+cudaError_t launch_plan(const lag::Params<E>& p, const Plan& q, int sms, cudaStream_t s) {
+  const size_t want = (q.words / 4 + lag::kThreads - 1) / lag::kThreads;
+  const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want < size_t(sms) * 8 ? want : size_t(sms) * 8);
+  return la_host::launch_pdl(lag::scan_plan_kernel<E>, grid, lag::kThreads, 0, s, p, q.words);
+}
+
+template <typename E>
+la_status launch_scan(const lag::Params<E>& p, const Plan& q, bool backward, float* dslopes, int sms, cudaStream_t s) {
+  cudaError_t ce = q.waits ? launch_plan(p, q, sms, s) : cudaSuccess;
+  const unsigned grid = static_cast<unsigned>(q.tiles) * q.columns;
+  const bool pair = p.C % 2 == 0 && paired<E>(p.x, p.ldx) && paired<E>(p.r, p.ldr) && paired<E>(p.g, p.ldg) &&
+                    (backward ? paired<E>(p.o_in, p.ldo) && paired<E>(p.dout, p.lddout) && paired<E>(p.dx, p.lddx) &&
+                                    paired<E>(p.dr, p.lddr) && paired<E>(p.dg, p.lddg)
+                              : paired<E>(p.o, p.ldo));
+  if (ce == cudaSuccess && q.tiles > 0) {
+    auto kernel = backward ? (pair ? lag::gated_scan_bwd_kernel<E, true> : lag::gated_scan_bwd_kernel<E, false>)
+                           : (pair ? lag::gated_scan_fwd_kernel<E, true> : lag::gated_scan_fwd_kernel<E, false>);
+    ce = la_host::launch_pdl(kernel, grid, lag::kScanThreads, 0, s, p);
+  }
+  if (ce == cudaSuccess && backward)
+    ce = la_host::launch_pdl(lag::column_sum_kernel, (p.C + 31) / 32, 1024, 0, s, static_cast<const float*>(p.part),
+                             q.tiles, p.C, static_cast<const int*>(p.cu_seqlens ? p.ticket : nullptr), dslopes);
+  if (ce == cudaSuccess) ce = cudaGetLastError();
   return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
-}
-
-unsigned grid_of(int N, int C) { return static_cast<unsigned>(N) * ((C + lag::kThreads - 1) / lag::kThreads); }
-
-template <typename E>
-la_status launch_fwd(const lag::Params<E>& p, bool decode, int* flag, cudaStream_t s) {
-  if (p.cu_seqlens) lag::check_seqlens_kernel<<<1, 256, 0, s>>>(p.cu_seqlens, p.N, p.T, flag, p.dev_error);
-  if (decode)
-    lag::gated_fwd_kernel<E, true><<<grid_of(p.N, p.C), lag::kThreads, 0, s>>>(p);
-  else
-    lag::gated_fwd_kernel<E, false><<<grid_of(p.N, p.C), lag::kThreads, 0, s>>>(p);
-  return launched();
-}
-
-template <typename E>
-la_status launch_bwd(const lag::Params<E>& p, int* flag, cudaStream_t s) {
-  if (p.cu_seqlens) lag::check_seqlens_kernel<<<1, 256, 0, s>>>(p.cu_seqlens, p.N, p.T, flag, p.dev_error);
-  if (p.N > 0) lag::gated_bwd_kernel<E><<<grid_of(p.N, p.C), lag::kThreads, 0, s>>>(p);
-  lag::column_sum_kernel<<<(p.C + lag::kThreads - 1) / lag::kThreads, lag::kThreads, 0, s>>>(p.part, p.N, p.C, p.bad,
-                                                                                             p.dslopes);
-  return launched();
 }
 
 template <typename E>
@@ -149,7 +202,11 @@ la_status decode_call(const void* x, const void* r, const void* g, const float* 
     p.start = state;
     p.finish = state_out;
     p.accepted_len = accepted_len;
-    return launch_fwd<E>(p, true, nullptr, static_cast<cudaStream_t>(stream));
+    const unsigned grid = static_cast<unsigned>(B) * ((C + lag::kThreads - 1) / lag::kThreads);
+    cudaError_t ce = la_host::launch_pdl(lag::gated_decode_kernel<E>, grid, lag::kThreads, 0,
+                                         static_cast<cudaStream_t>(stream), p);
+    if (ce == cudaSuccess) ce = cudaGetLastError();
+    return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
   };
   return dtype == LA_DTYPE_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }
@@ -164,7 +221,7 @@ la_status la_gated_scan_workspace(int B, int T, int N, int C, int packed, la_dty
   if (!bytes) return fail(LA_ERR_INVALID_ARGUMENT, "bytes is null");
   const la_status st = check_sizes(B, T, N, C, packed != 0, dtype);
   if (st != LA_OK) return st;
-  *bytes = workspace_of(N, C, packed != 0, backward != 0).bytes;
+  *bytes = plan_of(B, T, N, C, packed != 0, dtype, backward != 0).bytes;
   return LA_OK;
 }
 
@@ -181,7 +238,7 @@ la_status la_gated_scan_fwd(const void* x, const void* r, const void* g, const f
   const uint64_t es = la_host::element_size(dtype), rows = static_cast<uint64_t>(B) * T;
   if (!slopes || (rows > 0 && (!x || !r || !g || !o)))
     return fail(LA_ERR_INVALID_ARGUMENT, "x, r, g, slopes and o must be non-null");
-  const Workspace w = workspace_of(N, C, cu_seqlens != nullptr, false);
+  const Plan w = plan_of(B, T, N, C, cu_seqlens != nullptr, dtype, false);
   if ((st = la_host::check_workspace(workspace, workspace_bytes, w.bytes)) != LA_OK) return st;
   const RowSpan ins[] = {la_host::rows_of(x, ldx, rows, C, es, "x"),
                          la_host::rows_of(r, ldr, rows, C, es, "r"),
@@ -206,9 +263,9 @@ la_status la_gated_scan_fwd(const void* x, const void* r, const void* g, const f
     p.start = h0;
     p.finish = h_final;
     p.cu_seqlens = cu_seqlens;
-    int* flag = cu_seqlens ? reinterpret_cast<int*>(static_cast<char*>(workspace) + w.flag) : nullptr;
-    p.bad = flag;
-    return launch_fwd<E>(p, false, flag, static_cast<cudaStream_t>(stream));
+    p.rows = static_cast<int>(rows);
+    set_plan(&p, w, workspace);
+    return launch_scan<E>(p, w, false, nullptr, ds->sms, static_cast<cudaStream_t>(stream));
   };
   return dtype == LA_DTYPE_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }
@@ -227,7 +284,7 @@ la_status la_gated_scan_bwd(const void* x, const void* r, const void* g, const f
   const uint64_t es = la_host::element_size(dtype), rows = static_cast<uint64_t>(B) * T;
   if (!slopes || !dslopes || (rows > 0 && (!x || !r || !g || !o || !dout || !dx || !dr || !dg)))
     return fail(LA_ERR_INVALID_ARGUMENT, "x, r, g, slopes, o, dout, dx, dr, dg and dslopes must be non-null");
-  const Workspace w = workspace_of(N, C, cu_seqlens != nullptr, true);
+  const Plan w = plan_of(B, T, N, C, cu_seqlens != nullptr, dtype, true);
   if ((st = la_host::check_workspace(workspace, workspace_bytes, w.bytes)) != LA_OK) return st;
   const RowSpan ins[] = {la_host::rows_of(x, ldx, rows, C, es, "x"),
                          la_host::rows_of(r, ldr, rows, C, es, "r"),
@@ -266,13 +323,10 @@ la_status la_gated_scan_bwd(const void* x, const void* r, const void* g, const f
     p.start = dh_final;
     p.finish = dh0;
     p.h0 = h0;
-    p.dslopes = dslopes;
     p.cu_seqlens = cu_seqlens;
-    char* ws = static_cast<char*>(workspace);
-    p.part = reinterpret_cast<float*>(ws + w.part);
-    int* flag = cu_seqlens ? reinterpret_cast<int*>(ws + w.flag) : nullptr;
-    p.bad = flag;
-    return launch_bwd<E>(p, flag, static_cast<cudaStream_t>(stream));
+    p.rows = static_cast<int>(rows);
+    set_plan(&p, w, workspace);
+    return launch_scan<E>(p, w, true, dslopes, ds->sms, static_cast<cudaStream_t>(stream));
   };
   return dtype == LA_DTYPE_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }

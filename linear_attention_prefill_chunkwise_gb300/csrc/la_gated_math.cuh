@@ -85,7 +85,7 @@ __device__ __forceinline__ Decay decay_of(float u) {
 
 // The gradients of one token and channel, given G = dL/dh_t and h_prev = h_{t-1}.
 struct Grads {
-  float dx, dr, dg, ds;  // ds: the token's term of dslopes
+  float dx, dr, dg, ds, lambda;  // ds: the token's term of dslopes
 };
 
 template <bool kPrecise>
@@ -100,6 +100,7 @@ __device__ __forceinline__ Grads grads_of(float x, float r, float g, float slope
   const float du = d.lambda * (gs * x * (d.lambda * d.inv_beta) - G * h_prev);
   q.dr = du * u * (1.f - sr);
   q.ds = du * sr;
+  q.lambda = d.lambda;
   return q;
 }
 

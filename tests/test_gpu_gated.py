@@ -209,11 +209,17 @@ def test_in_place_pool_and_continuation(dtype):
 
 
 def test_closed_gates_keep_the_state():
-    """r = -inf keeps the state bit for bit and adds nothing; g = -inf adds nothing."""
+    """r = -inf keeps the state and adds nothing; g = -inf adds nothing.  The state is kept up to the
+    rounding of a blocked evaluation, which composes the rows before a tile in another order than
+    it walks them: each value is within its bound E of the exact one, two of them within 2 E."""
     b = Batch(5, lens=[400], C=96, packed=False, dtype="fp32")
     b.r[100:] = float("-inf")
     o, hf = b.fwd()
-    assert torch.equal(o[100:], o[99:100].expand(300, -1)) and torch.equal(hf[0], o[99])
+    ro, _, eo, _ = scan_one(f64(b.x), f64(b.r), f64(b.g), f64(b.slopes), b.start(0))
+    near(o, ro, eo, "fp32", "o under closed decay gates")
+    assert np.array_equal(ro[100:], np.tile(ro[99], (300, 1)))
+    assert np.all(np.abs(f64(o[100:]) - f64(o[99])) <= eo[100:] + eo[99] + 2.0 ** -23 * np.abs(ro[99]))
+    assert torch.equal(hf[0], o[399])
     b = Batch(6, lens=[400], C=96, packed=False)
     b.g[:] = float("-inf")
     b.r[:] = float("inf")
@@ -451,3 +457,19 @@ def test_decode_continues_a_scan():
     o2 = lap.la_gated_decode(b.x[tail], b.r[tail], b.g[tail], b.slopes, pool, 4, state_indices=b.idx)
     torch.testing.assert_close(o2, o[tail], rtol=2.0 ** -7, atol=1e-4)
     torch.testing.assert_close(pool[b.idx.long()], hf[b.idx.long()], rtol=1e-4, atol=1e-4)
+
+
+def test_fixed_length_zero_keeps_the_states():
+    """T == 0 through the C entry points: final states are the initial ones, gradients likewise."""
+    lib = lap.load_library()
+    h0, hf, dh0 = torch.randn(2, 70, device="cuda"), torch.empty(2, 70, device="cuda"), torch.empty(2, 70, device="cuda")
+    slopes, dsl = torch.ones(70, device="cuda"), torch.full((70,), float("nan"), device="cuda")
+    n = lap.la_gated_scan_workspace(2, 0, 2, 70, False, torch.bfloat16, True)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    assert lib.la_gated_scan_fwd(None, None, None, slopes.data_ptr(), h0.data_ptr(), None, None, None, hf.data_ptr(),
+                                 70, 70, 70, 70, 2, 0, 2, 70, 2, 0, ws.data_ptr(), n, None, s) == 0
+    assert lib.la_gated_scan_bwd(None, None, None, slopes.data_ptr(), None, None, None, h0.data_ptr(), None, None, None,
+                                 None, None, dsl.data_ptr(), dh0.data_ptr(), *[70] * 8, 2, 0, 2, 70, 2, 0, ws.data_ptr(),
+                                 n, None, s) == 0
+    assert torch.equal(hf, h0) and torch.equal(dh0, h0) and torch.equal(dsl, torch.zeros(70, device="cuda"))
