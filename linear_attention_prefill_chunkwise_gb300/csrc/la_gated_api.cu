@@ -32,9 +32,8 @@ constexpr int kGroup = 16;
 Plan plan_of(int B, int T, int N, int C, bool packed, la_dtype dtype, bool backward) {
   Plan q;
   if (N == 0) return q;
-  const int most = dtype == LA_DTYPE_BF16
-                       ? (backward ? lag::tile_rows<__nv_bfloat16, true>() : lag::tile_rows<__nv_bfloat16, false>())
-                       : (backward ? lag::tile_rows<float, true>() : lag::tile_rows<float, false>());
+  const int most = dtype == LA_DTYPE_BF16 ? lag::Shape<__nv_bfloat16, false, true>::kTileRows
+                                          : lag::Shape<float, false, true>::kTileRows;
   const int64_t rows = static_cast<int64_t>(B) * T;
   // short sequences of one length: tiles of whole sequences wait for nothing
   const bool whole = !packed && T > 0 && T <= most;
@@ -92,10 +91,6 @@ RowSpan pool_span(const void* p, const char* name, const int32_t* state_indices,
   return la_host::flat(p, static_cast<uint64_t>(state_indices ? pool_size : N) * C * 4, name);
 }
 
-la_status device(la_host::DeviceState** ds) {
-  return la_host::current_device(g_dev, ds, [] { return cudaSuccess; });
-}
-
 template <typename E>
 void set_plan(lag::Params<E>* p, const Plan& q, void* workspace) {
   char* ws = static_cast<char*>(workspace);
@@ -112,10 +107,30 @@ void set_plan(lag::Params<E>* p, const Plan& q, void* workspace) {
   p->part = reinterpret_cast<float*>(ws + q.part);
 }
 
-// Whether a lane may load two neighbouring elements at once from rows of this stride.
+// Whether rows of this stride can be read by TMA boxes / written two channels at a time.
 template <typename E>
-bool paired(const void* p, int64_t ld) {
+bool box_rows(const void* p, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * sizeof(E) % 16 == 0;
+}
+template <typename E>
+bool pair_rows(const void* p, int64_t ld) {
   return reinterpret_cast<uintptr_t>(p) % (2 * sizeof(E)) == 0 && ld % 2 == 0;
+}
+
+// Map over a [rows, C] matrix with its row stride: boxes of `box` rows x 64 channels, unswizzled.
+template <typename E>
+la_status encode_rows_map(CUtensorMap* map, const E* base, int64_t rows, int64_t C, int64_t ld, int box) {
+  auto enc = la_host::tensor_map_encoder();
+  if (!enc) return fail(LA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the CUDA driver");
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * sizeof(E)};
+  const cuuint32_t boxes[2] = {lag::kCols, static_cast<cuuint32_t>(box)}, steps[2] = {1, 1};
+  const CUresult r = enc(map, sizeof(E) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                         const_cast<E*>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(LA_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult %d", (int)r);
+  return LA_OK;
 }
 
 template <typename E>
@@ -125,24 +140,58 @@ cudaError_t launch_plan(const lag::Params<E>& p, const Plan& q, int sms, cudaStr
   return la_host::launch_pdl(lag::scan_plan_kernel<E>, grid, lag::kThreads, 0, s, p, q.words);
 }
 
-template <typename E>
-la_status launch_scan(const lag::Params<E>& p, const Plan& q, bool backward, float* dslopes, int sms, cudaStream_t s) {
-  cudaError_t ce = q.waits ? launch_plan(p, q, sms, s) : cudaSuccess;
-  const unsigned grid = static_cast<unsigned>(q.tiles) * q.columns;
-  const bool pair = p.C % 2 == 0 && paired<E>(p.x, p.ldx) && paired<E>(p.r, p.ldr) && paired<E>(p.g, p.ldg) &&
-                    (backward ? paired<E>(p.o_in, p.ldo) && paired<E>(p.dout, p.lddout) && paired<E>(p.dx, p.lddx) &&
-                                    paired<E>(p.dr, p.lddr) && paired<E>(p.dg, p.lddg)
-                              : paired<E>(p.o, p.ldo));
-  if (ce == cudaSuccess && q.tiles > 0) {
-    auto kernel = backward ? (pair ? lag::gated_scan_bwd_kernel<E, true> : lag::gated_scan_bwd_kernel<E, false>)
-                           : (pair ? lag::gated_scan_fwd_kernel<E, true> : lag::gated_scan_fwd_kernel<E, false>);
-    ce = la_host::launch_pdl(kernel, grid, lag::kScanThreads, 0, s, p);
+template <typename E, bool kBack, bool kTma>
+la_status launch_kernel(const lag::Params<E>& p, const Plan& q, int sms, cudaStream_t s) {
+  using S = lag::Shape<E, kBack, kTma>;
+  lag::Maps maps;
+  if constexpr (kTma) {
+    for (int i = 0; i < S::kInputs; ++i) {
+      const la_status st = encode_rows_map(&maps.of[i], p.in[i], p.rows, p.C, p.ld_in[i], S::kRows);
+      if (st != LA_OK) return st;
+    }
   }
-  if (ce == cudaSuccess && backward)
+  const int total = q.tiles * q.columns, most = sms * S::kBlocks;
+  const cudaError_t ce = la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma>, total < most ? total : most,
+                                             lag::kScanThreads, lag::scan_smem_bytes<E, kBack, kTma>(), s, p, maps);
+  return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
+}
+
+template <typename E, bool kBack>
+la_status launch_scan(const lag::Params<E>& p, const Plan& q, float* dslopes, int sms, cudaStream_t s) {
+  cudaError_t ce = q.waits ? launch_plan(p, q, sms, s) : cudaSuccess;
+  if (ce == cudaSuccess && q.tiles > 0) {
+    bool tma = p.rows > 0;
+    for (int i = 0; i < (kBack ? 5 : 3); ++i) tma = tma && box_rows<E>(p.in[i], p.ld_in[i]);
+    for (int i = 0; i < (kBack ? 3 : 1); ++i) tma = tma && p.C % 2 == 0 && pair_rows<E>(p.out[i], p.ld_out[i]);
+    const la_status st = tma ? launch_kernel<E, kBack, true>(p, q, sms, s) : launch_kernel<E, kBack, false>(p, q, sms, s);
+    if (st != LA_OK) return st;
+  }
+  if (ce == cudaSuccess && kBack)
     ce = la_host::launch_pdl(lag::column_sum_kernel, (p.C + 31) / 32, 1024, 0, s, static_cast<const float*>(p.part),
                              q.tiles, p.C, static_cast<const int*>(p.cu_seqlens ? p.ticket : nullptr), dslopes);
   if (ce == cudaSuccess) ce = cudaGetLastError();
   return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
+}
+
+// One-time setup per device: the stages of a scan exceed the default shared memory.
+template <typename E>
+cudaError_t setup_type() {
+  const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(lag::gated_scan_kernel<E, false, false>, attr, lag::scan_smem_bytes<E, false, false>());
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(lag::gated_scan_kernel<E, false, true>, attr, lag::scan_smem_bytes<E, false, true>());
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(lag::gated_scan_kernel<E, true, false>, attr, lag::scan_smem_bytes<E, true, false>());
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(lag::gated_scan_kernel<E, true, true>, attr, lag::scan_smem_bytes<E, true, true>());
+  return e;
+}
+
+la_status device(la_host::DeviceState** ds) {
+  return la_host::current_device(g_dev, ds, [] {
+    const cudaError_t e = setup_type<__nv_bfloat16>();
+    return e == cudaSuccess ? setup_type<float>() : e;
+  });
 }
 
 template <typename E>
@@ -150,13 +199,13 @@ lag::Params<E> params_of(const void* x, const void* r, const void* g, const floa
                          int64_t ldg, const int32_t* state_indices, int* dev_error, int T, int N, int C,
                          int pool_size) {
   lag::Params<E> p{};
-  p.x = static_cast<const E*>(x);
-  p.r = static_cast<const E*>(r);
-  p.g = static_cast<const E*>(g);
+  p.in[0] = static_cast<const E*>(x);
+  p.in[1] = static_cast<const E*>(r);
+  p.in[2] = static_cast<const E*>(g);
+  p.ld_in[0] = ldx;
+  p.ld_in[1] = ldr;
+  p.ld_in[2] = ldg;
   p.slopes = slopes;
-  p.ldx = ldx;
-  p.ldr = ldr;
-  p.ldg = ldg;
   p.state_indices = state_indices;
   p.dev_error = dev_error;
   p.T = T;
@@ -197,8 +246,8 @@ la_status decode_call(const void* x, const void* r, const void* g, const float* 
   auto run = [&](auto tag) {
     using E = decltype(tag);
     auto p = params_of<E>(x, r, g, slopes, ldx, ldr, ldg, state_indices, dev_error, T, B, C, pool_size);
-    p.o = static_cast<E*>(o);
-    p.ldo = ldo;
+    p.out[0] = static_cast<E*>(o);
+    p.ld_out[0] = ldo;
     p.start = state;
     p.finish = state_out;
     p.accepted_len = accepted_len;
@@ -258,14 +307,14 @@ la_status la_gated_scan_fwd(const void* x, const void* r, const void* g, const f
     using E = decltype(tag);
     auto p = params_of<E>(x, r, g, slopes, ldx, ldr, ldg, state_indices, dev_error, T, N, C,
                           la_host::effective_pool_size(h0, h_final, state_indices, pool_size, N));
-    p.o = static_cast<E*>(o);
-    p.ldo = ldo;
+    p.out[0] = static_cast<E*>(o);
+    p.ld_out[0] = ldo;
     p.start = h0;
     p.finish = h_final;
     p.cu_seqlens = cu_seqlens;
     p.rows = static_cast<int>(rows);
     set_plan(&p, w, workspace);
-    return launch_scan<E>(p, w, false, nullptr, ds->sms, static_cast<cudaStream_t>(stream));
+    return launch_scan<E, false>(p, w, nullptr, ds->sms, static_cast<cudaStream_t>(stream));
   };
   return dtype == LA_DTYPE_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }
@@ -310,23 +359,23 @@ la_status la_gated_scan_bwd(const void* x, const void* r, const void* g, const f
     using E = decltype(tag);
     const int pool = states ? pool_size : state_indices ? INT32_MAX : N;
     auto p = params_of<E>(x, r, g, slopes, ldx, ldr, ldg, state_indices, dev_error, T, N, C, pool);
-    p.o_in = static_cast<const E*>(o);
-    p.ldo = ldo;
-    p.dout = static_cast<const E*>(dout);
-    p.lddout = lddout;
-    p.dx = static_cast<E*>(dx);
-    p.lddx = lddx;
-    p.dr = static_cast<E*>(dr);
-    p.lddr = lddr;
-    p.dg = static_cast<E*>(dg);
-    p.lddg = lddg;
+    p.in[3] = static_cast<const E*>(dout);
+    p.in[4] = static_cast<const E*>(o);
+    p.ld_in[3] = lddout;
+    p.ld_in[4] = ldo;
+    p.out[0] = static_cast<E*>(dx);
+    p.out[1] = static_cast<E*>(dr);
+    p.out[2] = static_cast<E*>(dg);
+    p.ld_out[0] = lddx;
+    p.ld_out[1] = lddr;
+    p.ld_out[2] = lddg;
     p.start = dh_final;
     p.finish = dh0;
     p.h0 = h0;
     p.cu_seqlens = cu_seqlens;
     p.rows = static_cast<int>(rows);
     set_plan(&p, w, workspace);
-    return launch_scan<E>(p, w, true, dslopes, ds->sms, static_cast<cudaStream_t>(stream));
+    return launch_scan<E, true>(p, w, dslopes, ds->sms, static_cast<cudaStream_t>(stream));
   };
   return dtype == LA_DTYPE_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }

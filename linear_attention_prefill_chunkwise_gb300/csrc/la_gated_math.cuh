@@ -1,10 +1,12 @@
 // la_gated_math.cuh -- element arithmetic of the gated linear recurrence (include/la_gated.h),
 // shared by its scan, gradient and decode kernels: the gates, the decay and the input weight of
-// one token and channel, and the loads and stores of BF16 and FP32 activations.
+// one token, for one channel and for two at once.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cstdint>
+
+#include "sm103_ptx.cuh"
 
 namespace lag {
 
@@ -39,69 +41,78 @@ __device__ __forceinline__ float rsqrt_approx(float v) {
   return d;
 }
 
-// 1 / (1 + exp(-z)); 0 at -inf, 1 at +inf.
-template <bool kPrecise>
-__device__ __forceinline__ float sigmoid(float z) {
-  if constexpr (kPrecise) return 1.f / (1.f + expf(-z));
-  return rcp_approx(1.f + ex2_approx(-kLog2e * z));
-}
+// The hardware's exp2, reciprocal and rsqrt (each within 2^-22 relative) are arranged so that the
+// FP32 states keep FP32 accuracy over long memories.  With m = 1 - lambda:
+//   u < 1/8    m = u (1 + c1 u + c2 u^2 + c3 u^3), a polynomial fitted to (1 - e^-u) / u for the
+//              least relative error on [0, 1/8] (2e-8; evaluated in FP32: 1e-7).  Such a lambda
+//              is off by its own rounding alone, and it is here that 1 / m tokens add up its error.
+//   otherwise  m = 1 - exp2(-u log2 e), good to 2^-23 / m relative: 1e-6 at 1/8.
+// Then 1 - lambda^2 = m (2 - m) has no cancellation, and beta = w rsqrt(w) with w = 1 - lambda^2
+// (kept from rsqrt(0) by the smallest normal number; w = 0 gives beta = 0).
+constexpr float kNear = 0.125f;
+constexpr float kC1 = -0.4999971091747284f, kC2 = 0.16652604937553406f, kC3 = -0.039715882390737534f;
+constexpr float kLeast = 1.17549435e-38f;
 
-// What the recurrence and its gradient need of one decay gate: u = slope sig(r), lambda =
-// exp(-u), beta = sqrt(1 - lambda^2) and 1 / beta (0 where u = 0: the gradient's convention).
+// 1 / (1 + exp(-z)); 0 at -inf, 1 at +inf.
+__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + ex2_approx(-kLog2e * z)); }
+
 struct Decay {
-  float lambda, beta, inv_beta;
+  float lambda, beta;
 };
 
-// kPrecise (FP32 activations) calls the CUDA math functions.  Otherwise (BF16 activations, whose
-// own rounding is 2^-9 relative) the hardware approximations, arranged so that the FP32 states
-// keep FP32 accuracy over long memories: for u < 1/4, where 1 / (1 - lambda) tokens accumulate
-// lambda's error, 1 - lambda comes from its alternating series u - u^2/2! + ... - u^6/6! (the next
-// term is u^6 / 7! of the value, 4.8e-8 at u = 1/4), so that lambda is off by its own rounding alone and 1 - lambda^2 =
-// (1 - lambda)(1 + lambda) has no cancellation.
-template <bool kPrecise>
 __device__ __forceinline__ Decay decay_of(float u) {
-  Decay d;
-  if constexpr (kPrecise) {
-    d.lambda = expf(-u);
-    d.beta = sqrtf(-expm1f(-2.f * u));
-    d.inv_beta = u > 0.f ? 1.f / d.beta : 0.f;
-  } else {
-    float p = fmaf(u, -1.f / 720.f, 1.f / 120.f);
-    p = fmaf(u, -p, 1.f / 24.f);
-    p = fmaf(u, -p, 1.f / 6.f);
-    p = fmaf(u, -p, 0.5f);
-    p = fmaf(u, -p, 1.f);
-    const float near = u * p;                             // 1 - lambda
-    const float far = 1.f - ex2_approx(-kLog2e * u);
-    const float m = u < 0.25f ? near : far;
-    d.lambda = 1.f - m;
-    const float w = m * (2.f - m);                        // 1 - lambda^2
-    const float rs = rsqrt_approx(fmaxf(w, 1.17549435e-38f));
-    d.beta = w * rs;
-    d.inv_beta = u > 0.f ? rs : 0.f;
-  }
+  const float near = u * fmaf(u, fmaf(u, fmaf(u, kC3, kC2), kC1), 1.f);
+  const float far = 1.f - ex2_approx(-kLog2e * u);
+  const float m = u < kNear ? near : far;
+  const float w = m * (2.f - m);
+  return {1.f - m, w * rsqrt_approx(fmaxf(w, kLeast))};
+}
+
+// ---------------------------------------------------------------- two channels at once
+
+// Pairs of FP32 values in one 64-bit register pair: one instruction for two channels where the
+// operation is an add, a multiply or both.
+using lap::f2_fma;
+using lap::f2_mul;
+using lap::f2_pack;
+using lap::f2_sub;
+using lap::f2_unpack;
+typedef uint64_t f2;
+
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ f2 f2_all(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ f2 f2_of(float2 v) { return f2_pack(v.x, v.y); }
 
-// The gradients of one token and channel, given G = dL/dh_t and h_prev = h_{t-1}.
-struct Grads {
-  float dx, dr, dg, ds, lambda;  // ds: the token's term of dslopes
-};
+template <typename F>
+__device__ __forceinline__ f2 f2_each(f2 v, F f) {
+  const float2 t = f2_unpack(v);
+  return f2_pack(f(t.x), f(t.y));
+}
 
-template <bool kPrecise>
-__device__ __forceinline__ Grads grads_of(float x, float r, float g, float slope, float G, float h_prev) {
-  const float sr = sigmoid<kPrecise>(r), sg = sigmoid<kPrecise>(g);
-  const float u = slope * sr;
-  const Decay d = decay_of<kPrecise>(u);
-  Grads q;
-  const float gs = G * sg;
-  q.dx = gs * d.beta;
-  q.dg = q.dx * x * (1.f - sg);
-  const float du = d.lambda * (gs * x * (d.lambda * d.inv_beta) - G * h_prev);
-  q.dr = du * u * (1.f - sr);
-  q.ds = du * sr;
-  q.lambda = d.lambda;
-  return q;
+__device__ __forceinline__ f2 sigmoid2(f2 z) {
+  const f2 e = f2_each(f2_mul(z, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
+  return f2_each(f2_add(e, f2_all(1.f)), [](float v) { return rcp_approx(v); });
+}
+
+// m = 1 - lambda of two channels.
+__device__ __forceinline__ f2 one_minus_lambda2(f2 u) {
+  f2 p = f2_fma(u, f2_all(kC3), f2_all(kC2));
+  p = f2_fma(u, p, f2_all(kC1));
+  p = f2_fma(u, p, f2_all(1.f));
+  const float2 near = f2_unpack(f2_mul(u, p));
+  const f2 e = f2_each(f2_mul(u, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
+  const float2 far = f2_unpack(f2_sub(f2_all(1.f), e)), v = f2_unpack(u);
+  return f2_pack(v.x < kNear ? near.x : far.x, v.y < kNear ? near.y : far.y);
+}
+
+// rsqrt(w) of w = 1 - lambda^2 = m (2 - m), and w itself.
+__device__ __forceinline__ f2 inverse_beta2(f2 m, f2* w) {
+  *w = f2_mul(m, f2_sub(f2_all(2.f), m));
+  return f2_each(*w, [](float v) { return rsqrt_approx(fmaxf(v, kLeast)); });
 }
 
 }  // namespace lag
