@@ -25,6 +25,8 @@
  * Outputs may share no element with an input or with each other (LA_ERR_INVALID_ARGUMENT), except
  * residual_out, which may be the residual itself (same pointer and stride).
  *
+ * dev_error (nullable device int): LA_DEV_ERR_TIMEOUT reports that a copy within a kernel passed
+ * its time limit (the outputs are then incomplete).
  * Calls enqueue on `stream`, allocate nothing, never synchronise and may be captured in a CUDA
  * graph.  Results are bitwise repeatable.
  */
@@ -44,12 +46,13 @@ extern "C" {
 /* residual nullable; residual_out nullable, needs a residual. */
 la_status la_rms_norm_fwd(const void* x, const void* residual, const float* weight, float eps, void* y,
                           void* residual_out, int64_t ldx, int64_t ldres, int64_t ldy, int64_t ldres_out, int rows,
-                          int C, la_dtype dtype, void* stream);
+                          int C, la_dtype dtype, int* dev_error, void* stream);
 
 /* y is e4m3 [rows, C]; group 0 (a scale per row) or 128. */
 la_status la_rms_norm_fwd_fp8(const void* x, const void* residual, const float* weight, float eps, void* y,
                               float* scales, void* residual_out, int64_t ldx, int64_t ldres, int64_t ldy,
-                              int64_t ldres_out, int rows, int C, int group, la_dtype dtype, void* stream);
+                              int64_t ldres_out, int rows, int C, int group, la_dtype dtype, int* dev_error,
+                              void* stream);
 
 /* Bytes of device workspace la_rms_norm_bwd needs.  Host only. */
 la_status la_rms_norm_bwd_workspace(int rows, int C, size_t* bytes);
@@ -66,7 +69,7 @@ la_status la_rms_norm_bwd_workspace(int rows, int C, size_t* bytes);
  */
 la_status la_rms_norm_bwd(const void* s, const float* weight, float eps, const void* dy, const void* dres, void* dx,
                           float* dweight, int64_t lds, int64_t lddy, int64_t lddres, int64_t lddx, int rows, int C,
-                          la_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+                          la_dtype dtype, void* workspace, size_t workspace_bytes, int* dev_error, void* stream);
 
 #ifdef __cplusplus
 }

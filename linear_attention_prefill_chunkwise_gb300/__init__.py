@@ -115,11 +115,11 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
             lib.la_gated_decode.argtypes = [vp] * 7 + [i64] * 4 + [i32] * 5 + [vp, vp]
             lib.la_gated_verify.argtypes = [vp] * 7 + [i64] * 4 + [i32] * 5 + [vp, vp]
             lib.la_gated_commit.argtypes = [vp] * 7 + [i64] * 3 + [i32] * 5 + [vp, vp]
-            lib.la_rms_norm_fwd.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 2 + [i64] * 4 + [i32] * 3 + [vp]
-            lib.la_rms_norm_fwd_fp8.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 3 + [i64] * 4 + [i32] * 4 + [vp]
+            lib.la_rms_norm_fwd.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 2 + [i64] * 4 + [i32] * 3 + [vp] * 2
+            lib.la_rms_norm_fwd_fp8.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 3 + [i64] * 4 + [i32] * 4 + [vp] * 2
             lib.la_rms_norm_bwd_workspace.argtypes = [i32] * 2 + [vp]
             lib.la_rms_norm_bwd.argtypes = [vp] * 2 + [ctypes.c_float] + [vp] * 4 + [i64] * 4 + [i32] * 3 + \
-                [vp, ctypes.c_size_t, vp]
+                [vp, ctypes.c_size_t, vp, vp]
             for fn in ("la_gated_scan_workspace", "la_gated_scan_fwd", "la_gated_scan_bwd", "la_gated_decode",
                        "la_gated_verify", "la_gated_commit", "la_rms_norm_fwd", "la_rms_norm_fwd_fp8",
                        "la_rms_norm_bwd_workspace", "la_rms_norm_bwd"):
@@ -770,23 +770,26 @@ def _norm_inputs(x, weight, residual, residual_out, stream):
     return code, rows, C, residual_out, ldx, ldres, _rows_like(residual_out, "residual_out", x)
 
 
-def la_rms_norm_fwd(x, weight, eps, residual=None, y=None, residual_out=None, stream=None):
+def la_rms_norm_fwd(x, weight, eps, residual=None, y=None, residual_out=None, dev_error=None, stream=None):
     """RMS norm of s = x + residual over the columns: y = s / sqrt(mean(s^2) + eps) * weight.
 
     x, residual, y, residual_out: bf16 or fp32 [rows, C] (C <= 16384), columns contiguous, any row
     stride; weight: fp32 [C].  residual_out receives s rounded to x's type and may be the residual
     itself.  Returns (y, residual_out); residual_out is None without a residual."""
+    import torch
     lib = load_library()
     code, rows, C, residual_out, ldx, ldres, ldro = _norm_inputs(x, weight, residual, residual_out, stream)
     if y is None:
         y = _empty((rows, C), x.dtype, x, stream)
     ldy = _rows_like(y, "y", x)
+    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
     _call(lib.la_rms_norm_fwd, x, x.data_ptr(), _p(residual), _p(weight), eps, y.data_ptr(), _p(residual_out), ldx,
-          ldres, ldy, ldro, rows, C, code, _stream(stream, x))
+          ldres, ldy, ldro, rows, C, code, _p(dev_error), _stream(stream, x))
     return y, residual_out
 
 
-def la_rms_norm_fwd_fp8(x, weight, eps, residual=None, group=0, y=None, scales=None, residual_out=None, stream=None):
+def la_rms_norm_fwd_fp8(x, weight, eps, residual=None, group=0, y=None, scales=None, residual_out=None,
+                        dev_error=None, stream=None):
     """la_rms_norm_fwd with an 8-bit output: y (torch.float8_e4m3fn [rows, C]) and FP32 scales, the
     norm's value being y * scale; one scale per row (group = 0: scales [rows, 1]) or per 128
     columns (group = 128: scales [rows, ceil(C / 128)]).  Returns (y, scales, residual_out)."""
@@ -802,8 +805,9 @@ def la_rms_norm_fwd_fp8(x, weight, eps, residual=None, group=0, y=None, scales=N
     if scales is None:
         scales = _empty((rows, groups), torch.float32, x, stream)
     _on_device(scales, "scales", torch.float32, (rows, groups), x)
+    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
     _call(lib.la_rms_norm_fwd_fp8, x, x.data_ptr(), _p(residual), _p(weight), eps, y.data_ptr(), _p(scales),
-          _p(residual_out), ldx, ldres, ldy, ldro, rows, C, group, code, _stream(stream, x))
+          _p(residual_out), ldx, ldres, ldy, ldro, rows, C, group, code, _p(dev_error), _stream(stream, x))
     return y, scales, residual_out
 
 
@@ -818,7 +822,8 @@ def la_rms_norm_bwd_workspace(rows, C):
     return nbytes.value
 
 
-def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, workspace=None, stream=None):
+def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, workspace=None, dev_error=None,
+                    stream=None):
     """Gradients of the norm of s (la_rms_norm_fwd's residual_out, or its x without a residual):
     given dy = dL/dy and dres (the gradient reaching residual_out from later layers, or None),
     returns (dx, dweight); dx is dL/dx and dL/dresidual alike, dweight fp32 [C].  ``workspace``:
@@ -835,6 +840,7 @@ def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, worksp
     if dweight is None:
         dweight = _empty((C,), torch.float32, s, stream)
     _on_device(dweight, "dweight", torch.float32, (C,), s)
+    _on_device(dev_error, "dev_error", torch.int32, (None,), s)
     if workspace is None:
         nbytes = la_rms_norm_bwd_workspace(rows, C)
         workspace = _empty((nbytes,), torch.uint8, s, stream) if nbytes else None
@@ -842,7 +848,8 @@ def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, worksp
         _on_device(workspace, "workspace", torch.uint8, (None,), s)
         nbytes = workspace.numel()
     _call(lib.la_rms_norm_bwd, s, s.data_ptr(), _p(weight), eps, dy.data_ptr(), _p(dres), dx.data_ptr(),
-          dweight.data_ptr(), lds, lddy, lddres, lddx, rows, C, code, _p(workspace), nbytes, _stream(stream, s))
+          dweight.data_ptr(), lds, lddy, lddres, lddx, rows, C, code, _p(workspace), nbytes, _p(dev_error),
+          _stream(stream, s))
     return dx, dweight
 
 

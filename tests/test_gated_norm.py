@@ -39,7 +39,7 @@ def decode(fn="la_gated_decode", **over):
 
 def fwd(fp8=False, **over):
     a = dict(x=X, res=None, w=W, eps=1e-5, y=Y, sc=SC, ro=None, ldx=64, ldres=64, ldy=64, ldro=64, rows=4, C=64, group=0,
-             dt=0, stream=None)
+             dt=0, err=None, stream=None)
     a.update(over)
     if not fp8:
         del a["sc"], a["group"]
@@ -48,7 +48,7 @@ def fwd(fp8=False, **over):
 
 def nback(**over):
     a = dict(s=X, w=W, eps=1e-5, dy=DOUT, dres=None, dx=DX, dw=DSL, lds=64, lddy=64, lddres=64, lddx=64, rows=4, C=64,
-             dt=0, ws=WS, wsb=1 << 30, stream=None)
+             dt=0, ws=WS, wsb=1 << 30, err=None, stream=None)
     a.update(over)
     return lap.load_library().la_rms_norm_bwd(*a.values())
 
@@ -135,7 +135,7 @@ def test_nothing_to_do():
     (dict(C=0), INVALID), (dict(C=16385, ldx=20000, ldy=20000), UNSUPPORTED), (dict(rows=-1), INVALID),
     (dict(dt=3), UNSUPPORTED), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(ro=RO), INVALID),
     (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(w=None), INVALID), (dict(ldy=63), INVALID), (dict(y=X), INVALID),
-    (dict(res=RES, ro=RES, ldro=128), INVALID), (dict(res=RES, ro=X), INVALID), (dict(res=RES, ldres=1), INVALID)])
+    (dict(res=RES, ro=RES, ldro=128), INVALID), (dict(err=Y + 4), INVALID), (dict(res=RES, ro=X), INVALID), (dict(res=RES, ldres=1), INVALID)])
 def test_norm_refusals(fp8, over, status):
     assert fwd(fp8, **over) == status
     assert lap.load_library().la_last_error() != b""
