@@ -17,44 +17,94 @@ using la_host::RowSpan;
 
 la_host::DeviceState g_dev[la_host::kMaxDevices];
 
-// How a scan is cut, and its device workspace: the ticket, the sequences of each tile (packed),
-// the published runs and states, and for the gradients one row of partial sums of dslopes per tile.
+// How a scan is cut, and its device workspace: the ticket, each tile's place among the sequences or
+// the sequences' order (packed), the published runs and states; for the gradients one row of
+// partial sums of dslopes per chain or tile.
 struct Plan {
-  int tiles = 0, columns = 0, stride = 0, group = 0;
-  bool waits = false;  // tickets and published states are needed
-  size_t first_seq = 0, runs = 0, words = 0, before = 0, part = 0, bytes = 0;
+  int tiles = 0, columns = 0, stride = 0, group = 0, groups = 0, per = 0, parts = 0;
+  int items = 0;       // tiles or chains, times columns
+  bool ticket = false; // a plan kernel runs first
+  bool waits = false;  // states pass from block to block
+  bool order = false;  // packed, by chains
+  size_t table = 0, runs = 0, words = 0, before = 0, part = 0, bytes = 0;
 };
 
-// Tiles of a group: each composes half a group of published runs on average, and a scan is a
-// chain of one step per group.
-constexpr int kGroup = 16;
+// Blocks the largest part holds at once; a device with fewer SMs runs the same plan.
+constexpr int kSlots = 152 * 2;
 
-Plan plan_of(int B, int T, int N, int C, bool packed, la_dtype dtype, bool backward) {
+// Tiles of a group.  A scan is a chain of one step per group (1.4 us each), while a tile composes
+// half a group of published runs: so about half the tiles of a column that are computed at once
+// (a group then takes about as long as a step), and at least one run per warp, which costs nothing.
+int group_of(int columns, int warps) {
+  const int wide = kSlots / (2 * columns);
+  return wide < warps ? warps : wide < 64 ? wide : 64;
+}
+
+// Whether blocks take whole chains (a sequence's channels).  Sequences of one length: for short
+// chains, which need no plan kernel, and where the chains fill the device evenly enough (2 x 8192
+// tokens x 8192 channels, 256 chains: 218 us by chains and 219 by tiles; 19 x 1024 x 8192: 243 and 281).
+bool by_chains(int64_t chains, int per) {
+  const int64_t waves = (chains + kSlots - 1) / kSlots;
+  return per <= 4 || chains * 100 >= waves * kSlots * 80;
+}
+// Packed: where there are chains enough, of several tiles each on average (32 sequences of up to 4096
+// tokens: 4096 channels 394 us by chains and 568 by tiles, gradients of 1001 channels 427 and 665).
+bool packed_by_chains(int64_t tokens, int N, int columns, int stride) {
+  return N <= 1024 && static_cast<int64_t>(N) * columns * 2 >= 3 * kSlots && tokens >= static_cast<int64_t>(N) * stride * 4;
+}
+
+template <typename E, bool kBack, bool kTma>
+Plan plan_for(int B, int T, int N, int C, bool packed) {
+  using S = lag::Shape<E, kBack, kTma>;
   Plan q;
   if (N == 0) return q;
-  const int most = dtype == LA_DTYPE_BF16 ? lag::Shape<__nv_bfloat16, false, true>::kTileRows
-                                          : lag::Shape<float, false, true>::kTileRows;
   const int64_t rows = static_cast<int64_t>(B) * T;
-  // short sequences of one length: tiles of whole sequences wait for nothing
-  const bool whole = !packed && T > 0 && T <= most;
-  q.stride = whole ? most / T * T : most;
-  q.waits = !whole;
-  q.tiles = static_cast<int>((rows + q.stride - 1) / q.stride);
-  if (q.tiles == 0) q.tiles = 1;  // empty sequences alone
+  q.stride = S::kTileRows;
   q.columns = (C + lag::kCols - 1) / lag::kCols;
-  q.group = kGroup;
+  if (!packed && T > 0 && T <= q.stride) {  // tiles of whole sequences
+    q.stride = q.stride / T * T;
+  } else if (!packed && T > 0) {
+    q.per = (T + q.stride - 1) / q.stride;
+    q.waits = !by_chains(static_cast<int64_t>(B) * q.columns, q.per);
+  } else if (packed) {
+    q.order = packed_by_chains(rows, N, q.columns, q.stride);
+    q.waits = !q.order;
+  }
+  q.ticket = q.waits || q.order;
+  q.tiles = q.per ? B * q.per : static_cast<int>((rows + q.stride - 1) / q.stride);
+  if (q.tiles == 0) q.tiles = 1;  // empty sequences alone
+  q.parts = q.order ? N : q.per && !q.waits ? B : q.tiles;
+  q.items = q.parts * q.columns;
+  q.group = group_of(q.columns, S::kWarps);
+  q.groups = ((q.per ? q.per : q.tiles) + q.group - 1) / q.group;
+  if (q.ticket) {
+    q.table = 256;
+    const size_t table = q.order ? static_cast<size_t>(N) * 4 : packed ? (static_cast<size_t>(q.tiles) + 1) * sizeof(int2) : 0;
+    q.bytes = q.table + la_host::align256(table);
+  }
   if (q.waits) {
     const size_t width = static_cast<size_t>(q.columns) * lag::kCols;
-    const size_t groups = (q.tiles + q.group - 1) / q.group;
-    q.first_seq = 256;
-    q.runs = q.first_seq + (packed ? la_host::align256((static_cast<size_t>(q.tiles) + 1) * 4) : 0);
+    q.runs = q.bytes;
     q.before = q.runs + q.tiles * width * 8;
-    q.words = q.tiles * width * 2 + groups * width;
-    q.bytes = q.runs + q.words * 4;
+    q.words = q.tiles * width * 2 + static_cast<size_t>(q.per ? B : 1) * q.groups * width;
+    q.bytes = q.runs + la_host::align256(q.words * 4);
   }
   q.part = q.bytes;
-  if (backward) q.bytes += la_host::align256(static_cast<size_t>(q.tiles) * C * 4);
+  if (kBack) q.bytes += la_host::align256(static_cast<size_t>(q.parts) * C * 4);
   return q;
+}
+
+// The workspace a call needs, whether or not its rows can be read by TMA.
+template <typename E, bool kBack>
+size_t workspace_for(int B, int T, int N, int C, bool packed) {
+  const size_t a = plan_for<E, kBack, true>(B, T, N, C, packed).bytes, b = plan_for<E, kBack, false>(B, T, N, C, packed).bytes;
+  return a > b ? a : b;
+}
+size_t workspace_of(int B, int T, int N, int C, bool packed, la_dtype dtype, bool backward) {
+  if (dtype == LA_DTYPE_BF16)
+    return backward ? workspace_for<__nv_bfloat16, true>(B, T, N, C, packed)
+                    : workspace_for<__nv_bfloat16, false>(B, T, N, C, packed);
+  return backward ? workspace_for<float, true>(B, T, N, C, packed) : workspace_for<float, false>(B, T, N, C, packed);
 }
 
 la_status check_sizes(int B, int T, int N, int C, bool packed, la_dtype dtype) {
@@ -92,19 +142,22 @@ RowSpan pool_span(const void* p, const char* name, const int32_t* state_indices,
 }
 
 template <typename E>
-void set_plan(lag::Params<E>* p, const Plan& q, void* workspace) {
+void set_plan(lag::Params<E>* p, const Plan& q, bool backward, void* workspace) {
   char* ws = static_cast<char*>(workspace);
   p->tiles = q.tiles;
   p->columns = q.columns;
   p->stride = q.stride;
   p->group = q.group;
+  p->groups = q.groups;
+  p->per = q.per;
+  if (q.ticket) p->ticket = reinterpret_cast<int*>(ws);
+  if (q.order) p->order = reinterpret_cast<int32_t*>(ws + q.table);
   if (q.waits) {
-    p->ticket = reinterpret_cast<int*>(ws);
-    p->first_seq = reinterpret_cast<int32_t*>(ws + q.first_seq);
-    p->runs = reinterpret_cast<float2*>(ws + q.runs);
-    p->before = reinterpret_cast<float*>(ws + q.before);
+    if (p->cu_seqlens) p->places = reinterpret_cast<int2*>(ws + q.table);
+    p->runs = reinterpret_cast<float4*>(ws + q.runs);
+    p->before = reinterpret_cast<float2*>(ws + q.before);
   }
-  p->part = reinterpret_cast<float*>(ws + q.part);
+  if (backward) p->part = reinterpret_cast<float*>(ws + q.part);
 }
 
 // Whether rows of this stride can be read by TMA boxes / written two channels at a time.
@@ -135,14 +188,19 @@ la_status encode_rows_map(CUtensorMap* map, const E* base, int64_t rows, int64_t
 
 template <typename E>
 cudaError_t launch_plan(const lag::Params<E>& p, const Plan& q, int sms, cudaStream_t s) {
-  const size_t want = (q.words / 4 + lag::kThreads - 1) / lag::kThreads;
+  size_t want = q.words / 4;
+  if (q.order) want = static_cast<size_t>(p.N) * (p.part ? p.C / 16 + 1 : 1);
+  want = (want + lag::kThreads - 1) / lag::kThreads;
   const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want < size_t(sms) * 8 ? want : size_t(sms) * 8);
   return la_host::launch_pdl(lag::scan_plan_kernel<E>, grid, lag::kThreads, 0, s, p, q.words);
 }
 
 template <typename E, bool kBack, bool kTma>
-la_status launch_kernel(const lag::Params<E>& p, const Plan& q, int sms, cudaStream_t s) {
+la_status launch_scan_as(lag::Params<E> p, int B, void* workspace, float* dslopes, int sms, cudaStream_t s) {
   using S = lag::Shape<E, kBack, kTma>;
+  const bool packed = p.cu_seqlens != nullptr;
+  const Plan q = plan_for<E, kBack, kTma>(B, p.T, p.N, p.C, packed);
+  set_plan(&p, q, kBack, workspace);
   lag::Maps maps;
   if constexpr (kTma) {
     for (int i = 0; i < S::kInputs; ++i) {
@@ -150,27 +208,25 @@ la_status launch_kernel(const lag::Params<E>& p, const Plan& q, int sms, cudaStr
       if (st != LA_OK) return st;
     }
   }
-  const int total = q.tiles * q.columns, most = sms * S::kBlocks;
-  const cudaError_t ce = la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma>, total < most ? total : most,
-                                             lag::kScanThreads, lag::scan_smem_bytes<E, kBack, kTma>(), s, p, maps);
+  cudaError_t ce = q.ticket ? launch_plan(p, q, sms, s) : cudaSuccess;
+  if (ce == cudaSuccess && q.tiles > 0) {
+    const int most = sms * S::kBlocks;
+    ce = la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma>, q.items < most ? q.items : most, S::kThreads,
+                             lag::scan_smem_bytes<E, kBack, kTma>(), s, p, maps);
+  }
+  if (ce == cudaSuccess && kBack)
+    ce = la_host::launch_pdl(lag::column_sum_kernel, (p.C + 31) / 32, 1024, 0, s, static_cast<const float*>(p.part),
+                             q.parts, p.C, static_cast<const int*>(packed ? p.ticket : nullptr), dslopes);
   return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
 }
 
 template <typename E, bool kBack>
-la_status launch_scan(const lag::Params<E>& p, const Plan& q, float* dslopes, int sms, cudaStream_t s) {
-  cudaError_t ce = q.waits ? launch_plan(p, q, sms, s) : cudaSuccess;
-  if (ce == cudaSuccess && q.tiles > 0) {
-    bool tma = p.rows > 0;
-    for (int i = 0; i < (kBack ? 5 : 3); ++i) tma = tma && box_rows<E>(p.in[i], p.ld_in[i]);
-    for (int i = 0; i < (kBack ? 3 : 1); ++i) tma = tma && p.C % 2 == 0 && pair_rows<E>(p.out[i], p.ld_out[i]);
-    const la_status st = tma ? launch_kernel<E, kBack, true>(p, q, sms, s) : launch_kernel<E, kBack, false>(p, q, sms, s);
-    if (st != LA_OK) return st;
-  }
-  if (ce == cudaSuccess && kBack)
-    ce = la_host::launch_pdl(lag::column_sum_kernel, (p.C + 31) / 32, 1024, 0, s, static_cast<const float*>(p.part),
-                             q.tiles, p.C, static_cast<const int*>(p.cu_seqlens ? p.ticket : nullptr), dslopes);
-  if (ce == cudaSuccess) ce = cudaGetLastError();
-  return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
+la_status launch_scan(const lag::Params<E>& p, int B, void* workspace, float* dslopes, int sms, cudaStream_t s) {
+  bool tma = p.rows > 0;
+  for (int i = 0; i < (kBack ? 5 : 3); ++i) tma = tma && box_rows<E>(p.in[i], p.ld_in[i]);
+  for (int i = 0; i < (kBack ? 3 : 1); ++i) tma = tma && p.C % 2 == 0 && pair_rows<E>(p.out[i], p.ld_out[i]);
+  return tma ? launch_scan_as<E, kBack, true>(p, B, workspace, dslopes, sms, s)
+             : launch_scan_as<E, kBack, false>(p, B, workspace, dslopes, sms, s);
 }
 
 // One-time setup per device: the stages of a scan exceed the default shared memory.
@@ -270,7 +326,7 @@ la_status la_gated_scan_workspace(int B, int T, int N, int C, int packed, la_dty
   if (!bytes) return fail(LA_ERR_INVALID_ARGUMENT, "bytes is null");
   const la_status st = check_sizes(B, T, N, C, packed != 0, dtype);
   if (st != LA_OK) return st;
-  *bytes = plan_of(B, T, N, C, packed != 0, dtype, backward != 0).bytes;
+  *bytes = workspace_of(B, T, N, C, packed != 0, dtype, backward != 0);
   return LA_OK;
 }
 
@@ -287,8 +343,8 @@ la_status la_gated_scan_fwd(const void* x, const void* r, const void* g, const f
   const uint64_t es = la_host::element_size(dtype), rows = static_cast<uint64_t>(B) * T;
   if (!slopes || (rows > 0 && (!x || !r || !g || !o)))
     return fail(LA_ERR_INVALID_ARGUMENT, "x, r, g, slopes and o must be non-null");
-  const Plan w = plan_of(B, T, N, C, cu_seqlens != nullptr, dtype, false);
-  if ((st = la_host::check_workspace(workspace, workspace_bytes, w.bytes)) != LA_OK) return st;
+  const size_t need = workspace_of(B, T, N, C, cu_seqlens != nullptr, dtype, false);
+  if ((st = la_host::check_workspace(workspace, workspace_bytes, need)) != LA_OK) return st;
   const RowSpan ins[] = {la_host::rows_of(x, ldx, rows, C, es, "x"),
                          la_host::rows_of(r, ldr, rows, C, es, "r"),
                          la_host::rows_of(g, ldg, rows, C, es, "g"),
@@ -298,7 +354,7 @@ la_status la_gated_scan_fwd(const void* x, const void* r, const void* g, const f
                          la_host::flat(cu_seqlens, static_cast<uint64_t>(N) * 4 + 4, "cu_seqlens")};
   const RowSpan outs[] = {la_host::rows_of(o, ldo, rows, C, es, "o"),
                           pool_span(h_final, "h_final", state_indices, pool_size, N, C),
-                          la_host::flat(workspace, w.bytes, "workspace"),
+                          la_host::flat(workspace, need, "workspace"),
                           la_host::flat(dev_error, 4, "dev_error")};
   if ((st = la_host::check_rows(ins, 7, outs, 4)) != LA_OK) return st;
   la_host::DeviceState* ds = nullptr;
@@ -313,8 +369,7 @@ la_status la_gated_scan_fwd(const void* x, const void* r, const void* g, const f
     p.finish = h_final;
     p.cu_seqlens = cu_seqlens;
     p.rows = static_cast<int>(rows);
-    set_plan(&p, w, workspace);
-    return launch_scan<E, false>(p, w, nullptr, ds->sms, static_cast<cudaStream_t>(stream));
+    return launch_scan<E, false>(p, B, workspace, nullptr, ds->sms, static_cast<cudaStream_t>(stream));
   };
   return dtype == LA_DTYPE_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }
@@ -333,8 +388,8 @@ la_status la_gated_scan_bwd(const void* x, const void* r, const void* g, const f
   const uint64_t es = la_host::element_size(dtype), rows = static_cast<uint64_t>(B) * T;
   if (!slopes || !dslopes || (rows > 0 && (!x || !r || !g || !o || !dout || !dx || !dr || !dg)))
     return fail(LA_ERR_INVALID_ARGUMENT, "x, r, g, slopes, o, dout, dx, dr, dg and dslopes must be non-null");
-  const Plan w = plan_of(B, T, N, C, cu_seqlens != nullptr, dtype, true);
-  if ((st = la_host::check_workspace(workspace, workspace_bytes, w.bytes)) != LA_OK) return st;
+  const size_t need = workspace_of(B, T, N, C, cu_seqlens != nullptr, dtype, true);
+  if ((st = la_host::check_workspace(workspace, workspace_bytes, need)) != LA_OK) return st;
   const RowSpan ins[] = {la_host::rows_of(x, ldx, rows, C, es, "x"),
                          la_host::rows_of(r, ldr, rows, C, es, "r"),
                          la_host::rows_of(g, ldg, rows, C, es, "g"),
@@ -350,7 +405,7 @@ la_status la_gated_scan_bwd(const void* x, const void* r, const void* g, const f
                           la_host::rows_of(dg, lddg, rows, C, es, "dg"),
                           la_host::flat(dslopes, static_cast<uint64_t>(C) * 4, "dslopes"),
                           pool_span(dh0, "dh0", state_indices, pool_size, N, C),
-                          la_host::flat(workspace, w.bytes, "workspace"),
+                          la_host::flat(workspace, need, "workspace"),
                           la_host::flat(dev_error, 4, "dev_error")};
   if ((st = la_host::check_rows(ins, 10, outs, 7)) != LA_OK) return st;
   la_host::DeviceState* ds = nullptr;
@@ -374,8 +429,7 @@ la_status la_gated_scan_bwd(const void* x, const void* r, const void* g, const f
     p.h0 = h0;
     p.cu_seqlens = cu_seqlens;
     p.rows = static_cast<int>(rows);
-    set_plan(&p, w, workspace);
-    return launch_scan<E, true>(p, w, dslopes, ds->sms, static_cast<cudaStream_t>(stream));
+    return launch_scan<E, true>(p, B, workspace, dslopes, ds->sms, static_cast<cudaStream_t>(stream));
   };
   return dtype == LA_DTYPE_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }

@@ -21,8 +21,10 @@
 // last tile published; a long scan is thus a chain of one step per group, not per tile.  The
 // order of every sum is fixed, so results repeat bitwise.
 // A published word carries its own readiness: the workspace is filled with all-ones before the
-// scan (a NaN pattern that no arithmetic produces), a tile's (A, H) is one 64-bit store, and a
-// reader polls the word itself: no fence and no second flag on the way from block to block.
+// scan, no published word is all-ones, and a reader looks at the words themselves: no fence and no
+// second flag on the way from block to block.  A tile asks for the words it needs before it
+// computes its own rows, by asynchronous copies; they have nearly always been published by then,
+// so a block waits at one barrier per tile, and only where one was late it polls.
 // Where a sequence begins, A becomes -0: products of decays are >= +0, so the sign marks "what
 // came before does not matter", and composition then selects H instead of multiplying, which keeps
 // infinities and NaN of one sequence out of the next.
@@ -39,24 +41,30 @@ namespace lag {
 
 constexpr unsigned kErrBadSeqlens = 1u, kErrBadIndex = 2u, kErrTimeout = 4u;
 constexpr int kCols = 64;       // channels of a tile: two per lane
-constexpr int kWarps = 8;       // warps of a scan block
-constexpr int kScanThreads = kWarps * 32;
 constexpr int kThreads = 128;   // threads of the small kernels
 constexpr int kMaxInputs = 5;   // x, r, g; backward: dout and o (one row up: h_{t-1}) too
 constexpr int kStages = 2;
 
 // Shape of a scan kernel: rows per warp, blocks per SM and the stages' layout.  kTma: rows arrive
-// by TMA boxes of kRows x 64 channels; else by 4-byte copies, and a BF16 row takes one word more
-// where it begins in the middle of a word.
+// by TMA boxes of kRows x 64 channels; else by 16-byte copies of the aligned chunks that a row's
+// channels touch, one chunk more than the channels fill.
+// Rows per warp: as many as two blocks' registers (forward: a and b of each) and shared memory
+// hold; every tile costs the same few hundred instructions.  Forward of 19 x 1024 x 8192 BF16 in
+// chains: 16 rows 243 us, 14 279, 12 262 (three blocks of 8 rows 388: registers spill, and the
+// stages leave no cache for them); 1001 channels: 12 rows 290, 10 206, 8 226.  Gradients: 8 rows
+// 447, 10 572, 6 494; 1001 channels: 8 rows 426, 6 402.
 template <typename E, bool kBack, bool kTma>
 struct Shape {
-  static constexpr int kRows = sizeof(E) == 2 ? 8 : 4;
-  static constexpr int kBlocks = kBack ? 2 : 3;
+  static constexpr int kWarps = 8;
+  static constexpr int kRows = (kBack ? (kTma ? 8 : 6) : (kTma ? 16 : 10)) / (sizeof(E) / 2);
+  static constexpr int kBlocks = 2;
+  static constexpr int kAsk = kRows * 5 / 8;  // the row before which a warp asks for the published words
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kTileRows = kWarps * kRows;
   static constexpr int kInputs = kBack ? 5 : 3;
-  static constexpr int kPitch = kCols * sizeof(E) + (kTma || sizeof(E) == 4 ? 0 : 4);  // bytes of a row
-  static constexpr int kInputBytes = kRows * kPitch;                                 // one input, one warp
-  static constexpr int kStageBytes = (kInputs * kInputBytes + 127) / 128 * 128;
+  static constexpr int kPitch = kCols * sizeof(E) + (kTma ? 0 : 16);  // bytes of a row
+  static constexpr int kInputBytes = kTileRows * kPitch;
+  static constexpr int kStageBytes = kInputs * kInputBytes;
 };
 
 template <typename E>
@@ -75,12 +83,17 @@ struct Params {
   const int32_t* accepted_len;  // commit
   int* dev_error;
   // the workspace of a scan
-  int* ticket;         // next tile, then an abort flag; null: blocks take tiles in turn, nothing is waited for
-  int32_t* first_seq;  // [tiles + 1] (packed) first sequence that begins at or after the tile's first row
-  float2* runs;        // [tiles][padded C] published (A, H)
-  float* before;       // [groups][padded C] published states after each group
+  int* ticket;         // next tile or chain, an abort flag, running sequences; null: blocks take theirs in turn
+  int2* places;        // [tiles + 1] (packed, by tiles) where each tile lies among the sequences
+  int32_t* order;      // [N] (packed, by chains) the running sequences, longest first
+  float4* runs;        // [tiles][columns][32] published (A, H) of each lane's two channels; null: nothing waits
+  float2* before;      // [sequences, or 1][groups][columns][32] published states after each group
   int T, N, C, pool_size, rows;
-  int tiles, columns, stride, group;  // tiles along the rows, of `stride` rows; along the channels; per group
+  int tiles, columns, stride;  // tiles along the rows, of `stride` rows; along the channels
+  int group, groups;           // tiles per group; groups of a sequence (of all rows without `per`)
+  // Sequences of one length: tiles per sequence (the last may be short); 0: packed, or tiles that
+  // hold several whole sequences.
+  int per;
 };
 
 struct Maps {
@@ -95,7 +108,10 @@ __device__ __forceinline__ void report(int* dev_error, unsigned bit) {
 
 // Fills the published words, sets the ticket and, for a packed batch, checks cu_seqlens
 // (non-decreasing inside [0, T]; if not, the ticket starts past the last tile, so that the scan
-// does nothing) and finds the sequences of each tile.
+// does nothing).  By tiles, it finds each tile's place: x, the first sequence that begins at or
+// after its first row; y, whether all its rows lie inside one running sequence, away from its ends.
+// By chains, it orders the running sequences, longest first (ties by number), and clears the
+// partial sums of the others.
 template <typename E>
 __global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p, size_t words) {
   lap::griddep_wait();
@@ -104,16 +120,43 @@ __global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p, 
   const size_t all = static_cast<size_t>(gridDim.x) * kThreads;
   uint4* w = reinterpret_cast<uint4*>(p.runs);  // runs and before lie together, 16-byte multiples
   for (size_t i = id; i < words / 4; i += all) w[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
-  if (p.cu_seqlens) {
+  if (p.places) {
     for (size_t i = id; i <= static_cast<size_t>(p.tiles); i += all) {
       const int64_t row = static_cast<int64_t>(i) * p.stride;
-      int a = 0, b = p.N;  // the first n with cu[n] >= row; the last tile owns the rest
+      int a = 0, b = p.N;  // the first n with cu[n] >= row
       while (a < b) {
         const int m = (a + b) / 2;
         if (p.cu_seqlens[m] >= row) b = m; else a = m + 1;
       }
-      p.first_seq[i] = i == static_cast<size_t>(p.tiles) ? p.N : a;
+      bool inner = a > 0 && row + p.stride < p.cu_seqlens[a];
+      if (inner) {
+        const int slot = p.state_indices ? p.state_indices[a - 1] : a - 1;
+        inner = slot >= 0 && slot < p.pool_size;
+      }
+      p.places[i] = make_int2(i == static_cast<size_t>(p.tiles) ? p.N : a, inner);  // the last tile owns the rest
     }
+  }
+  if (p.order) {
+    auto length = [&](int n) {  // -1: does not run
+      const int slot = p.state_indices ? p.state_indices[n] : n;
+      return slot < 0 || slot >= p.pool_size ? -1 : p.cu_seqlens[n + 1] - p.cu_seqlens[n];
+    };
+    for (size_t i = id; i < static_cast<size_t>(p.N); i += all) {
+      const int n = static_cast<int>(i), mine = length(n);
+      int rank = 0, running = 0;
+#pragma unroll 8
+      for (int m = 0; m < p.N; ++m) {
+        const int other = length(m);
+        running += other >= 0;
+        rank += other > mine || (other == mine && m < n);
+      }
+      if (mine >= 0) p.order[rank] = n;
+      else if (p.state_indices && p.state_indices[n] >= p.pool_size) report(p.dev_error, kErrBadIndex);
+      if (n == 0) p.ticket[2] = running;
+    }
+    if (p.part)
+      for (size_t i = id; i < static_cast<size_t>(p.N) * p.C; i += all)
+        if (length(static_cast<int>(i / p.C)) < 0) p.part[i] = 0.f;
   }
   if (blockIdx.x == 0) {
     int wrong = 0;
@@ -140,25 +183,58 @@ struct Rows {
 
 // Sequence n's slot, or -1 where it is padded or its index is out of range.
 template <typename E>
-__device__ __forceinline__ int slot_of(const Params<E>& p, int n) {
-  const int slot = p.state_indices ? p.state_indices[n] : n;
+__device__ __forceinline__ int checked(const Params<E>& p, int slot) {
   if (slot >= p.pool_size) {
     report(p.dev_error, kErrBadIndex);
     return -1;
   }
   return slot;
 }
+template <typename E>
+__device__ __forceinline__ int slot_of(const Params<E>& p, int n) {
+  return checked(p, p.state_indices ? p.state_indices[n] : n);
+}
+
+// A tile: its number along the rows (-1: none), its channels, its sequence n and place i in that
+// sequence in walking order (where tiles hold rows of several sequences: 0 and its place among all
+// tiles), i's place j in its group, its lowest row and that row's token in the sequence, and the
+// sequence's length (-1: rows of several).
+struct Tile {
+  int t, column, n, i, j, row, token, length;
+};
 
 template <bool kBack, int K, typename E>
-__device__ __forceinline__ Rows rows_of(const Params<E>& p, int tile, int warp, int lane) {
-  Rows q{0u, 0u, 0u, -1};
+__device__ __forceinline__ Rows rows_of(const Params<E>& p, const Tile& q, int warp, int lane) {
+  if (q.length >= 0) {  // by arithmetic, the same for every lane
+    const int slot = p.state_indices ? p.state_indices[q.n] : q.n;
+    const int place = warp * K;
+    auto bit = [](int k) { return k >= 0 && k < K ? 1u << k : 0u; };
+    auto below = [](int k) { return k <= 0 ? 0u : k >= K ? (1u << K) - 1u : (1u << k) - 1u; };  // bits under k
+    Rows r{0u, 0u, 0u, checked(p, slot)};
+    if (r.slot < 0) return r;
+    if (kBack) {
+      const int top = q.token + p.stride - 1 - place;  // the token of row 0; they count down
+      r.live = ((1u << K) - 1u) & ~below(top - q.length + 1);
+      r.begin = bit(top - q.length + 1);
+      r.end = bit(top);
+    } else {
+      const int top = q.token + place;
+      r.live = below(q.length - top);
+      r.begin = bit(-top);
+      r.end = bit(q.length - 1 - top);
+    }
+    r.begin &= r.live;
+    r.end &= r.live;
+    return r;
+  }
+  Rows r{0u, 0u, 0u, -1};
   const int place = warp * K + lane;  // in walking order
   const int at = kBack ? p.stride - 1 - place : place;
-  const int64_t row = static_cast<int64_t>(tile) * p.stride + at;
+  const int64_t row = static_cast<int64_t>(q.t) * p.stride + at;
   bool first = false, last = false;
   if (lane < K && place < p.stride && row < p.rows) {
     if (p.cu_seqlens) {
-      int a = p.first_seq[tile], b = p.first_seq[tile + 1];
+      int a = p.places[q.t].x, b = p.places[q.t + 1].x;
       while (a < b) {  // the number of sequences that begin at or before the row
         const int m = (a + b) / 2;
         if (p.cu_seqlens[m] <= row) a = m + 1; else b = m;
@@ -166,22 +242,31 @@ __device__ __forceinline__ Rows rows_of(const Params<E>& p, int tile, int warp, 
       if (a > 0) {
         const int lo = p.cu_seqlens[a - 1], hi = p.cu_seqlens[a];
         if (row < hi) {
-          q.slot = slot_of(p, a - 1);
+          r.slot = slot_of(p, a - 1);
           first = row == lo;
           last = row == hi - 1;
         }
       }
     } else {
       const int n = static_cast<int>(row) / p.T, t = static_cast<int>(row) - n * p.T;
-      q.slot = slot_of(p, n);
+      r.slot = slot_of(p, n);
       first = t == 0;
       last = t == p.T - 1;
     }
   }
-  q.live = __ballot_sync(0xFFFFFFFFu, q.slot >= 0);
-  q.begin = __ballot_sync(0xFFFFFFFFu, q.slot >= 0 && (kBack ? last : first));
-  q.end = __ballot_sync(0xFFFFFFFFu, q.slot >= 0 && (kBack ? first : last));
-  return q;
+  r.live = __ballot_sync(0xFFFFFFFFu, r.slot >= 0);
+  r.begin = __ballot_sync(0xFFFFFFFFu, r.slot >= 0 && (kBack ? last : first));
+  r.end = __ballot_sync(0xFFFFFFFFu, r.slot >= 0 && (kBack ? first : last));
+  return r;
+}
+
+// Whether some row of the warp may begin or end a sequence or belong to none.  `inside`: what was
+// looked up for the tile (the sequence's slot, or whether a packed tile lies inside a sequence).
+template <bool kBack, int K, typename E>
+__device__ __forceinline__ bool has_edges(const Params<E>& p, const Tile& q, int inside, int warp) {
+  if (q.length < 0) return !inside;
+  const int low = q.token + (kBack ? p.stride - (warp + 1) * K : warp * K);  // the lowest row's token
+  return inside < 0 || inside >= p.pool_size || low <= 0 || low + K >= q.length;
 }
 
 // A lane's two channels: neighbours with TMA rows, else a warp's width apart.
@@ -244,59 +329,46 @@ __device__ __forceinline__ void store_state(float* pool, int slot, int C, const 
 
 // ---------------------------------------------------------------- a warp's rows in shared memory
 
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Starts the loads of a warp's kRows rows (the lowest is row `low`) of every input into `stage`.
+// Starts the loads of a tile's rows of every input into `stage`, whose first row is row `low` of
+// the matrices: each warp its own rows, from row `first` of the stage (kTma: one thread of it, a box
+// for each input).
 template <bool kBack, bool kTma, typename E>
 __device__ __forceinline__ void fetch(const Params<E>& p, const Maps& maps, char* stage, uint64_t* bar, int low,
-                                      int column, int lane) {
+                                      int column, int first, int lane) {
   using S = Shape<E, kBack, kTma>;
   if constexpr (kTma) {
-    if (lane == 0) {
-      lap::mbar_arrive_expect_tx(bar, S::kInputs * S::kInputBytes);
+    lap::mbar_arrive_expect_tx(bar, S::kInputs * S::kRows * S::kPitch);
 #pragma unroll
-      for (int i = 0; i < S::kInputs; ++i)  // o one row up; rows outside the matrix arrive as zeros
-        lap::tma_load_2d(stage + i * S::kInputBytes, &maps.of[i], bar, column * kCols, low - (i == 4));
-    }
+    for (int i = 0; i < S::kInputs; ++i)  // o one row up; rows outside the matrix arrive as zeros
+      lap::tma_load_2d(stage + i * S::kInputBytes + first * S::kPitch, &maps.of[i], bar, column * kCols,
+                       low + first - (i == 4));
   } else {
-    const uint32_t to = lap::smem_u32(stage);
+    constexpr int kChunks = S::kPitch / 16;
     const int64_t last = static_cast<int64_t>(p.rows) - 1;
+    const int bytes = min(kCols, p.C - column * kCols) * static_cast<int>(sizeof(E));
 #pragma unroll
     for (int i = 0; i < S::kInputs; ++i) {
+      const char* begin = reinterpret_cast<const char*>(p.in[i]);  // of the matrix
+      const char* end = begin + (last * p.ld_in[i] + p.C) * static_cast<int64_t>(sizeof(E));
 #pragma unroll
-      for (int k = 0; k < S::kRows; ++k) {
-        const int64_t row = static_cast<int64_t>(low) + k - (i == 4);
-        if (row < 0 || row > last) continue;
-        const int64_t first = row * p.ld_in[i] + column * kCols;  // element of the matrix
-        const uint32_t dst = to + i * S::kInputBytes + k * S::kPitch;
-        const E* src = p.in[i] + first;
-        if constexpr (sizeof(E) == 4) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (column * kCols + lane + 32 * j < p.C) copy4(dst + 4 * (lane + 32 * j), src + lane + 32 * j);
+      for (int j = 0; j < (S::kRows * kChunks + 31) / 32; ++j) {
+        const int id = lane + 32 * j, k = id / kChunks, c = id - k * kChunks;
+        const int64_t row = static_cast<int64_t>(low) + first + k - (i == 4);
+        if (k >= S::kRows || row < 0 || row > last) continue;
+        const char* src = begin + (row * p.ld_in[i] + column * kCols) * static_cast<int64_t>(sizeof(E));
+        const char* chunk = src - (reinterpret_cast<uintptr_t>(src) & 15u) + 16 * c;
+        if (chunk >= src + bytes) continue;
+        char* dst = stage + i * S::kInputBytes + (first + k) * S::kPitch + 16 * c;
+        if (chunk >= begin && chunk + 16 <= end) {
+          copy16(lap::smem_u32(dst), chunk);  // its neighbours lie inside the matrix
         } else {
-          // whole words that hold a channel of this tile; a word's other half may be a neighbour
-          // inside the matrix, but nothing outside it is read
-          const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(src) >> 1 & 1u);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int w = lane + 32 * j;
-            if (j == 1 && (lane > 0 || !odd)) break;
-            const int e = 2 * w - odd, c = column * kCols + e;
-            if (c + (e < 0) >= p.C) continue;
-            if (first + e >= 0 && first + e + 1 <= last * p.ld_in[i] + p.C - 1) {
-              copy4(dst + 4 * w, src + e);
-            } else {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (e + h >= 0 && c + h < p.C)
-                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 4 * w + 2 * h),
-                               "h"(reinterpret_cast<const unsigned short*>(src)[e + h])
-                               : "memory");
-            }
-          }
+          for (int e = 0; e < 16; e += sizeof(E))
+            if (chunk + e >= src && chunk + e < src + bytes)
+              *reinterpret_cast<E*>(dst + e) = *reinterpret_cast<const E*>(chunk + e);
         }
       }
     }
@@ -310,7 +382,7 @@ __device__ __forceinline__ bool arrived(uint64_t* bar, unsigned use, volatile in
   if constexpr (kTma) {
     return lap::mbar_wait(bar, use & 1u, abort);
   } else {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");  // all but the next stage's
     __syncwarp();
     return true;
   }
@@ -320,30 +392,30 @@ __device__ __forceinline__ bool arrived(uint64_t* bar, unsigned use, volatile in
 template <typename E, bool kBack, bool kTma>
 struct View {
   using S = Shape<E, kBack, kTma>;
-  const char* at[2];  // of even and odd rows of the stage: they may begin at different half words
-  __device__ __forceinline__ View(const Params<E>& p, const char* stage, int i, int low, int lane) {
-    const char* s = stage + i * S::kInputBytes;
-    if constexpr (kTma) {
-      at[0] = at[1] = s + lane * 2 * sizeof(E);
-    } else if constexpr (sizeof(E) == 4) {
-      at[0] = at[1] = s + lane * 4;
-    } else {
-      const unsigned base = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p.in[i]) >> 1);
-      const unsigned row = static_cast<unsigned>(low - (i == 4)), ld = static_cast<unsigned>(p.ld_in[i]);
-      at[0] = s + 2 * (lane + ((base + row * ld) & 1u));
-      at[1] = s + 2 * (lane + ((base + (row + 1) * ld) & 1u));
+  const char* at;
+  unsigned first, step;  // bytes before the first row's first channel in its chunk; more per row
+  // `rows`: the warp's first row in the stage, row `low` of the matrix
+  __device__ __forceinline__ View(const Params<E>& p, const char* rows, int i, int low, int lane) {
+    at = rows + i * S::kInputBytes + lane * sizeof(E) * (kTma ? 2 : 1);
+    if constexpr (!kTma) {
+      step = static_cast<unsigned>(p.ld_in[i]) * sizeof(E);
+      first = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p.in[i])) + static_cast<unsigned>(low - (i == 4)) * step;
     }
   }
   __device__ __forceinline__ f2 get(int k) const {
-    const char* s = at[k & 1] + k * S::kPitch;
-    if constexpr (sizeof(E) == 4) {
-      if constexpr (kTma) return *reinterpret_cast<const f2*>(s);
-      return f2_pack(*reinterpret_cast<const float*>(s), *reinterpret_cast<const float*>(s + 128));
+    const char* s = at + k * S::kPitch;
+    if constexpr (kTma) {
+      if constexpr (sizeof(E) == 4) return *reinterpret_cast<const f2*>(s);
+      else return lap::bf16x2_to_f2(*reinterpret_cast<const uint32_t*>(s));
     } else {
-      if constexpr (kTma) return lap::bf16x2_to_f2(*reinterpret_cast<const uint32_t*>(s));
-      const unsigned lo = *reinterpret_cast<const unsigned short*>(s);
-      const unsigned hi = *reinterpret_cast<const unsigned short*>(s + 64);
-      return f2_pack(__uint_as_float(lo << 16), __uint_as_float(hi << 16));
+      s += (first + k * step) & 15u;
+      if constexpr (sizeof(E) == 4) {
+        return f2_pack(*reinterpret_cast<const float*>(s), *reinterpret_cast<const float*>(s + 128));
+      } else {
+        const unsigned lo = *reinterpret_cast<const unsigned short*>(s);
+        const unsigned hi = *reinterpret_cast<const unsigned short*>(s + 64);
+        return f2_pack(__uint_as_float(lo << 16), __uint_as_float(hi << 16));
+      }
     }
   }
 };
@@ -365,22 +437,27 @@ __device__ __forceinline__ Run compose(const Run& first, const Run& then) {
   return {f2_pack(signbit(a.x) ? -0.f : v.x, signbit(a.y) ? -0.f : v.y), apply(then, first.h)};
 }
 
-constexpr unsigned long long kUnset = ~0ull;
+constexpr unsigned kUnset = ~0u;
 
-__device__ __forceinline__ void publish_run(float2* at, const Run& r) {
-  const float2 a = f2_unpack(r.a), h = f2_unpack(r.h);
-  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(at), "l"(f2_pack(a.x, h.x)), "l"(f2_pack(a.y, h.y))
-               : "memory");
-}
 __device__ __forceinline__ unsigned ready_bits(float v) {
   const unsigned u = __float_as_uint(v);
-  return u == ~0u ? 0x7FFFFFFFu : u;  // a NaN that looks unset becomes another NaN
+  return u == kUnset ? 0x7FFFFFFFu : u;  // a NaN that looks unset becomes another NaN
 }
-__device__ __forceinline__ void publish_state(float* at, f2 state) {
+__device__ __forceinline__ void publish_run(float4* at, const Run& r) {
+  const float2 a = f2_unpack(r.a), h = f2_unpack(r.h);
+  asm volatile("st.relaxed.gpu.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(at), "r"(ready_bits(a.x)),
+               "r"(ready_bits(a.y)), "r"(ready_bits(h.x)), "r"(ready_bits(h.y))
+               : "memory");
+}
+__device__ __forceinline__ void publish_state(float2* at, f2 state) {
   const float2 h = f2_unpack(state);
   asm volatile("st.relaxed.gpu.global.v2.b32 [%0], {%1, %2};" ::"l"(at), "r"(ready_bits(h.x)), "r"(ready_bits(h.y))
                : "memory");
 }
+__device__ __forceinline__ bool is_set(f2 v) {
+  return static_cast<unsigned>(v) != kUnset && static_cast<unsigned>(v >> 32) != kUnset;
+}
+__device__ __forceinline__ bool is_set(const Run& r) { return is_set(r.a) && is_set(r.h); }
 
 // Whether a poll may go on: false once a second has passed since `t0` or another block gave up.
 __device__ __noinline__ bool keep_polling(int* ticket, int* dev_error, uint64_t t0) {
@@ -393,100 +470,188 @@ __device__ __noinline__ bool keep_polling(int* ticket, int* dev_error, uint64_t 
   return false;
 }
 
-__device__ __forceinline__ Run await_run(const float2* at, int* ticket, int* dev_error) {
-  unsigned long long u, v;
+__device__ __forceinline__ Run read_run(const float4* at) {
+  float2 a, h;
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(a.x), "=f"(a.y), "=f"(h.x), "=f"(h.y)
+               : "l"(at)
+               : "memory");
+  return {f2_of(a), f2_of(h)};
+}
+__device__ __forceinline__ Run await_run(const float4* at, int* ticket, int* dev_error) {
+  Run r;
   uint64_t t0 = 0;
   for (unsigned i = 0;; ++i) {
-    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(u), "=l"(v) : "l"(at) : "memory");
-    if (u != kUnset && v != kUnset) break;
+    r = read_run(at);
+    if (is_set(r)) break;
     if (i == 0) t0 = lap::globaltimer_ns();
     if ((i & 15u) == 15u && !keep_polling(ticket, dev_error, t0)) break;
   }
-  const float2 x = f2_unpack(u), y = f2_unpack(v);
-  return {f2_pack(x.x, y.x), f2_pack(x.y, y.y)};
+  return r;
 }
 
-__device__ __forceinline__ f2 await_state(const float* at, int* ticket, int* dev_error) {
+__device__ __forceinline__ f2 await_state(const float2* at, int* ticket, int* dev_error) {
   unsigned u, v;
+  f2 h;
   uint64_t t0 = 0;
   for (unsigned i = 0;; ++i) {
     asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];" : "=r"(u), "=r"(v) : "l"(at) : "memory");
-    if (u != ~0u && v != ~0u) break;
+    h = f2_pack(__uint_as_float(u), __uint_as_float(v));
+    if (is_set(h)) break;
     if (i == 0) t0 = lap::globaltimer_ns();
     if ((i & 15u) == 15u && !keep_polling(ticket, dev_error, t0)) break;
   }
-  return f2_pack(__uint_as_float(u), __uint_as_float(v));
+  return h;
 }
 
 // What a tile shares between its warps; two of them in turn, so that a warp may begin the next
 // tile while another still reads this one's.
+template <int kWarps>
 struct Exchange {
-  Run own[kWarps][32];  // each warp's rows
-  int next;             // the tile to load next
-  int fresh;            // the tile's first row begins a sequence
+  Run own[kWarps][32];      // each warp's rows
+  Run earlier[kWarps][32];  // the group's earlier tiles, or pieces of them, in order
+  f2 base[32];              // the state before the group (by chains: before the tile)
+  unsigned char late[8];    // per warp: a word it asked for had not been published in time
+  unsigned char begins[8];  // per warp: some of its rows begin a sequence
+  int fresh;                // the tile's first row does
 };
+template <int kWarps>
 struct ScanSmem {
-  Exchange turn[2];
-  Run earlier[kWarps][32];  // pieces of the group's earlier tiles, in order
-  f2 base[32];              // the state before the group
+  Exchange<kWarps> turn[2];
+  Tile tile[4];             // of this turn, the next two and the last
   uint64_t bar[kWarps][kStages];
-  int first;                // the block's first tile
   int abort;                // a load did not arrive
 };
 
 template <typename E, bool kBack, bool kTma>
 __host__ __device__ constexpr int scan_smem_bytes() {
-  return kStages * kWarps * Shape<E, kBack, kTma>::kStageBytes + static_cast<int>(sizeof(ScanSmem));
+  using S = Shape<E, kBack, kTma>;
+  return kStages * S::kStageBytes + static_cast<int>(sizeof(ScanSmem<S::kWarps>));
 }
 
+// The published words a tile needs: where it has more than kWarps earlier tiles in its group, each
+// warp composes a piece [lo, hi) of them.
+template <int kWarps>
+struct Needs {
+  int j, per, lo, hi;
+  template <typename E>
+  __device__ __forceinline__ Needs(const Params<E>& p, const Tile& q, int warp) {
+    j = q.j;
+    per = (j + kWarps - 1) / kWarps;
+    lo = min(j, warp * per);
+    hi = min(j, lo + per);
+  }
+  // The run of the group's i-th tile (tiles are numbered in walking order within a sequence).
+  template <typename E>
+  __device__ __forceinline__ float4* run(const Params<E>& p, const Tile& q, int i, int lane) const {
+    return p.runs + (static_cast<size_t>(q.n * p.per + q.i - j + i) * p.columns + q.column) * 32 + lane;
+  }
+  // The state after this tile's group, or after the one `back` before it.
+  template <typename E>
+  __device__ __forceinline__ float2* state(const Params<E>& p, const Tile& q, int back, int lane) const {
+    return p.before + (static_cast<size_t>(q.n * p.groups + (q.i - j) / p.group - back) * p.columns + q.column) * 32 + lane;
+  }
+
+  // Asks for the words, where each warp needs one tile's (the last warp: the base too) ...
+  template <typename E>
+  __device__ __forceinline__ void ask(const Params<E>& p, Exchange<kWarps>& ex, const Tile& q, int warp, int lane) const {
+    if (per <= 1) {
+      if (lo < hi) copy16(lap::smem_u32(&ex.earlier[warp][lane]), run(p, q, lo, lane));
+      if (warp == kWarps - 1 && q.i > j && lane % 2 == 0)  // for two lanes: past the L1, which is not coherent
+        copy16(lap::smem_u32(&ex.base[lane]), state(p, q, 1, lane));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // ... and notes what has not come.
+  __device__ __forceinline__ void look(Exchange<kWarps>& ex, const Tile& q, int warp, int lane) const {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+    unsigned late = per > 1;
+    if (per <= 1) {
+      const bool run_ok = lo >= hi || is_set(ex.earlier[warp][lane]);
+      bool base_ok = true;
+      if (warp == kWarps - 1) {
+        if (q.i == j) ex.base[lane] = f2_all(0.f);
+        else base_ok = is_set(ex.base[lane]);
+      }
+      late = !__all_sync(0xFFFFFFFFu, run_ok && base_ok);
+    }
+    if (lane == 0) ex.late[warp] = static_cast<unsigned char>(late);
+  }
+  // The warp's piece and (the last warp) the base, by polling, up to four words at once.
+  template <typename E>
+  __device__ __forceinline__ void poll(const Params<E>& p, Exchange<kWarps>& ex, const Tile& q, int warp, int lane) const {
+    if (lo < hi) {
+      Run r = await_run(run(p, q, lo, lane), p.ticket, p.dev_error);
+#pragma unroll 1
+      for (int i = lo + 1; i < hi; i += 4) {
+        Run w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = read_run(run(p, q, min(i + k, hi - 1), lane));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (i + k >= hi) break;
+          if (!is_set(w[k])) w[k] = await_run(run(p, q, i + k, lane), p.ticket, p.dev_error);
+          r = compose(r, w[k]);
+        }
+      }
+      ex.earlier[warp][lane] = r;
+    }
+    if (warp == kWarps - 1)
+      ex.base[lane] = q.i > j ? await_state(state(p, q, 1, lane), p.ticket, p.dev_error) : f2_all(0.f);
+  }
+};
+
 // The state before this warp's rows.  `mine` (in ex.own already) is the composition of the warp's
-// rows; t the tile in walking order.  Publishes the tile for those that follow.
-template <typename E>
-__device__ __forceinline__ f2 state_before(const Params<E>& p, ScanSmem& sm, Exchange& ex, const Run& mine, int t,
-                                           int column, int warp, int lane) {
+// rows.  Where tiles wait for one another, publishes the tile for those that follow; else leaves the
+// state after it in `next`, the exchange of the block's next tile.
+template <typename E, int kWarps>
+__device__ __forceinline__ f2 state_before(const Params<E>& p, Exchange<kWarps>& ex, Exchange<kWarps>& next,
+                                           const Tile& q, const Run& mine, int warp, int lane) {
   f2 before = f2_all(0.f);
-  if (p.ticket) {
-    const size_t width = static_cast<size_t>(p.columns) * kCols;
-    const size_t at = static_cast<size_t>(column) * kCols + 2 * lane;
-    const int group = t / p.group, j = t - group * p.group;
-    const bool last = j == p.group - 1;
+  const bool fresh = __any_sync(0xFFFFFFFFu, ex.fresh);
+  if (p.runs) {
+    const Needs<kWarps> needs(p, q, warp);
+    const bool last = needs.j == p.group - 1;
     Run whole;
     if (warp == 0) {
       whole = mine;
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) whole = compose(whole, ex.own[w][lane]);
-      if (!last) publish_run(p.runs + t * width + at, whole);
+      if (!last) publish_run(needs.run(p, q, needs.j, lane), whole);
     }
-    if (!ex.fresh) {
-      // this warp's piece of the earlier tiles
-      const int per = (j + kWarps - 1) / kWarps, lo = min(j, warp * per), hi = min(j, lo + per);
-      const size_t g0 = static_cast<size_t>(group) * p.group;
-      if (lo < hi) {
-        Run q = await_run(p.runs + (g0 + lo) * width + at, p.ticket, p.dev_error);
-#pragma unroll 1
-        for (int i = lo + 1; i < hi; ++i) q = compose(q, await_run(p.runs + (g0 + i) * width + at, p.ticket, p.dev_error));
-        sm.earlier[warp][lane] = q;
+    if (!fresh) {
+      if (*reinterpret_cast<const unsigned long long*>(ex.late) != 0ull) {
+        if (ex.late[warp]) needs.poll(p, ex, q, warp, lane);
+        __syncthreads();
       }
-      if (warp == kWarps - 1)
-        sm.base[lane] = group == 0 ? before : await_state(p.before + (group - 1) * width + at, p.ticket, p.dev_error);
-      __syncthreads();
-      before = sm.base[lane];
-      const int pieces = j == 0 ? 0 : (j + per - 1) / per;
-#pragma unroll 1
-      for (int i = 0; i < pieces; ++i) before = apply(sm.earlier[i][lane], before);
+      before = ex.base[lane];
+      const int pieces = needs.per <= 1 ? needs.j : (needs.j + needs.per - 1) / needs.per;
+#pragma unroll 2
+      for (int i = 0; i < pieces; ++i) before = apply(ex.earlier[i][lane], before);
     }
-    if (warp == 0 && last) publish_state(p.before + group * width + at, apply(whole, before));
+    if (warp == 0 && last) publish_state(needs.state(p, q, 0, lane), apply(whole, before));
+  } else if (!fresh) {
+    before = ex.base[lane];
   }
+  if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<const unsigned long long*>(ex.begins) != 0ull)) {
 #pragma unroll 1
-  for (int w = 0; w < warp; ++w) before = apply(ex.own[w][lane], before);
+    for (int w = 0; w < warp; ++w) before = apply(ex.own[w][lane], before);
+  } else {
+#pragma unroll 4
+    for (int w = 0; w < warp; ++w) before = f2_fma(ex.own[w][lane].a, before, ex.own[w][lane].h);
+  }
+  if (!p.runs && warp == kWarps - 1) next.base[lane] = apply(mine, before);
   return before;
 }
 
-// The final states of the empty sequences that lie in this tile: their initial ones.
-template <typename E, bool kTma>
-__device__ __forceinline__ void empty_sequences(const Params<E>& p, int tile, const Lane<kTma>& l, int warp) {
-  if (!p.finish || (!p.cu_seqlens && p.T > 0)) return;
-  const int lo = p.cu_seqlens ? p.first_seq[tile] : 0, hi = p.cu_seqlens ? p.first_seq[tile + 1] : p.N;
+// The final states of the empty sequences that lie in this tile, or the tile's own: their initial
+// ones.
+template <int kWarps, typename E, bool kTma>
+__device__ __forceinline__ void empty_sequences(const Params<E>& p, const Tile& q, const Lane<kTma>& l, int warp) {
+  if (!p.finish || q.length > 0 || (!p.cu_seqlens && p.T > 0)) return;
+  const int lo = q.length == 0 ? q.n : p.cu_seqlens ? p.places[q.t].x : 0;
+  const int hi = q.length == 0 ? q.n + 1 : p.cu_seqlens ? p.places[q.t + 1].x : p.N;
   for (int n = lo + warp; n < hi; n += kWarps) {
     if (p.cu_seqlens && p.cu_seqlens[n] != p.cu_seqlens[n + 1]) continue;
     const int slot = slot_of(p, n);
@@ -496,13 +661,16 @@ __device__ __forceinline__ void empty_sequences(const Params<E>& p, int tile, co
 
 // ---------------------------------------------------------------- the forward scan
 
-// a = lambda and b = beta sig(g) x of one token.
+// a = lambda and b = beta sig(g) x of one token.  With w = beta^2 and q = 1 / sig(g), b is
+// w x / sqrt(w q^2): one rsqrt stands for beta's root and the gate's reciprocal (the special
+// function unit is what bounds this kernel after memory).  q^2 overflows below g = -44, where b
+// becomes 0 (2^-63 of beta x at most).
+template <bool kSmall>
 __device__ __forceinline__ void step2(f2 slope, f2 x, f2 r, f2 g, f2* a, f2* b) {
-  const f2 m = one_minus_lambda2(f2_mul(slope, sigmoid2(r)));
-  f2 w;
-  const f2 inv = inverse_beta2(m, &w);
+  const f2 m = one_minus_lambda2<kSmall>(f2_mul(slope, sigmoid2(r)));
+  const f2 w = one_minus_square2(m), q = inverse_sigmoid2(g);
   *a = f2_sub(f2_all(1.f), m);
-  *b = f2_mul(f2_mul(f2_mul(w, inv), sigmoid2(g)), x);
+  *b = f2_mul(f2_mul(w, x), rsqrt2(f2_mul(w, f2_mul(q, q))));
 }
 
 template <typename E, bool kTma>
@@ -512,9 +680,10 @@ struct Forward {
   f2 a[K], b[K];
 
   // The warp's rows composed.  kEdges: some row begins or ends a sequence or belongs to none.
-  template <bool kEdges>
+  // `ask` runs when most rows are done.
+  template <bool kEdges, bool kSmall, typename F>
   __device__ __forceinline__ Run first(const Params<E>& p, const char* stage, int low, f2 slope, const Rows& rows,
-                                       const Lane<kTma>& l, int lane) {
+                                       const Lane<kTma>& l, int lane, F ask) {
     const View<E, false, kTma> x(p, stage, 0, low, lane), r(p, stage, 1, low, lane), g(p, stage, 2, low, lane);
     if constexpr (kEdges) {
 #pragma unroll
@@ -526,8 +695,9 @@ struct Forward {
     Run run{f2_all(1.f), f2_all(0.f)};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      if (k == S::kAsk) ask();
       f2 in;
-      step2(slope, x.get(k), r.get(k), g.get(k), &a[k], &in);
+      step2<kSmall>(slope, x.get(k), r.get(k), g.get(k), &a[k], &in);
       if constexpr (kEdges) {
         b[k] = f2_fma(a[k], b[k], in);
         if (rows.begin >> k & 1u) run = {f2_all(-0.f), f2_all(0.f)};
@@ -565,15 +735,16 @@ struct Backward {
   static constexpr int K = S::kRows;
   f2 sr[K], m[K];  // sig(r) and 1 - lambda; row k in walking order is row K - 1 - k of the stage
 
-  template <bool kEdges>
+  template <bool kEdges, typename F>
   __device__ __forceinline__ Run first(const Params<E>& p, const char* stage, int low, f2 slope, const Rows& rows,
-                                       const Lane<kTma>& l, int lane) {
+                                       const Lane<kTma>& l, int lane, F ask) {
     const View<E, true, kTma> r(p, stage, 1, low, lane), d(p, stage, 3, low, lane);
     Run run{f2_all(1.f), f2_all(0.f)};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      if (k == S::kAsk) ask();
       sr[k] = sigmoid2(r.get(K - 1 - k));
-      m[k] = one_minus_lambda2(f2_mul(slope, sr[k]));
+      m[k] = one_minus_lambda2<false>(f2_mul(slope, sr[k]));
       const f2 a = f2_sub(f2_all(1.f), m[k]);
       if constexpr (kEdges) {
         if (rows.begin >> k & 1u)
@@ -607,9 +778,9 @@ struct Backward {
         if (rows.end >> k & 1u) before = load_state(p.h0, slot, p.C, l);
       }
       const f2 G = f2_add(d.get(at), w), vx = x.get(at), sg = sigmoid2(g.get(at)), u = f2_mul(slope, sr[k]);
-      f2 beta;
-      f2 inv = inverse_beta2(m[k], &beta);
-      beta = f2_mul(beta, inv);
+      const f2 beta2 = one_minus_square2(m[k]);
+      f2 inv = rsqrt2(beta2);
+      const f2 beta = f2_mul(beta2, inv);
       const float2 vu = f2_unpack(u), vi = f2_unpack(inv);
       inv = f2_pack(vu.x > 0.f ? vi.x : 0.f, vu.y > 0.f ? vi.y : 0.f);
       const f2 lambda = f2_sub(one, m[k]);
@@ -632,18 +803,23 @@ struct Backward {
 
 // ---------------------------------------------------------------- the scan kernel
 
+// Blocks are persistent and take tiles one after another.
+// By tiles (`runs`: long scans over few channels, packed batches of short sequences): by tickets in
+// walking order, all channels of a place before the next, the sequences of a fixed-length batch
+// side by side; the states pass from block to block.
+// By chains: all tiles of a sequence's channels in order, the state passing in shared memory and no
+// block waiting for another; chains in turn, or by tickets the longest first (packed).
+// Tiles of several whole sequences: in turn.
 template <typename E, bool kBack, bool kTma>
-__global__ void __launch_bounds__(kScanThreads, Shape<E, kBack, kTma>::kBlocks)
+__global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBack, kTma>::kBlocks)
     gated_scan_kernel(const __grid_constant__ Params<E> p, const __grid_constant__ Maps maps) {
   using S = Shape<E, kBack, kTma>;
-  constexpr int K = S::kRows;
+  constexpr int K = S::kRows, kWarps = S::kWarps;
   extern __shared__ __align__(128) char shared[];
-  ScanSmem& sm = *reinterpret_cast<ScanSmem*>(shared + kStages * kWarps * S::kStageBytes);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  char* stages = shared + warp * kStages * S::kStageBytes;
-  const int total = p.tiles * p.columns;
-  // Blocks that have one tile each take no second one ahead of a block that starts later.
-  const bool several = total > static_cast<int>(gridDim.x);
+  ScanSmem<kWarps>& sm = *reinterpret_cast<ScanSmem<kWarps>*>(shared + kStages * S::kStageBytes);
+  // uniform in the warp, and known to be
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  const int mine = (kBack ? kWarps - 1 - warp : warp) * K;  // the warp's first row in a stage
 
   if (threadIdx.x == 0) {
     sm.abort = 0;
@@ -652,95 +828,172 @@ __global__ void __launch_bounds__(kScanThreads, Shape<E, kBack, kTma>::kBlocks)
       lap::fence_mbar_init();
     }
   }
+  if (threadIdx.x < 2) {
+    for (int w = 0; w < 8; ++w) sm.turn[threadIdx.x].late[w] = sm.turn[threadIdx.x].begins[w] = 0;
+  }
   lap::griddep_wait();
   lap::griddep_launch_dependents();
 
-  // a tile's number is its place in walking order times `columns`, plus its column; -1: none
-  auto take = [&](int turn) {
-    const int id = p.ticket ? atomicAdd(p.ticket, 1) : static_cast<int>(blockIdx.x) + turn * static_cast<int>(gridDim.x);
-    return id < total ? id : -1;
+  // Thread 0's: the number of the next tile or chain (asked for early, looked at late), and the tile.
+  const int total = (p.order ? p.ticket[2] : p.tiles) * p.columns;
+  Tile chain{0, 0, 0, 0, 0, 0, 0, 0};
+  int step = 0, steps = 0, turns = static_cast<int>(blockIdx.x);
+  auto next_id = [&] {
+    if (p.runs || (p.order && step == steps)) return atomicAdd(p.ticket, 1);
+    return 0;
   };
-  auto lowest = [&](int id) {  // the warp's lowest row of a tile
-    const int t = id / p.columns;
-    return kBack ? (p.tiles - 1 - t) * p.stride + p.stride - 1 - warp * K - (K - 1) : t * p.stride + warp * K;
+  auto tile_of = [&](int id) -> Tile {
+    constexpr Tile kNone{-1, 0, 0, 0, 0, 0, 0, 0};
+    if (p.runs) {
+      if (id >= total) return kNone;
+      const int place = id / p.columns, column = id - place * p.columns;
+      const int i = p.per ? place / p.N : place, n = p.per ? place - i * p.N : 0;
+      const int at = kBack ? (p.per ? p.per : p.tiles) - 1 - i : i;
+      return {n * p.per + at, column, n, i, i % p.group, n * p.T + at * p.stride, at * p.stride, p.per ? p.T : -1};
+    }
+    if (step == steps) {  // the next chain
+      if (!p.order) {
+        id = turns;
+        turns += static_cast<int>(gridDim.x);
+      }
+      const int place = id / p.columns;
+      if (p.order ? id >= total : place >= (p.per ? p.N : p.tiles)) return kNone;
+      chain.column = id - place * p.columns;
+      chain.t = p.order ? p.order[place] : place;
+      chain.n = p.order || p.per ? chain.t : 0;
+      chain.row = p.order ? p.cu_seqlens[chain.n] : place * (p.per ? p.T : p.stride);
+      chain.length = p.order ? p.cu_seqlens[chain.n + 1] - chain.row : p.per ? p.T : -1;
+      step = 0;
+      steps = chain.length <= p.stride ? 1 : (chain.length + p.stride - 1) / p.stride;
+    }
+    Tile q = chain;
+    q.i = step;
+    q.token = (kBack ? steps - 1 - step : step) * p.stride;
+    q.row += q.token;
+    ++step;
+    return q;
   };
   int loaded = -1;  // the last turn whose tile has been asked for
-  auto load = [&](int id, int turn) {
-    if (id >= 0) {
-      fetch<kBack, kTma>(p, maps, stages + turn % kStages * S::kStageBytes, &sm.bar[warp][turn % kStages], lowest(id),
-                         id % p.columns, lane);
+  auto load = [&](int turn) {
+    const Tile& q = sm.tile[turn & 3];
+    if (q.t >= 0) {
+      if (!kTma || lane == 0)
+        fetch<kBack, kTma>(p, maps, shared + turn % kStages * S::kStageBytes, &sm.bar[warp][turn % kStages],
+                           q.row + (kBack ? p.stride - S::kTileRows : 0), q.column, mine, lane);
       loaded = turn;
     } else if constexpr (!kTma) {
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   };
+  // What has_edges wants to know of a tile, a turn ahead of its use.
+  auto look_up = [&](const Tile& q) {
+    if (q.t < 0) return 0;
+    if (q.length >= 0) return p.state_indices ? p.state_indices[q.n] : q.n;
+    return p.places ? p.places[q.t].y : 0;
+  };
 
-  if (threadIdx.x == 0) sm.first = take(0);
-  __syncthreads();
-  int id = sm.first, id1 = -1;
-  load(id, 0);
-  if (several) {
-    if (threadIdx.x == 0) sm.turn[1].next = take(1);
-    __syncthreads();
-    id1 = sm.turn[1].next;
+  if (threadIdx.x == 0) {
+    sm.tile[0] = tile_of(next_id());
+    // blocks that have one tile each take no second one ahead of a block that starts later
+    sm.tile[1] = p.runs && total <= static_cast<int>(gridDim.x) ? Tile{-1, 0, 0, 0, 0, 0, 0, 0} : tile_of(next_id());
   }
-  load(id1, 1);
+  __syncthreads();
+  load(0);
+  load(1);
+  int inside = look_up(sm.tile[0]);
+  f2 slope = load_state(p.slopes, 0, p.C, Lane<kTma>(sm.tile[0].column, lane, p.C));
+  f2 ds = f2_all(0.f);
 
-  for (int turn = 0; id >= 0; ++turn) {
-    Exchange& ex = sm.turn[turn & 1];
-    const int t = id / p.columns, column = id - t * p.columns, tile = kBack ? p.tiles - 1 - t : t;
-    const int low = lowest(id);
-    char* stage = stages + (turn % kStages) * S::kStageBytes;
-    int ahead = -1;
-    if (threadIdx.x == 0 && id1 >= 0) ahead = take(turn + 2);
-    const Lane<kTma> l(column, lane, p.C);
-    const Rows rows = rows_of<kBack, K>(p, tile, warp, lane);
-    constexpr unsigned kFull = (1u << K) - 1u;
-    const bool edges = rows.live != kFull || rows.begin || rows.end;
-    const f2 slope = load_state(p.slopes, 0, p.C, l);
+  for (int turn = 0;; ++turn) {
+    Tile q = sm.tile[turn & 3];  // uniform, and known to be
+    q.t = __shfl_sync(0xFFFFFFFFu, q.t, 0);
+    q.column = __shfl_sync(0xFFFFFFFFu, q.column, 0);
+    q.n = __shfl_sync(0xFFFFFFFFu, q.n, 0);
+    q.i = __shfl_sync(0xFFFFFFFFu, q.i, 0);
+    q.j = __shfl_sync(0xFFFFFFFFu, q.j, 0);
+    q.row = __shfl_sync(0xFFFFFFFFu, q.row, 0);
+    q.token = __shfl_sync(0xFFFFFFFFu, q.token, 0);
+    q.length = __shfl_sync(0xFFFFFFFFu, q.length, 0);
+    if (q.t < 0) break;
+    Exchange<kWarps>& ex = sm.turn[turn & 1];
+    const Tile& then = sm.tile[(turn + 1) & 3];
+    const bool more = threadIdx.x == 0 && then.t >= 0;
+    const int ahead = more ? next_id() : 0;
+    const int next_inside = look_up(then);
+    const f2 next_slope = load_state(p.slopes, 0, p.C, Lane<kTma>(then.column, lane, p.C));
+    const bool edges = __any_sync(0xFFFFFFFFu, has_edges<kBack, K>(p, q, inside, warp));
+    const int low = q.row + (kBack ? p.stride - S::kTileRows : 0) + mine;
+    const char* stage = shared + turn % kStages * S::kStageBytes + mine * S::kPitch;
+    auto ask = [&] {
+      if (p.runs) Needs<kWarps>(p, q, warp).ask(p, ex, q, warp, lane);
+    };
+    unsigned begins = 0u;
+    auto close = [&](const Run& run) {  // the warp's rows are composed
+      ex.own[warp][lane] = run;
+      if (lane == 0) ex.begins[warp] = begins != 0u;
+      if (threadIdx.x == 0) {
+        sm.tile[(turn + 2) & 3] = more ? tile_of(ahead) : Tile{-1, 0, 0, 0, 0, 0, 0, 0};
+        ex.fresh = q.length >= 0 ? q.i == 0 : begins & 1u;
+      }
+      if (p.runs) Needs<kWarps>(p, q, warp).look(ex, q, warp, lane);
+    };
     const bool here = arrived<kTma>(&sm.bar[warp][turn % kStages], turn / kStages, &sm.abort);
-    if (threadIdx.x == 0) {
-      ex.next = ahead;
-      ex.fresh = rows.begin & 1u;
-    }
-    int id2 = -1;
     if constexpr (!kBack) {
       Forward<E, kTma> f;
-      const Run run = edges ? f.template first<true>(p, stage, low, slope, rows, l, lane)
-                            : f.template first<false>(p, stage, low, slope, rows, l, lane);
-      ex.own[warp][lane] = run;
+      // u <= slope: where all of the tile's slopes are small, so is every u
+      const float2 s = f2_unpack(slope);
+      const bool small = __all_sync(0xFFFFFFFFu, s.x < kNear && s.y < kNear);
+      Run run;
+      if (edges) {
+        const Rows rows = rows_of<kBack, K>(p, q, warp, lane);
+        begins = rows.begin;
+        run = f.template first<true, false>(p, stage, low, slope, rows, Lane<kTma>(q.column, lane, p.C), lane, ask);
+      } else if (small) {
+        run = f.template first<false, true>(p, stage, low, slope, Rows{}, Lane<kTma>(q.column, lane, p.C), lane, ask);
+      } else {
+        run = f.template first<false, false>(p, stage, low, slope, Rows{}, Lane<kTma>(q.column, lane, p.C), lane, ask);
+      }
+      close(run);
       if (__syncthreads_or(!here)) break;
-      id2 = ex.next;
-      load(id2, turn + kStages);  // this tile's rows are in registers: their stage takes the tile after next
-      const f2 h = state_before(p, sm, ex, run, t, column, warp, lane);
-      if (edges) f.template second<true>(p, low, h, rows, l);
-      else f.template second<false>(p, low, h, rows, l);
+      load(turn + kStages);  // every warp has this tile's rows in registers: its stage takes the tile after next
+      const f2 h = state_before(p, ex, sm.turn[(turn + 1) & 1], q, run, warp, lane);
+      if (edges)
+        f.template second<true>(p, low, h, rows_of<kBack, K>(p, q, warp, lane), Lane<kTma>(q.column, lane, p.C));
+      else
+        f.template second<false>(p, low, h, Rows{}, Lane<kTma>(q.column, lane, p.C));
     } else {
       Backward<E, kTma> f;
-      const Run run = edges ? f.template first<true>(p, stage, low, slope, rows, l, lane)
-                            : f.template first<false>(p, stage, low, slope, rows, l, lane);
-      ex.own[warp][lane] = run;
+      const Lane<kTma> l(q.column, lane, p.C);
+      Run run;
+      if (edges) {
+        const Rows rows = rows_of<kBack, K>(p, q, warp, lane);
+        begins = rows.begin;
+        run = f.template first<true>(p, stage, low, slope, rows, l, lane, ask);
+      } else {
+        run = f.template first<false>(p, stage, low, slope, Rows{}, l, lane, ask);
+      }
+      close(run);
       if (__syncthreads_or(!here)) break;
-      id2 = ex.next;
-      const f2 w = state_before(p, sm, ex, run, t, column, warp, lane);
-      const f2 ds = edges ? f.template second<true>(p, stage, low, slope, w, rows, l, lane)
-                          : f.template second<false>(p, stage, low, slope, w, rows, l, lane);
-      __syncwarp();
-      load(id2, turn + kStages);
-      // the tile's terms of dslopes, warps in order
+      const f2 w = state_before(p, ex, sm.turn[(turn + 1) & 1], q, run, warp, lane);
+      const f2 sum = edges ? f.template second<true>(p, stage, low, slope, w, rows_of<kBack, K>(p, q, warp, lane), l, lane)
+                           : f.template second<false>(p, stage, low, slope, w, Rows{}, l, lane);
+      ds = f2_add(ds, sum);
       __syncthreads();
-      ex.own[warp][lane].h = ds;
-      __syncthreads();
-      if (warp == 0) {
-        f2 sum = ds;
+      load(turn + kStages);
+      if (p.runs || (q.i + 1) * p.stride >= q.length) {  // the end of a tile or chain: its terms of dslopes, warps in order
+        ex.own[warp][lane].h = ds;
+        __syncthreads();
+        if (warp == 0) {
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) sum = f2_add(sum, ex.own[i][lane].h);
-        store_state(p.part, tile, p.C, l, sum);
+          for (int i = 1; i < kWarps; ++i) ds = f2_add(ds, ex.own[i][lane].h);
+          store_state(p.part, q.t, p.C, l, ds);
+        }
+        ds = f2_all(0.f);
       }
     }
-    empty_sequences(p, tile, l, warp);
-    id = id1;
-    id1 = id2;
+    if (edges) empty_sequences<kWarps>(p, q, Lane<kTma>(q.column, lane, p.C), warp);
+    inside = next_inside;
+    slope = next_slope;
   }
   if constexpr (kTma) {
     if (sm.abort && lane == 0) {  // a load did not arrive in time: tell the others, outlive the copies in flight

@@ -93,26 +93,32 @@ __device__ __forceinline__ f2 f2_each(f2 v, F f) {
   return f2_pack(f(t.x), f(t.y));
 }
 
-__device__ __forceinline__ f2 sigmoid2(f2 z) {
+// 1 + exp(-z): the reciprocal of sig(z).
+__device__ __forceinline__ f2 inverse_sigmoid2(f2 z) {
   const f2 e = f2_each(f2_mul(z, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
-  return f2_each(f2_add(e, f2_all(1.f)), [](float v) { return rcp_approx(v); });
+  return f2_add(e, f2_all(1.f));
+}
+__device__ __forceinline__ f2 sigmoid2(f2 z) {
+  return f2_each(inverse_sigmoid2(z), [](float v) { return rcp_approx(v); });
 }
 
-// m = 1 - lambda of two channels.
+// m = 1 - lambda of two channels.  kSmall: u < kNear is known.
+template <bool kSmall>
 __device__ __forceinline__ f2 one_minus_lambda2(f2 u) {
   f2 p = f2_fma(u, f2_all(kC3), f2_all(kC2));
   p = f2_fma(u, p, f2_all(kC1));
   p = f2_fma(u, p, f2_all(1.f));
-  const float2 near = f2_unpack(f2_mul(u, p));
+  const f2 near = f2_mul(u, p);
+  if constexpr (kSmall) return near;
   const f2 e = f2_each(f2_mul(u, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
-  const float2 far = f2_unpack(f2_sub(f2_all(1.f), e)), v = f2_unpack(u);
-  return f2_pack(v.x < kNear ? near.x : far.x, v.y < kNear ? near.y : far.y);
+  const float2 n = f2_unpack(near), far = f2_unpack(f2_sub(f2_all(1.f), e)), v = f2_unpack(u);
+  return f2_pack(v.x < kNear ? n.x : far.x, v.y < kNear ? n.y : far.y);
 }
 
-// rsqrt(w) of w = 1 - lambda^2 = m (2 - m), and w itself.
-__device__ __forceinline__ f2 inverse_beta2(f2 m, f2* w) {
-  *w = f2_mul(m, f2_sub(f2_all(2.f), m));
-  return f2_each(*w, [](float v) { return rsqrt_approx(fmaxf(v, kLeast)); });
+// 1 - lambda^2 = m (2 - m).
+__device__ __forceinline__ f2 one_minus_square2(f2 m) { return f2_mul(m, f2_sub(f2_all(2.f), m)); }
+__device__ __forceinline__ f2 rsqrt2(f2 w) {
+  return f2_each(w, [](float v) { return rsqrt_approx(fmaxf(v, kLeast)); });
 }
 
 }  // namespace lag

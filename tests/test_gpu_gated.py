@@ -362,19 +362,82 @@ def test_offsets_past_32_bits():
     assert all(torch.equal(a, b) for a, b in zip(got[:4], want[:4]))
 
 
-def test_row_strides_alignment_and_odd_columns_agree_bitwise():
-    """The same values at any alignment and stride give the same bits."""
-    b = Batch(12, lens=[333, 70], C=64, pool=2)
-    o, hf = b.fwd()
-    for off, ld in ((0, 64 + 8), (1, 67), (2, 66), (4, 72), (8, 80)):
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_row_strides_and_alignment(dtype):
+    """The same values at any alignment and stride: each within its bound (16-byte rows are cut into
+    other tiles than the rest, and a sum's order follows the tiles, so the bits may differ)."""
+    b = Batch(12, lens=[333, 70], C=64, pool=2, dtype=dtype)
+    dout = b.mat()
+    want = b.fwd()[0]
+    grads = lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, want, dout, h0=b.h0, **b.kw)
+    for off, ld in ((0, 64 + 8), (1, 67), (2, 66), (4, 72), (8, 80), (3, 65)):
         views = []
-        for t in (b.x, b.r, b.g, b.blank()):
-            w = torch.zeros((b.tokens, ld + off), dtype=torch.bfloat16, device="cuda")
+        for t in (b.x, b.r, b.g, dout, *[b.blank() for _ in range(4)]):
+            w = torch.full((b.tokens, ld + off), 7.0, dtype=DT[dtype], device="cuda")
             v = w[:, off:off + 64]
             v.copy_(t)
-            views.append(v)
-        lap.la_gated_scan_fwd(*views[:3], b.slopes, h0=b.h0, o=views[3], **b.kw)
-        assert torch.equal(views[3], o), (off, ld)
+            views.append((w, v))
+        x, r, g, do, o, dx, dr, dg = (v for _, v in views)
+        lap.la_gated_scan_fwd(x, r, g, b.slopes, h0=b.h0, o=o, **b.kw)
+        lap.la_gated_scan_bwd(x, r, g, b.slopes, o, do, h0=b.h0, dx=dx, dr=dr, dg=dg, **b.kw)
+        for n in range(2):
+            s = b.rows(n)
+            ro, _, eo, _ = scan_one(f64(b.x[s]), f64(b.r[s]), f64(b.g[s]), f64(b.slopes), b.start(n))
+            near(o[s], ro, eo, dtype, f"o at offset {off}, stride {ld}")
+            ref = grad_one(f64(b.x[s]), f64(b.r[s]), f64(b.g[s]), f64(b.slopes), b.start(n), f64(o[s]), f64(dout[s]),
+                           np.zeros(64))
+            for t, name in ((dx, "dx"), (dr, "dr"), (dg, "dg")):
+                near(t[s], *ref[name], dtype, f"{name} at offset {off}, stride {ld}")
+        for w, _ in views[4:]:  # nothing beside the columns was written
+            assert (w[:, :off] == 7).all() and (w[:, off + 64:] == 7).all()
+
+
+CHAINS = [0, 600, 2000, 1, 517, 300, 1290, 128, 700, 64, 1025, 812, 0, 333, 901, 499]
+
+
+@pytest.mark.parametrize("dtype,back", [("bf16", False), ("bf16", True), ("fp32", False), ("fp32", True)])
+def test_packed_batches_by_chains(dtype, back):
+    """Wide packed batches of long sequences, which blocks take a sequence's channels at a time:
+    padded, empty and out-of-range sequences among them; checked on a range of channels."""
+    b = Batch(14, lens=CHAINS, C=4096, dtype=dtype, pool=20, pad=(4,))
+    b.slots[9] = 20
+    b.idx = b.kw["state_indices"] = torch.from_numpy(b.slots).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, hf = b.fwd(dev_error=err)
+    assert int(err) == lap.DEV_ERR_BAD_INDEX
+    b.slots[9] = -1
+    C, cols = 4096, slice(4000, 4064)
+    dout, dhf = (b.mat(), b.state()) if back else (None, None)
+    dh0 = torch.full_like(hf, float("nan"))
+    got = lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, dout, h0=b.h0, dh_final=dhf, dx=b.blank(), dr=b.blank(),
+                                dg=b.blank(), dh0=dh0, **b.kw) if back else None
+    dead = torch.ones(b.tokens, dtype=torch.bool, device="cuda")
+    sums = esum = terms = 0.0
+    for n, L in enumerate(CHAINS):
+        if b.slots[n] < 0:
+            continue
+        s, slot = b.rows(n), int(b.slots[n])
+        dead[s] = False
+        args = [f64(t[s, cols]) for t in (b.x, b.r, b.g)] + [f64(b.slopes[cols]), f64(b.h0[slot, cols])]
+        if not back:
+            ro, rh, eo, eh = scan_one(*args)
+            near(o[s, cols], ro, eo, dtype, f"o of sequence {n} ({L} tokens)")
+            near(hf[slot, cols], rh, eh, "fp32", f"h_final of sequence {n} ({L} tokens)")
+            continue
+        ref = grad_one(*args, f64(o[s, cols]), f64(dout[s, cols]), f64(dhf[slot, cols]))
+        for t, name in zip(got, ("dx", "dr", "dg")):
+            near(t[s, cols], *ref[name], dtype, f"{name} of sequence {n} ({L} tokens)")
+        near(dh0[slot, cols], *ref["dh0"], "fp32", f"dh0 of sequence {n} ({L} tokens)")
+        sums, esum, terms = sums + ref["ds"][0], esum + ref["ds"][1], terms + np.abs(ref["ds"][0])
+    if back:
+        near(got[3][cols], sums, esum + len(CHAINS) * 2.0 ** -24 * terms, "fp32", "dslopes")
+        assert all(torch.isnan(t[dead]).all() for t in got[:3])
+    else:
+        assert torch.isnan(o[dead]).all()
+        b.kw["cu_seqlens"] = b.cu_dev.flip(0).contiguous()
+        err.zero_()
+        o, hf = b.fwd(dev_error=err)
+        assert int(err) & lap.DEV_ERR_BAD_SEQLENS and torch.isnan(o).all() and torch.isnan(hf).all()
 
 
 # ---------------------------------------------------------------- decode, verify, commit
