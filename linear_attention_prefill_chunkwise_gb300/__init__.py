@@ -500,103 +500,113 @@ def la_commit(state, kbuf, vbuf, accepted_len, slopes, state_indices=None, dev_e
 
 # ---- rows of channels: the gated recurrence (include/la_gated.h) and the RMS norm (include/la_norm.h)
 
+# These calls serve single tokens too, where the host side is most of the time: each check is one
+# expression that holds for a good argument, and the reasons are sorted out only when it fails.
+
 def _matrix(t, name):
-    """Checks of a call's leading activation matrix; returns (la_dtype, rows, C, row stride)."""
+    """Checks of a call's leading activation matrix; returns (la_dtype, shape, rows, C, device, row stride)."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is torch.bfloat16:
+    dtype, shape = t.dtype, t.shape
+    if dtype is torch.bfloat16:
         code = 0
-    elif t.dtype is torch.float32:
+    elif dtype is torch.float32:
         code = 1
     else:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got shape {tuple(t.shape)}")
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dims, got shape {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    rows, C = t.shape
+    rows, C = shape
     if C < 1:
         raise ValueError(f"{name} must have at least one column")
-    return code, rows, C, _row_stride(t, name, rows, C)
+    return code, shape, rows, C, t.get_device(), _stride(t, name, rows, C)
 
 
-def _row_stride(t, name, rows, C):
+def _stride(t, name, rows, C):
     s0, s1 = t.stride()
+    if s1 == 1 and s0 >= C:
+        return s0
     if s1 != 1 and C > 1 and rows > 0:
         raise ValueError(f"the columns of {name} must be contiguous")
     if rows <= 1:
         return C
-    if s0 < C:
-        raise ValueError(f"the row stride of {name} must be at least its {C} columns, got {s0}")
-    return s0
+    raise ValueError(f"the row stride of {name} must be at least its {C} columns, got {s0}")
 
 
-def _rows_like(t, name, like, dtype=None):
-    """Checks a matrix of the leading one's shape, type and device; returns its row stride."""
+def _like(t, name, shape, dtype, dev):
+    """Row stride of a matrix that must have this shape, type and device."""
+    import torch
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        s0, s1 = t.stride()
+        return s0 if s1 == 1 and s0 >= shape[1] else _stride(t, name, *shape)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _array(t, name, dtype, shape, dev):
+    """Pointer of a contiguous tensor that must have this shape (None in it: any size), or None."""
+    if t is None:
+        return None
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not (dtype or like.dtype):
-        raise TypeError(f"{name} must be {dtype or like.dtype}, got {t.dtype}")
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    return _row_stride(t, name, *t.shape)
-
-
-def _on_device(t, name, dtype, shape, like):
-    """Checks an optional contiguous tensor; a None in ``shape`` stands for any size."""
-    if t is None:
-        return
+    have = t.shape
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and len(have) == len(shape):
+        if have == shape or all(w is None or h == w for h, w in zip(have, shape)):
+            return t.data_ptr()
+        raise ValueError(f"{name} must have shape {['any' if w is None else w for w in shape]}, got {tuple(have)}")
     _check(t, name, dtype, len(shape))
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    for have, want in zip(t.shape, shape):
-        if want is not None and have != want:
-            raise ValueError(f"{name} must have shape {['any' if w is None else w for w in shape]}, "
-                             f"got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
-def _empty(shape, dtype, like, stream):
-    """A new tensor whose memory belongs to the stream that the call runs on."""
+def _raw_stream(dev):
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream, like), device=like.device)):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _stream(stream, like):
-    import torch
+def _stream_of(stream, dev):
     if stream is None:
-        return torch.cuda.current_stream(like.device).cuda_stream
+        return _raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _call(fn, like, *args):
-    """Call a C entry point with ``like``'s device current; raise on a non-OK status."""
+def _empty(shape, dtype, dev, stream):
+    """A new tensor whose memory belongs to the stream that the call runs on."""
     import torch
-    if like.device.index == torch.cuda.current_device():
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_of(stream, dev), device=dev)):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _call(fn, dev, *args):
+    """Call a C entry point with device ``dev`` current; raise on a non-OK status."""
+    import torch
+    if dev == torch.cuda.current_device():
         st = fn(*args)
     else:
-        with torch.cuda.device(like.device):
+        with torch.cuda.device(dev):
             st = fn(*args)
     if st != 0:
         _raise(load_library(), st)
 
 
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-def _gated_sequences(x, state_indices, cu_seqlens, seq_len, pools):
-    """Batch mode of a gated scan; returns (B, T, N, pool size)."""
+def _gated_sequences(tokens, C, dev, state_indices, cu_seqlens, seq_len, pools):
+    """Batch mode of a gated scan; returns (B, T, N, pool size) and the pointers of state_indices,
+    cu_seqlens and the pools."""
     import torch
-    tokens, C = x.shape
+    cu = None
     if cu_seqlens is not None:
-        _on_device(cu_seqlens, "cu_seqlens", torch.int32, (None,), x)
+        cu = _array(cu_seqlens, "cu_seqlens", torch.int32, (None,), dev)
         N = cu_seqlens.shape[0] - 1
         if N < 0:
             raise ValueError("cu_seqlens must have N + 1 entries")
@@ -610,13 +620,12 @@ def _gated_sequences(x, state_indices, cu_seqlens, seq_len, pools):
         if tokens % T:
             raise ValueError("tokens must be a multiple of seq_len")
         B = N = tokens // T
-    pool = None
+    pool, ptrs = None, []
     for t, name in pools:
+        ptrs.append(_array(t, name, torch.float32, (pool, C), dev))
         if t is not None:
-            _on_device(t, name, torch.float32, (pool, C), x)
             pool = t.shape[0]
-    _on_device(state_indices, "state_indices", torch.int32, (N,), x)
-    return B, T, N, pool or 0
+    return B, T, N, pool or 0, _array(state_indices, "state_indices", torch.int32, (N,), dev), cu, ptrs
 
 
 @functools.lru_cache(maxsize=1024)
@@ -634,13 +643,16 @@ def la_gated_scan_workspace(B, T, N, C, packed, dtype, backward):
     return nbytes.value
 
 
-def _scan_workspace(workspace, x, B, T, N, C, packed, backward, stream):
+def _scan_workspace(workspace, dtype, dev, B, T, N, C, packed, backward, stream):
+    """(tensor that owns it, pointer, bytes) of a scan's workspace."""
     import torch
     if workspace is None:
-        nbytes = la_gated_scan_workspace(B, T, N, C, packed, x.dtype, backward)
-        return (None, 0) if nbytes == 0 else (_empty((nbytes,), torch.uint8, x, stream), nbytes)
-    _on_device(workspace, "workspace", torch.uint8, (None,), x)
-    return workspace, workspace.numel()
+        nbytes = la_gated_scan_workspace(B, T, N, C, packed, dtype, backward)
+        if nbytes == 0:
+            return None, None, 0
+        workspace = _empty(nbytes, torch.uint8, dev, stream)
+        return workspace, workspace.data_ptr(), nbytes
+    return workspace, _array(workspace, "workspace", torch.uint8, (None,), dev), workspace.numel()
 
 
 def la_gated_scan_fwd(x, r, g, slopes, h0=None, state_indices=None, cu_seqlens=None, o=None, h_final=None,
@@ -656,18 +668,19 @@ def la_gated_scan_fwd(x, r, g, slopes, h0=None, state_indices=None, cu_seqlens=N
     la_gated_scan_workspace(...) bytes, allocated here when None.  Returns ``o``."""
     import torch
     lib = load_library()
-    code, tokens, C, ldx = _matrix(x, "x")
-    ldr, ldg = _rows_like(r, "r", x), _rows_like(g, "g", x)
-    _on_device(slopes, "slopes", torch.float32, (C,), x)
-    B, T, N, pool = _gated_sequences(x, state_indices, cu_seqlens, seq_len, ((h0, "h0"), (h_final, "h_final")))
+    code, shape, tokens, C, dev, ldx = _matrix(x, "x")
+    dtype = x.dtype
+    ldr, ldg = _like(r, "r", shape, dtype, dev), _like(g, "g", shape, dtype, dev)
+    B, T, N, pool, idx, cu, (p0, pf) = _gated_sequences(tokens, C, dev, state_indices, cu_seqlens, seq_len,
+                                                        ((h0, "h0"), (h_final, "h_final")))
     if o is None:
-        o = _empty((tokens, C), x.dtype, x, stream)
-    ldo = _rows_like(o, "o", x)
-    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
-    workspace, nbytes = _scan_workspace(workspace, x, B, T, N, C, cu_seqlens is not None, False, stream)
-    _call(lib.la_gated_scan_fwd, x, x.data_ptr(), r.data_ptr(), g.data_ptr(), _p(slopes), _p(h0), _p(state_indices),
-          _p(cu_seqlens), o.data_ptr(), _p(h_final), ldx, ldr, ldg, ldo, B, T, N, C, pool, code, _p(workspace), nbytes,
-          _p(dev_error), _stream(stream, x))
+        o, ldo = _empty(shape, dtype, dev, stream), C
+    else:
+        ldo = _like(o, "o", shape, dtype, dev)
+    owner, ws, nbytes = _scan_workspace(workspace, dtype, dev, B, T, N, C, cu is not None, False, stream)
+    _call(lib.la_gated_scan_fwd, dev, x.data_ptr(), r.data_ptr(), g.data_ptr(),
+          _array(slopes, "slopes", torch.float32, (C,), dev), p0, idx, cu, o.data_ptr(), pf, ldx, ldr, ldg, ldo, B, T, N, C,
+          pool, code, ws, nbytes, _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))
     return o
 
 
@@ -680,50 +693,52 @@ def la_gated_scan_bwd(x, r, g, slopes, o, dout, h0=None, dh_final=None, state_in
     sequences and unselected slots are not written.  The other arguments as la_gated_scan_fwd."""
     import torch
     lib = load_library()
-    code, tokens, C, ldx = _matrix(x, "x")
-    lds = [_rows_like(t, n, x) for t, n in ((r, "r"), (g, "g"), (o, "o"), (dout, "dout"))]
-    _on_device(slopes, "slopes", torch.float32, (C,), x)
-    B, T, N, pool = _gated_sequences(x, state_indices, cu_seqlens, seq_len,
-                                     ((h0, "h0"), (dh_final, "dh_final"), (dh0, "dh0")))
-    dx, dr, dg = (_empty((tokens, C), x.dtype, x, stream) if t is None else t for t in (dx, dr, dg))
-    lds += [_rows_like(t, n, x) for t, n in ((dx, "dx"), (dr, "dr"), (dg, "dg"))]
+    code, shape, tokens, C, dev, ldx = _matrix(x, "x")
+    dtype = x.dtype
+    lds = [_like(t, n, shape, dtype, dev) for t, n in ((r, "r"), (g, "g"), (o, "o"), (dout, "dout"))]
+    B, T, N, pool, idx, cu, (p0, pdf, pd0) = _gated_sequences(
+        tokens, C, dev, state_indices, cu_seqlens, seq_len, ((h0, "h0"), (dh_final, "dh_final"), (dh0, "dh0")))
+    dx, dr, dg = (_empty(shape, dtype, dev, stream) if t is None else t for t in (dx, dr, dg))
+    lds += [_like(t, n, shape, dtype, dev) for t, n in ((dx, "dx"), (dr, "dr"), (dg, "dg"))]
     if dslopes is None:
-        dslopes = _empty((C,), torch.float32, x, stream)
-    _on_device(dslopes, "dslopes", torch.float32, (C,), x)
-    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
-    workspace, nbytes = _scan_workspace(workspace, x, B, T, N, C, cu_seqlens is not None, True, stream)
-    _call(lib.la_gated_scan_bwd, x, x.data_ptr(), r.data_ptr(), g.data_ptr(), _p(slopes), _p(h0), o.data_ptr(),
-          dout.data_ptr(), _p(dh_final), _p(state_indices), _p(cu_seqlens), dx.data_ptr(), dr.data_ptr(),
-          dg.data_ptr(), dslopes.data_ptr(), _p(dh0), ldx, *lds, B, T, N, C, pool, code, _p(workspace), nbytes,
-          _p(dev_error), _stream(stream, x))
+        dslopes = _empty((C,), torch.float32, dev, stream)
+    owner, ws, nbytes = _scan_workspace(workspace, dtype, dev, B, T, N, C, cu is not None, True, stream)
+    _call(lib.la_gated_scan_bwd, dev, x.data_ptr(), r.data_ptr(), g.data_ptr(),
+          _array(slopes, "slopes", torch.float32, (C,), dev), p0, o.data_ptr(), dout.data_ptr(), pdf, idx, cu,
+          dx.data_ptr(), dr.data_ptr(), dg.data_ptr(), _array(dslopes, "dslopes", torch.float32, (C,), dev), pd0, ldx, *lds,
+          B, T, N, C, pool, code, ws, nbytes, _array(dev_error, "dev_error", torch.int32, (None,), dev),
+          _stream_of(stream, dev))
     return dx, dr, dg, dslopes, dh0
 
 
 def _gated_requests(x, r, g, slopes, state, T, state_indices, dev_error):
-    """Checks shared by the gated speculative-decoding ops; returns (code, B, C, ldx, ldr, ldg, P)."""
+    """Checks shared by the gated speculative-decoding ops; returns (shape, B, C, P, la_dtype, device,
+    pointers of slopes, state, state_indices and dev_error, row strides)."""
     import torch
-    code, tokens, C, ldx = _matrix(x, "x")
-    ldr, ldg = _rows_like(r, "r", x), _rows_like(g, "g", x)
+    code, shape, tokens, C, dev, ldx = _matrix(x, "x")
+    dtype = x.dtype
+    lds = ldx, _like(r, "r", shape, dtype, dev), _like(g, "g", shape, dtype, dev)
     if T < 1 or tokens % T:
         raise ValueError("T must be >= 1 and x must have B*T rows")
     B = tokens // T
-    _on_device(slopes, "slopes", torch.float32, (C,), x)
     if state is None:
         raise TypeError("state must be a torch.Tensor")
-    _on_device(state, "state", torch.float32, (None, C), x)
-    _on_device(state_indices, "state_indices", torch.int32, (B,), x)
-    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
-    return code, B, C, ldx, ldr, ldg, state.shape[0]
+    ptrs = (_array(slopes, "slopes", torch.float32, (C,), dev), _array(state, "state", torch.float32, (None, C), dev),
+            _array(state_indices, "state_indices", torch.int32, (B,), dev),
+            _array(dev_error, "dev_error", torch.int32, (None,), dev))
+    return shape, B, C, state.shape[0], code, dev, ptrs, lds
 
 
 def _gated_outputs(fn, x, r, g, slopes, state, T, state_indices, o, dev_error, stream):
     T = int(T)
-    code, B, C, ldx, ldr, ldg, P = _gated_requests(x, r, g, slopes, state, T, state_indices, dev_error)
+    shape, B, C, P, code, dev, (sl, st, idx, err), lds = _gated_requests(x, r, g, slopes, state, T, state_indices,
+                                                                         dev_error)
     if o is None:
-        o = _empty(x.shape, x.dtype, x, stream)
-    ldo = _rows_like(o, "o", x)
-    _call(fn, x, x.data_ptr(), r.data_ptr(), g.data_ptr(), _p(slopes), state.data_ptr(), _p(state_indices),
-          o.data_ptr(), ldx, ldr, ldg, ldo, B, T, C, P, code, _p(dev_error), _stream(stream, x))
+        o, ldo = _empty(shape, x.dtype, dev, stream), C
+    else:
+        ldo = _like(o, "o", shape, x.dtype, dev)
+    _call(fn, dev, x.data_ptr(), r.data_ptr(), g.data_ptr(), sl, st, idx, o.data_ptr(), *lds, ldo, B, T, C, P, code, err,
+          _stream_of(stream, dev))
     return o
 
 
@@ -745,29 +760,32 @@ def la_gated_commit(x, r, g, slopes, state, T, accepted_len, state_indices=None,
     its T tokens; 0 = untouched, T = bitwise what la_gated_decode leaves.  Returns ``state``."""
     import torch
     T = int(T)
-    code, B, C, ldx, ldr, ldg, P = _gated_requests(x, r, g, slopes, state, T, state_indices, dev_error)
+    shape, B, C, P, code, dev, (sl, st, idx, err), lds = _gated_requests(x, r, g, slopes, state, T, state_indices,
+                                                                         dev_error)
     if accepted_len is None:
         raise TypeError("accepted_len must be a torch.Tensor")
-    _on_device(accepted_len, "accepted_len", torch.int32, (B,), x)
-    _call(load_library().la_gated_commit, x, x.data_ptr(), r.data_ptr(), g.data_ptr(), _p(slopes), state.data_ptr(),
-          _p(state_indices), accepted_len.data_ptr(), ldx, ldr, ldg, B, T, C, P, code, _p(dev_error),
-          _stream(stream, x))
+    _call(load_library().la_gated_commit, dev, x.data_ptr(), r.data_ptr(), g.data_ptr(), sl, st, idx,
+          _array(accepted_len, "accepted_len", torch.int32, (B,), dev), *lds, B, T, C, P, code, err,
+          _stream_of(stream, dev))
     return state
 
 
 def _norm_inputs(x, weight, residual, residual_out, stream):
-    """Checks shared by the norm's forwards; returns (code, rows, C, residual_out, ldx, ldres, ldres_out)."""
+    """Checks shared by the norm's forwards; returns (la_dtype, shape, device, pointers of residual,
+    weight and residual_out, row strides of x, residual and residual_out, residual_out)."""
     import torch
-    code, rows, C, ldx = _matrix(x, "x")
-    _on_device(weight, "weight", torch.float32, (C,), x)
+    code, shape, rows, C, dev, ldx = _matrix(x, "x")
+    w = _array(weight, "weight", torch.float32, (C,), dev)
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
-        return code, rows, C, None, ldx, 0, 0
-    ldres = _rows_like(residual, "residual", x)
+        return code, shape, dev, (None, w, None), (ldx, 0, 0), None
+    ldres = _like(residual, "residual", shape, x.dtype, dev)
     if residual_out is None:
-        residual_out = _empty((rows, C), x.dtype, x, stream)
-    return code, rows, C, residual_out, ldx, ldres, _rows_like(residual_out, "residual_out", x)
+        residual_out, ldro = _empty(shape, x.dtype, dev, stream), C
+    else:
+        ldro = _like(residual_out, "residual_out", shape, x.dtype, dev)
+    return code, shape, dev, (residual.data_ptr(), w, residual_out.data_ptr()), (ldx, ldres, ldro), residual_out
 
 
 def la_rms_norm_fwd(x, weight, eps, residual=None, y=None, residual_out=None, dev_error=None, stream=None):
@@ -778,13 +796,15 @@ def la_rms_norm_fwd(x, weight, eps, residual=None, y=None, residual_out=None, de
     itself.  Returns (y, residual_out); residual_out is None without a residual."""
     import torch
     lib = load_library()
-    code, rows, C, residual_out, ldx, ldres, ldro = _norm_inputs(x, weight, residual, residual_out, stream)
+    code, shape, dev, (res, w, ro), (ldx, ldres, ldro), residual_out = _norm_inputs(x, weight, residual, residual_out,
+                                                                                    stream)
+    rows, C = shape
     if y is None:
-        y = _empty((rows, C), x.dtype, x, stream)
-    ldy = _rows_like(y, "y", x)
-    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
-    _call(lib.la_rms_norm_fwd, x, x.data_ptr(), _p(residual), _p(weight), eps, y.data_ptr(), _p(residual_out), ldx,
-          ldres, ldy, ldro, rows, C, code, _p(dev_error), _stream(stream, x))
+        y, ldy = _empty(shape, x.dtype, dev, stream), C
+    else:
+        ldy = _like(y, "y", shape, x.dtype, dev)
+    _call(lib.la_rms_norm_fwd, dev, x.data_ptr(), res, w, eps, y.data_ptr(), ro, ldx, ldres, ldy, ldro, rows, C, code,
+          _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))
     return y, residual_out
 
 
@@ -795,19 +815,21 @@ def la_rms_norm_fwd_fp8(x, weight, eps, residual=None, group=0, y=None, scales=N
     columns (group = 128: scales [rows, ceil(C / 128)]).  Returns (y, scales, residual_out)."""
     import torch
     lib = load_library()
-    code, rows, C, residual_out, ldx, ldres, ldro = _norm_inputs(x, weight, residual, residual_out, stream)
+    code, shape, dev, (res, w, ro), (ldx, ldres, ldro), residual_out = _norm_inputs(x, weight, residual, residual_out,
+                                                                                    stream)
+    rows, C = shape
     if group not in (0, 128):
         raise ValueError(f"group must be 0 or 128, got {group}")
     if y is None:
-        y = _empty((rows, C), torch.float8_e4m3fn, x, stream)
-    ldy = _rows_like(y, "y", x, torch.float8_e4m3fn)
+        y, ldy = _empty(shape, torch.float8_e4m3fn, dev, stream), C
+    else:
+        ldy = _like(y, "y", shape, torch.float8_e4m3fn, dev)
     groups = -(-C // 128) if group else 1
     if scales is None:
-        scales = _empty((rows, groups), torch.float32, x, stream)
-    _on_device(scales, "scales", torch.float32, (rows, groups), x)
-    _on_device(dev_error, "dev_error", torch.int32, (None,), x)
-    _call(lib.la_rms_norm_fwd_fp8, x, x.data_ptr(), _p(residual), _p(weight), eps, y.data_ptr(), _p(scales),
-          _p(residual_out), ldx, ldres, ldy, ldro, rows, C, group, code, _p(dev_error), _stream(stream, x))
+        scales = _empty((rows, groups), torch.float32, dev, stream)
+    _call(lib.la_rms_norm_fwd_fp8, dev, x.data_ptr(), res, w, eps, y.data_ptr(),
+          _array(scales, "scales", torch.float32, (rows, groups), dev), ro, ldx, ldres, ldy, ldro, rows, C, group, code,
+          _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))
     return y, scales, residual_out
 
 
@@ -830,26 +852,26 @@ def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, worksp
     CUDA uint8, at least la_rms_norm_bwd_workspace(...) bytes, allocated here when None."""
     import torch
     lib = load_library()
-    code, rows, C, lds = _matrix(s, "s")
-    _on_device(weight, "weight", torch.float32, (C,), s)
-    lddy = _rows_like(dy, "dy", s)
-    lddres = 0 if dres is None else _rows_like(dres, "dres", s)
+    code, shape, rows, C, dev, lds = _matrix(s, "s")
+    dtype = s.dtype
+    lddy = _like(dy, "dy", shape, dtype, dev)
+    lddres = 0 if dres is None else _like(dres, "dres", shape, dtype, dev)
     if dx is None:
-        dx = _empty((rows, C), s.dtype, s, stream)
-    lddx = _rows_like(dx, "dx", s)
+        dx, lddx = _empty(shape, dtype, dev, stream), C
+    else:
+        lddx = _like(dx, "dx", shape, dtype, dev)
     if dweight is None:
-        dweight = _empty((C,), torch.float32, s, stream)
-    _on_device(dweight, "dweight", torch.float32, (C,), s)
-    _on_device(dev_error, "dev_error", torch.int32, (None,), s)
+        dweight = _empty((C,), torch.float32, dev, stream)
     if workspace is None:
         nbytes = la_rms_norm_bwd_workspace(rows, C)
-        workspace = _empty((nbytes,), torch.uint8, s, stream) if nbytes else None
+        workspace = _empty(nbytes, torch.uint8, dev, stream) if nbytes else None
     else:
-        _on_device(workspace, "workspace", torch.uint8, (None,), s)
         nbytes = workspace.numel()
-    _call(lib.la_rms_norm_bwd, s, s.data_ptr(), _p(weight), eps, dy.data_ptr(), _p(dres), dx.data_ptr(),
-          dweight.data_ptr(), lds, lddy, lddres, lddx, rows, C, code, _p(workspace), nbytes, _p(dev_error),
-          _stream(stream, s))
+    _call(lib.la_rms_norm_bwd, dev, s.data_ptr(), _array(weight, "weight", torch.float32, (C,), dev), eps, dy.data_ptr(),
+          None if dres is None else dres.data_ptr(), dx.data_ptr(),
+          _array(dweight, "dweight", torch.float32, (C,), dev), lds, lddy, lddres, lddx, rows, C, code,
+          _array(workspace, "workspace", torch.uint8, (None,), dev), nbytes,
+          _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))
     return dx, dweight
 
 

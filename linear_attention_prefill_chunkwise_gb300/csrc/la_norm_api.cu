@@ -113,9 +113,21 @@ la_status device(la_host::DeviceState** ds) {
 template <typename... Params, typename... Args>
 cudaError_t launch_resident(void (*kernel)(Params...), int sms, int most, int threads, int shared, cudaStream_t s,
                             int* blocks, Args... args) {
-  int per_sm = 0;
-  cudaError_t ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, shared);
-  if (ce != cudaSuccess) return ce;
+  // the last answers, by kernel and block (the query costs as much as a launch)
+  struct Known {
+    const void* kernel = nullptr;
+    int threads = 0, shared = 0, sms = 0, per_sm = 0;
+  };
+  thread_local Known known[16];
+  const void* id = reinterpret_cast<const void*>(kernel);
+  Known& k = known[(reinterpret_cast<uintptr_t>(id) / 16 + static_cast<uintptr_t>(shared) / 1024) % 16];
+  if (k.kernel != id || k.threads != threads || k.shared != shared || k.sms != sms) {
+    int n = 0;
+    const cudaError_t ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, shared);
+    if (ce != cudaSuccess) return ce;
+    k = {id, threads, shared, sms, n};
+  }
+  const int per_sm = k.per_sm;
   *blocks = per_sm * sms < most ? (per_sm < 1 ? 1 : per_sm * sms) : most;
   return la_host::launch_pdl(kernel, *blocks, threads, shared, s, args...);
 }
