@@ -307,9 +307,15 @@ la_status decode_call(const void* x, const void* r, const void* g, const float* 
     p.start = state;
     p.finish = state_out;
     p.accepted_len = accepted_len;
-    const unsigned grid = static_cast<unsigned>(B) * ((C + lag::kThreads - 1) / lag::kThreads);
-    cudaError_t ce = la_host::launch_pdl(lag::gated_decode_kernel<E>, grid, lag::kThreads, 0,
-                                         static_cast<cudaStream_t>(stream), p);
+    auto quads = [&](const void* ptr, int64_t ld, size_t element) {
+      return reinterpret_cast<uintptr_t>(ptr) % (4 * element) == 0 && ld % 4 == 0;
+    };
+    const bool wide = C % 4 == 0 && quads(x, ldx, es) && quads(r, ldr, es) && quads(g, ldg, es) && quads(o, ldo, es) &&
+                      quads(slopes, 0, 4) && quads(state, 0, 4);
+    const int span = lag::kThreads * (wide ? 4 : 2);
+    const unsigned grid = static_cast<unsigned>(B) * ((C + span - 1) / span);
+    cudaError_t ce = la_host::launch_pdl(wide ? lag::gated_decode_kernel<E, 4> : lag::gated_decode_kernel<E, 1>, grid,
+                                         lag::kThreads, 0, static_cast<cudaStream_t>(stream), p);
     if (ce == cudaSuccess) ce = cudaGetLastError();
     return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
   };

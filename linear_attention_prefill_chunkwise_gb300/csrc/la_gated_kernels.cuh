@@ -1029,15 +1029,66 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int
 
 // ---------------------------------------------------------------- decode, verify, commit
 
-// One thread per (request, channel) walks the request's tokens; neighbouring threads hold
-// neighbouring channels.
+// kVec = 4: four neighbouring channels per thread, 8- or 16-byte loads; kVec = 1: two channels, a
+// block's width apart, element by element.  Either way the same arithmetic per channel.
+template <typename E, int kVec>
+struct Chunk;  // as loaded
+template <>
+struct Chunk<float, 4> {
+  float4 w;
+  __device__ __forceinline__ f2 get(int i) const { return i == 0 ? f2_pack(w.x, w.y) : f2_pack(w.z, w.w); }
+};
+template <>
+struct Chunk<__nv_bfloat16, 4> {
+  uint2 w;
+  __device__ __forceinline__ f2 get(int i) const { return lap::bf16x2_to_f2(i == 0 ? w.x : w.y); }
+};
 template <typename E>
-__global__ void __launch_bounds__(kThreads) gated_decode_kernel(const Params<E> p) {
+struct Chunk<E, 1> {
+  E a, b;
+  __device__ __forceinline__ f2 get(int) const { return f2_pack(to_f32(a), to_f32(b)); }
+};
+template <typename E, int kVec>
+__device__ __forceinline__ Chunk<E, kVec> load_chunk(const E* row, int c, bool second) {
+  Chunk<E, kVec> q;
+  if constexpr (kVec == 4) {
+    q.w = *reinterpret_cast<const decltype(q.w)*>(row + c);
+  } else {
+    q.a = row[c];
+    q.b = second ? row[c + kThreads] : row[c];
+  }
+  return q;
+}
+template <int kVec, typename E>
+__device__ __forceinline__ void store_chunk(E* row, int c, bool second, const f2 (&v)[2]) {
+  const float2 a = f2_unpack(v[0]), b = f2_unpack(v[1]);
+  if constexpr (kVec == 4 && sizeof(E) == 4) {
+    *reinterpret_cast<float4*>(row + c) = make_float4(a.x, a.y, b.x, b.y);
+  } else if constexpr (kVec == 4) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(b.x, b.y);
+    *reinterpret_cast<uint2*>(row + c) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    row[c] = from_f32<E>(a.x);
+    if (second) row[c + kThreads] = from_f32<E>(a.y);
+  }
+}
+
+// Each thread walks a request's tokens for its channels.  The states are read and written once; many
+// threads with the loads of kAhead tokens in flight each keep the memory busy.  Bound by the bytes:
+// BF16 requests of 8192 channels, 128 x 1 token 4.8 us, 128 x 8 14.0 (0.79 of the copy rate),
+// 4096 x 8 of 4096 channels 184 (0.97); with 4 tokens ahead and 8 blocks per SM 5.7, 13.6, 194; with
+// 8 ahead 13.5, 24.9, 303.
+template <typename E, int kVec>
+__global__ void __launch_bounds__(kThreads, 12) gated_decode_kernel(const Params<E> p) {
+  using Q = Chunk<E, kVec>;
+  constexpr int kPairs = kVec == 4 ? 2 : 1, kAhead = sizeof(E) == 2 ? 2 : 1, kSpan = kThreads * (kVec == 4 ? 4 : 2);
   lap::griddep_wait();
   lap::griddep_launch_dependents();
-  const int tiles = (p.C + kThreads - 1) / kThreads;
-  const int n = static_cast<int>(blockIdx.x / tiles);
-  const int c = static_cast<int>(blockIdx.x % tiles) * kThreads + static_cast<int>(threadIdx.x);
+  const int tiles = (p.C + kSpan - 1) / kSpan;
+  const int n = static_cast<int>(blockIdx.x) / tiles;
+  const int c = (static_cast<int>(blockIdx.x) - n * tiles) * kSpan + static_cast<int>(threadIdx.x) * (kVec == 4 ? 4 : 1);
+  const bool second = c + kThreads < p.C;  // kVec = 1
   const int slot = slot_of(p, n);
   if (slot < 0 || c >= p.C) return;
   int rows = p.T;
@@ -1045,17 +1096,39 @@ __global__ void __launch_bounds__(kThreads) gated_decode_kernel(const Params<E> 
     rows = min(max(p.accepted_len[n], 0), p.T);
     if (rows == 0) return;
   }
-  const float slope = p.slopes[c];
-  const size_t at = static_cast<size_t>(slot) * p.C + c;
-  float h = p.start[at];
   const int64_t first = static_cast<int64_t>(n) * p.T;
-  for (int64_t t = first; t < first + rows; ++t) {
-    const float x = to_f32(p.in[0][t * p.ld_in[0] + c]);
-    const Decay d = decay_of(slope * sigmoid(to_f32(p.in[1][t * p.ld_in[1] + c])));
-    h = fmaf(d.lambda, h, d.beta * sigmoid(to_f32(p.in[2][t * p.ld_in[2] + c])) * x);
-    if (p.out[0]) p.out[0][t * p.ld_out[0] + c] = from_f32<E>(h);
+  const size_t at = static_cast<size_t>(slot) * p.C;
+  const auto slope = load_chunk<float, kVec>(p.slopes, c, second);
+  f2 h[2];
+  {
+    const auto q = load_chunk<float, kVec>(p.start + at, c, second);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) h[i] = q.get(i);
   }
-  if (p.finish) p.finish[at] = h;
+  for (int t0 = 0; t0 < rows; t0 += kAhead) {
+    Q x[kAhead], r[kAhead], g[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (t0 + k < rows) {
+        const int64_t row = first + t0 + k;
+        r[k] = load_chunk<E, kVec>(p.in[1] + row * p.ld_in[1], c, second);
+        g[k] = load_chunk<E, kVec>(p.in[2] + row * p.ld_in[2], c, second);
+        x[k] = load_chunk<E, kVec>(p.in[0] + row * p.ld_in[0], c, second);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (t0 + k >= rows) break;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        f2 a, b;
+        step2<false>(slope.get(i), x[k].get(i), r[k].get(i), g[k].get(i), &a, &b);
+        h[i] = f2_fma(a, h[i], b);
+      }
+      if (p.out[0]) store_chunk<kVec, E>(p.out[0] + (first + t0 + k) * p.ld_out[0], c, second, h);
+    }
+  }
+  if (p.finish) store_chunk<kVec, float>(p.finish + at, c, second, h);
 }
 
 }  // namespace lag

@@ -53,21 +53,6 @@ constexpr float kNear = 0.125f;
 constexpr float kC1 = -0.4999971091747284f, kC2 = 0.16652604937553406f, kC3 = -0.039715882390737534f;
 constexpr float kLeast = 1.17549435e-38f;
 
-// 1 / (1 + exp(-z)); 0 at -inf, 1 at +inf.
-__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + ex2_approx(-kLog2e * z)); }
-
-struct Decay {
-  float lambda, beta;
-};
-
-__device__ __forceinline__ Decay decay_of(float u) {
-  const float near = u * fmaf(u, fmaf(u, fmaf(u, kC3, kC2), kC1), 1.f);
-  const float far = 1.f - ex2_approx(-kLog2e * u);
-  const float m = u < kNear ? near : far;
-  const float w = m * (2.f - m);
-  return {1.f - m, w * rsqrt_approx(fmaxf(w, kLeast))};
-}
-
 // ---------------------------------------------------------------- two channels at once
 
 // Pairs of FP32 values in one 64-bit register pair: one instruction for two channels where the
@@ -93,7 +78,7 @@ __device__ __forceinline__ f2 f2_each(f2 v, F f) {
   return f2_pack(f(t.x), f(t.y));
 }
 
-// 1 + exp(-z): the reciprocal of sig(z).
+// 1 + exp(-z): the reciprocal of sig(z); 1 at z = +inf, inf at -inf.
 __device__ __forceinline__ f2 inverse_sigmoid2(f2 z) {
   const f2 e = f2_each(f2_mul(z, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
   return f2_add(e, f2_all(1.f));
