@@ -29,6 +29,8 @@ DEPENDS = ["la_prefill_api.cu", "la_prefill_kernel.cuh", "sm103_ptx.cuh", "la_de
            "la_gated_api.cu", "la_gated_kernels.cuh", "la_gated_math.cuh", "la_rows_common.h", "la_norm_api.cu",
            "la_norm_kernels.cuh"]
 HEADERS = ["la_prefill.h", "la_decode.h", "la_segment.h", "la_backward.h", "la_d256.h", "la_gated.h", "la_norm.h"]
+# parts that can be built alone with a short wait limit
+WAIT_LIMIT_PARTS = {"prefill": ["la_prefill_api.cu"], "gated": ["la_gated_api.cu", "la_norm_api.cu"]}
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -56,15 +58,15 @@ def _nvcc(args: list) -> str:
     return res.stdout + res.stderr
 
 
-def build(force: bool = False, verbose: bool = False, wait_limit_ns: int = 0) -> str:
+def build(force: bool = False, verbose: bool = False, wait_limit_ns: int = 0, part: str = "prefill") -> str:
     """Build the library if any source is newer than it; return its path.
 
-    wait_limit_ns > 0 builds the prefill entry point alone, as a separate file, with that
-    limit on every pipeline wait instead of one second: ordinary waits then exceed it, so the
-    kernels' timeout exit can be exercised on a healthy input."""
+    wait_limit_ns > 0 builds the entry points of one ``part`` alone, as a separate file, with that
+    limit on every wait inside a kernel instead of one second: ordinary waits then exceed it, so
+    the kernels' timeout exit can be exercised on a healthy input."""
     if wait_limit_ns:
-        out = os.path.join(BUILD_DIR, f"libla_prefill_wait{int(wait_limit_ns)}ns.so")
-        sources = ["la_prefill_api.cu"]
+        out = os.path.join(BUILD_DIR, f"libla_{part}_wait{int(wait_limit_ns)}ns.so")
+        sources = WAIT_LIMIT_PARTS[part]
     else:
         out = LIB_PATH
         sources = SOURCES

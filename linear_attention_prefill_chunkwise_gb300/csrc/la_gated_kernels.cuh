@@ -485,7 +485,7 @@ __device__ __forceinline__ Run await_run(const float4* at, int* ticket, int* dev
     r = read_run(at);
     if (is_set(r)) break;
     if (i == 0) t0 = lap::globaltimer_ns();
-    if ((i & 15u) == 15u && !keep_polling(ticket, dev_error, t0)) break;
+    if ((i & 3u) == 3u && !keep_polling(ticket, dev_error, t0)) break;
   }
   return r;
 }
@@ -499,7 +499,7 @@ __device__ __forceinline__ f2 await_state(const float2* at, int* ticket, int* de
     h = f2_pack(__uint_as_float(u), __uint_as_float(v));
     if (is_set(h)) break;
     if (i == 0) t0 = lap::globaltimer_ns();
-    if ((i & 15u) == 15u && !keep_polling(ticket, dev_error, t0)) break;
+    if ((i & 3u) == 3u && !keep_polling(ticket, dev_error, t0)) break;
   }
   return h;
 }

@@ -343,6 +343,29 @@ def test_garbage_workspace():
                 assert torch.equal(b.fwd(workspace=ws)[0], o)
 
 
+def test_calls_in_a_row_share_a_workspace():
+    """Calls of different batches on one stream, one workspace, nothing in between."""
+    bs = [Batch(60 + k, lens=lens, C=C, pool=6) for k, (lens, C) in enumerate((
+        ([900, 3, 1200], 72), ([5, 0, 700, 2], 200), ([2100], 40), ([300, 301, 302, 303, 1], 136)))]
+    refs = [b.fwd() for b in bs]
+    douts = [b.mat() for b in bs]
+    grads = [lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, d, h0=b.h0, **b.kw)[:4]
+             for b, (o, _), d in zip(bs, refs, douts)]
+    n = max(lap.la_gated_scan_workspace(1, b.tokens, len(b.lens), b.C, True, torch.bfloat16, True) for b in bs)
+    ws = torch.full((n,), 0x3C, dtype=torch.uint8, device="cuda")
+    outs = [(b.blank(), torch.full((b.P, b.C), float("nan"), device="cuda")) for b in bs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for b, (o, hf), d in zip(bs, outs, douts):
+            lap.la_gated_scan_fwd(b.x, b.r, b.g, b.slopes, h0=b.h0, o=o, h_final=hf, workspace=ws, **b.kw)
+            got.append(lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, d, h0=b.h0, workspace=ws, **b.kw)[:4])
+    torch.cuda.synchronize()
+    for (o, hf), (ro, rh), g, rg in zip(outs, refs, got, grads):
+        assert torch.equal(o, ro) and torch.equal(hf[~torch.isnan(rh)], rh[~torch.isnan(rh)])
+        assert all(torch.equal(a, b) for a, b in zip(g, rg))
+
+
 def test_offsets_past_32_bits():
     """Rows whose element offsets pass 2^31 give what a compact copy gives, bit for bit."""
     T, ld, C = (1 << 18) + 77, 8256, 24
