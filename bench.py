@@ -551,6 +551,8 @@ def run_sweep(args):
         run_decode_sweep(args, device, stream, flush, hbm, hbm_kind)
     if args.sweep_what in ("all", "segmented"):
         run_segment_sweep(args, device, stream, flush, hbm, hbm_kind, tflops, tf_kind)
+    if args.sweep_what in ("all", "gated"):
+        run_gated_sweep(args, device, stream, flush, hbm, hbm_kind)
     if args.sweep_what in ("all", "backward"):
         run_backward_sweep(args, device, stream, flush, hbm, hbm_kind)
 
@@ -659,6 +661,80 @@ def decode_sweep_one(args, p, device, stream, flush, hbm, hbm_kind):
                                     "sample": "every request and head, all 8 tokens (FP64 tokenwise recurrence, "
                                               "OpenMP over (request, head))"}
         print(json.dumps(line), flush=True)
+
+
+def run_gated_sweep(args, device, stream, flush, hbm, hbm_kind):
+    """The gated recurrence (scan, gradients, decode) and the RMS norm, BF16, timed as the other
+    sweeps; the roofline is the bytes that each call has to read and write once."""
+    import torch
+
+    import linear_attention_prefill_chunkwise_gb300 as lap
+
+    gen = torch.Generator(device=device).manual_seed(4000)
+
+    def rand(rows, cols, n):
+        return [torch.randn((rows, cols), generator=gen, device=device).to(torch.bfloat16) for _ in range(n)]
+
+    def timed(fn):
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                fn()
+            times = []
+            for _ in range(args.sweep_steps):
+                flush.fill_(1)
+                e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                e0.record(stream)
+                fn()
+                e1.record(stream)
+                times.append((e0, e1))
+        torch.cuda.synchronize(device)
+        return statistics.fmean(a.elapsed_time(b) for a, b in times)
+
+    def line(op, workload, nbytes, fn):
+        ms = timed(fn)
+        t_roof = nbytes / (hbm * 1e9)
+        print(json.dumps({"sweep": True, "op": op, "workload": workload, "ms": round(ms, 5), "alg_bytes": nbytes,
+                          "achieved_gbs": round(nbytes / (ms / 1e3) / 1e9, 1), "roofline_ms": round(t_roof * 1e3, 5),
+                          "frac": round(t_roof * 1e3 / ms, 4), "bound": "hbm",
+                          "peaks": {"hbm_gbs": hbm, "hbm_source": hbm_kind}, "steps": args.sweep_steps,
+                          "l2": "flushed between launches (256 MB write)"}), flush=True)
+
+    for Bn, Tn, Cn in ((1, 256, 512), (2, 8192, 8192), (1, 32768, 4096)):
+        n = Bn * Tn * Cn
+        x, r, g, o, dout, dx, dr, dg = rand(Bn * Tn, Cn, 8)
+        slopes = torch.exp2(-8.0 * torch.arange(1, Cn + 1, device=device) / Cn)
+        h0, hf = (torch.randn((Bn, Cn), generator=gen, device=device) for _ in range(2))
+        ws = torch.empty(max(1, lap.la_gated_scan_workspace(Bn, Tn, Bn, Cn, False, torch.bfloat16, True)),
+                         dtype=torch.uint8, device=device)
+        ds = torch.empty(Cn, device=device)
+        name = f"B={Bn} T={Tn} C={Cn}, h0 + final state"
+        line("gated_scan_fwd", name, 8 * n + 8 * Bn * Cn + 4 * Cn,
+             lambda: lap.la_gated_scan_fwd(x, r, g, slopes, h0=h0, o=o, h_final=hf, seq_len=Tn, workspace=ws,
+                                           stream=stream))
+        line("gated_scan_bwd", name, 16 * n + 8 * Bn * Cn + 8 * Cn,
+             lambda: lap.la_gated_scan_bwd(x, r, g, slopes, o, dout, h0=h0, dh_final=hf, dx=dx, dr=dr, dg=dg,
+                                           dslopes=ds, seq_len=Tn, workspace=ws, stream=stream))
+        del x, r, g, o, dout, dx, dr, dg
+    Bn, Cn, pool = 128, 8192, 256
+    idx = torch.randperm(pool, generator=gen, device=device)[:Bn].int()
+    state, slopes = torch.randn((pool, Cn), generator=gen, device=device), torch.rand(Cn, generator=gen, device=device)
+    for Tn in (1, 8):
+        x, r, g, o = rand(Bn * Tn, Cn, 4)
+        line("gated_decode", f"B={Bn} requests x T={Tn}, C={Cn}, 256-slot pool", 8 * Bn * Tn * Cn + 8 * Bn * Cn + 4 * Cn,
+             lambda: lap.la_gated_decode(x, r, g, slopes, state, Tn, state_indices=idx, o=o, stream=stream))
+    for rows, Cn in ((128, 8192), (16384, 8192)):
+        n = rows * Cn
+        x, res, y, s, dx = rand(rows, Cn, 5)
+        w, dw = torch.rand(Cn, generator=gen, device=device), torch.empty(Cn, device=device)
+        y8, sc = torch.empty((rows, Cn), dtype=torch.float8_e4m3fn, device=device), torch.empty((rows, 1), device=device)
+        ws = torch.empty(max(1, lap.la_rms_norm_bwd_workspace(rows, Cn)), dtype=torch.uint8, device=device)
+        name = f"{rows} rows of {Cn}, residual"
+        line("rms_norm_fwd", name, 8 * n + 4 * Cn,
+             lambda: lap.la_rms_norm_fwd(x, w, 1e-5, residual=res, y=y, residual_out=s, stream=stream))
+        line("rms_norm_fwd_fp8", name, 7 * n + 4 * rows + 4 * Cn,
+             lambda: lap.la_rms_norm_fwd_fp8(x, w, 1e-5, residual=res, y=y8, scales=sc, residual_out=s, stream=stream))
+        line("rms_norm_bwd", name, 8 * n + 8 * Cn,
+             lambda: lap.la_rms_norm_bwd(s, w, 1e-5, y, dres=x, dx=dx, dweight=dw, workspace=ws, stream=stream))
 
 
 SEGMENT_WORKLOADS = (
@@ -926,9 +1002,9 @@ def main():
     ap.add_argument("--sweep", action="store_true",
                     help="time every workload (1..5) instead, one JSON line each (not the headline line)")
     ap.add_argument("--sweep-steps", type=int, default=50)
-    ap.add_argument("--sweep-what", choices=["all", "prefill", "decode", "segmented", "backward"], default="all",
+    ap.add_argument("--sweep-what", choices=["all", "prefill", "decode", "segmented", "gated", "backward"], default="all",
                     help="with --sweep: the five prefill workloads, the speculative-decoding ops, the "
-                         "segmented prefill on few-chain batches, or all of them")
+                         "segmented prefill on few-chain batches, the gated recurrence and the norm, or all of them")
     args = ap.parse_args()
     if args.warmup < 3:
         ap.error("--warmup must be >= 3")
