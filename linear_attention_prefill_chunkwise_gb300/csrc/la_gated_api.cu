@@ -26,6 +26,7 @@ struct Plan {
   bool ticket = false; // a plan kernel runs first
   bool waits = false;  // states pass from block to block
   bool order = false;  // packed, by chains
+  lag::Mode mode = lag::kMixed;
   size_t table = 0, runs = 0, words = 0, before = 0, part = 0, bytes = 0;
 };
 
@@ -41,8 +42,10 @@ int group_of(int columns, int warps) {
 }
 
 // Whether blocks take whole chains (a sequence's channels).  Sequences of one length: for short
-// chains, which need no plan kernel, and where the chains fill the device evenly enough (2 x 8192
-// tokens x 8192 channels, 256 chains: 218 us by chains and 219 by tiles; 19 x 1024 x 8192: 243 and 281).
+// chains, which need no plan kernel, and where the chains fill the device evenly enough.  8192
+// channels, by chains and by tiles: 2 x 8192 tokens, 256 chains, 194 and 197 us (gradients 368 and
+// 374); with 7168 channels, 224 chains, 206 and 175 (368 and 331); 3 x 4096 tokens, 384 chains, 172
+// and 149 (305 and 282).
 bool by_chains(int64_t chains, int per) {
   const int64_t waves = (chains + kSlots - 1) / kSlots;
   return per <= 4 || chains * 100 >= waves * kSlots * 80;
@@ -71,9 +74,11 @@ Plan plan_for(int B, int T, int N, int C, bool packed) {
     q.waits = !q.order;
   }
   q.ticket = q.waits || q.order;
+  if (q.order || (q.per && !q.waits)) q.mode = lag::kByChains;
+  else if (q.per) q.mode = lag::kByTiles;
   q.tiles = q.per ? B * q.per : static_cast<int>((rows + q.stride - 1) / q.stride);
   if (q.tiles == 0) q.tiles = 1;  // empty sequences alone
-  q.parts = q.order ? N : q.per && !q.waits ? B : q.tiles;
+  q.parts = q.mode == lag::kByChains ? N : q.tiles;
   q.items = q.parts * q.columns;
   q.group = group_of(q.columns, S::kWarps);
   q.groups = ((q.per ? q.per : q.tiles) + q.group - 1) / q.group;
@@ -195,6 +200,11 @@ cudaError_t launch_plan(const lag::Params<E>& p, const Plan& q, int sms, cudaStr
   return la_host::launch_pdl(lag::scan_plan_kernel<E>, grid, lag::kThreads, 0, s, p, q.words);
 }
 
+template <lag::Mode kMode>
+struct ModeTag {
+  static constexpr lag::Mode value = kMode;
+};
+
 template <typename E, bool kBack, bool kTma>
 la_status launch_scan_as(lag::Params<E> p, int B, void* workspace, float* dslopes, int sms, cudaStream_t s) {
   using S = lag::Shape<E, kBack, kTma>;
@@ -210,9 +220,15 @@ la_status launch_scan_as(lag::Params<E> p, int B, void* workspace, float* dslope
   }
   cudaError_t ce = q.ticket ? launch_plan(p, q, sms, s) : cudaSuccess;
   if (ce == cudaSuccess && q.tiles > 0) {
-    const int most = sms * S::kBlocks;
-    ce = la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma>, q.items < most ? q.items : most, S::kThreads,
-                             lag::scan_smem_bytes<E, kBack, kTma>(), s, p, maps);
+    const int most = sms * S::kBlocks, grid = q.items < most ? q.items : most;
+    auto run = [&](auto mode) {
+      constexpr lag::Mode kMode = decltype(mode)::value;
+      return la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma, kMode>, grid, S::kThreads,
+                                 lag::scan_smem_bytes<E, kBack, kTma, kMode>(), s, p, maps);
+    };
+    ce = q.mode == lag::kByChains  ? run(ModeTag<lag::kByChains>{})
+         : q.mode == lag::kByTiles ? run(ModeTag<lag::kByTiles>{})
+                                   : run(ModeTag<lag::kMixed>{});
   }
   if (ce == cudaSuccess && kBack)
     ce = la_host::launch_pdl(lag::column_sum_kernel, (p.C + 31) / 32, 1024, 0, s, static_cast<const float*>(p.part),
@@ -230,16 +246,24 @@ la_status launch_scan(const lag::Params<E>& p, int B, void* workspace, float* ds
 }
 
 // One-time setup per device: the stages of a scan exceed the default shared memory.
+template <typename E, bool kBack, bool kTma, lag::Mode kMode>
+cudaError_t setup_kernel() {
+  return cudaFuncSetAttribute(lag::gated_scan_kernel<E, kBack, kTma, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              lag::scan_smem_bytes<E, kBack, kTma, kMode>());
+}
+template <typename E, bool kBack, bool kTma>
+cudaError_t setup_modes() {
+  cudaError_t e = setup_kernel<E, kBack, kTma, lag::kByChains>();
+  if (e == cudaSuccess) e = setup_kernel<E, kBack, kTma, lag::kByTiles>();
+  if (e == cudaSuccess) e = setup_kernel<E, kBack, kTma, lag::kMixed>();
+  return e;
+}
 template <typename E>
 cudaError_t setup_type() {
-  const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(lag::gated_scan_kernel<E, false, false>, attr, lag::scan_smem_bytes<E, false, false>());
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(lag::gated_scan_kernel<E, false, true>, attr, lag::scan_smem_bytes<E, false, true>());
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(lag::gated_scan_kernel<E, true, false>, attr, lag::scan_smem_bytes<E, true, false>());
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(lag::gated_scan_kernel<E, true, true>, attr, lag::scan_smem_bytes<E, true, true>());
+  cudaError_t e = setup_modes<E, false, false>();
+  if (e == cudaSuccess) e = setup_modes<E, false, true>();
+  if (e == cudaSuccess) e = setup_modes<E, true, false>();
+  if (e == cudaSuccess) e = setup_modes<E, true, true>();
   return e;
 }
 

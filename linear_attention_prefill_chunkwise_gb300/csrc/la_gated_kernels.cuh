@@ -48,15 +48,16 @@ constexpr int kStages = 2;
 // Shape of a scan kernel: rows per warp, blocks per SM and the stages' layout.  kTma: rows arrive
 // by TMA boxes of kRows x 64 channels; else by 16-byte copies of the aligned chunks that a row's
 // channels touch, one chunk more than the channels fill.
-// Rows per warp: as many as two blocks' registers (forward: a and b of each) and shared memory
-// hold; every tile costs the same few hundred instructions.  Forward of 19 x 1024 x 8192 BF16 in
-// chains: 16 rows 243 us, 14 279, 12 262 (three blocks of 8 rows 388: registers spill, and the
-// stages leave no cache for them); 1001 channels: 12 rows 290, 10 206, 8 226.  Gradients: 8 rows
-// 447, 10 572, 6 494; 1001 channels: 8 rows 426, 6 402.
+// Rows per warp: as many as two blocks' registers (forward: a and b of each) and shared memory hold,
+// since every tile costs the same few hundred instructions; more of them spill, or leave the copies
+// no cache.  2 x 8192 tokens of 8192 channels, BF16: forward 16 rows 194 us, 14 202, 12 212;
+// gradients 10 rows 370, 9 367, 8 383, 6 422.  Unaligned, 32 sequences of up to 4096 tokens of 1001
+// channels: forward 16 rows 273, 15 211, 14 193, 12 197; gradients 8 rows 416, 6 372.  FP32, 8192
+// tokens of 4096 channels: gradients 5 rows 231, 4 212, 3 254.
 template <typename E, bool kBack, bool kTma>
 struct Shape {
   static constexpr int kWarps = 8;
-  static constexpr int kRows = (kBack ? (kTma ? 8 : 6) : (kTma ? 16 : 10)) / (sizeof(E) / 2);
+  static constexpr int kRows = (kBack ? (kTma ? 9 : 6) : (kTma ? 16 : 14)) / (sizeof(E) / 2);
   static constexpr int kBlocks = 2;
   static constexpr int kAsk = kRows * 5 / 8;  // the row before which a warp asks for the published words
   static constexpr int kThreads = kWarps * 32;
@@ -65,6 +66,15 @@ struct Shape {
   static constexpr int kPitch = kCols * sizeof(E) + (kTma ? 0 : 16);  // bytes of a row
   static constexpr int kInputBytes = kTileRows * kPitch;
   static constexpr int kStageBytes = kInputs * kInputBytes;
+};
+
+// How blocks take their work; each is a kernel of its own, since the loop is held up by its own
+// instructions and registers (2 x 8192 tokens x 8192 channels by chains, one kernel for all and this:
+// forward 216 and 197 us, gradients 425 and 385).
+enum Mode {
+  kByChains,  // one block walks all tiles of a sequence's channels
+  kByTiles,   // tiles of sequences of one length, states from block to block
+  kMixed      // tiles that hold rows of several sequences: packed (states from block to block) or whole ones
 };
 
 template <typename E>
@@ -197,76 +207,70 @@ __device__ __forceinline__ int slot_of(const Params<E>& p, int n) {
 
 // A tile: its number along the rows (-1: none), its channels, its sequence n and place i in that
 // sequence in walking order (where tiles hold rows of several sequences: 0 and its place among all
-// tiles), i's place j in its group, its lowest row and that row's token in the sequence, and the
-// sequence's length (-1: rows of several).
+// tiles), i's place j in its group, its lowest row and that row's token in the sequence (walked from
+// the end, the last tile may begin before the sequence: below 0), and the sequence's length (-1:
+// rows of several).
 struct Tile {
   int t, column, n, i, j, row, token, length;
 };
 
-template <bool kBack, int K, typename E>
+template <Mode kMode, bool kBack, int K, typename E>
 __device__ __forceinline__ Rows rows_of(const Params<E>& p, const Tile& q, int warp, int lane) {
-  if (q.length >= 0) {  // by arithmetic, the same for every lane
+  if constexpr (kMode != kMixed) {  // by arithmetic, the same for every lane
     const int slot = p.state_indices ? p.state_indices[q.n] : q.n;
     const int place = warp * K;
     auto bit = [](int k) { return k >= 0 && k < K ? 1u << k : 0u; };
     auto below = [](int k) { return k <= 0 ? 0u : k >= K ? (1u << K) - 1u : (1u << k) - 1u; };  // bits under k
     Rows r{0u, 0u, 0u, checked(p, slot)};
     if (r.slot < 0) return r;
-    if (kBack) {
-      const int top = q.token + p.stride - 1 - place;  // the token of row 0; they count down
-      r.live = ((1u << K) - 1u) & ~below(top - q.length + 1);
-      r.begin = bit(top - q.length + 1);
-      r.end = bit(top);
-    } else {
-      const int top = q.token + place;
-      r.live = below(q.length - top);
-      r.begin = bit(-top);
-      r.end = bit(q.length - 1 - top);
+    // tiles begin where the walk does, so no row begins the sequence: its state comes from outside
+    const int left = kBack ? q.token + p.stride - place : q.length - q.token - place;  // rows to the walk's end
+    r.live = below(left);
+    r.end = bit(left - 1);
+    return r;
+  } else {
+    Rows r{0u, 0u, 0u, -1};
+    const int place = warp * K + lane;  // in walking order
+    const int at = kBack ? p.stride - 1 - place : place;
+    const int64_t row = static_cast<int64_t>(q.t) * p.stride + at;
+    bool first = false, last = false;
+    if (lane < K && place < p.stride && row < p.rows) {
+      if (p.cu_seqlens) {
+        int a = p.places[q.t].x, b = p.places[q.t + 1].x;
+        while (a < b) {  // the number of sequences that begin at or before the row
+          const int m = (a + b) / 2;
+          if (p.cu_seqlens[m] <= row) a = m + 1; else b = m;
+        }
+        if (a > 0) {
+          const int lo = p.cu_seqlens[a - 1], hi = p.cu_seqlens[a];
+          if (row < hi) {
+            r.slot = slot_of(p, a - 1);
+            first = row == lo;
+            last = row == hi - 1;
+          }
+        }
+      } else {
+        const int n = static_cast<int>(row) / p.T, t = static_cast<int>(row) - n * p.T;
+        r.slot = slot_of(p, n);
+        first = t == 0;
+        last = t == p.T - 1;
+      }
     }
-    r.begin &= r.live;
-    r.end &= r.live;
+    r.live = __ballot_sync(0xFFFFFFFFu, r.slot >= 0);
+    r.begin = __ballot_sync(0xFFFFFFFFu, r.slot >= 0 && (kBack ? last : first));
+    r.end = __ballot_sync(0xFFFFFFFFu, r.slot >= 0 && (kBack ? first : last));
     return r;
   }
-  Rows r{0u, 0u, 0u, -1};
-  const int place = warp * K + lane;  // in walking order
-  const int at = kBack ? p.stride - 1 - place : place;
-  const int64_t row = static_cast<int64_t>(q.t) * p.stride + at;
-  bool first = false, last = false;
-  if (lane < K && place < p.stride && row < p.rows) {
-    if (p.cu_seqlens) {
-      int a = p.places[q.t].x, b = p.places[q.t + 1].x;
-      while (a < b) {  // the number of sequences that begin at or before the row
-        const int m = (a + b) / 2;
-        if (p.cu_seqlens[m] <= row) a = m + 1; else b = m;
-      }
-      if (a > 0) {
-        const int lo = p.cu_seqlens[a - 1], hi = p.cu_seqlens[a];
-        if (row < hi) {
-          r.slot = slot_of(p, a - 1);
-          first = row == lo;
-          last = row == hi - 1;
-        }
-      }
-    } else {
-      const int n = static_cast<int>(row) / p.T, t = static_cast<int>(row) - n * p.T;
-      r.slot = slot_of(p, n);
-      first = t == 0;
-      last = t == p.T - 1;
-    }
-  }
-  r.live = __ballot_sync(0xFFFFFFFFu, r.slot >= 0);
-  r.begin = __ballot_sync(0xFFFFFFFFu, r.slot >= 0 && (kBack ? last : first));
-  r.end = __ballot_sync(0xFFFFFFFFu, r.slot >= 0 && (kBack ? first : last));
-  return r;
 }
 
-// Whether some row of the warp may begin or end a sequence or belong to none.  `inside`: what was
-// looked up for the tile (the sequence's slot, or whether a packed tile lies inside a sequence).
-template <bool kBack, int K, typename E>
-__device__ __forceinline__ bool has_edges(const Params<E>& p, const Tile& q, int inside, int warp) {
-  if (q.length < 0) return !inside;
-  const int low = q.token + (kBack ? p.stride - (warp + 1) * K : warp * K);  // the lowest row's token
-  return inside < 0 || inside >= p.pool_size || low <= 0 || low + K >= q.length;
+// Whether some row of the warp may end a sequence or belong to none (kMixed: or begin one).
+// `inside`: what was looked up for the tile (its sequence's slot; kMixed: whether the tile lies
+// inside a sequence); `first`: the warp's first row in the tile.
+template <Mode kMode, bool kBack, int K, typename E>
+__device__ __forceinline__ bool has_edges(const Params<E>& p, const Tile& q, int inside, int first) {
+  if constexpr (kMode == kMixed) return !inside;
+  const int low = q.token + first;
+  return inside < 0 || inside >= p.pool_size || (kBack ? low <= 0 : low + K >= q.length);
 }
 
 // A lane's two channels: neighbours with TMA rows, else a warp's width apart.
@@ -506,27 +510,27 @@ __device__ __forceinline__ f2 await_state(const float2* at, int* ticket, int* de
 
 // What a tile shares between its warps; two of them in turn, so that a warp may begin the next
 // tile while another still reads this one's.
-template <int kWarps>
+template <Mode kMode, int kWarps>
 struct Exchange {
   Run own[kWarps][32];      // each warp's rows
-  Run earlier[kWarps][32];  // the group's earlier tiles, or pieces of them, in order
-  f2 base[32];              // the state before the group (by chains: before the tile)
+  Run earlier[kMode == kByChains ? 1 : kWarps][32];  // the group's earlier tiles, or pieces of them, in order
+  f2 base[32];              // the state before the group (by chains: before the tile); the last warp's
   unsigned char late[8];    // per warp: a word it asked for had not been published in time
   unsigned char begins[8];  // per warp: some of its rows begin a sequence
-  int fresh;                // the tile's first row does
+  int fresh;                // the tile's first row does: what lies before the tile does not matter
 };
-template <int kWarps>
+template <Mode kMode, int kWarps>
 struct ScanSmem {
-  Exchange<kWarps> turn[2];
+  Exchange<kMode, kWarps> turn[2];
   Tile tile[4];             // of this turn, the next two and the last
   uint64_t bar[kWarps][kStages];
   int abort;                // a load did not arrive
 };
 
-template <typename E, bool kBack, bool kTma>
+template <typename E, bool kBack, bool kTma, Mode kMode>
 __host__ __device__ constexpr int scan_smem_bytes() {
   using S = Shape<E, kBack, kTma>;
-  return kStages * S::kStageBytes + static_cast<int>(sizeof(ScanSmem<S::kWarps>));
+  return kStages * S::kStageBytes + static_cast<int>(sizeof(ScanSmem<kMode, S::kWarps>));
 }
 
 // The published words a tile needs: where it has more than kWarps earlier tiles in its group, each
@@ -553,8 +557,8 @@ struct Needs {
   }
 
   // Asks for the words, where each warp needs one tile's (the last warp: the base too) ...
-  template <typename E>
-  __device__ __forceinline__ void ask(const Params<E>& p, Exchange<kWarps>& ex, const Tile& q, int warp, int lane) const {
+  template <typename E, typename X>
+  __device__ __forceinline__ void ask(const Params<E>& p, X& ex, const Tile& q, int warp, int lane) const {
     if (per <= 1) {
       if (lo < hi) copy16(lap::smem_u32(&ex.earlier[warp][lane]), run(p, q, lo, lane));
       if (warp == kWarps - 1 && q.i > j && lane % 2 == 0)  // for two lanes: past the L1, which is not coherent
@@ -563,24 +567,21 @@ struct Needs {
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   // ... and notes what has not come.
-  __device__ __forceinline__ void look(Exchange<kWarps>& ex, const Tile& q, int warp, int lane) const {
+  template <typename X>
+  __device__ __forceinline__ void look(X& ex, const Tile& q, int warp, int lane) const {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
     unsigned late = per > 1;
     if (per <= 1) {
       const bool run_ok = lo >= hi || is_set(ex.earlier[warp][lane]);
-      bool base_ok = true;
-      if (warp == kWarps - 1) {
-        if (q.i == j) ex.base[lane] = f2_all(0.f);
-        else base_ok = is_set(ex.base[lane]);
-      }
+      const bool base_ok = warp != kWarps - 1 || q.i == j || is_set(ex.base[lane]);
       late = !__all_sync(0xFFFFFFFFu, run_ok && base_ok);
     }
     if (lane == 0) ex.late[warp] = static_cast<unsigned char>(late);
   }
   // The warp's piece and (the last warp) the base, by polling, up to four words at once.
-  template <typename E>
-  __device__ __forceinline__ void poll(const Params<E>& p, Exchange<kWarps>& ex, const Tile& q, int warp, int lane) const {
+  template <typename E, typename X>
+  __device__ __forceinline__ void poll(const Params<E>& p, X& ex, const Tile& q, int warp, int lane) const {
     if (lo < hi) {
       Run r = await_run(run(p, q, lo, lane), p.ticket, p.dev_error);
 #pragma unroll 1
@@ -597,61 +598,67 @@ struct Needs {
       }
       ex.earlier[warp][lane] = r;
     }
-    if (warp == kWarps - 1)
-      ex.base[lane] = q.i > j ? await_state(state(p, q, 1, lane), p.ticket, p.dev_error) : f2_all(0.f);
+    if (warp == kWarps - 1 && q.i > j) ex.base[lane] = await_state(state(p, q, 1, lane), p.ticket, p.dev_error);
   }
 };
 
 // The state before this warp's rows.  `mine` (in ex.own already) is the composition of the warp's
-// rows.  Where tiles wait for one another, publishes the tile for those that follow; else leaves the
-// state after it in `next`, the exchange of the block's next tile.
-template <typename E, int kWarps>
-__device__ __forceinline__ f2 state_before(const Params<E>& p, Exchange<kWarps>& ex, Exchange<kWarps>& next,
-                                           const Tile& q, const Run& mine, int warp, int lane) {
-  f2 before = f2_all(0.f);
-  const bool fresh = __any_sync(0xFFFFFFFFu, ex.fresh);
-  if (p.runs) {
-    const Needs<kWarps> needs(p, q, warp);
-    const bool last = needs.j == p.group - 1;
-    Run whole;
-    if (warp == 0) {
-      whole = mine;
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) whole = compose(whole, ex.own[w][lane]);
-      if (!last) publish_run(needs.run(p, q, needs.j, lane), whole);
-    }
-    if (!fresh) {
-      if (*reinterpret_cast<const unsigned long long*>(ex.late) != 0ull) {
-        if (ex.late[warp]) needs.poll(p, ex, q, warp, lane);
-        __syncthreads();
-      }
-      before = ex.base[lane];
-      const int pieces = needs.per <= 1 ? needs.j : (needs.j + needs.per - 1) / needs.per;
-#pragma unroll 2
-      for (int i = 0; i < pieces; ++i) before = apply(ex.earlier[i][lane], before);
-    }
-    if (warp == 0 && last) publish_state(needs.state(p, q, 0, lane), apply(whole, before));
-  } else if (!fresh) {
-    before = ex.base[lane];
-  }
-  if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<const unsigned long long*>(ex.begins) != 0ull)) {
-#pragma unroll 1
-    for (int w = 0; w < warp; ++w) before = apply(ex.own[w][lane], before);
-  } else {
+// rows.  Where tiles wait for one another, publishes the tile for those that follow; by chains (where
+// `start` is the state before the chain), leaves the state after it in `next`, the exchange of the
+// block's next tile.
+template <Mode kMode, typename E, int kWarps>
+__device__ __forceinline__ f2 state_before(const Params<E>& p, Exchange<kMode, kWarps>& ex,
+                                           Exchange<kMode, kWarps>& next, const Tile& q, const Run& mine, f2 start,
+                                           int warp, int lane) {
+  if constexpr (kMode == kByChains) {
+    f2 before = q.i == 0 ? start : ex.base[lane];
 #pragma unroll 4
     for (int w = 0; w < warp; ++w) before = f2_fma(ex.own[w][lane].a, before, ex.own[w][lane].h);
+    if (warp == kWarps - 1) next.base[lane] = f2_fma(mine.a, before, mine.h);
+    return before;
+  } else {
+    f2 before = f2_all(0.f);
+    const bool fresh = kMode == kMixed && __any_sync(0xFFFFFFFFu, ex.fresh);
+    if (kMode == kByTiles || p.runs) {
+      const Needs<kWarps> needs(p, q, warp);
+      const bool last = needs.j == p.group - 1;
+      Run whole;
+      if (warp == 0) {
+        whole = mine;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) whole = compose(whole, ex.own[w][lane]);
+        if (!last) publish_run(needs.run(p, q, needs.j, lane), whole);
+      }
+      if (!fresh) {
+        if (*reinterpret_cast<const unsigned long long*>(ex.late) != 0ull) {
+          if (ex.late[warp]) needs.poll(p, ex, q, warp, lane);
+          __syncthreads();
+        }
+        before = ex.base[lane];
+        const int pieces = needs.per <= 1 ? needs.j : (needs.j + needs.per - 1) / needs.per;
+#pragma unroll 2
+        for (int i = 0; i < pieces; ++i) before = apply(ex.earlier[i][lane], before);
+      }
+      if (warp == 0 && last) publish_state(needs.state(p, q, 0, lane), apply(whole, before));
+    }
+    if (kMode == kMixed && __any_sync(0xFFFFFFFFu, *reinterpret_cast<const unsigned long long*>(ex.begins) != 0ull)) {
+#pragma unroll 1
+      for (int w = 0; w < warp; ++w) before = apply(ex.own[w][lane], before);
+    } else {
+#pragma unroll 4
+      for (int w = 0; w < warp; ++w) before = f2_fma(ex.own[w][lane].a, before, ex.own[w][lane].h);
+    }
+    return before;
   }
-  if (!p.runs && warp == kWarps - 1) next.base[lane] = apply(mine, before);
-  return before;
 }
 
 // The final states of the empty sequences that lie in this tile, or the tile's own: their initial
 // ones.
-template <int kWarps, typename E, bool kTma>
+template <Mode kMode, int kWarps, typename E, bool kTma>
 __device__ __forceinline__ void empty_sequences(const Params<E>& p, const Tile& q, const Lane<kTma>& l, int warp) {
   if (!p.finish || q.length > 0 || (!p.cu_seqlens && p.T > 0)) return;
-  const int lo = q.length == 0 ? q.n : p.cu_seqlens ? p.places[q.t].x : 0;
-  const int hi = q.length == 0 ? q.n + 1 : p.cu_seqlens ? p.places[q.t + 1].x : p.N;
+  const int lo = kMode == kByChains ? q.n : p.cu_seqlens ? p.places[q.t].x : 0;
+  const int hi = kMode == kByChains ? q.n + 1 : p.cu_seqlens ? p.places[q.t + 1].x : p.N;
   for (int n = lo + warp; n < hi; n += kWarps) {
     if (p.cu_seqlens && p.cu_seqlens[n] != p.cu_seqlens[n + 1]) continue;
     const int slot = slot_of(p, n);
@@ -804,19 +811,20 @@ struct Backward {
 // ---------------------------------------------------------------- the scan kernel
 
 // Blocks are persistent and take tiles one after another.
-// By tiles (`runs`: long scans over few channels, packed batches of short sequences): by tickets in
+// By tiles (long scans over few channels), and packed batches of short sequences: by tickets in
 // walking order, all channels of a place before the next, the sequences of a fixed-length batch
 // side by side; the states pass from block to block.
 // By chains: all tiles of a sequence's channels in order, the state passing in shared memory and no
 // block waiting for another; chains in turn, or by tickets the longest first (packed).
 // Tiles of several whole sequences: in turn.
-template <typename E, bool kBack, bool kTma>
+template <typename E, bool kBack, bool kTma, Mode kMode>
 __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBack, kTma>::kBlocks)
     gated_scan_kernel(const __grid_constant__ Params<E> p, const __grid_constant__ Maps maps) {
   using S = Shape<E, kBack, kTma>;
   constexpr int K = S::kRows, kWarps = S::kWarps;
+  const bool waits = kMode == kByTiles || (kMode == kMixed && p.runs);  // states pass from block to block
   extern __shared__ __align__(128) char shared[];
-  ScanSmem<kWarps>& sm = *reinterpret_cast<ScanSmem<kWarps>*>(shared + kStages * S::kStageBytes);
+  auto& sm = *reinterpret_cast<ScanSmem<kMode, kWarps>*>(shared + kStages * S::kStageBytes);
   // uniform in the warp, and known to be
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int mine = (kBack ? kWarps - 1 - warp : warp) * K;  // the warp's first row in a stage
@@ -839,39 +847,48 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
   Tile chain{0, 0, 0, 0, 0, 0, 0, 0};
   int step = 0, steps = 0, turns = static_cast<int>(blockIdx.x);
   auto next_id = [&] {
-    if (p.runs || (p.order && step == steps)) return atomicAdd(p.ticket, 1);
+    if (waits || (kMode == kByChains && p.order && step == steps)) return atomicAdd(p.ticket, 1);
     return 0;
   };
   auto tile_of = [&](int id) -> Tile {
     constexpr Tile kNone{-1, 0, 0, 0, 0, 0, 0, 0};
-    if (p.runs) {
-      if (id >= total) return kNone;
-      const int place = id / p.columns, column = id - place * p.columns;
-      const int i = p.per ? place / p.N : place, n = p.per ? place - i * p.N : 0;
-      const int at = kBack ? (p.per ? p.per : p.tiles) - 1 - i : i;
-      return {n * p.per + at, column, n, i, i % p.group, n * p.T + at * p.stride, at * p.stride, p.per ? p.T : -1};
-    }
-    if (step == steps) {  // the next chain
-      if (!p.order) {
+    if constexpr (kMode == kByChains) {
+      if (step == steps) {  // the next chain
+        if (!p.order) {
+          id = turns;
+          turns += static_cast<int>(gridDim.x);
+        }
+        const int place = id / p.columns;
+        if (p.order ? id >= total : place >= p.N) return kNone;
+        chain.column = id - place * p.columns;
+        chain.t = chain.n = p.order ? p.order[place] : place;
+        chain.row = p.order ? p.cu_seqlens[chain.n] : place * p.T;
+        chain.length = p.order ? p.cu_seqlens[chain.n + 1] - chain.row : p.T;
+        step = 0;
+        steps = chain.length <= p.stride ? 1 : (chain.length + p.stride - 1) / p.stride;
+      }
+      Tile q = chain;
+      q.i = step;
+      q.token = kBack ? q.length - (step + 1) * p.stride : step * p.stride;
+      q.row += q.token;
+      ++step;
+      return q;
+    } else {
+      if (!waits) {
         id = turns;
         turns += static_cast<int>(gridDim.x);
       }
-      const int place = id / p.columns;
-      if (p.order ? id >= total : place >= (p.per ? p.N : p.tiles)) return kNone;
-      chain.column = id - place * p.columns;
-      chain.t = p.order ? p.order[place] : place;
-      chain.n = p.order || p.per ? chain.t : 0;
-      chain.row = p.order ? p.cu_seqlens[chain.n] : place * (p.per ? p.T : p.stride);
-      chain.length = p.order ? p.cu_seqlens[chain.n + 1] - chain.row : p.per ? p.T : -1;
-      step = 0;
-      steps = chain.length <= p.stride ? 1 : (chain.length + p.stride - 1) / p.stride;
+      if (id >= total) return kNone;
+      const int place = id / p.columns, column = id - place * p.columns;
+      if constexpr (kMode == kByTiles) {
+        const int i = place / p.N, n = place - i * p.N, at = kBack ? p.per - 1 - i : i;
+        const int token = kBack ? p.T - (i + 1) * p.stride : i * p.stride;
+        return {n * p.per + at, column, n, i, i % p.group, n * p.T + token, token, p.T};
+      } else {
+        const int at = waits && kBack ? p.tiles - 1 - place : place, i = waits ? place : 0;
+        return {at, column, 0, i, i % p.group, at * p.stride, at * p.stride, -1};
+      }
     }
-    Tile q = chain;
-    q.i = step;
-    q.token = (kBack ? steps - 1 - step : step) * p.stride;
-    q.row += q.token;
-    ++step;
-    return q;
   };
   int loaded = -1;  // the last turn whose tile has been asked for
   auto load = [&](int turn) {
@@ -888,14 +905,14 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
   // What has_edges wants to know of a tile, a turn ahead of its use.
   auto look_up = [&](const Tile& q) {
     if (q.t < 0) return 0;
-    if (q.length >= 0) return p.state_indices ? p.state_indices[q.n] : q.n;
-    return p.places ? p.places[q.t].y : 0;
+    if constexpr (kMode == kMixed) return p.places ? p.places[q.t].y : 0;
+    return p.state_indices ? p.state_indices[q.n] : q.n;
   };
 
   if (threadIdx.x == 0) {
     sm.tile[0] = tile_of(next_id());
     // blocks that have one tile each take no second one ahead of a block that starts later
-    sm.tile[1] = p.runs && total <= static_cast<int>(gridDim.x) ? Tile{-1, 0, 0, 0, 0, 0, 0, 0} : tile_of(next_id());
+    sm.tile[1] = waits && total <= static_cast<int>(gridDim.x) ? Tile{-1, 0, 0, 0, 0, 0, 0, 0} : tile_of(next_id());
   }
   __syncthreads();
   load(0);
@@ -915,27 +932,36 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
     q.token = __shfl_sync(0xFFFFFFFFu, q.token, 0);
     q.length = __shfl_sync(0xFFFFFFFFu, q.length, 0);
     if (q.t < 0) break;
-    Exchange<kWarps>& ex = sm.turn[turn & 1];
+    auto& ex = sm.turn[turn & 1];
     const Tile& then = sm.tile[(turn + 1) & 3];
     const bool more = threadIdx.x == 0 && then.t >= 0;
     const int ahead = more ? next_id() : 0;
     const int next_inside = look_up(then);
     const f2 next_slope = load_state(p.slopes, 0, p.C, Lane<kTma>(then.column, lane, p.C));
-    const bool edges = __any_sync(0xFFFFFFFFu, has_edges<kBack, K>(p, q, inside, warp));
+    const bool edges = __any_sync(0xFFFFFFFFu, has_edges<kMode, kBack, K>(p, q, inside, mine));
+    auto start_state = [&] {
+      if (kMode == kMixed || inside < 0 || inside >= p.pool_size) return f2_all(0.f);
+      return load_state(p.start, inside, p.C, Lane<kTma>(q.column, lane, p.C));
+    };
+    const f2 start = kMode == kByChains && q.i == 0 ? start_state() : f2_all(0.f);
     const int low = q.row + (kBack ? p.stride - S::kTileRows : 0) + mine;
     const char* stage = shared + turn % kStages * S::kStageBytes + mine * S::kPitch;
     auto ask = [&] {
-      if (p.runs) Needs<kWarps>(p, q, warp).ask(p, ex, q, warp, lane);
+      if (waits) Needs<kWarps>(p, q, warp).ask(p, ex, q, warp, lane);
     };
     unsigned begins = 0u;
     auto close = [&](const Run& run) {  // the warp's rows are composed
       ex.own[warp][lane] = run;
-      if (lane == 0) ex.begins[warp] = begins != 0u;
+      if (kMode == kMixed && lane == 0) ex.begins[warp] = begins != 0u;
       if (threadIdx.x == 0) {
         sm.tile[(turn + 2) & 3] = more ? tile_of(ahead) : Tile{-1, 0, 0, 0, 0, 0, 0, 0};
-        ex.fresh = q.length >= 0 ? q.i == 0 : begins & 1u;
+        if (kMode == kMixed) ex.fresh = begins & 1u;
       }
-      if (p.runs) Needs<kWarps>(p, q, warp).look(ex, q, warp, lane);
+      if (waits) {
+        // the first group's; before the barrier, so read before any block may write a final state there
+        if (warp == kWarps - 1 && q.i == q.j) ex.base[lane] = start_state();
+        Needs<kWarps>(p, q, warp).look(ex, q, warp, lane);
+      }
     };
     const bool here = arrived<kTma>(&sm.bar[warp][turn % kStages], turn / kStages, &sm.abort);
     if constexpr (!kBack) {
@@ -944,8 +970,8 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
       const float2 s = f2_unpack(slope);
       const bool small = __all_sync(0xFFFFFFFFu, s.x < kNear && s.y < kNear);
       Run run;
-      if (edges) {
-        const Rows rows = rows_of<kBack, K>(p, q, warp, lane);
+      if (kMode == kMixed && edges) {
+        const Rows rows = rows_of<kMode, kBack, K>(p, q, warp, lane);
         begins = rows.begin;
         run = f.template first<true, false>(p, stage, low, slope, rows, Lane<kTma>(q.column, lane, p.C), lane, ask);
       } else if (small) {
@@ -956,17 +982,17 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
       close(run);
       if (__syncthreads_or(!here)) break;
       load(turn + kStages);  // every warp has this tile's rows in registers: its stage takes the tile after next
-      const f2 h = state_before(p, ex, sm.turn[(turn + 1) & 1], q, run, warp, lane);
+      const f2 h = state_before<kMode>(p, ex, sm.turn[(turn + 1) & 1], q, run, start, warp, lane);
       if (edges)
-        f.template second<true>(p, low, h, rows_of<kBack, K>(p, q, warp, lane), Lane<kTma>(q.column, lane, p.C));
+        f.template second<true>(p, low, h, rows_of<kMode, kBack, K>(p, q, warp, lane), Lane<kTma>(q.column, lane, p.C));
       else
         f.template second<false>(p, low, h, Rows{}, Lane<kTma>(q.column, lane, p.C));
     } else {
       Backward<E, kTma> f;
       const Lane<kTma> l(q.column, lane, p.C);
       Run run;
-      if (edges) {
-        const Rows rows = rows_of<kBack, K>(p, q, warp, lane);
+      if (kMode == kMixed && edges) {
+        const Rows rows = rows_of<kMode, kBack, K>(p, q, warp, lane);
         begins = rows.begin;
         run = f.template first<true>(p, stage, low, slope, rows, l, lane, ask);
       } else {
@@ -974,13 +1000,13 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
       }
       close(run);
       if (__syncthreads_or(!here)) break;
-      const f2 w = state_before(p, ex, sm.turn[(turn + 1) & 1], q, run, warp, lane);
-      const f2 sum = edges ? f.template second<true>(p, stage, low, slope, w, rows_of<kBack, K>(p, q, warp, lane), l, lane)
+      const f2 w = state_before<kMode>(p, ex, sm.turn[(turn + 1) & 1], q, run, start, warp, lane);
+      const f2 sum = edges ? f.template second<true>(p, stage, low, slope, w, rows_of<kMode, kBack, K>(p, q, warp, lane), l, lane)
                            : f.template second<false>(p, stage, low, slope, w, Rows{}, l, lane);
       ds = f2_add(ds, sum);
       __syncthreads();
       load(turn + kStages);
-      if (p.runs || (q.i + 1) * p.stride >= q.length) {  // the end of a tile or chain: its terms of dslopes, warps in order
+      if (kMode != kByChains || (q.i + 1) * p.stride >= q.length) {  // the end of a tile or chain: its terms of dslopes, warps in order
         ex.own[warp][lane].h = ds;
         __syncthreads();
         if (warp == 0) {
@@ -991,7 +1017,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
         ds = f2_all(0.f);
       }
     }
-    if (edges) empty_sequences<kWarps>(p, q, Lane<kTma>(q.column, lane, p.C), warp);
+    if (edges) empty_sequences<kMode, kWarps>(p, q, Lane<kTma>(q.column, lane, p.C), warp);
     inside = next_inside;
     slope = next_slope;
   }
