@@ -26,8 +26,9 @@ struct Plan {
   bool ticket = false; // a plan kernel runs first
   bool waits = false;  // states pass from block to block
   bool order = false;  // packed, by chains
+  bool table = false;  // packed, by tiles of one sequence each
   lag::Mode mode = lag::kMixed;
-  size_t table = 0, runs = 0, words = 0, before = 0, part = 0, bytes = 0;
+  size_t list = 0, runs = 0, words = 0, before = 0, part = 0, bytes = 0;
 };
 
 // Blocks the largest part holds at once; a device with fewer SMs runs the same plan.
@@ -50,11 +51,20 @@ bool by_chains(int64_t chains, int per) {
   const int64_t waves = (chains + kSlots - 1) / kSlots;
   return per <= 4 || chains * 100 >= waves * kSlots * 80;
 }
-// Packed: where there are chains enough, of several tiles each on average (32 sequences of up to 4096
-// tokens: 4096 channels 394 us by chains and 568 by tiles, gradients of 1001 channels 427 and 665).
+// Packed: by chains where there are enough of them to fill the device evenly and the sequences are
+// not mostly shorter than half a tile.  By chains, in tiles of one sequence each, and in tiles of
+// mixed rows, us: 32 sequences of up to 4096 tokens, 4096 channels, 2048 chains: 327, 413, 532; 40 of
+// up to 8192, 1024 channels, 640 chains: 218, 245, 467 (gradients 453, 463, 923); 16 of them, 2048
+// channels, 512 chains: 219, 203, 320 (442, 387, 600); 16, 1024 channels: 193, 127, 214 (359, 234,
+// 416).  2048 channels, 38400 tokens: 200 sequences 197, 326, 421; 600 249, 428, 246; 1200 499, 837, 250.
 bool packed_by_chains(int64_t tokens, int N, int columns, int stride) {
-  return N <= 1024 && static_cast<int64_t>(N) * columns * 2 >= 3 * kSlots && tokens >= static_cast<int64_t>(N) * stride * 4;
+  return static_cast<int64_t>(N) * columns >= 2 * kSlots && tokens * 2 >= static_cast<int64_t>(N) * stride;
 }
+// Else in tiles of one sequence each, where those are not mostly single tiles (2048 channels, 300
+// sequences of up to 256 tokens, two tiles of 128 rows or four of 72: forward 296 and 269 in mixed
+// ones, gradients 412 and 546).
+bool packed_by_tiles(int64_t tokens, int N, int stride) { return tokens * 2 >= static_cast<int64_t>(N) * stride * 3; }
+constexpr int kMostListed = 4096;  // sequences of a batch whose order the plan kernel finds by comparing all
 
 template <typename E, bool kBack, bool kTma>
 Plan plan_for(int B, int T, int N, int C, bool packed) {
@@ -69,29 +79,32 @@ Plan plan_for(int B, int T, int N, int C, bool packed) {
   } else if (!packed && T > 0) {
     q.per = (T + q.stride - 1) / q.stride;
     q.waits = !by_chains(static_cast<int64_t>(B) * q.columns, q.per);
-  } else if (packed) {
+  } else if (packed && N <= kMostListed) {
     q.order = packed_by_chains(rows, N, q.columns, q.stride);
-    q.waits = !q.order;
+    q.table = !q.order && packed_by_tiles(rows, N, q.stride);
   }
+  q.waits = q.waits || (packed && !q.order);
   q.ticket = q.waits || q.order;
   if (q.order || (q.per && !q.waits)) q.mode = lag::kByChains;
-  else if (q.per) q.mode = lag::kByTiles;
-  q.tiles = q.per ? B * q.per : static_cast<int>((rows + q.stride - 1) / q.stride);
+  else if (q.per || q.table) q.mode = lag::kByTiles;
+  q.tiles = q.per ? B * q.per : q.table ? static_cast<int>(rows / q.stride) + N : static_cast<int>((rows + q.stride - 1) / q.stride);
   if (q.tiles == 0) q.tiles = 1;  // empty sequences alone
   q.parts = q.mode == lag::kByChains ? N : q.tiles;
   q.items = q.parts * q.columns;
   q.group = group_of(q.columns, S::kWarps);
   q.groups = ((q.per ? q.per : q.tiles) + q.group - 1) / q.group;
   if (q.ticket) {
-    q.table = 256;
-    const size_t table = q.order ? static_cast<size_t>(N) * 4 : packed ? (static_cast<size_t>(q.tiles) + 1) * sizeof(int2) : 0;
-    q.bytes = q.table + la_host::align256(table);
+    q.list = 256;
+    const size_t list = q.order ? static_cast<size_t>(N) * sizeof(int32_t) : q.table ? q.tiles * sizeof(lag::Tile)
+                        : packed ? (static_cast<size_t>(q.tiles) + 1) * sizeof(int2) : 0;
+    q.bytes = q.list + la_host::align256(list);
   }
   if (q.waits) {
     const size_t width = static_cast<size_t>(q.columns) * lag::kCols;
+    const size_t groups = q.per ? static_cast<size_t>(B) * q.groups : static_cast<size_t>(q.groups) + (q.table ? N : 0);
     q.runs = q.bytes;
     q.before = q.runs + q.tiles * width * 8;
-    q.words = q.tiles * width * 2 + static_cast<size_t>(q.per ? B : 1) * q.groups * width;
+    q.words = q.tiles * width * 2 + groups * width;
     q.bytes = q.runs + la_host::align256(q.words * 4);
   }
   q.part = q.bytes;
@@ -123,8 +136,8 @@ la_status check_sizes(int B, int T, int N, int C, bool packed, la_dtype dtype) {
   }
   if (static_cast<int64_t>(B) * T > la_host::kMaxRows)
     return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)B * T);
-  // tiles of at least 32 rows and 64 channels, numbered below 2^30 (more than any memory holds)
-  if ((static_cast<int64_t>(B) * T / 32 + 1) * ((C + 63) / 64) >= int64_t(1) << 30)
+  // tiles of at least 16 rows and 64 channels, numbered below 2^30 (more than any memory holds)
+  if ((static_cast<int64_t>(B) * T / 16 + kMostListed) * ((C + 63) / 64) >= int64_t(1) << 30)
     return fail(LA_ERR_UNSUPPORTED, "B*T*C too large");
   if (static_cast<int64_t>(N) * ((C + 63) / 64) > INT32_MAX) return fail(LA_ERR_UNSUPPORTED, "N*C too large");
   return LA_OK;
@@ -156,9 +169,10 @@ void set_plan(lag::Params<E>* p, const Plan& q, bool backward, void* workspace) 
   p->groups = q.groups;
   p->per = q.per;
   if (q.ticket) p->ticket = reinterpret_cast<int*>(ws);
-  if (q.order) p->order = reinterpret_cast<int32_t*>(ws + q.table);
+  if (q.order) p->order = reinterpret_cast<int32_t*>(ws + q.list);
   if (q.waits) {
-    if (p->cu_seqlens) p->places = reinterpret_cast<int2*>(ws + q.table);
+    if (q.table) p->table = reinterpret_cast<lag::Tile*>(ws + q.list);
+    else if (p->cu_seqlens) p->places = reinterpret_cast<int2*>(ws + q.list);
     p->runs = reinterpret_cast<float4*>(ws + q.runs);
     p->before = reinterpret_cast<float2*>(ws + q.before);
   }
@@ -194,7 +208,7 @@ la_status encode_rows_map(CUtensorMap* map, const E* base, int64_t rows, int64_t
 template <typename E>
 cudaError_t launch_plan(const lag::Params<E>& p, const Plan& q, int sms, cudaStream_t s) {
   size_t want = q.words / 4;
-  if (q.order) want = static_cast<size_t>(p.N) * (p.part ? p.C / 16 + 1 : 1);
+  if (q.order) want = static_cast<size_t>(p.N);
   want = (want + lag::kThreads - 1) / lag::kThreads;
   const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want < size_t(sms) * 8 ? want : size_t(sms) * 8);
   return la_host::launch_pdl(lag::scan_plan_kernel<E>, grid, lag::kThreads, 0, s, p, q.words);
@@ -232,7 +246,7 @@ la_status launch_scan_as(lag::Params<E> p, int B, void* workspace, float* dslope
   }
   if (ce == cudaSuccess && kBack)
     ce = la_host::launch_pdl(lag::column_sum_kernel, (p.C + 31) / 32, 1024, 0, s, static_cast<const float*>(p.part),
-                             q.parts, p.C, static_cast<const int*>(packed ? p.ticket : nullptr), dslopes);
+                             q.parts, p.C, static_cast<const int*>(packed ? p.ticket : nullptr), q.order || q.table, dslopes);
   return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
 }
 

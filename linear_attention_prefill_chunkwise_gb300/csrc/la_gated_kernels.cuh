@@ -73,8 +73,17 @@ struct Shape {
 // forward 216 and 197 us, gradients 425 and 385).
 enum Mode {
   kByChains,  // one block walks all tiles of a sequence's channels
-  kByTiles,   // tiles of sequences of one length, states from block to block
+  kByTiles,   // tiles of one sequence each, states from block to block
   kMixed      // tiles that hold rows of several sequences: packed (states from block to block) or whole ones
+};
+
+// A tile: its number (-1: none), its channels, its sequence n, its place i in the walk over that
+// sequence (kMixed: n is 0 and i the place among all tiles), i's place j in its group and the group's
+// number, its lowest row, and the rows from the tile's first to the walk's last (kMixed: -1).  Walked
+// from the end, the last tile may begin before the sequence.
+// Numbers count in walking order, sequence after sequence; by chains the chain's; kMixed along the rows.
+struct __align__(16) Tile {
+  int t, column, n, i, j, g, row, left;
 };
 
 template <typename E>
@@ -87,20 +96,21 @@ struct Params {
   const float* start;  // [P, C] states the walk begins with (h0; dh_final) or null
   const float* h0;     // backward: [P, C] or null
   float* finish;       // [P, C] states it ends with (h_final; dh0) or null
-  float* part;         // backward: [tiles, C] sums of each tile's terms of dslopes
+  float* part;         // backward: [tiles or chains, C] sums of each one's terms of dslopes
   const int32_t* state_indices;
   const int32_t* cu_seqlens;
   const int32_t* accepted_len;  // commit
   int* dev_error;
   // the workspace of a scan
-  int* ticket;         // next tile or chain, an abort flag, running sequences; null: blocks take theirs in turn
-  int2* places;        // [tiles + 1] (packed, by tiles) where each tile lies among the sequences
+  int* ticket;         // next tile or chain, an abort flag, how many (packed); null: blocks take theirs in turn
+  int2* places;        // [tiles + 1] (packed, kMixed) where each tile lies among the sequences
   int32_t* order;      // [N] (packed, by chains) the running sequences, longest first
+  Tile* table;         // [tiles] (packed, by tiles) the tiles in the order in which they are taken
   float4* runs;        // [tiles][columns][32] published (A, H) of each lane's two channels; null: nothing waits
-  float2* before;      // [sequences, or 1][groups][columns][32] published states after each group
+  float2* before;      // [groups of all sequences][columns][32] published states after each group
   int T, N, C, pool_size, rows;
   int tiles, columns, stride;  // tiles along the rows, of `stride` rows; along the channels
-  int group, groups;           // tiles per group; groups of a sequence (of all rows without `per`)
+  int group, groups;           // tiles per group; groups of a sequence of one length
   // Sequences of one length: tiles per sequence (the last may be short); 0: packed, or tiles that
   // hold several whole sequences.
   int per;
@@ -118,10 +128,10 @@ __device__ __forceinline__ void report(int* dev_error, unsigned bit) {
 
 // Fills the published words, sets the ticket and, for a packed batch, checks cu_seqlens
 // (non-decreasing inside [0, T]; if not, the ticket starts past the last tile, so that the scan
-// does nothing).  By tiles, it finds each tile's place: x, the first sequence that begins at or
+// does nothing).  kMixed: it finds each tile's place: x, the first sequence that begins at or
 // after its first row; y, whether all its rows lie inside one running sequence, away from its ends.
-// By chains, it orders the running sequences, longest first (ties by number), and clears the
-// partial sums of the others.
+// By chains, it orders the running sequences, longest first (ties by number); by tiles, it lists the
+// running sequences' tiles: the first of each, longest sequence first, then the second of each, ...
 template <typename E>
 __global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p, size_t words) {
   lap::griddep_wait();
@@ -164,9 +174,45 @@ __global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p, 
       else if (p.state_indices && p.state_indices[n] >= p.pool_size) report(p.dev_error, kErrBadIndex);
       if (n == 0) p.ticket[2] = running;
     }
-    if (p.part)
-      for (size_t i = id; i < static_cast<size_t>(p.N) * p.C; i += all)
-        if (length(static_cast<int>(i / p.C)) < 0) p.part[i] = 0.f;
+  }
+  if (p.table) {
+    auto tiles_of = [&](int n) {  // 0: does not run
+      const int slot = p.state_indices ? p.state_indices[n] : n;
+      const int length = min(max(p.cu_seqlens[n + 1] - p.cu_seqlens[n], 0), p.T);
+      return slot < 0 || slot >= p.pool_size ? 0 : length <= p.stride ? 1 : (length + p.stride - 1) / p.stride;
+    };
+    for (size_t i = id; i < static_cast<size_t>(p.N); i += all)
+      if (p.state_indices && p.state_indices[i] >= p.pool_size) report(p.dev_error, kErrBadIndex);
+    for (size_t k = id; k < static_cast<size_t>(p.tiles); k += all) {
+      const int t = static_cast<int>(k);
+      int n = -1, sum = 0, first = 0, g = 0;  // t's sequence; tiles so far; n's first tile and group
+#pragma unroll 4
+      for (int m = 0; m < p.N; ++m) {
+        const int tiles = tiles_of(m);
+        if (n < 0) {
+          if (t - sum < tiles) {
+            n = m;
+            first = sum;
+          } else {
+            g += (tiles + p.group - 1) / p.group;
+          }
+        }
+        sum = min(sum + tiles, p.tiles);  // (as it is unless cu_seqlens is refused)
+      }
+      if (t == 0) p.ticket[2] = sum;
+      if (n < 0) continue;
+      const int i = t - first, mine = tiles_of(n);
+      int at = 0;
+#pragma unroll 4
+      for (int m = 0; m < p.N; ++m) {
+        const int tiles = tiles_of(m);
+        at = min(at + min(tiles, i) + (tiles > i && (tiles > mine || (tiles == mine && m < n))), p.tiles);
+      }
+      const int lo = p.cu_seqlens[n], hi = p.cu_seqlens[n + 1];
+      if (at < p.tiles)
+        p.table[at] = {t, 0, n, i, i % p.group, g + i / p.group,
+                       p.part ? hi - (i + 1) * p.stride : lo + i * p.stride, hi - lo - i * p.stride};
+    }
   }
   if (blockIdx.x == 0) {
     int wrong = 0;
@@ -205,26 +251,16 @@ __device__ __forceinline__ int slot_of(const Params<E>& p, int n) {
   return checked(p, p.state_indices ? p.state_indices[n] : n);
 }
 
-// A tile: its number along the rows (-1: none), its channels, its sequence n and place i in that
-// sequence in walking order (where tiles hold rows of several sequences: 0 and its place among all
-// tiles), i's place j in its group, its lowest row and that row's token in the sequence (walked from
-// the end, the last tile may begin before the sequence: below 0), and the sequence's length (-1:
-// rows of several).
-struct Tile {
-  int t, column, n, i, j, row, token, length;
-};
-
 template <Mode kMode, bool kBack, int K, typename E>
 __device__ __forceinline__ Rows rows_of(const Params<E>& p, const Tile& q, int warp, int lane) {
   if constexpr (kMode != kMixed) {  // by arithmetic, the same for every lane
     const int slot = p.state_indices ? p.state_indices[q.n] : q.n;
-    const int place = warp * K;
     auto bit = [](int k) { return k >= 0 && k < K ? 1u << k : 0u; };
     auto below = [](int k) { return k <= 0 ? 0u : k >= K ? (1u << K) - 1u : (1u << k) - 1u; };  // bits under k
     Rows r{0u, 0u, 0u, checked(p, slot)};
     if (r.slot < 0) return r;
     // tiles begin where the walk does, so no row begins the sequence: its state comes from outside
-    const int left = kBack ? q.token + p.stride - place : q.length - q.token - place;  // rows to the walk's end
+    const int left = q.left - warp * K;
     r.live = below(left);
     r.end = bit(left - 1);
     return r;
@@ -265,12 +301,11 @@ __device__ __forceinline__ Rows rows_of(const Params<E>& p, const Tile& q, int w
 
 // Whether some row of the warp may end a sequence or belong to none (kMixed: or begin one).
 // `inside`: what was looked up for the tile (its sequence's slot; kMixed: whether the tile lies
-// inside a sequence); `first`: the warp's first row in the tile.
-template <Mode kMode, bool kBack, int K, typename E>
-__device__ __forceinline__ bool has_edges(const Params<E>& p, const Tile& q, int inside, int first) {
+// inside a sequence).
+template <Mode kMode, int K, typename E>
+__device__ __forceinline__ bool has_edges(const Params<E>& p, const Tile& q, int inside, int warp) {
   if constexpr (kMode == kMixed) return !inside;
-  const int low = q.token + first;
-  return inside < 0 || inside >= p.pool_size || (kBack ? low <= 0 : low + K >= q.length);
+  return inside < 0 || inside >= p.pool_size || q.left <= (warp + 1) * K;
 }
 
 // A lane's two channels: neighbours with TMA rows, else a warp's width apart.
@@ -535,7 +570,7 @@ __host__ __device__ constexpr int scan_smem_bytes() {
 
 // The published words a tile needs: where it has more than kWarps earlier tiles in its group, each
 // warp composes a piece [lo, hi) of them.
-template <int kWarps>
+template <Mode kMode, int kWarps>
 struct Needs {
   int j, per, lo, hi;
   template <typename E>
@@ -545,15 +580,15 @@ struct Needs {
     lo = min(j, warp * per);
     hi = min(j, lo + per);
   }
-  // The run of the group's i-th tile (tiles are numbered in walking order within a sequence).
+  // The run of the group's i-th tile.
   template <typename E>
   __device__ __forceinline__ float4* run(const Params<E>& p, const Tile& q, int i, int lane) const {
-    return p.runs + (static_cast<size_t>(q.n * p.per + q.i - j + i) * p.columns + q.column) * 32 + lane;
+    return p.runs + (static_cast<size_t>((kMode == kMixed ? q.i : q.t) - j + i) * p.columns + q.column) * 32 + lane;
   }
   // The state after this tile's group, or after the one `back` before it.
   template <typename E>
   __device__ __forceinline__ float2* state(const Params<E>& p, const Tile& q, int back, int lane) const {
-    return p.before + (static_cast<size_t>(q.n * p.groups + (q.i - j) / p.group - back) * p.columns + q.column) * 32 + lane;
+    return p.before + (static_cast<size_t>(q.g - back) * p.columns + q.column) * 32 + lane;
   }
 
   // Asks for the words, where each warp needs one tile's (the last warp: the base too) ...
@@ -620,7 +655,7 @@ __device__ __forceinline__ f2 state_before(const Params<E>& p, Exchange<kMode, k
     f2 before = f2_all(0.f);
     const bool fresh = kMode == kMixed && __any_sync(0xFFFFFFFFu, ex.fresh);
     if (kMode == kByTiles || p.runs) {
-      const Needs<kWarps> needs(p, q, warp);
+      const Needs<kMode, kWarps> needs(p, q, warp);
       const bool last = needs.j == p.group - 1;
       Run whole;
       if (warp == 0) {
@@ -656,9 +691,9 @@ __device__ __forceinline__ f2 state_before(const Params<E>& p, Exchange<kMode, k
 // ones.
 template <Mode kMode, int kWarps, typename E, bool kTma>
 __device__ __forceinline__ void empty_sequences(const Params<E>& p, const Tile& q, const Lane<kTma>& l, int warp) {
-  if (!p.finish || q.length > 0 || (!p.cu_seqlens && p.T > 0)) return;
-  const int lo = kMode == kByChains ? q.n : p.cu_seqlens ? p.places[q.t].x : 0;
-  const int hi = kMode == kByChains ? q.n + 1 : p.cu_seqlens ? p.places[q.t + 1].x : p.N;
+  if (!p.finish || q.left > 0 || (!p.cu_seqlens && p.T > 0)) return;
+  const int lo = kMode != kMixed ? q.n : p.cu_seqlens ? p.places[q.t].x : 0;
+  const int hi = kMode != kMixed ? q.n + 1 : p.cu_seqlens ? p.places[q.t + 1].x : p.N;
   for (int n = lo + warp; n < hi; n += kWarps) {
     if (p.cu_seqlens && p.cu_seqlens[n] != p.cu_seqlens[n + 1]) continue;
     const int slot = slot_of(p, n);
@@ -813,7 +848,7 @@ struct Backward {
 // Blocks are persistent and take tiles one after another.
 // By tiles (long scans over few channels), and packed batches of short sequences: by tickets in
 // walking order, all channels of a place before the next, the sequences of a fixed-length batch
-// side by side; the states pass from block to block.
+// (or of a packed batch's table) side by side; the states pass from block to block.
 // By chains: all tiles of a sequence's channels in order, the state passing in shared memory and no
 // block waiting for another; chains in turn, or by tickets the longest first (packed).
 // Tiles of several whole sequences: in turn.
@@ -843,7 +878,8 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
   lap::griddep_launch_dependents();
 
   // Thread 0's: the number of the next tile or chain (asked for early, looked at late), and the tile.
-  const int total = (p.order ? p.ticket[2] : p.tiles) * p.columns;
+  const int total = (p.order || p.table ? p.ticket[2] : p.tiles) * p.columns;
+  constexpr Tile kNone{-1, 0, 0, 0, 0, 0, 0, 0};
   Tile chain{0, 0, 0, 0, 0, 0, 0, 0};
   int step = 0, steps = 0, turns = static_cast<int>(blockIdx.x);
   auto next_id = [&] {
@@ -851,7 +887,6 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
     return 0;
   };
   auto tile_of = [&](int id) -> Tile {
-    constexpr Tile kNone{-1, 0, 0, 0, 0, 0, 0, 0};
     if constexpr (kMode == kByChains) {
       if (step == steps) {  // the next chain
         if (!p.order) {
@@ -861,16 +896,17 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
         const int place = id / p.columns;
         if (p.order ? id >= total : place >= p.N) return kNone;
         chain.column = id - place * p.columns;
-        chain.t = chain.n = p.order ? p.order[place] : place;
-        chain.row = p.order ? p.cu_seqlens[chain.n] : place * p.T;
-        chain.length = p.order ? p.cu_seqlens[chain.n + 1] - chain.row : p.T;
+        chain.t = place;
+        chain.n = p.order ? p.order[place] : place;
+        chain.row = p.order ? p.cu_seqlens[chain.n] : place * p.T;  // of the sequence
+        chain.left = p.order ? p.cu_seqlens[chain.n + 1] - chain.row : p.T;
         step = 0;
-        steps = chain.length <= p.stride ? 1 : (chain.length + p.stride - 1) / p.stride;
+        steps = chain.left <= p.stride ? 1 : (chain.left + p.stride - 1) / p.stride;
       }
       Tile q = chain;
       q.i = step;
-      q.token = kBack ? q.length - (step + 1) * p.stride : step * p.stride;
-      q.row += q.token;
+      q.left -= step * p.stride;
+      q.row += kBack ? q.left - p.stride : step * p.stride;
       ++step;
       return q;
     } else {
@@ -881,12 +917,17 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
       if (id >= total) return kNone;
       const int place = id / p.columns, column = id - place * p.columns;
       if constexpr (kMode == kByTiles) {
-        const int i = place / p.N, n = place - i * p.N, at = kBack ? p.per - 1 - i : i;
-        const int token = kBack ? p.T - (i + 1) * p.stride : i * p.stride;
-        return {n * p.per + at, column, n, i, i % p.group, n * p.T + token, token, p.T};
+        if (p.table) {
+          Tile q = p.table[place];
+          q.column = column;
+          return q;
+        }
+        const int i = place / p.N, n = place - i * p.N, left = p.T - i * p.stride;
+        return {n * p.per + i, column, n, i, i % p.group, n * p.groups + i / p.group,
+                n * p.T + (kBack ? left - p.stride : i * p.stride), left};
       } else {
         const int at = waits && kBack ? p.tiles - 1 - place : place, i = waits ? place : 0;
-        return {at, column, 0, i, i % p.group, at * p.stride, at * p.stride, -1};
+        return {at, column, 0, i, i % p.group, i / p.group, at * p.stride, -1};
       }
     }
   };
@@ -912,7 +953,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
   if (threadIdx.x == 0) {
     sm.tile[0] = tile_of(next_id());
     // blocks that have one tile each take no second one ahead of a block that starts later
-    sm.tile[1] = waits && total <= static_cast<int>(gridDim.x) ? Tile{-1, 0, 0, 0, 0, 0, 0, 0} : tile_of(next_id());
+    sm.tile[1] = waits && total <= static_cast<int>(gridDim.x) ? kNone : tile_of(next_id());
   }
   __syncthreads();
   load(0);
@@ -928,9 +969,9 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
     q.n = __shfl_sync(0xFFFFFFFFu, q.n, 0);
     q.i = __shfl_sync(0xFFFFFFFFu, q.i, 0);
     q.j = __shfl_sync(0xFFFFFFFFu, q.j, 0);
+    q.g = __shfl_sync(0xFFFFFFFFu, q.g, 0);
     q.row = __shfl_sync(0xFFFFFFFFu, q.row, 0);
-    q.token = __shfl_sync(0xFFFFFFFFu, q.token, 0);
-    q.length = __shfl_sync(0xFFFFFFFFu, q.length, 0);
+    q.left = __shfl_sync(0xFFFFFFFFu, q.left, 0);
     if (q.t < 0) break;
     auto& ex = sm.turn[turn & 1];
     const Tile& then = sm.tile[(turn + 1) & 3];
@@ -938,7 +979,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
     const int ahead = more ? next_id() : 0;
     const int next_inside = look_up(then);
     const f2 next_slope = load_state(p.slopes, 0, p.C, Lane<kTma>(then.column, lane, p.C));
-    const bool edges = __any_sync(0xFFFFFFFFu, has_edges<kMode, kBack, K>(p, q, inside, mine));
+    const bool edges = __any_sync(0xFFFFFFFFu, has_edges<kMode, K>(p, q, inside, warp));
     auto start_state = [&] {
       if (kMode == kMixed || inside < 0 || inside >= p.pool_size) return f2_all(0.f);
       return load_state(p.start, inside, p.C, Lane<kTma>(q.column, lane, p.C));
@@ -946,21 +987,30 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
     const f2 start = kMode == kByChains && q.i == 0 ? start_state() : f2_all(0.f);
     const int low = q.row + (kBack ? p.stride - S::kTileRows : 0) + mine;
     const char* stage = shared + turn % kStages * S::kStageBytes + mine * S::kPitch;
+    // thread 0: whether the next tile but one is copied from the table, with the words
+    const auto listed = [&] { return kMode == kByTiles && p.table && more && ahead < total; };
     auto ask = [&] {
-      if (waits) Needs<kWarps>(p, q, warp).ask(p, ex, q, warp, lane);
+      if (listed()) {
+        const Tile* from = p.table + ahead / p.columns;
+        Tile* to = &sm.tile[(turn + 2) & 3];
+        copy16(lap::smem_u32(to), from);
+        copy16(lap::smem_u32(to) + 16, reinterpret_cast<const char*>(from) + 16);
+      }
+      if (waits) Needs<kMode, kWarps>(p, q, warp).ask(p, ex, q, warp, lane);
     };
     unsigned begins = 0u;
     auto close = [&](const Run& run) {  // the warp's rows are composed
       ex.own[warp][lane] = run;
       if (kMode == kMixed && lane == 0) ex.begins[warp] = begins != 0u;
       if (threadIdx.x == 0) {
-        sm.tile[(turn + 2) & 3] = more ? tile_of(ahead) : Tile{-1, 0, 0, 0, 0, 0, 0, 0};
+        if (!listed()) sm.tile[(turn + 2) & 3] = more ? tile_of(ahead) : kNone;
         if (kMode == kMixed) ex.fresh = begins & 1u;
       }
       if (waits) {
         // the first group's; before the barrier, so read before any block may write a final state there
         if (warp == kWarps - 1 && q.i == q.j) ex.base[lane] = start_state();
-        Needs<kWarps>(p, q, warp).look(ex, q, warp, lane);
+        Needs<kMode, kWarps>(p, q, warp).look(ex, q, warp, lane);
+        if (listed()) sm.tile[(turn + 2) & 3].column = ahead % p.columns;
       }
     };
     const bool here = arrived<kTma>(&sm.bar[warp][turn % kStages], turn / kStages, &sm.abort);
@@ -1006,7 +1056,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
       ds = f2_add(ds, sum);
       __syncthreads();
       load(turn + kStages);
-      if (kMode != kByChains || (q.i + 1) * p.stride >= q.length) {  // the end of a tile or chain: its terms of dslopes, warps in order
+      if (kMode != kByChains || q.left <= p.stride) {  // the end of a tile or chain: its terms of dslopes, warps in order
         ex.own[warp][lane].h = ds;
         __syncthreads();
         if (warp == 0) {
@@ -1031,14 +1081,15 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
   }
 }
 
-// out[c] = sum over rows of part[rows][C] (0 rows: 0), unless the scan was skipped: 32 channels a
-// block, each warp every 32nd row, the warps' sums in order.
+// out[c] = sum over rows of part[rows][C] (0 rows: 0; `count`: a packed scan's tickets[2] rows), unless
+// the scan was skipped: 32 channels a block, each warp every 32nd row, the warps' sums in order.
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int rows, int C, const int* ticket,
-                                                          float* out) {
+                                                          bool count, float* out) {
   __shared__ float sums[32][33];
   lap::griddep_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane;
   if (ticket && *ticket >= 1 << 30) return;  // cu_seqlens was refused
+  if (count) rows = ticket[2];
   float s = 0.f;
   if (c < C) {
 #pragma unroll 4

@@ -117,6 +117,11 @@ FORMS = {
     "long packed": dict(lens=[1500, 2500, 1, 700], C=130, pool=9, pad=(2,)),
     "long fp32": dict(lens=[3333], C=9, packed=False, dtype="fp32"),
     "many short": dict(lens=list(np.random.default_rng(5).integers(0, 6, 700)), C=65, pool=800),
+    "long sequences": dict(lens=[2000, 0, 1, 1300, 129, 128, 127, 900], C=72, pool=12, pad=(4,)),
+    "long sequences odd": dict(lens=[112, 2000, 113, 0, 48, 1, 1300, 336], C=67, fused=True, offset=1, pool=9, pad=(7,)),
+    "long sequences fp32": dict(lens=[64, 900, 0, 65, 1, 1300], C=68, dtype="fp32", tail=9),
+    "many sequences": dict(lens=list(np.random.default_rng(6).integers(0, 260, 700)), C=64, pool=701, pad=(699,)),
+    "thousands": dict(lens=list(np.random.default_rng(7).integers(0, 3, 5000)), C=3, dtype="fp32"),
     "all padded": dict(lens=[5, 9], C=64, pool=4, pad=(0, 1)),
     "empty sequences": dict(lens=[0, 0, 0], C=64, pool=4),
 }
@@ -242,10 +247,10 @@ def test_gradients_of_closed_decay_gates_and_zero_slopes_are_finite():
     assert np.all(np.isfinite(ref["dr"][0]))
 
 
+@pytest.mark.parametrize("lens", [[100, 37, 250, 64, 300], [700, 537, 850, 264, 900]])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
-def test_sequences_are_isolated(value):
+def test_sequences_are_isolated(value, lens):
     """Non-finite inputs and states of one sequence, and of padded ones, leave the others bitwise."""
-    lens = [100, 37, 250, 64, 300]
     b = Batch(8, lens=lens, C=72, pool=7, pad=(3,))
     o, hf = b.fwd()
     dout = b.mat()
