@@ -966,12 +966,16 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
     Tile q = sm.tile[turn & 3];  // uniform, and known to be
     q.t = __shfl_sync(0xFFFFFFFFu, q.t, 0);
     q.column = __shfl_sync(0xFFFFFFFFu, q.column, 0);
-    q.n = __shfl_sync(0xFFFFFFFFu, q.n, 0);
     q.i = __shfl_sync(0xFFFFFFFFu, q.i, 0);
-    q.j = __shfl_sync(0xFFFFFFFFu, q.j, 0);
-    q.g = __shfl_sync(0xFFFFFFFFu, q.g, 0);
     q.row = __shfl_sync(0xFFFFFFFFu, q.row, 0);
-    q.left = __shfl_sync(0xFFFFFFFFu, q.left, 0);
+    if constexpr (kMode != kMixed) {
+      q.n = __shfl_sync(0xFFFFFFFFu, q.n, 0);
+      q.left = __shfl_sync(0xFFFFFFFFu, q.left, 0);
+    }
+    if constexpr (kMode != kByChains) {
+      q.j = __shfl_sync(0xFFFFFFFFu, q.j, 0);
+      q.g = __shfl_sync(0xFFFFFFFFu, q.g, 0);
+    }
     if (q.t < 0) break;
     auto& ex = sm.turn[turn & 1];
     const Tile& then = sm.tile[(turn + 1) & 3];
