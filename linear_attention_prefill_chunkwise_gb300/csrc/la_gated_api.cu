@@ -35,11 +35,14 @@ struct Plan {
 constexpr int kSlots = 152 * 2;
 
 // Tiles of a group.  A scan is a chain of one step per group (1.4 us each), while a tile composes
-// half a group of published runs: so about half the tiles of a column that are computed at once
-// (a group then takes about as long as a step), and at least one run per warp, which costs nothing.
-int group_of(int columns, int warps) {
-  const int wide = kSlots / (2 * columns);
-  return wide < warps ? warps : wide < 64 ? wide : 64;
+// half a group of published runs.  `streams`: the sequences' columns, so kSlots / streams tiles of one
+// are computed at once.  Many streams hide the steps, and a run per warp costs nothing; few want whole
+// rounds of blocks in one group.  BF16 forward of one sequence, groups of 8, 40, 56, 96, 128 tiles:
+// 512 channels 420, 372, 362, 354, 351 us; 1024: 371, 317, 313, 311, 314; 2048: 297, 278, 279, 288,
+// 297; 4096: 239, 250, 257, 270, 283.
+int group_of(int64_t streams, int warps) {
+  const int64_t wide = 4 * kSlots / streams;
+  return wide < 24 ? warps : wide < 160 ? static_cast<int>(wide) : 160;
 }
 
 // Whether blocks take whole chains (a sequence's channels).  Sequences of one length: for short
@@ -91,7 +94,7 @@ Plan plan_for(int B, int T, int N, int C, bool packed) {
   if (q.tiles == 0) q.tiles = 1;  // empty sequences alone
   q.parts = q.mode == lag::kByChains ? N : q.tiles;
   q.items = q.parts * q.columns;
-  q.group = group_of(q.columns, S::kWarps);
+  q.group = group_of(static_cast<int64_t>(q.mode == lag::kByTiles ? N : 1) * q.columns, S::kWarps);
   q.groups = ((q.per ? q.per : q.tiles) + q.group - 1) / q.group;
   if (q.ticket) {
     q.list = 256;
