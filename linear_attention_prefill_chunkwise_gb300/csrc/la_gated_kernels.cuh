@@ -51,13 +51,13 @@ constexpr int kStages = 2;
 // Rows per warp: as many as two blocks' registers (forward: a and b of each) and shared memory hold,
 // since every tile costs the same few hundred instructions; more of them spill, or leave the copies
 // no cache.  2 x 8192 tokens of 8192 channels, BF16: forward 16 rows 194 us, 14 202, 12 212;
-// gradients 10 rows 370, 9 367, 8 383, 6 422.  Unaligned, 32 sequences of up to 4096 tokens of 1001
-// channels: forward 16 rows 273, 15 211, 14 193, 12 197; gradients 8 rows 416, 6 372.  FP32, 8192
-// tokens of 4096 channels: gradients 5 rows 231, 4 212, 3 254.
+// gradients 10 rows 362, 9 371, 8 373, 6 422 (by tiles, 32768 tokens of 4096 channels: 527, 440, 466).
+// Unaligned, 32 sequences of up to 4096 tokens of 1001 channels: forward 15 rows 241, 14 187, 12 180;
+// gradients 8 rows 403, 7 363, 6 363.  FP32, 8192 tokens of 4096 channels: gradients 5 rows 231, 4 212, 3 254.
 template <typename E, bool kBack, bool kTma>
 struct Shape {
   static constexpr int kWarps = 8;
-  static constexpr int kRows = (kBack ? (kTma ? 9 : 6) : (kTma ? 16 : 14)) / (sizeof(E) / 2);
+  static constexpr int kRows = (kBack ? (kTma ? 9 : 6) : (kTma ? 16 : 12)) / (sizeof(E) / 2);
   static constexpr int kBlocks = 2;
   static constexpr int kAsk = kRows * 5 / 8;  // the row before which a warp asks for the published words
   static constexpr int kThreads = kWarps * 32;
@@ -322,28 +322,29 @@ struct Lane {
   }
 };
 
-// Output rows: the lane's two channels (a TMA kernel's rows hold an even number of channels).
+// Output rows from the lane's first channel on: its two channels (a TMA kernel's rows hold an even
+// number of channels).
 template <bool kTma>
-__device__ __forceinline__ void store2(float* row, const Lane<kTma>& l, f2 v) {
+__device__ __forceinline__ void store2(float* at, const Lane<kTma>& l, f2 v) {
   const float2 t = f2_unpack(v);
   if constexpr (kTma) {
-    if (l.ok[0]) __stcs(reinterpret_cast<float2*>(row + l.c[0]), t);
+    if (l.ok[0]) __stcs(reinterpret_cast<float2*>(at), t);
   } else {
-    if (l.ok[0]) __stcs(row + l.c[0], t.x);
-    if (l.ok[1]) __stcs(row + l.c[1], t.y);
+    if (l.ok[0]) __stcs(at, t.x);
+    if (l.ok[1]) __stcs(at + 32, t.y);
   }
 }
 template <bool kTma>
-__device__ __forceinline__ void store2(__nv_bfloat16* row, const Lane<kTma>& l, f2 v) {
+__device__ __forceinline__ void store2(__nv_bfloat16* at, const Lane<kTma>& l, f2 v) {
   const float2 t = f2_unpack(v);
   const __nv_bfloat162 b = __floats2bfloat162_rn(t.x, t.y);
   const unsigned w = *reinterpret_cast<const unsigned*>(&b);
-  unsigned short* s = reinterpret_cast<unsigned short*>(row);
+  unsigned short* s = reinterpret_cast<unsigned short*>(at);
   if constexpr (kTma) {
-    if (l.ok[0]) __stcs(reinterpret_cast<unsigned*>(s + l.c[0]), w);
+    if (l.ok[0]) __stcs(reinterpret_cast<unsigned*>(s), w);
   } else {
-    if (l.ok[0]) __stcs(s + l.c[0], static_cast<unsigned short>(w));
-    if (l.ok[1]) __stcs(s + l.c[1], static_cast<unsigned short>(w >> 16));
+    if (l.ok[0]) __stcs(s, static_cast<unsigned short>(w));
+    if (l.ok[1]) __stcs(s + 32, static_cast<unsigned short>(w >> 16));
   }
 }
 
@@ -386,28 +387,38 @@ __device__ __forceinline__ void fetch(const Params<E>& p, const Maps& maps, char
       lap::tma_load_2d(stage + i * S::kInputBytes + first * S::kPitch, &maps.of[i], bar, column * kCols,
                        low + first - (i == 4));
   } else {
-    constexpr int kChunks = S::kPitch / 16;
+    constexpr int kChunks = S::kPitch / 16, kAtOnce = 32 / kChunks;  // of a row; rows
+    const int k0 = lane / kChunks, c = lane - k0 * kChunks;
     const int64_t last = static_cast<int64_t>(p.rows) - 1;
     const int bytes = min(kCols, p.C - column * kCols) * static_cast<int>(sizeof(E));
+    const bool on = k0 < kAtOnce && 16 * c < bytes + 15;
 #pragma unroll
     for (int i = 0; i < S::kInputs; ++i) {
       const char* begin = reinterpret_cast<const char*>(p.in[i]);  // of the matrix
-      const char* end = begin + (last * p.ld_in[i] + p.C) * static_cast<int64_t>(sizeof(E));
+      const int64_t pitch = p.ld_in[i] * static_cast<int64_t>(sizeof(E)), top = static_cast<int64_t>(low) + first - (i == 4);
+      const char* src = begin + (top + k0) * pitch + column * kCols * static_cast<int>(sizeof(E));
+      char* dst = stage + i * S::kInputBytes + (first + k0) * S::kPitch + 16 * c;
+      if (top * pitch >= 16 && (last - top - (S::kRows - 1)) * pitch >= 32) {
+        // what the chunks hold beside the channels lies inside the matrix
 #pragma unroll
-      for (int j = 0; j < (S::kRows * kChunks + 31) / 32; ++j) {
-        const int id = lane + 32 * j, k = id / kChunks, c = id - k * kChunks;
-        const int64_t row = static_cast<int64_t>(low) + first + k - (i == 4);
-        if (k >= S::kRows || row < 0 || row > last) continue;
-        const char* src = begin + (row * p.ld_in[i] + column * kCols) * static_cast<int64_t>(sizeof(E));
-        const char* chunk = src - (reinterpret_cast<uintptr_t>(src) & 15u) + 16 * c;
-        if (chunk >= src + bytes) continue;
-        char* dst = stage + i * S::kInputBytes + (first + k) * S::kPitch + 16 * c;
-        if (chunk >= begin && chunk + 16 <= end) {
-          copy16(lap::smem_u32(dst), chunk);  // its neighbours lie inside the matrix
-        } else {
-          for (int e = 0; e < 16; e += sizeof(E))
-            if (chunk + e >= src && chunk + e < src + bytes)
-              *reinterpret_cast<E*>(dst + e) = *reinterpret_cast<const E*>(chunk + e);
+        for (int k = 0; k < S::kRows; k += kAtOnce) {
+          if (on && k + k0 < S::kRows)
+            copy16(lap::smem_u32(dst) + k * S::kPitch, src - (reinterpret_cast<uintptr_t>(src) & 15u) + 16 * c);
+          src += kAtOnce * pitch;
+        }
+      } else {
+        const char* end = begin + last * pitch + static_cast<int64_t>(p.C) * sizeof(E);
+#pragma unroll 1
+        for (int k = 0; k < S::kRows; k += kAtOnce, src += kAtOnce * pitch) {
+          if (!on || k + k0 >= S::kRows || top + k + k0 < 0 || top + k + k0 > last) continue;
+          const char* chunk = src - (reinterpret_cast<uintptr_t>(src) & 15u) + 16 * c;
+          if (chunk >= begin && chunk + 16 <= end) {
+            copy16(lap::smem_u32(dst) + k * S::kPitch, chunk);
+          } else {
+            for (int e = 0; e < 16; e += sizeof(E))
+              if (chunk + e >= src && chunk + e < src + bytes)
+                *reinterpret_cast<E*>(dst + k * S::kPitch + e) = *reinterpret_cast<const E*>(chunk + e);
+          }
         }
       }
     }
@@ -754,14 +765,15 @@ struct Forward {
 
   template <bool kEdges>
   __device__ __forceinline__ void second(const Params<E>& p, int low, f2 h, const Rows& rows, const Lane<kTma>& l) {
-    E* o = p.out[0] + static_cast<int64_t>(low) * p.ld_out[0];
+    E* o = p.out[0] + static_cast<int64_t>(low) * p.ld_out[0] + l.c[0];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if constexpr (kEdges) {
         if (rows.begin >> k & 1u) h = f2_all(0.f);
       }
       h = f2_fma(a[k], h, b[k]);
-      if (!kEdges || (rows.live >> k & 1u)) store2(o + k * p.ld_out[0], l, h);
+      if (!kEdges || (rows.live >> k & 1u)) store2(o, l, h);
+      o += p.ld_out[0];
       if constexpr (kEdges) {
         if (p.finish && (rows.end >> k & 1u)) store_state(p.finish, __shfl_sync(0xFFFFFFFFu, rows.slot, k), p.C, l, h);
       }
@@ -806,13 +818,15 @@ struct Backward {
         h(p, stage, 4, low, lane);
     E* out[3];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) out[i] = p.out[i] + static_cast<int64_t>(low) * p.ld_out[i];
+    for (int i = 0; i < 3; ++i) out[i] = p.out[i] + static_cast<int64_t>(low + K) * p.ld_out[i] + l.c[0];
     f2 sum = f2_all(0.f);
     const f2 one = f2_all(1.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int at = K - 1 - k;
       f2 before = h.get(at);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) out[i] -= p.ld_out[i];
       if constexpr (kEdges) {
         if (!(rows.live >> k & 1u)) continue;
         const int slot = __shfl_sync(0xFFFFFFFFu, rows.slot, k);
@@ -827,12 +841,12 @@ struct Backward {
       inv = f2_pack(vu.x > 0.f ? vi.x : 0.f, vu.y > 0.f ? vi.y : 0.f);
       const f2 lambda = f2_sub(one, m[k]);
       const f2 gs = f2_mul(G, sg), dx = f2_mul(gs, beta);
-      store2(out[0] + at * p.ld_out[0], l, dx);
-      store2(out[2] + at * p.ld_out[2], l, f2_mul(f2_mul(dx, vx), f2_sub(one, sg)));
+      store2(out[0], l, dx);
+      store2(out[2], l, f2_mul(f2_mul(dx, vx), f2_sub(one, sg)));
       // du = lambda (gs x lambda / beta - G h_{t-1})
       const f2 t = f2_mul(f2_mul(gs, vx), f2_mul(lambda, inv));
       const f2 du = f2_mul(lambda, f2_sub(t, f2_mul(G, before)));
-      store2(out[1] + at * p.ld_out[1], l, f2_mul(f2_mul(du, u), f2_sub(one, sr[k])));
+      store2(out[1], l, f2_mul(f2_mul(du, u), f2_sub(one, sr[k])));
       sum = f2_fma(du, sr[k], sum);
       w = f2_mul(lambda, G);
       if constexpr (kEdges) {
