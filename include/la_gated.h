@@ -28,6 +28,9 @@
  * Rows past cu_seqlens[N] (and before cu_seqlens[0]) belong to no sequence and are left as they
  * are.  Pointers need the alignment of their element type only (16-byte rows run faster).
  *
+ * Sequences may share a slot that is only read; where states are written (h_final, dh0, decode,
+ * commit) a slot that two sequences name is left with an unspecified state.
+ *
  * Device-side checks: an index >= pool_size sets LA_DEV_ERR_BAD_INDEX and skips that sequence;
  * cu_seqlens that is not non-decreasing inside [0, T] sets LA_DEV_ERR_BAD_SEQLENS and skips the
  * whole call.  LA_DEV_ERR_TIMEOUT reports that a wait between the blocks of a scan passed its

@@ -3,31 +3,39 @@
 // The scan.  With a_t = lambda_t and b_t the token's input (beta_t sig(g_t) x_t forward; lambda_t
 // dout_t backward, where the state is w_t = lambda_t G_t and tokens are walked from the end), a
 // run of tokens maps the state before it to A h + H, A the product of its a's and H its own scan
-// from zero; two runs compose as (A2 A1, A2 H1 + H2).  So the rows of the whole batch, sequence
-// after sequence, are one scan whose state is replaced where a sequence begins: the rows are cut
-// into tiles whatever the sequences' lengths, which balances packed batches by construction.
+// from zero; two runs compose as (A2 A1, A2 H1 + H2).
 //
 // A tile is kWarps x kRows rows of 64 channels, two channels per lane, kRows rows per warp.  Blocks
 // are persistent, and each warp has two stages of shared memory for its rows of the inputs: while
 // one tile is computed the loads of the next are in flight, each warp's own TMA boxes (or, where
-// rows are not 16-byte aligned, its own asynchronous 4-byte copies), so no warp waits for another's
-// loads.  A warp composes its rows, the block its warps, and the tile's (A, H) is published in the
-// workspace.  Once the state before the tile is known, each warp walks its rows again (forward:
-// from a and b in registers) and writes the outputs: every input is read once and every output
-// written once.
-// The state before a tile: tiles are taken in order (by a ticket, so that whatever a block waits
-// for is already running), in groups of `group` along the rows.  A tile composes the published
-// (A, H) of the tiles before it in its group, in order, onto the state that the previous group's
-// last tile published; a long scan is thus a chain of one step per group, not per tile.  The
-// order of every sum is fixed, so results repeat bitwise.
+// rows are not 16-byte aligned, its own asynchronous 16-byte copies), so no warp waits for another's
+// loads.  A warp composes its rows, the block its warps; once the state before the tile is known,
+// each warp walks its rows again (forward: from a and b in registers) and writes the outputs: every
+// input is read once and every output written once.  What bounds it is the bytes, then the
+// instructions: a row of 64 channels takes a warp 59 forward and 128 for the gradients (unaligned:
+// 204), at 0.61 - 0.67 of the issue slots.  Measured, BF16, of the bytes at the copy rate: 2 x 8192
+// tokens of 8192 channels 188 us (0.84), gradients 371 (0.85); 32 packed sequences of up to 4096
+// tokens of 4096 channels 293 (0.97); one sequence of 32768 x 4096 232 (0.68), of 131072 x 1024 314
+// (0.50: the states' way from block to block); FP32 8192 x 8192 173 (0.92).
+//
+// Where the state before a tile comes from (Mode):
+// By chains, from the block itself, which walks all tiles of a sequence's channels: nothing waits.
+// By tiles, from the blocks that computed the tiles before it.  Tiles are taken in order (by a
+// ticket, so that whatever a block waits for is already running), in groups along the sequence.  A
+// tile's (A, H) is published in the workspace; a tile composes the published ones before it in its
+// group, in order, onto the state that the previous group's last tile published: a long scan is a
+// chain of one step per group, not per tile.
+// Batches of short packed sequences are one scan over all rows whose state is replaced where a
+// sequence begins (kMixed), cut whatever the sequences' lengths.
+// The order of every sum is fixed, so results repeat bitwise.
+//
 // A published word carries its own readiness: the workspace is filled with all-ones before the
 // scan, no published word is all-ones, and a reader looks at the words themselves: no fence and no
-// second flag on the way from block to block.  A tile asks for the words it needs before it
-// computes its own rows, by asynchronous copies; they have nearly always been published by then,
-// so a block waits at one barrier per tile, and only where one was late it polls.
-// Where a sequence begins, A becomes -0: products of decays are >= +0, so the sign marks "what
-// came before does not matter", and composition then selects H instead of multiplying, which keeps
-// infinities and NaN of one sequence out of the next.
+// second flag on the way from block to block.  A tile asks for the words it needs (one per warp)
+// before it computes its last rows, by asynchronous copies, and polls only where one was late.
+// Where a sequence begins inside a tile, A becomes -0: products of decays are >= +0, so the sign
+// marks "what came before does not matter", and composition then selects H instead of multiplying,
+// which keeps infinities and NaN of one sequence out of the next.
 #pragma once
 
 #include <cuda.h>
