@@ -122,6 +122,10 @@ FORMS = {
     "long sequences fp32": dict(lens=[64, 900, 0, 65, 1, 1300], C=68, dtype="fp32", tail=9),
     "many sequences": dict(lens=list(np.random.default_rng(6).integers(0, 260, 700)), C=64, pool=701, pad=(699,)),
     "thousands": dict(lens=list(np.random.default_rng(7).integers(0, 3, 5000)), C=3, dtype="fp32"),
+    "groups": dict(lens=[1100] * 20, C=200, packed=False, pool=23, pad=(11,)),
+    "groups packed": dict(lens=list(np.random.default_rng(9).integers(700, 1500, 20)), C=200, pool=23, pad=(3,)),
+    "groups fp32": dict(lens=[9000], C=9, packed=False, dtype="fp32"),
+    "groups of mixed rows": dict(lens=list(np.random.default_rng(8).integers(0, 5, 5000)), C=3, dtype="fp32"),
     "all padded": dict(lens=[5, 9], C=64, pool=4, pad=(0, 1)),
     "empty sequences": dict(lens=[0, 0, 0], C=64, pool=4),
 }
@@ -271,6 +275,20 @@ def test_sequences_are_isolated(value, lens):
         assert torch.equal(hf2[int(b.slots[n])], hf[int(b.slots[n])])
         for t, u in zip(got[:3], ref[:3]):
             assert torch.equal(t[s], u[s]), f"a gradient of sequence {n} changed"
+
+
+def test_sequences_may_share_a_slot_that_is_read():
+    """A common prompt's state: both sequences begin with it, and no state is written."""
+    b = Batch(13, lens=[300, 41], C=64, pool=3)
+    b.slots[:] = 2
+    b.idx.fill_(2)
+    o = b.blank()
+    lap.la_gated_scan_fwd(b.x, b.r, b.g, b.slopes, h0=b.h0, o=o, **b.kw)
+    torch.cuda.synchronize()
+    for n, L in enumerate(b.lens):
+        s = b.rows(n)
+        ro, _, eo, _ = scan_one(f64(b.x[s]), f64(b.r[s]), f64(b.g[s]), f64(b.slopes), b.start(n))
+        near(o[s], ro, eo, b.dtype, f"o of sequence {n} ({L} tokens)")
 
 
 def test_bad_bounds_and_indices_are_reported():
