@@ -3,6 +3,7 @@
 // memory or synchronises with the host.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/la_gated.h"
@@ -21,14 +22,14 @@ la_host::DeviceState g_dev[la_host::kMaxDevices];
 // the sequences' order (packed), the published runs and states; for the gradients one row of
 // partial sums of dslopes per chain or tile.
 struct Plan {
-  int tiles = 0, columns = 0, stride = 0, group = 0, groups = 0, per = 0, parts = 0;
+  int tiles = 0, columns = 0, stride = 0, group = 0, groups = 0, spans = 0, per = 0, parts = 0, longest = -1;
   int items = 0;       // tiles or chains, times columns
   bool ticket = false; // a plan kernel runs first
   bool waits = false;  // states pass from block to block
-  bool order = false;  // packed, by chains
-  bool table = false;  // packed, by tiles of one sequence each
+  bool order = false;  // packed, by chains: the sequences of at most `longest` tokens
+  bool table = false;  // packed, by tiles of one sequence each: the others
   lag::Mode mode = lag::kMixed;
-  size_t list = 0, runs = 0, words = 0, before = 0, part = 0, bytes = 0;
+  size_t order_at = 0, list = 0, runs = 0, words = 0, before = 0, part = 0, bytes = 0;
 };
 
 // Blocks the largest part holds at once; a device with fewer SMs runs the same plan.
@@ -56,18 +57,26 @@ bool by_chains(int64_t chains, int per) {
 }
 // Packed: by chains where there are enough of them to fill the device evenly and the sequences are
 // not mostly shorter than half a tile.  By chains, in tiles of one sequence each, and in tiles of
-// mixed rows, us: 32 sequences of up to 4096 tokens, 4096 channels, 2048 chains: 327, 413, 532; 40 of
-// up to 8192, 1024 channels, 640 chains: 218, 245, 467 (gradients 453, 463, 923); 16 of them, 2048
-// channels, 512 chains: 219, 203, 320 (442, 387, 600); 16, 1024 channels: 193, 127, 214 (359, 234,
-// 416).  2048 channels, 38400 tokens: 200 sequences 197, 326, 421; 600 249, 428, 246; 1200 499, 837, 250.
+// mixed rows, forward, us: 32 sequences of up to 4096 tokens, 4096 channels, 2048 chains: 327, 404,
+// 532; 640 chains: 218, 239, 467 (40 sequences of up to 8192 tokens, 1024 channels), uneven ones 405,
+// 238 (20 of 50 to 16384 tokens, 2048 channels); 16 of up to 8192 tokens, 1024 channels, 256 chains:
+// 193, 120, 214.  2048 channels, 38400 tokens: 200 sequences 197, 326, 421; 600 249, 428, 246; 1200
+// 499, 837, 250.
 bool packed_by_chains(int64_t tokens, int N, int columns, int stride) {
-  return static_cast<int64_t>(N) * columns >= 2 * kSlots && tokens * 2 >= static_cast<int64_t>(N) * stride;
+  return static_cast<int64_t>(N) * columns >= 3 * kSlots && tokens * 2 >= static_cast<int64_t>(N) * stride;
+}
+// A batch by chains takes sequences much longer than a block's share of the rows by tiles, in a launch
+// of its own behind.  One sequence of 32768 tokens among 100 of 330 on average, 4096 channels: 448 us,
+// all by chains 777 (gradients 816, 1469); one of 100000, 512 channels: 195 and 2212.  Without such
+// sequences the launch costs 3 us.
+int longest_chain(int64_t tokens, int columns, int stride) {
+  const int64_t share = tokens * columns / kSlots;
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(share + share / 4, 4 * stride), INT32_MAX - 1));
 }
 // Else in tiles of one sequence each, where those are not mostly single tiles (2048 channels, 300
 // sequences of up to 256 tokens, two tiles of 128 rows or four of 72: forward 296 and 269 in mixed
 // ones, gradients 412 and 546).
 bool packed_by_tiles(int64_t tokens, int N, int stride) { return tokens * 2 >= static_cast<int64_t>(N) * stride * 3; }
-constexpr int kMostListed = 4096;  // sequences of a batch whose order the plan kernel finds by comparing all
 
 template <typename E, bool kBack, bool kTma>
 Plan plan_for(int B, int T, int N, int C, bool packed) {
@@ -82,32 +91,36 @@ Plan plan_for(int B, int T, int N, int C, bool packed) {
   } else if (!packed && T > 0) {
     q.per = (T + q.stride - 1) / q.stride;
     q.waits = !by_chains(static_cast<int64_t>(B) * q.columns, q.per);
-  } else if (packed && N <= kMostListed) {
+  } else if (packed && N <= lag::kMostListed) {
     q.order = packed_by_chains(rows, N, q.columns, q.stride);
-    q.table = !q.order && packed_by_tiles(rows, N, q.stride);
+    if (q.order) q.longest = longest_chain(rows, q.columns, q.stride);
   }
-  q.waits = q.waits || (packed && !q.order);
+  // sequences of the table, at most
+  const int64_t listed = !packed || N > lag::kMostListed ? 0 : q.order ? std::min<int64_t>(N, rows / (q.longest + 1)) : N;
+  q.table = q.order ? listed > 0 : listed > 0 && packed_by_tiles(rows, N, q.stride);
+  q.waits = q.waits || q.table || (packed && !q.order);
   q.ticket = q.waits || q.order;
   if (q.order || (q.per && !q.waits)) q.mode = lag::kByChains;
   else if (q.per || q.table) q.mode = lag::kByTiles;
-  q.tiles = q.per ? B * q.per : q.table ? static_cast<int>(rows / q.stride) + N : static_cast<int>((rows + q.stride - 1) / q.stride);
+  q.tiles = q.per ? B * q.per : static_cast<int>(q.table ? rows / q.stride + listed : (rows + q.stride - 1) / q.stride);
   if (q.tiles == 0) q.tiles = 1;  // empty sequences alone
-  q.parts = q.mode == lag::kByChains ? N : q.tiles;
-  q.items = q.parts * q.columns;
-  q.group = group_of(static_cast<int64_t>(q.mode == lag::kByTiles ? N : 1) * q.columns, S::kWarps);
+  q.parts = (q.mode == lag::kByChains ? N : 0) + (q.mode != lag::kByChains || q.table ? q.tiles : 0);
+  q.items = (q.mode == lag::kByChains ? N : q.tiles) * q.columns;
+  const int64_t side_by_side = q.order ? 1 : q.mode == lag::kByTiles ? N : 1;
+  q.group = group_of(side_by_side * q.columns, S::kWarps);
   q.groups = ((q.per ? q.per : q.tiles) + q.group - 1) / q.group;
+  q.spans = q.per ? B * q.groups : q.groups + (q.table ? static_cast<int>(listed) : 0);
   if (q.ticket) {
-    q.list = 256;
-    const size_t list = q.order ? static_cast<size_t>(N) * sizeof(int32_t) : q.table ? q.tiles * sizeof(lag::Tile)
-                        : packed ? (static_cast<size_t>(q.tiles) + 1) * sizeof(int2) : 0;
+    q.order_at = 256;
+    q.list = q.order_at + (q.order ? la_host::align256(static_cast<size_t>(N) * sizeof(int32_t)) : 0);
+    const size_t list = q.table ? q.tiles * sizeof(lag::Tile) : packed ? (static_cast<size_t>(q.tiles) + 1) * sizeof(int2) : 0;
     q.bytes = q.list + la_host::align256(list);
   }
   if (q.waits) {
     const size_t width = static_cast<size_t>(q.columns) * lag::kCols;
-    const size_t groups = q.per ? static_cast<size_t>(B) * q.groups : static_cast<size_t>(q.groups) + (q.table ? N : 0);
     q.runs = q.bytes;
     q.before = q.runs + q.tiles * width * 8;
-    q.words = q.tiles * width * 2 + groups * width;
+    q.words = q.tiles * width * 2 + q.spans * width;
     q.bytes = q.runs + la_host::align256(q.words * 4);
   }
   q.part = q.bytes;
@@ -140,7 +153,7 @@ la_status check_sizes(int B, int T, int N, int C, bool packed, la_dtype dtype) {
   if (static_cast<int64_t>(B) * T > la_host::kMaxRows)
     return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)B * T);
   // tiles of at least 16 rows and 64 channels, numbered below 2^30 (more than any memory holds)
-  if ((static_cast<int64_t>(B) * T / 16 + kMostListed) * ((C + 63) / 64) >= int64_t(1) << 30)
+  if ((static_cast<int64_t>(B) * T / 16 + lag::kMostListed) * ((C + 63) / 64) >= int64_t(1) << 30)
     return fail(LA_ERR_UNSUPPORTED, "B*T*C too large");
   if (static_cast<int64_t>(N) * ((C + 63) / 64) > INT32_MAX) return fail(LA_ERR_UNSUPPORTED, "N*C too large");
   return LA_OK;
@@ -172,7 +185,9 @@ void set_plan(lag::Params<E>* p, const Plan& q, bool backward, void* workspace) 
   p->groups = q.groups;
   p->per = q.per;
   if (q.ticket) p->ticket = reinterpret_cast<int*>(ws);
-  if (q.order) p->order = reinterpret_cast<int32_t*>(ws + q.list);
+  p->spans = q.spans;
+  p->longest = q.longest;
+  if (q.order) p->order = reinterpret_cast<int32_t*>(ws + q.order_at);
   if (q.waits) {
     if (q.table) p->table = reinterpret_cast<lag::Tile*>(ws + q.list);
     else if (p->cu_seqlens) p->places = reinterpret_cast<int2*>(ws + q.list);
@@ -211,10 +226,10 @@ la_status encode_rows_map(CUtensorMap* map, const E* base, int64_t rows, int64_t
 template <typename E>
 cudaError_t launch_plan(const lag::Params<E>& p, const Plan& q, int sms, cudaStream_t s) {
   size_t want = q.words / 4;
-  if (q.order) want = static_cast<size_t>(p.N);
+  if (q.order || q.table) want = std::max(want, static_cast<size_t>(std::max(p.N, q.table ? q.tiles : 0)) * 32);
   want = (want + lag::kThreads - 1) / lag::kThreads;
   const unsigned grid = static_cast<unsigned>(want < 1 ? 1 : want < size_t(sms) * 8 ? want : size_t(sms) * 8);
-  return la_host::launch_pdl(lag::scan_plan_kernel<E>, grid, lag::kThreads, 0, s, p, q.words);
+  return la_host::launch_pdl(lag::scan_plan_kernel<E>, grid, lag::kThreads, 0, s, p);
 }
 
 template <lag::Mode kMode>
@@ -237,15 +252,20 @@ la_status launch_scan_as(lag::Params<E> p, int B, void* workspace, float* dslope
   }
   cudaError_t ce = q.ticket ? launch_plan(p, q, sms, s) : cudaSuccess;
   if (ce == cudaSuccess && q.tiles > 0) {
-    const int most = sms * S::kBlocks, grid = q.items < most ? q.items : most;
-    auto run = [&](auto mode) {
+    const int most = sms * S::kBlocks;
+    auto run = [&](auto mode, const lag::Params<E>& with, int64_t items) {
       constexpr lag::Mode kMode = decltype(mode)::value;
-      return la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma, kMode>, grid, S::kThreads,
-                                 lag::scan_smem_bytes<E, kBack, kTma, kMode>(), s, p, maps);
+      return la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma, kMode>,
+                                 static_cast<unsigned>(items < most ? items : most), S::kThreads,
+                                 lag::scan_smem_bytes<E, kBack, kTma, kMode>(), s, with, maps);
     };
-    ce = q.mode == lag::kByChains  ? run(ModeTag<lag::kByChains>{})
-         : q.mode == lag::kByTiles ? run(ModeTag<lag::kByTiles>{})
-                                   : run(ModeTag<lag::kMixed>{});
+    if (q.mode != lag::kByTiles)
+      ce = q.mode == lag::kByChains ? run(ModeTag<lag::kByChains>{}, p, q.items) : run(ModeTag<lag::kMixed>{}, p, q.items);
+    if (ce == cudaSuccess && (q.table || q.mode == lag::kByTiles)) {
+      lag::Params<E> with = p;
+      if (q.table) with.ticket += lag::kTicket;
+      ce = run(ModeTag<lag::kByTiles>{}, with, static_cast<int64_t>(q.tiles) * q.columns);
+    }
   }
   if (ce == cudaSuccess && kBack)
     ce = la_host::launch_pdl(lag::column_sum_kernel, (p.C + 31) / 32, 1024, 0, s, static_cast<const float*>(p.part),

@@ -110,19 +110,24 @@ struct Params {
   const int32_t* accepted_len;  // commit
   int* dev_error;
   // the workspace of a scan
-  int* ticket;         // next tile or chain, an abort flag, how many (packed); null: blocks take theirs in turn
+  int* ticket;         // kTicket words: next tile or chain, an abort flag, how many (packed); null: blocks
+                       // take theirs in turn.  Packed batches have the tiles' words behind the chains'
   int2* places;        // [tiles + 1] (packed, kMixed) where each tile lies among the sequences
-  int32_t* order;      // [N] (packed, by chains) the running sequences, longest first
-  Tile* table;         // [tiles] (packed, by tiles) the tiles in the order in which they are taken
+  int32_t* order;      // [N] (packed, by chains) the running sequences of at most `longest` tokens, longest first
+  Tile* table;         // [tiles] (packed, by tiles) the others' tiles in the order in which they are taken
   float4* runs;        // [tiles][columns][32] published (A, H) of each lane's two channels; null: nothing waits
   float2* before;      // [groups of all sequences][columns][32] published states after each group
   int T, N, C, pool_size, rows;
   int tiles, columns, stride;  // tiles along the rows, of `stride` rows; along the channels
-  int group, groups;           // tiles per group; groups of a sequence of one length
+  int group, groups, spans;    // tiles per group; groups of a sequence of one length, of all sequences
+  int longest;
   // Sequences of one length: tiles per sequence (the last may be short); 0: packed, or tiles that
   // hold several whole sequences.
   int per;
 };
+
+constexpr int kTicket = 4;
+constexpr int kMostListed = 4096;  // sequences of a batch that the plan kernel orders by comparing all
 
 struct Maps {
   CUtensorMap of[kMaxInputs];
@@ -140,14 +145,48 @@ __device__ __forceinline__ void report(int* dev_error, unsigned bit) {
 // after its first row; y, whether all its rows lie inside one running sequence, away from its ends.
 // By chains, it orders the running sequences, longest first (ties by number); by tiles, it lists the
 // running sequences' tiles: the first of each, longest sequence first, then the second of each, ...
+// A warp compares a sequence or a tile with all sequences (a thread for each: 118 us for 4000 sequences;
+// that call 551 us instead of 705, 32 sequences of 1001 channels 169 instead of 182).
 template <typename E>
-__global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p, size_t words) {
+__global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p) {
+  __shared__ unsigned long long sums[2];  // tiles and groups of the table
   lap::griddep_wait();
   lap::griddep_launch_dependents();
   const size_t id = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x;
   const size_t all = static_cast<size_t>(gridDim.x) * kThreads;
-  uint4* w = reinterpret_cast<uint4*>(p.runs);  // runs and before lie together, 16-byte multiples
-  for (size_t i = id; i < words / 4; i += all) w[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  auto length = [&](int n) {  // -1: does not run
+    const int slot = p.state_indices ? p.state_indices[n] : n;
+    return slot < 0 || slot >= p.pool_size ? -1 : min(max(p.cu_seqlens[n + 1] - p.cu_seqlens[n], 0), p.T);
+  };
+  auto tiles_of = [&](int n) {  // in the table
+    const int l = length(n);
+    return l <= p.longest ? 0 : l <= p.stride ? 1 : (l + p.stride - 1) / p.stride;
+  };
+  int tiles = p.tiles, spans = p.spans;
+  if (p.table) {
+    if (threadIdx.x < 2) sums[threadIdx.x] = 0ull;
+    __syncthreads();
+    unsigned long long mine = 0ull, groups = 0ull;
+    for (int n = threadIdx.x; n < p.N; n += kThreads) {
+      const int t = tiles_of(n);
+      mine += t;
+      groups += (t + p.group - 1) / p.group;
+    }
+    if (mine) {
+      atomicAdd(&sums[0], mine);
+      atomicAdd(&sums[1], groups);
+    }
+    __syncthreads();
+    tiles = static_cast<int>(min(sums[0], static_cast<unsigned long long>(tiles)));  // as they are unless
+    spans = static_cast<int>(min(sums[1], static_cast<unsigned long long>(spans)));  // cu_seqlens is refused
+  }
+  auto fill = [&](void* at, size_t chunks) {
+    for (size_t i = id; i < chunks; i += all) reinterpret_cast<uint4*>(at)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  };
+  if (p.runs) {
+    fill(p.runs, static_cast<size_t>(tiles) * p.columns * 32);
+    fill(p.before, static_cast<size_t>(spans) * p.columns * 16);
+  }
   if (p.places) {
     for (size_t i = id; i <= static_cast<size_t>(p.tiles); i += all) {
       const int64_t row = static_cast<int64_t>(i) * p.stride;
@@ -164,60 +203,59 @@ __global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p, 
       p.places[i] = make_int2(i == static_cast<size_t>(p.tiles) ? p.N : a, inner);  // the last tile owns the rest
     }
   }
+  if (p.cu_seqlens && p.state_indices && !p.places)
+    for (size_t i = id; i < static_cast<size_t>(p.N); i += all)
+      if (p.state_indices[i] >= p.pool_size) report(p.dev_error, kErrBadIndex);
+  // a warp for each sequence and for each tile
+  const int lane = threadIdx.x % 32, warp = static_cast<int>(id / 32), warps = static_cast<int>(all / 32);
+  constexpr unsigned kAll = 0xFFFFFFFFu;
   if (p.order) {
-    auto length = [&](int n) {  // -1: does not run
-      const int slot = p.state_indices ? p.state_indices[n] : n;
-      return slot < 0 || slot >= p.pool_size ? -1 : p.cu_seqlens[n + 1] - p.cu_seqlens[n];
+    auto chain = [&](int n) {  // -1: none
+      const int l = length(n);
+      return l > p.longest ? -1 : l;
     };
-    for (size_t i = id; i < static_cast<size_t>(p.N); i += all) {
-      const int n = static_cast<int>(i), mine = length(n);
-      int rank = 0, running = 0;
-#pragma unroll 8
-      for (int m = 0; m < p.N; ++m) {
-        const int other = length(m);
-        running += other >= 0;
+    for (int n = warp; n < p.N; n += warps) {
+      const int mine = chain(n);
+      int rank = 0, chains = 0;
+#pragma unroll 4
+      for (int m = lane; m < p.N; m += 32) {
+        const int other = chain(m);
+        chains += other >= 0;
         rank += other > mine || (other == mine && m < n);
       }
-      if (mine >= 0) p.order[rank] = n;
-      else if (p.state_indices && p.state_indices[n] >= p.pool_size) report(p.dev_error, kErrBadIndex);
-      if (n == 0) p.ticket[2] = running;
+      rank = __reduce_add_sync(kAll, rank);
+      chains = __reduce_add_sync(kAll, chains);
+      if (lane == 0 && mine >= 0) p.order[rank] = n;
+      if (lane == 0 && n == 0) p.ticket[2] = chains;
     }
   }
   if (p.table) {
-    auto tiles_of = [&](int n) {  // 0: does not run
-      const int slot = p.state_indices ? p.state_indices[n] : n;
-      const int length = min(max(p.cu_seqlens[n + 1] - p.cu_seqlens[n], 0), p.T);
-      return slot < 0 || slot >= p.pool_size ? 0 : length <= p.stride ? 1 : (length + p.stride - 1) / p.stride;
-    };
-    for (size_t i = id; i < static_cast<size_t>(p.N); i += all)
-      if (p.state_indices && p.state_indices[i] >= p.pool_size) report(p.dev_error, kErrBadIndex);
-    for (size_t k = id; k < static_cast<size_t>(p.tiles); k += all) {
-      const int t = static_cast<int>(k);
-      int n = -1, sum = 0, first = 0, g = 0;  // t's sequence; tiles so far; n's first tile and group
-#pragma unroll 4
-      for (int m = 0; m < p.N; ++m) {
-        const int tiles = tiles_of(m);
-        if (n < 0) {
-          if (t - sum < tiles) {
-            n = m;
-            first = sum;
-          } else {
-            g += (tiles + p.group - 1) / p.group;
-          }
+    for (int t = warp; t < tiles; t += warps) {
+      int n = -1, i = t, g = 0;  // t's sequence, its place there, the sequence's first group
+      for (int m0 = 0; m0 < p.N && n < 0; m0 += 32) {
+        const int here = m0 + lane < p.N ? tiles_of(m0 + lane) : 0;
+        int upto = here;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int v = __shfl_up_sync(kAll, upto, d);
+          if (lane >= d) upto += v;
         }
-        sum = min(sum + tiles, p.tiles);  // (as it is unless cu_seqlens is refused)
+        const unsigned found = __ballot_sync(kAll, i < upto);
+        const int src = found ? __ffs(found) - 1 : 32;
+        g += __reduce_add_sync(kAll, lane < src ? (here + p.group - 1) / p.group : 0);
+        i -= __shfl_sync(kAll, found ? upto - here : upto, found ? src : 31);
+        if (found) n = m0 + src;
       }
-      if (t == 0) p.ticket[2] = sum;
       if (n < 0) continue;
-      const int i = t - first, mine = tiles_of(n);
+      const int mine = tiles_of(n);
       int at = 0;
-#pragma unroll 4
-      for (int m = 0; m < p.N; ++m) {
-        const int tiles = tiles_of(m);
-        at = min(at + min(tiles, i) + (tiles > i && (tiles > mine || (tiles == mine && m < n))), p.tiles);
+      for (int m = lane; m < p.N; m += 32) {
+        const int other = tiles_of(m);
+        at += min(other, i) + (other > i && (other > mine || (other == mine && m < n)));
       }
+      at = __reduce_add_sync(kAll, at);
       const int lo = p.cu_seqlens[n], hi = p.cu_seqlens[n + 1];
-      if (at < p.tiles)
+      if (lane == 0 && static_cast<unsigned>(at) < static_cast<unsigned>(tiles))  // always, unless cu_seqlens is refused
         p.table[at] = {t, 0, n, i, i % p.group, g + i / p.group,
                        p.part ? hi - (i + 1) * p.stride : lo + i * p.stride, hi - lo - i * p.stride};
     }
@@ -229,8 +267,10 @@ __global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p, 
         wrong |= p.cu_seqlens[n] < 0 || p.cu_seqlens[n] > p.cu_seqlens[n + 1] || p.cu_seqlens[n + 1] > p.T;
     wrong = __syncthreads_or(wrong);
     if (threadIdx.x == 0) {
-      p.ticket[0] = wrong ? 1 << 30 : 0;
-      p.ticket[1] = 0;
+      p.ticket[0] = p.ticket[kTicket] = wrong ? 1 << 30 : 0;
+      p.ticket[1] = p.ticket[kTicket + 1] = 0;
+      if (!p.order) p.ticket[2] = 0;
+      p.ticket[kTicket + 2] = p.table ? tiles : 0;
       if (wrong) report(p.dev_error, kErrBadSeqlens);
     }
   }
@@ -901,6 +941,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
 
   // Thread 0's: the number of the next tile or chain (asked for early, looked at late), and the tile.
   const int total = (p.order || p.table ? p.ticket[2] : p.tiles) * p.columns;
+  const int part0 = kBack && kMode == kByChains && p.table ? p.ticket[kTicket + 2] : 0;  // sums of dslopes before the chains'
   constexpr Tile kNone{-1, 0, 0, 0, 0, 0, 0, 0};
   Tile chain{0, 0, 0, 0, 0, 0, 0, 0};
   int step = 0, steps = 0, turns = static_cast<int>(blockIdx.x);
@@ -918,7 +959,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
         const int place = id / p.columns;
         if (p.order ? id >= total : place >= p.N) return kNone;
         chain.column = id - place * p.columns;
-        chain.t = place;
+        chain.t = part0 + place;
         chain.n = p.order ? p.order[place] : place;
         chain.row = p.order ? p.cu_seqlens[chain.n] : place * p.T;  // of the sequence
         chain.left = p.order ? p.cu_seqlens[chain.n + 1] - chain.row : p.T;
@@ -1107,7 +1148,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
   }
 }
 
-// out[c] = sum over rows of part[rows][C] (0 rows: 0; `count`: a packed scan's tickets[2] rows), unless
+// out[c] = sum over rows of part[rows][C] (0 rows: 0; `count`: a packed scan's tiles and chains), unless
 // the scan was skipped: 32 channels a block, each warp every 32nd row, the warps' sums in order.
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int rows, int C, const int* ticket,
                                                           bool count, float* out) {
@@ -1115,7 +1156,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int
   lap::griddep_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane;
   if (ticket && *ticket >= 1 << 30) return;  // cu_seqlens was refused
-  if (count) rows = ticket[2];
+  if (count) rows = ticket[2] + ticket[kTicket + 2];
   float s = 0.f;
   if (c < C) {
 #pragma unroll 4

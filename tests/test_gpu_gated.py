@@ -486,6 +486,47 @@ def test_packed_batches_by_chains(dtype, back):
         assert int(err) & lap.DEV_ERR_BAD_SEQLENS and torch.isnan(o).all() and torch.isnan(hf).all()
 
 
+UNEVEN = [90, 6000, 0, 33, 128, 1, 5000] + [70] * 60
+
+
+@pytest.mark.parametrize("dtype,C", [("bf16", 1024), ("bf16", 1001), ("fp32", 1024)])
+def test_long_sequences_among_many_short_ones(dtype, C):
+    """Sequences far longer than the others, which blocks share by tiles while the others go by chains;
+    padded ones of either kind, both directions, checked on a range of channels, bitwise repeatable."""
+    b = Batch(15, lens=UNEVEN, C=C, dtype=dtype, pool=70, pad=(0, 6))
+    cols = slice(C - 41, C)
+    o, hf = b.fwd()
+    dout, dhf = b.mat(), b.state()
+
+    def bwd():
+        dh0 = torch.full_like(hf, float("nan"))
+        return lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, dout, h0=b.h0, dh_final=dhf, dx=b.blank(),
+                                     dr=b.blank(), dg=b.blank(), dh0=dh0, **b.kw)
+    got = bwd()
+    torch.cuda.synchronize()
+    live = torch.zeros(b.tokens, dtype=torch.bool, device="cuda")
+    sums = esum = terms = 0.0
+    for n, L in enumerate(UNEVEN):
+        if b.slots[n] < 0:
+            continue
+        s, slot = b.rows(n), int(b.slots[n])
+        live[s] = True
+        args = [f64(t[s, cols]) for t in (b.x, b.r, b.g)] + [f64(b.slopes[cols]), f64(b.h0[slot, cols])]
+        ro, rh, eo, eh = scan_one(*args)
+        near(o[s, cols], ro, eo, dtype, f"o of sequence {n} ({L} tokens)")
+        near(hf[slot, cols], rh, eh, "fp32", f"h_final of sequence {n} ({L} tokens)")
+        ref = grad_one(*args, f64(o[s, cols]), f64(dout[s, cols]), f64(dhf[slot, cols]))
+        for t, name in zip(got, ("dx", "dr", "dg")):
+            near(t[s, cols], *ref[name], dtype, f"{name} of sequence {n} ({L} tokens)")
+        near(got[4][slot, cols], *ref["dh0"], "fp32", f"dh0 of sequence {n} ({L} tokens)")
+        sums, esum, terms = sums + ref["ds"][0], esum + ref["ds"][1], terms + np.abs(ref["ds"][0])
+    near(got[3][cols], sums, esum + len(UNEVEN) * 2.0 ** -24 * terms, "fp32", "dslopes")
+    assert all(torch.isnan(t[~live]).all() for t in (o, *got[:3]))
+    again = bwd()
+    assert torch.equal(b.fwd()[0][live], o[live])
+    assert all(torch.equal(t[live], u[live]) for t, u in zip(again[:3], got[:3])) and torch.equal(again[3], got[3])
+
+
 # ---------------------------------------------------------------- decode, verify, commit
 
 DECODE = {
