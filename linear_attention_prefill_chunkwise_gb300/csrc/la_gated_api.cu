@@ -80,7 +80,7 @@ bool packed_by_tiles(int64_t tokens, int N, int stride) { return tokens * 2 >= s
 
 template <typename E, bool kBack, bool kTma>
 Plan plan_for(int B, int T, int N, int C, bool packed) {
-  using S = lag::Shape<E, kBack, kTma>;
+  using S = lag::Shape<E, kBack, kTma, lag::kByTiles>;  // and kMixed
   Plan q;
   if (N == 0) return q;
   const int64_t rows = static_cast<int64_t>(B) * T;
@@ -232,17 +232,12 @@ cudaError_t launch_plan(const lag::Params<E>& p, const Plan& q, int sms, cudaStr
   return la_host::launch_pdl(lag::scan_plan_kernel<E>, grid, lag::kThreads, 0, s, p);
 }
 
-template <lag::Mode kMode>
-struct ModeTag {
-  static constexpr lag::Mode value = kMode;
-};
-
-template <typename E, bool kBack, bool kTma>
-la_status launch_scan_as(lag::Params<E> p, int B, void* workspace, float* dslopes, int sms, cudaStream_t s) {
-  using S = lag::Shape<E, kBack, kTma>;
-  const bool packed = p.cu_seqlens != nullptr;
-  const Plan q = plan_for<E, kBack, kTma>(B, p.T, p.N, p.C, packed);
-  set_plan(&p, q, kBack, workspace);
+template <typename E, bool kBack, bool kTma, lag::Mode kMode>
+la_status launch_mode(const lag::Params<E>& p, int64_t items, int sms, cudaStream_t s) {
+  using S = lag::Shape<E, kBack, kTma, kMode>;
+  lag::Params<E> with = p;
+  if (kMode == lag::kByChains) with.stride = S::kTileRows;
+  if (kMode == lag::kByTiles && p.table) with.ticket += lag::kTicket;
   lag::Maps maps;
   if constexpr (kTma) {
     for (int i = 0; i < S::kInputs; ++i) {
@@ -250,23 +245,27 @@ la_status launch_scan_as(lag::Params<E> p, int B, void* workspace, float* dslope
       if (st != LA_OK) return st;
     }
   }
+  const int64_t most = static_cast<int64_t>(sms) * S::kBlocks;
+  const cudaError_t ce = la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma, kMode>,
+                                             static_cast<unsigned>(items < most ? items : most), S::kThreads,
+                                             lag::scan_smem_bytes<E, kBack, kTma, kMode>(), s, with, maps);
+  return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
+}
+
+template <typename E, bool kBack, bool kTma>
+la_status launch_scan_as(lag::Params<E> p, int B, void* workspace, float* dslopes, int sms, cudaStream_t s) {
+  const bool packed = p.cu_seqlens != nullptr;
+  const Plan q = plan_for<E, kBack, kTma>(B, p.T, p.N, p.C, packed);
+  set_plan(&p, q, kBack, workspace);
   cudaError_t ce = q.ticket ? launch_plan(p, q, sms, s) : cudaSuccess;
+  la_status st = LA_OK;
   if (ce == cudaSuccess && q.tiles > 0) {
-    const int most = sms * S::kBlocks;
-    auto run = [&](auto mode, const lag::Params<E>& with, int64_t items) {
-      constexpr lag::Mode kMode = decltype(mode)::value;
-      return la_host::launch_pdl(lag::gated_scan_kernel<E, kBack, kTma, kMode>,
-                                 static_cast<unsigned>(items < most ? items : most), S::kThreads,
-                                 lag::scan_smem_bytes<E, kBack, kTma, kMode>(), s, with, maps);
-    };
-    if (q.mode != lag::kByTiles)
-      ce = q.mode == lag::kByChains ? run(ModeTag<lag::kByChains>{}, p, q.items) : run(ModeTag<lag::kMixed>{}, p, q.items);
-    if (ce == cudaSuccess && (q.table || q.mode == lag::kByTiles)) {
-      lag::Params<E> with = p;
-      if (q.table) with.ticket += lag::kTicket;
-      ce = run(ModeTag<lag::kByTiles>{}, with, static_cast<int64_t>(q.tiles) * q.columns);
-    }
+    if (q.mode == lag::kByChains) st = launch_mode<E, kBack, kTma, lag::kByChains>(p, q.items, sms, s);
+    else if (q.mode == lag::kMixed) st = launch_mode<E, kBack, kTma, lag::kMixed>(p, q.items, sms, s);
+    if (st == LA_OK && (q.table || q.mode == lag::kByTiles))
+      st = launch_mode<E, kBack, kTma, lag::kByTiles>(p, static_cast<int64_t>(q.tiles) * q.columns, sms, s);
   }
+  if (st != LA_OK) return st;
   if (ce == cudaSuccess && kBack)
     ce = la_host::launch_pdl(lag::column_sum_kernel, (p.C + 31) / 32, 1024, 0, s, static_cast<const float*>(p.part),
                              q.parts, p.C, static_cast<const int*>(packed ? p.ticket : nullptr), q.order || q.table, dslopes);

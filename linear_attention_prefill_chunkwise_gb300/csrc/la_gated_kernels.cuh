@@ -53,19 +53,29 @@ constexpr int kThreads = 128;   // threads of the small kernels
 constexpr int kMaxInputs = 5;   // x, r, g; backward: dout and o (one row up: h_{t-1}) too
 constexpr int kStages = 2;
 
+// How blocks take their work; each is a kernel of its own, since the loop is held up by its own
+// instructions and registers (2 x 8192 tokens x 8192 channels by chains, one kernel for all and this:
+// forward 216 and 197 us, gradients 425 and 385).
+enum Mode {
+  kByChains,  // one block walks all tiles of a sequence's channels
+  kByTiles,   // tiles of one sequence each, states from block to block
+  kMixed      // tiles that hold rows of several sequences: packed (states from block to block) or whole ones
+};
+
 // Shape of a scan kernel: rows per warp, blocks per SM and the stages' layout.  kTma: rows arrive
 // by TMA boxes of kRows x 64 channels; else by 16-byte copies of the aligned chunks that a row's
 // channels touch, one chunk more than the channels fill.
 // Rows per warp: as many as two blocks' registers (forward: a and b of each) and shared memory hold,
 // since every tile costs the same few hundred instructions; more of them spill, or leave the copies
-// no cache.  2 x 8192 tokens of 8192 channels, BF16: forward 16 rows 194 us, 14 202, 12 212;
-// gradients 10 rows 362, 9 371, 8 373, 6 422 (by tiles, 32768 tokens of 4096 channels: 527, 440, 466).
-// Unaligned, 32 sequences of up to 4096 tokens of 1001 channels: forward 15 rows 241, 14 187, 12 180;
-// gradients 8 rows 403, 7 363, 6 363.  FP32, 8192 tokens of 4096 channels: gradients 5 rows 231, 4 212, 3 254.
-template <typename E, bool kBack, bool kTma>
+// no cache.  BF16, 2 x 8192 tokens of 8192 channels: forward 16 rows 188 us, 14 202, 12 212.
+// Gradients by chains 8 rows 362, 9 355, but of 32 x 1024 tokens of 4096 channels 357 and 391; by tiles
+// (32768 tokens of 4096 channels) 10 rows 525, 9 433, 8 468.  Unaligned, 32 sequences of up to 4096
+// tokens of 1001 channels: forward 15 rows 241, 14 187, 12 180; gradients 8 rows 403, 7 363, 6 363.
+// FP32, 8192 tokens of 4096 channels: gradients 5 rows 231, 4 212, 3 254.
+template <typename E, bool kBack, bool kTma, Mode kMode>
 struct Shape {
   static constexpr int kWarps = 8;
-  static constexpr int kRows = (kBack ? (kTma ? 9 : 6) : (kTma ? 16 : 12)) / (sizeof(E) / 2);
+  static constexpr int kRows = (kBack ? (!kTma ? 6 : kMode == kByChains ? 8 : 9) : (kTma ? 16 : 12)) / (sizeof(E) / 2);
   static constexpr int kBlocks = 2;
   static constexpr int kAsk = kRows * 5 / 8;  // the row before which a warp asks for the published words
   static constexpr int kThreads = kWarps * 32;
@@ -74,15 +84,6 @@ struct Shape {
   static constexpr int kPitch = kCols * sizeof(E) + (kTma ? 0 : 16);  // bytes of a row
   static constexpr int kInputBytes = kTileRows * kPitch;
   static constexpr int kStageBytes = kInputs * kInputBytes;
-};
-
-// How blocks take their work; each is a kernel of its own, since the loop is held up by its own
-// instructions and registers (2 x 8192 tokens x 8192 channels by chains, one kernel for all and this:
-// forward 216 and 197 us, gradients 425 and 385).
-enum Mode {
-  kByChains,  // one block walks all tiles of a sequence's channels
-  kByTiles,   // tiles of one sequence each, states from block to block
-  kMixed      // tiles that hold rows of several sequences: packed (states from block to block) or whole ones
 };
 
 // A tile: its number (-1: none), its channels, its sequence n, its place i in the walk over that
@@ -424,10 +425,10 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 // Starts the loads of a tile's rows of every input into `stage`, whose first row is row `low` of
 // the matrices: each warp its own rows, from row `first` of the stage (kTma: one thread of it, a box
 // for each input).
-template <bool kBack, bool kTma, typename E>
+template <Mode kMode, bool kBack, bool kTma, typename E>
 __device__ __forceinline__ void fetch(const Params<E>& p, const Maps& maps, char* stage, uint64_t* bar, int low,
                                       int column, int first, int lane) {
-  using S = Shape<E, kBack, kTma>;
+  using S = Shape<E, kBack, kTma, kMode>;
   if constexpr (kTma) {
     lap::mbar_arrive_expect_tx(bar, S::kInputs * S::kRows * S::kPitch);
 #pragma unroll
@@ -487,9 +488,9 @@ __device__ __forceinline__ bool arrived(uint64_t* bar, unsigned use, volatile in
 }
 
 // A lane's view of one input's rows in a stage.
-template <typename E, bool kBack, bool kTma>
+template <typename E, bool kBack, bool kTma, Mode kMode>
 struct View {
-  using S = Shape<E, kBack, kTma>;
+  using S = Shape<E, kBack, kTma, kMode>;
   const char* at;
   unsigned first, step;  // bytes before the first row's first channel in its chunk; more per row
   // `rows`: the warp's first row in the stage, row `low` of the matrix
@@ -623,7 +624,7 @@ struct ScanSmem {
 
 template <typename E, bool kBack, bool kTma, Mode kMode>
 __host__ __device__ constexpr int scan_smem_bytes() {
-  using S = Shape<E, kBack, kTma>;
+  using S = Shape<E, kBack, kTma, kMode>;
   return kStages * S::kStageBytes + static_cast<int>(sizeof(ScanSmem<kMode, S::kWarps>));
 }
 
@@ -774,9 +775,9 @@ __device__ __forceinline__ void step2(f2 slope, f2 x, f2 r, f2 g, f2* a, f2* b) 
   *b = f2_mul(f2_mul(w, x), rsqrt2(f2_mul(w, f2_mul(q, q))));
 }
 
-template <typename E, bool kTma>
+template <typename E, bool kTma, Mode kMode>
 struct Forward {
-  using S = Shape<E, false, kTma>;
+  using S = Shape<E, false, kTma, kMode>;
   static constexpr int K = S::kRows;
   f2 a[K], b[K];
 
@@ -785,7 +786,7 @@ struct Forward {
   template <bool kEdges, bool kSmall, typename F>
   __device__ __forceinline__ Run first(const Params<E>& p, const char* stage, int low, f2 slope, const Rows& rows,
                                        const Lane<kTma>& l, int lane, F ask) {
-    const View<E, false, kTma> x(p, stage, 0, low, lane), r(p, stage, 1, low, lane), g(p, stage, 2, low, lane);
+    const View<E, false, kTma, kMode> x(p, stage, 0, low, lane), r(p, stage, 1, low, lane), g(p, stage, 2, low, lane);
     if constexpr (kEdges) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -831,22 +832,22 @@ struct Forward {
 
 // ---------------------------------------------------------------- the gradients' scan
 
-template <typename E, bool kTma>
+template <typename E, bool kTma, Mode kMode>
 struct Backward {
-  using S = Shape<E, true, kTma>;
+  using S = Shape<E, true, kTma, kMode>;
   static constexpr int K = S::kRows;
   f2 sr[K], m[K];  // sig(r) and 1 - lambda; row k in walking order is row K - 1 - k of the stage
 
-  template <bool kEdges, typename F>
+  template <bool kEdges, bool kSmall, typename F>
   __device__ __forceinline__ Run first(const Params<E>& p, const char* stage, int low, f2 slope, const Rows& rows,
                                        const Lane<kTma>& l, int lane, F ask) {
-    const View<E, true, kTma> r(p, stage, 1, low, lane), d(p, stage, 3, low, lane);
+    const View<E, true, kTma, kMode> r(p, stage, 1, low, lane), d(p, stage, 3, low, lane);
     Run run{f2_all(1.f), f2_all(0.f)};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (k == S::kAsk) ask();
       sr[k] = sigmoid2(r.get(K - 1 - k));
-      m[k] = one_minus_lambda2<false>(f2_mul(slope, sr[k]));
+      m[k] = one_minus_lambda2<kSmall>(f2_mul(slope, sr[k]));
       const f2 a = f2_sub(f2_all(1.f), m[k]);
       if constexpr (kEdges) {
         if (rows.begin >> k & 1u)
@@ -862,7 +863,7 @@ struct Backward {
   template <bool kEdges>
   __device__ __forceinline__ f2 second(const Params<E>& p, const char* stage, int low, f2 slope, f2 w, const Rows& rows,
                                        const Lane<kTma>& l, int lane) {
-    const View<E, true, kTma> x(p, stage, 0, low, lane), g(p, stage, 2, low, lane), d(p, stage, 3, low, lane),
+    const View<E, true, kTma, kMode> x(p, stage, 0, low, lane), g(p, stage, 2, low, lane), d(p, stage, 3, low, lane),
         h(p, stage, 4, low, lane);
     E* out[3];
 #pragma unroll
@@ -915,9 +916,9 @@ struct Backward {
 // block waiting for another; chains in turn, or by tickets the longest first (packed).
 // Tiles of several whole sequences: in turn.
 template <typename E, bool kBack, bool kTma, Mode kMode>
-__global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBack, kTma>::kBlocks)
+__global__ void __launch_bounds__(Shape<E, kBack, kTma, kMode>::kThreads, Shape<E, kBack, kTma, kMode>::kBlocks)
     gated_scan_kernel(const __grid_constant__ Params<E> p, const __grid_constant__ Maps maps) {
-  using S = Shape<E, kBack, kTma>;
+  using S = Shape<E, kBack, kTma, kMode>;
   constexpr int K = S::kRows, kWarps = S::kWarps;
   const bool waits = kMode == kByTiles || (kMode == kMixed && p.runs);  // states pass from block to block
   extern __shared__ __align__(128) char shared[];
@@ -999,7 +1000,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
     const Tile& q = sm.tile[turn & 3];
     if (q.t >= 0) {
       if (!kTma || lane == 0)
-        fetch<kBack, kTma>(p, maps, shared + turn % kStages * S::kStageBytes, &sm.bar[warp][turn % kStages],
+        fetch<kMode, kBack, kTma>(p, maps, shared + turn % kStages * S::kStageBytes, &sm.bar[warp][turn % kStages],
                            q.row + (kBack ? p.stride - S::kTileRows : 0), q.column, mine, lane);
       loaded = turn;
     } else if constexpr (!kTma) {
@@ -1082,7 +1083,7 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
     };
     const bool here = arrived<kTma>(&sm.bar[warp][turn % kStages], turn / kStages, &sm.abort);
     if constexpr (!kBack) {
-      Forward<E, kTma> f;
+      Forward<E, kTma, kMode> f;
       // u <= slope: where all of the tile's slopes are small, so is every u
       const float2 s = f2_unpack(slope);
       const bool small = __all_sync(0xFFFFFFFFu, s.x < kNear && s.y < kNear);
@@ -1105,15 +1106,20 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma>::kThreads, Shape<E, kBac
       else
         f.template second<false>(p, low, h, Rows{}, Lane<kTma>(q.column, lane, p.C));
     } else {
-      Backward<E, kTma> f;
+      Backward<E, kTma, kMode> f;
       const Lane<kTma> l(q.column, lane, p.C);
       Run run;
       if (kMode == kMixed && edges) {
         const Rows rows = rows_of<kMode, kBack, K>(p, q, warp, lane);
         begins = rows.begin;
-        run = f.template first<true>(p, stage, low, slope, rows, l, lane, ask);
+        run = f.template first<true, false>(p, stage, low, slope, rows, l, lane, ask);
       } else {
-        run = f.template first<false>(p, stage, low, slope, Rows{}, l, lane, ask);
+        // as forward; 600 sequences of up to 128 tokens, 2048 channels: 301 us, 326 without
+        const float2 s = f2_unpack(slope);
+        if (kMode != kMixed && __all_sync(0xFFFFFFFFu, s.x < kNear && s.y < kNear))
+          run = f.template first<false, true>(p, stage, low, slope, Rows{}, l, lane, ask);
+        else
+          run = f.template first<false, false>(p, stage, low, slope, Rows{}, l, lane, ask);
       }
       close(run);
       if (__syncthreads_or(!here)) break;
