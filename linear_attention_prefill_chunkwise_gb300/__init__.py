@@ -588,6 +588,12 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _empty_like(t, shape, dev, stream):
+    """A new dense matrix of a checked matrix's shape and type (quicker by a microsecond than _empty)."""
+    import torch
+    return torch.empty_like(t) if stream is None else _empty(shape, t.dtype, dev, stream)
+
+
 def _call(fn, dev, *args):
     """Call a C entry point with device ``dev`` current; raise on a non-OK status."""
     import torch
@@ -674,7 +680,7 @@ def la_gated_scan_fwd(x, r, g, slopes, h0=None, state_indices=None, cu_seqlens=N
     B, T, N, pool, idx, cu, (p0, pf) = _gated_sequences(tokens, C, dev, state_indices, cu_seqlens, seq_len,
                                                         ((h0, "h0"), (h_final, "h_final")))
     if o is None:
-        o, ldo = _empty(shape, dtype, dev, stream), C
+        o, ldo = _empty_like(x, shape, dev, stream), C
     else:
         ldo = _like(o, "o", shape, dtype, dev)
     owner, ws, nbytes = _scan_workspace(workspace, dtype, dev, B, T, N, C, cu is not None, False, stream)
@@ -698,7 +704,7 @@ def la_gated_scan_bwd(x, r, g, slopes, o, dout, h0=None, dh_final=None, state_in
     lds = [_like(t, n, shape, dtype, dev) for t, n in ((r, "r"), (g, "g"), (o, "o"), (dout, "dout"))]
     B, T, N, pool, idx, cu, (p0, pdf, pd0) = _gated_sequences(
         tokens, C, dev, state_indices, cu_seqlens, seq_len, ((h0, "h0"), (dh_final, "dh_final"), (dh0, "dh0")))
-    dx, dr, dg = (_empty(shape, dtype, dev, stream) if t is None else t for t in (dx, dr, dg))
+    dx, dr, dg = (_empty_like(x, shape, dev, stream) if t is None else t for t in (dx, dr, dg))
     lds += [_like(t, n, shape, dtype, dev) for t, n in ((dx, "dx"), (dr, "dr"), (dg, "dg"))]
     if dslopes is None:
         dslopes = _empty((C,), torch.float32, dev, stream)
@@ -734,7 +740,7 @@ def _gated_outputs(fn, x, r, g, slopes, state, T, state_indices, o, dev_error, s
     shape, B, C, P, code, dev, (sl, st, idx, err), lds = _gated_requests(x, r, g, slopes, state, T, state_indices,
                                                                          dev_error)
     if o is None:
-        o, ldo = _empty(shape, x.dtype, dev, stream), C
+        o, ldo = _empty_like(x, shape, dev, stream), C
     else:
         ldo = _like(o, "o", shape, x.dtype, dev)
     _call(fn, dev, x.data_ptr(), r.data_ptr(), g.data_ptr(), sl, st, idx, o.data_ptr(), *lds, ldo, B, T, C, P, code, err,
@@ -782,7 +788,7 @@ def _norm_inputs(x, weight, residual, residual_out, stream):
         return code, shape, dev, (None, w, None), (ldx, 0, 0), None
     ldres = _like(residual, "residual", shape, x.dtype, dev)
     if residual_out is None:
-        residual_out, ldro = _empty(shape, x.dtype, dev, stream), C
+        residual_out, ldro = _empty_like(x, shape, dev, stream), C
     else:
         ldro = _like(residual_out, "residual_out", shape, x.dtype, dev)
     return code, shape, dev, (residual.data_ptr(), w, residual_out.data_ptr()), (ldx, ldres, ldro), residual_out
@@ -800,7 +806,7 @@ def la_rms_norm_fwd(x, weight, eps, residual=None, y=None, residual_out=None, de
                                                                                     stream)
     rows, C = shape
     if y is None:
-        y, ldy = _empty(shape, x.dtype, dev, stream), C
+        y, ldy = _empty_like(x, shape, dev, stream), C
     else:
         ldy = _like(y, "y", shape, x.dtype, dev)
     _call(lib.la_rms_norm_fwd, dev, x.data_ptr(), res, w, eps, y.data_ptr(), ro, ldx, ldres, ldy, ldro, rows, C, code,
@@ -857,7 +863,7 @@ def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, worksp
     lddy = _like(dy, "dy", shape, dtype, dev)
     lddres = 0 if dres is None else _like(dres, "dres", shape, dtype, dev)
     if dx is None:
-        dx, lddx = _empty(shape, dtype, dev, stream), C
+        dx, lddx = _empty_like(s, shape, dev, stream), C
     else:
         lddx = _like(dx, "dx", shape, dtype, dev)
     if dweight is None:

@@ -14,7 +14,7 @@
 // input is read once and every output written once.  What bounds it is the bytes, then the
 // instructions: a row of 64 channels takes a warp 59 forward and 128 for the gradients (unaligned:
 // 204), at 0.61 - 0.67 of the issue slots.  Measured, BF16, of the bytes at the copy rate: 2 x 8192
-// tokens of 8192 channels 188 us (0.84), gradients 371 (0.85); 32 packed sequences of up to 4096
+// tokens of 8192 channels 188 us (0.84), gradients 362 (0.87); 32 packed sequences of up to 4096
 // tokens of 4096 channels 301 (0.94); one sequence of 32768 x 4096 232 (0.68), of 131072 x 1024 314
 // (0.50: the states' way from block to block); FP32 8192 x 8192 173 (0.92).
 //
