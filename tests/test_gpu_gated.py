@@ -527,6 +527,22 @@ def test_long_sequences_among_many_short_ones(dtype, C):
     assert all(torch.equal(t[live], u[live]) for t, u in zip(again[:3], got[:3])) and torch.equal(again[3], got[3])
 
 
+@pytest.mark.parametrize("lens,C", [(UNEVEN, 1024), ([300] * 240, 256), ([1] * 900, 70)])
+def test_garbage_workspace_of_lists_and_tables(lens, C):
+    b = Batch(16, lens=lens, C=C, pool=len(lens))
+    o, _ = b.fwd()
+    ref = lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, o, h0=b.h0, **b.kw)
+    for fill in (0x00, 0x7F, 0xFF):
+        for back in (False, True):
+            n = lap.la_gated_scan_workspace(1, b.tokens, len(lens), C, True, torch.bfloat16, back)
+            ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+            if back:
+                got = lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, o, h0=b.h0, workspace=ws, **b.kw)
+                assert all(torch.equal(x, y) for x, y in zip(got[:4], ref[:4]))
+            else:
+                assert torch.equal(b.fwd(workspace=ws)[0], o)
+
+
 # ---------------------------------------------------------------- decode, verify, commit
 
 DECODE = {
