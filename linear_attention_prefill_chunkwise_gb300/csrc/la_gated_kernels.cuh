@@ -766,13 +766,14 @@ __device__ __forceinline__ void empty_sequences(const Params<E>& p, const Tile& 
 // a = lambda and b = beta sig(g) x of one token.  With w = beta^2 and q = 1 / sig(g), b is
 // w x / sqrt(w q^2): one rsqrt stands for beta's root and the gate's reciprocal (the special
 // function unit is what bounds this kernel after memory).  q^2 overflows below g = -44, where b
-// becomes 0 (2^-63 of beta x at most).
+// becomes 0 (2^-63 of beta x at most).  Only w is kept from 0, since a maximum drops NaN: w's own NaN
+// is in the product, and q's goes through the root.
 template <bool kSmall>
 __device__ __forceinline__ void step2(f2 slope, f2 x, f2 r, f2 g, f2* a, f2* b) {
   const f2 m = one_minus_lambda2<kSmall>(f2_mul(slope, sigmoid2(r)));
   const f2 w = one_minus_square2(m), q = inverse_sigmoid2(g);
   *a = f2_sub(f2_all(1.f), m);
-  *b = f2_mul(f2_mul(w, x), rsqrt2(f2_mul(w, f2_mul(q, q))));
+  *b = f2_mul(f2_mul(w, x), rsqrt2(f2_mul(positive2(w), f2_mul(q, q))));
 }
 
 template <typename E, bool kTma, Mode kMode>
@@ -884,7 +885,7 @@ struct Backward {
       }
       const f2 G = f2_add(d.get(at), w), vx = x.get(at), sg = sigmoid2(g.get(at)), u = f2_mul(slope, sr[k]);
       const f2 beta2 = one_minus_square2(m[k]);
-      f2 inv = rsqrt2(beta2);
+      f2 inv = rsqrt2(positive2(beta2));
       const f2 beta = f2_mul(beta2, inv);
       const float2 vu = f2_unpack(u), vi = f2_unpack(inv);
       inv = f2_pack(vu.x > 0.f ? vi.x : 0.f, vu.y > 0.f ? vi.y : 0.f);

@@ -102,8 +102,12 @@ __device__ __forceinline__ f2 one_minus_lambda2(f2 u) {
 
 // 1 - lambda^2 = m (2 - m).
 __device__ __forceinline__ f2 one_minus_square2(f2 m) { return f2_mul(m, f2_sub(f2_all(2.f), m)); }
+// w >= 0 kept from 0 (NaN too becomes kLeast).
+__device__ __forceinline__ f2 positive2(f2 w) {
+  return f2_each(w, [](float v) { return fmaxf(v, kLeast); });
+}
 __device__ __forceinline__ f2 rsqrt2(f2 w) {
-  return f2_each(w, [](float v) { return rsqrt_approx(fmaxf(v, kLeast)); });
+  return f2_each(w, [](float v) { return rsqrt_approx(v); });
 }
 
 }  // namespace lag

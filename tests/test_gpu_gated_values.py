@@ -1,0 +1,131 @@
+"""The gated recurrence on the GPU where its values are hard: NaN in one input.  Each
+kernel form is entered (whole sequences in a tile, chains, tiles, mixed rows, rows that are not 16-byte aligned)."""
+import numpy as np
+import pytest
+
+import linear_attention_prefill_chunkwise_gb300 as lap
+from test_gpu_gated import Batch
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+FORMS = {
+    "whole sequences": dict(lens=[40] * 7, C=72, packed=False),
+    "chains": dict(lens=[300] * 3, C=72, packed=False),
+    "tiles": dict(lens=[3000], C=72, packed=False),
+    "mixed rows": dict(lens=[50, 3, 0, 90, 41, 7, 120, 60], C=72),
+    "packed tiles": dict(lens=[700, 0, 900, 412], C=72),
+    "packed chains": dict(lens=[0, 600, 700, 1, 517, 300, 129, 128, 700, 64, 725, 812, 0, 333, 901, 499], C=4096),
+    "unaligned": dict(lens=[300, 41, 900], C=67),
+    "fp32": dict(lens=[300, 41, 900], C=72, dtype="fp32"),
+}
+
+
+def grads(b, o, dout, **kw):
+    dx, dr, dg = b.three(float("nan"))
+    dh0 = torch.full((b.P, b.C), float("nan"), device="cuda") if b.h0 is not None else None
+    res = lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, dout, h0=b.h0, dx=dx, dr=dr, dg=dg, dh0=dh0, **b.kw, **kw)
+    torch.cuda.synchronize()
+    return res
+
+
+@pytest.mark.parametrize("what", ["x", "r", "g", "h0"])
+@pytest.mark.parametrize("form", FORMS)
+def test_a_nan_reaches_what_depends_on_it(form, what):
+    """One NaN at one token of one channel: o from that token on and h_final are NaN, as the definition
+    has it; every other value keeps its bits."""
+    b = Batch(40, **FORMS[form])
+    o, hf = b.fwd()
+    n = int(np.argmax(b.lens))
+    s, slot, c = b.rows(n), int(b.slots[n]), 5
+    t = s.start if what == "h0" else (s.start + s.stop) // 2
+    if what == "h0":
+        b.h0[slot, c] = float("nan")
+    else:
+        getattr(b, what)[t, c] = float("nan")
+    o2, hf2 = b.fwd()
+    assert torch.isnan(o2[t:s.stop, c]).all() and torch.isnan(hf2[slot, c])
+    o2[t:s.stop, c], hf2[slot, c] = o[t:s.stop, c], hf[slot, c]
+    assert torch.equal(o2, o) and torch.equal(hf2, hf)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_a_nan_gate_reaches_its_gradients(form):
+    """NaN in g at one token: dx, dr, dg of that token and dslopes of its channel, nothing else."""
+    b = Batch(41, **FORMS[form])
+    o, _ = b.fwd()
+    dout = b.mat()
+    want = grads(b, o, dout)
+    n = int(np.argmax(b.lens))
+    t, c = (b.rows(n).start + b.rows(n).stop) // 2, 5
+    b.g[t, c] = float("nan")
+    got = grads(b, o, dout)
+    for k in range(3):
+        assert torch.isnan(got[k][t, c]), ("dx", "dr", "dg")[k]
+        got[k][t, c] = want[k][t, c]
+        assert torch.equal(got[k], want[k]), ("dx", "dr", "dg")[k]
+    assert torch.isnan(got[3][c])
+    got[3][c] = want[3][c]
+    assert torch.equal(got[3], want[3]) and torch.equal(got[4], want[4])
+
+
+@pytest.mark.parametrize("what", ["x", "r", "g", "state"])
+@pytest.mark.parametrize("C", [64, 67])
+def test_a_nan_in_decode(C, what):
+    B, T, c, t = 5, 6, 9, 3
+    b = Batch(42, lens=[T] * B, C=C, packed=False, pool=8)
+    slot, row = int(b.slots[2]), 2 * T + t
+
+    def calls():
+        st, cm = b.h0.clone(), b.h0.clone()
+        o = lap.la_gated_decode(b.x, b.r, b.g, b.slopes, st, T, state_indices=b.idx)
+        v = lap.la_gated_verify(b.x, b.r, b.g, b.slopes, b.h0, T, state_indices=b.idx)
+        lap.la_gated_commit(b.x, b.r, b.g, b.slopes, cm, T, torch.tensor([T, t, t + 1, T, 0], dtype=torch.int32,
+                                                                         device="cuda"), state_indices=b.idx)
+        return o, v, st, cm
+    want = calls()
+    if what == "state":
+        b.h0[slot, c] = float("nan")
+        row = 2 * T
+    else:
+        getattr(b, what)[row, c] = float("nan")
+    for k, (got, ref) in enumerate(zip(calls(), want)):
+        part = (slice(row, 3 * T), c) if k < 2 else (slot, c)
+        assert torch.isnan(got[part]).all(), ("decode", "verify", "state", "commit")[k]
+        got[part] = ref[part]
+        assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("form", FORMS)
+def test_other_sequences_keep_their_bits(form, value):
+    """Non-finite inputs and states of one sequence leave the others, in both directions."""
+    b = Batch(43, **FORMS[form])
+    o, hf = b.fwd()
+    dout, bad = b.mat(), int(np.argmax(b.lens))
+    want = grads(b, o, dout)
+    s, slot = b.rows(bad), int(b.slots[bad])
+    for t in (b.x, b.r, b.g, dout):
+        t[s] = value
+    b.h0[slot] = value
+    o2, hf2 = b.fwd()
+    got = grads(b, o2, dout)
+    for now, was, at in [(o2, o, s), (hf2, hf, slot), *((got[k], want[k], s) for k in range(3)), (got[4], want[4], slot)]:
+        now, was = now.clone(), was.clone()
+        now[at] = was[at] = 0
+        assert torch.equal(now, was)
+
+
+def test_other_requests_keep_their_bits_in_decode():
+    B, T, C = 4, 3, 72
+    b = Batch(44, lens=[T] * B, C=C, packed=False, pool=6)
+    st = b.h0.clone()
+    o = lap.la_gated_decode(b.x, b.r, b.g, b.slopes, st, T, state_indices=b.idx)
+    s, slot = b.rows(1), int(b.slots[1])
+    for t in (b.x, b.r, b.g):
+        t[s] = float("inf")
+    st2 = b.h0.clone()
+    st2[slot] = float("nan")
+    o2 = lap.la_gated_decode(b.x, b.r, b.g, b.slopes, st2, T, state_indices=b.idx)
+    o2[s], st2[slot] = o[s], st[slot]
+    assert torch.equal(o2, o) and torch.equal(st2, st)
