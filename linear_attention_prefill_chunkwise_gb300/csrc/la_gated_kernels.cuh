@@ -770,9 +770,9 @@ __device__ __forceinline__ void empty_sequences(const Params<E>& p, const Tile& 
 // is in the product, and q's goes through the root.
 template <bool kSmall>
 __device__ __forceinline__ void step2(f2 slope, f2 x, f2 r, f2 g, f2* a, f2* b) {
-  const f2 m = one_minus_lambda2<kSmall>(f2_mul(slope, sigmoid2(r)));
-  const f2 w = one_minus_square2(m), q = inverse_sigmoid2(g);
-  *a = f2_sub(f2_all(1.f), m);
+  const Decay d = decay2<kSmall>(f2_mul(slope, sigmoid2(r)));
+  const f2 w = one_minus_square2(d), q = inverse_sigmoid2(g);
+  *a = d.lambda;
   *b = f2_mul(f2_mul(w, x), rsqrt2(f2_mul(positive2(w), f2_mul(q, q))));
 }
 
@@ -837,7 +837,7 @@ template <typename E, bool kTma, Mode kMode>
 struct Backward {
   using S = Shape<E, true, kTma, kMode>;
   static constexpr int K = S::kRows;
-  f2 sr[K], m[K];  // sig(r) and 1 - lambda; row k in walking order is row K - 1 - k of the stage
+  f2 sr[K], kept[K];  // sig(r) and the decay, folded; row k in walking order is row K - 1 - k of the stage
 
   template <bool kEdges, bool kSmall, typename F>
   __device__ __forceinline__ Run first(const Params<E>& p, const char* stage, int low, f2 slope, const Rows& rows,
@@ -848,8 +848,10 @@ struct Backward {
     for (int k = 0; k < K; ++k) {
       if (k == S::kAsk) ask();
       sr[k] = sigmoid2(r.get(K - 1 - k));
-      m[k] = one_minus_lambda2<kSmall>(f2_mul(slope, sr[k]));
-      const f2 a = f2_sub(f2_all(1.f), m[k]);
+      const f2 u = f2_mul(slope, sr[k]);
+      const Decay decay = decay2<kSmall>(u);
+      const f2 a = decay.lambda;
+      kept[k] = fold2<kSmall>(u, decay);
       if constexpr (kEdges) {
         if (rows.begin >> k & 1u)
           run = {f2_all(-0.f), load_state(p.start, __shfl_sync(0xFFFFFFFFu, rows.slot, k), p.C, l)};
@@ -884,12 +886,12 @@ struct Backward {
         if (rows.end >> k & 1u) before = load_state(p.h0, slot, p.C, l);
       }
       const f2 G = f2_add(d.get(at), w), vx = x.get(at), sg = sigmoid2(g.get(at)), u = f2_mul(slope, sr[k]);
-      const f2 beta2 = one_minus_square2(m[k]);
+      const Decay decay = unfold2(kept[k]);
+      const f2 lambda = decay.lambda, beta2 = one_minus_square2(decay);
       f2 inv = rsqrt2(positive2(beta2));
       const f2 beta = f2_mul(beta2, inv);
       const float2 vu = f2_unpack(u), vi = f2_unpack(inv);
       inv = f2_pack(vu.x > 0.f ? vi.x : 0.f, vu.y > 0.f ? vi.y : 0.f);
-      const f2 lambda = f2_sub(one, m[k]);
       const f2 gs = f2_mul(G, sg), dx = f2_mul(gs, beta);
       store2(out[0], l, dx);
       store2(out[2], l, f2_mul(f2_mul(dx, vx), f2_sub(one, sg)));

@@ -47,7 +47,9 @@ __device__ __forceinline__ float rsqrt_approx(float v) {
 //              least relative error on [0, 1/8] (2e-8; evaluated in FP32: 1e-7).  Such a lambda
 //              is off by its own rounding alone, and it is here that 1 / m tokens add up its error.
 //   otherwise  m = 1 - exp2(-u log2 e), good to 2^-23 / m relative: 1e-6 at 1/8.
-// Then 1 - lambda^2 = m (2 - m) has no cancellation, and beta = w rsqrt(w) with w = 1 - lambda^2
+// lambda is 1 - m where u < 1/8 and the exp2 itself beyond, so steep slopes keep its digits too (as
+// 1 - m it is off by 2e-5 of itself at u = 8, and 0 from 17.4 on).
+// Then 1 - lambda^2 = m (1 + lambda) has no cancellation, and beta = w rsqrt(w) with w = 1 - lambda^2
 // (kept from rsqrt(0) by the smallest normal number; w = 0 gives beta = 0).
 constexpr float kNear = 0.125f;
 constexpr float kC1 = -0.4999971091747284f, kC2 = 0.16652604937553406f, kC3 = -0.039715882390737534f;
@@ -87,21 +89,39 @@ __device__ __forceinline__ f2 sigmoid2(f2 z) {
   return f2_each(inverse_sigmoid2(z), [](float v) { return rcp_approx(v); });
 }
 
-// m = 1 - lambda of two channels.  kSmall: u < kNear is known.
+// lambda = exp(-u) of two channels, and m = 1 - lambda.  kSmall: u < kNear is known.
+struct Decay {
+  f2 lambda, m;
+};
 template <bool kSmall>
-__device__ __forceinline__ f2 one_minus_lambda2(f2 u) {
+__device__ __forceinline__ Decay decay2(f2 u) {
   f2 p = f2_fma(u, f2_all(kC3), f2_all(kC2));
   p = f2_fma(u, p, f2_all(kC1));
   p = f2_fma(u, p, f2_all(1.f));
-  const f2 near = f2_mul(u, p);
-  if constexpr (kSmall) return near;
+  const f2 near = f2_mul(u, p), left = f2_sub(f2_all(1.f), near);
+  if constexpr (kSmall) return {left, near};
   const f2 e = f2_each(f2_mul(u, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
-  const float2 n = f2_unpack(near), far = f2_unpack(f2_sub(f2_all(1.f), e)), v = f2_unpack(u);
-  return f2_pack(v.x < kNear ? n.x : far.x, v.y < kNear ? n.y : far.y);
+  const float2 n = f2_unpack(near), l = f2_unpack(left), x = f2_unpack(e), far = f2_unpack(f2_sub(f2_all(1.f), e)),
+               v = f2_unpack(u);
+  return {f2_pack(v.x < kNear ? l.x : x.x, v.y < kNear ? l.y : x.y),
+          f2_pack(v.x < kNear ? n.x : far.x, v.y < kNear ? n.y : far.y)};
 }
 
-// 1 - lambda^2 = m (2 - m).
-__device__ __forceinline__ f2 one_minus_square2(f2 m) { return f2_mul(m, f2_sub(f2_all(2.f), m)); }
+// Both in one word per channel, the one that has more digits: m, or -lambda where u >= kNear.
+template <bool kSmall>
+__device__ __forceinline__ f2 fold2(f2 u, const Decay& d) {
+  if constexpr (kSmall) return d.m;
+  const float2 m = f2_unpack(d.m), l = f2_unpack(d.lambda), v = f2_unpack(u);
+  return f2_pack(v.x < kNear ? m.x : -l.x, v.y < kNear ? m.y : -l.y);
+}
+__device__ __forceinline__ Decay unfold2(f2 kept) {
+  const float2 t = f2_unpack(kept), o = make_float2(1.f - fabsf(t.x), 1.f - fabsf(t.y));
+  return {f2_pack(signbit(t.x) ? -t.x : o.x, signbit(t.y) ? -t.y : o.y),
+          f2_pack(signbit(t.x) ? o.x : t.x, signbit(t.y) ? o.y : t.y)};
+}
+
+// 1 - lambda^2 = m (1 + lambda).
+__device__ __forceinline__ f2 one_minus_square2(const Decay& d) { return f2_fma(d.m, d.lambda, d.m); }
 // w >= 0 kept from 0 (NaN too becomes kLeast).
 __device__ __forceinline__ f2 positive2(f2 w) {
   return f2_each(w, [](float v) { return fmaxf(v, kLeast); });

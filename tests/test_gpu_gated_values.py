@@ -1,10 +1,15 @@
-"""The gated recurrence on the GPU where its values are hard: NaN in one input.  Each
-kernel form is entered (whole sequences in a tile, chains, tiles, mixed rows, rows that are not 16-byte aligned)."""
+"""The gated recurrence on the GPU where its values are hard: NaN in one input and
+steep slopes.  Each kernel form is entered (whole sequences in a tile, chains, tiles,
+mixed rows, rows that are not 16-byte aligned).
+
+Tolerances are those computed beside the 64-bit reference (gated_reference.py) or, where a factor is
+small, derived here from the same roundings, relative to the value itself."""
 import numpy as np
 import pytest
 
 import linear_attention_prefill_chunkwise_gb300 as lap
-from test_gpu_gated import Batch
+from gated_reference import grad_one, scan_one
+from test_gpu_gated import Batch, f64, near
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -129,3 +134,63 @@ def test_other_requests_keep_their_bits_in_decode():
     o2 = lap.la_gated_decode(b.x, b.r, b.g, b.slopes, st2, T, state_indices=b.idx)
     o2[s], st2[slot] = o[s], st[slot]
     assert torch.equal(o2, o) and torch.equal(st2, st)
+
+
+# ---------------------------------------------------------------- steep slopes
+
+def steep(b, hi):
+    """Slopes from 2^-8 to `hi`, neighbours far apart."""
+    k = (np.arange(b.C) * 37) % b.C
+    b.slopes = torch.from_numpy((hi * np.exp2(-(8 + np.log2(hi)) * k / max(b.C - 1, 1))).astype(np.float32)).cuda()
+    return b
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_steep_slopes(form):
+    b = steep(Batch(45, **FORMS[form]), 64.0)
+    cols = slice(0, min(b.C, 72))
+    o, hf = b.fwd()
+    dout, dhf = b.mat(), b.state()
+    got = grads(b, o, dout, dh_final=dhf)
+    sums = esum = terms = 0.0
+    for n, L in enumerate(b.lens):
+        s, slot = b.rows(n), int(b.slots[n])
+        args = [f64(t[s, cols]) for t in (b.x, b.r, b.g)] + [f64(b.slopes[cols]), f64(b.h0[slot, cols])]
+        ro, rh, eo, eh = scan_one(*args)
+        near(o[s, cols], ro, eo, b.dtype, f"o of sequence {n} ({L} tokens)")
+        near(hf[slot, cols], rh, eh, "fp32", f"h_final of sequence {n} ({L} tokens)")
+        ref = grad_one(*args, f64(o[s, cols]), f64(dout[s, cols]), f64(dhf[slot, cols]))
+        for t, name in zip(got, ("dx", "dr", "dg")):
+            near(t[s, cols], *ref[name], b.dtype, f"{name} of sequence {n} ({L} tokens)")
+        near(got[4][slot, cols], *ref["dh0"], "fp32", f"dh0 of sequence {n} ({L} tokens)")
+        sums, esum, terms = sums + ref["ds"][0], esum + ref["ds"][1], terms + np.abs(ref["ds"][0])
+    near(got[3][cols], sums, esum + len(b.lens) * 2.0 ** -24 * terms, "fp32", "dslopes")
+
+
+def relative(got, ref, bound, label):
+    """As near, for FP32 values of any size: `bound` counts every rounding; results under the smallest
+    normal number (2^-126) may lose it."""
+    got = f64(got)
+    assert np.all(np.isfinite(got)), f"{label}: non-finite"
+    tol = bound + 2.0 ** -24 * (np.abs(ref) + bound) + 2.0 ** -125
+    worst = np.max(np.abs(got - ref) / tol)
+    assert worst <= 1, f"{label}: {worst:.3g} of its bound at {np.argmax(np.abs(got - ref) / tol)}"
+
+
+@pytest.mark.parametrize("T,C", [(1, 64), (3, 67), (5, 96)])
+def test_a_decayed_state_keeps_its_digits(T, C):
+    """Closed input gates: o is the state times the decays alone, exp(-u) of up to u = 16 a token."""
+    b = steep(Batch(46, lens=[T] * 9, C=C, dtype="fp32", packed=False), 16.0)
+    b.g[:] = float("-inf")
+    o, hf = b.fwd()
+    st = b.h0.clone()
+    od = lap.la_gated_decode(b.x, b.r, b.g, b.slopes, st, T)
+    dout = torch.zeros_like(o)
+    dh0 = torch.empty_like(b.h0)
+    lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, dout, h0=b.h0, dh_final=b.h0, dh0=dh0, seq_len=T)
+    for n in range(9):
+        s = b.rows(n)
+        ro, rh, eo, eh = scan_one(np.zeros((T, C)), f64(b.r[s]), np.zeros((T, C)), f64(b.slopes), f64(b.h0[n]))
+        for name, got, ref, e in (("o", o[s], ro, eo), ("h_final", hf[n], rh, eh), ("decode", od[s], ro, eo),
+                                  ("state", st[n], rh, eh), ("dh0", dh0[n], rh, eh)):
+            relative(got, ref, e, f"{name} of sequence {n}")
