@@ -13,6 +13,7 @@
  * r holds the decay gates' logits, g the input gates'; slopes >= 0 is expected (negative slopes
  * give unspecified values).  A gate logit of -inf is a closed gate: r = -inf keeps the state
  * unchanged and adds nothing (lambda = 1, beta = 0), g = -inf adds nothing for a finite x.
+ * (sig(z) under FP32's smallest normal number, z < -87.3, counts as 0.)
  * A NaN reaches every output that depends on it, and no other sequence, request or channel.
  * States and arithmetic are FP32; o is rounded once.
  *

@@ -80,13 +80,29 @@ __device__ __forceinline__ f2 f2_each(f2 v, F f) {
   return f2_pack(f(t.x), f(t.y));
 }
 
-// 1 + exp(-z): the reciprocal of sig(z); 1 at z = +inf, inf at -inf.
-__device__ __forceinline__ f2 inverse_sigmoid2(f2 z) {
-  const f2 e = f2_each(f2_mul(z, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
-  return f2_add(e, f2_all(1.f));
+__device__ __forceinline__ f2 exp_of2(f2 z) {
+  return f2_each(f2_mul(z, f2_all(kLog2e)), [](float v) { return ex2_approx(v); });
 }
+// 1 / (1 + exp(-z)): 1 at z = +inf, 0 at -inf.
 __device__ __forceinline__ f2 sigmoid2(f2 z) {
-  return f2_each(inverse_sigmoid2(z), [](float v) { return rcp_approx(v); });
+  const f2 e = f2_each(f2_mul(z, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
+  return f2_each(f2_add(e, f2_all(1.f)), [](float v) { return rcp_approx(v); });
+}
+
+// A logit from which on sig is 1 in FP32: exp(-40) is 2^-57.7; (1 + exp(40))^2 is 2^115.
+constexpr float kOpen = 40.f;
+__device__ __forceinline__ f2 at_most_open2(f2 z) {  // NaN stays
+  return f2_each(z, [](float v) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v), "f"(kOpen));
+    return d;
+  });
+}
+__device__ __forceinline__ uint32_t at_most_open_bf16x2(uint32_t z) {
+  const uint32_t open = __float_as_uint(kOpen) >> 16;  // kOpen is a BF16 number
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(z), "r"(open << 16 | open));
+  return d;
 }
 
 // lambda = exp(-u) of two channels, and m = 1 - lambda.  kSmall: u < kNear is known.

@@ -1,5 +1,5 @@
-"""The gated recurrence on the GPU where its values are hard: NaN in one input and
-steep slopes.  Each kernel form is entered (whole sequences in a tile, chains, tiles,
+"""The gated recurrence on the GPU where its values are hard: NaN in one input, steep slopes, gates
+far open and far closed.  Each kernel form is entered (whole sequences in a tile, chains, tiles,
 mixed rows, rows that are not 16-byte aligned).
 
 Tolerances are those computed beside the 64-bit reference (gated_reference.py) or, where a factor is
@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 import linear_attention_prefill_chunkwise_gb300 as lap
-from gated_reference import grad_one, scan_one
+from gated_reference import HALF_STEP, gate_errors, gates, grad_one, scan_one
 from test_gpu_gated import Batch, f64, near
 
 torch = pytest.importorskip("torch")
@@ -167,12 +167,12 @@ def test_steep_slopes(form):
     near(got[3][cols], sums, esum + len(b.lens) * 2.0 ** -24 * terms, "fp32", "dslopes")
 
 
-def relative(got, ref, bound, label):
-    """As near, for FP32 values of any size: `bound` counts every rounding; results under the smallest
-    normal number (2^-126) may lose it."""
+def relative(got, ref, bound, label, dtype="fp32"):
+    """As near, for values of any size: `bound` counts every rounding but the output's; results under the
+    smallest normal number (2^-126) may be lost."""
     got = f64(got)
     assert np.all(np.isfinite(got)), f"{label}: non-finite"
-    tol = bound + 2.0 ** -24 * (np.abs(ref) + bound) + 2.0 ** -125
+    tol = bound + HALF_STEP[dtype] * (np.abs(ref) + bound) + 2.0 ** -125
     worst = np.max(np.abs(got - ref) / tol)
     assert worst <= 1, f"{label}: {worst:.3g} of its bound at {np.argmax(np.abs(got - ref) / tol)}"
 
@@ -194,3 +194,24 @@ def test_a_decayed_state_keeps_its_digits(T, C):
         for name, got, ref, e in (("o", o[s], ro, eo), ("h_final", hf[n], rh, eh), ("decode", od[s], ro, eo),
                                   ("state", st[n], rh, eh), ("dh0", dh0[n], rh, eh)):
             relative(got, ref, e, f"{name} of sequence {n}")
+
+
+# ---------------------------------------------------------------- gates far open and far closed
+
+@pytest.mark.parametrize("dtype,C", [("fp32", 64), ("bf16", 64), ("fp32", 67), ("bf16", 67)])
+@pytest.mark.parametrize("lo,hi", [(-86, -44), (30, 100)])
+def test_an_input_gate_far_closed_or_open(lo, hi, dtype, C):
+    """sigmoid(g) down to exp(-86), and 1: o = beta sigmoid(g) x of one token, relative to itself."""
+    b = Batch(47, lens=[1] * 40, C=C, dtype=dtype, packed=False, states=False)
+    b.g = (lo + (hi - lo) * torch.from_numpy(b.rng.random((40, C))).cuda()).to(b.g.dtype)
+    if lo > 0:
+        b.g[::3] = float("inf")
+    o = lap.la_gated_scan_fwd(b.x, b.r, b.g, b.slopes, seq_len=1)
+    od = lap.la_gated_decode(b.x, b.r, b.g, b.slopes, torch.zeros(40, C, device="cuda"), 1)
+    dx = lap.la_gated_scan_bwd(b.x, b.r, b.g, b.slopes, o, b.x, seq_len=1)[0]
+    x, r, g = f64(b.x), f64(b.r), f64(b.g)
+    _, sg, u, _, beta = gates(x, r, g, f64(b.slopes))
+    _, eg, _, eb = gate_errors(r, g, u)
+    ref = beta * sg * x
+    for name, got in (("scan", o), ("decode", od), ("dx", dx)):  # dout = x: dx = beta sigmoid(g) x too
+        relative(got, ref, np.abs(ref) * (eb + eg + 2.0 ** -21), name, dtype)
