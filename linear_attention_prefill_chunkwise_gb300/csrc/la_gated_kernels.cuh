@@ -845,7 +845,7 @@ template <typename E, bool kTma, Mode kMode>
 struct Backward {
   using S = Shape<E, true, kTma, kMode>;
   static constexpr int K = S::kRows;
-  f2 sr[K], kept[K];  // sig(r) and the decay, folded; row k in walking order is row K - 1 - k of the stage
+  f2 er[K], kept[K];  // exp(-r) and the decay, folded; row k in walking order is row K - 1 - k of the stage
 
   template <bool kEdges, bool kSmall, typename F>
   __device__ __forceinline__ Run first(const Params<E>& p, const char* stage, int low, f2 slope, const Rows& rows,
@@ -855,8 +855,8 @@ struct Backward {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (k == S::kAsk) ask();
-      sr[k] = sigmoid2(r.get(K - 1 - k));
-      const f2 u = f2_mul(slope, sr[k]);
+      er[k] = exp_minus2(r.get(K - 1 - k));
+      const f2 u = f2_mul(slope, sigmoid_of2(er[k]));
       const Decay decay = decay2<kSmall>(u);
       const f2 a = decay.lambda;
       kept[k] = fold2<kSmall>(u, decay);
@@ -880,7 +880,6 @@ struct Backward {
 #pragma unroll
     for (int i = 0; i < 3; ++i) out[i] = p.out[i] + static_cast<int64_t>(low + K) * p.ld_out[i] + l.c[0];
     f2 sum = f2_all(0.f);
-    const f2 one = f2_all(1.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int at = K - 1 - k;
@@ -893,21 +892,21 @@ struct Backward {
         if (rows.begin >> k & 1u) w = load_state(p.start, slot, p.C, l);
         if (rows.end >> k & 1u) before = load_state(p.h0, slot, p.C, l);
       }
-      const f2 G = f2_add(d.get(at), w), vx = x.get(at), sg = sigmoid2(g.get(at)), u = f2_mul(slope, sr[k]);
+      const f2 G = f2_add(d.get(at), w), vx = x.get(at);
+      const Gate in = gate_of2(exp_minus2(g.get(at))), out_of = gate_of2(er[k]);
       const Decay decay = unfold2(kept[k]);
       const f2 lambda = decay.lambda, beta2 = one_minus_square2(decay);
-      f2 inv = rsqrt2(positive2(beta2));
-      const f2 beta = f2_mul(beta2, inv);
-      const float2 vu = f2_unpack(u), vi = f2_unpack(inv);
-      inv = f2_pack(vu.x > 0.f ? vi.x : 0.f, vu.y > 0.f ? vi.y : 0.f);
-      const f2 gs = f2_mul(G, sg), dx = f2_mul(gs, beta);
+      // 1 / beta, and beta, are 0 where u = 0 (or beta^2 is under the smallest normal number)
+      const float2 vb = f2_unpack(beta2), vi = f2_unpack(rsqrt2(beta2));
+      const f2 inv = f2_pack(vb.x >= kLeast ? vi.x : 0.f, vb.y >= kLeast ? vi.y : 0.f), beta = f2_mul(beta2, inv);
+      const f2 gs = f2_mul(G, in.open), dx = f2_mul(gs, beta);
       store2(out[0], l, dx);
-      store2(out[2], l, f2_mul(f2_mul(dx, vx), f2_sub(one, sg)));
-      // du = lambda (gs x lambda / beta - G h_{t-1})
+      store2(out[2], l, f2_mul(f2_mul(dx, vx), in.rest));
+      // du = lambda (gs x lambda / beta - G h_{t-1}); ds = du sig(r); with u = slope sig(r), dr = ds slope (1 - sig(r))
       const f2 t = f2_mul(f2_mul(gs, vx), f2_mul(lambda, inv));
-      const f2 du = f2_mul(lambda, f2_sub(t, f2_mul(G, before)));
-      store2(out[1], l, f2_mul(f2_mul(du, u), f2_sub(one, sr[k])));
-      sum = f2_fma(du, sr[k], sum);
+      const f2 ds = f2_mul(f2_mul(lambda, f2_sub(t, f2_mul(G, before))), out_of.open);
+      store2(out[1], l, f2_mul(ds, f2_mul(slope, out_of.rest)));
+      sum = f2_add(sum, ds);
       w = f2_mul(lambda, G);
       if constexpr (kEdges) {
         if (p.finish && (rows.end >> k & 1u)) store_state(p.finish, __shfl_sync(0xFFFFFFFFu, rows.slot, k), p.C, l, w);

@@ -83,10 +83,25 @@ __device__ __forceinline__ f2 f2_each(f2 v, F f) {
 __device__ __forceinline__ f2 exp_of2(f2 z) {
   return f2_each(f2_mul(z, f2_all(kLog2e)), [](float v) { return ex2_approx(v); });
 }
-// 1 / (1 + exp(-z)): 1 at z = +inf, 0 at -inf.
-__device__ __forceinline__ f2 sigmoid2(f2 z) {
-  const f2 e = f2_each(f2_mul(z, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
+__device__ __forceinline__ f2 exp_minus2(f2 z) {
+  return f2_each(f2_mul(z, f2_all(-kLog2e)), [](float v) { return ex2_approx(v); });
+}
+// sig(z) from e = exp(-z): 1 at z = +inf, 0 at -inf.
+__device__ __forceinline__ f2 sigmoid_of2(f2 e) {
   return f2_each(f2_add(e, f2_all(1.f)), [](float v) { return rcp_approx(v); });
+}
+__device__ __forceinline__ f2 sigmoid2(f2 z) { return sigmoid_of2(exp_minus2(z)); }
+// sig(z) and 1 - sig(z) from e = exp(-z), the latter as e sig(z), so that a gate far open keeps the digits
+// of what is left (1 minus a rounded sigmoid is off by 5e-4 of itself at z = 10, and 0 from 17 on).  Where e
+// has overflowed, e sig(z) is inf * 0, which the saturating product turns into 0: there `rest` only
+// stands in products with `open` = 0.  NaN stays in `open`.
+struct Gate {
+  f2 open, rest;
+};
+__device__ __forceinline__ Gate gate_of2(f2 e) {
+  const f2 open = sigmoid_of2(e);
+  const float2 v = f2_unpack(e), s = f2_unpack(open);
+  return {open, f2_pack(__saturatef(v.x * s.x), __saturatef(v.y * s.y))};
 }
 
 // A logit from which on sig is 1 in FP32: exp(-40) is 2^-57.7; (1 + exp(40))^2 is 2^115.

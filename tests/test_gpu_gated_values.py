@@ -215,3 +215,42 @@ def test_an_input_gate_far_closed_or_open(lo, hi, dtype, C):
     ref = beta * sg * x
     for name, got in (("scan", o), ("decode", od), ("dx", dx)):  # dout = x: dx = beta sigmoid(g) x too
         relative(got, ref, np.abs(ref) * (eb + eg + 2.0 ** -21), name, dtype)
+
+
+def complement(z):
+    """1 - sigmoid(z) and its error: exp(-z) / (1 + exp(-z)) from the argument's rounding |z| 2^-23, exp2
+    and the reciprocal (2^-22 each), a sum and a product."""
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, e / (1 + e), 1 / (1 + e)), 2.0 ** -20 + np.abs(z) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("C", [64, 67])
+@pytest.mark.parametrize("lo,hi,slope", [(-4, 4, 1.0), (8, 20, 1.0), (20, 80, 1.0), (-80, -8, 1.0), (-4, 4, 20.0),
+                                         (8, 20, 20.0)])
+def test_gradients_are_relative_to_their_factors(lo, hi, slope, C):
+    """One token: dg = dx x (1 - sigmoid(g)) and dr = du u (1 - sigmoid(r)) keep their digits however far
+    the gates are open, and du those of lambda however steep the slopes."""
+    b = steep(Batch(48, lens=[1] * 30, C=C, dtype="fp32", packed=False), slope)
+    gen = torch.Generator(device="cuda").manual_seed(48)
+    for t in (b.r, b.g):
+        t.copy_(lo + (hi - lo) * torch.rand(t.shape, generator=gen, device="cuda"))
+    o, _ = b.fwd()
+    dout = b.mat()
+    dx, dr, dg, ds, dh0 = grads(b, o, dout)
+    x, r, g, h, G = (f64(t) for t in (b.x, b.r, b.g, b.h0, dout))
+    sr, sg, u, lam, beta = gates(x, r, g, f64(b.slopes))
+    er, eg, d, eb = gate_errors(r, g, u)
+    (cg, ecg), (cr, ecr) = complement(g), complement(r)
+    rdx = G * beta * sg
+    edx = np.abs(rdx) * (eb + eg + 2.0 ** -21)
+    relative(dx, rdx, edx, "dx")
+    rdg = rdx * x * cg
+    relative(dg, rdg, np.abs(rdg) * (eb + eg + ecg + 2.0 ** -20), "dg")
+    a1, a2 = sg * x * lam * lam / beta, lam * h
+    du, size = G * (a1 - a2), np.abs(G) * (np.abs(a1) + np.abs(a2))
+    edu = size * (eb + eg + 2 * d + 2.0 ** -20)
+    rdr = du * u * cr
+    relative(dr, rdr, edu * u * cr + np.abs(rdr) * (er + ecr + 2.0 ** -21), "dr")
+    relative(dh0, lam * G, np.abs(lam * G) * (d + 2.0 ** -23), "dh0")
+    terms, eterms = du * sr, edu * sr + np.abs(du * sr) * (er + 2.0 ** -22)
+    relative(ds, terms.sum(0), eterms.sum(0) + 30 * 2.0 ** -24 * np.abs(terms).sum(0), "dslopes")
