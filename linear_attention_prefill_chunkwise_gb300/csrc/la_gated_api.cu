@@ -152,8 +152,10 @@ la_status check_sizes(int B, int T, int N, int C, bool packed, la_dtype dtype) {
   }
   if (static_cast<int64_t>(B) * T > la_host::kMaxRows)
     return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)B * T);
-  // tiles of at least 16 rows and 64 channels, numbered below 2^30 (more than any memory holds)
-  if ((static_cast<int64_t>(B) * T / 16 + lag::kMostListed) * ((C + 63) / 64) >= int64_t(1) << 30)
+  // Tiles times columns stay below 2^30 (more than any memory holds), the ticket of a packed batch whose
+  // cu_seqlens is refused.  The smallest tiles hold 24 rows (FP32 gradients, unaligned); a packed batch
+  // has one more per listed sequence, and a fixed one's hold 12 rows at least on average (T = 25: two).
+  if ((static_cast<int64_t>(B) * T / 12 + lag::kMostListed) * ((C + 63) / 64) >= int64_t(1) << 30)
     return fail(LA_ERR_UNSUPPORTED, "B*T*C too large");
   if (static_cast<int64_t>(N) * ((C + 63) / 64) > INT32_MAX) return fail(LA_ERR_UNSUPPORTED, "N*C too large");
   return LA_OK;
