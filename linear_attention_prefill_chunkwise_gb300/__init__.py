@@ -527,7 +527,7 @@ def _matrix(t, name):
 
 def _stride(t, name, rows, C):
     s0, s1 = t.stride()
-    if s1 == 1 and s0 >= C:
+    if (s1 == 1 or C == 1) and s0 >= C:  # one column has no neighbour
         return s0
     if s1 != 1 and C > 1 and rows > 0:
         raise ValueError(f"the columns of {name} must be contiguous")

@@ -18,3 +18,18 @@ def test_tiles_times_columns_stay_below_two_to_the_thirty(T):
         lap.la_gated_scan_workspace(most + 1, T, most + 1, 64 * columns, False, torch.float32, True)
     assert e.value.status == UNSUPPORTED
     assert lap.la_gated_scan_workspace(most // 3, T, most // 3, 64 * columns, False, torch.float32, True) > 0
+
+
+@pytest.mark.parametrize("t,stride", [(torch.zeros(1, 8).t(), 1), (torch.zeros(3, 8).t()[:, 1:2], 1),
+                                      (torch.zeros(8, 5)[:, 2:3], 5), (torch.zeros(8, 2, 3)[:, :, 1][:, :1], 6),
+                                      (torch.zeros(6).expand(1, 6), 6), (torch.zeros(0, 4), 4)])
+def test_row_strides_of_single_columns_and_rows(t, stride):
+    """A single column may have any column stride."""
+    assert lap._stride(t, "x", *t.shape) == stride
+
+
+@pytest.mark.parametrize("t", [torch.zeros(8, 1).expand(8, 4), torch.zeros(1).expand(8, 1), torch.zeros(4, 8).t(),
+                               torch.zeros(8).expand(4, 8)])
+def test_other_strides_are_refused(t):
+    with pytest.raises(ValueError, match="x"):
+        lap._stride(t, "x", *t.shape)

@@ -254,3 +254,26 @@ def test_gradients_are_relative_to_their_factors(lo, hi, slope, C):
     relative(dh0, lam * G, np.abs(lam * G) * (d + 2.0 ** -23), "dh0")
     terms, eterms = du * sr, edu * sr + np.abs(du * sr) * (er + 2.0 ** -22)
     relative(ds, terms.sum(0), eterms.sum(0) + 30 * 2.0 ** -24 * np.abs(terms).sum(0), "dslopes")
+
+
+# ---------------------------------------------------------------- a single column
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_single_column_of_any_stride(dtype):
+    """[rows, 1] tensors whose column stride is not 1, from a transposed or a wider matrix."""
+    gen = torch.Generator(device="cuda").manual_seed(49)
+    wide = torch.randn((7, 300), generator=gen, device="cuda").to(dtype)
+    cols = [wide[k:k + 1].t() for k in range(5)]  # strides (1, 300)
+    slopes = torch.tensor([0.3], device="cuda")
+    x, r, g, d, y = cols
+    o = lap.la_gated_scan_fwd(x, r, g, slopes, seq_len=300)
+    got = lap.la_gated_scan_bwd(x, r, g, slopes, o, d, seq_len=300)
+    want = [t.contiguous(memory_format=torch.contiguous_format).clone().reshape(300, 1) for t in cols]
+    x, r, g, d, y = want
+    ref = lap.la_gated_scan_fwd(x, r, g, slopes, seq_len=300)
+    assert torch.equal(o, ref)
+    for a, b in zip(got[:4], lap.la_gated_scan_bwd(x, r, g, slopes, ref, d, seq_len=300)[:4]):
+        assert torch.equal(a, b)
+    w = torch.tensor([1.5], device="cuda")
+    for a, b in zip(lap.la_rms_norm_fwd(cols[4], w, 1e-5, residual=cols[0]), lap.la_rms_norm_fwd(y, w, 1e-5, residual=x)):
+        assert torch.equal(a, b)
