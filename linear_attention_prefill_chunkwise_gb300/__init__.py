@@ -639,10 +639,12 @@ def la_gated_scan_workspace(B, T, N, C, packed, dtype, backward):
     """Bytes of device workspace la_gated_scan_fwd / la_gated_scan_bwd (``backward``) needs for
     these sizes; dtype is torch.bfloat16 or torch.float32."""
     import torch
+    code = {torch.bfloat16: 0, torch.float32: 1}.get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     lib = load_library()
     nbytes = ctypes.c_size_t(0)
-    st = lib.la_gated_scan_workspace(int(B), int(T), int(N), int(C), int(bool(packed)),
-                                     {torch.bfloat16: 0, torch.float32: 1}[dtype], int(bool(backward)),
+    st = lib.la_gated_scan_workspace(int(B), int(T), int(N), int(C), int(bool(packed)), code, int(bool(backward)),
                                      ctypes.byref(nbytes))
     if st != 0:
         _raise(lib, st)

@@ -33,3 +33,9 @@ def test_row_strides_of_single_columns_and_rows(t, stride):
 def test_other_strides_are_refused(t):
     with pytest.raises(ValueError, match="x"):
         lap._stride(t, "x", *t.shape)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, "bf16", None])
+def test_workspace_of_an_unknown_type_is_refused(dtype):
+    with pytest.raises(TypeError, match="bfloat16 or torch.float32"):
+        lap.la_gated_scan_workspace(1, 600, 3, 64, True, dtype, True)
