@@ -14,8 +14,10 @@
  * 8-bit output (la_rms_norm_fwd_fp8): y is stored as e4m3 values q with FP32 scales such that
  * y ~ q * scale, one scale per row (group = 0) or per 128 columns (group = 128; the last group
  * of a row may be shorter):
- *     scale = max(max|y|, 2^-40) / 448,      q = y / scale rounded to nearest even, clamped to
- *                                            +-448
+ *     top = max(max|y|, 2^-40),      scale = top / 448,      q = y * (448 / top) rounded to
+ *                                            nearest even, clamped to +-448
+ * each quotient and product rounded to FP32.  So q is y / scale but for 3 * 2^-24 of it, which
+ * decides where y / scale lies that near to the middle between two e4m3 numbers.
  * A NaN in y is stored as NaN and does not enter its group's maximum.
  *
  * Layouts: x, residual, residual_out, y, dy, dres, dx [rows, C], innermost contiguous, each with
