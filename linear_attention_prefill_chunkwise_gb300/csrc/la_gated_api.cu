@@ -39,18 +39,19 @@ constexpr int kSlots = 152 * 2;
 // half a group of published runs.  `streams`: the sequences' columns, so kSlots / streams tiles of one
 // are computed at once.  Many streams hide the steps, and a run per warp costs nothing; few want whole
 // rounds of blocks in one group.  BF16 forward of one sequence, groups of 8, 40, 56, 96, 128 tiles:
-// 512 channels 420, 372, 362, 354, 351 us; 1024: 371, 317, 313, 311, 314; 2048: 297, 278, 279, 288,
-// 297; 4096: 239, 250, 257, 270, 283.
+// 512 channels 455, 374, 361, 350, 344 us; 1024: 367, 319, 312, 310, 314; 2048: 303, 279, 278, 289,
+// 296; 4096: 240, 250, 255, 268, 282.
 int group_of(int64_t streams, int warps) {
   const int64_t wide = 4 * kSlots / streams;
   return wide < 24 ? warps : wide < 160 ? static_cast<int>(wide) : 160;
 }
 
 // Whether blocks take whole chains (a sequence's channels).  Sequences of one length: for short
-// chains, which need no plan kernel, and where the chains fill the device evenly enough.  8192
-// channels, by chains and by tiles: 2 x 8192 tokens, 256 chains, 194 and 197 us (gradients 368 and
-// 374); with 7168 channels, 224 chains, 206 and 175 (368 and 331); 3 x 4096 tokens, 384 chains, 172
-// and 149 (305 and 282).
+// chains, which need no plan kernel, and where the chains fill the device evenly enough.  2 x 8192
+// tokens, BF16, by chains and by tiles: 8704 channels, 272 chains, 205 and 215 us (gradients 390 and 403);
+// 8192, 256 chains, 195 and 203 (389 and 380); 7168, 224 chains, 205 and 180 (385 and 336); 3 x 4096
+// tokens of 8192 channels, 384 chains, 170 and 154 (306 and 288).  FP32 rows gain less by chains (2 x
+// 4096 tokens, 8192 channels 172 and 163, 366 and 338).
 bool by_chains(int64_t chains, int per) {
   const int64_t waves = (chains + kSlots - 1) / kSlots;
   return per <= 4 || chains * 100 >= waves * kSlots * 80;
@@ -58,24 +59,26 @@ bool by_chains(int64_t chains, int per) {
 // Packed: by chains where there are enough of them to fill the device evenly and the sequences are
 // not mostly shorter than half a tile.  By chains, in tiles of one sequence each, and in tiles of
 // mixed rows, forward, us: 32 sequences of up to 4096 tokens, 4096 channels, 2048 chains: 327, 404,
-// 532; 640 chains: 218, 239, 467 (40 sequences of up to 8192 tokens, 1024 channels), uneven ones 405,
-// 238 (20 of 50 to 16384 tokens, 2048 channels); 16 of up to 8192 tokens, 1024 channels, 256 chains:
-// 193, 120, 214.  2048 channels, 38400 tokens: 200 sequences 197, 326, 421; 600 249, 428, 246; 1200
-// 499, 837, 250.
+// 514; 640 chains: 223, 233, 392 (40 sequences of up to 8192 tokens, 1024 channels), uneven ones 415,
+// 238, 334 (20 of 50 to 16384 tokens, 2048 channels); 16 of up to 8192 tokens, 1024 channels, 256
+// chains: 196, 122, 186.  2048 channels, 38400 tokens (the bytes are 93): 200 sequences 136, 196, 257; 600
+// 211, 284, 239; 1200 417, 532, 246 (gradients, 185: 229, 317, 490; 308, 405, 492; 437, 542, 449).  By chains,
+// warps past a sequence's end load and compute rows that nobody uses; in mixed tiles every lane searches
+// cu_seqlens, for each of the columns anew.
 bool packed_by_chains(int64_t tokens, int N, int columns, int stride) {
   return static_cast<int64_t>(N) * columns >= 3 * kSlots && tokens * 2 >= static_cast<int64_t>(N) * stride;
 }
 // A batch by chains takes sequences much longer than a block's share of the rows by tiles, in a launch
-// of its own behind.  One sequence of 32768 tokens among 100 of 330 on average, 4096 channels: 448 us,
-// all by chains 777 (gradients 816, 1469); one of 100000, 512 channels: 195 and 2212.  Without such
-// sequences the launch costs 3 us.
+// of its own behind.  One sequence of 32768 tokens among 100 of 330 on average, 4096 channels: 453 us,
+// all by chains 800 (gradients 811, 1532); one of 100000, 512 channels: 200 and 2316.  Without such
+// sequences the launch costs 3 to 5 us.
 int longest_chain(int64_t tokens, int columns, int stride) {
   const int64_t share = tokens * columns / kSlots;
   return static_cast<int>(std::min<int64_t>(std::max<int64_t>(share + share / 4, 4 * stride), INT32_MAX - 1));
 }
-// Else in tiles of one sequence each, where those are not mostly single tiles (2048 channels, 300
-// sequences of up to 256 tokens, two tiles of 128 rows or four of 72: forward 296 and 269 in mixed
-// ones, gradients 412 and 546).
+// Else in tiles of one sequence each, where those are not mostly single tiles.  128 channels, 400
+// sequences of up to 128, 256, 384 and 512 tokens, tiles of 128 rows forward and 72 back: in tiles of
+// one sequence 51, 51, 57, 70 us, in mixed ones 23, 32, 43, 59; gradients 48, 58, 72, 84 and 35, 56, 82, 108.
 bool packed_by_tiles(int64_t tokens, int N, int stride) { return tokens * 2 >= static_cast<int64_t>(N) * stride * 3; }
 
 template <typename E, bool kBack, bool kTma>

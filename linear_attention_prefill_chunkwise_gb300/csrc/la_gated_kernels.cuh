@@ -12,11 +12,12 @@
 // loads.  A warp composes its rows, the block its warps; once the state before the tile is known,
 // each warp walks its rows again (forward: from a and b in registers) and writes the outputs: every
 // input is read once and every output written once.  What bounds it is the bytes, then the
-// instructions: a row of 64 channels takes a warp 59 forward and 128 for the gradients (unaligned:
-// 204), at 0.61 - 0.67 of the issue slots.  Measured, BF16, of the bytes at the copy rate: 2 x 8192
-// tokens of 8192 channels 188 us (0.84), gradients 362 (0.87); 32 packed sequences of up to 4096
-// tokens of 4096 channels 301 (0.94); one sequence of 32768 x 4096 232 (0.68), of 131072 x 1024 314
-// (0.50: the states' way from block to block); FP32 8192 x 8192 173 (0.92).
+// instructions: a row of 64 channels takes a warp 62 forward and 126 for the gradients by chains (0.60
+// and 0.63 of the issue slots), 74 forward by tiles (0.51), 207 for unaligned gradients (0.51).
+// Measured, BF16, of the bytes at the copy rate: 2 x 8192 tokens of 8192 channels 195 us (0.81),
+// gradients 389 (0.81; 19 x 1024 tokens 398, 0.94); 32 packed sequences of up to 4096 tokens of 4096
+// channels 303 (0.93); one sequence of 32768 x 4096 240 (0.66), of 131072 x 1024 313 (0.51: the states'
+// way from block to block); FP32 8192 x 8192 174 (0.91).
 //
 // Where the state before a tile comes from (Mode):
 // By chains, from the block itself, which walks all tiles of a sequence's channels: nothing waits.
@@ -54,8 +55,8 @@ constexpr int kMaxInputs = 5;   // x, r, g; backward: dout and o (one row up: h_
 constexpr int kStages = 2;
 
 // How blocks take their work; each is a kernel of its own, since the loop is held up by its own
-// instructions and registers (2 x 8192 tokens x 8192 channels by chains, one kernel for all and this:
-// forward 216 and 197 us, gradients 425 and 385).
+// instructions and registers (2 x 8192 tokens x 8192 channels by chains, one kernel for all was slower
+// by a tenth, when the kernels were split: 1.18 stalls per issue for missing instructions, now 0.13).
 enum Mode {
   kByChains,  // one block walks all tiles of a sequence's channels
   kByTiles,   // tiles of one sequence each, states from block to block
@@ -67,11 +68,13 @@ enum Mode {
 // channels touch, one chunk more than the channels fill.
 // Rows per warp: as many as two blocks' registers (forward: a and b of each) and shared memory hold,
 // since every tile costs the same few hundred instructions; more of them spill, or leave the copies
-// no cache.  BF16, 2 x 8192 tokens of 8192 channels: forward 16 rows 188 us, 14 202, 12 212.
-// Gradients by chains 8 rows 362, 9 355, but of 32 x 1024 tokens of 4096 channels 357 and 391; by tiles
-// (32768 tokens of 4096 channels) 10 rows 525, 9 433, 8 468.  Unaligned, 32 sequences of up to 4096
-// tokens of 1001 channels: forward 15 rows 241, 14 187, 12 180; gradients 8 rows 403, 7 363, 6 363.
-// FP32, 8192 tokens of 4096 channels: gradients 5 rows 231, 4 212, 3 254.
+// no cache.  BF16, 2 x 8192 tokens of 8192 channels: forward 18 rows 233 us, 16 195, 14 207, 12 210.
+// Gradients by chains 9 rows 380, 8 388, 7 407, and of 32 x 1024 tokens of 4096 channels 365, 346, 358;
+// by tiles (32768 tokens of 4096 channels) 10 rows 537, 9 451, 8 474.  Unaligned, 32 sequences of up to
+// 4096 tokens of 1001 channels: forward 14 rows 178, 12 171, 11 174, 10 180; gradients 9 rows 444, 8 318,
+// 7 329, 6 341, but of 600 sequences of up to 128 tokens of 2047 channels 493, 487, 476, 460.
+// FP32, 8192 tokens of 4096 channels: gradients by tiles 5 rows 229, 4 212, 3 253; by chains (2 x 4096
+// tokens of 8192 channels) 4 rows 367.
 template <typename E, bool kBack, bool kTma, Mode kMode>
 struct Shape {
   static constexpr int kWarps = 8;
@@ -146,8 +149,8 @@ __device__ __forceinline__ void report(int* dev_error, unsigned bit) {
 // after its first row; y, whether all its rows lie inside one running sequence, away from its ends.
 // By chains, it orders the running sequences, longest first (ties by number); by tiles, it lists the
 // running sequences' tiles: the first of each, longest sequence first, then the second of each, ...
-// A warp compares a sequence or a tile with all sequences (a thread for each: 118 us for 4000 sequences;
-// that call 551 us instead of 705, 32 sequences of 1001 channels 169 instead of 182).
+// A warp compares a sequence or a tile with all sequences (a thread for each took 118 us for 4000
+// sequences, and a fifth of such a call more).
 template <typename E>
 __global__ void __launch_bounds__(kThreads) scan_plan_kernel(const Params<E> p) {
   __shared__ unsigned long long sums[2];  // tiles and groups of the table
@@ -668,7 +671,8 @@ struct Needs {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  // ... and notes what has not come.
+  // ... and notes what has not come.  (Without TMA the next tile's rows, asked for before the words, are
+  // waited for too.)
   template <typename X>
   __device__ __forceinline__ void look(X& ex, const Tile& q, int warp, int lane) const {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -1124,7 +1128,8 @@ __global__ void __launch_bounds__(Shape<E, kBack, kTma, kMode>::kThreads, Shape<
         begins = rows.begin;
         run = f.template first<true, false>(p, stage, low, slope, rows, l, lane, ask);
       } else {
-        // as forward; 600 sequences of up to 128 tokens, 2048 channels: 301 us, 326 without
+        // as forward; 600 sequences of up to 128 tokens, 2048 channels: 314 us, 321 without (2 x 8192
+        // tokens of 8192 channels 388 and 383, 32768 of 4096 450 and 453)
         const float2 s = f2_unpack(slope);
         if (kMode != kMixed && __all_sync(0xFFFFFFFFu, s.x < kNear && s.y < kNear))
           run = f.template first<false, true>(p, stage, low, slope, Rows{}, l, lane, ask);
@@ -1235,10 +1240,11 @@ __device__ __forceinline__ void store_chunk(E* row, int c, bool second, const f2
 }
 
 // Each thread walks a request's tokens for its channels.  The states are read and written once; many
-// threads with the loads of kAhead tokens in flight each keep the memory busy.  Bound by the bytes:
-// BF16 requests of 8192 channels, 128 x 1 token 4.8 us, 128 x 8 14.0 (0.79 of the copy rate),
-// 4096 x 8 of 4096 channels 184 (0.97); with 4 tokens ahead and 8 blocks per SM 5.7, 13.6, 194; with
-// 8 ahead 13.5, 24.9, 303.
+// threads with the loads of kAhead tokens in flight each keep the memory busy.  The next tokens' loads
+// are issued once these are computed, so where few requests leave the memory idle (128 x 8: 0.77 of the
+// copy rate) it is their latency that bounds.  BF16 requests of 8192 channels, 128 x 1 token 4.8 us,
+// 128 x 8 14.5 (verify 14.5; commit of 0 to 8 tokens 10.0), 4096 x 8 of 4096 channels 188 (0.95); with 4
+// tokens ahead and 8 blocks per SM 5.1, 13.8, 189; with 8 ahead (registers spill) 20, 40, 487.
 template <typename E, int kVec>
 __global__ void __launch_bounds__(kThreads, 12) gated_decode_kernel(const Params<E> p) {
   using Q = Chunk<E, kVec>;
