@@ -93,9 +93,9 @@ la_status la_gated_scan_fwd(const void* x, const void* r, const void* g, const f
  *
  * o is the forward's output, which holds h_{t-1} for every token but the first (that one's is
  * h0's).  The term lambda^2 / beta is taken as 0 where u_t = 0 (or beta_t^2 is under FP32's smallest
- * normal number).  dslopes sums the sequences that run, in a fixed order, and is written (0) when there are none; rows of padded sequences and
- * unselected slots are not written.  dh0 nullable (not computed).  The gradients' row strides
- * are lddx, lddr, lddg.
+ * normal number).  dslopes sums the sequences that run, in a fixed order, and is written (0) when there
+ * are none; rows of padded sequences and unselected slots are not written.  dh0 nullable (not
+ * computed).  The gradients' row strides are lddx, lddr, lddg.
  */
 la_status la_gated_scan_bwd(const void* x, const void* r, const void* g, const float* slopes, const float* h0,
                             const void* o, const void* dout, const float* dh_final, const int32_t* state_indices,
