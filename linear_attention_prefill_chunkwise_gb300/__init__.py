@@ -1,13 +1,15 @@
 """GB300 (sm_103a) Lightning Attention chunkwise prefill and speculative-decoding ops, and the
-gated linear recurrence and RMS norm beside them.
+gated linear recurrence, the RMS norm and a hybrid model's softmax attention beside them.
 
 ``la_prefill_fwd`` (include/la_prefill.h), ``la_prefill_bwd`` (include/la_backward.h),
 ``la_prefill_fwd_segmented``,
 ``la_prefill_fwd_segmented_static`` and ``la_prefill_segmented_workspace``
 (include/la_segment.h) and ``la_decode_mtp``,
 ``la_verify``, ``la_commit`` (include/la_decode.h), ``la_gated_scan_fwd``, ``la_gated_scan_bwd``,
-``la_gated_decode``, ``la_gated_verify``, ``la_gated_commit`` (include/la_gated.h) and
-``la_rms_norm_fwd``, ``la_rms_norm_fwd_fp8``, ``la_rms_norm_bwd`` (include/la_norm.h) are thin ctypes bindings of the C
+``la_gated_decode``, ``la_gated_verify``, ``la_gated_commit`` (include/la_gated.h),
+``la_rms_norm_fwd``, ``la_rms_norm_fwd_fp8``, ``la_rms_norm_bwd`` (include/la_norm.h),
+``la_qk_norm_rope_fwd``, ``la_qk_norm_rope_bwd`` (include/la_rotary.h) and ``la_attn_prefill_fwd``,
+``la_attn_prefill_bwd``, ``la_attn_verify``, ``la_attn_commit`` (include/la_attention.h) are thin ctypes bindings of the C
 entry points of the same names: they check dtypes and shapes of torch tensors, pass their device
 pointers and the current CUDA stream, and raise on a non-OK status.  Every step of the
 computation runs in the library's CUDA kernels; there is no other implementation in
@@ -28,6 +30,9 @@ __all__ = ["la_prefill_fwd", "la_prefill_fwd_segmented", "la_prefill_fwd_segment
            "la_prefill_segmented_workspace", "la_decode_mtp", "la_verify", "la_commit",
            "la_gated_scan_fwd", "la_gated_scan_bwd", "la_gated_scan_workspace", "la_gated_decode", "la_gated_verify",
            "la_gated_commit", "la_rms_norm_fwd", "la_rms_norm_fwd_fp8", "la_rms_norm_bwd", "la_rms_norm_bwd_workspace",
+           "la_qk_norm_rope_fwd", "la_qk_norm_rope_bwd", "la_qk_norm_rope_bwd_workspace", "la_attn_prefill_fwd",
+           "la_attn_prefill_bwd", "la_attn_prefill_bwd_workspace", "la_attn_verify", "la_attn_verify_workspace",
+           "la_attn_commit",
            "LaError", "load_library", "SCHEDULES", "DEV_ERR_BAD_SEQLENS",
            "DEV_ERR_BAD_INDEX", "DEV_ERR_TIMEOUT", "EXPORTED_SYMBOLS"]
 
@@ -42,7 +47,10 @@ EXPORTED_SYMBOLS = ("la_prefill_fwd", "la_status_string", "la_last_error", "la_p
                     "la_prefill_d256_workspace", "la_prefill_fwd_d256", "la_prefill_d256_segmented_workspace",
                     "la_prefill_fwd_d256_segmented", "la_gated_scan_workspace", "la_gated_scan_fwd", "la_gated_scan_bwd",
                     "la_gated_decode", "la_gated_verify", "la_gated_commit", "la_rms_norm_fwd", "la_rms_norm_fwd_fp8",
-                    "la_rms_norm_bwd_workspace", "la_rms_norm_bwd")
+                    "la_rms_norm_bwd_workspace", "la_rms_norm_bwd", "la_qk_norm_rope_fwd",
+                    "la_qk_norm_rope_bwd_workspace", "la_qk_norm_rope_bwd", "la_attn_prefill_fwd",
+                    "la_attn_prefill_bwd_workspace", "la_attn_prefill_bwd", "la_attn_verify_workspace", "la_attn_verify",
+                    "la_attn_commit")
 
 _lock = threading.Lock()
 _lib = None
@@ -120,9 +128,24 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
             lib.la_rms_norm_bwd_workspace.argtypes = [i32] * 2 + [vp]
             lib.la_rms_norm_bwd.argtypes = [vp] * 2 + [ctypes.c_float] + [vp] * 4 + [i64] * 4 + [i32] * 3 + \
                 [vp, ctypes.c_size_t, vp, vp]
+            lib.la_qk_norm_rope_fwd.argtypes = [vp] * 4 + [ctypes.c_float] + [vp] * 4 + [i64] * 8 + [i32] * 7 + [vp]
+            lib.la_qk_norm_rope_bwd_workspace.argtypes = [i32] * 4 + [vp]
+            lib.la_qk_norm_rope_bwd.argtypes = [vp] * 4 + [ctypes.c_float] + [vp] * 8 + [i64] * 12 + [i32] * 7 + \
+                [vp, ctypes.c_size_t, vp]
+            lib.la_attn_prefill_fwd.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 3 + [i64] * 8 + [i32] * 6 + [vp] * 2
+            lib.la_attn_prefill_bwd_workspace.argtypes = [i32] * 3 + [vp]
+            lib.la_attn_prefill_bwd.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 7 + [i64] * 16 + [i32] * 6 + \
+                [vp, ctypes.c_size_t, vp, vp]
+            lib.la_attn_verify_workspace.argtypes = [i32] * 5 + [vp]
+            lib.la_attn_verify.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 6 + [i64] * 15 + [i32] * 8 + \
+                [vp, ctypes.c_size_t, vp, vp]
+            lib.la_attn_commit.argtypes = [vp] * 9 + [i64] * 11 + [i32] * 7 + [vp] * 2
             for fn in ("la_gated_scan_workspace", "la_gated_scan_fwd", "la_gated_scan_bwd", "la_gated_decode",
                        "la_gated_verify", "la_gated_commit", "la_rms_norm_fwd", "la_rms_norm_fwd_fp8",
-                       "la_rms_norm_bwd_workspace", "la_rms_norm_bwd"):
+                       "la_rms_norm_bwd_workspace", "la_rms_norm_bwd", "la_qk_norm_rope_fwd",
+                       "la_qk_norm_rope_bwd_workspace", "la_qk_norm_rope_bwd", "la_attn_prefill_fwd",
+                       "la_attn_prefill_bwd_workspace", "la_attn_prefill_bwd", "la_attn_verify_workspace",
+                       "la_attn_verify", "la_attn_commit"):
                 getattr(lib, fn).restype = ctypes.c_int
             _lib = lib
         return _lib
@@ -881,6 +904,332 @@ def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, worksp
           _array(workspace, "workspace", torch.uint8, (None,), dev), nbytes,
           _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))
     return dx, dweight
+
+
+# ---- queries, keys and values as heads: norm and rotation (include/la_rotary.h), softmax attention
+#      (include/la_attention.h)
+
+def _heads(t, name, dtype=None, dev=None, shape=None):
+    """Checks of a tensor [tokens, heads, D] with contiguous D; returns (pointer, token stride, head stride)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    have = t.shape
+    if len(have) != 3:
+        raise ValueError(f"{name} must have 3 dims, got shape {tuple(have)}")
+    if shape is not None and have != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(have)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    ld, hs, one = t.stride()
+    if one != 1 and have[2] > 1 and have[0] * have[1] > 0:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t.data_ptr(), ld, hs
+
+
+def _out_heads(t, name, shape, dtype, dev, stream):
+    """(tensor, pointer, strides) of an output, a new dense tensor when not given."""
+    if t is not None:
+        return t, *_heads(t, name, dtype, dev, shape)
+    t = _empty(shape, dtype, dev, stream)
+    return t, t.data_ptr(), shape[1] * shape[2], shape[2]
+
+
+def _qk(q, k):
+    """Checks shared by the norm and rotation calls; returns (la_dtype, dtype, device, q shape, k shape, q, k)."""
+    import torch
+    qs = _heads(q, "q")
+    dtype, dev = q.dtype, q.get_device()
+    code = 0 if dtype is torch.bfloat16 else 1 if dtype is torch.float32 else None
+    if code is None:
+        raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {dtype}")
+    tokens, H, D = q.shape
+    ks = _heads(k, "k", dtype, dev)
+    if k.shape[0] != tokens or k.shape[2] != D:
+        raise ValueError(f"q and k must have the same tokens and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
+    return code, dtype, dev, q.shape, k.shape, qs, ks
+
+
+def _rotation(positions, inv_freq, tokens, dev):
+    """(pointer of positions, pointer of inv_freq, R)."""
+    import torch
+    if inv_freq is None:
+        if positions is not None:
+            raise ValueError("positions needs inv_freq")
+        return None, None, 0
+    if positions is None:
+        raise ValueError("inv_freq needs positions")
+    return (_array(positions, "positions", torch.int32, (tokens,), dev),
+            _array(inv_freq, "inv_freq", torch.float32, (None,), dev), 2 * inv_freq.shape[0])
+
+
+def la_qk_norm_rope_fwd(q, k, q_weight, k_weight, eps, positions=None, inv_freq=None, interleaved=False, q_out=None,
+                        k_out=None, stream=None):
+    """RMS norm of every query and key head over its D elements, then the position rotation of the
+    first R of them: pair i by the angle positions[t] * inv_freq[i] (pairs (i, i + R/2), or (2i, 2i + 1)
+    with ``interleaved``).
+
+    q: bf16 or fp32 [tokens, H, D]; k: [tokens, HK, D] (D = 64, 128, 256), D contiguous, any strides
+    between tokens and heads (column ranges of one projection's output work in place); q_weight,
+    k_weight: fp32 [D] or None (ones); positions: int32 [tokens]; inv_freq: fp32 [R / 2] (both None: no
+    rotation).  q_out and k_out may be q and k themselves.  Returns (q_out, k_out)."""
+    import torch
+    lib = load_library()
+    code, dtype, dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk) = _qk(q, k)
+    pos, freq, R = _rotation(positions, inv_freq, tokens, dev)
+    q_out, pqo, ldqo, hsqo = _out_heads(q_out, "q_out", q.shape, dtype, dev, stream)
+    k_out, pko, ldko, hsko = _out_heads(k_out, "k_out", k.shape, dtype, dev, stream)
+    _call(lib.la_qk_norm_rope_fwd, dev, pq, pk, _array(q_weight, "q_weight", torch.float32, (D,), dev),
+          _array(k_weight, "k_weight", torch.float32, (D,), dev), eps, pos, freq, pqo, pko, ldq, hsq, ldk, hsk, ldqo, hsqo,
+          ldko, hsko, tokens, H, HK, D, R, int(bool(interleaved)), code, _stream_of(stream, dev))
+    return q_out, k_out
+
+
+@functools.lru_cache(maxsize=1024)
+def la_qk_norm_rope_bwd_workspace(tokens, H, HK, D):
+    """Bytes of device workspace la_qk_norm_rope_bwd needs for these sizes."""
+    return _bytes_of(load_library().la_qk_norm_rope_bwd_workspace, tokens, H, HK, D)
+
+
+def _bytes_of(fn, *sizes):
+    nbytes = ctypes.c_size_t(0)
+    st = fn(*(int(n) for n in sizes), ctypes.byref(nbytes))
+    if st != 0:
+        _raise(load_library(), st)
+    return nbytes.value
+
+
+def _workspace(workspace, query, sizes, dev, stream):
+    """(tensor that owns it, pointer, bytes) of a call's workspace."""
+    import torch
+    if workspace is None:
+        nbytes = query(*sizes)
+        workspace = _empty(nbytes, torch.uint8, dev, stream)
+        return workspace, workspace.data_ptr(), nbytes
+    return workspace, _array(workspace, "workspace", torch.uint8, (None,), dev), workspace.numel()
+
+
+def la_qk_norm_rope_bwd(q, k, q_weight, k_weight, eps, dq_out, dk_out, positions=None, inv_freq=None, interleaved=False,
+                        dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """Gradients of la_qk_norm_rope_fwd for its inputs q and k, given those of its outputs; returns
+    (dq, dk, dq_weight, dk_weight).  dq and dk may be dq_out and dk_out themselves.  ``workspace``:
+    CUDA uint8, at least la_qk_norm_rope_bwd_workspace(...) bytes, allocated here when None."""
+    import torch
+    lib = load_library()
+    code, dtype, dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk) = _qk(q, k)
+    pos, freq, R = _rotation(positions, inv_freq, tokens, dev)
+    pgq, ldgq, hsgq = _heads(dq_out, "dq_out", dtype, dev, q.shape)
+    pgk, ldgk, hsgk = _heads(dk_out, "dk_out", dtype, dev, k.shape)
+    dq, pdq, lddq, hsdq = _out_heads(dq, "dq", q.shape, dtype, dev, stream)
+    dk, pdk, lddk, hsdk = _out_heads(dk, "dk", k.shape, dtype, dev, stream)
+    if dq_weight is None:
+        dq_weight = _empty((D,), torch.float32, dev, stream)
+    if dk_weight is None:
+        dk_weight = _empty((D,), torch.float32, dev, stream)
+    owner, ws, nbytes = _workspace(workspace, la_qk_norm_rope_bwd_workspace, (tokens, H, HK, D), dev, stream)
+    _call(lib.la_qk_norm_rope_bwd, dev, pq, pk, _array(q_weight, "q_weight", torch.float32, (D,), dev),
+          _array(k_weight, "k_weight", torch.float32, (D,), dev), eps, pos, freq, pgq, pgk, pdq, pdk,
+          _array(dq_weight, "dq_weight", torch.float32, (D,), dev), _array(dk_weight, "dk_weight", torch.float32, (D,), dev),
+          ldq, hsq, ldk, hsk, ldgq, hsgq, ldgk, hsgk, lddq, hsdq, lddk, hsdk, tokens, H, HK, D, R, int(bool(interleaved)),
+          code, ws, nbytes, _stream_of(stream, dev))
+    return dq, dk, dq_weight, dk_weight
+
+
+def _qkv(q, k, v):
+    """Checks shared by the attention calls; returns (device, q and k shapes, q, k, v as _heads)."""
+    import torch
+    qs = _heads(q, "q", torch.bfloat16)
+    dev = q.get_device()
+    ks = _heads(k, "k", torch.bfloat16, dev)
+    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError(f"q and k must have the same tokens and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
+    return dev, q.shape, k.shape, qs, ks, _heads(v, "v", torch.bfloat16, dev, k.shape)
+
+
+def _prompt_sequences(tokens, dev, cu_seqlens, seq_len):
+    """(B, T, N, pointer of cu_seqlens) of a prompt call."""
+    import torch
+    if cu_seqlens is not None:
+        N = cu_seqlens.shape[0] - 1 if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() == 1 else 0
+        cu = _array(cu_seqlens, "cu_seqlens", torch.int32, (None,), dev)
+        if N < 0:
+            raise ValueError("cu_seqlens must have N + 1 entries")
+        return 1, tokens, N, cu
+    if seq_len is None:
+        raise ValueError("fixed-length mode needs seq_len")
+    T = int(seq_len)
+    if T < 1:
+        raise ValueError("seq_len must be positive in fixed-length mode")
+    if tokens % T:
+        raise ValueError("tokens must be a multiple of seq_len")
+    return tokens // T, T, tokens // T, None
+
+
+def la_attn_prefill_fwd(q, k, v, scale, cu_seqlens=None, seq_len=None, o=None, lse=None, dev_error=None, stream=None):
+    """Causal softmax attention over whole sequences with grouped heads.
+
+    q: bf16 [tokens, H, D]; k, v: bf16 [tokens, HK, D] (D = 64, 128; H a multiple of HK), D contiguous,
+    strides between tokens and heads multiples of 8 elements, 16-byte aligned; cu_seqlens: int32
+    [N + 1] or None (then ``seq_len`` tokens per sequence).  Rows of no sequence are not written.
+    Returns (o, lse), lse fp32 [H, tokens], both allocated when not given."""
+    import torch
+    lib = load_library()
+    dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk), (pv, ldv, hsv) = _qkv(q, k, v)
+    B, T, N, cu = _prompt_sequences(tokens, dev, cu_seqlens, seq_len)
+    o, po, ldo, hso = _out_heads(o, "o", q.shape, torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _empty((H, tokens), torch.float32, dev, stream)
+    _call(lib.la_attn_prefill_fwd, dev, pq, pk, pv, scale, cu, po, _array(lse, "lse", torch.float32, (H, tokens), dev), ldq,
+          hsq, ldk, hsk, ldv, hsv, ldo, hso, B, T, N, H, HK, D, _array(dev_error, "dev_error", torch.int32, (None,), dev),
+          _stream_of(stream, dev))
+    return o, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def la_attn_prefill_bwd_workspace(B, T, H):
+    """Bytes of device workspace la_attn_prefill_bwd needs for B sequences of T tokens (packed: 1, tokens)."""
+    return _bytes_of(load_library().la_attn_prefill_bwd_workspace, B, T, H)
+
+
+def la_attn_prefill_bwd(q, k, v, scale, o, lse, dout, cu_seqlens=None, seq_len=None, dq=None, dk=None, dv=None,
+                        workspace=None, dev_error=None, stream=None):
+    """Gradients of la_attn_prefill_fwd, given its outputs o and lse and dout = dL/do; returns
+    (dq, dk, dv).  Rows of no sequence are not written.  ``workspace``: CUDA uint8, at least
+    la_attn_prefill_bwd_workspace(...) bytes, allocated here when None."""
+    import torch
+    lib = load_library()
+    bf16 = torch.bfloat16
+    dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk), (pv, ldv, hsv) = _qkv(q, k, v)
+    B, T, N, cu = _prompt_sequences(tokens, dev, cu_seqlens, seq_len)
+    po, ldo, hso = _heads(o, "o", bf16, dev, q.shape)
+    pg, ldg, hsg = _heads(dout, "dout", bf16, dev, q.shape)
+    if lse is None:
+        raise TypeError("lse must be a torch.Tensor")
+    plse = _array(lse, "lse", torch.float32, (H, tokens), dev)
+    dq, pdq, lddq, hsdq = _out_heads(dq, "dq", q.shape, bf16, dev, stream)
+    dk, pdk, lddk, hsdk = _out_heads(dk, "dk", k.shape, bf16, dev, stream)
+    dv, pdv, lddv, hsdv = _out_heads(dv, "dv", v.shape, bf16, dev, stream)
+    owner, ws, nbytes = _workspace(workspace, la_attn_prefill_bwd_workspace, (B, T, H), dev, stream)
+    _call(lib.la_attn_prefill_bwd, dev, pq, pk, pv, scale, po, plse, pg, cu, pdq, pdk, pdv, ldq, hsq, ldk, hsk, ldv, hsv,
+          ldo, hso, ldg, hsg, lddq, hsdq, lddk, hsdk, lddv, hsdv, B, T, N, H, HK, D, ws, nbytes,
+          _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))
+    return dq, dk, dv
+
+
+def _cache(k_cache, v_cache, HK, D, cache_lens, page_table, B, dev):
+    """Checks of a key/value cache; returns (pointers of k_cache, v_cache, cache_lens, page_table; the
+    strides; (pages, page_size, table_width))."""
+    import torch
+    ptrs, strides = [], []
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+        if t.dim() != 4 or t.shape[2] != HK or t.shape[3] != D:
+            raise ValueError(f"{name} must have shape [pages, page_size, {HK}, {D}], got {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+        s = t.stride()
+        if s[3] != 1:
+            raise ValueError(f"the last axis of {name} must be contiguous")
+        ptrs.append(t.data_ptr())
+        strides += s[:3]
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if cache_lens is None:
+        raise TypeError("cache_lens must be a torch.Tensor")
+    ptrs.append(_array(cache_lens, "cache_lens", torch.int32, (B,), dev))
+    pages, size, width, ld = k_cache.shape[0], k_cache.shape[1], 0, 0
+    if page_table is None:
+        ptrs.append(None)
+    else:
+        if not isinstance(page_table, torch.Tensor):
+            raise TypeError("page_table must be a torch.Tensor")
+        if page_table.dtype is not torch.int32:
+            raise TypeError(f"page_table must be torch.int32, got {page_table.dtype}")
+        if page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError(f"page_table must have shape [{B}, width], got {tuple(page_table.shape)}")
+        if page_table.get_device() != dev:
+            raise ValueError(f"page_table must be on cuda:{dev}, got {page_table.device}")
+        width, (ld, one) = page_table.shape[1], page_table.stride()
+        if one != 1 and width > 1:
+            raise ValueError("the rows of page_table must be contiguous")
+        ptrs.append(page_table.data_ptr())
+    return ptrs, (*strides, ld), (pages, size, width)
+
+
+@functools.lru_cache(maxsize=1024)
+def la_attn_verify_workspace(B, T, H, HK, D):
+    """Bytes of device workspace la_attn_verify needs for these sizes."""
+    return _bytes_of(load_library().la_attn_verify_workspace, B, T, H, HK, D)
+
+
+def la_attn_verify(q, k, v, scale, k_cache, v_cache, cache_lens, T, page_table=None, mask=None, o=None, workspace=None,
+                   dev_error=None, stream=None):
+    """Softmax attention of each request's T drafted tokens over its cache and the drafted tokens
+    themselves, the cache left untouched (T = 1: decode).
+
+    q: bf16 [B*T, H, D]; k, v: bf16 [B*T, HK, D]; k_cache, v_cache: bf16 [pages, page_size, HK, D], any
+    strides between pages, tokens and heads that are multiples of 8; cache_lens: int32 [B] (negative =
+    padded request, nothing written); page_table: int32 [B, width] or None (request b has page b);
+    mask: int64 [B, T] or None: bit u of mask[b, t] lets token t see drafted token u (None: tokens
+    0 .. t).  ``workspace``: CUDA uint8, at least la_attn_verify_workspace(...) bytes, allocated here
+    when None.  Returns ``o``."""
+    import torch
+    lib = load_library()
+    T = int(T)
+    dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk), (pv, ldv, hsv) = _qkv(q, k, v)
+    if T < 1 or tokens % T:
+        raise ValueError("T must be >= 1 and q must have B*T rows")
+    B = tokens // T
+    (pkc, pvc, lens, table), strides, sizes = _cache(k_cache, v_cache, HK, D, cache_lens, page_table, B, dev)
+    o, po, ldo, hso = _out_heads(o, "o", q.shape, torch.bfloat16, dev, stream)
+    owner, ws, nbytes = _workspace(workspace, la_attn_verify_workspace, (B, T, H, HK, D), dev, stream)
+    _call(lib.la_attn_verify, dev, pq, pk, pv, scale, pkc, pvc, lens, table, _array(mask, "mask", torch.int64, (B, T), dev),
+          po, ldq, hsq, ldk, hsk, ldv, hsv, ldo, hso, *strides, B, T, H, HK, D, *sizes, ws, nbytes,
+          _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))
+    return o
+
+
+def la_attn_commit(k, v, k_cache, v_cache, cache_lens, T=None, cu_seqlens=None, accepted_len=None, path=None,
+                   page_table=None, dev_error=None, stream=None):
+    """Write tokens' keys and values (bf16 [tokens, HK, D]) into the cache behind each request's
+    cache_lens tokens (the caller then advances cache_lens).
+
+    With ``T``: request b has tokens b*T .. and commits accepted_len[b] of them (int32 [B]; None: all),
+    those that path[b] lists (int32 [B, T]; None: the first).  With ``cu_seqlens`` (int32 [B + 1]):
+    request b commits tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1, as after a prompt.  The cache as
+    in la_attn_verify.  Returns (k_cache, v_cache)."""
+    import torch
+    lib = load_library()
+    pk, ldk, hsk = _heads(k, "k", torch.bfloat16)
+    dev = k.get_device()
+    tokens, HK, D = k.shape
+    pv, ldv, hsv = _heads(v, "v", torch.bfloat16, dev, k.shape)
+    if (T is None) == (cu_seqlens is None):
+        raise ValueError("give either T or cu_seqlens")
+    if cu_seqlens is not None:
+        cu = _array(cu_seqlens, "cu_seqlens", torch.int32, (None,), dev)
+        B, T = cu_seqlens.shape[0] - 1, tokens
+        if B < 0:
+            raise ValueError("cu_seqlens must have B + 1 entries")
+        if accepted_len is not None or path is not None:
+            raise ValueError("accepted_len and path go with T, not with cu_seqlens")
+    else:
+        cu, T = None, int(T)
+        if T < 1 or tokens % T:
+            raise ValueError("T must be >= 1 and k must have B*T rows")
+        B = tokens // T
+    (pkc, pvc, lens, table), strides, sizes = _cache(k_cache, v_cache, HK, D, cache_lens, page_table, B, dev)
+    _call(lib.la_attn_commit, dev, pk, pv, pkc, pvc, lens, cu, _array(accepted_len, "accepted_len", torch.int32, (B,), dev),
+          _array(path, "path", torch.int32, (B, T), dev), table, ldk, hsk, ldv, hsv, *strides, B, T, HK, D, *sizes,
+          _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))
+    return k_cache, v_cache
 
 
 def la_prefill_fwd_raw(*args):

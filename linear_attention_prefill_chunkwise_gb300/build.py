@@ -1,8 +1,8 @@
 """Compile the sm_103a C-ABI library ``libla_prefill.so`` in-tree.
 
-Eight translation units (prefill; speculative-decoding ops; segmented prefill; its variant
-with a built-in scratch buffer; backward pass; D = 256 prefill; gated recurrence; RMS norm),
-compiled side by side, one ``-gencode`` (sm_103a), static CUDA runtime, no
+Ten translation units (prefill; speculative-decoding ops; segmented prefill; its variant
+with a built-in scratch buffer; backward pass; D = 256 prefill; gated recurrence; RMS norm; norm
+and rotation of queries and keys; softmax attention), compiled side by side, one ``-gencode`` (sm_103a), static CUDA runtime, no
 link-time dependency on the driver library (the tensor-map encoder is fetched
 through the runtime's driver entry-point query), so the library loads on a
 machine without a GPU.
@@ -22,13 +22,16 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 INCLUDE_DIR = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["la_prefill_api.cu", "la_decode_api.cu", "la_segment_api.cu", "la_segment_static_api.cu",
-           "la_backward_api.cu", "la_d256_api.cu", "la_gated_api.cu", "la_norm_api.cu"]
+           "la_backward_api.cu", "la_d256_api.cu", "la_gated_api.cu", "la_norm_api.cu", "la_rotary_api.cu",
+           "la_attention_api.cu"]
 DEPENDS = ["la_prefill_api.cu", "la_prefill_kernel.cuh", "sm103_ptx.cuh", "la_decode_api.cu", "la_decode_kernels.cuh",
            "la_segment_api.cu", "la_segment_kernels.cuh", "la_segment_static_api.cu", "la_host_common.h",
            "la_backward_api.cu", "la_verify_kernel.cuh", "la_prefill_internal.h", "la_d256_api.cu",
            "la_gated_api.cu", "la_gated_kernels.cuh", "la_gated_math.cuh", "la_rows_common.h", "la_norm_api.cu",
-           "la_norm_kernels.cuh"]
-HEADERS = ["la_prefill.h", "la_decode.h", "la_segment.h", "la_backward.h", "la_d256.h", "la_gated.h", "la_norm.h"]
+           "la_norm_kernels.cuh", "la_vec.cuh", "la_heads_common.h", "la_rotary_api.cu", "la_rotary_kernels.cuh",
+           "la_attention_api.cu", "la_attention_params.cuh", "la_attention_simple.cuh", "la_attention_commit.cuh"]
+HEADERS = ["la_prefill.h", "la_decode.h", "la_segment.h", "la_backward.h", "la_d256.h", "la_gated.h", "la_norm.h",
+           "la_rotary.h", "la_attention.h"]
 # parts that can be built alone with a short wait limit
 WAIT_LIMIT_PARTS = {"prefill": ["la_prefill_api.cu"], "gated": ["la_gated_api.cu", "la_norm_api.cu"]}
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,0 +1,366 @@
+// la_attention_api.cu -- host side of the C ABI declared in include/la_attention.h: argument
+// validation and the launches.  Nothing here allocates device memory, reads device memory or
+// synchronises with the host.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/la_attention.h"
+#include "la_attention_commit.cuh"
+#include "la_attention_simple.cuh"
+#include "la_heads_common.h"
+#include "la_host_common.h"
+
+namespace {
+
+using la_host::fail;
+using la_host::flat;
+using la_host::heads_arg;
+using la_host::HeadsArg;
+using la_host::RowSpan;
+using laa::bf16;
+
+la_host::DeviceState g_dev[la_host::kMaxDevices];
+
+la_status device(la_host::DeviceState** ds) {
+  return la_host::current_device(g_dev, ds, [] { return cudaSuccess; });
+}
+
+la_status launched(cudaError_t ce) {
+  return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
+}
+
+constexpr int64_t kMostTokens = INT32_MAX - 1024;  // row numbers and tile ends stay within int32
+
+HeadsArg rows(const void* p, int64_t ld, int64_t hs, int64_t tokens, int heads, int D, const char* name) {
+  return heads_arg(p, ld, hs, tokens, heads, D, 2, 16, name);
+}
+
+laa::Heads<const bf16> in(const HeadsArg& h) { return {static_cast<const bf16*>(h.p), h.ld, h.hs}; }
+laa::Heads<bf16> out(const HeadsArg& h) { return {static_cast<bf16*>(const_cast<void*>(h.p)), h.ld, h.hs}; }
+
+la_status check_heads_of(int H, int HK, int D) {
+  if (D != 64 && D != 128) return fail(LA_ERR_UNSUPPORTED, "only D = 64 and 128 are implemented (got %d)", D);
+  if (H < 1 || HK < 1) return fail(LA_ERR_INVALID_ARGUMENT, "H and HK must be >= 1 (got %d, %d)", H, HK);
+  if (H % HK != 0) return fail(LA_ERR_UNSUPPORTED, "H (%d) must be a multiple of HK (%d)", H, HK);
+  if (H > (1 << 15)) return fail(LA_ERR_UNSUPPORTED, "H too large (%d)", H);
+  return LA_OK;
+}
+
+// Shapes and batch mode of the prompt calls.
+la_status check_prompt(const int32_t* cu_seqlens, int B, int T, int N, int H, int HK, int D) {
+  const la_status st = check_heads_of(H, HK, D);
+  if (st != LA_OK) return st;
+  if (B < 0 || T < 0 || N < 0) return fail(LA_ERR_INVALID_ARGUMENT, "B, T, N must be >= 0");
+  if (cu_seqlens) {
+    if (B != 1) return fail(LA_ERR_INVALID_ARGUMENT, "packed mode (cu_seqlens given) needs B == 1 (got %d)", B);
+    if (!la_host::aligned4(cu_seqlens)) return fail(LA_ERR_INVALID_ARGUMENT, "cu_seqlens must be 4-byte aligned");
+  } else if (N != B) {
+    return fail(LA_ERR_INVALID_ARGUMENT, "fixed-length mode needs N == B (got N=%d, B=%d)", N, B);
+  }
+  if (static_cast<int64_t>(B) * T + static_cast<int64_t>(N) * 128 > kMostTokens)
+    return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)B * T);
+  return LA_OK;
+}
+
+la_status check_scale(float scale) {
+  // a scale of 0 is a plain mean; anything not finite has no meaning
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(LA_ERR_INVALID_ARGUMENT, "scale must be finite");
+  return LA_OK;
+}
+
+// Checks strides and alignment of every tensor, then outputs (the last n_out) against the others and
+// against each other, and both against the flat buffers.
+la_status check_tensors(const HeadsArg* args, int n, int n_out, const RowSpan* flat_in, int n_flat_in,
+                        const RowSpan* flat_out, int n_flat_out) {
+  RowSpan ins[16], outs[16];
+  int ni = 0, no = 0;
+  for (int i = 0; i < n; ++i) {
+    if (!args[i].p) return fail(LA_ERR_INVALID_ARGUMENT, "%s must be non-null", args[i].name);
+    const la_status st = la_host::check_heads(args[i]);
+    if (st != LA_OK) return st;
+    (i < n - n_out ? ins[ni++] : outs[no++]) = la_host::span_of(args[i]);
+  }
+  for (int i = 0; i < n_flat_in; ++i) ins[ni++] = flat_in[i];
+  for (int i = 0; i < n_flat_out; ++i) outs[no++] = flat_out[i];
+  return la_host::check_apart(ins, ni, outs, no);
+}
+
+// ---------------------------------------------------------------- the cache
+
+struct CacheArg {
+  const void* p;
+  int64_t pages, tokens, heads;  // extents
+  int64_t ps, ts, hs;            // strides
+  const char* name;
+};
+
+// Strides that keep every row of the cache apart (its three outer axes in some order), and the
+// cache as rows for the overlap checks: the outer axes that lie gaplessly within one another are
+// one, so that key and value pages that interleave token by token share nothing.
+la_status check_cache(CacheArg& c, int D, RowSpan* span) {
+  if (c.heads == 1) c.hs = D;
+  if (c.tokens == 1) c.ts = (c.heads - 1) * c.hs + D;
+  if (c.pages == 1) c.ps = std::max((c.tokens - 1) * c.ts, (c.heads - 1) * c.hs) + std::max(c.ts, c.hs);
+  struct Axis {
+    int64_t n, s;
+  } a[3] = {{c.pages, c.ps}, {c.tokens, c.ts}, {c.heads, c.hs}};
+  std::sort(a, a + 3, [](const Axis& x, const Axis& y) { return x.s > y.s; });
+  constexpr int64_t kMost = int64_t(1) << 38;
+  int64_t width = D;
+  for (int i = 2; i >= 0; --i) {
+    if (a[i].s < width || a[i].s > kMost || a[i].n > kMost / (a[i].s > 0 ? a[i].s : 1))
+      return fail(LA_ERR_INVALID_ARGUMENT, "the strides of %s (%lld between pages, %lld between tokens, %lld between heads) do not keep its rows apart",
+                  c.name, (long long)c.ps, (long long)c.ts, (long long)c.hs);
+    width += (a[i].n - 1) * a[i].s;
+  }
+  if (!la_host::aligned16(c.p)) return fail(LA_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", c.name);
+  if (c.ps % 8 || c.ts % 8 || c.hs % 8)
+    return fail(LA_ERR_INVALID_ARGUMENT, "the strides of %s must be multiples of 8 elements", c.name);
+  int64_t n = a[0].n, s = a[0].s, inner = (a[2].n - 1) * a[2].s + D;
+  if (s == a[1].n * a[1].s) {
+    n *= a[1].n;
+    s = a[1].s;
+  } else {
+    inner += (a[1].n - 1) * a[1].s;
+  }
+  *span = {c.p, static_cast<uint64_t>(inner) * 2, static_cast<uint64_t>(s) * 2, static_cast<uint64_t>(n), 16, 0, 0, c.name};
+  return LA_OK;
+}
+
+// What la_attn_verify and la_attn_commit share: the sizes of the cache.
+la_status check_pages(const int32_t* cache_lens, const int32_t* page_table, int B, int T, int HK, int pages,
+                      int page_size, int table_width, int64_t ld_table) {
+  if (B < 0 || T < 0) return fail(LA_ERR_INVALID_ARGUMENT, "B and T must be >= 0 (got %d, %d)", B, T);
+  if (pages < 1 || page_size < 1) return fail(LA_ERR_INVALID_ARGUMENT, "pages and page_size must be >= 1 (got %d, %d)", pages, page_size);
+  if (page_size > kMostTokens) return fail(LA_ERR_UNSUPPORTED, "page_size too large (%d)", page_size);
+  if (!cache_lens && B > 0) return fail(LA_ERR_INVALID_ARGUMENT, "cache_lens must be non-null");
+  if (!la_host::aligned4(cache_lens) || !la_host::aligned4(page_table))
+    return fail(LA_ERR_INVALID_ARGUMENT, "cache_lens and page_table must be 4-byte aligned");
+  if (page_table) {
+    if (page_size % 16 != 0) return fail(LA_ERR_UNSUPPORTED, "page_size must be a multiple of 16 with a page table (got %d)", page_size);
+    if (table_width < 1 || (B > 1 && ld_table < table_width))
+      return fail(LA_ERR_INVALID_ARGUMENT, "page_table's row stride (%lld) must be at least its width (%d >= 1)", (long long)ld_table, table_width);
+    if (static_cast<int64_t>(table_width) * page_size > kMostTokens)
+      return fail(LA_ERR_UNSUPPORTED, "table_width * page_size too large (%d, %d)", table_width, page_size);
+  } else if (pages < B) {
+    return fail(LA_ERR_INVALID_ARGUMENT, "pages (%d) must be >= B (%d) without a page table", pages, B);
+  }
+  return LA_OK;
+}
+
+uint64_t table_bytes(const int32_t* page_table, int B, int table_width, int64_t ld_table) {
+  return page_table && B > 0 ? (static_cast<uint64_t>(B - 1) * ld_table + table_width) * 4 : 0;
+}
+
+template <typename F>
+cudaError_t with_dim(int D, F f) {
+  if (D == 64) return f(std::integral_constant<int, 64>{});
+  return f(std::integral_constant<int, 128>{});
+}
+
+}  // namespace
+
+extern "C" {
+
+la_status la_attn_prefill_fwd(const void* q, const void* k, const void* v, float scale, const int32_t* cu_seqlens,
+                              void* o, float* lse, int64_t ldq, int64_t hsq, int64_t ldk, int64_t hsk, int64_t ldv,
+                              int64_t hsv, int64_t ldo, int64_t hso, int B, int T, int N, int H, int HK, int D,
+                              int* dev_error, void* stream) {
+  la_host::g_last_error[0] = '\0';
+  la_status st = check_prompt(cu_seqlens, B, T, N, H, HK, D);
+  if (st != LA_OK) return st;
+  if ((st = check_scale(scale)) != LA_OK) return st;
+  const int64_t tokens = static_cast<int64_t>(B) * T;
+  if (tokens == 0 || N == 0) return LA_OK;
+  if (!la_host::aligned4(lse) || !la_host::aligned4(dev_error))
+    return fail(LA_ERR_INVALID_ARGUMENT, "lse and dev_error must be 4-byte aligned");
+  const HeadsArg a[] = {rows(q, ldq, hsq, tokens, H, D, "q"), rows(k, ldk, hsk, tokens, HK, D, "k"),
+                        rows(v, ldv, hsv, tokens, HK, D, "v"), rows(o, ldo, hso, tokens, H, D, "o")};
+  const RowSpan fin[] = {flat(cu_seqlens, cu_seqlens ? (static_cast<uint64_t>(N) + 1) * 4 : 0, "cu_seqlens")};
+  const RowSpan fout[] = {flat(lse, static_cast<uint64_t>(H) * tokens * 4, "lse"), flat(dev_error, 4, "dev_error")};
+  if ((st = check_tensors(a, 4, 1, fin, 1, fout, 2)) != LA_OK) return st;
+  la_host::DeviceState* ds = nullptr;
+  if ((st = device(&ds)) != LA_OK) return st;
+  laa::PrefillParams p{};
+  p.q = in(a[0]), p.k = in(a[1]), p.v = in(a[2]), p.o = out(a[3]);
+  p.lse = lse;
+  p.cu_seqlens = cu_seqlens;
+  p.dev_error = dev_error;
+  p.scale = scale;
+  p.tokens = static_cast<int>(tokens), p.T = T, p.N = N, p.H = H, p.HK = HK, p.D = D;
+  return launched(with_dim(D, [&](auto d) {
+    laa::simple_fwd_kernel<decltype(d)::value><<<dim3((p.tokens + 3) / 4, H), 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError();
+  }));
+}
+
+la_status la_attn_prefill_bwd_workspace(int B, int T, int H, size_t* bytes) {
+  la_host::g_last_error[0] = '\0';
+  if (!bytes) return fail(LA_ERR_INVALID_ARGUMENT, "bytes is null");
+  if (B < 0 || T < 0 || H < 1) return fail(LA_ERR_INVALID_ARGUMENT, "B, T must be >= 0 and H >= 1");
+  if (static_cast<int64_t>(B) * T > kMostTokens) return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)B * T);
+  *bytes = la_host::align256(static_cast<size_t>(B) * T * H * sizeof(float));
+  return LA_OK;
+}
+
+la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float scale, const void* o,
+                              const float* lse, const void* dout, const int32_t* cu_seqlens, void* dq, void* dk,
+                              void* dv, int64_t ldq, int64_t hsq, int64_t ldk, int64_t hsk, int64_t ldv, int64_t hsv,
+                              int64_t ldo, int64_t hso, int64_t lddo, int64_t hsdo, int64_t lddq, int64_t hsdq,
+                              int64_t lddk, int64_t hsdk, int64_t lddv, int64_t hsdv, int B, int T, int N, int H,
+                              int HK, int D, void* workspace, size_t workspace_bytes, int* dev_error, void* stream) {
+  la_host::g_last_error[0] = '\0';
+  la_status st = check_prompt(cu_seqlens, B, T, N, H, HK, D);
+  if (st != LA_OK) return st;
+  if ((st = check_scale(scale)) != LA_OK) return st;
+  const int64_t tokens = static_cast<int64_t>(B) * T;
+  if (tokens == 0 || N == 0) return LA_OK;
+  if (!lse) return fail(LA_ERR_INVALID_ARGUMENT, "lse must be non-null");
+  if (!la_host::aligned4(lse) || !la_host::aligned4(dev_error))
+    return fail(LA_ERR_INVALID_ARGUMENT, "lse and dev_error must be 4-byte aligned");
+  size_t need = 0;
+  if ((st = la_attn_prefill_bwd_workspace(B, T, H, &need)) != LA_OK) return st;
+  if ((st = la_host::check_workspace(workspace, workspace_bytes, need)) != LA_OK) return st;
+  const HeadsArg a[] = {rows(q, ldq, hsq, tokens, H, D, "q"),       rows(k, ldk, hsk, tokens, HK, D, "k"),
+                        rows(v, ldv, hsv, tokens, HK, D, "v"),      rows(o, ldo, hso, tokens, H, D, "o"),
+                        rows(dout, lddo, hsdo, tokens, H, D, "dout"), rows(dq, lddq, hsdq, tokens, H, D, "dq"),
+                        rows(dk, lddk, hsdk, tokens, HK, D, "dk"),  rows(dv, lddv, hsdv, tokens, HK, D, "dv")};
+  const RowSpan fin[] = {flat(cu_seqlens, cu_seqlens ? (static_cast<uint64_t>(N) + 1) * 4 : 0, "cu_seqlens"),
+                         flat(lse, static_cast<uint64_t>(H) * tokens * 4, "lse")};
+  const RowSpan fout[] = {flat(workspace, need, "workspace"), flat(dev_error, 4, "dev_error")};
+  if ((st = check_tensors(a, 8, 3, fin, 2, fout, 2)) != LA_OK) return st;
+  la_host::DeviceState* ds = nullptr;
+  if ((st = device(&ds)) != LA_OK) return st;
+  laa::PrefillParams p{};
+  p.q = in(a[0]), p.k = in(a[1]), p.v = in(a[2]), p.o_in = in(a[3]), p.dout = in(a[4]);
+  p.dq = out(a[5]), p.dk = out(a[6]), p.dv = out(a[7]);
+  p.lse_in = lse;
+  p.delta = static_cast<float*>(workspace);
+  p.cu_seqlens = cu_seqlens;
+  p.dev_error = dev_error;
+  p.scale = scale;
+  p.tokens = static_cast<int>(tokens), p.T = T, p.N = N, p.H = H, p.HK = HK, p.D = D;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launched(with_dim(D, [&](auto d) {
+    laa::simple_dq_kernel<decltype(d)::value><<<dim3((p.tokens + 3) / 4, H), 128, 0, s>>>(p);
+    laa::simple_dkdv_kernel<decltype(d)::value><<<dim3((p.tokens + 3) / 4, HK), 128, 0, s>>>(p);
+    return cudaGetLastError();
+  }));
+}
+
+la_status la_attn_verify_workspace(int B, int T, int H, int HK, int D, size_t* bytes) {
+  la_host::g_last_error[0] = '\0';
+  if (!bytes) return fail(LA_ERR_INVALID_ARGUMENT, "bytes is null");
+  const la_status st = check_heads_of(H, HK, D);
+  if (st != LA_OK) return st;
+  if (B < 0 || T < 1) return fail(LA_ERR_INVALID_ARGUMENT, "B must be >= 0 and T >= 1 (got %d, %d)", B, T);
+  *bytes = 256;
+  return LA_OK;
+}
+
+la_status la_attn_verify(const void* q, const void* k, const void* v, float scale, const void* k_cache,
+                         const void* v_cache, const int32_t* cache_lens, const int32_t* page_table,
+                         const int64_t* mask, void* o, int64_t ldq, int64_t hsq, int64_t ldk, int64_t hsk, int64_t ldv,
+                         int64_t hsv, int64_t ldo, int64_t hso, int64_t kp, int64_t kt, int64_t kh, int64_t vp,
+                         int64_t vt, int64_t vh, int64_t ld_table, int B, int T, int H, int HK, int D, int pages,
+                         int page_size, int table_width, void* workspace, size_t workspace_bytes, int* dev_error,
+                         void* stream) {
+  la_host::g_last_error[0] = '\0';
+  la_status st = check_heads_of(H, HK, D);
+  if (st != LA_OK) return st;
+  if ((st = check_scale(scale)) != LA_OK) return st;
+  if ((st = check_pages(cache_lens, page_table, B, T, HK, pages, page_size, table_width, ld_table)) != LA_OK) return st;
+  if (T < 1) return fail(LA_ERR_INVALID_ARGUMENT, "T must be >= 1 (got %d)", T);
+  if (mask && T > 64) return fail(LA_ERR_UNSUPPORTED, "a mask has at most 64 tokens (got %d)", T);
+  if (H / HK > 128) return fail(LA_ERR_UNSUPPORTED, "H / HK up to 128 is implemented (got %d)", H / HK);
+  const int64_t tokens = static_cast<int64_t>(B) * T;
+  if (tokens > kMostTokens) return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)tokens);
+  if (B == 0) return LA_OK;
+  if (!k_cache || !v_cache) return fail(LA_ERR_INVALID_ARGUMENT, "k_cache and v_cache must be non-null");
+  if (!la_host::aligned4(dev_error) || reinterpret_cast<uintptr_t>(mask) % 8)
+    return fail(LA_ERR_INVALID_ARGUMENT, "mask must be 8-byte and dev_error 4-byte aligned");
+  size_t need = 0;
+  if ((st = la_attn_verify_workspace(B, T, H, HK, D, &need)) != LA_OK) return st;
+  if ((st = la_host::check_workspace(workspace, workspace_bytes, need)) != LA_OK) return st;
+  CacheArg kc{k_cache, pages, page_size, HK, kp, kt, kh, "k_cache"}, vc{v_cache, pages, page_size, HK, vp, vt, vh, "v_cache"};
+  RowSpan fin[5];
+  if ((st = check_cache(kc, D, &fin[0])) != LA_OK || (st = check_cache(vc, D, &fin[1])) != LA_OK) return st;
+  fin[2] = flat(cache_lens, static_cast<uint64_t>(B) * 4, "cache_lens");
+  fin[3] = flat(page_table, table_bytes(page_table, B, table_width, ld_table), "page_table");
+  fin[4] = flat(mask, mask ? static_cast<uint64_t>(tokens) * 8 : 0, "mask");
+  const HeadsArg a[] = {rows(q, ldq, hsq, tokens, H, D, "q"), rows(k, ldk, hsk, tokens, HK, D, "k"),
+                        rows(v, ldv, hsv, tokens, HK, D, "v"), rows(o, ldo, hso, tokens, H, D, "o")};
+  const RowSpan fout[] = {flat(workspace, need, "workspace"), flat(dev_error, 4, "dev_error")};
+  if ((st = check_tensors(a, 4, 1, fin, 5, fout, 2)) != LA_OK) return st;
+  la_host::DeviceState* ds = nullptr;
+  if ((st = device(&ds)) != LA_OK) return st;
+  laa::CacheParams p{};
+  p.q = in(a[0]), p.k = in(a[1]), p.v = in(a[2]), p.o = out(a[3]);
+  p.k_cache = static_cast<const bf16*>(k_cache);
+  p.v_cache = static_cast<const bf16*>(v_cache);
+  p.kp = kc.ps, p.kt = kc.ts, p.kh = kc.hs, p.vp = vc.ps, p.vt = vc.ts, p.vh = vc.hs;
+  p.ld_table = ld_table;
+  p.cache_lens = cache_lens;
+  p.page_table = page_table;
+  p.mask = mask;
+  p.part = static_cast<float*>(workspace);
+  p.dev_error = dev_error;
+  p.scale = scale;
+  p.B = B, p.T = T, p.H = H, p.HK = HK, p.D = D, p.pages = pages, p.page_size = page_size, p.table_width = table_width;
+  return launched(with_dim(D, [&](auto d) {
+    laa::simple_verify_kernel<decltype(d)::value><<<dim3(static_cast<unsigned>(tokens), H), 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError();
+  }));
+}
+
+la_status la_attn_commit(const void* k, const void* v, void* k_cache, void* v_cache, const int32_t* cache_lens,
+                         const int32_t* cu_seqlens, const int32_t* accepted_len, const int32_t* path,
+                         const int32_t* page_table, int64_t ldk, int64_t hsk, int64_t ldv, int64_t hsv, int64_t kp,
+                         int64_t kt, int64_t kh, int64_t vp, int64_t vt, int64_t vh, int64_t ld_table, int B, int T,
+                         int HK, int D, int pages, int page_size, int table_width, int* dev_error, void* stream) {
+  la_host::g_last_error[0] = '\0';
+  la_status st = check_heads_of(HK, HK, D);
+  if (st != LA_OK) return st;
+  if ((st = check_pages(cache_lens, page_table, B, T, HK, pages, page_size, table_width, ld_table)) != LA_OK) return st;
+  if (cu_seqlens && (accepted_len || path))
+    return fail(LA_ERR_INVALID_ARGUMENT, "accepted_len and path belong to the fixed-length mode (cu_seqlens null)");
+  const int64_t tokens = cu_seqlens ? T : static_cast<int64_t>(B) * T;
+  if (tokens > kMostTokens) return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)tokens);
+  if (B == 0 || tokens == 0) return LA_OK;
+  if (!k_cache || !v_cache) return fail(LA_ERR_INVALID_ARGUMENT, "k_cache and v_cache must be non-null");
+  if (!la_host::aligned4(dev_error) || !la_host::aligned4(cu_seqlens) || !la_host::aligned4(accepted_len) || !la_host::aligned4(path))
+    return fail(LA_ERR_INVALID_ARGUMENT, "cu_seqlens, accepted_len, path and dev_error must be 4-byte aligned");
+  CacheArg kc{k_cache, pages, page_size, HK, kp, kt, kh, "k_cache"}, vc{v_cache, pages, page_size, HK, vp, vt, vh, "v_cache"};
+  RowSpan fout[3];
+  if ((st = check_cache(kc, D, &fout[0])) != LA_OK || (st = check_cache(vc, D, &fout[1])) != LA_OK) return st;
+  fout[2] = flat(dev_error, 4, "dev_error");
+  const RowSpan fin[] = {flat(cache_lens, static_cast<uint64_t>(B) * 4, "cache_lens"),
+                         flat(cu_seqlens, cu_seqlens ? (static_cast<uint64_t>(B) + 1) * 4 : 0, "cu_seqlens"),
+                         flat(accepted_len, accepted_len ? static_cast<uint64_t>(B) * 4 : 0, "accepted_len"),
+                         flat(path, path ? static_cast<uint64_t>(tokens) * 4 : 0, "path"),
+                         flat(page_table, table_bytes(page_table, B, table_width, ld_table), "page_table")};
+  const HeadsArg a[] = {rows(k, ldk, hsk, tokens, HK, D, "k"), rows(v, ldv, hsv, tokens, HK, D, "v")};
+  if ((st = check_tensors(a, 2, 0, fin, 5, fout, 3)) != LA_OK) return st;
+  la_host::DeviceState* ds = nullptr;
+  if ((st = device(&ds)) != LA_OK) return st;
+  laa::CacheParams p{};
+  p.k = in(a[0]), p.v = in(a[1]);
+  p.k_out = static_cast<bf16*>(k_cache);
+  p.v_out = static_cast<bf16*>(v_cache);
+  p.kp = kc.ps, p.kt = kc.ts, p.kh = kc.hs, p.vp = vc.ps, p.vt = vc.ts, p.vh = vc.hs;
+  p.ld_table = ld_table;
+  p.cache_lens = cache_lens, p.page_table = page_table, p.cu_seqlens = cu_seqlens, p.accepted_len = accepted_len, p.path = path;
+  p.dev_error = dev_error;
+  p.B = B, p.T = T, p.H = HK, p.HK = HK, p.D = D, p.pages = pages, p.page_size = page_size, p.table_width = table_width;
+  // blocks of a request: its tokens (packed: their number is on the device, so at most what a batch
+  // of one would take, and few enough that the empty ones cost little)
+  const int64_t most = (T + laa::kCommitTokens - 1) / laa::kCommitTokens;
+  const int64_t share = std::max<int64_t>(1, 16 * ds->sms / B);
+  const int tiles = static_cast<int>(std::min<int64_t>(std::min<int64_t>(most, cu_seqlens ? share : most), 65535));
+  return launched(la_host::launch_pdl(laa::commit_kernel, dim3(B, tiles), laa::kCommitThreads, 0,
+                                      static_cast<cudaStream_t>(stream), p));
+}
+
+}  // extern "C"
