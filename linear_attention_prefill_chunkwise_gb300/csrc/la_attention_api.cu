@@ -8,6 +8,7 @@
 
 #include "../../include/la_attention.h"
 #include "la_attention_commit.cuh"
+#include "la_attention_fwd.cuh"
 #include "la_attention_simple.cuh"
 #include "la_heads_common.h"
 #include "la_host_common.h"
@@ -23,8 +24,16 @@ using laa::bf16;
 
 la_host::DeviceState g_dev[la_host::kMaxDevices];
 
+template <int D>
+constexpr int fwd_shared() { return static_cast<int>(sizeof(laa::FwdShared<D>)) + 1024; }
+
 la_status device(la_host::DeviceState** ds) {
-  return la_host::current_device(g_dev, ds, [] { return cudaSuccess; });
+  return la_host::current_device(g_dev, ds, [] {
+    const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(laa::attn_fwd_kernel<64>, most, fwd_shared<64>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_fwd_kernel<128>, most, fwd_shared<128>());
+    return e;
+  });
 }
 
 la_status launched(cudaError_t ce) {
@@ -36,6 +45,25 @@ constexpr int64_t kMostTokens = INT32_MAX - 1024;  // row numbers and tile ends 
 HeadsArg rows(const void* p, int64_t ld, int64_t hs, int64_t tokens, int heads, int D, const char* name) {
   return heads_arg(p, ld, hs, tokens, heads, D, 2, 16, name);
 }
+
+// Map over a tensor of heads with boxes of `heads` heads x `tokens` tokens x 64 columns (a head's rows
+// of 128 bytes, 128-byte swizzle).
+la_status encode_heads(CUtensorMap* map, const HeadsArg& h, int heads, int tokens) {
+  auto enc = la_host::tensor_map_encoder();
+  if (!enc) return fail(LA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the CUDA driver");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(h.D), static_cast<cuuint64_t>(h.heads), static_cast<cuuint64_t>(h.tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(h.hs) * 2, static_cast<cuuint64_t>(h.ld) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(h.p), dims, strides, box, ones,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(LA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", h.name, (int)r);
+  return LA_OK;
+}
+
+// Blocks for at most this many items of work, one per SM.
+int blocks_for(int64_t items, int sms) { return static_cast<int>(std::min<int64_t>(items, sms)); }
 
 laa::Heads<const bf16> in(const HeadsArg& h) { return {static_cast<const bf16*>(h.p), h.ld, h.hs}; }
 laa::Heads<bf16> out(const HeadsArg& h) { return {static_cast<bf16*>(const_cast<void*>(h.p)), h.ld, h.hs}; }
@@ -190,9 +218,16 @@ la_status la_attn_prefill_fwd(const void* q, const void* k, const void* v, float
   p.dev_error = dev_error;
   p.scale = scale;
   p.tokens = static_cast<int>(tokens), p.T = T, p.N = N, p.H = H, p.HK = HK, p.D = D;
+  laa::FwdMaps maps;
+  if ((st = encode_heads(&maps.q, a[0], 1, laa::kTile)) != LA_OK || (st = encode_heads(&maps.k, a[1], 1, laa::kTile)) != LA_OK ||
+      (st = encode_heads(&maps.v, a[2], 1, laa::kTile)) != LA_OK)
+    return st;
+  // tiles of the queries: exact in fixed-length mode, at most in packed mode
+  const int64_t tiles = cu_seqlens ? tokens / laa::kFwdRows + N : static_cast<int64_t>(N) * ((T + laa::kFwdRows - 1) / laa::kFwdRows);
   return launched(with_dim(D, [&](auto d) {
-    laa::simple_fwd_kernel<decltype(d)::value><<<dim3((p.tokens + 3) / 4, H), 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError();
+    constexpr int kD = decltype(d)::value;
+    return la_host::launch_pdl(laa::attn_fwd_kernel<kD>, blocks_for(tiles * H, ds->sms), laa::kFwdThreads, fwd_shared<kD>(),
+                               static_cast<cudaStream_t>(stream), maps, p);
   }));
 }
 

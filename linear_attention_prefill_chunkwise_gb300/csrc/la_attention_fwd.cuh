@@ -1,0 +1,408 @@
+// la_attention_fwd.cuh -- causal attention over whole prompts (include/la_attention.h) on the tensor
+// cores.
+//
+// A block takes 256 query rows of one head, as two tiles of 128, and walks over the sequence's keys,
+// 128 at a time, with an unnormalised output and a running maximum and sum per row:
+//     S = q k^T,  p = 2^(c S - m) with c = scale log2 e,  O += p v,  l += sum p;   o = O / l.
+// Warps 0-3 and 4-7 own one query tile each, a thread per row: S is read from tensor memory, p goes
+// back over it as BF16 (the operand of the second product; rounding it costs 2^-8 of each term, no
+// more than the output's own rounding), and the maximum m moves only when a row outgrows it by 2^8,
+// so that O is rarely rescaled and always by its owners, which need no extra warps for it.  Warp 8
+// issues the products: while one tile's softmax runs, the other tile's two products keep the tensor
+// cores busy (S_a, S_b, then p v and the next S of each in turn, in one queue, so that S can
+// overwrite p).  Warp 9 loads: queries once per item, keys and values through a ring.
+// The two tiles share keys and values, which halves their traffic from L2.
+//
+// Bound: the tensor cores at D = 128; at D = 64, where the products halve, the softmax.
+#pragma once
+
+#include "la_attention_tiles.cuh"
+
+namespace laa {
+
+constexpr int kFwdRows = 2 * kTile, kFwdThreads = 384, kItems = 4;
+// Registers: 3 x 168 at launch; a softmax thread holds a row of scores.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "register shares");
+constexpr float kSlack = 8.f;  // log2 of how far a row may outgrow its maximum
+
+template <int D>
+struct FwdShared {
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  TileMem<D> q[2];
+  TileMem<D> kv[kStages];
+  Item items[kItems];
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2];
+  uint64_t final_bar;
+  uint32_t bad[2][2][4];  // [item parity][tile][warp]: value rows that are not finite
+  uint32_t tmem;
+  int abort;
+};
+
+struct FwdMaps {
+  CUtensorMap q, k, v;
+};
+
+// Tiles of keys that query tile s of an item sees; 0 where it has no row.
+__device__ __forceinline__ int key_tiles(const Item& it, int s) {
+  const int r0 = it.tile * kFwdRows + s * kTile;
+  return r0 < it.len ? r0 / kTile + 1 : 0;
+}
+
+template <int D>
+__device__ __forceinline__ void fwd_load(FwdShared<D>& sm, const PrefillParams& p, const FwdMaps& maps, int lane,
+                                         volatile int* abort) {
+  constexpr int kStages = FwdShared<D>::kStages;
+  constexpr uint32_t kBytes = kBox * (D / 64);
+  const int group = p.H / p.HK;
+  ItemWalk walk(kFwdRows, p.H);
+  uint32_t slots = 0, q_loads[2] = {0, 0};
+  bool ok = true;
+  auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int head, int row) {
+    lap::mbar_arrive_expect_tx(bar, kBytes);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) lap::tma_load_3d(dst + b * kBox, map, bar, 64 * b, head, row);
+  };
+  for (uint32_t i = 0; ok; ++i) {
+    const uint32_t is = i % kItems;
+    if (!warp_wait(&sm.item_empty[is], ((i / kItems) & 1u) ^ 1u, abort)) break;
+    const Item it = walk.take(p, lane);
+    if (lane == 0) {
+      sm.items[is] = it;
+      lap::mbar_arrive(&sm.item_full[is]);
+    }
+    __syncwarp();
+    if (it.len < 0) break;
+    const int n = max(key_tiles(it, 0), key_tiles(it, 1)), hk = it.head / group;
+    for (int j = 0; j < 2 * n && ok; ++j) {
+      const uint32_t st = slots % kStages;
+      if (!(ok = warp_wait(&sm.kv_empty[st], ((slots / kStages) & 1u) ^ 1u, abort))) break;
+      if (lane == 0)
+        load(j & 1 ? &maps.v : &maps.k, sm.kv[st][0], &sm.kv_full[st], hk, it.lo + (j >> 1) * kTile);
+      ++slots;
+      if (j == 0)  // the first keys are on their way while the last item still reads its queries
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (key_tiles(it, s) == 0) continue;
+          if (!(ok = warp_wait(&sm.q_empty[s], (q_loads[s] & 1u) ^ 1u, abort))) break;
+          if (lane == 0) load(&maps.q, sm.q[s][0], &sm.q_full[s], it.head, it.lo + it.tile * kFwdRows + s * kTile);
+          ++q_loads[s];
+        }
+    }
+  }
+  // every load has landed before the block's shared memory is given up, also after an abort
+  if (lane == 0) {
+    for (uint32_t i = 0; i < static_cast<uint32_t>(kStages) && i < slots; ++i) {
+      const uint32_t j = slots - 1 - i;
+      drain(&sm.kv_full[j % kStages], (j / kStages) & 1u);
+    }
+    for (int s = 0; s < 2; ++s)
+      if (q_loads[s]) drain(&sm.q_full[s], (q_loads[s] - 1) & 1u);
+  }
+  __syncwarp();
+}
+
+template <int D>
+__device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, int lane, volatile int* abort) {
+  constexpr int kStages = FwdShared<D>::kStages;
+  uint32_t slots = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+  bool ok = true;
+  for (uint32_t i = 0; ok; ++i) {
+    const uint32_t is = i % kItems;
+    if (!warp_wait(&sm.item_full[is], (i / kItems) & 1u, abort)) break;
+    const Item it = sm.items[is];
+    warp_arrive(&sm.item_empty[is], lane);
+    if (it.len < 0) break;
+    const int n[2] = {key_tiles(it, 0), key_tiles(it, 1)};
+    const int most = max(n[0], n[1]);
+    auto slot_of = [&](int j, bool value) { return slots + 2 * j + value; };
+    auto wait_slot = [&](uint32_t x) { return warp_wait(&sm.kv_full[x % kStages], (x / kStages) & 1u, abort); };
+    auto scores = [&](int s, uint32_t x) {
+      lap::tc_fence_after();
+      if (lane == 0) {
+        product_rows<D>(tmem + s * kTile, desc_rows(sm.q[s]), desc_rows(sm.kv[x % kStages]));
+        lap::mma_commit(&sm.s_full[s]);
+      }
+    };
+    if (!(ok = wait_slot(slot_of(0, false)))) break;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (!ok || !n[s]) continue;
+      if (!(ok = warp_wait(&sm.q_full[s], q_uses[s] & 1u, abort))) continue;
+      scores(s, slot_of(0, false));
+      if (n[s] == 1 && lane == 0) lap::mma_commit(&sm.q_empty[s]);
+    }
+    if (!ok) break;
+    if (lane == 0) lap::mma_commit(&sm.kv_empty[slot_of(0, false) % kStages]);
+    for (int j = 0; j < most && ok; ++j) {
+      const uint32_t xv = slot_of(j, true), xk = slot_of(j + 1, false);
+      bool keys = false;
+      if (!(ok = wait_slot(xv))) break;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!ok || j >= n[s]) continue;
+        if (!(ok = warp_wait(&sm.p_ready[s], p_uses[s]++ & 1u, abort))) continue;
+        if (j == 0 && !(ok = warp_wait(&sm.o_free[s], (q_uses[s] & 1u) ^ 1u, abort))) continue;
+        lap::tc_fence_after();
+        if (lane == 0)
+          product_tmem<D>(tmem + 2 * kTile + s * D, tmem + s * kTile, desc_columns(sm.kv[xv % kStages]), j > 0);
+        if (j == n[s] - 1) {
+          if (lane == 0) lap::mma_commit(&sm.o_full[s]);
+          ++q_uses[s];
+        } else {
+          if (!keys && !(ok = wait_slot(xk))) continue;
+          keys = true;
+          scores(s, xk);
+          if (j + 1 == n[s] - 1 && lane == 0) lap::mma_commit(&sm.q_empty[s]);
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) {
+        lap::mma_commit(&sm.kv_empty[xv % kStages]);
+        if (keys) lap::mma_commit(&sm.kv_empty[xk % kStages]);
+      }
+      __syncwarp();
+    }
+    slots += 2 * most;
+  }
+  if (lane == 0) {
+    lap::mma_commit(&sm.final_bar);
+    drain(&sm.final_bar, 0);  // every product has retired, also after an abort
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void load_scores(uint32_t t_s, float (&s)[kTile]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float part[32];
+    lap::tmem_ld32(t_s + 32 * g, part);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[32 * g + i] = part[i];
+  }
+}
+
+// One tile of scores of this thread's row, in registers, to probabilities in tensor memory.  `keep`:
+// keys that the row sees (128: all).  Returns the sum of the probabilities as two partial sums.
+template <bool kMasked>
+__device__ __forceinline__ uint64_t probabilities(float (&s)[kTile], uint32_t t_p, float c, float m, int keep) {
+  const uint64_t c2 = lap::f2_pack(c, c), m2 = lap::f2_pack(-m, -m);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = 32 * g + 2 * i;
+      const float2 z = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, m2));
+      float a = lap::exp2_approx(z.x), b = lap::exp2_approx(z.y);
+      if (kMasked) {
+        a = k < keep ? a : 0.f;
+        b = k + 1 < keep ? b : 0.f;
+      }
+      u[i] = lap::pack_bf16x2(a, b);
+      sum[i & 1] = lap::f2_add(sum[i & 1], lap::f2_pack(a, b));
+    }
+    lap::tmem_st16_nowait(t_p + 16 * g, u);
+  }
+  lap::tmem_wait_st();
+  return lap::f2_add(sum[0], sum[1]);
+}
+
+// c times the largest (c < 0: smallest) of the row's first `keep` scores.
+template <bool kMasked>
+__device__ __forceinline__ float top_score(float (&s)[kTile], float c, int keep) {
+  const bool up = c >= 0.f;
+  if (kMasked) {
+    const float out = up ? -3.4e38f : 3.4e38f;
+#pragma unroll
+    for (int k = 0; k < kTile; ++k) s[k] = k < keep ? s[k] : out;
+  }
+  float t[4] = {s[0], s[1], s[2], s[3]};
+  if (up) {
+#pragma unroll
+    for (int k = 4; k < kTile; k += 8)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = fmaxf(fmaxf(t[e], s[k + e]), k + 4 + e < kTile ? s[k + 4 + e] : t[e]);
+    return c * fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  }
+#pragma unroll
+  for (int k = 4; k < kTile; ++k) t[k & 3] = fminf(t[k & 3], s[k]);
+  return c * fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+}
+
+// Multiplies this thread's row of O in tensor memory.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t t_o, float f) {
+  const uint64_t f2 = lap::f2_pack(f, f);
+#pragma unroll 1
+  for (int g = 0; g < D / 16; ++g) {
+    float o[16];
+    uint32_t u[16];
+    lap::tmem_ld16(t_o + 16 * g, o);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float2 r = lap::f2_unpack(lap::f2_mul(lap::f2_pack(o[i], o[i + 1]), f2));
+      u[i] = __float_as_uint(r.x);
+      u[i + 1] = __float_as_uint(r.y);
+    }
+    lap::tmem_st16_nowait(t_o + 16 * g, u);
+  }
+  lap::tmem_wait_st();
+}
+
+// A row's running maximum (of c S) and sum; the maximum moves when some row of the warp outgrows its
+// own by kSlack.  Whole-warp call; `first`: nothing has been added yet.
+template <int D>
+__device__ __forceinline__ void move_top(float z, bool first, uint32_t t_o, float& m, uint64_t& l) {
+  if (first) {
+    m = z;
+  } else if (__any_sync(0xFFFFFFFFu, z > m + kSlack)) {
+    const float top = fmaxf(m, z), f = top == m ? 1.f : lap::exp2_approx(m - top);
+    m = top;
+    l = lap::f2_mul(l, lap::f2_pack(f, f));
+    rescale_row<D>(t_o, f);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
+                                            volatile int* abort) {
+  constexpr int kStages = FwdShared<D>::kStages;
+  const int s = tid / kTile, row = tid % kTile, warp = row / 32, lane = tid % 32;
+  const uint32_t t_s = tmem + s * kTile + (static_cast<uint32_t>(32 * warp) << 16);
+  const uint32_t t_o = tmem + 2 * kTile + s * D + (static_cast<uint32_t>(32 * warp) << 16);
+  const float c = p.scale * kLog2e;
+  uint32_t slots = 0, tiles = 0, uses = 0;
+  for (uint32_t i = 0;; ++i) {
+    const uint32_t is = i % kItems;
+    if (!warp_wait(&sm.item_full[is], (i / kItems) & 1u, abort)) return;
+    const Item it = sm.items[is];
+    warp_arrive(&sm.item_empty[is], lane);
+    if (it.len < 0) return;
+    const int n = key_tiles(it, s), first_slot = slots;
+    slots += 2 * max(n, key_tiles(it, s ^ 1));
+    if (n == 0) continue;
+    const int r0 = it.tile * kFwdRows + s * kTile;
+    float m = 0.f;
+    uint64_t l = 0;
+    float scores[kTile];
+    for (int j = 0; j < n - 1; ++j) {
+      if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
+      lap::tc_fence_after();
+      load_scores(t_s, scores);
+      move_top<D>(top_score<false>(scores, c, kTile), j == 0, t_o, m, l);
+      const uint64_t sum = probabilities<false>(scores, t_s, c, m, kTile);
+      lap::tc_fence_before();
+      warp_arrive(&sm.p_ready[s], lane);
+      l = lap::f2_add(l, sum);
+    }
+    {
+      // the tile on the diagonal: row r sees its keys 0 .. r; its values are made harmless first
+      const uint32_t x = first_slot + 2 * (n - 1) + 1;
+      if (!warp_wait(&sm.kv_full[x % kStages], (x / kStages) & 1u, abort)) return;
+      const uint32_t bad =
+          __ballot_sync(0xFFFFFFFFu, clean_row<D>(sm.kv[x % kStages], row, r0 + row >= it.len));
+      if (lane == 0) sm.bad[i & 1][s][warp] = bad;
+      lap::fence_proxy_async_smem();
+      if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
+      lap::tc_fence_after();
+      load_scores(t_s, scores);
+      move_top<D>(top_score<true>(scores, c, row + 1), n == 1, t_o, m, l);
+      const uint64_t sum = probabilities<true>(scores, t_s, c, m, row + 1);
+      lap::tc_fence_before();
+      warp_arrive(&sm.p_ready[s], lane);
+      l = lap::f2_add(l, sum);
+    }
+    const float2 lp = lap::f2_unpack(l);
+    const float total = lp.x + lp.y, inv = 1.f / total;
+    const int64_t at = it.lo + r0 + row;
+    const bool live = r0 + row < it.len;
+    if (!warp_wait(&sm.o_full[s], uses++ & 1u, abort)) return;
+    lap::tc_fence_after();
+    uint32_t bad[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) bad[w] = sm.bad[i & 1][s][w];
+    const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
+    bf16* out = p.o.row(at, it.head);
+#pragma unroll 1
+    for (int g = 0; g < D / 32; ++g) {
+      float o[32];
+      lap::tmem_ld32(t_o + 32 * g, o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] *= inv;
+      if (any_bad)
+        for (int r = 0; r <= row; ++r)
+          if (bad[r >> 5] >> (r & 31) & 1u) restore(o, p.v.row(it.lo + r0 + r, it.head / (p.H / p.HK)) + 32 * g);
+      if (live) store_row32(out + 32 * g, o);
+    }
+    lap::tc_fence_before();
+    warp_arrive(&sm.o_free[s], lane);
+    if (p.lse && live) p.lse[static_cast<int64_t>(it.head) * p.tokens + at] = (m + log2f(total)) * kLn2;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  FwdShared<D>& sm =
+      *reinterpret_cast<FwdShared<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  volatile int* abort = &sm.abort;
+  lap::griddep_wait();
+  lap::griddep_launch_dependents();
+  if (warp == 8) {
+    lap::tmem_alloc(&sm.tmem, 512);
+    lap::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kItems; ++i) {
+      lap::mbar_init(&sm.item_full[i], 1);
+      lap::mbar_init(&sm.item_empty[i], 9);
+    }
+    for (int i = 0; i < FwdShared<D>::kStages; ++i) {
+      lap::mbar_init(&sm.kv_full[i], 1);
+      lap::mbar_init(&sm.kv_empty[i], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      lap::mbar_init(&sm.q_full[s], 1);
+      lap::mbar_init(&sm.q_empty[s], 1);
+      lap::mbar_init(&sm.s_full[s], 1);
+      lap::mbar_init(&sm.p_ready[s], 4);
+      lap::mbar_init(&sm.o_full[s], 1);
+      lap::mbar_init(&sm.o_free[s], 4);
+    }
+    lap::mbar_init(&sm.final_bar, 1);
+    sm.abort = 0;
+    lap::fence_mbar_init();
+    lap::tma_prefetch_desc(&maps.q);
+    lap::tma_prefetch_desc(&maps.k);
+    lap::tma_prefetch_desc(&maps.v);
+  }
+  lap::tc_fence_before();
+  __syncthreads();
+  lap::tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  if (warp < 8) {
+    lap::registers_grow<kSoftmaxRegs>();
+    fwd_softmax<D>(sm, p, tmem, tid, abort);
+  } else {
+    lap::registers_shrink<kOtherRegs>();
+    if (warp == 8)
+      fwd_products<D>(sm, tmem, lane, abort);
+    else if (warp == 9)
+      fwd_load<D>(sm, p, maps, lane, abort);
+  }
+  lap::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sm.abort && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
+  if (warp == 8) {
+    __syncwarp();
+    lap::tc_fence_after();
+    lap::tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace laa

@@ -1,0 +1,205 @@
+// la_attention_tiles.cuh -- what the tensor-core attention kernels share: tiles of 128 rows in shared
+// memory, the products between them, and the walk over a batch's query tiles.
+//
+// A tile is 128 rows of D BF16 values as D / 64 boxes of 64 columns (128-byte rows, 128-byte
+// swizzle, 16 KiB each), the form in which a tensor map with 64-column boxes delivers rows of a
+// tensor of heads and in which both a product along D (K-major) and one along the rows (MN-major)
+// can read it.
+#pragma once
+
+#include "la_attention_params.cuh"
+#include "sm103_ptx.cuh"
+
+namespace laa {
+
+constexpr int kTile = 128;                 // rows of a tile: the M of one MMA
+constexpr uint32_t kBox = kTile * 128;     // bytes of a box
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D>
+using TileMem = uint8_t[D / 64][kBox];
+
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) { return base + (bytes >> 4); }
+// A tile as an operand whose rows are M or N and whose columns are summed over ...
+__device__ __forceinline__ uint64_t desc_rows(const void* tile) {
+  return lap::sdesc_sw128(lap::smem_u32(tile), 16, 1024);
+}
+// ... and as one whose columns are M or N and whose rows are summed over.
+__device__ __forceinline__ uint64_t desc_columns(const void* tile) {
+  return lap::sdesc_sw128(lap::smem_u32(tile), kBox, 1024);
+}
+// Byte offset of the kk-th 16 columns (desc_rows) or rows (desc_columns) of a tile.
+__device__ __forceinline__ uint32_t step_columns(int kk) { return (kk >> 2) * kBox + (kk & 3) * 32; }
+__device__ __forceinline__ uint32_t step_rows(int kk) { return kk * 2048; }
+
+// d (+)= a b^T over D columns: scores, dP.
+template <int D>
+__device__ __forceinline__ void product_rows(uint32_t d, uint64_t a, uint64_t b) {
+  constexpr uint32_t id = lap::idesc_bf16_f32(kTile, kTile, false, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    lap::mma_ss(d, desc_at(a, step_columns(kk)), desc_at(b, step_columns(kk)), id, kk > 0);
+}
+// d (+)= a b with a [128 rows, 128 summed] BF16 in tensor memory (64 columns) and b's rows summed.
+template <int D>
+__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint64_t b, bool accumulate) {
+  constexpr uint32_t id = lap::idesc_bf16_f32(kTile, D, false, true);
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    lap::mma_ts(d, a + 8 * kk, desc_at(b, step_rows(kk)), id, accumulate || kk > 0);
+}
+
+// Whole-warp wait; false once the block gives up: after a wait of kWaitLimitNs, which sets *abort.
+// (Inline: a kernel that moves registers between its warpgroups makes no calls.)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool ok = lap::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = lap::globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+      ok = lap::mbar_try_wait(bar, parity);
+      if (ok) break;
+      if ((i & 31u) == 0u) {
+        if (*abort) break;
+        if (lap::globaltimer_ns() - t0 > lap::kWaitLimitNs) {
+          *abort = 1;
+          break;
+        }
+      }
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+// lap::mbar_wait_drain, inline.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = lap::globaltimer_ns();
+  while (!lap::mbar_try_wait(bar, parity))
+    if (lap::globaltimer_ns() - t0 > lap::kDrainLimitNs) return;
+}
+// One arrival for the warp, after all of its lanes' work.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) lap::mbar_arrive(bar);
+}
+
+// A tile of `rows` query rows of a sequence, for one head; len < 0 ends the list.
+struct Item {
+  int lo, len, tile, head;
+};
+
+// The block's items, every gridDim.x-th of all: heads innermost, so that blocks that run side by
+// side read the same keys; then tiles, a sequence's last (which sees most keys) first; a batch of
+// one length takes the last tiles of all its sequences first.  Packed sequences are walked 32 at a
+// time by the warp's lanes.  Whole-warp calls.
+struct ItemWalk {
+  int64_t next;  // item number
+  int n0 = 0, rows, heads;
+  int64_t before = 0;  // tiles before sequence n0
+  int lo = 0, len = 0, tiles = 0, upto = 0;  // this lane's sequence n0 + lane; tiles up to it
+  bool loaded = false;
+
+  __device__ ItemWalk(int rows, int heads) : next(blockIdx.x), rows(rows), heads(heads) {}
+
+  __device__ __forceinline__ void load(const PrefillParams& p, int lane) {
+    const int n = n0 + lane;
+    int hi = 0;
+    lo = 0;
+    if (n < p.N && !sequence_rows(p, n, lo, hi) && blockIdx.x == 0 && p.dev_error) atomicOr(p.dev_error, kErrSeqlens);
+    len = hi - lo;
+    tiles = (len + rows - 1) / rows;
+    upto = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    loaded = true;
+  }
+
+  __device__ __forceinline__ Item take(const PrefillParams& p, int lane) {
+    const int64_t t = next / heads;
+    Item it{0, -1, 0, static_cast<int>(next - t * heads)};
+    next += gridDim.x;
+    if (!p.cu_seqlens) {
+      const int tiles_each = (p.T + rows - 1) / rows;
+      if (t < static_cast<int64_t>(p.N) * tiles_each) {
+        const int level = static_cast<int>(t / p.N);
+        it.lo = (static_cast<int>(t) - level * p.N) * p.T;
+        it.len = p.T;
+        it.tile = tiles_each - 1 - level;
+      }
+      return it;
+    }
+    while (n0 < p.N) {
+      if (!loaded) load(p, lane);
+      const uint32_t reach = __ballot_sync(0xFFFFFFFFu, before + upto > t);
+      if (reach) {
+        const int at = __ffs(reach) - 1;
+        it.lo = __shfl_sync(0xFFFFFFFFu, lo, at);
+        it.len = __shfl_sync(0xFFFFFFFFu, len, at);
+        it.tile = static_cast<int>(before + __shfl_sync(0xFFFFFFFFu, upto, at) - 1 - t);
+        return it;
+      }
+      before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      n0 += 32;
+      loaded = false;
+    }
+    return it;
+  }
+};
+
+// Bits of a packed pair of BF16 values that are infinite or NaN (bit 15, bit 31).
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// Makes a row of a tile of values harmless where its probabilities are zero because of a mask:
+// 0 * inf is NaN.  A row behind the sequence becomes zero; in a row within it, what is not finite
+// becomes zero and is added again by `restore`.  Returns whether the row held such a value.
+template <int D>
+__device__ __forceinline__ bool clean_row(TileMem<D>& tile, int row, bool behind) {
+  bool found = false;
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b) {
+    uint4* at = reinterpret_cast<uint4*>(tile[b] + row * 128);
+    if (behind) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) at[c] = make_uint4(0, 0, 0, 0);
+    } else {
+      uint32_t any = 0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int x = c ^ (row & 7);  // lanes of neighbouring rows read different banks
+        const uint4 v = at[x];
+        any |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
+      }
+      if (any) {
+        found = true;
+        uint32_t* w = reinterpret_cast<uint32_t*>(at);
+        for (int c = 0; c < 32; ++c) {
+          const uint32_t f = not_finite(w[c]);
+          w[c] &= ~((f >> 15 & 1u) * 0xFFFFu) & ~((f >> 31) * 0xFFFF0000u);
+        }
+      }
+    }
+  }
+  return found;
+}
+
+// Adds the values of a row that are not finite to a part of an output row.
+template <int N>
+__device__ __forceinline__ void restore(float (&o)[N], const bf16* v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float x = __bfloat162float(v[i]);
+    if (!isfinite(x)) o[i] += x;
+  }
+}
+
+// An output row's part of 32 columns.
+__device__ __forceinline__ void store_row32(bf16* p, const float (&o)[32]) {
+  uint4* out = reinterpret_cast<uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    out[i] = make_uint4(lap::pack_bf16x2(o[8 * i], o[8 * i + 1]), lap::pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                        lap::pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), lap::pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+}
+
+}  // namespace laa
