@@ -10,6 +10,7 @@
 #include "la_attention_commit.cuh"
 #include "la_attention_fwd.cuh"
 #include "la_attention_simple.cuh"
+#include "la_attention_verify.cuh"
 #include "la_heads_common.h"
 #include "la_host_common.h"
 
@@ -27,11 +28,16 @@ la_host::DeviceState g_dev[la_host::kMaxDevices];
 template <int D>
 constexpr int fwd_shared() { return static_cast<int>(sizeof(laa::FwdShared<D>)) + 1024; }
 
+template <int D>
+constexpr int verify_shared() { return static_cast<int>(sizeof(laa::VerifyShared<D>)) + 1024; }
+
 la_status device(la_host::DeviceState** ds) {
   return la_host::current_device(g_dev, ds, [] {
     const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
     cudaError_t e = cudaFuncSetAttribute(laa::attn_fwd_kernel<64>, most, fwd_shared<64>());
     if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_fwd_kernel<128>, most, fwd_shared<128>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_verify_kernel<64>, most, verify_shared<64>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_verify_kernel<128>, most, verify_shared<128>());
     return e;
   });
 }
@@ -45,6 +51,13 @@ constexpr int64_t kMostTokens = INT32_MAX - 1024;  // row numbers and tile ends 
 HeadsArg rows(const void* p, int64_t ld, int64_t hs, int64_t tokens, int heads, int D, const char* name) {
   return heads_arg(p, ld, hs, tokens, heads, D, 2, 16, name);
 }
+
+struct CacheArg {
+  const void* p;
+  int64_t pages, tokens, heads;  // extents
+  int64_t ps, ts, hs;            // strides
+  const char* name;
+};
 
 // Map over a tensor of heads with boxes of `heads` heads x `tokens` tokens x 64 columns (a head's rows
 // of 128 bytes, 128-byte swizzle).
@@ -60,6 +73,39 @@ la_status encode_heads(CUtensorMap* map, const HeadsArg& h, int heads, int token
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(LA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", h.name, (int)r);
   return LA_OK;
+}
+
+// Map over the cache with boxes of `rows` rows of one page and head x 64 columns.
+la_status encode_cache(CUtensorMap* map, const CacheArg& c, int D, int rows) {
+  auto enc = la_host::tensor_map_encoder();
+  if (!enc) return fail(LA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the CUDA driver");
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.tokens),
+                              static_cast<cuuint64_t>(c.pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.hs) * 2, static_cast<cuuint64_t>(c.ts) * 2,
+                                 static_cast<cuuint64_t>(c.ps) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(c.p), dims, strides, box, ones,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(LA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", c.name, (int)r);
+  return LA_OK;
+}
+
+// How a call's items are cut: see laa::VerifyShape.
+laa::VerifyShape verify_shape(int T, int H, int HK, bool mask, int page_size, bool paged) {
+  laa::VerifyShape v{};
+  v.group = H / HK;
+  v.per_tile = std::min(T, laa::kTile / v.group);
+  v.rows = v.per_tile * v.group;
+  v.q_tiles = (T + v.per_tile - 1) / v.per_tile;
+  v.box = laa::kTile;
+  if (paged)
+    while (page_size % v.box) v.box /= 2;
+  v.draft_box = std::min(laa::kTile, (T + 7) / 8 * 8);
+  for (int i = 0; i < v.q_tiles; ++i)
+    v.drafts += mask ? 1 : static_cast<int>((std::min<int64_t>(T, (i + int64_t(1)) * v.per_tile) + laa::kTile - 1) / laa::kTile);
+  return v;
 }
 
 // Blocks for at most this many items of work, one per SM.
@@ -117,12 +163,6 @@ la_status check_tensors(const HeadsArg* args, int n, int n_out, const RowSpan* f
 
 // ---------------------------------------------------------------- the cache
 
-struct CacheArg {
-  const void* p;
-  int64_t pages, tokens, heads;  // extents
-  int64_t ps, ts, hs;            // strides
-  const char* name;
-};
 
 // Strides that keep every row of the cache apart (its three outer axes in some order), and the
 // cache as rows for the overlap checks: the outer axes that lie gaplessly within one another are
@@ -291,7 +331,8 @@ la_status la_attn_verify_workspace(int B, int T, int H, int HK, int D, size_t* b
   const la_status st = check_heads_of(H, HK, D);
   if (st != LA_OK) return st;
   if (B < 0 || T < 1) return fail(LA_ERR_INVALID_ARGUMENT, "B must be >= 0 and T >= 1 (got %d, %d)", B, T);
-  *bytes = 256;
+  if (H / HK > laa::kTile) return fail(LA_ERR_UNSUPPORTED, "H / HK up to %d is implemented (got %d)", laa::kTile, H / HK);
+  *bytes = la_host::align256(laa::verify_part_bytes(verify_shape(T, H, HK, false, 16, false).rows, D));
   return LA_OK;
 }
 
@@ -340,13 +381,28 @@ la_status la_attn_verify(const void* q, const void* k, const void* v, float scal
   p.cache_lens = cache_lens;
   p.page_table = page_table;
   p.mask = mask;
-  p.part = static_cast<float*>(workspace);
   p.dev_error = dev_error;
   p.scale = scale;
   p.B = B, p.T = T, p.H = H, p.HK = HK, p.D = D, p.pages = pages, p.page_size = page_size, p.table_width = table_width;
+  p.part = workspace;
+  const laa::VerifyShape shape = verify_shape(T, H, HK, mask != nullptr, page_size, page_table != nullptr);
+  laa::VerifyMaps maps;
+  if ((st = encode_heads(&maps.q, a[0], shape.group, shape.per_tile)) != LA_OK ||
+      (st = encode_heads(&maps.k, a[1], 1, shape.draft_box)) != LA_OK ||
+      (st = encode_heads(&maps.v, a[2], 1, shape.draft_box)) != LA_OK ||
+      (st = encode_cache(&maps.k_cache, kc, D, shape.box)) != LA_OK || (st = encode_cache(&maps.v_cache, vc, D, shape.box)) != LA_OK)
+    return st;
+  const int64_t room = page_table ? static_cast<int64_t>(table_width) * page_size : page_size;
+  const int64_t most = static_cast<int64_t>(B) * HK * (shape.q_tiles * ((room + laa::kTile - 1) / laa::kTile) + shape.drafts);
+  const int blocks = blocks_for(most, std::min(ds->sms, laa::kVerifyBlocks));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launched(with_dim(D, [&](auto d) {
-    laa::simple_verify_kernel<decltype(d)::value><<<dim3(static_cast<unsigned>(tokens), H), 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError();
+    constexpr int kD = decltype(d)::value;
+    const cudaError_t ce = la_host::launch_pdl(laa::attn_verify_kernel<kD>, blocks, laa::kVerifyThreads, verify_shared<kD>(), s,
+                                               maps, p, shape);
+    if (ce != cudaSuccess) return ce;
+    return la_host::launch_pdl(laa::attn_join_kernel<kD>, dim3(blocks, std::min(laa::kJoinShares, shape.rows)), laa::kJoinThreads,
+                               0, s, p, shape);
   }));
 }
 

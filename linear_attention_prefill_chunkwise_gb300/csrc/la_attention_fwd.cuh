@@ -2,12 +2,10 @@
 // cores.
 //
 // A block takes 256 query rows of one head, as two tiles of 128, and walks over the sequence's keys,
-// 128 at a time, with an unnormalised output and a running maximum and sum per row:
-//     S = q k^T,  p = 2^(c S - m) with c = scale log2 e,  O += p v,  l += sum p;   o = O / l.
-// Warps 0-3 and 4-7 own one query tile each, a thread per row: S is read from tensor memory, p goes
-// back over it as BF16 (the operand of the second product; rounding it costs 2^-8 of each term, no
-// more than the output's own rounding), and the maximum m moves only when a row outgrows it by 2^8,
-// so that O is rarely rescaled and always by its owners, which need no extra warps for it.  Warp 8
+// 128 at a time, with an unnormalised output and a running maximum and sum per row.
+// Warps 0-3 and 4-7 own one query tile each, a thread per row: S is read from tensor memory and p goes
+// back over it as the operand of the second product; O is rarely rescaled and always by its owners,
+// which need no extra warps for it.  Warp 8
 // issues the products: while one tile's softmax runs, the other tile's two products keep the tensor
 // cores busy (S_a, S_b, then p v and the next S of each in turn, in one queue, so that S can
 // overwrite p).  Warp 9 loads: queries once per item, keys and values through a ring.
@@ -16,7 +14,7 @@
 // Bound: the tensor cores at D = 128; at D = 64, where the products halve, the softmax.
 #pragma once
 
-#include "la_attention_tiles.cuh"
+#include "la_attention_softmax.cuh"
 
 namespace laa {
 
@@ -24,8 +22,6 @@ constexpr int kFwdRows = 2 * kTile, kFwdThreads = 384, kItems = 4;
 // Registers: 3 x 168 at launch; a softmax thread holds a row of scores.
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "register shares");
-constexpr float kSlack = 8.f;  // log2 of how far a row may outgrow its maximum
-
 template <int D>
 struct FwdShared {
   static constexpr int kStages = D == 128 ? 5 : 8;
@@ -173,99 +169,6 @@ __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, in
   __syncwarp();
 }
 
-__device__ __forceinline__ void load_scores(uint32_t t_s, float (&s)[kTile]) {
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    float part[32];
-    lap::tmem_ld32(t_s + 32 * g, part);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[32 * g + i] = part[i];
-  }
-}
-
-// One tile of scores of this thread's row, in registers, to probabilities in tensor memory.  `keep`:
-// keys that the row sees (128: all).  Returns the sum of the probabilities as two partial sums.
-template <bool kMasked>
-__device__ __forceinline__ uint64_t probabilities(float (&s)[kTile], uint32_t t_p, float c, float m, int keep) {
-  const uint64_t c2 = lap::f2_pack(c, c), m2 = lap::f2_pack(-m, -m);
-  uint64_t sum[2] = {0, 0};
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint32_t u[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int k = 32 * g + 2 * i;
-      const float2 z = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, m2));
-      float a = lap::exp2_approx(z.x), b = lap::exp2_approx(z.y);
-      if (kMasked) {
-        a = k < keep ? a : 0.f;
-        b = k + 1 < keep ? b : 0.f;
-      }
-      u[i] = lap::pack_bf16x2(a, b);
-      sum[i & 1] = lap::f2_add(sum[i & 1], lap::f2_pack(a, b));
-    }
-    lap::tmem_st16_nowait(t_p + 16 * g, u);
-  }
-  lap::tmem_wait_st();
-  return lap::f2_add(sum[0], sum[1]);
-}
-
-// c times the largest (c < 0: smallest) of the row's first `keep` scores.
-template <bool kMasked>
-__device__ __forceinline__ float top_score(float (&s)[kTile], float c, int keep) {
-  const bool up = c >= 0.f;
-  if (kMasked) {
-    const float out = up ? -3.4e38f : 3.4e38f;
-#pragma unroll
-    for (int k = 0; k < kTile; ++k) s[k] = k < keep ? s[k] : out;
-  }
-  float t[4] = {s[0], s[1], s[2], s[3]};
-  if (up) {
-#pragma unroll
-    for (int k = 4; k < kTile; k += 8)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = fmaxf(fmaxf(t[e], s[k + e]), k + 4 + e < kTile ? s[k + 4 + e] : t[e]);
-    return c * fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-  }
-#pragma unroll
-  for (int k = 4; k < kTile; ++k) t[k & 3] = fminf(t[k & 3], s[k]);
-  return c * fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
-}
-
-// Multiplies this thread's row of O in tensor memory.
-template <int D>
-__device__ __forceinline__ void rescale_row(uint32_t t_o, float f) {
-  const uint64_t f2 = lap::f2_pack(f, f);
-#pragma unroll 1
-  for (int g = 0; g < D / 16; ++g) {
-    float o[16];
-    uint32_t u[16];
-    lap::tmem_ld16(t_o + 16 * g, o);
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float2 r = lap::f2_unpack(lap::f2_mul(lap::f2_pack(o[i], o[i + 1]), f2));
-      u[i] = __float_as_uint(r.x);
-      u[i + 1] = __float_as_uint(r.y);
-    }
-    lap::tmem_st16_nowait(t_o + 16 * g, u);
-  }
-  lap::tmem_wait_st();
-}
-
-// A row's running maximum (of c S) and sum; the maximum moves when some row of the warp outgrows its
-// own by kSlack.  Whole-warp call; `first`: nothing has been added yet.
-template <int D>
-__device__ __forceinline__ void move_top(float z, bool first, uint32_t t_o, float& m, uint64_t& l) {
-  if (first) {
-    m = z;
-  } else if (__any_sync(0xFFFFFFFFu, z > m + kSlack)) {
-    const float top = fmaxf(m, z), f = top == m ? 1.f : lap::exp2_approx(m - top);
-    m = top;
-    l = lap::f2_mul(l, lap::f2_pack(f, f));
-    rescale_row<D>(t_o, f);
-  }
-}
-
 template <int D>
 __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
                                             volatile int* abort) {
@@ -274,6 +177,7 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
   const uint32_t t_s = tmem + s * kTile + (static_cast<uint32_t>(32 * warp) << 16);
   const uint32_t t_o = tmem + 2 * kTile + s * D + (static_cast<uint32_t>(32 * warp) << 16);
   const float c = p.scale * kLog2e;
+  const Keys keys{row + 1, {0, 0}};
   uint32_t slots = 0, tiles = 0, uses = 0;
   for (uint32_t i = 0;; ++i) {
     const uint32_t is = i % kItems;
@@ -292,25 +196,35 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
       if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
       lap::tc_fence_after();
       load_scores(t_s, scores);
-      move_top<D>(top_score<false>(scores, c, kTile), j == 0, t_o, m, l);
-      const uint64_t sum = probabilities<false>(scores, t_s, c, m, kTile);
+      const float z = top_score<kAll>(scores, c, keys);
+      // S follows the last product into O in the queue, so O may be rescaled
+      if (j == 0)
+        m = z;
+      else if (__any_sync(0xFFFFFFFFu, z > m + kSlack))
+        rescale_row<D>(t_o, outgrow(z, m, l));
+      const uint64_t sum = probabilities<kAll>(scores, t_s, c, m, keys);
       lap::tc_fence_before();
       warp_arrive(&sm.p_ready[s], lane);
       l = lap::f2_add(l, sum);
     }
     {
-      // the tile on the diagonal: row r sees its keys 0 .. r; its values are made harmless first
+      // the tile on the diagonal: row r sees its keys 0 .. r; its values are made harmless first.  (The
+      // scores, made from the slot before, prove that the ring has come to this phase of the values'.)
       const uint32_t x = first_slot + 2 * (n - 1) + 1;
+      if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
       if (!warp_wait(&sm.kv_full[x % kStages], (x / kStages) & 1u, abort)) return;
       const uint32_t bad =
           __ballot_sync(0xFFFFFFFFu, clean_row<D>(sm.kv[x % kStages], row, r0 + row >= it.len));
       if (lane == 0) sm.bad[i & 1][s][warp] = bad;
       lap::fence_proxy_async_smem();
-      if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
       lap::tc_fence_after();
       load_scores(t_s, scores);
-      move_top<D>(top_score<true>(scores, c, row + 1), n == 1, t_o, m, l);
-      const uint64_t sum = probabilities<true>(scores, t_s, c, m, row + 1);
+      const float z = top_score<kFirst>(scores, c, keys);
+      if (n == 1)
+        m = z;
+      else if (__any_sync(0xFFFFFFFFu, z > m + kSlack))
+        rescale_row<D>(t_o, outgrow(z, m, l));
+      const uint64_t sum = probabilities<kFirst>(scores, t_s, c, m, keys);
       lap::tc_fence_before();
       warp_arrive(&sm.p_ready[s], lane);
       l = lap::f2_add(l, sum);

@@ -39,7 +39,7 @@ struct CacheParams {
   int64_t kp, kt, kh, vp, vt, vh, ld_table;
   const int32_t *cache_lens, *page_table, *cu_seqlens, *accepted_len, *path;
   const int64_t* mask;
-  float* part;  // workspace
+  void* part;  // workspace
   int* dev_error;
   float scale;
   int B, T, H, HK, D, pages, page_size, table_width;

@@ -1,0 +1,116 @@
+// la_attention_softmax.cuh -- a thread's row of scores in tensor memory to probabilities, with a
+// running maximum and sum, as the forward kernels share it.
+//
+//     p = 2^(c S - m) with c = scale log2 e,  O += p v,  l += sum p;   o = O / l
+// The maximum m moves only when a row outgrows it by 2^kSlack, so that O is rarely rescaled.  p is
+// rounded to BF16 as an operand of the product with v: 2^-8 of each term, no more than the
+// output's own rounding; l sums the values before that rounding.
+#pragma once
+
+#include "la_attention_tiles.cuh"
+
+namespace laa {
+
+constexpr float kSlack = 8.f;  // log2 of how far a row may outgrow its maximum
+
+// Which of a tile's keys a row sees: all, its first `keep`, or (64 at most) those whose bits are set.
+enum Seen { kAll, kFirst, kBits };
+struct Keys {
+  int keep;
+  uint32_t bits[2];
+};
+template <Seen kSeen>
+__device__ __forceinline__ bool sees(const Keys& keys, int k) {
+  if (kSeen == kAll) return true;
+  if (kSeen == kFirst) return k < keys.keep;
+  return k < 64 && (keys.bits[(k >> 5) & 1] >> (k & 31) & 1u);
+}
+
+__device__ __forceinline__ void load_scores(uint32_t t_s, float (&s)[kTile]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float part[32];
+    lap::tmem_ld32(t_s + 32 * g, part);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[32 * g + i] = part[i];
+  }
+}
+
+// The row's probabilities over its scores in tensor memory; returns their sum as two partial sums.
+template <Seen kSeen>
+__device__ __forceinline__ uint64_t probabilities(float (&s)[kTile], uint32_t t_p, float c, float m, const Keys& keys) {
+  const uint64_t c2 = lap::f2_pack(c, c), m2 = lap::f2_pack(-m, -m);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = 32 * g + 2 * i;
+      const float2 z = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, m2));
+      float a = lap::exp2_approx(z.x), b = lap::exp2_approx(z.y);
+      if (kSeen != kAll) {
+        a = sees<kSeen>(keys, k) ? a : 0.f;
+        b = sees<kSeen>(keys, k + 1) ? b : 0.f;
+      }
+      u[i] = lap::pack_bf16x2(a, b);
+      sum[i & 1] = lap::f2_add(sum[i & 1], lap::f2_pack(a, b));
+    }
+    lap::tmem_st16_nowait(t_p + 16 * g, u);
+  }
+  lap::tmem_wait_st();
+  return lap::f2_add(sum[0], sum[1]);
+}
+
+// c times the largest (c < 0: smallest) of the scores that the row sees; about -3.4e38 |c| for none.
+template <Seen kSeen>
+__device__ __forceinline__ float top_score(float (&s)[kTile], float c, const Keys& keys) {
+  const bool up = c >= 0.f;
+  if (kSeen != kAll) {
+    const float out = up ? -3.4e38f : 3.4e38f;
+#pragma unroll
+    for (int k = 0; k < kTile; ++k) s[k] = sees<kSeen>(keys, k) ? s[k] : out;
+  }
+  float t[4] = {s[0], s[1], s[2], s[3]};
+  if (up) {
+#pragma unroll
+    for (int k = 4; k < kTile; k += 8)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = fmaxf(fmaxf(t[e], s[k + e]), k + 4 + e < kTile ? s[k + 4 + e] : t[e]);
+    return c * fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  }
+#pragma unroll
+  for (int k = 4; k < kTile; ++k) t[k & 3] = fminf(t[k & 3], s[k]);
+  return c * fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+}
+
+// Multiplies this thread's row of O in tensor memory.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t t_o, float f) {
+  const uint64_t f2 = lap::f2_pack(f, f);
+#pragma unroll 1
+  for (int g = 0; g < D / 16; ++g) {
+    float o[16];
+    uint32_t u[16];
+    lap::tmem_ld16(t_o + 16 * g, o);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float2 r = lap::f2_unpack(lap::f2_mul(lap::f2_pack(o[i], o[i + 1]), f2));
+      u[i] = __float_as_uint(r.x);
+      u[i + 1] = __float_as_uint(r.y);
+    }
+    lap::tmem_st16_nowait(t_o + 16 * g, u);
+  }
+  lap::tmem_wait_st();
+}
+
+// Where a row outgrows its maximum: the new one, and the factor of what was summed under the old.  Each
+// row moves by itself, so that its result does not depend on the rows beside it.
+__device__ __forceinline__ float outgrow(float z, float& m, uint64_t& l) {
+  const float top = z > m + kSlack ? z : m, f = top == m ? 1.f : lap::exp2_approx(m - top);
+  m = top;
+  l = lap::f2_mul(l, lap::f2_pack(f, f));
+  return f;
+}
+
+}  // namespace laa
