@@ -29,8 +29,9 @@ DEPENDS = ["la_prefill_api.cu", "la_prefill_kernel.cuh", "sm103_ptx.cuh", "la_de
            "la_backward_api.cu", "la_verify_kernel.cuh", "la_prefill_internal.h", "la_d256_api.cu",
            "la_gated_api.cu", "la_gated_kernels.cuh", "la_gated_math.cuh", "la_rows_common.h", "la_norm_api.cu",
            "la_norm_kernels.cuh", "la_vec.cuh", "la_heads_common.h", "la_rotary_api.cu", "la_rotary_kernels.cuh",
-           "la_attention_api.cu", "la_attention_params.cuh", "la_attention_simple.cuh", "la_attention_commit.cuh",
-           "la_attention_tiles.cuh", "la_attention_softmax.cuh", "la_attention_fwd.cuh", "la_attention_verify.cuh"]
+           "la_attention_api.cu", "la_attention_params.cuh", "la_attention_commit.cuh",
+           "la_attention_tiles.cuh", "la_attention_softmax.cuh", "la_attention_fwd.cuh", "la_attention_verify.cuh",
+           "la_attention_bwd.cuh"]
 HEADERS = ["la_prefill.h", "la_decode.h", "la_segment.h", "la_backward.h", "la_d256.h", "la_gated.h", "la_norm.h",
            "la_rotary.h", "la_attention.h"]
 # parts that can be built alone with a short wait limit

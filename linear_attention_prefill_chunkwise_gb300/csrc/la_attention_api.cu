@@ -7,9 +7,9 @@
 #include <cstdint>
 
 #include "../../include/la_attention.h"
+#include "la_attention_bwd.cuh"
 #include "la_attention_commit.cuh"
 #include "la_attention_fwd.cuh"
-#include "la_attention_simple.cuh"
 #include "la_attention_verify.cuh"
 #include "la_heads_common.h"
 #include "la_host_common.h"
@@ -29,6 +29,11 @@ template <int D>
 constexpr int fwd_shared() { return static_cast<int>(sizeof(laa::FwdShared<D>)) + 1024; }
 
 template <int D>
+constexpr int bwd_shared() {
+  static_assert(sizeof(laa::BwdShared<D>) <= 227 * 1024, "shared memory");
+  return static_cast<int>(sizeof(laa::BwdShared<D>));
+}
+template <int D>
 constexpr int verify_shared() { return static_cast<int>(sizeof(laa::VerifyShared<D>)) + 1024; }
 
 la_status device(la_host::DeviceState** ds) {
@@ -36,6 +41,10 @@ la_status device(la_host::DeviceState** ds) {
     const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
     cudaError_t e = cudaFuncSetAttribute(laa::attn_fwd_kernel<64>, most, fwd_shared<64>());
     if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_fwd_kernel<128>, most, fwd_shared<128>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_bwd_kernel<64, false>, most, bwd_shared<64>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_bwd_kernel<64, true>, most, bwd_shared<64>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_bwd_kernel<128, false>, most, bwd_shared<128>());
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_bwd_kernel<128, true>, most, bwd_shared<128>());
     if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_verify_kernel<64>, most, verify_shared<64>());
     if (e == cudaSuccess) e = cudaFuncSetAttribute(laa::attn_verify_kernel<128>, most, verify_shared<128>());
     return e;
@@ -318,10 +327,22 @@ la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float
   p.scale = scale;
   p.tokens = static_cast<int>(tokens), p.T = T, p.N = N, p.H = H, p.HK = HK, p.D = D;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  laa::BwdMaps maps;
+  if ((st = encode_heads(&maps.q, a[0], 1, laa::kTile)) != LA_OK || (st = encode_heads(&maps.k, a[1], 1, laa::kTile)) != LA_OK ||
+      (st = encode_heads(&maps.v, a[2], 1, laa::kTile)) != LA_OK || (st = encode_heads(&maps.dout, a[4], 1, laa::kTile)) != LA_OK)
+    return st;
+  const int64_t tiles = cu_seqlens ? tokens / laa::kTile + N : static_cast<int64_t>(N) * ((T + laa::kTile - 1) / laa::kTile);
+  const int64_t delta_threads = tokens * H * (D / 8);
+  if (delta_threads / laa::kDeltaThreads >= INT32_MAX) return fail(LA_ERR_UNSUPPORTED, "B*T*H too large (%lld)", (long long)(tokens * H));
   return launched(with_dim(D, [&](auto d) {
-    laa::simple_dq_kernel<decltype(d)::value><<<dim3((p.tokens + 3) / 4, H), 128, 0, s>>>(p);
-    laa::simple_dkdv_kernel<decltype(d)::value><<<dim3((p.tokens + 3) / 4, HK), 128, 0, s>>>(p);
-    return cudaGetLastError();
+    constexpr int kD = decltype(d)::value;
+    cudaError_t ce = la_host::launch_pdl(laa::attn_delta_kernel<kD>, static_cast<unsigned>((delta_threads + laa::kDeltaThreads - 1) / laa::kDeltaThreads),
+                                         laa::kDeltaThreads, 0, s, p);
+    if (ce == cudaSuccess)
+      ce = la_host::launch_pdl(laa::attn_bwd_kernel<kD, false>, blocks_for(tiles * HK, ds->sms), laa::kBwdThreads, bwd_shared<kD>(), s, maps, p);
+    if (ce == cudaSuccess)
+      ce = la_host::launch_pdl(laa::attn_bwd_kernel<kD, true>, blocks_for(tiles * H, ds->sms), laa::kBwdThreads, bwd_shared<kD>(), s, maps, p);
+    return ce;
   }));
 }
 

@@ -1,0 +1,572 @@
+// la_attention_bwd.cuh -- gradients of causal attention (include/la_attention.h) on the tensor cores.
+//
+// With p = 2^(c q.k - lse log2 e), c = scale log2 e, and delta_t = sum_d dO o:
+//     dS = p (dO.v - delta),   dv_j = sum_t p dO_t,   dk_j = scale sum_t dS q_t,   dq_t = scale sum_j dS k_j
+// Two kernels, so that every sum stays in tensor memory, in one order, without atomics or partial
+// sums in memory (a single pass would save two of the seven products and pay for it with FP32
+// additions of dq in memory, whose order changes):
+//   dk, dv: a block owns 128 keys and walks over the rows that see them, of every head of the group.
+//     K Q^T and V dO^T give scores and dP transposed, keys along the lanes, so that p and dS, written
+//     back over them as BF16, are operands from tensor memory of p^T dO and dS^T Q.
+//   dq: a block owns 128 rows and walks over the keys that they see: Q K^T, dO V^T, then dS K.
+// Two warpgroups share each tile of scores, 64 columns each (a thread has one row).  Warp 8 issues the
+// products in an order that leaves a product or two to run whenever the warpgroups work:
+//   dk, dv:  p^T dO (n), S (n + 1), dS^T Q (n), dP (n + 1)
+//   dq:      S (n + 1), dP (n + 1), dS K (n)
+// Warp 9 loads: a pair of tiles that stays for the item, and rings of three and two tiles for the
+// operands that pass, as long as each is in use.  Warp 10 brings lse and delta of the rows that pass.
+//
+// Bound: the tensor cores.
+#pragma once
+
+#include "la_attention_softmax.cuh"
+
+namespace laa {
+
+constexpr int kBwdThreads = 384, kBwdItems = 2, kDeltaThreads = 256;
+
+template <int D>
+struct alignas(1024) BwdShared {
+  TileMem<D> own[2];    // dk, dv: K, V of the item; dq: Q, dO
+  TileMem<D> long_[3];  // dk, dv: Q;  dq: K     (in use by two products)
+  TileMem<D> brief[2];  // dk, dv: dO; dq: V
+  float lse[2][kTile], delta[2][kTile];  // dk, dv
+  Item items[kBwdItems];
+  uint64_t item_full[kBwdItems], item_empty[kBwdItems];
+  uint64_t own_full, own_empty, long_full[3], long_empty[3], brief_full[2], brief_empty[2], stat_full[2], stat_empty[2];
+  uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready, acc_full, acc_free, final_bar;
+  uint32_t tmem;
+  int abort;
+};
+
+struct BwdMaps {
+  CUtensorMap q, k, v, dout;
+};
+
+// What an item of either kernel walks over: tile n is rows (keys) of tile `first + n % each`, of head
+// `head + n / each`.
+struct Passes {
+  int first, each, count, head;
+};
+template <bool kDq>
+__device__ __forceinline__ Passes passes_of(const PrefillParams& p, const Item& it) {
+  const int tiles = (it.len + kTile - 1) / kTile, group = p.H / p.HK;
+  if (kDq) return {0, it.tile + 1, it.tile + 1, it.head / group};
+  return {it.tile, tiles - it.tile, (tiles - it.tile) * group, it.head * group};
+}
+
+template <int D, bool kDq>
+__device__ __forceinline__ void bwd_load(BwdShared<D>& sm, const PrefillParams& p, const BwdMaps& maps, int lane,
+                                         volatile int* abort) {
+  constexpr uint32_t kBytes = kBox * (D / 64);
+  ItemWalk<!kDq> walk(kTile, kDq ? p.H : p.HK);
+  const CUtensorMap *own0 = kDq ? &maps.q : &maps.k, *own1 = kDq ? &maps.dout : &maps.v;
+  const CUtensorMap *lng = kDq ? &maps.k : &maps.q, *brf = kDq ? &maps.v : &maps.dout;
+  uint32_t items = 0, own_loads = 0, longs = 0, briefs = 0;
+  bool ok = true;
+  auto load = [&](const CUtensorMap* map, TileMem<D>& dst, uint64_t* bar, int head, int row) {
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) lap::tma_load_3d(dst[b], map, bar, 64 * b, head, row);
+  };
+  for (; ok; ++items) {
+    const uint32_t is = items % kBwdItems;
+    if (!warp_wait(&sm.item_empty[is], ((items / kBwdItems) & 1u) ^ 1u, abort)) break;
+    const Item it = walk.take(p, lane);
+    if (lane == 0) {
+      sm.items[is] = it;
+      lap::mbar_arrive(&sm.item_full[is]);
+    }
+    __syncwarp();
+    if (it.len < 0) break;
+    const Passes w = passes_of<kDq>(p, it);
+    int head = w.head, tile = w.first;
+    for (int n = 0; n < w.count; ++n) {
+      const uint32_t l = longs % 3, b = briefs % 2;
+      if (!(ok = warp_wait(&sm.long_empty[l], ((longs / 3) & 1u) ^ 1u, abort))) break;
+      if (lane == 0) {
+        lap::mbar_arrive_expect_tx(&sm.long_full[l], kBytes);
+        load(lng, sm.long_[l], &sm.long_full[l], head, it.lo + tile * kTile);
+      }
+      ++longs;
+      if (!(ok = warp_wait(&sm.brief_empty[b], ((briefs / 2) & 1u) ^ 1u, abort))) break;
+      if (lane == 0) {
+        lap::mbar_arrive_expect_tx(&sm.brief_full[b], kBytes);
+        load(brf, sm.brief[b], &sm.brief_full[b], head, it.lo + tile * kTile);
+      }
+      ++briefs;
+      if (n == 0) {  // the first tiles that pass are on their way while the last item still reads its own
+        if (!(ok = warp_wait(&sm.own_empty, (own_loads & 1u) ^ 1u, abort))) break;
+        if (lane == 0) {
+          lap::mbar_arrive_expect_tx(&sm.own_full, 2 * kBytes);
+          load(own0, sm.own[0], &sm.own_full, it.head, it.lo + it.tile * kTile);
+          load(own1, sm.own[1], &sm.own_full, it.head, it.lo + it.tile * kTile);
+        }
+        ++own_loads;
+      }
+      if (++tile == w.first + w.each) tile = w.first, ++head;
+    }
+  }
+  // every load has landed before the block's shared memory is given up, also after an abort
+  if (lane == 0) {
+    if (own_loads) drain(&sm.own_full, (own_loads - 1) & 1u);
+    for (uint32_t i = 0; i < 3 && i < longs; ++i) drain(&sm.long_full[(longs - 1 - i) % 3], ((longs - 1 - i) / 3) & 1u);
+    for (uint32_t i = 0; i < 2 && i < briefs; ++i) drain(&sm.brief_full[(briefs - 1 - i) % 2], ((briefs - 1 - i) / 2) & 1u);
+  }
+  __syncwarp();
+}
+
+// dk, dv: lse log2 e and delta of the rows that pass.
+template <int D>
+__device__ __forceinline__ void bwd_stats(BwdShared<D>& sm, const PrefillParams& p, int lane, volatile int* abort) {
+  uint32_t tiles = 0;
+  for (uint32_t i = 0;; ++i) {
+    const uint32_t is = i % kBwdItems;
+    if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) return;
+    const Item it = sm.items[is];
+    warp_arrive(&sm.item_empty[is], lane);
+    if (it.len < 0) return;
+    const Passes w = passes_of<false>(p, it);
+    int head = w.head, tile = w.first;
+    for (int n = 0; n < w.count; ++n, ++tiles) {
+      float lse[4], delta[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = tile * kTile + 32 * e + lane;
+        const int64_t at = static_cast<int64_t>(head) * p.tokens + it.lo + row;
+        lse[e] = row < it.len ? __ldg(p.lse_in + at) * kLog2e : 0.f;
+        delta[e] = row < it.len ? p.delta[at] : 0.f;
+      }
+      const uint32_t st = tiles & 1;
+      if (!warp_wait(&sm.stat_empty[st], ((tiles >> 1) & 1u) ^ 1u, abort)) return;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sm.lse[st][32 * e + lane] = lse[e];
+        sm.delta[st][32 * e + lane] = delta[e];
+      }
+      warp_arrive(&sm.stat_full[st], lane);
+      if (++tile == w.first + w.each) tile = w.first, ++head;
+    }
+  }
+}
+
+// Tensor memory: S at 0, dP at 128, then dv and dk, or two buffers of dS and dq.
+constexpr int kColDp = kTile, kColDv = 2 * kTile, kColDs = 2 * kTile, kColDq = 3 * kTile;
+
+template <int D, bool kDq>
+__device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int lane,
+                                             volatile int* abort) {
+  const uint32_t t_dp = tmem + kColDp, t_dv = tmem + kColDv, t_dk = t_dv + D;
+  uint32_t tiles = 0;  // of all items; tile t has long slot t % 3 and brief slot t % 2
+  bool ok = true;
+  auto wait_long = [&](uint32_t t) { return warp_wait(&sm.long_full[t % 3], (t / 3) & 1u, abort); };
+  auto wait_brief = [&](uint32_t t) { return warp_wait(&sm.brief_full[t % 2], (t / 2) & 1u, abort); };
+  auto scores = [&](uint32_t t) {
+    lap::tc_fence_after();
+    if (lane == 0) {
+      product_rows<D>(tmem, desc_rows(sm.own[0]), desc_rows(sm.long_[t % 3]));
+      lap::mma_commit(&sm.s_full);
+    }
+  };
+  auto dps = [&](uint32_t t, bool last) {
+    lap::tc_fence_after();
+    if (lane == 0) {
+      product_rows<D>(t_dp, desc_rows(sm.own[1]), desc_rows(sm.brief[t % 2]));
+      lap::mma_commit(&sm.dp_full);
+      if (kDq) lap::mma_commit(&sm.brief_empty[t % 2]);
+      if (last) lap::mma_commit(&sm.own_empty);
+    }
+  };
+  for (uint32_t i = 0; ok; ++i) {
+    const uint32_t is = i % kBwdItems;
+    if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) break;
+    const Item it = sm.items[is];
+    warp_arrive(&sm.item_empty[is], lane);
+    if (it.len < 0) break;
+    const int count = passes_of<kDq>(p, it).count;
+    if (!(ok = warp_wait(&sm.own_full, i & 1u, abort))) break;
+    // the first tile's scores and dP; their columns were read before the last item's last product
+    if (!(ok = wait_long(tiles)) || (kDq && !(ok = warp_wait(&sm.s_free, (tiles & 1u) ^ 1u, abort)))) break;
+    scores(tiles);
+    if (!(ok = wait_brief(tiles)) || (kDq && !(ok = warp_wait(&sm.dp_free, (tiles & 1u) ^ 1u, abort)))) break;
+    dps(tiles, count == 1);
+    for (int n = 0; n < count; ++n) {
+      const uint32_t t = tiles + n;
+      const bool more = n + 1 < count;
+      if (kDq) {
+        if (more) {
+          if (!(ok = wait_long(t + 1)) || !(ok = warp_wait(&sm.s_free, t & 1u, abort))) break;
+          scores(t + 1);
+          if (!(ok = wait_brief(t + 1)) || !(ok = warp_wait(&sm.dp_free, t & 1u, abort))) break;
+          dps(t + 1, n + 2 == count);
+        }
+        if (!(ok = warp_wait(&sm.ds_ready, t & 1u, abort))) break;
+        if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
+        lap::tc_fence_after();
+        if (lane == 0) {
+          product_tmem<D>(tmem + kColDq, tmem + kColDs + 64 * (t & 1), desc_columns(sm.long_[t % 3]), n > 0);
+          lap::mma_commit(&sm.long_empty[t % 3]);
+          if (!more) lap::mma_commit(&sm.acc_full);
+        }
+      } else {
+        if (!(ok = warp_wait(&sm.p_ready, t & 1u, abort))) break;
+        if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
+        lap::tc_fence_after();
+        if (lane == 0) {
+          product_tmem<D, 64>(t_dv, tmem, desc_columns(sm.brief[t % 2]), n > 0);
+          lap::mma_commit(&sm.brief_empty[t % 2]);
+        }
+        if (more) {
+          if (!(ok = wait_long(t + 1))) break;
+          scores(t + 1);
+        }
+        if (!(ok = warp_wait(&sm.ds_ready, t & 1u, abort))) break;
+        lap::tc_fence_after();
+        if (lane == 0) {
+          product_tmem<D, 64>(t_dk, t_dp, desc_columns(sm.long_[t % 3]), n > 0);
+          lap::mma_commit(&sm.long_empty[t % 3]);
+          if (!more) lap::mma_commit(&sm.acc_full);
+        }
+        if (more) {
+          if (!(ok = wait_brief(t + 1))) break;
+          dps(t + 1, n + 2 == count);
+        }
+      }
+      __syncwarp();
+    }
+    tiles += count;
+  }
+  if (lane == 0) {
+    lap::mma_commit(&sm.final_bar);
+    drain(&sm.final_bar, 0);  // every product has retired, also after an abort
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void load_half(uint32_t t, float (&s)[64]) {
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    float part[32];
+    lap::tmem_ld32(t + 32 * g, part);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[32 * g + i] = part[i];
+  }
+}
+
+// Rows of a tile that lie behind the sequence become zero: box `box` of row `row`.
+template <int D>
+__device__ __forceinline__ void clear_row(TileMem<D>& tile, int box, int row) {
+  if (box >= D / 64) return;
+  uint4* at = reinterpret_cast<uint4*>(tile[box] + row * 128);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) at[c] = make_uint4(0, 0, 0, 0);
+}
+
+// An output row's D columns from tensor memory, times a factor.
+template <int D>
+__device__ __forceinline__ void write_row(uint32_t t, bf16* out, float f, bool live, int from, int to) {
+#pragma unroll 1
+  for (int g = from; g < to; ++g) {
+    float o[32];
+    lap::tmem_ld32(t + 32 * g, o);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] *= f;
+    if (live) store_row32(out + 32 * g, o);
+  }
+}
+
+// dk, dv.  A thread has one key and 64 of a tile's rows.
+template <int D>
+__device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
+                                         volatile int* abort) {
+  const int half = tid / kTile, key = tid % kTile, lane = tid % 32;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(key & ~31) << 16);
+  const uint32_t t_s = t_lane + 64 * half, t_dp = t_lane + kColDp + 64 * half;
+  const float c = p.scale * kLog2e;
+  const uint64_t c2 = lap::f2_pack(c, c), minus = lap::f2_pack(-1.f, -1.f);
+  uint32_t tiles = 0;
+  for (uint32_t i = 0;; ++i) {
+    const uint32_t is = i % kBwdItems;
+    if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) return;
+    const Item it = sm.items[is];
+    warp_arrive(&sm.item_empty[is], lane);
+    if (it.len < 0) return;
+    const Passes w = passes_of<false>(p, it);
+    int tile = w.first;
+    for (int n = 0; n < w.count; ++n, ++tiles) {
+      const uint32_t st = tiles & 1;
+      const int valid = min(kTile, it.len - tile * kTile);
+      // this thread's rows [from, to) of its 64 see the key
+      const int from = tile == it.tile ? key - 64 * half : 0, to = valid - 64 * half;
+      const bool masked = tile == it.tile || valid < kTile;
+      if (!warp_wait(&sm.s_full, tiles & 1u, abort)) return;
+      if (valid < kTile) {
+        // rows behind the sequence must not enter the sums over rows (0 * inf is NaN)
+        if (!warp_wait(&sm.dp_full, tiles & 1u, abort)) return;
+        if (key >= valid) {
+          clear_row<D>(sm.long_[tiles % 3], half, key);
+          clear_row<D>(sm.brief[tiles % 2], half, key);
+        }
+        lap::fence_proxy_async_smem();
+      }
+      if (!warp_wait(&sm.stat_full[st], (tiles >> 1) & 1u, abort)) return;
+      lap::tc_fence_after();
+      float s[64];
+      load_half(t_s, s);
+      const float4* lse = reinterpret_cast<const float4*>(sm.lse[st] + 64 * half);
+      const float4* delta = reinterpret_cast<const float4*>(sm.delta[st] + 64 * half);
+      auto weights = [&](auto has_mask) {
+        constexpr bool kMasked = decltype(has_mask)::value;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = 32 * g + 4 * e;
+            const float4 l = lse[k / 4];
+            const float2 z0 = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, lap::f2_mul(minus, lap::f2_pack(l.x, l.y))));
+            const float2 z1 = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k + 2], s[k + 3]), c2, lap::f2_mul(minus, lap::f2_pack(l.z, l.w))));
+            s[k] = lap::exp2_approx(z0.x), s[k + 1] = lap::exp2_approx(z0.y);
+            s[k + 2] = lap::exp2_approx(z1.x), s[k + 3] = lap::exp2_approx(z1.y);
+            if (kMasked)
+#pragma unroll
+              for (int x = k; x < k + 4; ++x) s[x] = x >= from && x < to ? s[x] : 0.f;
+            u[2 * e] = lap::pack_bf16x2(s[k], s[k + 1]);
+            u[2 * e + 1] = lap::pack_bf16x2(s[k + 2], s[k + 3]);
+          }
+          lap::tmem_st16_nowait(t_s + 16 * g, u);
+        }
+      };
+      if (masked) weights(std::true_type{}); else weights(std::false_type{});
+      lap::tmem_wait_st();
+      lap::tc_fence_before();
+      warp_arrive(&sm.p_ready, lane);
+      if (!warp_wait(&sm.dp_full, tiles & 1u, abort)) return;
+      lap::tc_fence_after();
+      auto slopes = [&](auto has_mask) {
+        constexpr bool kMasked = decltype(has_mask)::value;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float dp[32];
+          uint32_t u[16];
+          lap::tmem_ld32(t_dp + 32 * g, dp);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int k = 32 * g + 4 * e;
+            const float4 d = delta[k / 4];
+            float2 a = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k], s[k + 1]),
+                                                  lap::f2_sub(lap::f2_pack(dp[4 * e], dp[4 * e + 1]), lap::f2_pack(d.x, d.y))));
+            float2 b = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k + 2], s[k + 3]),
+                                                  lap::f2_sub(lap::f2_pack(dp[4 * e + 2], dp[4 * e + 3]), lap::f2_pack(d.z, d.w))));
+            if (kMasked) {
+              a.x = k >= from && k < to ? a.x : 0.f;
+              a.y = k + 1 >= from && k + 1 < to ? a.y : 0.f;
+              b.x = k + 2 >= from && k + 2 < to ? b.x : 0.f;
+              b.y = k + 3 >= from && k + 3 < to ? b.y : 0.f;
+            }
+            u[2 * e] = lap::pack_bf16x2(a.x, a.y);
+            u[2 * e + 1] = lap::pack_bf16x2(b.x, b.y);
+          }
+          lap::tmem_st16_nowait(t_dp + 16 * g, u);
+        }
+      };
+      if (masked) slopes(std::true_type{}); else slopes(std::false_type{});
+      lap::tmem_wait_st();
+      lap::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        lap::mbar_arrive(&sm.ds_ready);
+        lap::mbar_arrive(&sm.stat_empty[st]);
+      }
+      if (++tile == w.first + w.each) tile = w.first;
+    }
+    if (!warp_wait(&sm.acc_full, i & 1u, abort)) return;
+    lap::tc_fence_after();
+    const int64_t at = it.lo + it.tile * kTile + key;
+    const bool live = it.tile * kTile + key < it.len;
+    if (half == 0)
+      write_row<D>(t_lane + kColDv, p.dv.row(at, it.head), 1.f, live, 0, D / 32);
+    else
+      write_row<D>(t_lane + kColDv + D, p.dk.row(at, it.head), p.scale, live, 0, D / 32);
+    lap::tc_fence_before();
+    warp_arrive(&sm.acc_free, lane);
+  }
+}
+
+// dq.  A thread has one row and 64 of a tile's keys.
+template <int D>
+__device__ __forceinline__ void bwd_dq(BwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
+                                       volatile int* abort) {
+  const int half = tid / kTile, row = tid % kTile, lane = tid % 32;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(row & ~31) << 16);
+  const uint32_t t_s = t_lane + 64 * half, t_dp = t_lane + kColDp + 64 * half;
+  const float c = p.scale * kLog2e;
+  const uint64_t c2 = lap::f2_pack(c, c);
+  uint32_t tiles = 0;
+  for (uint32_t i = 0;; ++i) {
+    const uint32_t is = i % kBwdItems;
+    if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) return;
+    const Item it = sm.items[is];
+    warp_arrive(&sm.item_empty[is], lane);
+    if (it.len < 0) return;
+    const int64_t at = it.lo + it.tile * kTile + row, stat = static_cast<int64_t>(it.head) * p.tokens + at;
+    const bool live = it.tile * kTile + row < it.len;
+    const float lse = live ? __ldg(p.lse_in + stat) * kLog2e : 0.f, delta = live ? p.delta[stat] : 0.f;
+    const uint64_t l2 = lap::f2_pack(-lse, -lse), d2 = lap::f2_pack(delta, delta);
+    for (int n = 0; n <= it.tile; ++n, ++tiles) {
+      const bool masked = n == it.tile;
+      const int keep = row + 1 - 64 * half;  // of this thread's 64 keys, on the diagonal
+      if (!warp_wait(&sm.s_full, tiles & 1u, abort)) return;
+      if (masked && it.len < (it.tile + 1) * kTile) {
+        // keys behind the sequence must not enter the sum over keys (0 * inf is NaN)
+        if (it.tile * kTile + row >= it.len) clear_row<D>(sm.long_[tiles % 3], half, row);
+        lap::fence_proxy_async_smem();
+      }
+      lap::tc_fence_after();
+      float s[64];
+      load_half(t_s, s);
+      lap::tc_fence_before();
+      warp_arrive(&sm.s_free, lane);
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        const float2 z = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, l2));
+        s[k] = lap::exp2_approx(z.x), s[k + 1] = lap::exp2_approx(z.y);
+      }
+      if (!warp_wait(&sm.dp_full, tiles & 1u, abort)) return;
+      lap::tc_fence_after();
+      float dp[64];
+      load_half(t_dp, dp);
+      lap::tc_fence_before();
+      warp_arrive(&sm.dp_free, lane);
+      const uint32_t t_ds = t_lane + kColDs + 64 * (tiles & 1) + 32 * half;
+      auto slopes = [&](auto has_mask) {
+        constexpr bool kMasked = decltype(has_mask)::value;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int k = 32 * g + 2 * e;
+            float2 a = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k], s[k + 1]), lap::f2_sub(lap::f2_pack(dp[k], dp[k + 1]), d2)));
+            if (kMasked) {
+              a.x = k < keep ? a.x : 0.f;
+              a.y = k + 1 < keep ? a.y : 0.f;
+            }
+            u[e] = lap::pack_bf16x2(a.x, a.y);
+          }
+          lap::tmem_st16_nowait(t_ds + 16 * g, u);
+        }
+      };
+      if (masked) slopes(std::true_type{}); else slopes(std::false_type{});
+      lap::tmem_wait_st();
+      lap::tc_fence_before();
+      warp_arrive(&sm.ds_ready, lane);
+    }
+    if (!warp_wait(&sm.acc_full, i & 1u, abort)) return;
+    lap::tc_fence_after();
+    write_row<D>(t_lane + kColDq, p.dq.row(at, it.head), p.scale, live, half * (D / 64), (half + 1) * (D / 64));
+    lap::tc_fence_before();
+    warp_arrive(&sm.acc_free, lane);
+  }
+}
+
+template <int D, bool kDq>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ PrefillParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];  // without room to align it: it begins aligned
+  BwdShared<D>& sm = *reinterpret_cast<BwdShared<D>*>(smem_tiles);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  volatile int* abort = &sm.abort;
+  lap::griddep_wait();
+  lap::griddep_launch_dependents();
+  if (lap::smem_u32(smem_tiles) & 1023u) {  // swizzled tiles would land elsewhere: leave at once
+    if (tid == 0 && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
+    return;
+  }
+  if (warp == 8) {
+    lap::tmem_alloc(&sm.tmem, 512);
+    lap::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kBwdItems; ++i) {
+      lap::mbar_init(&sm.item_full[i], 1);
+      lap::mbar_init(&sm.item_empty[i], kDq ? 9 : 10);
+    }
+    lap::mbar_init(&sm.own_full, 1);
+    lap::mbar_init(&sm.own_empty, 1);
+    for (int i = 0; i < 3; ++i) {
+      lap::mbar_init(&sm.long_full[i], 1);
+      lap::mbar_init(&sm.long_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      lap::mbar_init(&sm.brief_full[i], 1);
+      lap::mbar_init(&sm.brief_empty[i], 1);
+      lap::mbar_init(&sm.stat_full[i], 1);
+      lap::mbar_init(&sm.stat_empty[i], 8);
+    }
+    lap::mbar_init(&sm.s_full, 1);
+    lap::mbar_init(&sm.s_free, 8);
+    lap::mbar_init(&sm.dp_full, 1);
+    lap::mbar_init(&sm.dp_free, 8);
+    lap::mbar_init(&sm.p_ready, 8);
+    lap::mbar_init(&sm.ds_ready, 8);
+    lap::mbar_init(&sm.acc_full, 1);
+    lap::mbar_init(&sm.acc_free, 8);
+    lap::mbar_init(&sm.final_bar, 1);
+    sm.abort = 0;
+    lap::fence_mbar_init();
+    lap::tma_prefetch_desc(&maps.q);
+    lap::tma_prefetch_desc(&maps.k);
+    lap::tma_prefetch_desc(&maps.v);
+    lap::tma_prefetch_desc(&maps.dout);
+  }
+  lap::tc_fence_before();
+  __syncthreads();
+  lap::tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  if (warp < 8) {
+    if constexpr (kDq)
+      bwd_dq<D>(sm, p, tmem, tid, abort);
+    else
+      bwd_dkdv<D>(sm, p, tmem, tid, abort);
+  } else if (warp == 8) {
+    bwd_products<D, kDq>(sm, p, tmem, lane, abort);
+  } else if (warp == 9) {
+    bwd_load<D, kDq>(sm, p, maps, lane, abort);
+  } else if (warp == 10 && !kDq) {
+    bwd_stats<D>(sm, p, lane, abort);
+  }
+  lap::tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && sm.abort && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
+  if (warp == 8) {
+    __syncwarp();
+    lap::tc_fence_after();
+    lap::tmem_dealloc(tmem, 512);
+  }
+}
+
+// delta[h][t] = sum over D of dO o, D / 8 threads a row; bound by reading both once.
+template <int D>
+__global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const __grid_constant__ PrefillParams p) {
+  constexpr int kLanes = D / 8;
+  lap::griddep_wait();
+  lap::griddep_launch_dependents();
+  const int64_t r = (static_cast<int64_t>(blockIdx.x) * kDeltaThreads + threadIdx.x) / kLanes;
+  const int64_t t = r / p.H;
+  const int h = static_cast<int>(r - t * p.H), c = threadIdx.x % kLanes * 8;
+  float sum = 0.f;
+  if (t < p.tokens) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p.dout.row(t, h) + c), b = *reinterpret_cast<const uint4*>(p.o_in.row(t, h) + c);
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum = fmaf(lap::bf16lo_to_f32(x[i]), lap::bf16lo_to_f32(y[i]), sum);
+      sum = fmaf(lap::bf16hi_to_f32(x[i]), lap::bf16hi_to_f32(y[i]), sum);
+    }
+  }
+#pragma unroll
+  for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  if (t < p.tokens && c == 0) p.delta[h * static_cast<int64_t>(p.tokens) + t] = sum;
+}
+
+}  // namespace laa

@@ -53,7 +53,7 @@ __device__ __forceinline__ void fwd_load(FwdShared<D>& sm, const PrefillParams& 
   constexpr int kStages = FwdShared<D>::kStages;
   constexpr uint32_t kBytes = kBox * (D / 64);
   const int group = p.H / p.HK;
-  ItemWalk walk(kFwdRows, p.H);
+  ItemWalk<false> walk(kFwdRows, p.H);
   uint32_t slots = 0, q_loads[2] = {0, 0};
   bool ok = true;
   auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int head, int row) {

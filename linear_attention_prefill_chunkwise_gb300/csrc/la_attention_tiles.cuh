@@ -40,13 +40,14 @@ __device__ __forceinline__ void product_rows(uint32_t d, uint64_t a, uint64_t b)
   for (int kk = 0; kk < D / 16; ++kk)
     lap::mma_ss(d, desc_at(a, step_columns(kk)), desc_at(b, step_columns(kk)), id, kk > 0);
 }
-// d (+)= a b with a [128 rows, 128 summed] BF16 in tensor memory (64 columns) and b's rows summed.
-template <int D>
+// d (+)= a b with a [128 rows, 128 summed] BF16 in tensor memory and b's rows summed.  a's two halves
+// along the sum are 32 columns each, the second kHalf columns behind the first.
+template <int D, int kHalf = 32>
 __device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint64_t b, bool accumulate) {
   constexpr uint32_t id = lap::idesc_bf16_f32(kTile, D, false, true);
 #pragma unroll
   for (int kk = 0; kk < kTile / 16; ++kk)
-    lap::mma_ts(d, a + 8 * kk, desc_at(b, step_rows(kk)), id, accumulate || kk > 0);
+    lap::mma_ts(d, a + (kk >> 2) * kHalf + 8 * (kk & 3), desc_at(b, step_rows(kk)), id, accumulate || kk > 0);
 }
 
 // Whole-warp wait; false once the block gives up: after a wait of kWaitLimitNs, which sets *abort.
@@ -86,18 +87,20 @@ struct Item {
   int lo, len, tile, head;
 };
 
-// The block's items, every gridDim.x-th of all: heads innermost, so that blocks that run side by
-// side read the same keys; then tiles, a sequence's last (which sees most keys) first; a batch of
-// one length takes the last tiles of all its sequences first.  Packed sequences are walked 32 at a
-// time by the warp's lanes.  Whole-warp calls.
+// The block's items: each round of gridDim.x items goes to the blocks in order, every other one
+// backwards, and the costliest items come first, so that the sums are alike.  Heads are innermost, so
+// that blocks that run side by side read the same keys; then tiles, a sequence's last one first
+// (kAscending: its first one); a batch of one length takes all sequences' last (first) tiles first.
+// Packed sequences are walked 32 at a time by the warp's lanes.  Whole-warp calls.
+template <bool kAscending>
 struct ItemWalk {
-  int64_t next;  // item number
+  int64_t round = 0;
   int n0 = 0, rows, heads;
   int64_t before = 0;  // tiles before sequence n0
   int lo = 0, len = 0, tiles = 0, upto = 0;  // this lane's sequence n0 + lane; tiles up to it
   bool loaded = false;
 
-  __device__ ItemWalk(int rows, int heads) : next(blockIdx.x), rows(rows), heads(heads) {}
+  __device__ ItemWalk(int rows, int heads) : rows(rows), heads(heads) {}
 
   __device__ __forceinline__ void load(const PrefillParams& p, int lane) {
     const int n = n0 + lane;
@@ -116,16 +119,18 @@ struct ItemWalk {
   }
 
   __device__ __forceinline__ Item take(const PrefillParams& p, int lane) {
+    const int64_t next = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     const int64_t t = next / heads;
     Item it{0, -1, 0, static_cast<int>(next - t * heads)};
-    next += gridDim.x;
+    ++round;
     if (!p.cu_seqlens) {
       const int tiles_each = (p.T + rows - 1) / rows;
       if (t < static_cast<int64_t>(p.N) * tiles_each) {
         const int level = static_cast<int>(t / p.N);
         it.lo = (static_cast<int>(t) - level * p.N) * p.T;
         it.len = p.T;
-        it.tile = tiles_each - 1 - level;
+        it.tile = kAscending ? level : tiles_each - 1 - level;
+        return it;
       }
       return it;
     }
@@ -136,7 +141,8 @@ struct ItemWalk {
         const int at = __ffs(reach) - 1;
         it.lo = __shfl_sync(0xFFFFFFFFu, lo, at);
         it.len = __shfl_sync(0xFFFFFFFFu, len, at);
-        it.tile = static_cast<int>(before + __shfl_sync(0xFFFFFFFFu, upto, at) - 1 - t);
+        const int left = static_cast<int>(before + __shfl_sync(0xFFFFFFFFu, upto, at) - 1 - t);  // tiles after it
+        it.tile = kAscending ? __shfl_sync(0xFFFFFFFFu, tiles, at) - 1 - left : left;
         return it;
       }
       before += __shfl_sync(0xFFFFFFFFu, upto, 31);
