@@ -578,6 +578,11 @@ def _array(t, name, dtype, shape, dev):
     """Pointer of a contiguous tensor that must have this shape (None in it: any size), or None."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -620,7 +625,7 @@ def _empty_like(t, shape, dev, stream):
 def _call(fn, dev, *args):
     """Call a C entry point with device ``dev`` current; raise on a non-OK status."""
     import torch
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():  # a tensor on the device exists, so CUDA is up
         st = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -909,8 +914,18 @@ def la_rms_norm_bwd(s, weight, eps, dy, dres=None, dx=None, dweight=None, worksp
 # ---- queries, keys and values as heads: norm and rotation (include/la_rotary.h), softmax attention
 #      (include/la_attention.h)
 
+# As above, a check is one expression that holds for a good argument.
+
 def _heads(t, name, dtype=None, dev=None, shape=None):
-    """Checks of a tensor [tokens, heads, D] with contiguous D; returns (pointer, token stride, head stride)."""
+    """Checks of a tensor [tokens, heads, D] with contiguous D (dtype, dev, shape None: any); returns
+    (pointer, token stride, head stride)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            ld, hs, one = t.stride()
+            if one == 1:
+                return t.data_ptr(), ld, hs
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -931,12 +946,27 @@ def _heads(t, name, dtype=None, dev=None, shape=None):
     return t.data_ptr(), ld, hs
 
 
-def _out_heads(t, name, shape, dtype, dev, stream):
-    """(tensor, pointer, strides) of an output, a new dense tensor when not given."""
+def _out_heads(t, like, name, dtype, dev, stream):
+    """(tensor, pointer, strides) of an output of a checked tensor's shape and type, a new dense tensor
+    when not given."""
+    shape = like.shape
     if t is not None:
         return t, *_heads(t, name, dtype, dev, shape)
+    if stream is None:
+        import torch
+        t = torch.empty_like(like)  # the quickest of torch's ways; dense, in the order of like's strides
+        ld, hs, _ = t.stride()
+        return t, t.data_ptr(), ld, hs
     t = _empty(shape, dtype, dev, stream)
     return t, t.data_ptr(), shape[1] * shape[2], shape[2]
+
+
+def _count(t):
+    """Heads of a tensor that is about to be checked."""
+    try:
+        return t.shape[1]
+    except (AttributeError, IndexError):
+        return None
 
 
 def _qk(q, k):
@@ -948,9 +978,7 @@ def _qk(q, k):
     if code is None:
         raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {dtype}")
     tokens, H, D = q.shape
-    ks = _heads(k, "k", dtype, dev)
-    if k.shape[0] != tokens or k.shape[2] != D:
-        raise ValueError(f"q and k must have the same tokens and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
+    ks = _heads(k, "k", dtype, dev, (tokens, _count(k), D))
     return code, dtype, dev, q.shape, k.shape, qs, ks
 
 
@@ -981,8 +1009,8 @@ def la_qk_norm_rope_fwd(q, k, q_weight, k_weight, eps, positions=None, inv_freq=
     lib = load_library()
     code, dtype, dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk) = _qk(q, k)
     pos, freq, R = _rotation(positions, inv_freq, tokens, dev)
-    q_out, pqo, ldqo, hsqo = _out_heads(q_out, "q_out", q.shape, dtype, dev, stream)
-    k_out, pko, ldko, hsko = _out_heads(k_out, "k_out", k.shape, dtype, dev, stream)
+    q_out, pqo, ldqo, hsqo = _out_heads(q_out, q, "q_out", dtype, dev, stream)
+    k_out, pko, ldko, hsko = _out_heads(k_out, k, "k_out", dtype, dev, stream)
     _call(lib.la_qk_norm_rope_fwd, dev, pq, pk, _array(q_weight, "q_weight", torch.float32, (D,), dev),
           _array(k_weight, "k_weight", torch.float32, (D,), dev), eps, pos, freq, pqo, pko, ldq, hsq, ldk, hsk, ldqo, hsqo,
           ldko, hsko, tokens, H, HK, D, R, int(bool(interleaved)), code, _stream_of(stream, dev))
@@ -1024,8 +1052,8 @@ def la_qk_norm_rope_bwd(q, k, q_weight, k_weight, eps, dq_out, dk_out, positions
     pos, freq, R = _rotation(positions, inv_freq, tokens, dev)
     pgq, ldgq, hsgq = _heads(dq_out, "dq_out", dtype, dev, q.shape)
     pgk, ldgk, hsgk = _heads(dk_out, "dk_out", dtype, dev, k.shape)
-    dq, pdq, lddq, hsdq = _out_heads(dq, "dq", q.shape, dtype, dev, stream)
-    dk, pdk, lddk, hsdk = _out_heads(dk, "dk", k.shape, dtype, dev, stream)
+    dq, pdq, lddq, hsdq = _out_heads(dq, q, "dq", dtype, dev, stream)
+    dk, pdk, lddk, hsdk = _out_heads(dk, k, "dk", dtype, dev, stream)
     if dq_weight is None:
         dq_weight = _empty((D,), torch.float32, dev, stream)
     if dk_weight is None:
@@ -1044,10 +1072,10 @@ def _qkv(q, k, v):
     import torch
     qs = _heads(q, "q", torch.bfloat16)
     dev = q.get_device()
-    ks = _heads(k, "k", torch.bfloat16, dev)
-    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
-        raise ValueError(f"q and k must have the same tokens and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
-    return dev, q.shape, k.shape, qs, ks, _heads(v, "v", torch.bfloat16, dev, k.shape)
+    shape = q.shape
+    kshape = (shape[0], _count(k), shape[2])
+    ks = _heads(k, "k", torch.bfloat16, dev, kshape)
+    return dev, shape, kshape, qs, ks, _heads(v, "v", torch.bfloat16, dev, kshape)
 
 
 def _prompt_sequences(tokens, dev, cu_seqlens, seq_len):
@@ -1080,7 +1108,7 @@ def la_attn_prefill_fwd(q, k, v, scale, cu_seqlens=None, seq_len=None, o=None, l
     lib = load_library()
     dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk), (pv, ldv, hsv) = _qkv(q, k, v)
     B, T, N, cu = _prompt_sequences(tokens, dev, cu_seqlens, seq_len)
-    o, po, ldo, hso = _out_heads(o, "o", q.shape, torch.bfloat16, dev, stream)
+    o, po, ldo, hso = _out_heads(o, q, "o", torch.bfloat16, dev, stream)
     if lse is None:
         lse = _empty((H, tokens), torch.float32, dev, stream)
     _call(lib.la_attn_prefill_fwd, dev, pq, pk, pv, scale, cu, po, _array(lse, "lse", torch.float32, (H, tokens), dev), ldq,
@@ -1110,9 +1138,9 @@ def la_attn_prefill_bwd(q, k, v, scale, o, lse, dout, cu_seqlens=None, seq_len=N
     if lse is None:
         raise TypeError("lse must be a torch.Tensor")
     plse = _array(lse, "lse", torch.float32, (H, tokens), dev)
-    dq, pdq, lddq, hsdq = _out_heads(dq, "dq", q.shape, bf16, dev, stream)
-    dk, pdk, lddk, hsdk = _out_heads(dk, "dk", k.shape, bf16, dev, stream)
-    dv, pdv, lddv, hsdv = _out_heads(dv, "dv", v.shape, bf16, dev, stream)
+    dq, pdq, lddq, hsdq = _out_heads(dq, q, "dq", bf16, dev, stream)
+    dk, pdk, lddk, hsdk = _out_heads(dk, k, "dk", bf16, dev, stream)
+    dv, pdv, lddv, hsdv = _out_heads(dv, v, "dv", bf16, dev, stream)
     owner, ws, nbytes = _workspace(workspace, la_attn_prefill_bwd_workspace, (B, T, H), dev, stream)
     _call(lib.la_attn_prefill_bwd, dev, pq, pk, pv, scale, po, plse, pg, cu, pdq, pdk, pdv, ldq, hsq, ldk, hsk, ldv, hsv,
           ldo, hso, ldg, hsg, lddq, hsdq, lddk, hsdk, lddv, hsdv, B, T, N, H, HK, D, ws, nbytes,
@@ -1130,8 +1158,9 @@ def _cache(k_cache, v_cache, HK, D, cache_lens, page_table, B, dev):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype is not torch.bfloat16:
             raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.dim() != 4 or t.shape[2] != HK or t.shape[3] != D:
-            raise ValueError(f"{name} must have shape [pages, page_size, {HK}, {D}], got {tuple(t.shape)}")
+        have = t.shape
+        if len(have) != 4 or have[2] != HK or have[3] != D:
+            raise ValueError(f"{name} must have shape [pages, page_size, {HK}, {D}], got {tuple(have)}")
         if t.get_device() != dev:
             raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
         s = t.stride()
@@ -1188,7 +1217,7 @@ def la_attn_verify(q, k, v, scale, k_cache, v_cache, cache_lens, T, page_table=N
         raise ValueError("T must be >= 1 and q must have B*T rows")
     B = tokens // T
     (pkc, pvc, lens, table), strides, sizes = _cache(k_cache, v_cache, HK, D, cache_lens, page_table, B, dev)
-    o, po, ldo, hso = _out_heads(o, "o", q.shape, torch.bfloat16, dev, stream)
+    o, po, ldo, hso = _out_heads(o, q, "o", torch.bfloat16, dev, stream)
     owner, ws, nbytes = _workspace(workspace, la_attn_verify_workspace, (B, T, H, HK, D), dev, stream)
     _call(lib.la_attn_verify, dev, pq, pk, pv, scale, pkc, pvc, lens, table, _array(mask, "mask", torch.int64, (B, T), dev),
           po, ldq, hsq, ldk, hsk, ldv, hsv, ldo, hso, *strides, B, T, H, HK, D, *sizes, ws, nbytes,

@@ -109,29 +109,6 @@ la_status device(la_host::DeviceState** ds) {
   });
 }
 
-// Launches a persistent kernel with as many blocks as the device holds at once, `most` at most.
-template <typename... Params, typename... Args>
-cudaError_t launch_resident(void (*kernel)(Params...), int sms, int most, int threads, int shared, cudaStream_t s,
-                            int* blocks, Args... args) {
-  // the last answers, by kernel and block (the query costs as much as a launch)
-  struct Known {
-    const void* kernel = nullptr;
-    int threads = 0, shared = 0, sms = 0, per_sm = 0;
-  };
-  thread_local Known known[16];
-  const void* id = reinterpret_cast<const void*>(kernel);
-  Known& k = known[(reinterpret_cast<uintptr_t>(id) / 16 + static_cast<uintptr_t>(shared) / 1024) % 16];
-  if (k.kernel != id || k.threads != threads || k.shared != shared || k.sms != sms) {
-    int n = 0;
-    const cudaError_t ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, shared);
-    if (ce != cudaSuccess) return ce;
-    k = {id, threads, shared, sms, n};
-  }
-  const int per_sm = k.per_sm;
-  *blocks = per_sm * sms < most ? (per_sm < 1 ? 1 : per_sm * sms) : most;
-  return la_host::launch_pdl(kernel, *blocks, threads, shared, s, args...);
-}
-
 // Most blocks of the gradient kernel (rows of partial sums): eight per SM of the largest part.
 constexpr int kMostBlocks = 8 * 152;
 int bwd_blocks(int rows) { return rows < kMostBlocks ? rows : kMostBlocks; }
@@ -201,7 +178,7 @@ la_status forward(const void* x, const void* residual, const float* weight, floa
     if (fp8 && stages > 0 && rows / at_once >= 8 * ds->sms) {
       int blocks;
       ce = with_split<E>(vec, q.elements, [&](auto v, auto l) {
-        return launch_resident(lan::norm_fwd_ring_kernel<E, decltype(v)::value, decltype(l)::value>, ds->sms,
+        return la_host::launch_resident(lan::norm_fwd_ring_kernel<E, decltype(v)::value, decltype(l)::value>, ds->sms,
                                (rows + at_once - 1) / at_once, q.threads, static_cast<int>(stage * stages), s, &blocks,
                                p, stages);
       });
@@ -299,12 +276,12 @@ la_status la_rms_norm_bwd(const void* s, const float* weight, float eps, const v
         constexpr int kVec = decltype(v)::value, kLoads = decltype(l)::value;
         if (stages > 0) {
           const int ring = static_cast<int>(stage * stages);
-          return launch_resident(lan::norm_bwd_kernel<E, true, kVec, kLoads>, ds->sms, most, q.threads,
+          return la_host::launch_resident(lan::norm_bwd_kernel<E, true, kVec, kLoads>, ds->sms, most, q.threads,
                                  ring > add ? ring : add, cs, &blocks, p, stages);
         }
         // FP32 rows of more than about 9600 columns: two stages do not fit
         if constexpr (sizeof(E) == 4 && kVec * kLoads == 32)
-          return launch_resident(lan::norm_bwd_kernel<E, false, kVec, kLoads>, ds->sms, most, q.threads, add, cs,
+          return la_host::launch_resident(lan::norm_bwd_kernel<E, false, kVec, kLoads>, ds->sms, most, q.threads, add, cs,
                                  &blocks, p, 0);
         return cudaErrorInvalidConfiguration;
       });

@@ -21,9 +21,8 @@ using la_host::RowSpan;
 
 la_host::DeviceState g_dev[la_host::kMaxDevices];
 
-// Blocks of the gradient kernel at most: five per SM of the largest part (its shared memory and
-// registers let that many run at once).
-constexpr int kMostBlocks = 5 * 152;
+// Most blocks of the gradient kernel (rows of partial sums): eight per SM of the largest part.
+constexpr int kMostBlocks = 8 * 152;
 
 la_status check_sizes(int tokens, int H, int HK, int D, int R, la_dtype dtype) {
   if (dtype != LA_DTYPE_BF16 && dtype != LA_DTYPE_FP32) return fail(LA_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
@@ -40,11 +39,13 @@ la_status device(la_host::DeviceState** ds) {
   return la_host::current_device(g_dev, ds, [] { return cudaSuccess; });
 }
 
-// Tokens of a block: whole turns of the block's groups of threads, up to 16 tokens' angles, as long
-// as the grid still holds `want` blocks.
+// Tokens whose angles a block holds at once, at most.
+constexpr int kAngleTokens = 16;
+
+// Tokens of a block of the forward kernel, as long as the grid still holds `want` blocks.
 int tokens_per_block(int tokens, int want) {
   int n = 1;
-  while (n < 16 && tokens / (2 * n) >= want) n *= 2;
+  while (n < kAngleTokens && tokens / (2 * n) >= want) n *= 2;
   return n;
 }
 
@@ -146,7 +147,7 @@ la_status la_qk_norm_rope_fwd(const void* q, const void* k, const float* q_weigh
     p.heads[1] = HK;
     p.R = R;
     p.interleaved = interleaved != 0;
-    p.per_block = tokens_per_block(tokens, 8 * ds->sms);
+    p.per_block = tokens_per_block(tokens, 16 * ds->sms);
     const int blocks = (tokens + p.per_block - 1) / p.per_block;
     return launched(with_layout<E>(vec, D, [&](auto v, auto d) {
       return la_host::launch_pdl(lar::norm_rope_fwd_kernel<E, decltype(v)::value, decltype(d)::value>, blocks,
@@ -232,14 +233,14 @@ la_status la_qk_norm_rope_bwd(const void* q, const void* k, const float* q_weigh
     p.heads[1] = HK;
     p.R = R;
     p.interleaved = interleaved != 0;
-    p.per_block = tokens_per_block(tokens, kMostBlocks);
-    int blocks = (tokens + p.per_block - 1) / p.per_block;
-    if (blocks > kMostBlocks) blocks = kMostBlocks;
+    p.per_block = kAngleTokens;
+    int blocks = 0;
     cudaError_t ce = cudaSuccess;
     if (tokens > 0)
       ce = with_layout<E>(vec, D, [&](auto v, auto d) {
-        return la_host::launch_pdl(lar::norm_rope_bwd_kernel<E, decltype(v)::value, decltype(d)::value>, blocks,
-                                   lar::kThreads, p.per_block * (R / 2) * static_cast<int>(sizeof(float2)), cs, p);
+        return la_host::launch_resident(lar::norm_rope_bwd_kernel<E, decltype(v)::value, decltype(d)::value>, ds->sms,
+                                        bwd_blocks(tokens), lar::kThreads,
+                                        p.per_block * (R / 2) * static_cast<int>(sizeof(float2)), cs, &blocks, p);
       });
     if (ce == cudaSuccess && sums)
       ce = la_host::launch_pdl(lar::weight_sum_kernel, dim3(D / 32, 2), 1024, 0, cs,

@@ -15,6 +15,7 @@
 
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "la_vec.cuh"
 #include "sm103_ptx.cuh"
@@ -107,6 +108,15 @@ __device__ __forceinline__ void turn(float (&a)[kVec], float (&b)[kVec], const f
   }
 }
 
+// kVec elements as loaded: the next head's are on their way while one is computed.
+template <typename E, int kVec>
+struct Raw {
+  using T = std::conditional_t<kVec == 1, E, uint4>;
+  T v;
+  __device__ __forceinline__ void load(const E* p) { v = *reinterpret_cast<const T*>(p); }
+  __device__ __forceinline__ void expand(float (&f)[kVec]) const { lan::load<kVec>(reinterpret_cast<const E*>(&v), f); }
+};
+
 template <int kLanes>
 __device__ __forceinline__ float sum_lanes(float v) {
 #pragma unroll
@@ -152,9 +162,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const FwdParams
   lap::griddep_launch_dependents();
   const int first = blockIdx.x * p.per_block;
   const int count = min(p.per_block, p.tokens - first);
-  fill_angles(p, cs, first, count);
   const int lane = threadIdx.x % L::kLanes, group = threadIdx.x / L::kLanes;
-  __syncthreads();
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int heads = p.heads[which], rows = count * heads;
@@ -163,23 +171,39 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const FwdParams
     int at[L::kChunks], bt[L::kChunks];
     float wa[L::kChunks][kVec], wb[L::kChunks][kVec];
     own_weights<E, kVec, D>(p.weight[which], lane, p.R, p.interleaved, at, bt, wa, wb);
+    Raw<E, kVec> xa[L::kChunks], xb[L::kChunks];
+    auto fetch = [&](int r) {
+      if (r >= rows) return;
+      const int t = r / heads, h = r - t * heads;
+      const E* x = hx.p + (first + t) * hx.ld + h * hx.hs;
+#pragma unroll
+      for (int i = 0; i < L::kChunks; ++i) {
+        xa[i].load(x + at[i]);
+        xb[i].load(x + bt[i]);
+      }
+    };
+    fetch(group);
+    if (which == 0) {
+      fill_angles(p, cs, first, count);
+      __syncthreads();
+    }
     // every lane of a warp takes the same number of turns (the sums are over whole warps)
     for (int r0 = 0; r0 < rows; r0 += L::kGroups) {
       const int r = r0 + group;
       const bool live = r < rows;
       const int t = live ? r / heads : 0, h = live ? r - t * heads : 0;
-      const E* x = hx.p + (first + t) * hx.ld + h * hx.hs;
       E* y = hy.p + (first + t) * hy.ld + h * hy.hs;
       float a[L::kChunks][kVec], b[L::kChunks][kVec], ss = 0.f;
 #pragma unroll
       for (int i = 0; i < L::kChunks; ++i) {
-        if (live) {
-          lan::load<kVec>(x + at[i], a[i]);
-          lan::load<kVec>(x + bt[i], b[i]);
-        }
+        xa[i].expand(a[i]);
+        xb[i].expand(b[i]);
+      }
+      fetch(r + L::kGroups);
+#pragma unroll
+      for (int i = 0; i < L::kChunks; ++i) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          if (!live) a[i][e] = b[i][e] = 0.f;
           ss = fmaf(a[i][e], a[i][e], ss);
           ss = fmaf(b[i][e], b[i][e], ss);
         }
@@ -204,8 +228,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const FwdParams
   }
 }
 
-// The gradients.  A block walks over tiles of tokens, first all of its queries, then all of its
-// keys, and keeps the sums for the weight gradients of its threads' own elements in registers.
+// The gradients.  A block walks over its share of the tokens, first all of its queries, then
+// all of its keys, and keeps the sums for the weight gradients of its threads' own elements in registers.
 template <typename E, int kVec, int D>
 __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const BwdParams<E> p) {
   using L = Layout<E, kVec, D>;
@@ -223,33 +247,42 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const BwdParams
     float wa[L::kChunks][kVec], wb[L::kChunks][kVec];
     own_weights<E, kVec, D>(p.weight[which], lane, p.R, p.interleaved, at, bt, wa, wb);
     float da[L::kChunks][kVec] = {}, db[L::kChunks][kVec] = {};
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.per_block; first < p.tokens;
-         first += static_cast<int64_t>(gridDim.x) * p.per_block) {
-      const int count = min(static_cast<int64_t>(p.per_block), p.tokens - first);
+    const int64_t stop = static_cast<int64_t>(blockIdx.x + 1) * p.tokens / gridDim.x;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.tokens / gridDim.x; first < stop; first += p.per_block) {
+      const int count = static_cast<int>(min(static_cast<int64_t>(p.per_block), stop - first));
+      const int rows = count * heads;
+      Raw<E, kVec> xa[L::kChunks], xb[L::kChunks], ya[L::kChunks], yb[L::kChunks];
+      auto fetch = [&](int r) {
+        if (r >= rows) return;
+        const int t = r / heads, h = r - t * heads;
+        const E* x = hx.p + (first + t) * hx.ld + h * hx.hs;
+        const E* dy = hdy.p + (first + t) * hdy.ld + h * hdy.hs;
+#pragma unroll
+        for (int i = 0; i < L::kChunks; ++i) {
+          xa[i].load(x + at[i]);
+          xb[i].load(x + bt[i]);
+          ya[i].load(dy + at[i]);
+          yb[i].load(dy + bt[i]);
+        }
+      };
+      fetch(group);
       __syncthreads();
       fill_angles(p, cs, static_cast<int>(first), count);
       __syncthreads();
-      const int rows = count * heads;
       for (int r0 = 0; r0 < rows; r0 += L::kGroups) {
         const int r = r0 + group;
         const bool live = r < rows;
         const int t = live ? r / heads : 0, h = live ? r - t * heads : 0;
-        const E* x = hx.p + (first + t) * hx.ld + h * hx.hs;
-        const E* dy = hdy.p + (first + t) * hdy.ld + h * hdy.hs;
         float a[L::kChunks][kVec], b[L::kChunks][kVec], ga[L::kChunks][kVec], gb[L::kChunks][kVec];
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int i = 0; i < L::kChunks; ++i) {
-          if (live) {
-            lan::load<kVec>(x + at[i], a[i]);
-            lan::load<kVec>(x + bt[i], b[i]);
-            lan::load<kVec>(dy + at[i], ga[i]);
-            lan::load<kVec>(dy + bt[i], gb[i]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) a[i][e] = b[i][e] = ga[i][e] = gb[i][e] = 0.f;
-          }
+          xa[i].expand(a[i]);
+          xb[i].expand(b[i]);
+          ya[i].expand(ga[i]);
+          yb[i].expand(gb[i]);
         }
+        fetch(r + L::kGroups);
 #pragma unroll
         for (int i = 0; i < L::kChunks; ++i) {
           const int c = lane + 32 * i;
