@@ -162,24 +162,20 @@ __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillPara
   auto wait_brief = [&](uint32_t t) { return warp_wait(&sm.brief_full[t % 2], (t / 2) & 1u, abort); };
   auto scores = [&](uint32_t t) {
     lap::tc_fence_after();
-    if (lane == 0) {
-      product_rows<D>(tmem, desc_rows(sm.own[0]), desc_rows(sm.long_[t % 3]));
-      lap::mma_commit(&sm.s_full);
-    }
+    product_rows<D>(tmem, desc_rows(sm.own[0]), desc_rows(sm.long_[t % 3]));
+    commit(&sm.s_full);
   };
   auto dps = [&](uint32_t t, bool last) {
     lap::tc_fence_after();
-    if (lane == 0) {
-      product_rows<D>(t_dp, desc_rows(sm.own[1]), desc_rows(sm.brief[t % 2]));
-      lap::mma_commit(&sm.dp_full);
-      if (kDq) lap::mma_commit(&sm.brief_empty[t % 2]);
-      if (last) lap::mma_commit(&sm.own_empty);
-    }
+    product_rows<D>(t_dp, desc_rows(sm.own[1]), desc_rows(sm.brief[t % 2]));
+    commit(&sm.dp_full);
+    if (kDq) commit(&sm.brief_empty[t % 2]);
+    if (last) commit(&sm.own_empty);
   };
   for (uint32_t i = 0; ok; ++i) {
     const uint32_t is = i % kBwdItems;
     if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) break;
-    const Item it = sm.items[is];
+    const Item it = uniform(sm.items[is]);
     warp_arrive(&sm.item_empty[is], lane);
     if (it.len < 0) break;
     const int count = passes_of<kDq>(p, it).count;
@@ -202,43 +198,34 @@ __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillPara
         if (!(ok = warp_wait(&sm.ds_ready, t & 1u, abort))) break;
         if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
         lap::tc_fence_after();
-        if (lane == 0) {
-          product_tmem<D>(tmem + kColDq, tmem + kColDs + 64 * (t & 1), desc_columns(sm.long_[t % 3]), n > 0);
-          lap::mma_commit(&sm.long_empty[t % 3]);
-          if (!more) lap::mma_commit(&sm.acc_full);
-        }
+        product_tmem<D>(tmem + kColDq, tmem + kColDs + 64 * (t & 1), desc_columns(sm.long_[t % 3]), n > 0);
+        commit(&sm.long_empty[t % 3]);
+        if (!more) commit(&sm.acc_full);
       } else {
         if (!(ok = warp_wait(&sm.p_ready, t & 1u, abort))) break;
         if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
         lap::tc_fence_after();
-        if (lane == 0) {
-          product_tmem<D, 64>(t_dv, tmem, desc_columns(sm.brief[t % 2]), n > 0);
-          lap::mma_commit(&sm.brief_empty[t % 2]);
-        }
+        product_tmem<D, 64>(t_dv, tmem, desc_columns(sm.brief[t % 2]), n > 0);
+        commit(&sm.brief_empty[t % 2]);
         if (more) {
           if (!(ok = wait_long(t + 1))) break;
           scores(t + 1);
         }
         if (!(ok = warp_wait(&sm.ds_ready, t & 1u, abort))) break;
         lap::tc_fence_after();
-        if (lane == 0) {
-          product_tmem<D, 64>(t_dk, t_dp, desc_columns(sm.long_[t % 3]), n > 0);
-          lap::mma_commit(&sm.long_empty[t % 3]);
-          if (!more) lap::mma_commit(&sm.acc_full);
-        }
+        product_tmem<D, 64>(t_dk, t_dp, desc_columns(sm.long_[t % 3]), n > 0);
+        commit(&sm.long_empty[t % 3]);
+        if (!more) commit(&sm.acc_full);
         if (more) {
           if (!(ok = wait_brief(t + 1))) break;
           dps(t + 1, n + 2 == count);
         }
       }
-      __syncwarp();
     }
     tiles += count;
   }
-  if (lane == 0) {
-    lap::mma_commit(&sm.final_bar);
-    drain(&sm.final_bar, 0);  // every product has retired, also after an abort
-  }
+  commit(&sm.final_bar);
+  drain(&sm.final_bar, 0);  // every product has retired, also after an abort
   __syncwarp();
 }
 
@@ -474,7 +461,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ PrefillParams p) {
   extern __shared__ __align__(1024) uint8_t smem_tiles[];  // without room to align it: it begins aligned
   BwdShared<D>& sm = *reinterpret_cast<BwdShared<D>*>(smem_tiles);
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   volatile int* abort = &sm.abort;
   lap::griddep_wait();
   lap::griddep_launch_dependents();
@@ -522,7 +509,7 @@ attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Pr
   lap::tc_fence_before();
   __syncthreads();
   lap::tc_fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = uniform(sm.tmem);
   if (warp < 8) {
     if constexpr (kDq)
       bwd_dq<D>(sm, p, tmem, tid, abort);

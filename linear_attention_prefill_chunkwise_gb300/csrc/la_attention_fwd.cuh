@@ -107,7 +107,7 @@ __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, in
   for (uint32_t i = 0; ok; ++i) {
     const uint32_t is = i % kItems;
     if (!warp_wait(&sm.item_full[is], (i / kItems) & 1u, abort)) break;
-    const Item it = sm.items[is];
+    const Item it = uniform(sm.items[is]);
     warp_arrive(&sm.item_empty[is], lane);
     if (it.len < 0) break;
     const int n[2] = {key_tiles(it, 0), key_tiles(it, 1)};
@@ -116,10 +116,8 @@ __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, in
     auto wait_slot = [&](uint32_t x) { return warp_wait(&sm.kv_full[x % kStages], (x / kStages) & 1u, abort); };
     auto scores = [&](int s, uint32_t x) {
       lap::tc_fence_after();
-      if (lane == 0) {
-        product_rows<D>(tmem + s * kTile, desc_rows(sm.q[s]), desc_rows(sm.kv[x % kStages]));
-        lap::mma_commit(&sm.s_full[s]);
-      }
+      product_rows<D>(tmem + s * kTile, desc_rows(sm.q[s]), desc_rows(sm.kv[x % kStages]));
+      commit(&sm.s_full[s]);
     };
     if (!(ok = wait_slot(slot_of(0, false)))) break;
 #pragma unroll
@@ -127,10 +125,10 @@ __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, in
       if (!ok || !n[s]) continue;
       if (!(ok = warp_wait(&sm.q_full[s], q_uses[s] & 1u, abort))) continue;
       scores(s, slot_of(0, false));
-      if (n[s] == 1 && lane == 0) lap::mma_commit(&sm.q_empty[s]);
+      if (n[s] == 1) commit(&sm.q_empty[s]);
     }
     if (!ok) break;
-    if (lane == 0) lap::mma_commit(&sm.kv_empty[slot_of(0, false) % kStages]);
+    commit(&sm.kv_empty[slot_of(0, false) % kStages]);
     for (int j = 0; j < most && ok; ++j) {
       const uint32_t xv = slot_of(j, true), xk = slot_of(j + 1, false);
       bool keys = false;
@@ -141,31 +139,25 @@ __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, in
         if (!(ok = warp_wait(&sm.p_ready[s], p_uses[s]++ & 1u, abort))) continue;
         if (j == 0 && !(ok = warp_wait(&sm.o_free[s], (q_uses[s] & 1u) ^ 1u, abort))) continue;
         lap::tc_fence_after();
-        if (lane == 0)
-          product_tmem<D>(tmem + 2 * kTile + s * D, tmem + s * kTile, desc_columns(sm.kv[xv % kStages]), j > 0);
+        product_tmem<D>(tmem + 2 * kTile + s * D, tmem + s * kTile, desc_columns(sm.kv[xv % kStages]), j > 0);
         if (j == n[s] - 1) {
-          if (lane == 0) lap::mma_commit(&sm.o_full[s]);
+          commit(&sm.o_full[s]);
           ++q_uses[s];
         } else {
           if (!keys && !(ok = wait_slot(xk))) continue;
           keys = true;
           scores(s, xk);
-          if (j + 1 == n[s] - 1 && lane == 0) lap::mma_commit(&sm.q_empty[s]);
+          if (j + 1 == n[s] - 1) commit(&sm.q_empty[s]);
         }
       }
       if (!ok) break;
-      if (lane == 0) {
-        lap::mma_commit(&sm.kv_empty[xv % kStages]);
-        if (keys) lap::mma_commit(&sm.kv_empty[xk % kStages]);
-      }
-      __syncwarp();
+      commit(&sm.kv_empty[xv % kStages]);
+      if (keys) commit(&sm.kv_empty[xk % kStages]);
     }
     slots += 2 * most;
   }
-  if (lane == 0) {
-    lap::mma_commit(&sm.final_bar);
-    drain(&sm.final_bar, 0);  // every product has retired, also after an abort
-  }
+  commit(&sm.final_bar);
+  drain(&sm.final_bar, 0);  // every product has retired, also after an abort
   __syncwarp();
 }
 
@@ -263,7 +255,7 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
   extern __shared__ uint8_t smem_raw[];
   FwdShared<D>& sm =
       *reinterpret_cast<FwdShared<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   volatile int* abort = &sm.abort;
   lap::griddep_wait();
   lap::griddep_launch_dependents();
@@ -298,7 +290,7 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
   lap::tc_fence_before();
   __syncthreads();
   lap::tc_fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = uniform(sm.tmem);
   if (warp < 8) {
     lap::registers_grow<kSoftmaxRegs>();
     fwd_softmax<D>(sm, p, tmem, tid, abort);

@@ -19,52 +19,102 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 template <int D>
 using TileMem = uint8_t[D / 64][kBox];
 
-__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) { return base + (bytes >> 4); }
-// A tile as an operand whose rows are M or N and whose columns are summed over ...
-__device__ __forceinline__ uint64_t desc_rows(const void* tile) {
-  return lap::sdesc_sw128(lap::smem_u32(tile), 16, 1024);
+// A tile as an operand whose rows are M or N and whose columns are summed over (desc_rows), and as one
+// whose columns are M or N and whose rows are summed over (desc_columns): the low word of the matrix
+// descriptor lap::sdesc_sw128 builds; the high word is the same for both.
+__device__ __forceinline__ uint32_t desc_rows(const void* tile) {
+  return static_cast<uint32_t>(lap::sdesc_sw128(lap::smem_u32(tile), 16, 1024));
 }
-// ... and as one whose columns are M or N and whose rows are summed over.
-__device__ __forceinline__ uint64_t desc_columns(const void* tile) {
-  return lap::sdesc_sw128(lap::smem_u32(tile), kBox, 1024);
+__device__ __forceinline__ uint32_t desc_columns(const void* tile) {
+  return static_cast<uint32_t>(lap::sdesc_sw128(lap::smem_u32(tile), kBox, 1024));
 }
-// Byte offset of the kk-th 16 columns (desc_rows) or rows (desc_columns) of a tile.
-__device__ __forceinline__ uint32_t step_columns(int kk) { return (kk >> 2) * kBox + (kk & 3) * 32; }
-__device__ __forceinline__ uint32_t step_rows(int kk) { return kk * 2048; }
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
 
-// d (+)= a b^T over D columns: scores, dP.
+// The products and commits are whole-warp calls without a branch: one elected lane issues, and
+// descriptors stay warp-uniform values to which constants are added.  (A branch to one lane with
+// 64-bit descriptors cost 85 cycles an instruction, more than the 64 that one of 128 x 128 x 16 runs.)
+
+// Four instructions of d (+)= a b^T along 64 columns of two tiles (16 columns, 32 bytes, each).
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma4_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b32 x, y;\n\t.reg .b64 s, t;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 s, {%1, %3};\n\tmov.b64 t, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], s, t, %4, p;\n\t"
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 s, {x, %3};\n\tmov.b64 t, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], s, t, %4, 1;\n\t"
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 s, {x, %3};\n\tmov.b64 t, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], s, t, %4, 1;\n\t"
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 s, {x, %3};\n\tmov.b64 t, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], s, t, %4, 1;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHigh), "r"(kIdesc), "r"(accumulate)
+      : "memory");
+}
+// Four instructions of d (+)= a b with 64 summed elements of a in tensor memory (8 columns each) and 64
+// rows of b (16 rows, 2048 bytes, each).
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma4_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b32 x, y;\n\t.reg .b64 t;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 t, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], t, %4, p;\n\t"
+      "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 t, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], t, %4, 1;\n\t"
+      "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 t, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], t, %4, 1;\n\t"
+      "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 t, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], t, %4, 1;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHigh), "r"(kIdesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives once on `bar` when every product issued so far has completed.
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(lap::smem_u32(bar))
+      : "memory");
+}
+
+// d = a b^T over D columns: scores, dP.
 template <int D>
-__device__ __forceinline__ void product_rows(uint32_t d, uint64_t a, uint64_t b) {
+__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t id = lap::idesc_bf16_f32(kTile, kTile, false, false);
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk)
-    lap::mma_ss(d, desc_at(a, step_columns(kk)), desc_at(b, step_columns(kk)), id, kk > 0);
+  for (int h = 0; h < D / 64; ++h) mma4_rows<id>(d, a + h * (kBox >> 4), b + h * (kBox >> 4), h > 0);
 }
 // d (+)= a b with a [128 rows, 128 summed] BF16 in tensor memory and b's rows summed.  a's two halves
 // along the sum are 32 columns each, the second kHalf columns behind the first.
 template <int D, int kHalf = 32>
-__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint64_t b, bool accumulate) {
+__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
   constexpr uint32_t id = lap::idesc_bf16_f32(kTile, D, false, true);
-#pragma unroll
-  for (int kk = 0; kk < kTile / 16; ++kk)
-    lap::mma_ts(d, a + (kk >> 2) * kHalf + 8 * (kk & 3), desc_at(b, step_rows(kk)), id, accumulate || kk > 0);
+  mma4_tmem<id>(d, a, b, accumulate);
+  mma4_tmem<id>(d, a + kHalf, b + 512, true);
 }
+
+// A value that is the same in every lane, known to the compiler as such.
+template <typename T>
+__device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // Whole-warp wait; false once the block gives up: after a wait of kWaitLimitNs, which sets *abort.
 // (Inline: a kernel that moves registers between its warpgroups makes no calls.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   bool ok = lap::mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = lap::globaltimer_ns();
-    for (uint32_t i = 1;; ++i) {
-      ok = lap::mbar_try_wait(bar, parity);
-      if (ok) break;
-      if ((i & 31u) == 0u) {
-        if (*abort) break;
-        if (lap::globaltimer_ns() - t0 > lap::kWaitLimitNs) {
-          *abort = 1;
-          break;
-        }
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !ok; ++i) {
+    ok = lap::mbar_try_wait(bar, parity);
+    if ((i & 63u) == 0u && !ok) {  // the clock is slow to read: not in an ordinary wait
+      if (*abort) break;
+      const uint64_t now = lap::globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > lap::kWaitLimitNs) {
+        *abort = 1;
+        break;
       }
     }
   }
@@ -86,6 +136,9 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 struct Item {
   int lo, len, tile, head;
 };
+__device__ __forceinline__ Item uniform(const Item& it) {
+  return {uniform(it.lo), uniform(it.len), uniform(it.tile), uniform(it.head)};
+}
 
 // The block's items: each round of gridDim.x items goes to the blocks in order, every other one
 // backwards, and the costliest items come first, so that the sums are alike.  Heads are innermost, so

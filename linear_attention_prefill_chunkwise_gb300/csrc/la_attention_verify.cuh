@@ -277,7 +277,7 @@ __device__ __forceinline__ void verify_products(VerifyShared<D>& sm, uint32_t tm
   for (uint32_t i = 0; ok; ++i) {
     const uint32_t is = i % kPieces, qs = i & 1;
     if (!warp_wait(&sm.piece_full[is], (i / kPieces) & 1u, abort)) break;
-    const int count = sm.pieces[is].b < 0 ? 0 : sm.pieces[is].count;
+    const int count = uniform(sm.pieces[is].b < 0 ? 0 : sm.pieces[is].count);
     warp_arrive(&sm.piece_empty[is], lane);
     if (count == 0) break;
     // the scores of tile j go to buffer (tiles + j) & 1, whose last probabilities the product of tile
@@ -286,13 +286,10 @@ __device__ __forceinline__ void verify_products(VerifyShared<D>& sm, uint32_t tm
       const uint32_t x = slots + 2 * j;
       if (!wait_slot(x)) return false;
       lap::tc_fence_after();
-      if (lane == 0) {
-        product_rows<D>(tmem + ((tiles + j) & 1) * kTile, desc_rows(sm.q[qs]), desc_rows(sm.kv[x % kStages]));
-        lap::mma_commit(&sm.s_full[(tiles + j) & 1]);
-        lap::mma_commit(&sm.kv_empty[x % kStages]);
-        if (j == count - 1) lap::mma_commit(&sm.q_empty[qs]);
-      }
-      __syncwarp();
+      product_rows<D>(tmem + ((tiles + j) & 1) * kTile, desc_rows(sm.q[qs]), desc_rows(sm.kv[x % kStages]));
+      commit(&sm.s_full[(tiles + j) & 1]);
+      commit(&sm.kv_empty[x % kStages]);
+      if (j == count - 1) commit(&sm.q_empty[qs]);
       return true;
     };
     if (!(ok = warp_wait(&sm.q_full[qs], (i >> 1) & 1u, abort)) || !(ok = scores(0))) break;
@@ -302,20 +299,15 @@ __device__ __forceinline__ void verify_products(VerifyShared<D>& sm, uint32_t tm
       if (!(ok = wait_slot(x)) || !(ok = warp_wait(&sm.p_ready[t & 1], (t >> 1) & 1u, abort))) break;
       if (j == 0 && !(ok = warp_wait(&sm.o_free, (i & 1u) ^ 1u, abort))) break;
       lap::tc_fence_after();
-      if (lane == 0) {
-        product_tmem<D>(tmem + 2 * kTile, tmem + (t & 1) * kTile, desc_columns(sm.kv[x % kStages]), j > 0);
-        lap::mma_commit(&sm.pv_done[t & 1]);
-        lap::mma_commit(&sm.kv_empty[x % kStages]);
-      }
-      __syncwarp();
+      product_tmem<D>(tmem + 2 * kTile, tmem + (t & 1) * kTile, desc_columns(sm.kv[x % kStages]), j > 0);
+      commit(&sm.pv_done[t & 1]);
+      commit(&sm.kv_empty[x % kStages]);
     }
     slots += 2 * count;
     tiles += count;
   }
-  if (lane == 0) {
-    lap::mma_commit(&sm.final_bar);
-    drain(&sm.final_bar, 0);  // every product has retired, also after an abort
-  }
+  commit(&sm.final_bar);
+  drain(&sm.final_bar, 0);  // every product has retired, also after an abort
   __syncwarp();
 }
 
@@ -453,7 +445,7 @@ attn_verify_kernel(const __grid_constant__ VerifyMaps maps, const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   VerifyShared<D>& sm =
       *reinterpret_cast<VerifyShared<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   volatile int* abort = &sm.abort;
   lap::griddep_wait();
   lap::griddep_launch_dependents();
@@ -490,7 +482,7 @@ attn_verify_kernel(const __grid_constant__ VerifyMaps maps, const __grid_constan
   lap::tc_fence_before();
   __syncthreads();
   lap::tc_fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = uniform(sm.tmem);
   if (warp < 4)
     verify_softmax<D>(sm, p, v, tmem, tid, abort);
   else if (warp == 4)
