@@ -30,7 +30,7 @@ struct FwdShared {
   Item items[kItems];
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], o_free[2];
   uint64_t final_bar;
   uint32_t bad[2][2][4];  // [item parity][tile][warp]: value rows that are not finite
   uint32_t tmem;
@@ -136,10 +136,15 @@ __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, in
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (!ok || j >= n[s]) continue;
-        if (!(ok = warp_wait(&sm.p_ready[s], p_uses[s]++ & 1u, abort))) continue;
+        // the product with the first 64 values runs while the other probabilities are made
+        if (!(ok = warp_wait(&sm.p_ready[s][0], p_uses[s] & 1u, abort))) continue;
         if (j == 0 && !(ok = warp_wait(&sm.o_free[s], (q_uses[s] & 1u) ^ 1u, abort))) continue;
         lap::tc_fence_after();
-        product_tmem<D>(tmem + 2 * kTile + s * D, tmem + s * kTile, desc_columns(sm.kv[xv % kStages]), j > 0);
+        const uint32_t t_o = tmem + 2 * kTile + s * D, t_p = tmem + s * kTile, v = desc_columns(sm.kv[xv % kStages]);
+        half_product_tmem<D>(t_o, t_p, v, 0, j > 0);
+        if (!(ok = warp_wait(&sm.p_ready[s][1], p_uses[s]++ & 1u, abort))) continue;
+        lap::tc_fence_after();
+        half_product_tmem<D>(t_o, t_p, v, 1, true);
         if (j == n[s] - 1) {
           commit(&sm.o_full[s]);
           ++q_uses[s];
@@ -184,20 +189,26 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
     float m = 0.f;
     uint64_t l = 0;
     float scores[kTile];
-    for (int j = 0; j < n - 1; ++j) {
-      if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
+    auto step = [&](auto seen, bool first) {
+      constexpr Seen kSeen = decltype(seen)::value;
       lap::tc_fence_after();
-      load_scores(t_s, scores);
-      const float z = top_score<kAll>(scores, c, keys);
+      const float z = load_scores<kSeen>(t_s, scores, c, keys);
       // S follows the last product into O in the queue, so O may be rescaled
-      if (j == 0)
+      if (first)
         m = z;
       else if (__any_sync(0xFFFFFFFFu, z > m + kSlack))
         rescale_row<D>(t_o, outgrow(z, m, l));
-      const uint64_t sum = probabilities<kAll>(scores, t_s, c, m, keys);
-      lap::tc_fence_before();
-      warp_arrive(&sm.p_ready[s], lane);
-      l = lap::f2_add(l, sum);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        probabilities<kSeen>(scores, half, t_s, c, m, keys);
+        lap::tc_fence_before();
+        warp_arrive(&sm.p_ready[s][half], lane);
+      }
+      add_sums(scores, l);
+    };
+    for (int j = 0; j < n - 1; ++j) {
+      if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
+      step(std::integral_constant<Seen, kAll>{}, j == 0);
     }
     {
       // the tile on the diagonal: row r sees its keys 0 .. r; its values are made harmless first.  (The
@@ -209,17 +220,7 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
           __ballot_sync(0xFFFFFFFFu, clean_row<D>(sm.kv[x % kStages], row, r0 + row >= it.len));
       if (lane == 0) sm.bad[i & 1][s][warp] = bad;
       lap::fence_proxy_async_smem();
-      lap::tc_fence_after();
-      load_scores(t_s, scores);
-      const float z = top_score<kFirst>(scores, c, keys);
-      if (n == 1)
-        m = z;
-      else if (__any_sync(0xFFFFFFFFu, z > m + kSlack))
-        rescale_row<D>(t_o, outgrow(z, m, l));
-      const uint64_t sum = probabilities<kFirst>(scores, t_s, c, m, keys);
-      lap::tc_fence_before();
-      warp_arrive(&sm.p_ready[s], lane);
-      l = lap::f2_add(l, sum);
+      step(std::integral_constant<Seen, kFirst>{}, n == 1);
     }
     const float2 lp = lap::f2_unpack(l);
     const float total = lp.x + lp.y, inv = 1.f / total;
@@ -276,7 +277,8 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
       lap::mbar_init(&sm.q_full[s], 1);
       lap::mbar_init(&sm.q_empty[s], 1);
       lap::mbar_init(&sm.s_full[s], 1);
-      lap::mbar_init(&sm.p_ready[s], 4);
+      lap::mbar_init(&sm.p_ready[s][0], 4);
+      lap::mbar_init(&sm.p_ready[s][1], 4);
       lap::mbar_init(&sm.o_full[s], 1);
       lap::mbar_init(&sm.o_free[s], 4);
     }

@@ -26,62 +26,62 @@ __device__ __forceinline__ bool sees(const Keys& keys, int k) {
   return k < 64 && (keys.bits[(k >> 5) & 1] >> (k & 31) & 1u);
 }
 
-__device__ __forceinline__ void load_scores(uint32_t t_s, float (&s)[kTile]) {
+// A row's scores of a tile, in registers, and c times the largest (c < 0: smallest) of those that the
+// row sees; about -3.4e38 |c| for none.  What it does not see becomes that as well.
+template <Seen kSeen>
+__device__ __forceinline__ float load_scores(uint32_t t_s, float (&s)[kTile], float c, const Keys& keys) {
+  const bool up = c >= 0.f;
+  const float out = up ? -3.4e38f : 3.4e38f;
+  float t[4] = {out, out, out, out};
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float part[32];
     lap::tmem_ld32(t_s + 32 * g, part);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s[32 * g + i] = part[i];
+    for (int i = 0; i < 32; ++i) s[32 * g + i] = sees<kSeen>(keys, 32 * g + i) ? part[i] : out;
   }
+  if (up) {
+#pragma unroll
+    for (int k = 0; k < kTile; k += 8)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = fmaxf(fmaxf(t[e], s[k + e]), s[k + 4 + e]);
+    return c * fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  }
+#pragma unroll
+  for (int k = 0; k < kTile; ++k) t[k & 3] = fminf(t[k & 3], s[k]);
+  return c * fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
 }
 
-// The row's probabilities over its scores in tensor memory; returns their sum as two partial sums.
+// Half of the row's probabilities over its scores, in registers and, as BF16, in tensor memory.
 template <Seen kSeen>
-__device__ __forceinline__ uint64_t probabilities(float (&s)[kTile], uint32_t t_p, float c, float m, const Keys& keys) {
+__device__ __forceinline__ void probabilities(float (&s)[kTile], int half, uint32_t t_p, float c, float m, const Keys& keys) {
   const uint64_t c2 = lap::f2_pack(c, c), m2 = lap::f2_pack(-m, -m);
-  uint64_t sum[2] = {0, 0};
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
+  for (int g = 2 * half; g < 2 * half + 2; ++g) {
     uint32_t u[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int k = 32 * g + 2 * i;
       const float2 z = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, m2));
-      float a = lap::exp2_approx(z.x), b = lap::exp2_approx(z.y);
+      s[k] = lap::exp2_approx(z.x);
+      s[k + 1] = lap::exp2_approx(z.y);
       if (kSeen != kAll) {
-        a = sees<kSeen>(keys, k) ? a : 0.f;
-        b = sees<kSeen>(keys, k + 1) ? b : 0.f;
+        s[k] = sees<kSeen>(keys, k) ? s[k] : 0.f;
+        s[k + 1] = sees<kSeen>(keys, k + 1) ? s[k + 1] : 0.f;
       }
-      u[i] = lap::pack_bf16x2(a, b);
-      sum[i & 1] = lap::f2_add(sum[i & 1], lap::f2_pack(a, b));
+      u[i] = lap::pack_bf16x2(s[k], s[k + 1]);
     }
     lap::tmem_st16_nowait(t_p + 16 * g, u);
   }
   lap::tmem_wait_st();
-  return lap::f2_add(sum[0], sum[1]);
 }
 
-// c times the largest (c < 0: smallest) of the scores that the row sees; about -3.4e38 |c| for none.
-template <Seen kSeen>
-__device__ __forceinline__ float top_score(float (&s)[kTile], float c, const Keys& keys) {
-  const bool up = c >= 0.f;
-  if (kSeen != kAll) {
-    const float out = up ? -3.4e38f : 3.4e38f;
+// The sum of a row's probabilities, as two partial sums, added to l.
+__device__ __forceinline__ void add_sums(const float (&s)[kTile], uint64_t& l) {
+  uint64_t t[4] = {l, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < kTile; ++k) s[k] = sees<kSeen>(keys, k) ? s[k] : out;
-  }
-  float t[4] = {s[0], s[1], s[2], s[3]};
-  if (up) {
-#pragma unroll
-    for (int k = 4; k < kTile; k += 8)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = fmaxf(fmaxf(t[e], s[k + e]), k + 4 + e < kTile ? s[k + 4 + e] : t[e]);
-    return c * fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-  }
-#pragma unroll
-  for (int k = 4; k < kTile; ++k) t[k & 3] = fminf(t[k & 3], s[k]);
-  return c * fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+  for (int k = 0; k < kTile; k += 2) t[k / 2 & 3] = lap::f2_add(t[k / 2 & 3], lap::f2_pack(s[k], s[k + 1]));
+  l = lap::f2_add(lap::f2_add(t[0], t[1]), lap::f2_add(t[2], t[3]));
 }
 
 // Multiplies this thread's row of O in tensor memory.

@@ -87,13 +87,17 @@ __device__ __forceinline__ void product_rows(uint32_t d, uint32_t a, uint32_t b)
 #pragma unroll
   for (int h = 0; h < D / 64; ++h) mma4_rows<id>(d, a + h * (kBox >> 4), b + h * (kBox >> 4), h > 0);
 }
-// d (+)= a b with a [128 rows, 128 summed] BF16 in tensor memory and b's rows summed.  a's two halves
-// along the sum are 32 columns each, the second kHalf columns behind the first.
+// d (+)= a b with a [128 rows, 128 summed] BF16 in tensor memory and b's rows summed; its two halves
+// along the sum apart.  a's halves are 32 columns each, the second kHalf columns behind the first.
+template <int D, int kHalf = 32>
+__device__ __forceinline__ void half_product_tmem(uint32_t d, uint32_t a, uint32_t b, int half, bool accumulate) {
+  constexpr uint32_t id = lap::idesc_bf16_f32(kTile, D, false, true);
+  mma4_tmem<id>(d, a + half * kHalf, b + half * 512, accumulate);
+}
 template <int D, int kHalf = 32>
 __device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
-  constexpr uint32_t id = lap::idesc_bf16_f32(kTile, D, false, true);
-  mma4_tmem<id>(d, a, b, accumulate);
-  mma4_tmem<id>(d, a + kHalf, b + 512, true);
+  half_product_tmem<D, kHalf>(d, a, b, 0, accumulate);
+  half_product_tmem<D, kHalf>(d, a, b, 1, true);
 }
 
 // A value that is the same in every lane, known to the compiler as such.

@@ -367,10 +367,9 @@ __device__ __forceinline__ void verify_softmax(VerifyShared<D>& sm, const CacheP
       if (busy) {
         lap::tc_fence_after();
         float s[kTile];
-        load_scores(t_s, s);
         auto step = [&](auto seen) {
           constexpr Seen kSeen = decltype(seen)::value;
-          const float z = top_score<kSeen>(s, c, keys);
+          const float z = load_scores<kSeen>(t_s, s, c, keys);
           if (j == 0) {
             m = z;
           } else if (__any_sync(0xFFFFFFFFu, z > m + kSlack)) {
@@ -379,7 +378,8 @@ __device__ __forceinline__ void verify_softmax(VerifyShared<D>& sm, const CacheP
             lap::tc_fence_after();
             rescale_row<D>(t_o, outgrow(z, m, l));
           }
-          l = lap::f2_add(l, probabilities<kSeen>(s, t_s, c, m, keys));
+          probabilities<kSeen>(s, 0, t_s, c, m, keys);
+          probabilities<kSeen>(s, 1, t_s, c, m, keys);
           return true;
         };
         const bool done = all                 ? step(std::integral_constant<Seen, kAll>{})
@@ -387,8 +387,11 @@ __device__ __forceinline__ void verify_softmax(VerifyShared<D>& sm, const CacheP
                                               : step(std::integral_constant<Seen, kFirst>{});
         if (!done) return;
         lap::tc_fence_before();
+        warp_arrive(&sm.p_ready[buf], lane);
+        add_sums(s, l);
+      } else {
+        warp_arrive(&sm.p_ready[buf], lane);
       }
-      warp_arrive(&sm.p_ready[buf], lane);
     }
     slots += 2 * pc.count;
     if (!warp_wait(&sm.pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1u, abort)) return;
