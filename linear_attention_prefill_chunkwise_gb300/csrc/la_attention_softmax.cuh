@@ -32,24 +32,19 @@ template <Seen kSeen>
 __device__ __forceinline__ float load_scores(uint32_t t_s, float (&s)[kTile], float c, const Keys& keys) {
   const bool up = c >= 0.f;
   const float out = up ? -3.4e38f : 3.4e38f;
+  lap::tmem_ld128(t_s, s);
+  if (kSeen != kAll)
+#pragma unroll
+    for (int k = 0; k < kTile; ++k) s[k] = sees<kSeen>(keys, k) ? s[k] : out;
   float t[4] = {out, out, out, out};
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    float part[32];
-    lap::tmem_ld32(t_s + 32 * g, part);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[32 * g + i] = sees<kSeen>(keys, 32 * g + i) ? part[i] : out;
-  }
   if (up) {
 #pragma unroll
-    for (int k = 0; k < kTile; k += 8)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = fmaxf(fmaxf(t[e], s[k + e]), s[k + 4 + e]);
-    return c * fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    for (int k = 0; k < kTile; k += 2) t[k / 2 & 3] = lap::max3(t[k / 2 & 3], s[k], s[k + 1]);
+    return c * lap::max3(fmaxf(t[0], t[1]), t[2], t[3]);
   }
 #pragma unroll
-  for (int k = 0; k < kTile; ++k) t[k & 3] = fminf(t[k & 3], s[k]);
-  return c * fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+  for (int k = 0; k < kTile; k += 2) t[k / 2 & 3] = lap::min3(t[k / 2 & 3], s[k], s[k + 1]);
+  return c * lap::min3(fminf(t[0], t[1]), t[2], t[3]);
 }
 
 // Half of the row's probabilities over its scores, in registers and, as BF16, in tensor memory.
