@@ -26,7 +26,10 @@ using laa::bf16;
 la_host::DeviceState g_dev[la_host::kMaxDevices];
 
 template <int D>
-constexpr int fwd_shared() { return static_cast<int>(sizeof(laa::FwdShared<D>)) + 1024; }
+constexpr int fwd_shared() {
+  static_assert(sizeof(laa::FwdShared<D>) <= 227 * 1024, "shared memory");
+  return static_cast<int>(sizeof(laa::FwdShared<D>));
+}
 
 template <int D>
 constexpr int bwd_shared() {

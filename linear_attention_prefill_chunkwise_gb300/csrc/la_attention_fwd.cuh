@@ -3,12 +3,16 @@
 //
 // A block takes 256 query rows of one head, as two tiles of 128, and walks over the sequence's keys,
 // 128 at a time, with an unnormalised output and a running maximum and sum per row.
-// Warps 0-3 and 4-7 own one query tile each, a thread per row: S is read from tensor memory and p goes
-// back over it as the operand of the second product; O is rarely rescaled and always by its owners,
-// which need no extra warps for it.  Warp 8
+// Warps 0-7 and 8-15 own one query tile each, two threads per row, each with 64 of a tile's keys: S is
+// read from tensor memory and p goes back over it as the operand of the second product; O is rarely
+// rescaled and always by its owners, which need no extra warps for it.  The two threads of a row meet
+// to agree on its maximum: they tell each other what they found and compute on with the old one
+// meanwhile.  (A thread per row, with half the warps, left each scheduler two warps to hide their
+// latencies: 3250 cycles for a round of both tiles, 1.53 ms for 2 x 8192 tokens of 64 heads of 128.)
+// Warp 16
 // issues the products: while one tile's softmax runs, the other tile's two products keep the tensor
 // cores busy (S_a, S_b, then p v and the next S of each in turn, in one queue, so that S can
-// overwrite p).  Warp 9 loads: queries once per item, keys and values through a ring.
+// overwrite p).  Warp 17 loads: queries once per item, keys and values through a ring.
 // The two tiles share keys and values, which halves their traffic from L2.
 //
 // Bound: the tensor cores at D = 128; at D = 64, where the products halve, the softmax.
@@ -18,12 +22,13 @@
 
 namespace laa {
 
-constexpr int kFwdRows = 2 * kTile, kFwdThreads = 384, kItems = 4;
-// Registers: 3 x 168 at launch; a softmax thread holds a row of scores.
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "register shares");
+constexpr int kFwdRows = 2 * kTile, kFwdThreads = 640, kItems = 4;
+// Registers: 5 x 96 at launch.
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
+static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * 96, "register shares");
+
 template <int D>
-struct FwdShared {
+struct alignas(1024) FwdShared {
   static constexpr int kStages = D == 128 ? 5 : 8;
   TileMem<D> q[2];
   TileMem<D> kv[kStages];
@@ -32,7 +37,9 @@ struct FwdShared {
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], o_free[2];
   uint64_t final_bar;
-  uint32_t bad[2][2][4];  // [item parity][tile][warp]: value rows that are not finite
+  uint64_t pair[2][4];       // [tile][warp]: the two halves of its rows meet
+  float said[2][2][kTile];   // [tile][half][row]
+  uint32_t bad[2][2][2][4];  // [item parity][tile][box][32 rows]: value rows that are not finite
   uint32_t tmem;
   int abort;
 };
@@ -141,10 +148,10 @@ __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, in
         if (j == 0 && !(ok = warp_wait(&sm.o_free[s], (q_uses[s] & 1u) ^ 1u, abort))) continue;
         lap::tc_fence_after();
         const uint32_t t_o = tmem + 2 * kTile + s * D, t_p = tmem + s * kTile, v = desc_columns(sm.kv[xv % kStages]);
-        half_product_tmem<D>(t_o, t_p, v, 0, j > 0);
+        half_product_tmem<D, 64>(t_o, t_p, v, 0, j > 0);
         if (!(ok = warp_wait(&sm.p_ready[s][1], p_uses[s]++ & 1u, abort))) continue;
         lap::tc_fence_after();
-        half_product_tmem<D>(t_o, t_p, v, 1, true);
+        half_product_tmem<D, 64>(t_o, t_p, v, 1, true);
         if (j == n[s] - 1) {
           commit(&sm.o_full[s]);
           ++q_uses[s];
@@ -170,12 +177,20 @@ template <int D>
 __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
                                             volatile int* abort) {
   constexpr int kStages = FwdShared<D>::kStages;
-  const int s = tid / kTile, row = tid % kTile, warp = row / 32, lane = tid % 32;
-  const uint32_t t_s = tmem + s * kTile + (static_cast<uint32_t>(32 * warp) << 16);
-  const uint32_t t_o = tmem + 2 * kTile + s * D + (static_cast<uint32_t>(32 * warp) << 16);
+  const int s = tid / (2 * kTile), half = tid / kTile & 1, row = tid % kTile, warp = row / 32, lane = tid % 32;
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+  const uint32_t t_s = t_lane + s * kTile + 64 * half;  // probabilities go over their own scores
+  const uint32_t t_o = t_lane + 2 * kTile + s * D + half * (D / 2);
   const float c = p.scale * kLog2e;
-  const Keys keys{row + 1, {0, 0}};
-  uint32_t slots = 0, tiles = 0, uses = 0;
+  uint64_t* pair = &sm.pair[s][warp];
+  uint32_t slots = 0, tiles = 0, uses = 0, meets = 0;
+  // Tells the row's other half; both halves call it, and then hear what the other said.
+  auto say = [&](float mine) {
+    sm.said[s][half][row] = mine;
+    warp_arrive(pair, lane);
+  };
+  auto meet = [&] { return warp_wait(pair, meets++ & 1u, abort); };
+  const volatile float* theirs = &sm.said[s][half ^ 1][row];
   for (uint32_t i = 0;; ++i) {
     const uint32_t is = i % kItems;
     if (!warp_wait(&sm.item_full[is], (i / kItems) & 1u, abort)) return;
@@ -186,88 +201,119 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
     slots += 2 * max(n, key_tiles(it, s ^ 1));
     if (n == 0) continue;
     const int r0 = it.tile * kFwdRows + s * kTile;
+    const int keep = row + 1 - 64 * half;  // keys of this half that the row sees in the tile on the diagonal
     float m = 0.f;
     uint64_t l = 0;
-    float scores[kTile];
-    auto step = [&](auto seen, bool first) {
-      constexpr Seen kSeen = decltype(seen)::value;
-      lap::tc_fence_after();
-      const float z = load_scores<kSeen>(t_s, scores, c, keys);
-      // S follows the last product into O in the queue, so O may be rescaled
-      if (first)
-        m = z;
-      else if (__any_sync(0xFFFFFFFFu, z > m + kSlack))
-        rescale_row<D>(t_o, outgrow(z, m, l));
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        probabilities<kSeen>(scores, half, t_s, c, m, keys);
-        lap::tc_fence_before();
-        warp_arrive(&sm.p_ready[s][half], lane);
+    auto tile = [&](auto on_diagonal, bool first) {
+      constexpr bool kMasked = decltype(on_diagonal)::value;
+      float x[64];
+      uint32_t u[32];
+      float z = half_scores<kMasked>(t_s, x, c, keep);
+      if (first && uses > 0 && !meet()) return false;  // the other half has heard the last item's sum
+      say(z);
+      if (first) {
+        if (!meet()) return false;
+        m = fmaxf(z, *theirs);
       }
-      add_sums(scores, l);
+      uint64_t sum = half_probabilities<kMasked>(x, u, c, m, keep);
+      if (!first) {
+        // made with the maximum as it was, and again where the row outgrew it
+        if (!meet()) return false;
+        z = fmaxf(z, *theirs);
+        if (__any_sync(0xFFFFFFFFu, z > m + kSlack)) {
+          // S follows the last product into O in the queue, so O may be rescaled
+          rescale_row<D / 2>(t_o, outgrow(z, m, l));
+          half_scores<kMasked>(t_s, x, c, keep);
+          sum = half_probabilities<kMasked>(x, u, c, m, keep);
+        }
+      }
+      lap::tmem_st32_nowait(t_s, u);
+      lap::tmem_wait_st();
+      lap::tc_fence_before();
+      warp_arrive(&sm.p_ready[s][half], lane);
+      l = lap::f2_add(l, sum);
+      return true;
     };
     for (int j = 0; j < n - 1; ++j) {
       if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
-      step(std::integral_constant<Seen, kAll>{}, j == 0);
+      lap::tc_fence_after();
+      if (!tile(std::false_type{}, j == 0)) return;
     }
     {
-      // the tile on the diagonal: row r sees its keys 0 .. r; its values are made harmless first.  (The
-      // scores, made from the slot before, prove that the ring has come to this phase of the values'.)
+      // the tile on the diagonal: row r sees its keys 0 .. r; its values are made harmless first, each
+      // half those that its own probabilities meet.  (The scores, made from the slot before, prove that
+      // the ring has come to this phase of the values'.)
       const uint32_t x = first_slot + 2 * (n - 1) + 1;
       if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
       if (!warp_wait(&sm.kv_full[x % kStages], (x / kStages) & 1u, abort)) return;
+      const int v = 64 * half + row % 64, box = row / 64;
       const uint32_t bad =
-          __ballot_sync(0xFFFFFFFFu, clean_row<D>(sm.kv[x % kStages], row, r0 + row >= it.len));
-      if (lane == 0) sm.bad[i & 1][s][warp] = bad;
+          __ballot_sync(0xFFFFFFFFu, box < D / 64 && clean_box(sm.kv[x % kStages][box < D / 64 ? box : 0], v, r0 + v >= it.len));
+      if (lane == 0) sm.bad[i & 1][s][box][v / 32] = bad;
       lap::fence_proxy_async_smem();
-      step(std::integral_constant<Seen, kFirst>{}, n == 1);
+      lap::tc_fence_after();
+      if (!tile(std::true_type{}, n == 1)) return;
     }
-    const float2 lp = lap::f2_unpack(l);
-    const float total = lp.x + lp.y, inv = 1.f / total;
     const int64_t at = it.lo + r0 + row;
     const bool live = r0 + row < it.len;
+    // (the last product proves that the other half has heard the last maximum)
     if (!warp_wait(&sm.o_full[s], uses++ & 1u, abort)) return;
     lap::tc_fence_after();
-    uint32_t bad[4];
+    const float2 lp = lap::f2_unpack(l);
+    float total = lp.x + lp.y;
+    say(total);
+    if (!meet()) return;
+    total = half ? *theirs + total : total + *theirs;
+    warp_arrive(pair, lane);  // heard: see the next item's first tile
+    const float inv = 1.f / total;
+    uint32_t bad[4], any_bad = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) bad[w] = sm.bad[i & 1][s][w];
-    const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
-    bf16* out = p.o.row(at, it.head);
+    for (int w = 0; w < 4; ++w) {
+      bad[w] = sm.bad[i & 1][s][0][w] | sm.bad[i & 1][s][1][w];
+      any_bad |= bad[w];
+    }
+    bf16* out = p.o.row(at, it.head) + half * (D / 2);
 #pragma unroll 1
-    for (int g = 0; g < D / 32; ++g) {
+    for (int g = 0; g < D / 64; ++g) {
       float o[32];
       lap::tmem_ld32(t_o + 32 * g, o);
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] *= inv;
       if (any_bad)
-        for (int r = 0; r <= row; ++r)
-          if (bad[r >> 5] >> (r & 31) & 1u) restore(o, p.v.row(it.lo + r0 + r, it.head / (p.H / p.HK)) + 32 * g);
+        for (int r = 0; r <= row; ++r) {
+          const uint32_t w = r < 64 ? (r < 32 ? bad[0] : bad[1]) : (r < 96 ? bad[2] : bad[3]);
+          if (w >> (r & 31) & 1u)
+            restore(o, p.v.row(it.lo + r0 + r, it.head / (p.H / p.HK)) + half * (D / 2) + 32 * g);
+        }
       if (live) store_row32(out + 32 * g, o);
     }
     lap::tc_fence_before();
     warp_arrive(&sm.o_free[s], lane);
-    if (p.lse && live) p.lse[static_cast<int64_t>(it.head) * p.tokens + at] = (m + log2f(total)) * kLn2;
+    if (p.lse && live && half == 0) p.lse[static_cast<int64_t>(it.head) * p.tokens + at] = (m + log2f(total)) * kLn2;
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ PrefillParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  FwdShared<D>& sm =
-      *reinterpret_cast<FwdShared<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_tiles[];  // without room to align it: it begins aligned
+  FwdShared<D>& sm = *reinterpret_cast<FwdShared<D>*>(smem_tiles);
   const int tid = threadIdx.x, warp = uniform(tid / 32), lane = tid % 32;
   volatile int* abort = &sm.abort;
   lap::griddep_wait();
   lap::griddep_launch_dependents();
-  if (warp == 8) {
+  if (lap::smem_u32(smem_tiles) & 1023u) {  // swizzled tiles would land elsewhere: leave at once
+    if (tid == 0 && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
+    return;
+  }
+  if (warp == 16) {
     lap::tmem_alloc(&sm.tmem, 512);
     lap::tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < kItems; ++i) {
       lap::mbar_init(&sm.item_full[i], 1);
-      lap::mbar_init(&sm.item_empty[i], 9);
+      lap::mbar_init(&sm.item_empty[i], 17);
     }
     for (int i = 0; i < FwdShared<D>::kStages; ++i) {
       lap::mbar_init(&sm.kv_full[i], 1);
@@ -280,7 +326,8 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
       lap::mbar_init(&sm.p_ready[s][0], 4);
       lap::mbar_init(&sm.p_ready[s][1], 4);
       lap::mbar_init(&sm.o_full[s], 1);
-      lap::mbar_init(&sm.o_free[s], 4);
+      lap::mbar_init(&sm.o_free[s], 8);
+      for (int w = 0; w < 4; ++w) lap::mbar_init(&sm.pair[s][w], 2);
     }
     lap::mbar_init(&sm.final_bar, 1);
     sm.abort = 0;
@@ -293,20 +340,21 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
   __syncthreads();
   lap::tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem);
-  if (warp < 8) {
+  if (tid < 16) sm.bad[tid / 8][tid / 4 % 2][1][tid % 4] = 0;  // D = 64: there is no second box
+  if (warp < 16) {
     lap::registers_grow<kSoftmaxRegs>();
     fwd_softmax<D>(sm, p, tmem, tid, abort);
   } else {
     lap::registers_shrink<kOtherRegs>();
-    if (warp == 8)
+    if (warp == 16)
       fwd_products<D>(sm, tmem, lane, abort);
-    else if (warp == 9)
+    else if (warp == 17)
       fwd_load<D>(sm, p, maps, lane, abort);
   }
   lap::tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
-  if (warp == 8) {
+  if (warp == 16) {
     __syncwarp();
     lap::tc_fence_after();
     lap::tmem_dealloc(tmem, 512);

@@ -213,36 +213,35 @@ struct ItemWalk {
 // Bits of a packed pair of BF16 values that are infinite or NaN (bit 15, bit 31).
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
-// Makes a row of a tile of values harmless where its probabilities are zero because of a mask:
-// 0 * inf is NaN.  A row behind the sequence becomes zero; in a row within it, what is not finite
-// becomes zero and is added again by `restore`.  Returns whether the row held such a value.
+// Makes a row of a box of values harmless where its probabilities are zero because of a mask: 0 * inf
+// is NaN.  A row behind the sequence becomes zero; in a row within it, what is not finite becomes
+// zero and is added again by `restore`.  Returns whether the row held such a value.
+__device__ __forceinline__ bool clean_box(uint8_t (&box)[kBox], int row, bool behind) {
+  uint4* at = reinterpret_cast<uint4*>(box + row * 128);
+  if (behind) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) at[c] = make_uint4(0, 0, 0, 0);
+    return false;
+  }
+  uint32_t any = 0;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint4 v = at[c ^ (row & 7)];  // lanes of neighbouring rows read different banks
+    any |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
+  }
+  if (!any) return false;
+  uint32_t* w = reinterpret_cast<uint32_t*>(at);
+  for (int c = 0; c < 32; ++c) {
+    const uint32_t f = not_finite(w[c]);
+    w[c] &= ~((f >> 15 & 1u) * 0xFFFFu) & ~((f >> 31) * 0xFFFF0000u);
+  }
+  return true;
+}
 template <int D>
 __device__ __forceinline__ bool clean_row(TileMem<D>& tile, int row, bool behind) {
   bool found = false;
 #pragma unroll
-  for (int b = 0; b < D / 64; ++b) {
-    uint4* at = reinterpret_cast<uint4*>(tile[b] + row * 128);
-    if (behind) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) at[c] = make_uint4(0, 0, 0, 0);
-    } else {
-      uint32_t any = 0;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int x = c ^ (row & 7);  // lanes of neighbouring rows read different banks
-        const uint4 v = at[x];
-        any |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
-      }
-      if (any) {
-        found = true;
-        uint32_t* w = reinterpret_cast<uint32_t*>(at);
-        for (int c = 0; c < 32; ++c) {
-          const uint32_t f = not_finite(w[c]);
-          w[c] &= ~((f >> 15 & 1u) * 0xFFFFu) & ~((f >> 31) * 0xFFFF0000u);
-        }
-      }
-    }
-  }
+  for (int b = 0; b < D / 64; ++b) found |= clean_box(tile[b], row, behind);
   return found;
 }
 
