@@ -1,19 +1,20 @@
 // la_attention_fwd.cuh -- causal attention over whole prompts (include/la_attention.h) on the tensor
 // cores.
 //
-// A block takes 256 query rows of one head, as two tiles of 128, and walks over the sequence's keys,
-// 128 at a time, with an unnormalised output and a running maximum and sum per row.
-// Warps 0-7 and 8-15 own one query tile each, two threads per row, each with 64 of a tile's keys: S is
-// read from tensor memory and p goes back over it as the operand of the second product; O is rarely
-// rescaled and always by its owners, which need no extra warps for it.  The two threads of a row meet
-// to agree on its maximum: they tell each other what they found and compute on with the old one
-// meanwhile.  (A thread per row, with half the warps, left each scheduler two warps to hide their
-// latencies: 3250 cycles for a round of both tiles, 1.53 ms for 2 x 8192 tokens of 64 heads of 128.)
-// Warp 16
-// issues the products: while one tile's softmax runs, the other tile's two products keep the tensor
-// cores busy (S_a, S_b, then p v and the next S of each in turn, in one queue, so that S can
-// overwrite p).  Warp 17 loads: queries once per item, keys and values through a ring.
-// The two tiles share keys and values, which halves their traffic from L2.
+// A block takes 256 query rows of one head, as two tiles of 128, and walks over the sequence's keys in
+// steps of 64, with an unnormalised output and a running maximum and sum per row.
+// Warps 0-3 and 4-7 own one query tile each, a thread per row: S is read from tensor memory and p goes
+// back over it as the operand of the second product; O is rarely rescaled and always by its owners,
+// which need no extra warps for it.  Warp 8 issues the products: for each tile in turn p v of a step,
+// then S of the step after next, so that the next step's scores are there when a tile's softmax comes
+// to them.  Warp 9 loads: queries once per item, keys and values through a ring of 128-row tiles.
+// The two query tiles share keys and values, which halves their traffic from L2.
+//
+// Steps: an S of 128 x 128 and one operand p over it would fill tensor memory beside two O of D = 128,
+// and the next S would wait for p v: a round of both tiles then took 3250 cycles for 2048 cycles of
+// products, with a thread or with two per row alike.  With 64 keys there is room for two S of each
+// tile; their products read the queries from shared memory twice as often and take 768 cycles
+// instead of 512 for 128 keys (measured alone), 2480 for the round.
 //
 // Bound: the tensor cores at D = 128; at D = 64, where the products halve, the softmax.
 #pragma once
@@ -22,10 +23,7 @@
 
 namespace laa {
 
-constexpr int kFwdRows = 2 * kTile, kFwdThreads = 640, kItems = 4;
-// Registers: 5 x 96 at launch.
-constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
-static_assert(4 * kSoftmaxRegs + kOtherRegs <= 5 * 96, "register shares");
+constexpr int kFwdRows = 2 * kTile, kStep = 64, kFwdThreads = 320, kItems = 4;
 
 template <int D>
 struct alignas(1024) FwdShared {
@@ -35,10 +33,8 @@ struct alignas(1024) FwdShared {
   Item items[kItems];
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], o_free[2];
+  uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2][2], pv_done[2], o_full[2], o_free[2];
   uint64_t final_bar;
-  uint64_t pair[2][4];       // [tile][warp]: the two halves of its rows meet
-  float said[2][2][kTile];   // [tile][half][row]
   uint32_t bad[2][2][2][4];  // [item parity][tile][box][32 rows]: value rows that are not finite
   uint32_t tmem;
   int abort;
@@ -106,10 +102,26 @@ __device__ __forceinline__ void fwd_load(FwdShared<D>& sm, const PrefillParams& 
   __syncwarp();
 }
 
+// The queue must never run dry, and this warp shares its scheduler with busy ones: it keeps slots and
+// parities as running values, its branches over tile and half are unrolled, and it commits no more
+// than is waited for.  (Computing them anew cost 1100 cycles a visit where its products take 640.)
 template <int D>
 __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, int lane, volatile int* abort) {
-  constexpr int kStages = FwdShared<D>::kStages;
-  uint32_t slots = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+  constexpr uint32_t kStages = FwdShared<D>::kStages, kSlot = sizeof(TileMem<D>) >> 4;
+  constexpr uint32_t id_scores = lap::idesc_bf16_f32(kTile, kStep, false, false);
+  constexpr uint32_t id_values = lap::idesc_bf16_f32(kTile, D, false, true);
+  const uint32_t q0 = desc_rows(sm.q[0]), k0 = desc_rows(sm.kv[0]), v0 = desc_columns(sm.kv[0]);
+  uint32_t slot = 0, phase = 0, items_of[2] = {0, 0}, parity[2] = {0, 0};
+  auto advance = [&] {
+    if (++slot == kStages) slot = 0, phase ^= 1;
+  };
+  auto scores = [&](int s, int h, uint32_t k) {
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x)
+      mma4_rows<id_scores>(tmem + s * kTile + h * kStep, q0 + s * kSlot + x * (kBox >> 4),
+                           k + h * 512 + x * (kBox >> 4), x > 0);
+    commit(&sm.s_full[s][h]);
+  };
   bool ok = true;
   for (uint32_t i = 0; ok; ++i) {
     const uint32_t is = i % kItems;
@@ -119,54 +131,53 @@ __device__ __forceinline__ void fwd_products(FwdShared<D>& sm, uint32_t tmem, in
     if (it.len < 0) break;
     const int n[2] = {key_tiles(it, 0), key_tiles(it, 1)};
     const int most = max(n[0], n[1]);
-    auto slot_of = [&](int j, bool value) { return slots + 2 * j + value; };
-    auto wait_slot = [&](uint32_t x) { return warp_wait(&sm.kv_full[x % kStages], (x / kStages) & 1u, abort); };
-    auto scores = [&](int s, uint32_t x) {
-      lap::tc_fence_after();
-      product_rows<D>(tmem + s * kTile, desc_rows(sm.q[s]), desc_rows(sm.kv[x % kStages]));
-      commit(&sm.s_full[s]);
-    };
-    if (!(ok = wait_slot(slot_of(0, false)))) break;
+    if (!(ok = warp_wait(&sm.kv_full[slot], phase, abort))) break;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (!ok || !n[s]) continue;
-      if (!(ok = warp_wait(&sm.q_full[s], q_uses[s] & 1u, abort))) continue;
-      scores(s, slot_of(0, false));
+      if (!(ok = warp_wait(&sm.q_full[s], items_of[s] & 1u, abort))) continue;
+      lap::tc_fence_after();
+      scores(s, 0, k0 + slot * kSlot);
+      scores(s, 1, k0 + slot * kSlot);
       if (n[s] == 1) commit(&sm.q_empty[s]);
     }
     if (!ok) break;
-    commit(&sm.kv_empty[slot_of(0, false) % kStages]);
-    for (int j = 0; j < most && ok; ++j) {
-      const uint32_t xv = slot_of(j, true), xk = slot_of(j + 1, false);
-      bool keys = false;
-      if (!(ok = wait_slot(xv))) break;
+    commit(&sm.kv_empty[slot]);
+    advance();
+    for (int j = 0; j < most; ++j) {
+      const uint32_t vs = slot, v = v0 + slot * kSlot;
+      if (!(ok = warp_wait(&sm.kv_full[slot], phase, abort))) break;
+      advance();
+      const uint32_t k = k0 + slot * kSlot;  // of the next tile, where there is one
+      const bool more = j + 1 < most;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (!ok || j >= n[s]) continue;
-        // the product with the first 64 values runs while the other probabilities are made
-        if (!(ok = warp_wait(&sm.p_ready[s][0], p_uses[s] & 1u, abort))) continue;
-        if (j == 0 && !(ok = warp_wait(&sm.o_free[s], (q_uses[s] & 1u) ^ 1u, abort))) continue;
-        lap::tc_fence_after();
-        const uint32_t t_o = tmem + 2 * kTile + s * D, t_p = tmem + s * kTile, v = desc_columns(sm.kv[xv % kStages]);
-        half_product_tmem<D, 64>(t_o, t_p, v, 0, j > 0);
-        if (!(ok = warp_wait(&sm.p_ready[s][1], p_uses[s]++ & 1u, abort))) continue;
-        lap::tc_fence_after();
-        half_product_tmem<D, 64>(t_o, t_p, v, 1, true);
-        if (j == n[s] - 1) {
-          commit(&sm.o_full[s]);
-          ++q_uses[s];
-        } else {
-          if (!keys && !(ok = wait_slot(xk))) continue;
-          keys = true;
-          scores(s, xk);
-          if (j + 1 == n[s] - 1) commit(&sm.q_empty[s]);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || j >= n[s]) continue;
+          if (!(ok = warp_wait(&sm.p_ready[s][h], parity[s], abort))) continue;
+          if (h == 0 && j == 0 && !(ok = warp_wait(&sm.o_free[s], (items_of[s] & 1u) ^ 1u, abort))) continue;
+          lap::tc_fence_after();
+          mma4_tmem<id_values>(tmem + 2 * kTile + s * D, tmem + s * kTile + h * kStep, v + h * 512, h > 0 || j > 0);
+          if (j + 1 < n[s]) {
+            // (tile 1 sees every key tile that tile 0 sees, so tile 0 waits for it first if it does)
+            if (h == 0 && (s == 0 || j + 1 >= n[0]) && !(ok = warp_wait(&sm.kv_full[slot], phase, abort))) continue;
+            scores(s, h, k);
+            if (h == 1 && j + 2 == n[s]) commit(&sm.q_empty[s]);
+          } else {
+            commit(h == 0 ? &sm.pv_done[s] : &sm.o_full[s]);
+            if (h == 1) ++items_of[s];
+          }
+          if (h == 1) parity[s] ^= 1;
         }
       }
       if (!ok) break;
-      commit(&sm.kv_empty[xv % kStages]);
-      if (keys) commit(&sm.kv_empty[xk % kStages]);
+      commit(&sm.kv_empty[vs]);
+      if (more) {
+        commit(&sm.kv_empty[slot]);
+        advance();
+      }
     }
-    slots += 2 * most;
   }
   commit(&sm.final_bar);
   drain(&sm.final_bar, 0);  // every product has retired, also after an abort
@@ -177,20 +188,11 @@ template <int D>
 __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
                                             volatile int* abort) {
   constexpr int kStages = FwdShared<D>::kStages;
-  const int s = tid / (2 * kTile), half = tid / kTile & 1, row = tid % kTile, warp = row / 32, lane = tid % 32;
+  const int s = tid / kTile, row = tid % kTile, warp = row / 32, lane = tid % 32;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-  const uint32_t t_s = t_lane + s * kTile + 64 * half;  // probabilities go over their own scores
-  const uint32_t t_o = t_lane + 2 * kTile + s * D + half * (D / 2);
+  const uint32_t t_o = t_lane + 2 * kTile + s * D;
   const float c = p.scale * kLog2e;
-  uint64_t* pair = &sm.pair[s][warp];
-  uint32_t slots = 0, tiles = 0, uses = 0, meets = 0;
-  // Tells the row's other half; both halves call it, and then hear what the other said.
-  auto say = [&](float mine) {
-    sm.said[s][half][row] = mine;
-    warp_arrive(pair, lane);
-  };
-  auto meet = [&] { return warp_wait(pair, meets++ & 1u, abort); };
-  const volatile float* theirs = &sm.said[s][half ^ 1][row];
+  uint32_t slots = 0, steps = 0, uses = 0;
   for (uint32_t i = 0;; ++i) {
     const uint32_t is = i % kItems;
     if (!warp_wait(&sm.item_full[is], (i / kItems) & 1u, abort)) return;
@@ -201,80 +203,70 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
     slots += 2 * max(n, key_tiles(it, s ^ 1));
     if (n == 0) continue;
     const int r0 = it.tile * kFwdRows + s * kTile;
-    const int keep = row + 1 - 64 * half;  // keys of this half that the row sees in the tile on the diagonal
     float m = 0.f;
     uint64_t l = 0;
-    auto tile = [&](auto on_diagonal, bool first) {
-      constexpr bool kMasked = decltype(on_diagonal)::value;
-      float x[64];
-      uint32_t u[32];
-      float z = half_scores<kMasked>(t_s, x, c, keep);
-      if (first && uses > 0 && !meet()) return false;  // the other half has heard the last item's sum
-      say(z);
+    // One step: 64 keys, of which the row sees the first `keep` (kMasked).
+    auto step = [&](auto masked, bool first, bool last, int keep) {
+      constexpr bool kMasked = decltype(masked)::value;
+      const uint32_t b = steps & 1, t_s = t_lane + s * kTile + b * kStep;
+      lap::tc_fence_after();
+      float x[kStep];
+      const float z = half_scores<kMasked>(t_s, x, c, keep);
       if (first) {
-        if (!meet()) return false;
-        m = fmaxf(z, *theirs);
+        m = z;
+      } else if (__any_sync(0xFFFFFFFFu, z > m + kSlack)) {
+        // the scores were made ahead of the last product into O, which has to be done: it is followed by
+        // the next step's scores, or in the last step by a commit of its own
+        if (!(last ? warp_wait(&sm.pv_done[s], uses & 1u, abort)
+                   : warp_wait(&sm.s_full[s][b ^ 1], (steps + 1) >> 1 & 1u, abort)))
+          return false;
+        lap::tc_fence_after();
+        rescale_row<D>(t_o, outgrow(z, m, l));
       }
-      uint64_t sum = half_probabilities<kMasked>(x, u, c, m, keep);
-      if (!first) {
-        // made with the maximum as it was, and again where the row outgrew it
-        if (!meet()) return false;
-        z = fmaxf(z, *theirs);
-        if (__any_sync(0xFFFFFFFFu, z > m + kSlack)) {
-          // S follows the last product into O in the queue, so O may be rescaled
-          rescale_row<D / 2>(t_o, outgrow(z, m, l));
-          half_scores<kMasked>(t_s, x, c, keep);
-          sum = half_probabilities<kMasked>(x, u, c, m, keep);
-        }
-      }
+      uint32_t u[kStep / 2];
+      const uint64_t sum = half_probabilities<kMasked>(x, u, c, m, keep);
       lap::tmem_st32_nowait(t_s, u);
       lap::tmem_wait_st();
       lap::tc_fence_before();
-      warp_arrive(&sm.p_ready[s][half], lane);
+      warp_arrive(&sm.p_ready[s][b], lane);
       l = lap::f2_add(l, sum);
+      ++steps;
       return true;
     };
-    for (int j = 0; j < n - 1; ++j) {
-      if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
-      lap::tc_fence_after();
-      if (!tile(std::false_type{}, j == 0)) return;
+    for (int u = 0; u < 2 * n - 2; ++u) {
+      if (!warp_wait(&sm.s_full[s][steps & 1], steps >> 1 & 1u, abort)) return;
+      if (!step(std::false_type{}, u == 0, false, kStep)) return;
     }
-    {
-      // the tile on the diagonal: row r sees its keys 0 .. r; its values are made harmless first, each
-      // half those that its own probabilities meet.  (The scores, made from the slot before, prove that
-      // the ring has come to this phase of the values'.)
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      // the tile on the diagonal: row r sees its keys 0 .. r; the values of a step are made harmless
+      // first.  (The scores, made from the slot before, prove that the ring has come to this phase of
+      // the values'.)
       const uint32_t x = first_slot + 2 * (n - 1) + 1;
-      if (!warp_wait(&sm.s_full[s], tiles++ & 1u, abort)) return;
+      if (!warp_wait(&sm.s_full[s][steps & 1], steps >> 1 & 1u, abort)) return;
       if (!warp_wait(&sm.kv_full[x % kStages], (x / kStages) & 1u, abort)) return;
-      const int v = 64 * half + row % 64, box = row / 64;
+      const int v = kStep * h + row % kStep, box = row / kStep;
       const uint32_t bad =
           __ballot_sync(0xFFFFFFFFu, box < D / 64 && clean_box(sm.kv[x % kStages][box < D / 64 ? box : 0], v, r0 + v >= it.len));
       if (lane == 0) sm.bad[i & 1][s][box][v / 32] = bad;
       lap::fence_proxy_async_smem();
-      lap::tc_fence_after();
-      if (!tile(std::true_type{}, n == 1)) return;
+      if (!step(std::true_type{}, n == 1 && h == 0, h == 1, row + 1 - kStep * h)) return;
     }
     const int64_t at = it.lo + r0 + row;
     const bool live = r0 + row < it.len;
-    // (the last product proves that the other half has heard the last maximum)
+    const float2 lp = lap::f2_unpack(l);
+    const float total = lp.x + lp.y, inv = 1.f / total;
     if (!warp_wait(&sm.o_full[s], uses++ & 1u, abort)) return;
     lap::tc_fence_after();
-    const float2 lp = lap::f2_unpack(l);
-    float total = lp.x + lp.y;
-    say(total);
-    if (!meet()) return;
-    total = half ? *theirs + total : total + *theirs;
-    warp_arrive(pair, lane);  // heard: see the next item's first tile
-    const float inv = 1.f / total;
     uint32_t bad[4], any_bad = 0;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       bad[w] = sm.bad[i & 1][s][0][w] | sm.bad[i & 1][s][1][w];
       any_bad |= bad[w];
     }
-    bf16* out = p.o.row(at, it.head) + half * (D / 2);
+    bf16* out = p.o.row(at, it.head);
 #pragma unroll 1
-    for (int g = 0; g < D / 64; ++g) {
+    for (int g = 0; g < D / 32; ++g) {
       float o[32];
       lap::tmem_ld32(t_o + 32 * g, o);
 #pragma unroll
@@ -282,14 +274,13 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
       if (any_bad)
         for (int r = 0; r <= row; ++r) {
           const uint32_t w = r < 64 ? (r < 32 ? bad[0] : bad[1]) : (r < 96 ? bad[2] : bad[3]);
-          if (w >> (r & 31) & 1u)
-            restore(o, p.v.row(it.lo + r0 + r, it.head / (p.H / p.HK)) + half * (D / 2) + 32 * g);
+          if (w >> (r & 31) & 1u) restore(o, p.v.row(it.lo + r0 + r, it.head / (p.H / p.HK)) + 32 * g);
         }
       if (live) store_row32(out + 32 * g, o);
     }
     lap::tc_fence_before();
     warp_arrive(&sm.o_free[s], lane);
-    if (p.lse && live && half == 0) p.lse[static_cast<int64_t>(it.head) * p.tokens + at] = (m + log2f(total)) * kLn2;
+    if (p.lse && live) p.lse[static_cast<int64_t>(it.head) * p.tokens + at] = (m + log2f(total)) * kLn2;
   }
 }
 
@@ -306,14 +297,14 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
     if (tid == 0 && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
     return;
   }
-  if (warp == 16) {
+  if (warp == 8) {
     lap::tmem_alloc(&sm.tmem, 512);
     lap::tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < kItems; ++i) {
       lap::mbar_init(&sm.item_full[i], 1);
-      lap::mbar_init(&sm.item_empty[i], 17);
+      lap::mbar_init(&sm.item_empty[i], 9);
     }
     for (int i = 0; i < FwdShared<D>::kStages; ++i) {
       lap::mbar_init(&sm.kv_full[i], 1);
@@ -322,12 +313,13 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
     for (int s = 0; s < 2; ++s) {
       lap::mbar_init(&sm.q_full[s], 1);
       lap::mbar_init(&sm.q_empty[s], 1);
-      lap::mbar_init(&sm.s_full[s], 1);
-      lap::mbar_init(&sm.p_ready[s][0], 4);
-      lap::mbar_init(&sm.p_ready[s][1], 4);
+      lap::mbar_init(&sm.o_free[s], 4);
+      for (int b = 0; b < 2; ++b) {
+        lap::mbar_init(&sm.s_full[s][b], 1);
+        lap::mbar_init(&sm.p_ready[s][b], 4);
+      }
+      lap::mbar_init(&sm.pv_done[s], 1);
       lap::mbar_init(&sm.o_full[s], 1);
-      lap::mbar_init(&sm.o_free[s], 8);
-      for (int w = 0; w < 4; ++w) lap::mbar_init(&sm.pair[s][w], 2);
     }
     lap::mbar_init(&sm.final_bar, 1);
     sm.abort = 0;
@@ -341,20 +333,16 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
   lap::tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem);
   if (tid < 16) sm.bad[tid / 8][tid / 4 % 2][1][tid % 4] = 0;  // D = 64: there is no second box
-  if (warp < 16) {
-    lap::registers_grow<kSoftmaxRegs>();
+  if (warp < 8)
     fwd_softmax<D>(sm, p, tmem, tid, abort);
-  } else {
-    lap::registers_shrink<kOtherRegs>();
-    if (warp == 16)
-      fwd_products<D>(sm, tmem, lane, abort);
-    else if (warp == 17)
-      fwd_load<D>(sm, p, maps, lane, abort);
-  }
+  else if (warp == 8)
+    fwd_products<D>(sm, tmem, lane, abort);
+  else
+    fwd_load<D>(sm, p, maps, lane, abort);
   lap::tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
-  if (warp == 16) {
+  if (warp == 8) {
     __syncwarp();
     lap::tc_fence_after();
     lap::tmem_dealloc(tmem, 512);
