@@ -152,25 +152,31 @@ __device__ __forceinline__ void bwd_stats(BwdShared<D>& sm, const PrefillParams&
 // Tensor memory: S at 0, dP at 128, then dv and dk, or two buffers of dS and dq.
 constexpr int kColDp = kTile, kColDv = 2 * kTile, kColDs = 2 * kTile, kColDq = 3 * kTile;
 
+// (Slots and parities are running values, as in the forward kernel.)
 template <int D, bool kDq>
 __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int lane,
                                              volatile int* abort) {
+  constexpr uint32_t kSlot = sizeof(TileMem<D>) >> 4;
   const uint32_t t_dp = tmem + kColDp, t_dv = tmem + kColDv, t_dk = t_dv + D;
-  uint32_t tiles = 0;  // of all items; tile t has long slot t % 3 and brief slot t % 2
+  const uint32_t own0 = desc_rows(sm.own[0]), long_rows = desc_rows(sm.long_[0]), long_columns = desc_columns(sm.long_[0]);
+  const uint32_t brief_rows = desc_rows(sm.brief[0]), brief_columns = desc_columns(sm.brief[0]);
+  uint32_t next = 0, next_phase = 0;  // long slot of the next scores
+  uint32_t tiles = 0;                 // whose products have begun; parities of barriers used once a tile
   bool ok = true;
-  auto wait_long = [&](uint32_t t) { return warp_wait(&sm.long_full[t % 3], (t / 3) & 1u, abort); };
-  auto wait_brief = [&](uint32_t t) { return warp_wait(&sm.brief_full[t % 2], (t / 2) & 1u, abort); };
-  auto scores = [&](uint32_t t) {
+  auto scores = [&](uint32_t slot) {
     lap::tc_fence_after();
-    product_rows<D>(tmem, desc_rows(sm.own[0]), desc_rows(sm.long_[t % 3]));
+    product_rows<D>(tmem, own0, long_rows + slot * kSlot);
     commit(&sm.s_full);
   };
-  auto dps = [&](uint32_t t, bool last) {
+  auto dps = [&](uint32_t slot, bool last) {
     lap::tc_fence_after();
-    product_rows<D>(t_dp, desc_rows(sm.own[1]), desc_rows(sm.brief[t % 2]));
+    product_rows<D>(t_dp, own0 + kSlot, brief_rows + slot * kSlot);
     commit(&sm.dp_full);
-    if (kDq) commit(&sm.brief_empty[t % 2]);
+    if (kDq) commit(&sm.brief_empty[slot]);
     if (last) commit(&sm.own_empty);
+  };
+  auto advance = [&] {
+    if (++next == 3) next = 0, next_phase ^= 1;
   };
   for (uint32_t i = 0; ok; ++i) {
     const uint32_t is = i % kBwdItems;
@@ -181,48 +187,57 @@ __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillPara
     const int count = passes_of<kDq>(p, it).count;
     if (!(ok = warp_wait(&sm.own_full, i & 1u, abort))) break;
     // the first tile's scores and dP; their columns were read before the last item's last product
-    if (!(ok = wait_long(tiles)) || (kDq && !(ok = warp_wait(&sm.s_free, (tiles & 1u) ^ 1u, abort)))) break;
-    scores(tiles);
-    if (!(ok = wait_brief(tiles)) || (kDq && !(ok = warp_wait(&sm.dp_free, (tiles & 1u) ^ 1u, abort)))) break;
-    dps(tiles, count == 1);
-    for (int n = 0; n < count; ++n) {
-      const uint32_t t = tiles + n;
+    uint32_t slot = next;  // long slot of the tile whose sums are next
+    if (!(ok = warp_wait(&sm.long_full[next], next_phase, abort)) ||
+        (kDq && !(ok = warp_wait(&sm.s_free, (tiles & 1u) ^ 1u, abort))))
+      break;
+    scores(next);
+    advance();
+    if (!(ok = warp_wait(&sm.brief_full[tiles & 1], tiles >> 1 & 1u, abort)) ||
+        (kDq && !(ok = warp_wait(&sm.dp_free, (tiles & 1u) ^ 1u, abort))))
+      break;
+    dps(tiles & 1, count == 1);
+    for (int n = 0; n < count; ++n, ++tiles) {
       const bool more = n + 1 < count;
+      const uint32_t parity = tiles & 1, other = parity ^ 1, brief_phase = (tiles + 1) >> 1 & 1u;
       if (kDq) {
         if (more) {
-          if (!(ok = wait_long(t + 1)) || !(ok = warp_wait(&sm.s_free, t & 1u, abort))) break;
-          scores(t + 1);
-          if (!(ok = wait_brief(t + 1)) || !(ok = warp_wait(&sm.dp_free, t & 1u, abort))) break;
-          dps(t + 1, n + 2 == count);
+          if (!(ok = warp_wait(&sm.long_full[next], next_phase, abort)) || !(ok = warp_wait(&sm.s_free, parity, abort))) break;
+          scores(next);
+          if (!(ok = warp_wait(&sm.brief_full[other], brief_phase, abort)) || !(ok = warp_wait(&sm.dp_free, parity, abort))) break;
+          dps(other, n + 2 == count);
         }
-        if (!(ok = warp_wait(&sm.ds_ready, t & 1u, abort))) break;
+        if (!(ok = warp_wait(&sm.ds_ready, parity, abort))) break;
         if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
         lap::tc_fence_after();
-        product_tmem<D>(tmem + kColDq, tmem + kColDs + 64 * (t & 1), desc_columns(sm.long_[t % 3]), n > 0);
-        commit(&sm.long_empty[t % 3]);
+        product_tmem<D>(tmem + kColDq, tmem + kColDs + 64 * parity, long_columns + slot * kSlot, n > 0);
+        commit(&sm.long_empty[slot]);
         if (!more) commit(&sm.acc_full);
       } else {
-        if (!(ok = warp_wait(&sm.p_ready, t & 1u, abort))) break;
+        if (!(ok = warp_wait(&sm.p_ready, parity, abort))) break;
         if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
         lap::tc_fence_after();
-        product_tmem<D, 64>(t_dv, tmem, desc_columns(sm.brief[t % 2]), n > 0);
-        commit(&sm.brief_empty[t % 2]);
+        product_tmem<D, 64>(t_dv, tmem, brief_columns + parity * kSlot, n > 0);
+        commit(&sm.brief_empty[parity]);
         if (more) {
-          if (!(ok = wait_long(t + 1))) break;
-          scores(t + 1);
+          if (!(ok = warp_wait(&sm.long_full[next], next_phase, abort))) break;
+          scores(next);
         }
-        if (!(ok = warp_wait(&sm.ds_ready, t & 1u, abort))) break;
+        if (!(ok = warp_wait(&sm.ds_ready, parity, abort))) break;
         lap::tc_fence_after();
-        product_tmem<D, 64>(t_dk, t_dp, desc_columns(sm.long_[t % 3]), n > 0);
-        commit(&sm.long_empty[t % 3]);
+        product_tmem<D, 64>(t_dk, t_dp, long_columns + slot * kSlot, n > 0);
+        commit(&sm.long_empty[slot]);
         if (!more) commit(&sm.acc_full);
         if (more) {
-          if (!(ok = wait_brief(t + 1))) break;
-          dps(t + 1, n + 2 == count);
+          if (!(ok = warp_wait(&sm.brief_full[other], brief_phase, abort))) break;
+          dps(other, n + 2 == count);
         }
       }
+      if (more) {
+        slot = next;
+        advance();
+      }
     }
-    tiles += count;
   }
   commit(&sm.final_bar);
   drain(&sm.final_bar, 0);  // every product has retired, also after an abort

@@ -108,42 +108,4 @@ __device__ __forceinline__ float outgrow(float z, float& m, uint64_t& l) {
   return f;
 }
 
-// The same for a thread that has 64 of the tile's keys (forward); masked: it sees the first `keep`.
-template <bool kMasked>
-__device__ __forceinline__ float half_scores(uint32_t t_s, float (&s)[64], float c, int keep) {
-  const bool up = c >= 0.f;
-  const float out = up ? -3.4e38f : 3.4e38f;
-  lap::tmem_ld64(t_s, s);
-  if (kMasked)
-#pragma unroll
-    for (int k = 0; k < 64; ++k) s[k] = k < keep ? s[k] : out;
-  float t[4] = {out, out, out, out};
-  if (up) {
-#pragma unroll
-    for (int k = 0; k < 64; k += 2) t[k / 2 & 3] = lap::max3(t[k / 2 & 3], s[k], s[k + 1]);
-    return c * lap::max3(fmaxf(t[0], t[1]), t[2], t[3]);
-  }
-#pragma unroll
-  for (int k = 0; k < 64; k += 2) t[k / 2 & 3] = lap::min3(t[k / 2 & 3], s[k], s[k + 1]);
-  return c * lap::min3(fminf(t[0], t[1]), t[2], t[3]);
-}
-// Its probabilities as BF16 pairs; returns their sum as two partial sums.
-template <bool kMasked>
-__device__ __forceinline__ uint64_t half_probabilities(const float (&s)[64], uint32_t (&u)[32], float c, float m, int keep) {
-  const uint64_t c2 = lap::f2_pack(c, c), m2 = lap::f2_pack(-m, -m);
-  uint64_t sum[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 64; k += 2) {
-    const float2 z = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, m2));
-    float a = lap::exp2_approx(z.x), b = lap::exp2_approx(z.y);
-    if (kMasked) {
-      a = k < keep ? a : 0.f;
-      b = k + 1 < keep ? b : 0.f;
-    }
-    u[k / 2] = lap::pack_bf16x2(a, b);
-    sum[k / 2 & 1] = lap::f2_add(sum[k / 2 & 1], lap::f2_pack(a, b));
-  }
-  return lap::f2_add(sum[0], sum[1]);
-}
-
 }  // namespace laa
