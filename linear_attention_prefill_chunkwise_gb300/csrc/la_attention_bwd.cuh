@@ -9,12 +9,12 @@
 //     K Q^T and V dO^T give scores and dP transposed, keys along the lanes, so that p and dS, written
 //     back over them as BF16, are operands from tensor memory of p^T dO and dS^T Q.
 //   dq: a block owns 128 rows and walks over the keys that they see: Q K^T, dO V^T, then dS K.
-// Two warpgroups share each tile of scores, 64 columns each (a thread has one row).  Warp 8 issues the
+// Four warpgroups share each tile of scores, 32 columns each (a thread has one row).  Warp 16 issues the
 // products in an order that leaves a product or two to run whenever the warpgroups work:
 //   dk, dv:  p^T dO (n), S (n + 1), dS^T Q (n), dP (n + 1)
 //   dq:      S (n + 1), dP (n + 1), dS K (n)
-// Warp 9 loads: a pair of tiles that stays for the item, and rings of three and two tiles for the
-// operands that pass, as long as each is in use.  Warp 10 brings lse and delta of the rows that pass.
+// Warp 17 loads: a pair of tiles that stays for the item, and rings of three and two tiles for the
+// operands that pass, as long as each is in use.  Warp 18 brings lse and delta of the rows that pass.
 //
 // Bound: the tensor cores.
 #pragma once
@@ -23,7 +23,8 @@
 
 namespace laa {
 
-constexpr int kBwdThreads = 384, kBwdItems = 2, kDeltaThreads = 256;
+constexpr int kParts = 4, kColumns = kTile / kParts;  // warpgroups of a tile of scores, columns of each
+constexpr int kBwdThreads = kParts * kTile + 128, kBwdItems = 2, kDeltaThreads = 256;
 
 template <int D>
 struct alignas(1024) BwdShared {
@@ -115,7 +116,7 @@ __device__ __forceinline__ void bwd_load(BwdShared<D>& sm, const PrefillParams& 
   __syncwarp();
 }
 
-// dk, dv: lse log2 e and delta of the rows that pass.
+// dk, dv: -lse log2 e and delta of the rows that pass.
 template <int D>
 __device__ __forceinline__ void bwd_stats(BwdShared<D>& sm, const PrefillParams& p, int lane, volatile int* abort) {
   uint32_t tiles = 0;
@@ -133,7 +134,7 @@ __device__ __forceinline__ void bwd_stats(BwdShared<D>& sm, const PrefillParams&
       for (int e = 0; e < 4; ++e) {
         const int row = tile * kTile + 32 * e + lane;
         const int64_t at = static_cast<int64_t>(head) * p.tokens + it.lo + row;
-        lse[e] = row < it.len ? __ldg(p.lse_in + at) * kLog2e : 0.f;
+        lse[e] = row < it.len ? -__ldg(p.lse_in + at) * kLog2e : 0.f;
         delta[e] = row < it.len ? p.delta[at] : 0.f;
       }
       const uint32_t st = tiles & 1;
@@ -217,7 +218,7 @@ __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillPara
         if (!(ok = warp_wait(&sm.p_ready, parity, abort))) break;
         if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
         lap::tc_fence_after();
-        product_tmem<D, 64>(t_dv, tmem, brief_columns + parity * kSlot, n > 0);
+        product_tmem<D, kColumns>(t_dv, tmem, brief_columns + parity * kSlot, n > 0);
         commit(&sm.brief_empty[parity]);
         if (more) {
           if (!(ok = warp_wait(&sm.long_full[next], next_phase, abort))) break;
@@ -225,7 +226,7 @@ __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillPara
         }
         if (!(ok = warp_wait(&sm.ds_ready, parity, abort))) break;
         lap::tc_fence_after();
-        product_tmem<D, 64>(t_dk, t_dp, long_columns + slot * kSlot, n > 0);
+        product_tmem<D, kColumns>(t_dk, t_dp, long_columns + slot * kSlot, n > 0);
         commit(&sm.long_empty[slot]);
         if (!more) commit(&sm.acc_full);
         if (more) {
@@ -242,16 +243,6 @@ __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillPara
   commit(&sm.final_bar);
   drain(&sm.final_bar, 0);  // every product has retired, also after an abort
   __syncwarp();
-}
-
-__device__ __forceinline__ void load_half(uint32_t t, float (&s)[64]) {
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    float part[32];
-    lap::tmem_ld32(t + 32 * g, part);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[32 * g + i] = part[i];
-  }
 }
 
 // Rows of a tile that lie behind the sequence become zero: box `box` of row `row`.
@@ -276,16 +267,16 @@ __device__ __forceinline__ void write_row(uint32_t t, bf16* out, float f, bool l
   }
 }
 
-// dk, dv.  A thread has one key and 64 of a tile's rows.
+// dk, dv.  A thread has one key and kColumns of a tile's rows.
 template <int D>
 __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
                                          volatile int* abort) {
-  const int half = tid / kTile, key = tid % kTile, lane = tid % 32;
+  const int part = tid / kTile, key = tid % kTile, lane = tid % 32;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(key & ~31) << 16);
-  const uint32_t t_s = t_lane + 64 * half, t_dp = t_lane + kColDp + 64 * half;
+  const uint32_t t_s = t_lane + kColumns * part, t_dp = t_lane + kColDp + kColumns * part;
   const float c = p.scale * kLog2e;
-  const uint64_t c2 = lap::f2_pack(c, c), minus = lap::f2_pack(-1.f, -1.f);
-  uint32_t tiles = 0;
+  const uint64_t c2 = lap::f2_pack(c, c);
+  uint32_t tiles = 0, slot = 0;  // slot: tiles % 3
   for (uint32_t i = 0;; ++i) {
     const uint32_t is = i % kBwdItems;
     if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) return;
@@ -297,46 +288,39 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
     for (int n = 0; n < w.count; ++n, ++tiles) {
       const uint32_t st = tiles & 1;
       const int valid = min(kTile, it.len - tile * kTile);
-      // this thread's rows [from, to) of its 64 see the key
-      const int from = tile == it.tile ? key - 64 * half : 0, to = valid - 64 * half;
+      // this thread's rows [from, to) see the key
+      const int from = tile == it.tile ? key - kColumns * part : 0, to = valid - kColumns * part;
       const bool masked = tile == it.tile || valid < kTile;
       if (!warp_wait(&sm.s_full, tiles & 1u, abort)) return;
       if (valid < kTile) {
         // rows behind the sequence must not enter the sums over rows (0 * inf is NaN)
         if (!warp_wait(&sm.dp_full, tiles & 1u, abort)) return;
-        if (key >= valid) {
-          clear_row<D>(sm.long_[tiles % 3], half, key);
-          clear_row<D>(sm.brief[tiles % 2], half, key);
-        }
+        if (key >= valid) clear_row<D>(part < 2 ? sm.long_[slot] : sm.brief[tiles & 1], part & 1, key);
         lap::fence_proxy_async_smem();
       }
       if (!warp_wait(&sm.stat_full[st], (tiles >> 1) & 1u, abort)) return;
       lap::tc_fence_after();
-      float s[64];
-      load_half(t_s, s);
-      const float4* lse = reinterpret_cast<const float4*>(sm.lse[st] + 64 * half);
-      const float4* delta = reinterpret_cast<const float4*>(sm.delta[st] + 64 * half);
+      float s[kColumns];
+      lap::tmem_ld32(t_s, s);
+      const float4* lse = reinterpret_cast<const float4*>(sm.lse[st] + kColumns * part);
+      const float4* delta = reinterpret_cast<const float4*>(sm.delta[st] + kColumns * part);
       auto weights = [&](auto has_mask) {
         constexpr bool kMasked = decltype(has_mask)::value;
+        uint32_t u[kColumns / 2];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t u[16];
+        for (int k = 0; k < kColumns; k += 4) {
+          const float4 l = lse[k / 4];  // minus lse log2 e
+          const float2 z0 = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, lap::f2_pack(l.x, l.y)));
+          const float2 z1 = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k + 2], s[k + 3]), c2, lap::f2_pack(l.z, l.w)));
+          s[k] = lap::exp2_approx(z0.x), s[k + 1] = lap::exp2_approx(z0.y);
+          s[k + 2] = lap::exp2_approx(z1.x), s[k + 3] = lap::exp2_approx(z1.y);
+          if (kMasked)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = 32 * g + 4 * e;
-            const float4 l = lse[k / 4];
-            const float2 z0 = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, lap::f2_mul(minus, lap::f2_pack(l.x, l.y))));
-            const float2 z1 = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k + 2], s[k + 3]), c2, lap::f2_mul(minus, lap::f2_pack(l.z, l.w))));
-            s[k] = lap::exp2_approx(z0.x), s[k + 1] = lap::exp2_approx(z0.y);
-            s[k + 2] = lap::exp2_approx(z1.x), s[k + 3] = lap::exp2_approx(z1.y);
-            if (kMasked)
-#pragma unroll
-              for (int x = k; x < k + 4; ++x) s[x] = x >= from && x < to ? s[x] : 0.f;
-            u[2 * e] = lap::pack_bf16x2(s[k], s[k + 1]);
-            u[2 * e + 1] = lap::pack_bf16x2(s[k + 2], s[k + 3]);
-          }
-          lap::tmem_st16_nowait(t_s + 16 * g, u);
+            for (int x = k; x < k + 4; ++x) s[x] = x >= from && x < to ? s[x] : 0.f;
+          u[k / 2] = lap::pack_bf16x2(s[k], s[k + 1]);
+          u[k / 2 + 1] = lap::pack_bf16x2(s[k + 2], s[k + 3]);
         }
+        lap::tmem_st16_nowait(t_s, u);
       };
       if (masked) weights(std::true_type{}); else weights(std::false_type{});
       lap::tmem_wait_st();
@@ -344,32 +328,28 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
       warp_arrive(&sm.p_ready, lane);
       if (!warp_wait(&sm.dp_full, tiles & 1u, abort)) return;
       lap::tc_fence_after();
+      float dp[kColumns];
+      lap::tmem_ld32(t_dp, dp);
       auto slopes = [&](auto has_mask) {
         constexpr bool kMasked = decltype(has_mask)::value;
+        uint32_t u[kColumns / 2];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float dp[32];
-          uint32_t u[16];
-          lap::tmem_ld32(t_dp + 32 * g, dp);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = 32 * g + 4 * e;
-            const float4 d = delta[k / 4];
-            float2 a = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k], s[k + 1]),
-                                                  lap::f2_sub(lap::f2_pack(dp[4 * e], dp[4 * e + 1]), lap::f2_pack(d.x, d.y))));
-            float2 b = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k + 2], s[k + 3]),
-                                                  lap::f2_sub(lap::f2_pack(dp[4 * e + 2], dp[4 * e + 3]), lap::f2_pack(d.z, d.w))));
-            if (kMasked) {
-              a.x = k >= from && k < to ? a.x : 0.f;
-              a.y = k + 1 >= from && k + 1 < to ? a.y : 0.f;
-              b.x = k + 2 >= from && k + 2 < to ? b.x : 0.f;
-              b.y = k + 3 >= from && k + 3 < to ? b.y : 0.f;
-            }
-            u[2 * e] = lap::pack_bf16x2(a.x, a.y);
-            u[2 * e + 1] = lap::pack_bf16x2(b.x, b.y);
+        for (int k = 0; k < kColumns; k += 4) {
+          const float4 d = delta[k / 4];
+          float2 a = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k], s[k + 1]),
+                                                lap::f2_sub(lap::f2_pack(dp[k], dp[k + 1]), lap::f2_pack(d.x, d.y))));
+          float2 b = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k + 2], s[k + 3]),
+                                                lap::f2_sub(lap::f2_pack(dp[k + 2], dp[k + 3]), lap::f2_pack(d.z, d.w))));
+          if (kMasked) {
+            a.x = k >= from && k < to ? a.x : 0.f;
+            a.y = k + 1 >= from && k + 1 < to ? a.y : 0.f;
+            b.x = k + 2 >= from && k + 2 < to ? b.x : 0.f;
+            b.y = k + 3 >= from && k + 3 < to ? b.y : 0.f;
           }
-          lap::tmem_st16_nowait(t_dp + 16 * g, u);
+          u[k / 2] = lap::pack_bf16x2(a.x, a.y);
+          u[k / 2 + 1] = lap::pack_bf16x2(b.x, b.y);
         }
+        lap::tmem_st16_nowait(t_dp, u);
       };
       if (masked) slopes(std::true_type{}); else slopes(std::false_type{});
       lap::tmem_wait_st();
@@ -380,30 +360,32 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
         lap::mbar_arrive(&sm.stat_empty[st]);
       }
       if (++tile == w.first + w.each) tile = w.first;
+      if (++slot == 3) slot = 0;
     }
     if (!warp_wait(&sm.acc_full, i & 1u, abort)) return;
     lap::tc_fence_after();
     const int64_t at = it.lo + it.tile * kTile + key;
     const bool live = it.tile * kTile + key < it.len;
-    if (half == 0)
-      write_row<D>(t_lane + kColDv, p.dv.row(at, it.head), 1.f, live, 0, D / 32);
+    const int g = (part & 1) * (D / 64);
+    if (part < 2)
+      write_row<D>(t_lane + kColDv, p.dv.row(at, it.head), 1.f, live, g, g + D / 64);
     else
-      write_row<D>(t_lane + kColDv + D, p.dk.row(at, it.head), p.scale, live, 0, D / 32);
+      write_row<D>(t_lane + kColDv + D, p.dk.row(at, it.head), p.scale, live, g, g + D / 64);
     lap::tc_fence_before();
     warp_arrive(&sm.acc_free, lane);
   }
 }
 
-// dq.  A thread has one row and 64 of a tile's keys.
+// dq.  A thread has one row and kColumns of a tile's keys.
 template <int D>
 __device__ __forceinline__ void bwd_dq(BwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
                                        volatile int* abort) {
-  const int half = tid / kTile, row = tid % kTile, lane = tid % 32;
+  const int part = tid / kTile, row = tid % kTile, lane = tid % 32;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(row & ~31) << 16);
-  const uint32_t t_s = t_lane + 64 * half, t_dp = t_lane + kColDp + 64 * half;
+  const uint32_t t_s = t_lane + kColumns * part, t_dp = t_lane + kColDp + kColumns * part;
   const float c = p.scale * kLog2e;
   const uint64_t c2 = lap::f2_pack(c, c);
-  uint32_t tiles = 0;
+  uint32_t tiles = 0, slot = 0;  // slot: tiles % 3
   for (uint32_t i = 0;; ++i) {
     const uint32_t is = i % kBwdItems;
     if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) return;
@@ -416,56 +398,52 @@ __device__ __forceinline__ void bwd_dq(BwdShared<D>& sm, const PrefillParams& p,
     const uint64_t l2 = lap::f2_pack(-lse, -lse), d2 = lap::f2_pack(delta, delta);
     for (int n = 0; n <= it.tile; ++n, ++tiles) {
       const bool masked = n == it.tile;
-      const int keep = row + 1 - 64 * half;  // of this thread's 64 keys, on the diagonal
+      const int keep = row + 1 - kColumns * part;  // of this thread's keys, on the diagonal
       if (!warp_wait(&sm.s_full, tiles & 1u, abort)) return;
       if (masked && it.len < (it.tile + 1) * kTile) {
         // keys behind the sequence must not enter the sum over keys (0 * inf is NaN)
-        if (it.tile * kTile + row >= it.len) clear_row<D>(sm.long_[tiles % 3], half, row);
+        if (it.tile * kTile + row >= it.len && part < 2) clear_row<D>(sm.long_[slot], part, row);
         lap::fence_proxy_async_smem();
       }
       lap::tc_fence_after();
-      float s[64];
-      load_half(t_s, s);
+      float s[kColumns];
+      lap::tmem_ld32(t_s, s);
       lap::tc_fence_before();
       warp_arrive(&sm.s_free, lane);
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
+      for (int k = 0; k < kColumns; k += 2) {
         const float2 z = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, l2));
         s[k] = lap::exp2_approx(z.x), s[k + 1] = lap::exp2_approx(z.y);
       }
       if (!warp_wait(&sm.dp_full, tiles & 1u, abort)) return;
       lap::tc_fence_after();
-      float dp[64];
-      load_half(t_dp, dp);
+      float dp[kColumns];
+      lap::tmem_ld32(t_dp, dp);
       lap::tc_fence_before();
       warp_arrive(&sm.dp_free, lane);
-      const uint32_t t_ds = t_lane + kColDs + 64 * (tiles & 1) + 32 * half;
       auto slopes = [&](auto has_mask) {
         constexpr bool kMasked = decltype(has_mask)::value;
+        uint32_t u[kColumns / 2];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t u[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int k = 32 * g + 2 * e;
-            float2 a = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k], s[k + 1]), lap::f2_sub(lap::f2_pack(dp[k], dp[k + 1]), d2)));
-            if (kMasked) {
-              a.x = k < keep ? a.x : 0.f;
-              a.y = k + 1 < keep ? a.y : 0.f;
-            }
-            u[e] = lap::pack_bf16x2(a.x, a.y);
+        for (int k = 0; k < kColumns; k += 2) {
+          float2 a = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k], s[k + 1]), lap::f2_sub(lap::f2_pack(dp[k], dp[k + 1]), d2)));
+          if (kMasked) {
+            a.x = k < keep ? a.x : 0.f;
+            a.y = k + 1 < keep ? a.y : 0.f;
           }
-          lap::tmem_st16_nowait(t_ds + 16 * g, u);
+          u[k / 2] = lap::pack_bf16x2(a.x, a.y);
         }
+        lap::tmem_st16_nowait(t_lane + kColDs + 64 * (tiles & 1) + kColumns / 2 * part, u);
       };
       if (masked) slopes(std::true_type{}); else slopes(std::false_type{});
       lap::tmem_wait_st();
       lap::tc_fence_before();
       warp_arrive(&sm.ds_ready, lane);
+      if (++slot == 3) slot = 0;
     }
     if (!warp_wait(&sm.acc_full, i & 1u, abort)) return;
     lap::tc_fence_after();
-    write_row<D>(t_lane + kColDq, p.dq.row(at, it.head), p.scale, live, half * (D / 64), (half + 1) * (D / 64));
+    if (part < 2) write_row<D>(t_lane + kColDq, p.dq.row(at, it.head), p.scale, live, part * (D / 64), (part + 1) * (D / 64));
     lap::tc_fence_before();
     warp_arrive(&sm.acc_free, lane);
   }
@@ -484,14 +462,14 @@ attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Pr
     if (tid == 0 && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
     return;
   }
-  if (warp == 8) {
+  if (warp == 16) {
     lap::tmem_alloc(&sm.tmem, 512);
     lap::tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < kBwdItems; ++i) {
       lap::mbar_init(&sm.item_full[i], 1);
-      lap::mbar_init(&sm.item_empty[i], kDq ? 9 : 10);
+      lap::mbar_init(&sm.item_empty[i], kDq ? 17 : 18);
     }
     lap::mbar_init(&sm.own_full, 1);
     lap::mbar_init(&sm.own_empty, 1);
@@ -503,16 +481,16 @@ attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Pr
       lap::mbar_init(&sm.brief_full[i], 1);
       lap::mbar_init(&sm.brief_empty[i], 1);
       lap::mbar_init(&sm.stat_full[i], 1);
-      lap::mbar_init(&sm.stat_empty[i], 8);
+      lap::mbar_init(&sm.stat_empty[i], 16);
     }
     lap::mbar_init(&sm.s_full, 1);
-    lap::mbar_init(&sm.s_free, 8);
+    lap::mbar_init(&sm.s_free, 16);
     lap::mbar_init(&sm.dp_full, 1);
-    lap::mbar_init(&sm.dp_free, 8);
-    lap::mbar_init(&sm.p_ready, 8);
-    lap::mbar_init(&sm.ds_ready, 8);
+    lap::mbar_init(&sm.dp_free, 16);
+    lap::mbar_init(&sm.p_ready, 16);
+    lap::mbar_init(&sm.ds_ready, 16);
     lap::mbar_init(&sm.acc_full, 1);
-    lap::mbar_init(&sm.acc_free, 8);
+    lap::mbar_init(&sm.acc_free, 16);
     lap::mbar_init(&sm.final_bar, 1);
     sm.abort = 0;
     lap::fence_mbar_init();
@@ -525,22 +503,22 @@ attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Pr
   __syncthreads();
   lap::tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem);
-  if (warp < 8) {
+  if (warp < 16) {
     if constexpr (kDq)
       bwd_dq<D>(sm, p, tmem, tid, abort);
     else
       bwd_dkdv<D>(sm, p, tmem, tid, abort);
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     bwd_products<D, kDq>(sm, p, tmem, lane, abort);
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     bwd_load<D, kDq>(sm, p, maps, lane, abort);
-  } else if (warp == 10 && !kDq) {
+  } else if (warp == 18 && !kDq) {
     bwd_stats<D>(sm, p, lane, abort);
   }
   lap::tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
-  if (warp == 8) {
+  if (warp == 16) {
     __syncwarp();
     lap::tc_fence_after();
     lap::tmem_dealloc(tmem, 512);
