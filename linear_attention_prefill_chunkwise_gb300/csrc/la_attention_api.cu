@@ -418,7 +418,9 @@ la_status la_attn_verify(const void* q, const void* k, const void* v, float scal
     return st;
   const int64_t room = page_table ? static_cast<int64_t>(table_width) * page_size : page_size;
   const int64_t most = static_cast<int64_t>(B) * HK * (shape.q_tiles * ((room + laa::kTile - 1) / laa::kTile) + shape.drafts);
-  const int blocks = blocks_for(most, std::min(ds->sms, laa::kVerifyBlocks));
+  // one block per SM, and a number that the heads divide where that leaves few SMs out (see laa::PieceWalk)
+  int blocks = blocks_for(most, std::min(ds->sms, laa::kVerifyBlocks));
+  if (blocks / HK * HK * 16 >= blocks * 15) blocks = blocks / HK * HK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launched(with_dim(D, [&](auto d) {
     constexpr int kD = decltype(d)::value;

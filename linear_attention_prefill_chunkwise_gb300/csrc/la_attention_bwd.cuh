@@ -287,10 +287,8 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
     int tile = w.first;
     for (int n = 0; n < w.count; ++n, ++tiles) {
       const uint32_t st = tiles & 1;
-      const int valid = min(kTile, it.len - tile * kTile);
-      // this thread's rows [from, to) see the key
-      const int from = tile == it.tile ? key - kColumns * part : 0, to = valid - kColumns * part;
-      const bool masked = tile == it.tile || valid < kTile;
+      const int valid = it.len - tile * kTile;
+      if (!warp_wait(&sm.stat_full[st], (tiles >> 1) & 1u, abort)) return;  // there long before the scores
       if (!warp_wait(&sm.s_full, tiles & 1u, abort)) return;
       if (valid < kTile) {
         // rows behind the sequence must not enter the sums over rows (0 * inf is NaN)
@@ -298,7 +296,9 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
         if (key >= valid) clear_row<D>(part < 2 ? sm.long_[slot] : sm.brief[tiles & 1], part & 1, key);
         lap::fence_proxy_async_smem();
       }
-      if (!warp_wait(&sm.stat_full[st], (tiles >> 1) & 1u, abort)) return;
+      // this thread's rows [from, to) see the key
+      const bool masked = tile == it.tile || valid < kTile;
+      const int from = tile == it.tile ? key - kColumns * part : 0, to = valid - kColumns * part;
       lap::tc_fence_after();
       float s[kColumns];
       lap::tmem_ld32(t_s, s);

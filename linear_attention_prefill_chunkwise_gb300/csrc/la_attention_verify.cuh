@@ -90,13 +90,16 @@ __device__ __forceinline__ int draft_tiles(const CacheParams& p, const VerifySha
   return p.mask ? 1 : (min(p.T, (tile + 1) * v.per_tile) + kTile - 1) / kTile;
 }
 
-// The pieces of a block, in order.  Whole-warp calls.
+// The pieces of a block, in order.  The batch's tiles count by key/value head first, then by request, query
+// tile and tile of keys: with a grid that the heads divide, the blocks that read the same tokens of
+// different heads, which lie side by side in the cache, do so at the same time.  Whole-warp calls.
 struct PieceWalk {
-  int64_t at, end, total;  // tiles of the whole batch: this block's next, its end, all
-  int64_t before = 0;      // tiles before request b0
+  int64_t at, end;        // tiles of the whole batch: this block's next, its end
+  int64_t line, total;    // tiles of one head, all
+  int64_t before = 0;     // tiles of the head before request b0
   int b0 = 0, blocks = 0;
-  int len = 0;                      // this lane's request b0 + lane
-  int64_t cost = 0, upto = 0;       // its tiles, and those up to it
+  int len = 0;                 // this lane's request b0 + lane
+  int64_t cost = 0, upto = 0;  // its tiles of a head, and those up to it
   bool loaded = false;
 
   __device__ __forceinline__ int64_t tiles_of(const CacheParams& p, const VerifyShape& v, int b, int& n) const {
@@ -106,17 +109,18 @@ struct PieceWalk {
       if (blockIdx.x == 0 && p.dev_error) atomicOr(p.dev_error, kErrSeqlens);
       return 0;
     }
-    return static_cast<int64_t>(p.HK) * (static_cast<int64_t>(v.q_tiles) * ((n + kTile - 1) / kTile) + v.drafts);
+    return static_cast<int64_t>(v.q_tiles) * ((n + kTile - 1) / kTile) + v.drafts;
   }
 
   __device__ PieceWalk(const CacheParams& p, const VerifyShape& v, int lane) {
-    total = 0;
+    line = 0;
     for (int b = lane; b < p.B; b += 32) {
       int n;
-      total += tiles_of(p, v, b, n);
+      line += tiles_of(p, v, b, n);
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    for (int d = 16; d > 0; d >>= 1) line += __shfl_xor_sync(0xFFFFFFFFu, line, d);
+    total = line * p.HK;
     // no more blocks than tiles, so that none between two others is without one
     blocks = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
     at = end = 0;
@@ -134,7 +138,10 @@ struct PieceWalk {
   __device__ __forceinline__ Piece take(const CacheParams& p, const VerifyShape& v, int lane) {
     Piece pc{-1, 0, 0, 0, 0, 0, 0, 0};
     if (at >= end) return pc;
-    for (;;) {  // at < total, so some request holds it
+    pc.hk = static_cast<int>(at / line);
+    const int64_t place = at - pc.hk * line;
+    if (place < before) before = 0, b0 = 0, loaded = false;  // the next head: from the first request
+    for (;;) {  // place < line, so some request holds it
       if (!loaded) {
         cost = tiles_of(p, v, b0 + lane, len);
         upto = cost;
@@ -145,16 +152,13 @@ struct PieceWalk {
         }
         loaded = true;
       }
-      const uint32_t reach = __ballot_sync(0xFFFFFFFFu, before + upto > at);
+      const uint32_t reach = __ballot_sync(0xFFFFFFFFu, before + upto > place);
       if (reach) {
         const int l = __ffs(reach) - 1;
         pc.b = b0 + l;
         pc.len = __shfl_sync(0xFFFFFFFFu, len, l);
-        int64_t x = at - (before + __shfl_sync(0xFFFFFFFFu, upto, l) - __shfl_sync(0xFFFFFFFFu, cost, l));
+        int64_t x = place - (before + __shfl_sync(0xFFFFFFFFu, upto, l) - __shfl_sync(0xFFFFFFFFu, cost, l));
         const int ct = (pc.len + kTile - 1) / kTile;
-        const int64_t per_head = static_cast<int64_t>(v.q_tiles) * ct + v.drafts;
-        pc.hk = static_cast<int>(x / per_head);
-        x -= pc.hk * per_head;
         pc.tiles = ct + draft_tiles(p, v, 0);
         while (x >= pc.tiles) {
           x -= pc.tiles;
@@ -169,7 +173,7 @@ struct PieceWalk {
       before += __shfl_sync(0xFFFFFFFFu, upto, 31);
       b0 += 32;
       loaded = false;
-      if (b0 >= p.B) return pc;
+      if (b0 >= p.B) return Piece{-1, 0, 0, 0, 0, 0, 0, 0};
     }
   }
 };
@@ -503,8 +507,9 @@ attn_verify_kernel(const __grid_constant__ VerifyMaps maps, const __grid_constan
 }
 
 // Joins the parts of the items that begin in block blockIdx.x of the kernel above and end in
-// another: parts 2 c + 1 of that block c, then 2 (c + 1), .. of the blocks up to the last.  A block
-// here takes every kJoinShares-th row; its warps take the parts in turn and are added in order.
+// another: parts 2 c + 1 of that block c, then 2 (c + 1), .. of the blocks up to the last, in order.
+// Few parts: a warp per row.  Many (few, long requests): a block per row, its warps taking the parts
+// in turn, their sums added in order.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ CacheParams p,
                                                                  const __grid_constant__ VerifyShape v) {
@@ -519,51 +524,68 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   if (sp.b < 0) return;
   const int n = sp.last_block - c + 1;
   auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+  const bool wide = n > 32;  // each way, `step` warps share a row's parts, from part `first`
+  const int step = wide ? kWarps : 1, first = wide ? warp : 0;
   bool bad = false;
-  for (int i = threadIdx.x; i < n; i += kJoinThreads) bad = bad || parts.bad[slot(i)];
-  if (__syncthreads_or(bad)) return;
-  for (int row = blockIdx.y; row < v.rows; row += kJoinShares) {
-    const int t = sp.tile * v.per_tile + row / v.group;
-    if (t >= p.T) break;
+  for (int i = lane; i < n; i += 32) bad = bad || parts.bad[slot(i)];
+  if (__any_sync(0xFFFFFFFFu, bad)) return;
+  const int rows_at_once = wide ? 1 : kWarps;
+  for (int r0 = blockIdx.y * rows_at_once; r0 < v.rows; r0 += gridDim.y * rows_at_once) {
+    const int row = r0 + (wide ? 0 : warp), t = sp.tile * v.per_tile + row / v.group;
+    const bool live = row < v.rows && t < p.T;
     float top = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
-      const float2 ml = parts.ml[static_cast<int64_t>(slot(i)) * v.rows + row];
-      if (ml.y != 0.f) top = fmaxf(top, ml.x);
-    }
+    if (live)
+      for (int i = wide ? threadIdx.x : lane; i < n; i += wide ? kJoinThreads : 32) {
+        const float2 ml = parts.ml[static_cast<int64_t>(slot(i)) * v.rows + row];
+        if (ml.y != 0.f) top = fmaxf(top, ml.x);
+      }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
+    if (wide) {
+      if (lane == 0) tops[warp] = top;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
-    float acc[kEach] = {}, total = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < n; i += kWarps) {
-      const int64_t at = static_cast<int64_t>(slot(i)) * v.rows + row;
-      const float2 ml = parts.ml[at];
-      const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
-      total += w * ml.y;
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const float o = parts.o[at * D + 32 * e + lane];
-        acc[e] = ml.y == 0.f ? acc[e] : fmaf(w, o, acc[e]);
-      }
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
     }
+    float acc[kEach] = {}, total = 0.f;
+    if (live)
+#pragma unroll 4
+      for (int i = first; i < n; i += step) {
+        const int64_t at = static_cast<int64_t>(slot(i)) * v.rows + row;
+        const float2 ml = parts.ml[at];
+        const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
+        total += w * ml.y;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) sums[warp][32 * e + lane] = acc[e];
-    if (lane == 0) weights[warp] = total;
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float o = 0.f, w = 0.f;
+        for (int e = 0; e < kEach; ++e) {
+          const float o = parts.o[at * D + kEach * lane + e];
+          acc[e] = ml.y == 0.f ? acc[e] : fmaf(w, o, acc[e]);
+        }
+      }
+    if (wide) {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) sums[warp][kEach * lane + e] = acc[e];
+      if (lane == 0) weights[warp] = total;
+      __syncthreads();
+      total = 0.f;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        o += sums[k][threadIdx.x];
-        w += weights[k];
+        total += weights[k];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) acc[e] += sums[k][kEach * lane + e];
       }
-      p.o.row(static_cast<int64_t>(sp.b) * p.T + t, sp.hk * v.group + row % v.group)[threadIdx.x] =
-          __float2bfloat16_rn(w == 0.f ? 0.f : o / w);
     }
-    __syncthreads();
+    if (live && (!wide || warp == 0)) {
+      bf16* out = p.o.row(static_cast<int64_t>(sp.b) * p.T + t, sp.hk * v.group + row % v.group) + kEach * lane;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) acc[e] = total == 0.f ? 0.f : acc[e] / total;
+      if constexpr (kEach == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(lap::pack_bf16x2(acc[0], acc[1]), lap::pack_bf16x2(acc[2], acc[3]));
+      else
+        *reinterpret_cast<uint32_t*>(out) = lap::pack_bf16x2(acc[0], acc[1]);
+    }
+    if (wide) __syncthreads();
   }
 }
 
