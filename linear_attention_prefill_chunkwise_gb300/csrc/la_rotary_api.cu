@@ -35,9 +35,13 @@ la_status check_sizes(int tokens, int H, int HK, int D, int R, la_dtype dtype) {
   return LA_OK;
 }
 
-la_status device(la_host::DeviceState** ds) {
-  return la_host::current_device(g_dev, ds, [] { return cudaSuccess; });
+// Dynamic shared memory: the rows read ahead, then the angles of the block's tokens.
+template <typename E, int kVec, int D>
+constexpr int rows_bytes(bool backward) {
+  constexpr int kChunks = lar::Layout<E, kVec, D>::kChunks;
+  return backward ? lar::Ahead<E, kVec, 4 * kChunks>::kBytes : lar::Ahead<E, kVec, 2 * kChunks>::kBytes;
 }
+int angle_bytes(int tokens, int R) { return tokens * (R / 2) * static_cast<int>(sizeof(float2)); }
 
 // Tokens whose angles a block holds at once, at most.
 constexpr int kAngleTokens = 16;
@@ -60,6 +64,31 @@ cudaError_t with_layout(bool vec, int D, F f) {
     return f(v, integral_constant<int, 256>{});
   };
   return vec ? at(integral_constant<int, kVec>{}) : at(integral_constant<int, 1>{});
+}
+
+// One-time setup per device: the rows read ahead exceed the default shared memory.
+template <typename E>
+cudaError_t setup_type() {
+  cudaError_t e = cudaSuccess;
+  for (int D = 64; D <= 256; D *= 2)
+    if (e == cudaSuccess)
+      e = with_layout<E>(true, D, [](auto v, auto d) {
+        constexpr int kVec = decltype(v)::value, kD = decltype(d)::value;
+        const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        const cudaError_t r = cudaFuncSetAttribute(lar::norm_rope_fwd_kernel<E, kVec, kD>, most,
+                                                   rows_bytes<E, kVec, kD>(false) + angle_bytes(kAngleTokens, kD));
+        return r != cudaSuccess ? r
+                                : cudaFuncSetAttribute(lar::norm_rope_bwd_kernel<E, kVec, kD>, most,
+                                                       rows_bytes<E, kVec, kD>(true) + angle_bytes(kAngleTokens, kD));
+      });
+  return e;
+}
+
+la_status device(la_host::DeviceState** ds) {
+  return la_host::current_device(g_dev, ds, [] {
+    const cudaError_t e = setup_type<__nv_bfloat16>();
+    return e == cudaSuccess ? setup_type<float>() : e;
+  });
 }
 
 // Whether the heads can be read and written 16 bytes at a time.
@@ -150,8 +179,9 @@ la_status la_qk_norm_rope_fwd(const void* q, const void* k, const float* q_weigh
     p.per_block = tokens_per_block(tokens, 16 * ds->sms);
     const int blocks = (tokens + p.per_block - 1) / p.per_block;
     return launched(with_layout<E>(vec, D, [&](auto v, auto d) {
-      return la_host::launch_pdl(lar::norm_rope_fwd_kernel<E, decltype(v)::value, decltype(d)::value>, blocks,
-                                 lar::kThreads, p.per_block * (R / 2) * static_cast<int>(sizeof(float2)),
+      constexpr int kVec = decltype(v)::value, kD = decltype(d)::value;
+      return la_host::launch_pdl(lar::norm_rope_fwd_kernel<E, kVec, kD>, blocks, lar::kThreads,
+                                 rows_bytes<E, kVec, kD>(false) + angle_bytes(p.per_block, R),
                                  static_cast<cudaStream_t>(stream), p);
     }));
   };
@@ -238,9 +268,9 @@ la_status la_qk_norm_rope_bwd(const void* q, const void* k, const float* q_weigh
     cudaError_t ce = cudaSuccess;
     if (tokens > 0)
       ce = with_layout<E>(vec, D, [&](auto v, auto d) {
-        return la_host::launch_resident(lar::norm_rope_bwd_kernel<E, decltype(v)::value, decltype(d)::value>, ds->sms,
-                                        bwd_blocks(tokens), lar::kThreads,
-                                        p.per_block * (R / 2) * static_cast<int>(sizeof(float2)), cs, &blocks, p);
+        constexpr int kVec = decltype(v)::value, kD = decltype(d)::value;
+        return la_host::launch_resident(lar::norm_rope_bwd_kernel<E, kVec, kD>, ds->sms, bwd_blocks(tokens), lar::kThreads,
+                                        rows_bytes<E, kVec, kD>(true) + angle_bytes(p.per_block, R), cs, &blocks, p);
       });
     if (ce == cudaSuccess && sums)
       ce = la_host::launch_pdl(lar::weight_sum_kernel, dim3(D / 32, 2), 1024, 0, cs,

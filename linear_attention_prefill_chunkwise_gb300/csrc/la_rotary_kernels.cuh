@@ -8,6 +8,10 @@
 // the heads (read once, written once); a token's cosines and sines are shared by all of its heads,
 // so a block takes whole tokens and computes them once into shared memory.
 //
+// What bounds it beside the bytes is the number of instructions (at 276 and 452 per row of a warp the
+// kernels ran at 0.86 and 0.6 of the copy rate), so elements go in packed FP32 pairs and a thread's
+// pointers move from head to head without a division.
+//
 // The angle of a pair, in turns, is position * frequency / 2 pi modulo 1: the frequency is scaled
 // to a 64-bit fraction of a turn once, and the product wraps around by itself.  Its error is
 // |position| 2^-53 |frequency| radians, 2^-24 of a turn's half after the conversion to FP32.
@@ -86,26 +90,64 @@ __device__ __forceinline__ float2 angle(int32_t position, float inv_freq) {
   return make_float2(c, s);
 }
 
-// The rotation of kVec pairs; sign = -1 turns back.
+// kVec neighbouring elements as packed FP32 pairs; a single one is a pair whose other half is zero.
 template <int kVec>
-__device__ __forceinline__ void turn(float (&a)[kVec], float (&b)[kVec], const float2* cs, int interleaved, float sign) {
-  if (interleaved && kVec > 1) {
+struct Vec {
+  static constexpr int kN = kVec > 1 ? kVec / 2 : 1;
+  uint64_t v[kN];
+};
+template <int kVec>
+__device__ __forceinline__ Vec<kVec> mul(const Vec<kVec>& x, const Vec<kVec>& y) {
+  Vec<kVec> r;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      float& lo = 2 * e < kVec ? a[(2 * e) % kVec] : b[(2 * e) % kVec];
-      float& hi = 2 * e < kVec ? a[(2 * e + 1) % kVec] : b[(2 * e + 1) % kVec];
-      const float c = cs[e].x, s = sign * cs[e].y, x = lo, y = hi;
-      lo = x * c - y * s;
-      hi = x * s + y * c;
-    }
+  for (int i = 0; i < Vec<kVec>::kN; ++i) r.v[i] = lap::f2_mul(x.v[i], y.v[i]);
+  return r;
+}
+template <int kVec>
+__device__ __forceinline__ Vec<kVec> mul(const Vec<kVec>& x, uint64_t f) {
+  Vec<kVec> r;
+#pragma unroll
+  for (int i = 0; i < Vec<kVec>::kN; ++i) r.v[i] = lap::f2_mul(x.v[i], f);
+  return r;
+}
+template <int kVec>
+__device__ __forceinline__ void add_product(Vec<kVec>& sum, const Vec<kVec>& x, const Vec<kVec>& y) {
+#pragma unroll
+  for (int i = 0; i < Vec<kVec>::kN; ++i) sum.v[i] = lap::f2_fma(x.v[i], y.v[i], sum.v[i]);
+}
+template <int kVec>
+__device__ __forceinline__ void add_dot(uint64_t& sum, const Vec<kVec>& x, const Vec<kVec>& y) {
+#pragma unroll
+  for (int i = 0; i < Vec<kVec>::kN; ++i) sum = lap::f2_fma(x.v[i], y.v[i], sum);
+}
+__device__ __forceinline__ uint64_t both(float f) { return lap::f2_pack(f, f); }
+__device__ __forceinline__ float halves_sum(uint64_t v) {
+  const float2 f = lap::f2_unpack(v);
+  return f.x + f.y;
+}
+
+template <int kVec>
+__device__ __forceinline__ Vec<kVec> load_floats(const float* p) {  // aligned for kVec > 1
+  Vec<kVec> r;
+  if constexpr (kVec == 1) {
+    r.v[0] = lap::f2_pack(*p, 0.f);
   } else {
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const float c = cs[e].x, s = sign * cs[e].y, x = a[e], y = b[e];
-      a[e] = x * c - y * s;
-      b[e] = x * s + y * c;
+    for (int i = 0; i < kVec / 4; ++i) {
+      const float4 f = reinterpret_cast<const float4*>(p)[i];
+      r.v[2 * i] = lap::f2_pack(f.x, f.y);
+      r.v[2 * i + 1] = lap::f2_pack(f.z, f.w);
     }
   }
+  return r;
+}
+template <int kVec>
+__device__ __forceinline__ Vec<kVec> load_weight(const float* w, int at) {
+  Vec<kVec> r;
+#pragma unroll
+  for (int i = 0; i < Vec<kVec>::kN; ++i)
+    r.v[i] = lap::f2_pack(w ? __ldg(w + at + 2 * i) : 1.f, kVec == 1 ? 0.f : w ? __ldg(w + at + (kVec == 1 ? 0 : 2 * i + 1)) : 1.f);
+  return r;
 }
 
 // kVec elements as loaded: the next head's are on their way while one is computed.
@@ -114,8 +156,101 @@ struct Raw {
   using T = std::conditional_t<kVec == 1, E, uint4>;
   T v;
   __device__ __forceinline__ void load(const E* p) { v = *reinterpret_cast<const T*>(p); }
-  __device__ __forceinline__ void expand(float (&f)[kVec]) const { lan::load<kVec>(reinterpret_cast<const E*>(&v), f); }
+  __device__ __forceinline__ Vec<kVec> expand() const {
+    Vec<kVec> r;
+    if constexpr (kVec == 1) {
+      r.v[0] = lap::f2_pack(static_cast<float>(v), 0.f);
+    } else if constexpr (kVec == 4) {
+      r.v[0] = lap::f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+      r.v[1] = lap::f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
+    } else {
+      r.v[0] = lap::bf16x2_to_f2(v.x), r.v[1] = lap::bf16x2_to_f2(v.y);
+      r.v[2] = lap::bf16x2_to_f2(v.z), r.v[3] = lap::bf16x2_to_f2(v.w);
+    }
+    return r;
+  }
 };
+// The rows that a thread reads ahead, kN vectors of each.  With 16-byte vectors they wait in shared
+// memory, kDepth - 1 rows ahead (a thread reads only what it has copied itself, so nothing is waited
+// for but its own copies); single elements in registers, one row ahead.  Of one row ahead in
+// registers, 32 KiB per SM, the gradients came to 0.6 of the copy rate.
+constexpr int kDepth = 4;
+template <typename E, int kVec, int kN>
+struct Ahead {
+  static constexpr int kRows = kVec > 1 ? kDepth - 1 : 1;                    // rows ahead
+  static constexpr int kBytes = kVec > 1 ? kDepth * kN * kThreads * 16 : 0;  // of shared memory
+  Raw<E, kVec> one[kVec > 1 ? 1 : kN];
+  uint4* mine;  // [kDepth][kN][kThreads]
+  int in = 0, out = 0;
+  __device__ explicit Ahead(void* ring) : mine(static_cast<uint4*>(ring) + threadIdx.x) {}
+  __device__ __forceinline__ void load(int i, const E* p) {
+    if constexpr (kVec > 1)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(lap::smem_u32(mine + (in * kN + i) * kThreads)),
+                   "l"(__cvta_generic_to_global(p))
+                   : "memory");
+    else
+      one[i].load(p);
+  }
+  // a row's loads have been issued (or there was none)
+  __device__ __forceinline__ void close() {
+    if constexpr (kVec > 1) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      in = in + 1 == kDepth ? 0 : in + 1;
+    }
+  }
+  // the next row has arrived
+  __device__ __forceinline__ void open() {
+    if constexpr (kVec > 1) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+  }
+  __device__ __forceinline__ Vec<kVec> get(int i) const {
+    if constexpr (kVec > 1) {
+      Raw<E, kVec> r;
+      r.v = mine[(out * kN + i) * kThreads];
+      return r.expand();
+    } else {
+      return one[i].expand();
+    }
+  }
+  __device__ __forceinline__ void drop() {
+    if constexpr (kVec > 1) out = out + 1 == kDepth ? 0 : out + 1;
+  }
+};
+
+template <typename E, int kVec>
+__device__ __forceinline__ void store(E* p, const Vec<kVec>& x) {
+  float f[kVec];
+#pragma unroll
+  for (int i = 0; i < Vec<kVec>::kN; ++i) {
+    const float2 t = lap::f2_unpack(x.v[i]);
+    f[kVec == 1 ? 0 : 2 * i] = t.x;
+    if (kVec > 1) f[(2 * i + 1) % kVec] = t.y;
+  }
+  lan::store<kVec>(p, f);
+}
+
+// The rotation of kVec pairs by the angles of cos[] and sin[]; kBack turns back.
+template <int kVec, bool kBack>
+__device__ __forceinline__ void turn(Vec<kVec>& a, Vec<kVec>& b, const float* cos, const float* sin, int interleaved) {
+  constexpr uint64_t kBoth = 0x8000000080000000ull;  // sign bits
+  if (kVec > 1 && interleaved) {
+    // pairs are neighbours: (x, y) (c, c) + (y, x) (-s, s)
+#pragma unroll
+    for (int i = 0; i < 2 * Vec<kVec>::kN; ++i) {
+      uint64_t& v = i < Vec<kVec>::kN ? a.v[i % Vec<kVec>::kN] : b.v[i % Vec<kVec>::kN];
+      const float2 f = lap::f2_unpack(v);
+      const float s = kBack ? -sin[i] : sin[i];
+      v = lap::f2_fma(v, both(cos[i]), lap::f2_mul(lap::f2_pack(f.y, f.x), lap::f2_pack(-s, s)));
+    }
+    return;
+  }
+  const Vec<kVec> c = load_floats<kVec>(cos), s = load_floats<kVec>(sin);
+#pragma unroll
+  for (int i = 0; i < Vec<kVec>::kN; ++i) {
+    const uint64_t x = a.v[i], y = b.v[i], minus = s.v[i] ^ kBoth;
+    a.v[i] = lap::f2_fma(x, c.v[i], lap::f2_mul(y, kBack ? s.v[i] : minus));
+    b.v[i] = lap::f2_fma(x, kBack ? minus : s.v[i], lap::f2_mul(y, c.v[i]));
+  }
+}
 
 template <int kLanes>
 __device__ __forceinline__ float sum_lanes(float v) {
@@ -124,106 +259,119 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
-template <int kVec>
-__device__ __forceinline__ void load_weight(const float* p, float (&v)[kVec]) {
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) v[e] = p ? __ldg(p + e) : 1.f;
-}
-
-// A thread's own elements of a head and their weights.
-template <typename E, int kVec, int D>
-__device__ __forceinline__ void own_weights(const float* w, int lane, int R, int interleaved,
-                                            int (&at)[Layout<E, kVec, D>::kChunks], int (&bt)[Layout<E, kVec, D>::kChunks],
-                                            float (&wa)[Layout<E, kVec, D>::kChunks][kVec],
-                                            float (&wb)[Layout<E, kVec, D>::kChunks][kVec]) {
-#pragma unroll
-  for (int i = 0; i < Layout<E, kVec, D>::kChunks; ++i) {
-    places<kVec>(lane + 32 * i, R, interleaved, at[i], bt[i]);
-    load_weight<kVec>(w ? w + at[i] : nullptr, wa[i]);
-    load_weight<kVec>(w ? w + bt[i] : nullptr, wb[i]);
-  }
-}
-
-// Cosines and sines of a block's tokens into shared memory, [tokens][R / 2].
+// Cosines and sines of a block's tokens into shared memory, [tokens][R / 2] each.
 template <typename P>
-__device__ __forceinline__ void fill_angles(const P& p, float2* cs, int first, int count) {
+__device__ __forceinline__ void fill_angles(const P& p, float* cos, float* sin, int64_t first, int count) {
   const int half = p.R / 2;
   for (int i = threadIdx.x; i < count * half; i += kThreads) {
     const int t = i / half;
-    cs[i] = angle(__ldg(p.positions + first + t), __ldg(p.inv_freq + (i - t * half)));
+    const float2 cs = angle(__ldg(p.positions + first + t), __ldg(p.inv_freq + (i - t * half)));
+    cos[i] = cs.x;
+    sin[i] = cs.y;
   }
 }
 
+// Heads kGroups rows apart, in the order (token, head): a pointer's steps, and the token within the tile.
+struct Step {
+  int tokens, heads;  // kGroups rows are so many tokens and heads
+  __device__ __forceinline__ Step(int groups, int heads_of) : tokens(groups / heads_of), heads(groups % heads_of) {}
+};
+// Where a thread's rows are: token and head, `rows` rows on each time.
+struct Place {
+  int t, h;
+  __device__ __forceinline__ bool next(const Step& s, int heads) {
+    h += s.heads;
+    const bool wrapped = h >= heads;
+    if (wrapped) h -= heads;
+    t += s.tokens + wrapped;
+    return wrapped;
+  }
+};
+template <typename E>
+struct Walk {
+  E* p;
+  int64_t step, back;
+  __device__ __forceinline__ Walk(const Heads<E>& h, int64_t t, int head, int heads, const Step& s)
+      : p(h.p + t * h.ld + head * h.hs), step(s.tokens * h.ld + s.heads * h.hs), back(h.ld - heads * h.hs) {}
+  __device__ __forceinline__ void next(bool wrapped) { p += wrapped ? step + back : step; }
+};
+
 template <typename E, int kVec, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const FwdParams<E> p) {
+__global__ void __launch_bounds__(kThreads, kVec > 1 ? 3 : 1) norm_rope_fwd_kernel(const FwdParams<E> p) {
   using L = Layout<E, kVec, D>;
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float angles[];
   lap::griddep_wait();
   lap::griddep_launch_dependents();
-  const int first = blockIdx.x * p.per_block;
-  const int count = min(p.per_block, p.tokens - first);
-  const int lane = threadIdx.x % L::kLanes, group = threadIdx.x / L::kLanes;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.per_block;
+  const int count = static_cast<int>(min(static_cast<int64_t>(p.per_block), p.tokens - first));
+  const int lane = threadIdx.x % L::kLanes, group = threadIdx.x / L::kLanes, half = p.R / 2;
+  using Rows = Ahead<E, kVec, 2 * L::kChunks>;
+  float *cos = angles + Rows::kBytes / 4, *sin = cos + p.per_block * half;
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int heads = p.heads[which], rows = count * heads;
-    const Heads<const E> hx = p.x[which];
-    const Heads<E> hy = p.y[which];
+    const Step step(L::kGroups, heads);
+    Place now{group / heads, group % heads}, then = now;
+    Walk<const E> x(p.x[which], first + now.t, now.h, heads, step);
+    Walk<E> y(p.y[which], first + now.t, now.h, heads, step);
     int at[L::kChunks], bt[L::kChunks];
-    float wa[L::kChunks][kVec], wb[L::kChunks][kVec];
-    own_weights<E, kVec, D>(p.weight[which], lane, p.R, p.interleaved, at, bt, wa, wb);
-    Raw<E, kVec> xa[L::kChunks], xb[L::kChunks];
-    auto fetch = [&](int r) {
-      if (r >= rows) return;
-      const int t = r / heads, h = r - t * heads;
-      const E* x = hx.p + (first + t) * hx.ld + h * hx.hs;
+    Vec<kVec> wa[L::kChunks], wb[L::kChunks];
 #pragma unroll
-      for (int i = 0; i < L::kChunks; ++i) {
-        xa[i].load(x + at[i]);
-        xb[i].load(x + bt[i]);
-      }
+    for (int i = 0; i < L::kChunks; ++i) places<kVec>(lane + 32 * i, p.R, p.interleaved, at[i], bt[i]);
+    Rows in(angles);
+    auto fetch = [&](int r) {
+      if (r < rows)
+#pragma unroll
+        for (int i = 0; i < L::kChunks; ++i) {
+          in.load(2 * i, x.p + at[i]);
+          in.load(2 * i + 1, x.p + bt[i]);
+        }
+      in.close();
+      x.next(then.next(step, heads));
     };
-    fetch(group);
+#pragma unroll
+    for (int k = 0; k < Rows::kRows; ++k) fetch(group + k * L::kGroups);
+#pragma unroll
+    for (int i = 0; i < L::kChunks; ++i) {
+      wa[i] = load_weight<kVec>(p.weight[which], at[i]);
+      wb[i] = load_weight<kVec>(p.weight[which], bt[i]);
+    }
     if (which == 0) {
-      fill_angles(p, cs, first, count);
+      fill_angles(p, cos, sin, first, count);
       __syncthreads();
     }
     // every lane of a warp takes the same number of turns (the sums are over whole warps)
-    for (int r0 = 0; r0 < rows; r0 += L::kGroups) {
-      const int r = r0 + group;
+    for (int r = group; r - group < rows; r += L::kGroups) {
       const bool live = r < rows;
-      const int t = live ? r / heads : 0, h = live ? r - t * heads : 0;
-      E* y = hy.p + (first + t) * hy.ld + h * hy.hs;
-      float a[L::kChunks][kVec], b[L::kChunks][kVec], ss = 0.f;
+      Vec<kVec> a[L::kChunks], b[L::kChunks];
+      const float *c = cos + now.t * half, *s = sin + now.t * half;
+      in.open();
 #pragma unroll
       for (int i = 0; i < L::kChunks; ++i) {
-        xa[i].expand(a[i]);
-        xb[i].expand(b[i]);
+        a[i] = in.get(2 * i);
+        b[i] = in.get(2 * i + 1);
       }
-      fetch(r + L::kGroups);
+      in.drop();
+      fetch(r + Rows::kRows * L::kGroups);
+      uint64_t ss = 0;
 #pragma unroll
       for (int i = 0; i < L::kChunks; ++i) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          ss = fmaf(a[i][e], a[i][e], ss);
-          ss = fmaf(b[i][e], b[i][e], ss);
-        }
+        add_dot(ss, a[i], a[i]);
+        add_dot(ss, b[i], b[i]);
       }
-      ss = sum_lanes<L::kLanes>(ss);
-      const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
+      const uint64_t rstd = both(rsqrtf(sum_lanes<L::kLanes>(halves_sum(ss)) * (1.f / D) + p.eps));
 #pragma unroll
       for (int i = 0; i < L::kChunks; ++i) {
-        const int c = lane + 32 * i;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          a[i][e] *= rstd * wa[i][e];
-          b[i][e] *= rstd * wb[i][e];
-        }
-        if (c < p.R / (2 * kVec)) turn<kVec>(a[i], b[i], cs + t * (p.R / 2) + c * kVec, p.interleaved, 1.f);
+        const int g = lane + 32 * i;
+        a[i] = mul(mul(a[i], rstd), wa[i]);
+        b[i] = mul(mul(b[i], rstd), wb[i]);
         if (live) {
-          lan::store<kVec>(y + at[i], a[i]);
-          lan::store<kVec>(y + bt[i], b[i]);
+          if (g < p.R / (2 * kVec)) turn<kVec, false>(a[i], b[i], c + g * kVec, s + g * kVec, p.interleaved);
+          store(y.p + at[i], a[i]);
+          store(y.p + bt[i], b[i]);
         }
       }
+      y.next(now.next(step, heads));
     }
   }
 }
@@ -231,104 +379,112 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const FwdParams
 // The gradients.  A block walks over its share of the tokens, first all of its queries, then
 // all of its keys, and keeps the sums for the weight gradients of its threads' own elements in registers.
 template <typename E, int kVec, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const BwdParams<E> p) {
+__global__ void __launch_bounds__(kThreads, kVec > 1 ? 2 : 1) norm_rope_bwd_kernel(const BwdParams<E> p) {
   using L = Layout<E, kVec, D>;
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float angles[];
   __shared__ float sums[L::kGroups][D];
   lap::griddep_wait();
   lap::griddep_launch_dependents();
-  const int lane = threadIdx.x % L::kLanes, group = threadIdx.x / L::kLanes;
+  const int lane = threadIdx.x % L::kLanes, group = threadIdx.x / L::kLanes, half = p.R / 2;
+  using Rows = Ahead<E, kVec, 4 * L::kChunks>;
+  float *cos = angles + Rows::kBytes / 4, *sin = cos + p.per_block * half;
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int heads = p.heads[which];
-    const Heads<const E> hx = p.x[which], hdy = p.dy[which];
-    const Heads<E> hdx = p.dx[which];
+    const Step step(L::kGroups, heads);
     int at[L::kChunks], bt[L::kChunks];
-    float wa[L::kChunks][kVec], wb[L::kChunks][kVec];
-    own_weights<E, kVec, D>(p.weight[which], lane, p.R, p.interleaved, at, bt, wa, wb);
-    float da[L::kChunks][kVec] = {}, db[L::kChunks][kVec] = {};
+    Vec<kVec> wa[L::kChunks], wb[L::kChunks], da[L::kChunks] = {}, db[L::kChunks] = {};
+#pragma unroll
+    for (int i = 0; i < L::kChunks; ++i) {
+      places<kVec>(lane + 32 * i, p.R, p.interleaved, at[i], bt[i]);
+      wa[i] = load_weight<kVec>(p.weight[which], at[i]);
+      wb[i] = load_weight<kVec>(p.weight[which], bt[i]);
+    }
     const int64_t stop = static_cast<int64_t>(blockIdx.x + 1) * p.tokens / gridDim.x;
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.tokens / gridDim.x; first < stop; first += p.per_block) {
       const int count = static_cast<int>(min(static_cast<int64_t>(p.per_block), stop - first));
       const int rows = count * heads;
-      Raw<E, kVec> xa[L::kChunks], xb[L::kChunks], ya[L::kChunks], yb[L::kChunks];
+      Place now{group / heads, group % heads}, then = now;
+      Walk<const E> x(p.x[which], first + now.t, now.h, heads, step), dy(p.dy[which], first + now.t, now.h, heads, step);
+      Walk<E> dx(p.dx[which], first + now.t, now.h, heads, step);
+      Rows in(angles);
       auto fetch = [&](int r) {
-        if (r >= rows) return;
-        const int t = r / heads, h = r - t * heads;
-        const E* x = hx.p + (first + t) * hx.ld + h * hx.hs;
-        const E* dy = hdy.p + (first + t) * hdy.ld + h * hdy.hs;
+        if (r < rows)
 #pragma unroll
-        for (int i = 0; i < L::kChunks; ++i) {
-          xa[i].load(x + at[i]);
-          xb[i].load(x + bt[i]);
-          ya[i].load(dy + at[i]);
-          yb[i].load(dy + bt[i]);
-        }
+          for (int i = 0; i < L::kChunks; ++i) {
+            in.load(4 * i, x.p + at[i]);
+            in.load(4 * i + 1, x.p + bt[i]);
+            in.load(4 * i + 2, dy.p + at[i]);
+            in.load(4 * i + 3, dy.p + bt[i]);
+          }
+        in.close();
+        const bool wrapped = then.next(step, heads);
+        x.next(wrapped);
+        dy.next(wrapped);
       };
-      fetch(group);
+#pragma unroll
+      for (int k = 0; k < Rows::kRows; ++k) fetch(group + k * L::kGroups);
       __syncthreads();
-      fill_angles(p, cs, static_cast<int>(first), count);
+      fill_angles(p, cos, sin, first, count);
       __syncthreads();
-      for (int r0 = 0; r0 < rows; r0 += L::kGroups) {
-        const int r = r0 + group;
+      for (int r = group; r - group < rows; r += L::kGroups) {
         const bool live = r < rows;
-        const int t = live ? r / heads : 0, h = live ? r - t * heads : 0;
-        float a[L::kChunks][kVec], b[L::kChunks][kVec], ga[L::kChunks][kVec], gb[L::kChunks][kVec];
-        float ss = 0.f, dot = 0.f;
+        Vec<kVec> a[L::kChunks], b[L::kChunks], ga[L::kChunks], gb[L::kChunks];
+        const float *c = cos + now.t * half, *s = sin + now.t * half;
+        in.open();
 #pragma unroll
         for (int i = 0; i < L::kChunks; ++i) {
-          xa[i].expand(a[i]);
-          xb[i].expand(b[i]);
-          ya[i].expand(ga[i]);
-          yb[i].expand(gb[i]);
+          a[i] = in.get(4 * i);
+          b[i] = in.get(4 * i + 1);
+          ga[i] = in.get(4 * i + 2);
+          gb[i] = in.get(4 * i + 3);
         }
-        fetch(r + L::kGroups);
+        in.drop();
+        fetch(r + Rows::kRows * L::kGroups);
+        uint64_t ss = 0, dot = 0;
 #pragma unroll
         for (int i = 0; i < L::kChunks; ++i) {
-          const int c = lane + 32 * i;
-          if (c < p.R / (2 * kVec)) turn<kVec>(ga[i], gb[i], cs + t * (p.R / 2) + c * kVec, p.interleaved, -1.f);
+          const int g = lane + 32 * i;
+          if (live && g < p.R / (2 * kVec)) turn<kVec, true>(ga[i], gb[i], c + g * kVec, s + g * kVec, p.interleaved);
+          add_dot(ss, a[i], a[i]);
+          add_dot(ss, b[i], b[i]);
+          add_dot(dot, mul(wa[i], ga[i]), a[i]);
+          add_dot(dot, mul(wb[i], gb[i]), b[i]);
+        }
+        const float rstd = rsqrtf(sum_lanes<L::kLanes>(halves_sum(ss)) * (1.f / D) + p.eps);
+        const float m = sum_lanes<L::kLanes>(halves_sum(dot)) * rstd * (1.f / D);  // mean of weight g n
+        const uint64_t r2 = both(rstd), m2 = both(-rstd * m);
+        if (live) {
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            ss = fmaf(a[i][e], a[i][e], ss);
-            ss = fmaf(b[i][e], b[i][e], ss);
-            dot = fmaf(wa[i][e] * ga[i][e], a[i][e], dot);
-            dot = fmaf(wb[i][e] * gb[i][e], b[i][e], dot);
+          for (int i = 0; i < L::kChunks; ++i) {
+            // dx = rstd weight g - n rstd m
+            const Vec<kVec> na = mul(a[i], r2), nb = mul(b[i], r2);
+            add_product(da[i], ga[i], na);
+            add_product(db[i], gb[i], nb);
+            Vec<kVec> oa = mul(na, m2), ob = mul(nb, m2);
+            add_product(oa, mul(ga[i], r2), wa[i]);
+            add_product(ob, mul(gb[i], r2), wb[i]);
+            store(dx.p + at[i], oa);
+            store(dx.p + bt[i], ob);
           }
         }
-        ss = sum_lanes<L::kLanes>(ss);
-        dot = sum_lanes<L::kLanes>(dot);
-        const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
-        const float m = dot * rstd * (1.f / D);  // mean of weight g n
-        E* dx = hdx.p + (first + t) * hdx.ld + h * hdx.hs;
-#pragma unroll
-        for (int i = 0; i < L::kChunks; ++i) {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            const float na = a[i][e] * rstd, nb = b[i][e] * rstd;
-            if (live) {
-              da[i][e] = fmaf(ga[i][e], na, da[i][e]);
-              db[i][e] = fmaf(gb[i][e], nb, db[i][e]);
-            }
-            a[i][e] = rstd * (wa[i][e] * ga[i][e] - na * m);
-            b[i][e] = rstd * (wb[i][e] * gb[i][e] - nb * m);
-          }
-          if (live) {
-            lan::store<kVec>(dx + at[i], a[i]);
-            lan::store<kVec>(dx + bt[i], b[i]);
-          }
-        }
+        dx.next(now.next(step, heads));
       }
     }
     if (p.part == nullptr) continue;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < L::kChunks; ++i) {
+    for (int i = 0; i < L::kChunks; ++i)
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        sums[group][at[i] + e] = da[i][e];
-        sums[group][bt[i] + e] = db[i][e];
+      for (int e = 0; e < Vec<kVec>::kN; ++e) {
+        const float2 fa = lap::f2_unpack(da[i].v[e]), fb = lap::f2_unpack(db[i].v[e]);
+        sums[group][at[i] + 2 * e] = fa.x;
+        sums[group][bt[i] + 2 * e] = fb.x;
+        if (kVec > 1) {
+          sums[group][at[i] + 2 * e + 1] = fa.y;
+          sums[group][bt[i] + 2 * e + 1] = fb.y;
+        }
       }
-    }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kThreads) {
       float s = 0.f;
