@@ -35,7 +35,8 @@ DEPENDS = ["la_prefill_api.cu", "la_prefill_kernel.cuh", "sm103_ptx.cuh", "la_de
 HEADERS = ["la_prefill.h", "la_decode.h", "la_segment.h", "la_backward.h", "la_d256.h", "la_gated.h", "la_norm.h",
            "la_rotary.h", "la_attention.h"]
 # parts that can be built alone with a short wait limit
-WAIT_LIMIT_PARTS = {"prefill": ["la_prefill_api.cu"], "gated": ["la_gated_api.cu", "la_norm_api.cu"]}
+WAIT_LIMIT_PARTS = {"prefill": ["la_prefill_api.cu"], "gated": ["la_gated_api.cu", "la_norm_api.cu"],
+                    "attention": ["la_attention_api.cu"]}
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

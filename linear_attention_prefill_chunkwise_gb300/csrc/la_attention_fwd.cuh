@@ -34,7 +34,7 @@ struct alignas(1024) FwdShared {
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], o_free[2];
   uint64_t final_bar;
-  uint32_t bad[2][2][4];  // [item parity][tile][warp]: value rows that are not finite
+  uint32_t bad[kItems][2][4];  // [item][tile][warp]: value rows on its diagonal that are not finite
   uint32_t tmem;
   int abort;
 };
@@ -192,11 +192,13 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
     const uint32_t is = i % kItems;
     if (!warp_wait(&sm.item_full[is], (i / kItems) & 1u, abort)) return;
     const Item it = sm.items[is];
-    warp_arrive(&sm.item_empty[is], lane);
     if (it.len < 0) return;
     const int n = key_tiles(it, s), first_slot = slots;
     slots += 2 * max(n, key_tiles(it, s ^ 1));
-    if (n == 0) continue;
+    if (n == 0) {
+      warp_arrive(&sm.item_empty[is], lane);
+      continue;
+    }
     const int r0 = it.tile * kFwdRows + s * kTile;
     float m = 0.f;
     uint64_t l = 0;
@@ -230,7 +232,7 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
       if (!warp_wait(&sm.kv_full[x % kStages], (x / kStages) & 1u, abort)) return;
       const uint32_t bad =
           __ballot_sync(0xFFFFFFFFu, clean_row<D>(sm.kv[x % kStages], row, r0 + row >= it.len));
-      if (lane == 0) sm.bad[i & 1][s][warp] = bad;
+      if (lane == 0) sm.bad[is][s][warp] = bad;
       lap::fence_proxy_async_smem();
       step(std::integral_constant<Seen, kFirst>{}, n == 1);
     }
@@ -240,10 +242,11 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
     const bool live = r0 + row < it.len;
     if (!warp_wait(&sm.o_full[s], uses++ & 1u, abort)) return;
     lap::tc_fence_after();
-    uint32_t bad[4];
+    // Tile 1 reads the values on tile 0's diagonal from the same memory: what was taken out of them
+    // there it gets back as well, every row of it.
+    uint32_t any_bad = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) bad[w] = sm.bad[i & 1][s][w];
-    const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
+    for (int w = 0; w < 4; ++w) any_bad |= sm.bad[is][s][w] | (s ? sm.bad[is][0][w] : 0u);
     bf16* out = p.o.row(at, it.head);
 #pragma unroll 1
     for (int g = 0; g < D / 32; ++g) {
@@ -252,12 +255,15 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] *= inv;
       if (any_bad)
-        for (int r = 0; r <= row; ++r)
-          if (bad[r >> 5] >> (r & 31) & 1u) restore(o, p.v.row(it.lo + r0 + r, it.head / (p.H / p.HK)) + 32 * g);
+        for (int x = 0; x <= s; ++x)
+          for (int r = 0; r < kTile && (x < s || r <= row); ++r)
+            if (sm.bad[is][x][r >> 5] >> (r & 31) & 1u)
+              restore(o, p.v.row(it.lo + it.tile * kFwdRows + x * kTile + r, it.head / (p.H / p.HK)) + 32 * g);
       if (live) store_row32(out + 32 * g, o);
     }
     lap::tc_fence_before();
     warp_arrive(&sm.o_free[s], lane);
+    warp_arrive(&sm.item_empty[is], lane);
     if (p.lse && live) p.lse[static_cast<int64_t>(it.head) * p.tokens + at] = (m + log2f(total)) * kLn2;
   }
 }

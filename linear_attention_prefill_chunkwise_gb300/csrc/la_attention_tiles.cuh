@@ -105,13 +105,16 @@ template <typename T>
 __device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // Whole-warp wait; false once the block gives up: after a wait of kWaitLimitNs, which sets *abort.
-// (Inline: a kernel that moves registers between its warpgroups makes no calls.)
+// (Inline: a kernel that moves registers between its warpgroups makes no calls.  A build whose limit
+// is short, so that ordinary waits exceed it, polls, as try_wait sits out ordinary latencies itself.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  bool ok = lap::mbar_try_wait(bar, parity);
+  constexpr bool kPoll = lap::kWaitLimitNs < 1000000ull;
+  constexpr uint32_t kEvery = kPoll ? 1 : 16;  // the clock is slow to read: not in an ordinary wait
+  bool ok = kPoll ? lap::mbar_test(bar, parity) : lap::mbar_try_wait(bar, parity);
   uint64_t t0 = 0;
   for (uint32_t i = 1; !ok; ++i) {
-    ok = lap::mbar_try_wait(bar, parity);
-    if ((i & 63u) == 0u && !ok) {  // the clock is slow to read: not in an ordinary wait
+    ok = kPoll ? lap::mbar_test(bar, parity) : lap::mbar_try_wait(bar, parity);
+    if (i % kEvery == 0u && !ok) {
       if (*abort) break;
       const uint64_t now = lap::globaltimer_ns();
       if (t0 == 0) {

@@ -296,3 +296,28 @@ def test_wrong_arguments_are_refused():
         a = dict(q=q, k=q, v=q, scale=1.0, seq_len=4)
         with pytest.raises(kind):
             lap.la_attn_prefill_fwd(**{**a, **over})
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_value_that_is_not_finite_reaches_only_rows_that_see_it(D):
+    """Masked places hold it too: rows before it, in its own tile of keys, keep their bits."""
+    rng = np.random.default_rng(12)
+    q, k, v = make(rng, 400, (4, 2, 2), D, "fused")
+    o, lse = lap.la_attn_prefill_fwd(q, k, v, 0.2, seq_len=400)
+    for row in (0, 1, 63, 64, 127, 128, 200, 255, 300, 399):
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            keep = v[row].clone()
+            v[row, 1, D // 2 + 3] = bad
+            o2, lse2 = lap.la_attn_prefill_fwd(q, k, v, 0.2, seq_len=400)
+            v[row] = keep
+            assert torch.equal(lse, lse2) and torch.equal(o[:row], o2[:row]) and torch.equal(o[:, :2], o2[:, :2])
+            cols = [c for c in range(D) if c != D // 2 + 3]
+            # other columns: the row's own values count in full, except that what is not finite is apart
+            assert torch.equal(o[:, 2:, cols], o2[:, 2:, cols])
+            assert not torch.isfinite(o2[row:, 2:, D // 2 + 3]).any()
+        keepk, keepq = k[row].clone(), q[row].clone()
+        k[row], q[row] = float("nan"), float("nan")
+        o2, lse2 = lap.la_attn_prefill_fwd(q, k, v, 0.2, seq_len=400)
+        k[row], q[row] = keepk, keepq
+        assert torch.equal(o[:row], o2[:row]) and torch.equal(lse[:, :row], lse2[:, :row])
+        assert torch.isnan(o2[row:]).all() and torch.isnan(lse2[:, row:]).all()
