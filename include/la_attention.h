@@ -49,7 +49,7 @@ la_status la_attn_prefill_fwd(const void* q, const void* k, const void* v, float
                               int* dev_error, void* stream);
 
 /* Bytes of device workspace la_attn_prefill_bwd needs for B * T tokens.  Host only. */
-la_status la_attn_prefill_bwd_workspace(int B, int T, int H, size_t* bytes);
+la_status la_attn_prefill_bwd_workspace(int B, int T, int H, int HK, int D, size_t* bytes);
 
 /*
  * la_attn_prefill_bwd -- gradients of la_attn_prefill_fwd for q, k, v, given its o and lse and

@@ -133,7 +133,7 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
             lib.la_qk_norm_rope_bwd.argtypes = [vp] * 4 + [ctypes.c_float] + [vp] * 8 + [i64] * 12 + [i32] * 7 + \
                 [vp, ctypes.c_size_t, vp]
             lib.la_attn_prefill_fwd.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 3 + [i64] * 8 + [i32] * 6 + [vp] * 2
-            lib.la_attn_prefill_bwd_workspace.argtypes = [i32] * 3 + [vp]
+            lib.la_attn_prefill_bwd_workspace.argtypes = [i32] * 5 + [vp]
             lib.la_attn_prefill_bwd.argtypes = [vp] * 3 + [ctypes.c_float] + [vp] * 7 + [i64] * 16 + [i32] * 6 + \
                 [vp, ctypes.c_size_t, vp, vp]
             lib.la_attn_verify_workspace.argtypes = [i32] * 5 + [vp]
@@ -1118,9 +1118,9 @@ def la_attn_prefill_fwd(q, k, v, scale, cu_seqlens=None, seq_len=None, o=None, l
 
 
 @functools.lru_cache(maxsize=1024)
-def la_attn_prefill_bwd_workspace(B, T, H):
+def la_attn_prefill_bwd_workspace(B, T, H, HK, D):
     """Bytes of device workspace la_attn_prefill_bwd needs for B sequences of T tokens (packed: 1, tokens)."""
-    return _bytes_of(load_library().la_attn_prefill_bwd_workspace, B, T, H)
+    return _bytes_of(load_library().la_attn_prefill_bwd_workspace, B, T, H, HK, D)
 
 
 def la_attn_prefill_bwd(q, k, v, scale, o, lse, dout, cu_seqlens=None, seq_len=None, dq=None, dk=None, dv=None,
@@ -1141,7 +1141,7 @@ def la_attn_prefill_bwd(q, k, v, scale, o, lse, dout, cu_seqlens=None, seq_len=N
     dq, pdq, lddq, hsdq = _out_heads(dq, q, "dq", bf16, dev, stream)
     dk, pdk, lddk, hsdk = _out_heads(dk, k, "dk", bf16, dev, stream)
     dv, pdv, lddv, hsdv = _out_heads(dv, v, "dv", bf16, dev, stream)
-    owner, ws, nbytes = _workspace(workspace, la_attn_prefill_bwd_workspace, (B, T, H), dev, stream)
+    owner, ws, nbytes = _workspace(workspace, la_attn_prefill_bwd_workspace, (B, T, H, HK, D), dev, stream)
     _call(lib.la_attn_prefill_bwd, dev, pq, pk, pv, scale, po, plse, pg, cu, pdq, pdk, pdv, ldq, hsq, ldk, hsk, ldv, hsv,
           ldo, hso, ldg, hsg, lddq, hsdq, lddk, hsdk, lddv, hsdv, B, T, N, H, HK, D, ws, nbytes,
           _array(dev_error, "dev_error", torch.int32, (None,), dev), _stream_of(stream, dev))

@@ -234,6 +234,33 @@ uint64_t table_bytes(const int32_t* page_table, int B, int table_width, int64_t 
   return page_table && B > 0 ? (static_cast<uint64_t>(B - 1) * ld_table + table_width) * 4 : 0;
 }
 
+// The gradients' workspace: delta, and, where a group's heads are shared out, the parts' sums and marks.
+// They are shared out where the tiles of all key/value heads are few for the SMs (of the largest part), so
+// that some have none or the busiest has far more than the mean, unless there is little to share.
+// Measured, gradients of one sequence, D = 128, 8 heads on 1: 8192 tokens 332 us (whole groups 766), 4096
+// 108 (363), 300 46 (70), 16384 with 4 heads 587 (872); but 4 x 2048 tokens, 32 heads on 4 (256 items) 425
+// (361), and 128 tokens, 16 heads on 2, 50 (43).
+struct BwdWorkspace {
+  int splits;
+  size_t part, marks, bytes;
+};
+BwdWorkspace bwd_workspace(int64_t tokens, int H, int HK, int D) {
+  constexpr int64_t kSms = 152;
+  const int group = H / HK;
+  const int64_t tiles = (tokens + laa::kTile - 1) / laa::kTile, items = tiles * HK;
+  BwdWorkspace w{1, 0, 0, 0};
+  if (items < kSms + kSms / 4 && group > 1 && tiles * group >= 16) {
+    const int64_t want = std::min<int64_t>(group, (4 * kSms + items - 1) / items);
+    const int each = static_cast<int>((group + want - 1) / want);  // heads of a part
+    w.splits = (group + each - 1) / each;
+  }
+  w.part = la_host::align256(static_cast<size_t>(tokens) * H * sizeof(float));
+  w.marks = w.part;
+  if (w.splits > 1) w.marks += la_host::align256(static_cast<size_t>(w.splits) * 2 * HK * tokens * D * sizeof(float));
+  w.bytes = w.marks + (w.splits > 1 ? la_host::align256(static_cast<size_t>(HK) * tokens) : 0);
+  return w;
+}
+
 template <typename F>
 cudaError_t with_dim(int D, F f) {
   if (D == 64) return f(std::integral_constant<int, 64>{});
@@ -283,12 +310,14 @@ la_status la_attn_prefill_fwd(const void* q, const void* k, const void* v, float
   }));
 }
 
-la_status la_attn_prefill_bwd_workspace(int B, int T, int H, size_t* bytes) {
+la_status la_attn_prefill_bwd_workspace(int B, int T, int H, int HK, int D, size_t* bytes) {
   la_host::g_last_error[0] = '\0';
   if (!bytes) return fail(LA_ERR_INVALID_ARGUMENT, "bytes is null");
-  if (B < 0 || T < 0 || H < 1) return fail(LA_ERR_INVALID_ARGUMENT, "B, T must be >= 0 and H >= 1");
+  const la_status st = check_heads_of(H, HK, D);
+  if (st != LA_OK) return st;
+  if (B < 0 || T < 0) return fail(LA_ERR_INVALID_ARGUMENT, "B and T must be >= 0 (got %d, %d)", B, T);
   if (static_cast<int64_t>(B) * T > kMostTokens) return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)B * T);
-  *bytes = la_host::align256(static_cast<size_t>(B) * T * H * sizeof(float));
+  *bytes = bwd_workspace(static_cast<int64_t>(B) * T, H, HK, D).bytes;
   return LA_OK;
 }
 
@@ -308,7 +337,7 @@ la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float
   if (!la_host::aligned4(lse) || !la_host::aligned4(dev_error))
     return fail(LA_ERR_INVALID_ARGUMENT, "lse and dev_error must be 4-byte aligned");
   size_t need = 0;
-  if ((st = la_attn_prefill_bwd_workspace(B, T, H, &need)) != LA_OK) return st;
+  if ((st = la_attn_prefill_bwd_workspace(B, T, H, HK, D, &need)) != LA_OK) return st;
   if ((st = la_host::check_workspace(workspace, workspace_bytes, need)) != LA_OK) return st;
   const HeadsArg a[] = {rows(q, ldq, hsq, tokens, H, D, "q"),       rows(k, ldk, hsk, tokens, HK, D, "k"),
                         rows(v, ldv, hsv, tokens, HK, D, "v"),      rows(o, ldo, hso, tokens, H, D, "o"),
@@ -324,7 +353,13 @@ la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float
   p.q = in(a[0]), p.k = in(a[1]), p.v = in(a[2]), p.o_in = in(a[3]), p.dout = in(a[4]);
   p.dq = out(a[5]), p.dk = out(a[6]), p.dv = out(a[7]);
   p.lse_in = lse;
+  const BwdWorkspace w = bwd_workspace(tokens, H, HK, D);
   p.delta = static_cast<float*>(workspace);
+  p.splits = w.splits;
+  if (w.splits > 1) {
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part);
+    p.marks = static_cast<uint8_t*>(workspace) + w.marks;
+  }
   p.cu_seqlens = cu_seqlens;
   p.dev_error = dev_error;
   p.scale = scale;
@@ -342,9 +377,12 @@ la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float
     cudaError_t ce = la_host::launch_pdl(laa::attn_delta_kernel<kD>, static_cast<unsigned>((delta_threads + laa::kDeltaThreads - 1) / laa::kDeltaThreads),
                                          laa::kDeltaThreads, 0, s, p);
     if (ce == cudaSuccess)
-      ce = la_host::launch_pdl(laa::attn_bwd_kernel<kD, false>, blocks_for(tiles * HK, ds->sms), laa::kBwdThreads, bwd_shared<kD>(), s, maps, p);
+      ce = la_host::launch_pdl(laa::attn_bwd_kernel<kD, false>, blocks_for(tiles * HK * p.splits, ds->sms), laa::kBwdThreads, bwd_shared<kD>(), s, maps, p);
     if (ce == cudaSuccess)
       ce = la_host::launch_pdl(laa::attn_bwd_kernel<kD, true>, blocks_for(tiles * H, ds->sms), laa::kBwdThreads, bwd_shared<kD>(), s, maps, p);
+    if (ce == cudaSuccess && p.splits > 1)
+      ce = la_host::launch_pdl(laa::attn_sum_kernel<kD>, static_cast<unsigned>((delta_threads / (H / HK) + laa::kDeltaThreads - 1) / laa::kDeltaThreads),
+                               laa::kDeltaThreads, 0, s, p);
     return ce;
   }));
 }

@@ -16,7 +16,11 @@
 // Warp 17 loads: a pair of tiles that stays for the item, and rings of three and two tiles for the
 // operands that pass, as long as each is in use.  Warp 18 brings lse and delta of the rows that pass.
 //
-// Bound: the tensor cores.
+// Where a batch has few key/value heads and tiles for the SMs, a group's heads are shared out among
+// several items, whose FP32 sums a last kernel adds in order.
+//
+// Bound: the tensor cores at D = 128 (2 x 8192 tokens, 32 heads of 128 on 4: 2.36 ms, the seven
+// products at 1.63 PFLOP/s); at D = 64 the warpgroups' way from scores to probabilities to dS.
 #pragma once
 
 #include "la_attention_softmax.cuh"
@@ -45,22 +49,24 @@ struct BwdMaps {
 };
 
 // What an item of either kernel walks over: tile n is rows (keys) of tile `first + n % each`, of head
-// `head + n / each`.
+// `head + n / each`; `own` is the head of the item's own tiles.  (dk, dv: items go by key/value head and
+// by part of its group's heads.)
 struct Passes {
-  int first, each, count, head;
+  int first, each, count, head, own;
 };
 template <bool kDq>
 __device__ __forceinline__ Passes passes_of(const PrefillParams& p, const Item& it) {
   const int tiles = (it.len + kTile - 1) / kTile, group = p.H / p.HK;
-  if (kDq) return {0, it.tile + 1, it.tile + 1, it.head / group};
-  return {it.tile, tiles - it.tile, (tiles - it.tile) * group, it.head * group};
+  if (kDq) return {0, it.tile + 1, it.tile + 1, it.head / group, it.head};
+  const int hk = it.head / p.splits, part = it.head - hk * p.splits, most = (group + p.splits - 1) / p.splits;
+  return {it.tile, tiles - it.tile, (tiles - it.tile) * min(most, group - part * most), hk * group + part * most, hk};
 }
 
 template <int D, bool kDq>
 __device__ __forceinline__ void bwd_load(BwdShared<D>& sm, const PrefillParams& p, const BwdMaps& maps, int lane,
                                          volatile int* abort) {
   constexpr uint32_t kBytes = kBox * (D / 64);
-  ItemWalk<!kDq> walk(kTile, kDq ? p.H : p.HK);
+  ItemWalk<!kDq> walk(kTile, kDq ? p.H : p.HK * p.splits);
   const CUtensorMap *own0 = kDq ? &maps.q : &maps.k, *own1 = kDq ? &maps.dout : &maps.v;
   const CUtensorMap *lng = kDq ? &maps.k : &maps.q, *brf = kDq ? &maps.v : &maps.dout;
   uint32_t items = 0, own_loads = 0, longs = 0, briefs = 0;
@@ -99,8 +105,8 @@ __device__ __forceinline__ void bwd_load(BwdShared<D>& sm, const PrefillParams& 
         if (!(ok = warp_wait(&sm.own_empty, (own_loads & 1u) ^ 1u, abort))) break;
         if (lane == 0) {
           lap::mbar_arrive_expect_tx(&sm.own_full, 2 * kBytes);
-          load(own0, sm.own[0], &sm.own_full, it.head, it.lo + it.tile * kTile);
-          load(own1, sm.own[1], &sm.own_full, it.head, it.lo + it.tile * kTile);
+          load(own0, sm.own[0], &sm.own_full, w.own, it.lo + it.tile * kTile);
+          load(own1, sm.own[1], &sm.own_full, w.own, it.lo + it.tile * kTile);
         }
         ++own_loads;
       }
@@ -267,6 +273,21 @@ __device__ __forceinline__ void write_row(uint32_t t, bf16* out, float f, bool l
   }
 }
 
+// The same in FP32.
+template <int D>
+__device__ __forceinline__ void write_part(uint32_t t, float* out, float f, bool live, int from, int to) {
+#pragma unroll 1
+  for (int g = from; g < to; ++g) {
+    float o[32];
+    lap::tmem_ld32(t + 32 * g, o);
+    if (live)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        reinterpret_cast<float4*>(out + 32 * g)[e] =
+            make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+  }
+}
+
 // dk, dv.  A thread has one key and kColumns of a tile's rows.
 template <int D>
 __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int tid,
@@ -366,11 +387,17 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
     lap::tc_fence_after();
     const int64_t at = it.lo + it.tile * kTile + key;
     const bool live = it.tile * kTile + key < it.len;
-    const int g = (part & 1) * (D / 64);
-    if (part < 2)
-      write_row<D>(t_lane + kColDv, p.dv.row(at, it.head), 1.f, live, g, g + D / 64);
-    else
-      write_row<D>(t_lane + kColDv + D, p.dk.row(at, it.head), p.scale, live, g, g + D / 64);
+    const int g = (part & 1) * (D / 64), is_dk = part >> 1;
+    const uint32_t t_sum = t_lane + kColDv + D * is_dk;
+    const float f = is_dk ? p.scale : 1.f;
+    if (p.part == nullptr) {
+      write_row<D>(t_sum, (is_dk ? p.dk : p.dv).row(at, w.own), f, live, g, g + D / 64);
+    } else {
+      const int split = it.head - w.own * p.splits;
+      if (live && split == 0 && part == 0) p.marks[static_cast<int64_t>(w.own) * p.tokens + at] = 1;
+      write_part<D>(t_sum, p.part + (((static_cast<int64_t>(split) * 2 + is_dk) * p.HK + w.own) * p.tokens + at) * D, f, live,
+                    g, g + D / 64);
+    }
     lap::tc_fence_before();
     warp_arrive(&sm.acc_free, lane);
   }
@@ -546,7 +573,38 @@ __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const __grid_
   }
 #pragma unroll
   for (int d = kLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  if (t < p.tokens && c == 0) p.delta[h * static_cast<int64_t>(p.tokens) + t] = sum;
+  if (t < p.tokens && c == 0) {
+    p.delta[h * static_cast<int64_t>(p.tokens) + t] = sum;
+    if (p.part && h < p.HK) p.marks[h * static_cast<int64_t>(p.tokens) + t] = 0;
+  }
+}
+
+// dk and dv from the sums over the parts of their group's heads, in order; 8 columns a thread, rows that
+// belong to a sequence.
+template <int D>
+__global__ void __launch_bounds__(kDeltaThreads) attn_sum_kernel(const __grid_constant__ PrefillParams p) {
+  constexpr int kLanes = D / 8;
+  lap::griddep_wait();
+  lap::griddep_launch_dependents();
+  const int64_t r = (static_cast<int64_t>(blockIdx.x) * kDeltaThreads + threadIdx.x) / kLanes;
+  const int64_t t = r / p.HK;
+  const int hk = static_cast<int>(r - t * p.HK), c = threadIdx.x % kLanes * 8;
+  if (t >= p.tokens || !p.marks[static_cast<int64_t>(hk) * p.tokens + t]) return;
+#pragma unroll
+  for (int is_dk = 0; is_dk < 2; ++is_dk) {
+    float s[8] = {};
+#pragma unroll 4
+    for (int x = 0; x < p.splits; ++x) {
+      const float4* at = reinterpret_cast<const float4*>(
+          p.part + (((static_cast<int64_t>(x) * 2 + is_dk) * p.HK + hk) * p.tokens + t) * D + c);
+      const float4 a = at[0], b = at[1];
+      s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
+      s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+    }
+    *reinterpret_cast<uint4*>((is_dk ? p.dk : p.dv).row(t, hk) + c) =
+        make_uint4(lap::pack_bf16x2(s[0], s[1]), lap::pack_bf16x2(s[2], s[3]), lap::pack_bf16x2(s[4], s[5]),
+                   lap::pack_bf16x2(s[6], s[7]));
+  }
 }
 
 }  // namespace laa

@@ -25,10 +25,12 @@ struct PrefillParams {
   float* lse;           // [H, tokens]
   const float* lse_in;  // gradients
   float* delta;         // [H, tokens] rowsum(dO o), gradients' workspace
+  float* part;          // [splits][dk, dv][HK][tokens][D] sums over parts of a group's heads; null: one part
+  uint8_t* marks;       // [HK, tokens] whether a row has such sums
   const int32_t* cu_seqlens;
   int* dev_error;
   float scale;
-  int tokens, T, N, H, HK, D;
+  int tokens, T, N, H, HK, D, splits;
 };
 
 struct CacheParams {

@@ -181,13 +181,13 @@ def test_allowed_layouts_pass_every_host_check():
 def test_workspace_queries():
     lib = lap.load_library()
     assert lap.la_qk_norm_rope_bwd_workspace(0, 4, 2, 64) == 0 and lap.la_qk_norm_rope_bwd_workspace(100, 4, 2, 64) % 256 == 0
-    assert lap.la_attn_prefill_bwd_workspace(2, 100, 4) >= 3200 and lap.la_attn_verify_workspace(3, 4, 4, 2, 64) % 256 == 0
-    for bad in ((lap.la_qk_norm_rope_bwd_workspace, (1, 4, 2, 100)), (lap.la_attn_prefill_bwd_workspace, (1, -1, 4)),
+    assert lap.la_attn_prefill_bwd_workspace(2, 100, 4, 2, 64) >= 3200 and lap.la_attn_verify_workspace(3, 4, 4, 2, 64) % 256 == 0
+    for bad in ((lap.la_qk_norm_rope_bwd_workspace, (1, 4, 2, 100)), (lap.la_attn_prefill_bwd_workspace, (1, -1, 4, 2, 64)), (lap.la_attn_prefill_bwd_workspace, (1, 1, 4, 3, 64)),
                 (lap.la_attn_verify_workspace, (1, 0, 4, 2, 64)), (lap.la_attn_verify_workspace, (1, 1, 4, 3, 64))):
         with pytest.raises(lap.LaError):
             bad[0](*bad[1])
     assert lib.la_attn_verify_workspace(1, 1, 4, 2, 64, None) == INVALID
-    assert lib.la_attn_prefill_bwd_workspace(1, 1, 4, None) == INVALID
+    assert lib.la_attn_prefill_bwd_workspace(1, 1, 4, 2, 64, None) == INVALID
     assert lib.la_qk_norm_rope_bwd_workspace(1, 4, 2, 64, None) == INVALID
 
 

@@ -227,7 +227,7 @@ def test_captured_and_replayed_with_new_values_and_streams():
         return o, lse, *lap.la_attn_prefill_bwd(q, k, v, 0.1, o, lse, do, seq_len=T, stream=stream, workspace=ws)
     want = step()
     torch.cuda.synchronize()
-    ws = torch.full((lap.la_attn_prefill_bwd_workspace(2, T, H),), 255, dtype=torch.uint8, device="cuda")  # NaN
+    ws = torch.full((lap.la_attn_prefill_bwd_workspace(2, T, H, HK, D),), 255, dtype=torch.uint8, device="cuda")  # NaN
     side = torch.cuda.Stream()
     got = step(side, ws)
     side.synchronize()
@@ -321,3 +321,24 @@ def test_a_value_that_is_not_finite_reaches_only_rows_that_see_it(D):
         k[row], q[row] = keepk, keepq
         assert torch.equal(o[:row], o2[:row]) and torch.equal(lse[:, :row], lse2[:, :row])
         assert torch.isnan(o2[row:]).all() and torch.isnan(lse2[:, row:]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,HK", [(8, 1), (14, 2), (5, 1), (40, 1), (6, 6)])
+def test_groups_of_heads_shared_out(H, HK, D):
+    """Few key/value heads and tiles: a group's heads are summed in parts, on a workspace of NaN."""
+    rng = np.random.default_rng(13)
+    lens = [300, 0, 129, 5]
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    tokens = int(cu[-1]) + 30
+    q, k, v = make(rng, tokens, (H, HK, HK), D, "fused")
+    do, = make(rng, tokens, (H,), D)
+    dcu = torch.from_numpy(cu).cuda()
+    o, lse = lap.la_attn_prefill_fwd(q, k, v, 0.15, cu_seqlens=dcu)
+    ws = torch.full((lap.la_attn_prefill_bwd_workspace(1, tokens, H, HK, D),), 255, dtype=torch.uint8, device="cuda")
+    grads = [torch.full((tokens, n, D), 7.0, dtype=torch.bfloat16, device="cuda") for n in (H, HK, HK)]
+    lap.la_attn_prefill_bwd(q, k, v, 0.15, o, lse, do, cu_seqlens=dcu, dq=grads[0], dk=grads[1], dv=grads[2], workspace=ws)
+    check_backward(q, k, v, 0.15, [(a, b) for a, b in zip(cu, cu[1:]) if b > a], o, lse, do, grads)
+    assert all((g[cu[-1]:] == 7).all() for g in grads)
+    if H > HK:
+        assert ws.numel() > 4 * H * tokens * 2

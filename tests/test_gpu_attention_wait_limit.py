@@ -40,7 +40,7 @@ def test_prompt(short, D):
     lq, lk = (H * D, D), (HK * D, D)
     timed_out(lambda err: short.la_attn_prefill_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), 0.1, None, o.data_ptr(),
                                                     lse.data_ptr(), *lq, *lk, *lk, *lq, B, T, B, H, HK, D, err, s))
-    n = lap.la_attn_prefill_bwd_workspace(B, T, H)
+    n = lap.la_attn_prefill_bwd_workspace(B, T, H, HK, D)
     ws = torch.empty(n, dtype=torch.uint8, device="cuda")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     timed_out(lambda err: short.la_attn_prefill_bwd(
