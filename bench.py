@@ -553,6 +553,8 @@ def run_sweep(args):
         run_segment_sweep(args, device, stream, flush, hbm, hbm_kind, tflops, tf_kind)
     if args.sweep_what in ("all", "gated"):
         run_gated_sweep(args, device, stream, flush, hbm, hbm_kind)
+    if args.sweep_what in ("all", "attention"):
+        run_attention_sweep(args, device, stream, flush, hbm, hbm_kind, tflops, tf_kind)
     if args.sweep_what in ("all", "backward"):
         run_backward_sweep(args, device, stream, flush, hbm, hbm_kind)
 
@@ -735,6 +737,85 @@ def run_gated_sweep(args, device, stream, flush, hbm, hbm_kind):
              lambda: lap.la_rms_norm_fwd_fp8(x, w, 1e-5, residual=res, y=y8, scales=sc, residual_out=s, stream=stream))
         line("rms_norm_bwd", name, 8 * n + 8 * Cn,
              lambda: lap.la_rms_norm_bwd(s, w, 1e-5, y, dres=x, dx=dx, dweight=dw, workspace=ws, stream=stream))
+
+
+def run_attention_sweep(args, device, stream, flush, hbm, hbm_kind, tflops, tf_kind):
+    """Norm and rotation of queries and keys, softmax attention over prompts (and its gradients), drafted
+    tokens over a paged cache and the writes into it, BF16, timed as the other sweeps; the roofline is
+    the bytes that each call has to move once, or its products under the causal mask, whichever is more."""
+    import torch
+
+    import linear_attention_prefill_chunkwise_gb300 as lap
+
+    gen = torch.Generator(device=device).manual_seed(5000)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=gen, device=device).to(torch.bfloat16)
+
+    def line(op, workload, nbytes, flops, fn):
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                fn()
+            times = []
+            for _ in range(args.sweep_steps):
+                flush.fill_(1)
+                e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                e0.record(stream)
+                fn()
+                e1.record(stream)
+                times.append((e0, e1))
+        torch.cuda.synchronize(device)
+        ms = statistics.fmean(a.elapsed_time(b) for a, b in times)
+        t_hbm, t_flop = nbytes / (hbm * 1e9), flops / (tflops * 1e12)
+        roof = max(t_hbm, t_flop) * 1e3
+        print(json.dumps({"sweep": True, "op": op, "workload": workload, "ms": round(ms, 5), "alg_bytes": nbytes,
+                          "alg_flops": flops, "achieved_gbs": round(nbytes / (ms / 1e3) / 1e9, 1),
+                          "achieved_tflops": round(flops / (ms / 1e3) / 1e12, 1), "roofline_ms": round(roof, 5),
+                          "frac": round(roof / ms, 4), "bound": "hbm" if t_hbm >= t_flop else "tensor",
+                          "peaks": {"hbm_gbs": hbm, "hbm_source": hbm_kind, "tflops": tflops, "tflops_source": tf_kind},
+                          "steps": args.sweep_steps, "l2": "flushed between launches (256 MB write)"}), flush=True)
+
+    D = 128
+    w = torch.rand(D, generator=gen, device=device)
+    freq = 10000.0 ** (-torch.arange(0, D, 2, device=device) / D)
+    for tokens, H, HK in ((1024, 64, 8), (16384, 64, 8)):
+        q, k, v, o = rand(tokens, H, D), rand(tokens, HK, D), rand(tokens, HK, D), rand(tokens, H, D)
+        dq, dk, dv, dout = (torch.empty_like(t) for t in (q, k, v, o))
+        dout.copy_(rand(tokens, H, D))
+        pos = torch.arange(tokens, dtype=torch.int32, device=device)
+        n, name = tokens * (H + HK) * D, f"{tokens} tokens, {H} + {HK} heads of {D}"
+        ws = torch.empty(lap.la_qk_norm_rope_bwd_workspace(tokens, H, HK, D), dtype=torch.uint8, device=device)
+        dw = torch.empty(2, D, device=device)
+        line("qk_norm_rope_fwd", name, 4 * n + 4 * tokens, 0,
+             lambda: lap.la_qk_norm_rope_fwd(q, k, w, w, 1e-6, pos, freq, q_out=dq, k_out=dk, stream=stream))
+        line("qk_norm_rope_bwd", name, 6 * n + 4 * tokens, 0,
+             lambda: lap.la_qk_norm_rope_bwd(q, k, w, w, 1e-6, dout, v, pos, freq, dq=dq, dk=dk, dq_weight=dw[0],
+                                             dk_weight=dw[1], workspace=ws, stream=stream))
+        Bn = 2
+        T = tokens // Bn
+        pairs, lse = Bn * H * T * (T + 1) // 2, torch.empty(H, tokens, device=device)
+        name = f"B={Bn} T={T} H={H} HK={HK} D={D}, causal"
+        ws = torch.empty(lap.la_attn_prefill_bwd_workspace(Bn, T, H, HK, D), dtype=torch.uint8, device=device)
+        line("attn_prefill_fwd", name, 2 * (q.numel() + o.numel() + k.numel() + v.numel()) + 4 * lse.numel(),
+             4 * D * pairs, lambda: lap.la_attn_prefill_fwd(q, k, v, D ** -0.5, seq_len=T, o=o, lse=lse, stream=stream))
+        line("attn_prefill_bwd", name, 2 * (4 * q.numel() + 4 * k.numel()) + 4 * lse.numel(), 10 * D * pairs,
+             lambda: lap.la_attn_prefill_bwd(q, k, v, D ** -0.5, o, lse, dout, seq_len=T, dq=dq, dk=dk, dv=dv,
+                                             workspace=ws, stream=stream))
+    del q, k, v, o, dq, dk, dv, dout, lse, ws
+    Bn, H, HK, page, top = 64, 64, 8, 64, 8192
+    table = torch.randperm(Bn * top // page, generator=gen, device=device).int().view(Bn, -1)
+    kc, vc = rand(Bn * top // page, page, HK, D), rand(Bn * top // page, page, HK, D)
+    lens = torch.randint(top // 2, top - 8, (Bn,), generator=gen, device=device, dtype=torch.int32)
+    held = int(lens.sum())
+    for T in (1, 8):
+        q, k, v, o = rand(Bn * T, H, D), rand(Bn * T, HK, D), rand(Bn * T, HK, D), rand(Bn * T, H, D)
+        ws = torch.empty(lap.la_attn_verify_workspace(Bn, T, H, HK, D), dtype=torch.uint8, device=device)
+        name = f"B={Bn} requests x T={T}, {held} cached tokens in pages of {page}, H={H} HK={HK} D={D}"
+        line("attn_verify", name, 4 * (held + Bn * T) * HK * D + 4 * Bn * T * H * D, 4 * D * H * T * (held + Bn * T),
+             lambda: lap.la_attn_verify(q, k, v, D ** -0.5, kc, vc, lens, T, page_table=table, o=o, workspace=ws,
+                                        stream=stream))
+        line("attn_commit", f"B={Bn} requests x T={T} tokens, pages of {page}, HK={HK} D={D}", 8 * Bn * T * HK * D, 0,
+             lambda: lap.la_attn_commit(k, v, kc, vc, lens, T=T, page_table=table, stream=stream))
 
 
 SEGMENT_WORKLOADS = (
@@ -1002,9 +1083,11 @@ def main():
     ap.add_argument("--sweep", action="store_true",
                     help="time every workload (1..5) instead, one JSON line each (not the headline line)")
     ap.add_argument("--sweep-steps", type=int, default=50)
-    ap.add_argument("--sweep-what", choices=["all", "prefill", "decode", "segmented", "gated", "backward"], default="all",
+    ap.add_argument("--sweep-what", choices=["all", "prefill", "decode", "segmented", "gated", "attention", "backward"],
+                    default="all",
                     help="with --sweep: the five prefill workloads, the speculative-decoding ops, the "
-                         "segmented prefill on few-chain batches, the gated recurrence and the norm, or all of them")
+                         "segmented prefill on few-chain batches, the gated recurrence and the norm, the norm and "
+                         "rotation of queries and keys with softmax attention and its cache, or all of them")
     args = ap.parse_args()
     if args.warmup < 3:
         ap.error("--warmup must be >= 3")

@@ -10,10 +10,12 @@
 // turn, in one queue, so that S can overwrite p).  Warp 9 loads: queries once per item, keys and values
 // through a ring.  The two tiles share keys and values, which halves their traffic from L2.
 //
-// Bound: the tensor cores at D = 128 (2 x 8192 tokens, 64 heads of 128 on 8: 1.43 ms, 1.54 PFLOP/s);
-// at D = 64, where the products halve, the softmax.  Measured against it on that case: two threads per
+// Bound: the tensor cores at D = 128 (2 x 8192 tokens, 64 heads of 128 on 8: 1.40 ms, 1.57 PFLOP/s, where
+// the power limit holds the clock; 1.28 ms when cool); at D = 64, where the products halve, the softmax
+// (1229 cycles per tile of scores and SM against 1524).  Measured against it on that case: two threads per
 // row, which meet to agree on a maximum, 1.57 ms; steps of 64 keys with two buffers of scores per tile,
-// whose products read the queries twice as often, 1.53 ms.
+// whose products read the queries twice as often, 1.53 ms; half of p made before the new maximum is
+// known, 1.61 ms.
 #pragma once
 
 #include "la_attention_softmax.cuh"
