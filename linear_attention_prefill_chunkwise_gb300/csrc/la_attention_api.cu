@@ -235,22 +235,26 @@ uint64_t table_bytes(const int32_t* page_table, int B, int table_width, int64_t 
 }
 
 // The gradients' workspace: delta, and, where a group's heads are shared out, the parts' sums and marks.
-// They are shared out where the tiles of all key/value heads are few for the SMs (of the largest part), so
-// that some have none or the busiest has far more than the mean, unless there is little to share.
-// Measured, gradients of one sequence, D = 128, 8 heads on 1: 8192 tokens 332 us (whole groups 766), 4096
-// 108 (363), 300 46 (70), 16384 with 4 heads 587 (872); but 4 x 2048 tokens, 32 heads on 4 (256 items) 425
-// (361), and 128 tokens, 16 heads on 2, 50 (43).
+// Parts: as many as give each SM one item, with two tiles or more each, or two items, with eight or more (by the
+// mean number of tiles that an item walks over, here of eight at least).  N sequences; a query for a packed
+// batch does not know them and takes one, whose parts are not fewer.
+// Measured, gradients, us with whole groups; by the rule (parts; others): one sequence of 8192, 8 heads of 128
+// on 1 764; 307 (4; 8: 322); of 2048, 32 on 8 135; 114 (2; 4: 141); 2 x 512, 64 on 8 79; 68 (2; 8: 102); 512,
+// 64 on 8 67; 47 (4; 8: 56); 16 x 64, 16 on 1 71; 37 (8; 16: 49); 128, 16 of 64 on 2 25; 20 (4; 8: 22);
+// 4 x 2048, 32 on 4 stays whole: 353 (2: 381).
 struct BwdWorkspace {
   int splits;
   size_t part, marks, bytes;
 };
-BwdWorkspace bwd_workspace(int64_t tokens, int H, int HK, int D) {
+BwdWorkspace bwd_workspace(int64_t tokens, int N, int H, int HK, int D) {
   constexpr int64_t kSms = 152;
   const int group = H / HK;
-  const int64_t tiles = (tokens + laa::kTile - 1) / laa::kTile, items = tiles * HK;
+  const int64_t tiles = std::max<int64_t>((tokens + laa::kTile - 1) / laa::kTile, N), items = tiles * HK;
   BwdWorkspace w{1, 0, 0, 0};
-  if (items < kSms + kSms / 4 && group > 1 && tiles * group >= 16) {
-    const int64_t want = std::min<int64_t>(group, (4 * kSms + items - 1) / items);
+  const int64_t walk = (std::max<int64_t>(1, tiles / std::max(N, 1)) + 1) * group / 2;
+  if (tiles > 0 && walk >= 8) {
+    const int64_t one = std::min(kSms / items, walk / 2), two = std::min(2 * kSms / items, walk / 8);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(group, std::max(one, two)));
     const int each = static_cast<int>((group + want - 1) / want);  // heads of a part
     w.splits = (group + each - 1) / each;
   }
@@ -317,7 +321,7 @@ la_status la_attn_prefill_bwd_workspace(int B, int T, int H, int HK, int D, size
   if (st != LA_OK) return st;
   if (B < 0 || T < 0) return fail(LA_ERR_INVALID_ARGUMENT, "B and T must be >= 0 (got %d, %d)", B, T);
   if (static_cast<int64_t>(B) * T > kMostTokens) return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)B * T);
-  *bytes = bwd_workspace(static_cast<int64_t>(B) * T, H, HK, D).bytes;
+  *bytes = bwd_workspace(static_cast<int64_t>(B) * T, B, H, HK, D).bytes;
   return LA_OK;
 }
 
@@ -353,7 +357,7 @@ la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float
   p.q = in(a[0]), p.k = in(a[1]), p.v = in(a[2]), p.o_in = in(a[3]), p.dout = in(a[4]);
   p.dq = out(a[5]), p.dk = out(a[6]), p.dv = out(a[7]);
   p.lse_in = lse;
-  const BwdWorkspace w = bwd_workspace(tokens, H, HK, D);
+  const BwdWorkspace w = bwd_workspace(tokens, N, H, HK, D);
   p.delta = static_cast<float*>(workspace);
   p.splits = w.splits;
   if (w.splits > 1) {
