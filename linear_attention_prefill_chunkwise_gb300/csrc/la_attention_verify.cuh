@@ -368,11 +368,11 @@ __device__ __forceinline__ void verify_softmax(VerifyShared<D>& sm, const CacheP
         // (the scores prove that the ring slot's last contents have been used: its phase is this one)
         const uint32_t xs = slots + 2 * j + 1;
         if (!warp_wait(&sm.kv_full[xs % kStages], (xs / kStages) & 1u, abort)) return;
-        const bool behind = row >= valid;
-        const bool found = (d >= 0 || behind) && clean_row<D>(sm.kv[xs % kStages], row, behind);
+        const bool behind = row >= valid, masked = d >= drafts - 2 && d >= 0;
+        const bool found = (masked || behind) && clean_row<D>(sm.kv[xs % kStages], row, behind);
         const uint32_t bad = __ballot_sync(0xFFFFFFFFu, found);
         // (drafted tiles before the last two are seen whole, by every row)
-        if (d >= 0 && drafts - 1 - d < 2 && lane == 0) sm.bad[i & 1][drafts - 1 - d][warp] = bad;
+        if (masked && lane == 0) sm.bad[i & 1][drafts - 1 - d][warp] = bad;
         lap::fence_proxy_async_smem();
       }
       if (busy) {

@@ -174,6 +174,25 @@ def test_non_finite_drafts_reach_only_rows_that_see_them(D):
         assert not torch.isfinite(got[5]).all() and not torch.isfinite(got[T + 3]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_non_finite_values_of_many_drafted_tokens(D):
+    """Values that are not finite reach every later drafted token, also from the tiles of drafted tokens
+    that a query tile sees whole, and no earlier one."""
+    rng = np.random.default_rng(31)
+    T, H, HK, n = 420, 8, 1, 70
+    ks, vs, kc, vc, table = make_cache(rng, [n], HK, D, 16, "dense")
+    q, k, v = bf(rng, T, H, D), bf(rng, T, HK, D), bf(rng, T, HK, D)
+    v[5, 0, 3], v[131, 0, 40], v[300, 0, 7], v[419, 0, 0] = float("inf"), float("nan"), float("-inf"), float("inf")
+    o = lap.la_attn_verify(q, k, v, 0.15, kc, vc, torch.tensor([n], dtype=torch.int32, device="cuda"), T, page_table=table)
+    o = f64(o)
+    for t, d, want in ((5, 3, np.inf), (131, 40, np.nan), (300, 7, -np.inf), (419, 0, np.inf)):
+        assert np.isfinite(o[:t, :, d]).all()
+        assert np.array_equal(o[t:, :, d], np.full((T - t, H), want), equal_nan=True)
+    rest = np.ones(D, bool)
+    rest[[3, 40, 7, 0]] = False
+    assert np.isfinite(o[:, :, rest]).all()
+
+
 def test_bad_lengths_and_pages_skip_their_request():
     rng = np.random.default_rng(12)
     D, T, H, HK, lens = 64, 2, 2, 1, [100, 60, 200, 30]
