@@ -111,9 +111,9 @@ la_status launched(cudaError_t ce) {
 bool same(const HeadsArg& a, const HeadsArg& b) { return a.p == b.p && a.ld == b.ld && a.hs == b.hs; }
 
 la_status check_tables(const int32_t* positions, const float* inv_freq, const float* wq, const float* wk, float eps,
-                       int R) {
+                       int tokens, int R) {
   if (!(eps >= 0.f)) return fail(LA_ERR_INVALID_ARGUMENT, "eps must be >= 0");
-  if (R > 0 && (!positions || !inv_freq))
+  if (R > 0 && ((tokens > 0 && !positions) || !inv_freq))
     return fail(LA_ERR_INVALID_ARGUMENT, "positions and inv_freq must be non-null with R > 0");
   if (!la_host::aligned4(positions) || !la_host::aligned4(inv_freq) || !la_host::aligned4(wq) || !la_host::aligned4(wk))
     return fail(LA_ERR_INVALID_ARGUMENT, "positions, inv_freq and the weights must be 4-byte aligned");
@@ -137,7 +137,7 @@ la_status la_qk_norm_rope_fwd(const void* q, const void* k, const float* q_weigh
   la_host::g_last_error[0] = '\0';
   la_status st = check_sizes(tokens, H, HK, D, R, dtype);
   if (st != LA_OK) return st;
-  if ((st = check_tables(positions, inv_freq, q_weight, k_weight, eps, R)) != LA_OK) return st;
+  if ((st = check_tables(positions, inv_freq, q_weight, k_weight, eps, tokens, R)) != LA_OK) return st;
   if (tokens == 0) return LA_OK;
   if (!q || !k || !q_out || !k_out) return fail(LA_ERR_INVALID_ARGUMENT, "q, k, q_out and k_out must be non-null");
   const uint64_t es = la_host::element_size(dtype);
@@ -211,7 +211,7 @@ la_status la_qk_norm_rope_bwd(const void* q, const void* k, const float* q_weigh
   la_host::g_last_error[0] = '\0';
   la_status st = check_sizes(tokens, H, HK, D, R, dtype);
   if (st != LA_OK) return st;
-  if ((st = check_tables(positions, inv_freq, q_weight, k_weight, eps, R)) != LA_OK) return st;
+  if ((st = check_tables(positions, inv_freq, q_weight, k_weight, eps, tokens, R)) != LA_OK) return st;
   if (tokens > 0 && (!q || !k || !dq_out || !dk_out || !dq || !dk))
     return fail(LA_ERR_INVALID_ARGUMENT, "q, k, dq_out, dk_out, dq and dk must be non-null");
   if (!la_host::aligned4(dq_weight) || !la_host::aligned4(dk_weight))

@@ -153,6 +153,12 @@ def test_nothing_to_do():
     assert commit(T=0) == OK and rope_back(tokens=0, dwq=None, dwk=None, ws=None, wsb=0) == OK
 
 
+def test_no_tokens_have_no_positions():
+    """An empty tensor's pointer is null."""
+    assert rope(tokens=0, pos=None) == rope_back(tokens=0, pos=None, dwq=None, dwk=None) == OK
+    assert rope(tokens=0, freq=None) == rope(tokens=1, pos=None) == rope_back(tokens=1, pos=None) == INVALID
+
+
 def test_allowed_layouts_pass_every_host_check():
     torch = pytest.importorskip("torch")
     if torch.cuda.is_available():
