@@ -1186,6 +1186,8 @@ def _cache(k_cache, v_cache, HK, D, cache_lens, page_table, B, dev):
         if page_table.get_device() != dev:
             raise ValueError(f"page_table must be on cuda:{dev}, got {page_table.device}")
         width, (ld, one) = page_table.shape[1], page_table.stride()
+        if width < 1:  # (its pointer is null, which would mean no table)
+            raise ValueError("page_table must have at least one column")
         if one != 1 and width > 1:
             raise ValueError("the rows of page_table must be contiguous")
         ptrs.append(page_table.data_ptr())

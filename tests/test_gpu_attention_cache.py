@@ -384,6 +384,18 @@ def test_captured_and_replayed_as_the_cache_grows():
         assert torch.equal(o, got[i])
 
 
+def test_a_page_table_without_columns_is_refused():
+    """Its pointer is null, which is not to mean that requests have whole pages."""
+    q = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    kc, vc = (torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lens, table = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros((4, 0), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="column"):
+        lap.la_attn_verify(q, q, q, 1.0, kc, vc, lens, 1, page_table=table)
+    with pytest.raises(ValueError, match="column"):
+        lap.la_attn_commit(q, q, kc, vc, lens, T=1, page_table=table)
+    assert not kc.any() and not vc.any()
+
+
 def test_wrong_arguments_are_refused():
     q = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device="cuda")
     kc = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
