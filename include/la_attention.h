@@ -54,7 +54,8 @@ la_status la_attn_prefill_bwd_workspace(int B, int T, int H, int HK, int D, size
 /*
  * la_attn_prefill_bwd -- gradients of la_attn_prefill_fwd for q, k, v, given its o and lse and
  * dout = dL/do.  dk and dv sum over the H / HK query heads that share them, in FP32, before one
- * rounding.  workspace: 256-byte aligned.
+ * rounding.  A value that is not finite may reach any gradient of its own sequence.  workspace: 256-byte
+ * aligned.
  */
 la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float scale, const void* o,
                               const float* lse, const void* dout, const int32_t* cu_seqlens, void* dq, void* dk,
@@ -86,7 +87,7 @@ la_status la_attn_verify_workspace(int B, int T, int H, int HK, int D, size_t* b
  * [B*T, H, D] and the drafted tokens' own k, v [B*T, HK, D] are token-major by request; the cache
  * is left untouched.  A drafted token sees the request's whole cache and, of the drafted tokens,
  * those whose bits are set in mask[b][t] (int64 [B, T], nullable; bit u = drafted token u; T <= 64;
- * bits from T on are ignored); without a mask it sees drafted tokens 0 .. t (any T).
+ * bits from T on are ignored); without a mask it sees drafted tokens 0 .. t (T <= 262144).
  * workspace: 256-byte aligned.  H / HK <= 128.
  */
 la_status la_attn_verify(const void* q, const void* k, const void* v, float scale, const void* k_cache,

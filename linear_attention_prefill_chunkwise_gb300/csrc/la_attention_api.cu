@@ -58,6 +58,7 @@ la_status launched(cudaError_t ce) {
   return ce == cudaSuccess ? LA_OK : fail(LA_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(ce));
 }
 
+constexpr int kMostDrafts = 1 << 18;  // drafted tokens of a request: their tiles, of all query tiles, stay within int32
 constexpr int64_t kMostTokens = INT32_MAX - 1024;  // row numbers and tile ends stay within int32
 
 HeadsArg rows(const void* p, int64_t ld, int64_t hs, int64_t tokens, int heads, int D, const char* name) {
@@ -398,6 +399,7 @@ la_status la_attn_verify_workspace(int B, int T, int H, int HK, int D, size_t* b
   if (st != LA_OK) return st;
   if (B < 0 || T < 1) return fail(LA_ERR_INVALID_ARGUMENT, "B must be >= 0 and T >= 1 (got %d, %d)", B, T);
   if (H / HK > laa::kTile) return fail(LA_ERR_UNSUPPORTED, "H / HK up to %d is implemented (got %d)", laa::kTile, H / HK);
+  if (T > kMostDrafts) return fail(LA_ERR_UNSUPPORTED, "T up to %d is implemented (got %d)", kMostDrafts, T);
   *bytes = la_host::align256(laa::verify_part_bytes(verify_shape(T, H, HK, false, 16, false).rows, D));
   return LA_OK;
 }
@@ -416,7 +418,8 @@ la_status la_attn_verify(const void* q, const void* k, const void* v, float scal
   if ((st = check_pages(cache_lens, page_table, B, T, HK, pages, page_size, table_width, ld_table)) != LA_OK) return st;
   if (T < 1) return fail(LA_ERR_INVALID_ARGUMENT, "T must be >= 1 (got %d)", T);
   if (mask && T > 64) return fail(LA_ERR_UNSUPPORTED, "a mask has at most 64 tokens (got %d)", T);
-  if (H / HK > 128) return fail(LA_ERR_UNSUPPORTED, "H / HK up to 128 is implemented (got %d)", H / HK);
+  if (H / HK > laa::kTile) return fail(LA_ERR_UNSUPPORTED, "H / HK up to %d is implemented (got %d)", laa::kTile, H / HK);
+  if (T > kMostDrafts) return fail(LA_ERR_UNSUPPORTED, "T up to %d is implemented (got %d)", kMostDrafts, T);
   const int64_t tokens = static_cast<int64_t>(B) * T;
   if (tokens > kMostTokens) return fail(LA_ERR_UNSUPPORTED, "B*T too large (%lld)", (long long)tokens);
   if (B == 0) return LA_OK;

@@ -184,6 +184,14 @@ def test_allowed_layouts_pass_every_host_check():
     assert rope(R=0, pos=None, freq=None) == rope(wq=None, wk=None) == CUDA
 
 
+def test_drafted_tokens_whose_tiles_pass_32_bits_are_refused():
+    big = dict(B=1, tab=None, pages=1, H=128, HK=1, ldq=128 * 64, ldo=128 * 64, ldk=64, ldv=64, kt=64, vt=64, kp=1024, vp=1024)
+    assert verify(T=(1 << 18) + 1, **big) == UNSUPPORTED
+    assert lap.la_attn_verify_workspace(1, 1 << 18, 128, 1, 64) > 0
+    with pytest.raises(lap.LaError):
+        lap.la_attn_verify_workspace(1, (1 << 18) + 1, 128, 1, 64)
+
+
 def test_workspace_queries():
     lib = lap.load_library()
     assert lap.la_qk_norm_rope_bwd_workspace(0, 4, 2, 64) == 0 and lap.la_qk_norm_rope_bwd_workspace(100, 4, 2, 64) % 256 == 0
