@@ -32,16 +32,32 @@ namespace laa {
 constexpr int kParts = 4, kColumns = kTile / kParts;  // warpgroups of a tile of scores, columns of each
 constexpr int kBwdThreads = kParts * kTile + 128, kBwdItems = 2, kDeltaThreads = 256;
 
+// dk, dv: a thread needs lse and delta of 32 rows per tile, and 512 threads that read them from shared memory
+// keep it busy for 1024 cycles.  Where shared memory has room (D = 64) they go through the products instead: 16
+// columns more of Q (dO) hold -lse / scale (-delta) in three BF16 parts, 24 bits, against ones in K (V).
+// (2 x 4096 tokens, 32 heads of 64 on 8, dk and dv: 266 us without, 258 with.)
+template <int D>
+constexpr bool kFold = D == 64;
+struct FoldedStats {
+  uint8_t stats[2][kBox];  // columns 0 .. 2: -lse log2 e / c, 16 .. 18: -delta of the rows
+  uint8_t ones[kBox];      // 1 in those columns, 0 up to 31
+};
+struct PlainStats {
+  float lse[2][kTile], delta[2][kTile];
+};
+
 template <int D>
 struct alignas(1024) BwdShared {
-  TileMem<D> own[2];    // dk, dv: K, V of the item; dq: Q, dO
-  TileMem<D> long_[3];  // dk, dv: Q;  dq: K     (in use by two products)
-  TileMem<D> brief[2];  // dk, dv: dO; dq: V
-  float lse[2][kTile], delta[2][kTile];  // dk, dv
+  static constexpr uint32_t kLong = D == 64 ? 4 : 3, kBrief = D == 64 ? 3 : 2;  // slots of the rings
+  TileMem<D> own[2];         // dk, dv: K, V of the item; dq: Q, dO
+  TileMem<D> long_[kLong];   // dk, dv: Q;  dq: K     (in use by two products)
+  TileMem<D> brief[kBrief];  // dk, dv: dO; dq: V
+  std::conditional_t<kFold<D>, FoldedStats, PlainStats> st;  // dk, dv
   Item items[kBwdItems];
   uint64_t item_full[kBwdItems], item_empty[kBwdItems];
-  uint64_t own_full, own_empty, long_full[3], long_empty[3], brief_full[2], brief_empty[2], stat_full[2], stat_empty[2];
-  uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready, acc_full, acc_free, final_bar;
+  uint64_t own_full, own_empty, long_full[kLong], long_empty[kLong], brief_full[kBrief], brief_empty[kBrief];
+  uint64_t stat_full[2], stat_empty[2];
+  uint64_t s_full[2], s_free, dp_full, dp_free, p_ready[2], ds_ready, acc_full, acc_free, final_bar;
   uint32_t tmem;
   int abort;
 };
@@ -67,7 +83,7 @@ __device__ __forceinline__ Passes passes_of(const PrefillParams& p, const Item& 
 template <int D, bool kDq>
 __device__ __forceinline__ void bwd_load(BwdShared<D>& sm, const PrefillParams& p, const BwdMaps& maps, int lane,
                                          volatile int* abort) {
-  constexpr uint32_t kBytes = kBox * (D / 64);
+  constexpr uint32_t kBytes = kBox * (D / 64), kLong = BwdShared<D>::kLong, kBrief = BwdShared<D>::kBrief;
   ItemWalk<!kDq> walk(kTile, kDq ? p.H : p.HK * p.splits);
   const CUtensorMap *own0 = kDq ? &maps.q : &maps.k, *own1 = kDq ? &maps.dout : &maps.v;
   const CUtensorMap *lng = kDq ? &maps.k : &maps.q, *brf = kDq ? &maps.v : &maps.dout;
@@ -90,14 +106,14 @@ __device__ __forceinline__ void bwd_load(BwdShared<D>& sm, const PrefillParams& 
     const Passes w = passes_of<kDq>(p, it);
     int head = w.head, tile = w.first;
     for (int n = 0; n < w.count; ++n) {
-      const uint32_t l = longs % 3, b = briefs % 2;
-      if (!(ok = warp_wait(&sm.long_empty[l], ((longs / 3) & 1u) ^ 1u, abort))) break;
+      const uint32_t l = longs % kLong, b = briefs % kBrief;
+      if (!(ok = warp_wait(&sm.long_empty[l], ((longs / kLong) & 1u) ^ 1u, abort))) break;
       if (lane == 0) {
         lap::mbar_arrive_expect_tx(&sm.long_full[l], kBytes);
         load(lng, sm.long_[l], &sm.long_full[l], head, it.lo + tile * kTile);
       }
       ++longs;
-      if (!(ok = warp_wait(&sm.brief_empty[b], ((briefs / 2) & 1u) ^ 1u, abort))) break;
+      if (!(ok = warp_wait(&sm.brief_empty[b], ((briefs / kBrief) & 1u) ^ 1u, abort))) break;
       if (lane == 0) {
         lap::mbar_arrive_expect_tx(&sm.brief_full[b], kBytes);
         load(brf, sm.brief[b], &sm.brief_full[b], head, it.lo + tile * kTile);
@@ -118,16 +134,28 @@ __device__ __forceinline__ void bwd_load(BwdShared<D>& sm, const PrefillParams& 
   // every load has landed before the block's shared memory is given up, also after an abort
   if (lane == 0) {
     if (own_loads) drain(&sm.own_full, (own_loads - 1) & 1u);
-    for (uint32_t i = 0; i < 3 && i < longs; ++i) drain(&sm.long_full[(longs - 1 - i) % 3], ((longs - 1 - i) / 3) & 1u);
-    for (uint32_t i = 0; i < 2 && i < briefs; ++i) drain(&sm.brief_full[(briefs - 1 - i) % 2], ((briefs - 1 - i) / 2) & 1u);
+    for (uint32_t i = 1; i <= kLong && i <= longs; ++i) drain(&sm.long_full[(longs - i) % kLong], ((longs - i) / kLong) & 1u);
+    for (uint32_t i = 1; i <= kBrief && i <= briefs; ++i)
+      drain(&sm.brief_full[(briefs - i) % kBrief], ((briefs - i) / kBrief) & 1u);
   }
   __syncwarp();
 }
+
+// A value as three BF16 parts, the first three of eight elements.
+__device__ __forceinline__ uint4 three_parts(float x) {
+  const float hi = __bfloat162float(__float2bfloat16_rn(x)), rest = x - hi;
+  const float mid = __bfloat162float(__float2bfloat16_rn(rest));
+  return make_uint4(lap::pack_bf16x2(hi, mid), lap::pack_bf16x2(rest - mid, 0.f), 0, 0);
+}
+
+// c, and where it is so small that lse / c may be infinite, a c that changes no score.
+__device__ __forceinline__ float fold_scale(float c) { return fabsf(c) < 1e-30f ? copysignf(1e-30f, c) : c; }
 
 // dk, dv: -lse log2 e and delta of the rows that pass.
 template <int D>
 __device__ __forceinline__ void bwd_stats(BwdShared<D>& sm, const PrefillParams& p, int lane, volatile int* abort) {
   uint32_t tiles = 0;
+  const float per_c = 1.f / fold_scale(p.scale * kLog2e);
   for (uint32_t i = 0;; ++i) {
     const uint32_t is = i % kBwdItems;
     if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) return;
@@ -149,43 +177,77 @@ __device__ __forceinline__ void bwd_stats(BwdShared<D>& sm, const PrefillParams&
       if (!warp_wait(&sm.stat_empty[st], ((tiles >> 1) & 1u) ^ 1u, abort)) return;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        sm.lse[st][32 * e + lane] = lse[e];
-        sm.delta[st][32 * e + lane] = delta[e];
+        const int row = 32 * e + lane;
+        if constexpr (kFold<D>) {
+          uint4* at = reinterpret_cast<uint4*>(sm.st.stats[st] + row * 128);  // 16-byte chunk x lies at x ^ (row % 8)
+          at[row & 7] = three_parts(lse[e] * per_c);
+          at[2 ^ (row & 7)] = three_parts(-delta[e]);
+        } else {
+          sm.st.lse[st][row] = lse[e];
+          sm.st.delta[st][row] = delta[e];
+        }
       }
+      if (kFold<D>) lap::fence_proxy_async_smem();
       warp_arrive(&sm.stat_full[st], lane);
       if (++tile == w.first + w.each) tile = w.first, ++head;
     }
   }
 }
 
-// Tensor memory: S at 0, dP at 128, then dv and dk, or two buffers of dS and dq.
-constexpr int kColDp = kTile, kColDv = 2 * kTile, kColDs = 2 * kTile, kColDq = 3 * kTile;
+// Tensor memory: S at 0, dP behind it, then dv and dk, or two buffers of dS and dq.  For dk and dv at D = 64 there is
+// room for a second S, whose product then need not wait for the last p (258 us to 240).
+template <int D, bool kDq>
+constexpr bool kTwo = !kDq && D == 64;
+template <int D, bool kDq>
+constexpr int kColDp = kTwo<D, kDq> ? 2 * kTile : kTile;
+template <int D>
+constexpr int kColDv = kColDp<D, false> + kTile;
+constexpr int kColDs = 2 * kTile, kColDq = 3 * kTile;
 
 // (Slots and parities are running values, as in the forward kernel.)
 template <int D, bool kDq>
 __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillParams& p, uint32_t tmem, int lane,
                                              volatile int* abort) {
-  constexpr uint32_t kSlot = sizeof(TileMem<D>) >> 4;
-  const uint32_t t_dp = tmem + kColDp, t_dv = tmem + kColDv, t_dk = t_dv + D;
+  constexpr uint32_t kSlot = sizeof(TileMem<D>) >> 4, kLong = BwdShared<D>::kLong, kBrief = BwdShared<D>::kBrief;
+  constexpr bool kFolded = !kDq && kFold<D>, kTwoS = kTwo<D, kDq>;
+  const uint32_t t_dp = tmem + kColDp<D, kDq>, t_dv = tmem + kColDv<D>, t_dk = t_dv + D;
   const uint32_t own0 = desc_rows(sm.own[0]), long_rows = desc_rows(sm.long_[0]), long_columns = desc_columns(sm.long_[0]);
   const uint32_t brief_rows = desc_rows(sm.brief[0]), brief_columns = desc_columns(sm.brief[0]);
-  uint32_t next = 0, next_phase = 0;  // long slot of the next scores
-  uint32_t tiles = 0;                 // whose products have begun; parities of barriers used once a tile
+  constexpr uint32_t kId = lap::idesc_bf16_f32(kTile, kTile, false, false), kStat = kBox >> 4;
+  uint32_t ones = 0, stats = 0;
+  if constexpr (kFolded) ones = desc_rows(sm.st.ones), stats = desc_rows(sm.st.stats[0]);
+  uint32_t next = 0, next_phase = 0, slot = 0;     // long slots: of the next scores, of the tile whose sums are next
+  uint32_t bnext = 0, bnext_phase = 0, bslot = 0;  // brief slots: of the next dP, of the next p^T dO
+  uint32_t tiles = 0;                              // tiles whose sums have begun
   bool ok = true;
-  auto scores = [&](uint32_t slot) {
+  // scores and dP of tile x, in order
+  auto scores = [&](uint32_t x) {
+    if (!warp_wait(&sm.long_full[next], next_phase, abort) ||
+        (kFolded && !warp_wait(&sm.stat_full[x & 1], x >> 1 & 1u, abort)) ||
+        (kDq && !warp_wait(&sm.s_free, (x & 1u) ^ 1u, abort)))
+      return false;
+    const uint32_t t_s = tmem + (kTwoS ? (x & 1) * kTile : 0);
     lap::tc_fence_after();
-    product_rows<D>(tmem, own0, long_rows + slot * kSlot);
-    commit(&sm.s_full);
+    product_rows<D>(t_s, own0, long_rows + next * kSlot);
+    if (kFolded) mma1_rows<kId>(t_s, ones, stats + (x & 1) * kStat);
+    commit(&sm.s_full[kTwoS ? x & 1 : 0]);
+    if (++next == kLong) next = 0, next_phase ^= 1;
+    return true;
   };
-  auto dps = [&](uint32_t slot, bool last) {
+  auto dps = [&](uint32_t x, bool last) {
+    if (!warp_wait(&sm.brief_full[bnext], bnext_phase, abort) || (kDq && !warp_wait(&sm.dp_free, (x & 1u) ^ 1u, abort)))
+      return false;
     lap::tc_fence_after();
-    product_rows<D>(t_dp, own0 + kSlot, brief_rows + slot * kSlot);
+    product_rows<D>(t_dp, own0 + kSlot, brief_rows + bnext * kSlot);
+    if (kFolded) {
+      mma1_rows<kId>(t_dp, ones + 2, stats + (x & 1) * kStat + 2);
+      commit(&sm.stat_empty[x & 1]);
+    }
     commit(&sm.dp_full);
-    if (kDq) commit(&sm.brief_empty[slot]);
+    if (kDq) commit(&sm.brief_empty[bnext]);
     if (last) commit(&sm.own_empty);
-  };
-  auto advance = [&] {
-    if (++next == 3) next = 0, next_phase ^= 1;
+    if (++bnext == kBrief) bnext = 0, bnext_phase ^= 1;
+    return true;
   };
   for (uint32_t i = 0; ok; ++i) {
     const uint32_t is = i % kBwdItems;
@@ -196,26 +258,13 @@ __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillPara
     const int count = passes_of<kDq>(p, it).count;
     if (!(ok = warp_wait(&sm.own_full, i & 1u, abort))) break;
     // the first tile's scores and dP; their columns were read before the last item's last product
-    uint32_t slot = next;  // long slot of the tile whose sums are next
-    if (!(ok = warp_wait(&sm.long_full[next], next_phase, abort)) ||
-        (kDq && !(ok = warp_wait(&sm.s_free, (tiles & 1u) ^ 1u, abort))))
-      break;
-    scores(next);
-    advance();
-    if (!(ok = warp_wait(&sm.brief_full[tiles & 1], tiles >> 1 & 1u, abort)) ||
-        (kDq && !(ok = warp_wait(&sm.dp_free, (tiles & 1u) ^ 1u, abort))))
-      break;
-    dps(tiles & 1, count == 1);
+    if (!(ok = scores(tiles)) || !(ok = dps(tiles, count == 1))) break;
+    if (kTwoS && count > 1 && !(ok = scores(tiles + 1))) break;
     for (int n = 0; n < count; ++n, ++tiles) {
       const bool more = n + 1 < count;
-      const uint32_t parity = tiles & 1, other = parity ^ 1, brief_phase = (tiles + 1) >> 1 & 1u;
+      const uint32_t parity = tiles & 1;
       if (kDq) {
-        if (more) {
-          if (!(ok = warp_wait(&sm.long_full[next], next_phase, abort)) || !(ok = warp_wait(&sm.s_free, parity, abort))) break;
-          scores(next);
-          if (!(ok = warp_wait(&sm.brief_full[other], brief_phase, abort)) || !(ok = warp_wait(&sm.dp_free, parity, abort))) break;
-          dps(other, n + 2 == count);
-        }
+        if (more && (!(ok = scores(tiles + 1)) || !(ok = dps(tiles + 1, n + 2 == count)))) break;
         if (!(ok = warp_wait(&sm.ds_ready, parity, abort))) break;
         if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
         lap::tc_fence_after();
@@ -223,29 +272,22 @@ __device__ __forceinline__ void bwd_products(BwdShared<D>& sm, const PrefillPara
         commit(&sm.long_empty[slot]);
         if (!more) commit(&sm.acc_full);
       } else {
-        if (!(ok = warp_wait(&sm.p_ready, parity, abort))) break;
+        constexpr int kAhead = kTwoS ? 2 : 1;  // tiles that the scores are ahead
+        if (!(ok = warp_wait(&sm.p_ready[kTwoS ? parity : 0], kTwoS ? tiles >> 1 & 1u : parity, abort))) break;
         if (n == 0 && !(ok = warp_wait(&sm.acc_free, (i & 1u) ^ 1u, abort))) break;
         lap::tc_fence_after();
-        product_tmem<D, kColumns>(t_dv, tmem, brief_columns + parity * kSlot, n > 0);
-        commit(&sm.brief_empty[parity]);
-        if (more) {
-          if (!(ok = warp_wait(&sm.long_full[next], next_phase, abort))) break;
-          scores(next);
-        }
+        product_tmem<D, kColumns>(t_dv, tmem + (kTwoS ? parity * kTile : 0), brief_columns + bslot * kSlot, n > 0);
+        commit(&sm.brief_empty[bslot]);
+        if (++bslot == kBrief) bslot = 0;
+        if (n + kAhead < count && !(ok = scores(tiles + kAhead))) break;
         if (!(ok = warp_wait(&sm.ds_ready, parity, abort))) break;
         lap::tc_fence_after();
         product_tmem<D, kColumns>(t_dk, t_dp, long_columns + slot * kSlot, n > 0);
         commit(&sm.long_empty[slot]);
         if (!more) commit(&sm.acc_full);
-        if (more) {
-          if (!(ok = warp_wait(&sm.brief_full[other], brief_phase, abort))) break;
-          dps(other, n + 2 == count);
-        }
+        if (more && !(ok = dps(tiles + 1, n + 2 == count))) break;
       }
-      if (more) {
-        slot = next;
-        advance();
-      }
+      if (++slot == kLong) slot = 0;
     }
   }
   commit(&sm.final_bar);
@@ -296,10 +338,11 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
                                          volatile int* abort) {
   const int part = tid / kTile, key = tid % kTile, lane = tid % 32;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(key & ~31) << 16);
-  const uint32_t t_s = t_lane + kColumns * part, t_dp = t_lane + kColDp + kColumns * part;
-  const float c = p.scale * kLog2e;
+  constexpr bool kTwoS = kTwo<D, false>;
+  const uint32_t t_s0 = t_lane + kColumns * part, t_dp = t_s0 + kColDp<D, false>;
+  const float c = kFold<D> ? fold_scale(p.scale * kLog2e) : p.scale * kLog2e;
   const uint64_t c2 = lap::f2_pack(c, c);
-  uint32_t tiles = 0, slot = 0;  // slot: tiles % 3
+  uint32_t tiles = 0, slot = 0, bslot = 0;  // slots of the rings
   for (uint32_t i = 0;; ++i) {
     const uint32_t is = i % kBwdItems;
     if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) return;
@@ -309,14 +352,14 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
     const Passes w = passes_of<false>(p, it);
     int tile = w.first;
     for (int n = 0; n < w.count; ++n, ++tiles) {
-      const uint32_t st = tiles & 1;
+      const uint32_t st = tiles & 1, t_s = t_s0 + (kTwoS ? st * kTile : 0);
       const int valid = it.len - tile * kTile;
-      if (!warp_wait(&sm.stat_full[st], (tiles >> 1) & 1u, abort)) return;  // there long before the scores
-      if (!warp_wait(&sm.s_full, tiles & 1u, abort)) return;
+      if (!kFold<D> && !warp_wait(&sm.stat_full[st], (tiles >> 1) & 1u, abort)) return;  // there long before the scores
+      if (!warp_wait(&sm.s_full[kTwoS ? st : 0], kTwoS ? tiles >> 1 & 1u : st, abort)) return;
       if (valid < kTile) {
         // rows behind the sequence must not enter the sums over rows (0 * inf is NaN)
         if (!warp_wait(&sm.dp_full, tiles & 1u, abort)) return;
-        if (key >= valid) clear_row<D>(part < 2 ? sm.long_[slot] : sm.brief[tiles & 1], part & 1, key);
+        if (key >= valid) clear_row<D>(part < 2 ? sm.long_[slot] : sm.brief[bslot], part & 1, key);
         lap::fence_proxy_async_smem();
       }
       // this thread's rows [from, to) see the key
@@ -325,16 +368,24 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
       lap::tc_fence_after();
       float s[kColumns];
       lap::tmem_ld32(t_s, s);
-      const float4* lse = reinterpret_cast<const float4*>(sm.lse[st] + kColumns * part);
-      const float4* delta = reinterpret_cast<const float4*>(sm.delta[st] + kColumns * part);
+      const float4 *lse = nullptr, *delta = nullptr;
+      if constexpr (!kFold<D>) {
+        lse = reinterpret_cast<const float4*>(sm.st.lse[st] + kColumns * part);
+        delta = reinterpret_cast<const float4*>(sm.st.delta[st] + kColumns * part);
+      }
       auto weights = [&](auto has_mask) {
         constexpr bool kMasked = decltype(has_mask)::value;
         uint32_t u[kColumns / 2];
 #pragma unroll
         for (int k = 0; k < kColumns; k += 4) {
-          const float4 l = lse[k / 4];  // minus lse log2 e
-          const float2 z0 = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k], s[k + 1]), c2, lap::f2_pack(l.x, l.y)));
-          const float2 z1 = lap::f2_unpack(lap::f2_fma(lap::f2_pack(s[k + 2], s[k + 3]), c2, lap::f2_pack(l.z, l.w)));
+          uint64_t z01 = lap::f2_pack(s[k], s[k + 1]), z23 = lap::f2_pack(s[k + 2], s[k + 3]);
+          if constexpr (kFold<D>) {
+            z01 = lap::f2_mul(z01, c2), z23 = lap::f2_mul(z23, c2);
+          } else {
+            const float4 l = lse[k / 4];  // minus lse log2 e
+            z01 = lap::f2_fma(z01, c2, lap::f2_pack(l.x, l.y)), z23 = lap::f2_fma(z23, c2, lap::f2_pack(l.z, l.w));
+          }
+          const float2 z0 = lap::f2_unpack(z01), z1 = lap::f2_unpack(z23);
           s[k] = lap::exp2_approx(z0.x), s[k + 1] = lap::exp2_approx(z0.y);
           s[k + 2] = lap::exp2_approx(z1.x), s[k + 3] = lap::exp2_approx(z1.y);
           if (kMasked)
@@ -348,7 +399,7 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
       if (masked) weights(std::true_type{}); else weights(std::false_type{});
       lap::tmem_wait_st();
       lap::tc_fence_before();
-      warp_arrive(&sm.p_ready, lane);
+      warp_arrive(&sm.p_ready[kTwoS ? st : 0], lane);
       if (!warp_wait(&sm.dp_full, tiles & 1u, abort)) return;
       lap::tc_fence_after();
       float dp[kColumns];
@@ -358,11 +409,13 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
         uint32_t u[kColumns / 2];
 #pragma unroll
         for (int k = 0; k < kColumns; k += 4) {
-          const float4 d = delta[k / 4];
-          float2 a = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k], s[k + 1]),
-                                                lap::f2_sub(lap::f2_pack(dp[k], dp[k + 1]), lap::f2_pack(d.x, d.y))));
-          float2 b = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k + 2], s[k + 3]),
-                                                lap::f2_sub(lap::f2_pack(dp[k + 2], dp[k + 3]), lap::f2_pack(d.z, d.w))));
+          uint64_t d01 = lap::f2_pack(dp[k], dp[k + 1]), d23 = lap::f2_pack(dp[k + 2], dp[k + 3]);
+          if constexpr (!kFold<D>) {
+            const float4 d = delta[k / 4];
+            d01 = lap::f2_sub(d01, lap::f2_pack(d.x, d.y)), d23 = lap::f2_sub(d23, lap::f2_pack(d.z, d.w));
+          }
+          float2 a = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k], s[k + 1]), d01));
+          float2 b = lap::f2_unpack(lap::f2_mul(lap::f2_pack(s[k + 2], s[k + 3]), d23));
           if (kMasked) {
             a.x = k >= from && k < to ? a.x : 0.f;
             a.y = k + 1 >= from && k + 1 < to ? a.y : 0.f;
@@ -380,17 +433,18 @@ __device__ __forceinline__ void bwd_dkdv(BwdShared<D>& sm, const PrefillParams& 
       __syncwarp();
       if (lane == 0) {
         lap::mbar_arrive(&sm.ds_ready);
-        lap::mbar_arrive(&sm.stat_empty[st]);
+        if (!kFold<D>) lap::mbar_arrive(&sm.stat_empty[st]);
       }
       if (++tile == w.first + w.each) tile = w.first;
-      if (++slot == 3) slot = 0;
+      if (++slot == BwdShared<D>::kLong) slot = 0;
+      if (++bslot == BwdShared<D>::kBrief) bslot = 0;
     }
     if (!warp_wait(&sm.acc_full, i & 1u, abort)) return;
     lap::tc_fence_after();
     const int64_t at = it.lo + it.tile * kTile + key;
     const bool live = it.tile * kTile + key < it.len;
     const int g = (part & 1) * (D / 64), is_dk = part >> 1;
-    const uint32_t t_sum = t_lane + kColDv + D * is_dk;
+    const uint32_t t_sum = t_lane + kColDv<D> + D * is_dk;
     const float f = is_dk ? p.scale : 1.f;
     if (p.part == nullptr) {
       write_row<D>(t_sum, (is_dk ? p.dk : p.dv).row(at, w.own), f, live, g, g + D / 64);
@@ -411,10 +465,10 @@ __device__ __forceinline__ void bwd_dq(BwdShared<D>& sm, const PrefillParams& p,
                                        volatile int* abort) {
   const int part = tid / kTile, row = tid % kTile, lane = tid % 32;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(row & ~31) << 16);
-  const uint32_t t_s = t_lane + kColumns * part, t_dp = t_lane + kColDp + kColumns * part;
+  const uint32_t t_s = t_lane + kColumns * part, t_dp = t_lane + kColDp<D, true> + kColumns * part;
   const float c = p.scale * kLog2e;
   const uint64_t c2 = lap::f2_pack(c, c);
-  uint32_t tiles = 0, slot = 0;  // slot: tiles % 3
+  uint32_t tiles = 0, slot = 0;  // slot of the long ring
   for (uint32_t i = 0;; ++i) {
     const uint32_t is = i % kBwdItems;
     if (!warp_wait(&sm.item_full[is], (i / kBwdItems) & 1u, abort)) return;
@@ -428,7 +482,7 @@ __device__ __forceinline__ void bwd_dq(BwdShared<D>& sm, const PrefillParams& p,
     for (int n = 0; n <= it.tile; ++n, ++tiles) {
       const bool masked = n == it.tile;
       const int keep = row + 1 - kColumns * part;  // of this thread's keys, on the diagonal
-      if (!warp_wait(&sm.s_full, tiles & 1u, abort)) return;
+      if (!warp_wait(&sm.s_full[0], tiles & 1u, abort)) return;
       if (masked && it.len < (it.tile + 1) * kTile) {
         // keys behind the sequence must not enter the sum over keys (0 * inf is NaN)
         if (it.tile * kTile + row >= it.len && part < 2) clear_row<D>(sm.long_[slot], part, row);
@@ -468,7 +522,7 @@ __device__ __forceinline__ void bwd_dq(BwdShared<D>& sm, const PrefillParams& p,
       lap::tmem_wait_st();
       lap::tc_fence_before();
       warp_arrive(&sm.ds_ready, lane);
-      if (++slot == 3) slot = 0;
+      if (++slot == BwdShared<D>::kLong) slot = 0;
     }
     if (!warp_wait(&sm.acc_full, i & 1u, abort)) return;
     lap::tc_fence_after();
@@ -502,21 +556,23 @@ attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Pr
     }
     lap::mbar_init(&sm.own_full, 1);
     lap::mbar_init(&sm.own_empty, 1);
-    for (int i = 0; i < 3; ++i) {
+    for (uint32_t i = 0; i < BwdShared<D>::kLong; ++i) {
       lap::mbar_init(&sm.long_full[i], 1);
       lap::mbar_init(&sm.long_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < BwdShared<D>::kBrief; ++i) {
       lap::mbar_init(&sm.brief_full[i], 1);
       lap::mbar_init(&sm.brief_empty[i], 1);
-      lap::mbar_init(&sm.stat_full[i], 1);
-      lap::mbar_init(&sm.stat_empty[i], 16);
     }
-    lap::mbar_init(&sm.s_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      lap::mbar_init(&sm.stat_full[i], 1);
+      lap::mbar_init(&sm.stat_empty[i], kFold<D> ? 1 : 16);
+      lap::mbar_init(&sm.s_full[i], 1);
+      lap::mbar_init(&sm.p_ready[i], 16);
+    }
     lap::mbar_init(&sm.s_free, 16);
     lap::mbar_init(&sm.dp_full, 1);
     lap::mbar_init(&sm.dp_free, 16);
-    lap::mbar_init(&sm.p_ready, 16);
     lap::mbar_init(&sm.ds_ready, 16);
     lap::mbar_init(&sm.acc_full, 1);
     lap::mbar_init(&sm.acc_free, 16);
@@ -527,6 +583,16 @@ attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Pr
     lap::tma_prefetch_desc(&maps.k);
     lap::tma_prefetch_desc(&maps.v);
     lap::tma_prefetch_desc(&maps.dout);
+  }
+  if constexpr (!kDq && kFold<D>) {
+    for (int x = tid; x < kTile * 8; x += kBwdThreads) {
+      const int row = x / 8, chunk = x % 8;
+      const uint32_t one = 0x3F80u;
+      reinterpret_cast<uint4*>(sm.st.ones + row * 128)[chunk ^ (row & 7)] =
+          chunk == 0 || chunk == 2 ? make_uint4(one | one << 16, one, 0, 0) : make_uint4(0, 0, 0, 0);
+      for (int s = 0; s < 2; ++s) reinterpret_cast<uint4*>(sm.st.stats[s] + row * 128)[chunk ^ (row & 7)] = make_uint4(0, 0, 0, 0);
+    }
+    lap::fence_proxy_async_smem();
   }
   lap::tc_fence_before();
   __syncthreads();

@@ -52,6 +52,17 @@ __device__ __forceinline__ void mma4_rows(uint32_t d, uint32_t a, uint32_t b, ui
       "r"(a), "r"(b), "r"(kDescHigh), "r"(kIdesc), "r"(accumulate)
       : "memory");
 }
+// One instruction of d += a b^T, 16 columns of two tiles.
+template <uint32_t kIdesc>
+__device__ __forceinline__ void mma1_rows(uint32_t d, uint32_t a, uint32_t b) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b64 s, t;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "mov.b64 s, {%1, %3};\n\tmov.b64 t, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], s, t, %4, 1;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHigh), "r"(kIdesc)
+      : "memory");
+}
 // Four instructions of d (+)= a b with 64 summed elements of a in tensor memory (8 columns for each
 // instruction, the second two kGap columns behind the first) and 64 rows of b (16 rows, 2048 bytes, each).
 template <uint32_t kIdesc, uint32_t kGap = 16>
