@@ -11,18 +11,23 @@
 //   dq: a block owns 128 rows and walks over the keys that they see: Q K^T, dO V^T, then dS K.
 // Four warpgroups share each tile of scores, 32 columns each (a thread has one row).  Warp 16 issues the
 // products in an order that leaves a product or two to run whenever the warpgroups work:
-//   dk, dv:  p^T dO (n), S (n + 1), dS^T Q (n), dP (n + 1)
+//   dk, dv:  p^T dO (n), S (n + 1; D = 64: n + 2), dS^T Q (n), dP (n + 1)
 //   dq:      S (n + 1), dP (n + 1), dS K (n)
-// Warp 17 loads: a pair of tiles that stays for the item, and rings of three and two tiles for the
-// operands that pass, as long as each is in use.  Warp 18 brings lse and delta of the rows that pass.
+// Warp 17 loads: a pair of tiles that stays for the item, and rings for the operands that pass, as long as
+// each is in use.  Warp 18 brings lse and delta of the rows that pass (dk, dv).
 //
 // Where a batch has few key/value heads and tiles for the SMs, a group's heads are shared out among
 // several items, whose FP32 sums a last kernel adds in order.
 //
 // Bound: the tensor cores at D = 128 (2 x 8192 tokens, 32 heads of 128 on 4: 2.48 ms in a row, the seven
 // products at 1.55 PFLOP/s under the power limit; 2.19 ms when cool); at D = 64 the warpgroups' way from
-// scores to probabilities to dS (24 packed sequences of up to 2047 tokens, 16 heads: 0.48 ms; 2330 cycles
-// per tile of scores and SM for dk and dv, 1474 for dq, of which the products take 1024 and 768).
+// scores to probabilities to dS (24 packed sequences of up to 2047 tokens, 16 heads: 0.45 ms; 2100 cycles
+// per tile of scores and SM for dk and dv, 1474 for dq, of which the products take 1152 and 768 and the
+// warps' instructions 800: what is left is the latency of barriers and tensor memory, which all warps meet
+// at the same time).  There, two teams of eight warps with 64 columns a thread, a tile each in turn, were no
+// faster: tensor memory has room for one dP, which each team holds for most of its tile (dk, dv 235 us
+// against 240 for 2 x 4096 tokens of 32 heads on 8; dq 245 against 202); neither was taking scores and dP out of
+// tensor memory before the last stores there are done (319 against 266).
 #pragma once
 
 #include "la_attention_softmax.cuh"

@@ -279,6 +279,10 @@ attn_fwd_kernel(const __grid_constant__ FwdMaps maps, const __grid_constant__ Pr
   volatile int* abort = &sm.abort;
   lap::griddep_wait();
   lap::griddep_launch_dependents();
+  if (lap::smem_u32(smem_tiles) & 1023u) {  // swizzled tiles would land elsewhere: leave at once
+    if (tid == 0 && p.dev_error) atomicOr(p.dev_error, kErrTimeout);
+    return;
+  }
   if (warp == 8) {
     lap::tmem_alloc(&sm.tmem, 512);
     lap::tmem_relinquish();

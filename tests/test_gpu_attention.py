@@ -324,6 +324,18 @@ def test_a_value_that_is_not_finite_reaches_only_rows_that_see_it(D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale", [1e-38, -1e-33, 1e-12])
+def test_tiny_scales(scale, D):
+    """Scores that are all but equal: lse stands far beyond them, in units of the scale."""
+    rng = np.random.default_rng(41)
+    q, k, v = make(rng, 200, (4, 2, 2), D)
+    o, lse = lap.la_attn_prefill_fwd(q, k, v, scale, seq_len=200)
+    check_forward(q, k, v, scale, [(0, 200)], o, lse)
+    do, = make(rng, 200, (4,), D)
+    check_backward(q, k, v, scale, [(0, 200)], o, lse, do, lap.la_attn_prefill_bwd(q, k, v, scale, o, lse, do, seq_len=200))
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("H,HK", [(8, 1), (14, 2), (5, 1), (40, 1), (6, 6)])
 def test_groups_of_heads_shared_out(H, HK, D):
     """Few key/value heads and tiles: a group's heads are summed in parts, on a workspace of NaN."""
