@@ -579,7 +579,9 @@ def _array(t, name, dtype, shape, dev):
     if t is None:
         return None
     try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        have = t.shape
+        if (t.dtype is dtype and (have == shape or (shape == (None,) and len(have) == 1)) and t.get_device() == dev
+                and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
         pass
@@ -1148,35 +1150,38 @@ def la_attn_prefill_bwd(q, k, v, scale, o, lse, dout, cu_seqlens=None, seq_len=N
     return dq, dk, dv
 
 
+def _pages(t, name, HK, D, dev):
+    """(strides between pages, tokens and heads, shape) of a checked half of a cache."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    have = t.shape
+    if len(have) != 4 or have[2] != HK or have[3] != D:
+        raise ValueError(f"{name} must have shape [pages, page_size, {HK}, {D}], got {tuple(have)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    pages, tokens, heads, one = t.stride()
+    if one != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return pages, tokens, heads, have
+
+
 def _cache(k_cache, v_cache, HK, D, cache_lens, page_table, B, dev):
     """Checks of a key/value cache; returns (pointers of k_cache, v_cache, cache_lens, page_table; the
     strides; (pages, page_size, table_width))."""
     import torch
-    ptrs, strides = [], []
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        have = t.shape
-        if len(have) != 4 or have[2] != HK or have[3] != D:
-            raise ValueError(f"{name} must have shape [pages, page_size, {HK}, {D}], got {tuple(have)}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-        s = t.stride()
-        if s[3] != 1:
-            raise ValueError(f"the last axis of {name} must be contiguous")
-        ptrs.append(t.data_ptr())
-        strides += s[:3]
-    if v_cache.shape != k_cache.shape:
+    kp, kt, kh, shape = _pages(k_cache, "k_cache", HK, D, dev)
+    vp, vt, vh, vshape = _pages(v_cache, "v_cache", HK, D, dev)
+    if vshape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
     if cache_lens is None:
         raise TypeError("cache_lens must be a torch.Tensor")
-    ptrs.append(_array(cache_lens, "cache_lens", torch.int32, (B,), dev))
-    pages, size, width, ld = k_cache.shape[0], k_cache.shape[1], 0, 0
-    if page_table is None:
-        ptrs.append(None)
-    else:
+    lens = _array(cache_lens, "cache_lens", torch.int32, (B,), dev)
+    pages, size, _, _ = shape
+    table, width, ld = None, 0, 0
+    if page_table is not None:
         if not isinstance(page_table, torch.Tensor):
             raise TypeError("page_table must be a torch.Tensor")
         if page_table.dtype is not torch.int32:
@@ -1190,8 +1195,8 @@ def _cache(k_cache, v_cache, HK, D, cache_lens, page_table, B, dev):
             raise ValueError("page_table must have at least one column")
         if one != 1 and width > 1:
             raise ValueError("the rows of page_table must be contiguous")
-        ptrs.append(page_table.data_ptr())
-    return ptrs, (*strides, ld), (pages, size, width)
+        table = page_table.data_ptr()
+    return (k_cache.data_ptr(), v_cache.data_ptr(), lens, table), (kp, kt, kh, vp, vt, vh, ld), (pages, size, width)
 
 
 @functools.lru_cache(maxsize=1024)
