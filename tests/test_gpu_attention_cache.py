@@ -414,3 +414,19 @@ def test_wrong_arguments_are_refused():
         a = dict(k=q, v=q, k_cache=kc, v_cache=kc2, cache_lens=lens, T=1, page_table=table)
         with pytest.raises(kind):
             lap.la_attn_commit(**{**a, **over})
+
+
+def test_a_call_keeps_no_workspace():
+    """The workspace that a call takes for itself is free again when it returns or raises, on any stream."""
+    q = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    kc = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    lens, o, side = torch.full((4,), 9, dtype=torch.int32, device="cuda"), torch.empty_like(q), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for stream in (None, side, side.cuda_stream):
+        lap.la_attn_verify(q, q, q, 0.1, kc, kc, lens, 1, o=o, stream=stream)
+        assert torch.cuda.memory_allocated() == before
+        torch.cuda.synchronize()
+    with pytest.raises(lap.LaError):
+        lap.la_attn_verify(q, q, q, float("nan"), kc, kc, lens, 1, o=o)
+    assert torch.cuda.memory_allocated() == before
