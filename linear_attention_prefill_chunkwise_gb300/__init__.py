@@ -1017,7 +1017,7 @@ def la_qk_norm_rope_fwd(q, k, q_weight, k_weight, eps, positions=None, inv_freq=
     k_weight: fp32 [D] or None (ones); positions: int32 [tokens]; inv_freq: fp32 [R / 2] (both None: no
     rotation).  q_out and k_out may be q and k themselves.  Returns (q_out, k_out)."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     code, dtype, dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk) = _qk(q, k)
     pos, freq, R = _rotation(positions, inv_freq, tokens, dev)
     q_out, pqo, ldqo, hsqo = _out_heads(q_out, q, "q_out", dtype, dev, stream)
@@ -1076,7 +1076,7 @@ def la_qk_norm_rope_bwd(q, k, q_weight, k_weight, eps, dq_out, dk_out, positions
     (dq, dk, dq_weight, dk_weight).  dq and dk may be dq_out and dk_out themselves.  ``workspace``:
     CUDA uint8, at least la_qk_norm_rope_bwd_workspace(...) bytes, allocated here when None."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     code, dtype, dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk) = _qk(q, k)
     pos, freq, R = _rotation(positions, inv_freq, tokens, dev)
     pgq, ldgq, hsgq = _heads(dq_out, "dq_out", dtype, dev, q.shape)
@@ -1131,7 +1131,7 @@ def la_attn_prefill_fwd(q, k, v, scale, cu_seqlens=None, seq_len=None, o=None, l
     [N + 1] or None (then ``seq_len`` tokens per sequence).  Rows of no sequence are not written.
     Returns (o, lse), lse fp32 [H, tokens], both allocated when not given."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk), (pv, ldv, hsv) = _qkv(q, k, v)
     B, T, N, cu = _prompt_sequences(tokens, dev, cu_seqlens, seq_len)
     o, po, ldo, hso = _out_heads(o, q, "o", torch.bfloat16, dev, stream)
@@ -1153,7 +1153,7 @@ def la_attn_prefill_bwd(q, k, v, scale, o, lse, dout, cu_seqlens=None, seq_len=N
     (dq, dk, dv).  Rows of no sequence are not written.  ``workspace``: CUDA uint8, at least
     la_attn_prefill_bwd_workspace(...) bytes, allocated here when None."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     bf16 = torch.bfloat16
     dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk), (pv, ldv, hsv) = _qkv(q, k, v)
     B, T, N, cu = _prompt_sequences(tokens, dev, cu_seqlens, seq_len)
@@ -1239,7 +1239,7 @@ def la_attn_verify(q, k, v, scale, k_cache, v_cache, cache_lens, T, page_table=N
     0 .. t).  ``workspace``: CUDA uint8, at least la_attn_verify_workspace(...) bytes, allocated here
     when None.  Returns ``o``."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     T = int(T)
     dev, (tokens, H, D), (_, HK, _), (pq, ldq, hsq), (pk, ldk, hsk), (pv, ldv, hsv) = _qkv(q, k, v)
     if T < 1 or tokens % T:
@@ -1264,7 +1264,7 @@ def la_attn_commit(k, v, k_cache, v_cache, cache_lens, T=None, cu_seqlens=None, 
     request b commits tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1, as after a prompt.  The cache as
     in la_attn_verify.  Returns (k_cache, v_cache)."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     pk, ldk, hsk = _heads(k, "k", torch.bfloat16)
     dev = k.get_device()
     tokens, HK, D = k.shape
