@@ -3,6 +3,7 @@
 // the host.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -43,8 +44,9 @@ constexpr int rows_bytes(bool backward) {
 }
 int angle_bytes(int tokens, int R) { return tokens * (R / 2) * static_cast<int>(sizeof(float2)); }
 
-// Tokens whose angles a block holds at once, at most.
-constexpr int kAngleTokens = 16;
+// Tokens whose angles a block holds at once, at most; in bytes for the gradients, whose two blocks per SM
+// leave that much beside the rows read ahead and the sums.
+constexpr int kAngleTokens = 16, kAngleBytes = 28 * 1024;
 
 // Tokens of a block of the forward kernel: enough for eight turns of its groups of threads, as long as
 // the grid still holds the three blocks that run at once on each SM.  Measured, BF16, D = 128, us for 1, 2,
@@ -55,6 +57,14 @@ int tokens_per_block(int tokens, int heads, int groups, int sms) {
   while (n < kAngleTokens && n * heads < 8 * groups && tokens / (2 * n) >= 3 * sms) n *= 2;
   return n;
 }
+
+// Tokens that a block of the gradients takes at a time, by the bytes of a token's queries.  Reading ahead begins
+// anew with each such part, which costs most where a token's rows are few; where they are many, the start of
+// a part brings the block's threads together, so that they write neighbouring rows at the same time.
+// Measured, D = 128, us for 8, 16, 32, 56 tokens: 16384 of 64 + 8 heads BF16 149, 158, 164, 165; of 32 + 4
+// 88, 82.4, 82.2, 82; of 16 + 2 61, 54, 50, 45; of 16 + 4 FP32 83.4, 82.4, 84.3, 88.9; 65536 of 8 + 1 BF16
+// 159, 132, 116, 113.
+int part_tokens(int64_t bytes) { return bytes >= 12 * 1024 ? 8 : bytes >= 6 * 1024 ? 16 : INT32_MAX; }
 
 // Calls f(vector length, head size) as integral constants.
 template <typename E, typename F>
@@ -82,7 +92,7 @@ cudaError_t setup_type() {
                                                    rows_bytes<E, kVec, kD>(false) + angle_bytes(kAngleTokens, kD));
         return r != cudaSuccess ? r
                                 : cudaFuncSetAttribute(lar::norm_rope_bwd_kernel<E, kVec, kD>, most,
-                                                       rows_bytes<E, kVec, kD>(true) + angle_bytes(kAngleTokens, kD));
+                                                       rows_bytes<E, kVec, kD>(true) + kAngleBytes);
       });
   return e;
 }
@@ -267,7 +277,8 @@ la_status la_qk_norm_rope_bwd(const void* q, const void* k, const float* q_weigh
     p.heads[1] = HK;
     p.R = R;
     p.interleaved = interleaved != 0;
-    p.per_block = kAngleTokens;
+    const int each = (tokens + 2 * ds->sms - 1) / (2 * ds->sms);  // tokens of a block, about
+    p.per_block = std::max(1, std::min({each, part_tokens(static_cast<int64_t>(H) * D * es), R > 0 ? kAngleBytes / angle_bytes(1, R) : each}));
     int blocks = 0;
     cudaError_t ce = cudaSuccess;
     if (tokens > 0)

@@ -14,8 +14,8 @@
 // 104 us (0.87 of the copy rate); gradients, 32 + 4 heads, 91 us (0.74).
 //
 // The angle of a pair, in turns, is position * frequency / 2 pi modulo 1: the frequency is scaled
-// to a 64-bit fraction of a turn once, and the product wraps around by itself.  Its error is
-// |position| 2^-53 |frequency| radians, 2^-24 of a turn's half after the conversion to FP32.
+// to a 64-bit fraction of a turn, and the product wraps around by itself.  Its error is |position|
+// (1 + |frequency|) 2^-64 turns, 2^-24 of a turn's half after the conversion to FP32.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -80,14 +80,29 @@ __device__ __forceinline__ void places(int c, int R, int interleaved, int& a, in
   }
 }
 
+// A frequency as a fraction of a turn per position, in units of 2^-64 turns, cut: mantissa times 2^64 / 2 pi, 88
+// bits, shifted by the exponent.  (In integers: FP64 instructions for this cost more than the rest of an angle.)
+__device__ __forceinline__ uint64_t turn_units(float inv_freq) {
+  constexpr uint64_t kUnits = 0x28BE60DB9391054Aull;  // 2^64 / 2 pi
+  const uint32_t bits = __float_as_uint(inv_freq), field = bits >> 23 & 255u;
+  const uint64_t m = (bits & 0x7FFFFFu) | (field ? 0x800000u : 0u);
+  const int down = 150 - static_cast<int>(max(field, 1u));
+  const uint64_t lo = m * kUnits, hi = __umul64hi(m, kUnits);
+  uint64_t r;
+  if (down <= 0)
+    r = down > -64 ? lo << -down : 0;
+  else if (down < 64)
+    r = lo >> down | hi << (64 - down);
+  else
+    r = down < 128 ? hi >> (down - 64) : 0;
+  return bits >> 31 ? 0 - r : r;
+}
+
 // cos and sin of the angle of pair i at a position.
 __device__ __forceinline__ float2 angle(int32_t position, float inv_freq) {
-  const double turn = static_cast<double>(inv_freq) * 0.15915494309189535;  // 1 / 2 pi
-  const long long unit = __double2ll_rn((turn - rint(turn)) * 0x1p63);      // half fractions of 2^64
-  const long long phase = static_cast<long long>(static_cast<unsigned long long>(unit) *
-                                                 (2ull * static_cast<unsigned long long>(static_cast<long long>(position))));
+  const int64_t phase = static_cast<int64_t>(turn_units(inv_freq) * static_cast<uint64_t>(static_cast<int64_t>(position)));
   float s, c;
-  sincospif(static_cast<float>(phase) * 0x1p-63f, &s, &c);
+  sincospif(static_cast<float>(phase) * 0x1p-63f, &s, &c);  // half turns
   return make_float2(c, s);
 }
 
@@ -401,8 +416,9 @@ __global__ void __launch_bounds__(kThreads, kVec > 1 ? 2 : 1) norm_rope_bwd_kern
       wa[i] = load_weight<kVec>(p.weight[which], at[i]);
       wb[i] = load_weight<kVec>(p.weight[which], bt[i]);
     }
+    const int64_t start = static_cast<int64_t>(blockIdx.x) * p.tokens / gridDim.x;
     const int64_t stop = static_cast<int64_t>(blockIdx.x + 1) * p.tokens / gridDim.x;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.tokens / gridDim.x; first < stop; first += p.per_block) {
+    for (int64_t first = start; first < stop; first += p.per_block) {
       const int count = static_cast<int>(min(static_cast<int64_t>(p.per_block), stop - first));
       const int rows = count * heads;
       Place now{group / heads, group % heads}, then = now;
@@ -425,9 +441,11 @@ __global__ void __launch_bounds__(kThreads, kVec > 1 ? 2 : 1) norm_rope_bwd_kern
       };
 #pragma unroll
       for (int k = 0; k < Rows::kRows; ++k) fetch(group + k * L::kGroups);
-      __syncthreads();
-      fill_angles(p, cos, sin, first, count);
-      __syncthreads();
+      if (which == 0 || stop - start > p.per_block) {  // (the keys' tokens are the queries')
+        __syncthreads();
+        fill_angles(p, cos, sin, first, count);
+        __syncthreads();
+      }
       for (int r = group; r - group < rows; r += L::kGroups) {
         const bool live = r < rows;
         Vec<kVec> a[L::kChunks], b[L::kChunks], ga[L::kChunks], gb[L::kChunks];
