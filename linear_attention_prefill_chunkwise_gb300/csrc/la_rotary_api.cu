@@ -66,32 +66,34 @@ int tokens_per_block(int tokens, int heads, int groups, int sms) {
 // 159, 132, 116, 113.
 int part_tokens(int64_t bytes) { return bytes >= 12 * 1024 ? 8 : bytes >= 6 * 1024 ? 16 : INT32_MAX; }
 
-// Calls f(vector length, head size) as integral constants.
+// Calls f(vector length, head size, whether neighbours rotate) as integral constants.
 template <typename E, typename F>
-cudaError_t with_layout(bool vec, int D, F f) {
+cudaError_t with_layout(bool vec, int D, bool near, F f) {
   using std::integral_constant;
   constexpr int kVec = 16 / static_cast<int>(sizeof(E));
-  auto at = [&](auto v) {
-    if (D == 64) return f(v, integral_constant<int, 64>{});
-    if (D == 128) return f(v, integral_constant<int, 128>{});
-    return f(v, integral_constant<int, 256>{});
+  auto at = [&](auto v, auto n) {
+    if (D == 64) return f(v, integral_constant<int, 64>{}, n);
+    if (D == 128) return f(v, integral_constant<int, 128>{}, n);
+    return f(v, integral_constant<int, 256>{}, n);
   };
-  return vec ? at(integral_constant<int, kVec>{}) : at(integral_constant<int, 1>{});
+  auto of = [&](auto n) { return vec ? at(integral_constant<int, kVec>{}, n) : at(integral_constant<int, 1>{}, n); };
+  return near ? of(std::true_type{}) : of(std::false_type{});
 }
 
 // One-time setup per device: the rows read ahead exceed the default shared memory.
 template <typename E>
 cudaError_t setup_type() {
   cudaError_t e = cudaSuccess;
-  for (int D = 64; D <= 256; D *= 2)
+  for (int x = 0; x < 6; ++x)
     if (e == cudaSuccess)
-      e = with_layout<E>(true, D, [](auto v, auto d) {
+      e = with_layout<E>(true, 64 << x / 2, x % 2, [](auto v, auto d, auto near) {
         constexpr int kVec = decltype(v)::value, kD = decltype(d)::value;
+        constexpr bool kNear = decltype(near)::value;
         const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        const cudaError_t r = cudaFuncSetAttribute(lar::norm_rope_fwd_kernel<E, kVec, kD>, most,
+        const cudaError_t r = cudaFuncSetAttribute(lar::norm_rope_fwd_kernel<E, kVec, kD, kNear>, most,
                                                    rows_bytes<E, kVec, kD>(false) + angle_bytes(kAngleTokens, kD));
         return r != cudaSuccess ? r
-                                : cudaFuncSetAttribute(lar::norm_rope_bwd_kernel<E, kVec, kD>, most,
+                                : cudaFuncSetAttribute(lar::norm_rope_bwd_kernel<E, kVec, kD, kNear>, most,
                                                        rows_bytes<E, kVec, kD>(true) + kAngleBytes);
       });
   return e;
@@ -188,13 +190,13 @@ la_status la_qk_norm_rope_fwd(const void* q, const void* k, const float* q_weigh
     p.heads[0] = H;
     p.heads[1] = HK;
     p.R = R;
-    p.interleaved = interleaved != 0;
     const int lanes = vec ? D * static_cast<int>(es) / 32 : 32;
     p.per_block = tokens_per_block(tokens, H + HK, lar::kThreads / lanes, ds->sms);
     const int blocks = (tokens + p.per_block - 1) / p.per_block;
-    return launched(with_layout<E>(vec, D, [&](auto v, auto d) {
+    return launched(with_layout<E>(vec, D, interleaved != 0, [&](auto v, auto d, auto near) {
       constexpr int kVec = decltype(v)::value, kD = decltype(d)::value;
-      return la_host::launch_pdl(lar::norm_rope_fwd_kernel<E, kVec, kD>, blocks, lar::kThreads,
+      constexpr bool kNear = decltype(near)::value;
+      return la_host::launch_pdl(lar::norm_rope_fwd_kernel<E, kVec, kD, kNear>, blocks, lar::kThreads,
                                  rows_bytes<E, kVec, kD>(false) + angle_bytes(p.per_block, R),
                                  static_cast<cudaStream_t>(stream), p);
     }));
@@ -276,15 +278,15 @@ la_status la_qk_norm_rope_bwd(const void* q, const void* k, const float* q_weigh
     p.heads[0] = H;
     p.heads[1] = HK;
     p.R = R;
-    p.interleaved = interleaved != 0;
     const int each = (tokens + 2 * ds->sms - 1) / (2 * ds->sms);  // tokens of a block, about
     p.per_block = std::max(1, std::min({each, part_tokens(static_cast<int64_t>(H) * D * es), R > 0 ? kAngleBytes / angle_bytes(1, R) : each}));
     int blocks = 0;
     cudaError_t ce = cudaSuccess;
     if (tokens > 0)
-      ce = with_layout<E>(vec, D, [&](auto v, auto d) {
+      ce = with_layout<E>(vec, D, interleaved != 0, [&](auto v, auto d, auto near) {
         constexpr int kVec = decltype(v)::value, kD = decltype(d)::value;
-        return la_host::launch_resident(lar::norm_rope_bwd_kernel<E, kVec, kD>, ds->sms, bwd_blocks(tokens), lar::kThreads,
+        constexpr bool kNear = decltype(near)::value;
+        return la_host::launch_resident(lar::norm_rope_bwd_kernel<E, kVec, kD, kNear>, ds->sms, bwd_blocks(tokens), lar::kThreads,
                                         rows_bytes<E, kVec, kD>(true) + angle_bytes(p.per_block, R), cs, &blocks, p);
       });
     if (ce == cudaSuccess && sums)

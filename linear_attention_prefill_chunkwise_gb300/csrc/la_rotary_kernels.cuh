@@ -44,7 +44,7 @@ struct FwdParams {
   const int32_t* positions;
   const float* inv_freq;
   float eps;
-  int tokens, heads[2], R, interleaved, per_block;  // tokens of a block
+  int tokens, heads[2], R, per_block;  // tokens of a block
 };
 
 template <typename E>
@@ -56,7 +56,7 @@ struct BwdParams {
   const float* inv_freq;
   float* part;  // [2][blocks][D] sums of each block's rows; null: no weight gradients
   float eps;
-  int tokens, heads[2], R, interleaved, per_block;
+  int tokens, heads[2], R, per_block;
 };
 
 template <typename E, int kVec, int D>
@@ -67,13 +67,22 @@ struct Layout {
   static constexpr int kGroups = kThreads / kLanes;  // heads that a block holds at once
 };
 
-// Where the two vectors of pair group c begin.
-template <int kVec>
-__device__ __forceinline__ void places(int c, int R, int interleaved, int& a, int& b) {
+// Where the two vectors of group c begin, so that each access of a warp covers whole sectors: neighbouring groups
+// have neighbouring vectors also where elements do not rotate or rotate with their neighbours (16384 tokens
+// of 64 + 8 heads of 128, half of each rotated: 105 us with the two vectors of the other half side by side;
+// neighbours rotated: 126 us, gradients 239).
+template <int kVec, int D, bool kNear>
+__device__ __forceinline__ void places(int c, int R, int& a, int& b) {
   const int rotated = R / (2 * kVec);
-  if (c >= rotated || interleaved) {
-    a = 2 * kVec * c;
-    b = a + kVec;
+  if (kNear && kVec > 1) {  // each vector holds whole pairs
+    a = kVec * c;
+    b = a + D / 2;
+  } else if (c >= rotated) {
+    a = R + kVec * (c - rotated);
+    b = a + (D - R) / 2;
+  } else if (kNear) {
+    a = 2 * c;
+    b = a + 1;
   } else {
     a = kVec * c;
     b = a + R / 2;
@@ -244,27 +253,33 @@ __device__ __forceinline__ void store(E* p, const Vec<kVec>& x) {
   lan::store<kVec>(p, f);
 }
 
-// The rotation of kVec pairs by the angles of cos[] and sin[]; kBack turns back.
+// The rotation of a vector of neighbouring pairs by the angles of cos[] and sin[]; kBack turns back.
 template <int kVec, bool kBack>
-__device__ __forceinline__ void turn(Vec<kVec>& a, Vec<kVec>& b, const float* cos, const float* sin, int interleaved) {
-  constexpr uint64_t kBoth = 0x8000000080000000ull;  // sign bits
-  if (kVec > 1 && interleaved) {
-    // pairs are neighbours: (x, y) (c, c) + (y, x) (-s, s)
-#pragma unroll
-    for (int i = 0; i < 2 * Vec<kVec>::kN; ++i) {
-      uint64_t& v = i < Vec<kVec>::kN ? a.v[i % Vec<kVec>::kN] : b.v[i % Vec<kVec>::kN];
-      const float2 f = lap::f2_unpack(v);
-      const float s = kBack ? -sin[i] : sin[i];
-      v = lap::f2_fma(v, both(cos[i]), lap::f2_mul(lap::f2_pack(f.y, f.x), lap::f2_pack(-s, s)));
-    }
-    return;
-  }
-  const Vec<kVec> c = load_floats<kVec>(cos), s = load_floats<kVec>(sin);
+__device__ __forceinline__ void turn_near(Vec<kVec>& v, const float* cos, const float* sin) {
 #pragma unroll
   for (int i = 0; i < Vec<kVec>::kN; ++i) {
-    const uint64_t x = a.v[i], y = b.v[i], minus = s.v[i] ^ kBoth;
-    a.v[i] = lap::f2_fma(x, c.v[i], lap::f2_mul(y, kBack ? s.v[i] : minus));
-    b.v[i] = lap::f2_fma(x, kBack ? minus : s.v[i], lap::f2_mul(y, c.v[i]));
+    // (x, y) (c, c) + (y, x) (-s, s)
+    const float2 f = lap::f2_unpack(v.v[i]);
+    const float s = kBack ? -sin[i] : sin[i];
+    v.v[i] = lap::f2_fma(v.v[i], both(cos[i]), lap::f2_mul(lap::f2_pack(f.y, f.x), lap::f2_pack(-s, s)));
+  }
+}
+// That of a group's elements, which begin at a0 and b0 (places), by the angles of their token.
+template <int kVec, bool kNear, bool kBack>
+__device__ __forceinline__ void turn(Vec<kVec>& a, Vec<kVec>& b, int a0, int b0, const float* cos, const float* sin, int R) {
+  constexpr uint64_t kBoth = 0x8000000080000000ull;  // sign bits
+  if (kNear && kVec > 1) {
+    if (a0 < R) turn_near<kVec, kBack>(a, cos + a0 / 2, sin + a0 / 2);
+    if (b0 < R) turn_near<kVec, kBack>(b, cos + b0 / 2, sin + b0 / 2);
+  } else if (a0 < (kNear ? R : R / 2)) {
+    const int pair = kNear ? a0 / 2 : a0;  // the first
+    const Vec<kVec> c = load_floats<kVec>(cos + pair), s = load_floats<kVec>(sin + pair);
+#pragma unroll
+    for (int i = 0; i < Vec<kVec>::kN; ++i) {
+      const uint64_t x = a.v[i], y = b.v[i], minus = s.v[i] ^ kBoth;
+      a.v[i] = lap::f2_fma(x, c.v[i], lap::f2_mul(y, kBack ? s.v[i] : minus));
+      b.v[i] = lap::f2_fma(x, kBack ? minus : s.v[i], lap::f2_mul(y, c.v[i]));
+    }
   }
 }
 
@@ -312,7 +327,7 @@ struct Walk {
   __device__ __forceinline__ void next(bool wrapped) { p += wrapped ? step + back : step; }
 };
 
-template <typename E, int kVec, int D>
+template <typename E, int kVec, int D, bool kNear>
 __global__ void __launch_bounds__(kThreads, kVec > 1 ? 3 : 1) norm_rope_fwd_kernel(const FwdParams<E> p) {
   using L = Layout<E, kVec, D>;
   extern __shared__ __align__(16) float angles[];
@@ -333,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, kVec > 1 ? 3 : 1) norm_rope_fwd_kern
     int at[L::kChunks], bt[L::kChunks];
     Vec<kVec> wa[L::kChunks], wb[L::kChunks];
 #pragma unroll
-    for (int i = 0; i < L::kChunks; ++i) places<kVec>(lane + 32 * i, p.R, p.interleaved, at[i], bt[i]);
+    for (int i = 0; i < L::kChunks; ++i) places<kVec, D, kNear>(lane + 32 * i, p.R, at[i], bt[i]);
     Rows in(angles);
     auto fetch = [&](int r) {
       if (r < rows)
@@ -378,11 +393,10 @@ __global__ void __launch_bounds__(kThreads, kVec > 1 ? 3 : 1) norm_rope_fwd_kern
       const uint64_t rstd = both(rsqrtf(sum_lanes<L::kLanes>(halves_sum(ss)) * (1.f / D) + p.eps));
 #pragma unroll
       for (int i = 0; i < L::kChunks; ++i) {
-        const int g = lane + 32 * i;
         a[i] = mul(mul(a[i], rstd), wa[i]);
         b[i] = mul(mul(b[i], rstd), wb[i]);
         if (live) {
-          if (g < p.R / (2 * kVec)) turn<kVec, false>(a[i], b[i], c + g * kVec, s + g * kVec, p.interleaved);
+          turn<kVec, kNear, false>(a[i], b[i], at[i], bt[i], c, s, p.R);
           store(y.p + at[i], a[i]);
           store(y.p + bt[i], b[i]);
         }
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, kVec > 1 ? 3 : 1) norm_rope_fwd_kern
 
 // The gradients.  A block walks over its share of the tokens, first all of its queries, then
 // all of its keys, and keeps the sums for the weight gradients of its threads' own elements in registers.
-template <typename E, int kVec, int D>
+template <typename E, int kVec, int D, bool kNear>
 __global__ void __launch_bounds__(kThreads, kVec > 1 ? 2 : 1) norm_rope_bwd_kernel(const BwdParams<E> p) {
   using L = Layout<E, kVec, D>;
   extern __shared__ __align__(16) float angles[];
@@ -412,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, kVec > 1 ? 2 : 1) norm_rope_bwd_kern
     Vec<kVec> wa[L::kChunks], wb[L::kChunks], da[L::kChunks] = {}, db[L::kChunks] = {};
 #pragma unroll
     for (int i = 0; i < L::kChunks; ++i) {
-      places<kVec>(lane + 32 * i, p.R, p.interleaved, at[i], bt[i]);
+      places<kVec, D, kNear>(lane + 32 * i, p.R, at[i], bt[i]);
       wa[i] = load_weight<kVec>(p.weight[which], at[i]);
       wb[i] = load_weight<kVec>(p.weight[which], bt[i]);
     }
@@ -463,8 +477,7 @@ __global__ void __launch_bounds__(kThreads, kVec > 1 ? 2 : 1) norm_rope_bwd_kern
         uint64_t ss = 0, dot = 0;
 #pragma unroll
         for (int i = 0; i < L::kChunks; ++i) {
-          const int g = lane + 32 * i;
-          if (live && g < p.R / (2 * kVec)) turn<kVec, true>(ga[i], gb[i], c + g * kVec, s + g * kVec, p.interleaved);
+            if (live) turn<kVec, kNear, true>(ga[i], gb[i], at[i], bt[i], c, s, p.R);
           add_dot(ss, a[i], a[i]);
           add_dot(ss, b[i], b[i]);
           add_dot(dot, mul(wa[i], ga[i]), a[i]);
