@@ -11,13 +11,13 @@
 // Lengths differ and are known on the device only, so the blocks (one per SM) share out the tiles
 // of all requests evenly.  Tiles are counted head by head, and within a head request by request, so a
 // block has a run of one head's tiles (blocks at work on neighbouring heads of a request then share
-// its pages' rows in DRAM: 353 us against 387 with the tiles of a request counted first, for 128
+// its pages' rows in DRAM: 345 us against 387 with the tiles of a request counted first, for 128
 // requests of one token, 64 heads of 128 on 8, up to 8192 tokens in pages of 64).  Its pieces are whole
 // items (request, head, query tile), which it writes out, and at its ends parts of items, whose
 // unnormalised output, maximum and sum go to the workspace; a second kernel joins the parts of each
 // item in order.
 //
-// That case reads at 0.93 of the copy rate.  A load is a box of one page's rows: pages of 16 (2 KiB a
+// That case reads at 0.95 of the copy rate.  A load is a box of one page's rows: pages of 16 (2 KiB a
 // box) take 240 us where pages of 32 and more take 197 to 201 (16 requests of 16 tokens).
 //
 // Warps 0-3: softmax, a thread per row; two buffers of scores, so that the product for the next tile

@@ -46,12 +46,13 @@ int angle_bytes(int tokens, int R) { return tokens * (R / 2) * static_cast<int>(
 
 // Tokens whose angles a block holds at once, at most; in bytes for the gradients, whose two blocks per SM
 // leave that much beside the rows read ahead and the sums.
-constexpr int kAngleTokens = 16, kAngleBytes = 28 * 1024;
+constexpr int kAngleTokens = 32, kAngleBytes = 28 * 1024;
 
 // Tokens of a block of the forward kernel: enough for eight turns of its groups of threads, as long as
 // the grid still holds the three blocks that run at once on each SM.  Measured, BF16, D = 128, us for 1, 2,
-// 4, 8, 16 tokens a block: 128 tokens of 72 heads 3.4, 4.2, 5.9, 9.8, 17; 1024 of 72 (in L2) 11.5, 9.9, 11.2,
-// 10, 18; 4096 of 18 (in L2) 30, 17, 12.8, 12.6, 15; 16384 of 72 168, 125, 104, 105, 115.
+// 4, 8, 16, 32 tokens a block: 128 tokens of 72 heads 3.5, 4.4, 6, 9.9, 17; 1024 of 72 (in L2) 12, 10.2, 11.3,
+// 9.9, 17; 4096 of 18 (in L2) 31, 18, 12.3, 10.9, 12.6; 16384 of 72 166, 118, 95, 92, 98; 65536 of 9 474, 249,
+// 140, 96, 73, 63.
 int tokens_per_block(int tokens, int heads, int groups, int sms) {
   int n = 1;
   while (n < kAngleTokens && n * heads < 8 * groups && tokens / (2 * n) >= 3 * sms) n *= 2;

@@ -10,8 +10,8 @@
 //
 // What bounds it beside the bytes is the number of instructions and the bytes in flight, so elements go
 // in packed FP32 pairs, a thread's pointers move from head to head without a division, and rows
-// are read ahead into shared memory.  16384 tokens, heads of 128 BF16: forward, 64 + 8 heads,
-// 104 us (0.87 of the copy rate); gradients, 32 + 4 heads, 91 us (0.74).
+// are read ahead into shared memory.  16384 tokens, heads of 128 BF16: forward, 64 + 8 heads, 95 us (0.95 of
+// the copy rate); gradients, 32 + 4 heads, 82 us (0.82).
 //
 // The angle of a pair, in turns, is position * frequency / 2 pi modulo 1: the frequency is scaled
 // to a 64-bit fraction of a turn, and the product wraps around by itself.  Its error is |position|

@@ -93,6 +93,31 @@ def test_no_rotation_is_the_norm_of_each_head():
     near(y.view_as(qo), ref, bound, "fp32", "la_rms_norm_fwd")
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_frequencies_of_any_size(interleaved):
+    """Angles of frequencies from denormal to 2^25, of either sign.  The products are exact in 64 bits; the kernels' turn
+    is off by position (1 + frequency) 2^-64 of a turn and by 2^-24 when it becomes FP32; the norm by 32 2^-24 + 2^-21 of
+    its value, which is less than 2^-18; sine and cosine by 2^-21."""
+    freq = np.array([1e-42, -3e-39, 1e-30, 2.0 ** -66, 1e-12, -1e-7, 1e-3, 0.7, 1.0, -1.0, 3.3, 1e3, -65537.0, 2.0 ** 23 + 1,
+                     2.0 ** 24 + 2, -33554430.0], dtype=np.float32)
+    pos = np.array([0, 1, -1, 2, 17, 4095, -65536, 2 ** 20 - 1], dtype=np.int32)
+    rng = np.random.default_rng(51)
+    q = torch.from_numpy(rng.standard_normal((len(pos), 3, 64)).astype(np.float32)).cuda()
+    out, _ = lap.la_qk_norm_rope_fwd(q, q, None, None, EPS, torch.from_numpy(pos).cuda(), torch.from_numpy(freq).cuda(),
+                                     interleaved=interleaved)
+    x = q.double().cpu().numpy()
+    y = x / np.sqrt((x * x).mean(-1, keepdims=True) + EPS)
+    a = pos.astype(np.float64)[:, None, None] * freq.astype(np.float64)
+    lo, hi = (slice(0, 32, 2), slice(1, 32, 2)) if interleaved else (slice(0, 16), slice(16, 32))
+    ref = y.copy()
+    ref[..., lo], ref[..., hi] = y[..., lo] * np.cos(a) - y[..., hi] * np.sin(a), y[..., lo] * np.sin(a) + y[..., hi] * np.cos(a)
+    off = 2 * np.pi * (np.abs(pos)[:, None, None] * (1 + np.abs(freq.astype(np.float64))) * 2.0 ** -64 + 2.0 ** -24) + 2.0 ** -21
+    tol = np.abs(ref) * 2.0 ** -18 + 1e-30
+    both = (np.abs(y[..., lo]) + np.abs(y[..., hi])) * (off + 2.0 ** -18)
+    tol[..., lo], tol[..., hi] = both, both
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+
+
 @pytest.mark.parametrize("start", [-5, 2 ** 24 - 3, 2 ** 31 - 9])
 def test_far_positions(start):
     rng = np.random.default_rng(2)
