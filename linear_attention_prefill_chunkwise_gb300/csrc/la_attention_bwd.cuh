@@ -27,7 +27,9 @@
 // at the same time).  There, two teams of eight warps with 64 columns a thread, a tile each in turn, were no
 // faster: tensor memory has room for one dP, which each team holds for most of its tile (dk, dv 235 us
 // against 240 for 2 x 4096 tokens of 32 heads on 8; dq 245 against 202); neither was taking scores and dP out of
-// tensor memory before the last stores there are done (319 against 266).
+// tensor memory before the last stores there are done (319 against 266).  Two blocks per SM with 64 rows
+// passing at a time took 428 us for the packed case, but 438 against 430 for the other, and where items are
+// few 110 against 75 (4096 tokens, 8 heads of 64 on 1).
 #pragma once
 
 #include "la_attention_softmax.cuh"
