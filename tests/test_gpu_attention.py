@@ -354,3 +354,38 @@ def test_groups_of_heads_shared_out(H, HK, D):
     assert all((g[cu[-1]:] == 7).all() for g in grads)
     if H > HK:
         assert ws.numel() > 4 * H * tokens * 2
+
+
+def test_calls_at_once_on_several_streams():
+    """Whole layers on five streams at a time give the bits that they give one after the other."""
+    rng = np.random.default_rng(61)
+    jobs = []
+    for D, H, HK, lens in ((64, 8, 1, [300, 0, 1]), (128, 6, 2, [129, 700]), (64, 4, 4, [257]), (128, 10, 1, [5, 64, 500]),
+                           (64, 2, 1, [1500]), (128, 16, 4, [100, 128, 256]), (64, 6, 3, [90, 91])):
+        cu = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).cuda()
+        q, do, k, v = make(rng, sum(lens), (H, H, HK, HK), D)
+        per = -(-max(lens) // 16)
+        kc, vc = make(rng, len(lens) * per * 16, (HK, HK), D)
+        kc, vc = kc.view(-1, 16, HK, D), vc.view(-1, 16, HK, D)
+        table = torch.from_numpy(rng.permutation(len(lens) * per).reshape(len(lens), per).astype(np.int32)).cuda()
+        held, pos = torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.arange(sum(lens), dtype=torch.int32, device="cuda")
+        freq, w, draft = 10000.0 ** (-torch.arange(0, D, 2, device="cuda") / D), torch.ones(D, device="cuda"), make(rng, 3 * len(lens), (H, HK, HK), D)
+
+        def layer(q=q, k=k, v=v, do=do, cu=cu, D=D, w=w, pos=pos, freq=freq, draft=draft, kc=kc, vc=vc, held=held, table=table):
+            qr, kr = lap.la_qk_norm_rope_fwd(q, k, w, w, 1e-6, pos, freq)
+            o, lse = lap.la_attn_prefill_fwd(qr, kr, v, D ** -0.5, cu_seqlens=cu)
+            g = lap.la_attn_prefill_bwd(qr, kr, v, D ** -0.5, o, lse, do, cu_seqlens=cu)
+            back = lap.la_qk_norm_rope_bwd(q, k, w, w, 1e-6, g[0], g[1], pos, freq)
+            return qr, kr, o, lse, *g, *back, lap.la_attn_verify(*draft, D ** -0.5, kc, vc, held, 3, page_table=table)
+
+        jobs.append(layer)
+    ref = [job() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(5)]
+    for turn in range(4):
+        out = []
+        for i, job in enumerate(jobs):
+            with torch.cuda.stream(streams[(i + turn) % 5]):
+                out.append(job())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(ref, out) for a, b in zip(x, y))
