@@ -211,7 +211,7 @@ __device__ __forceinline__ void fwd_softmax(FwdShared<D>& sm, const PrefillParam
       const float z = load_scores<kSeen>(t_s, scores, c, keys);
       // S follows the last product into O in the queue, so O may be rescaled
       if (first)
-        m = z;
+        m = first_maximum(z);
       else if (__any_sync(0xFFFFFFFFu, z > m + kSlack))
         rescale_row<D>(t_o, outgrow(z, m, l));
 #pragma unroll

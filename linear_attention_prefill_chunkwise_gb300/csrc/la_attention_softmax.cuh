@@ -26,6 +26,10 @@ __device__ __forceinline__ bool sees(const Keys& keys, int k) {
   return k < 64 && (keys.bits[(k >> 5) & 1] >> (k & 31) & 1u);
 }
 
+// Where a row's maximum begins: the first tile's largest c S, or, where none of those is within FP32 (c S
+// overflows for |c| > 1), a value below every other.  From -inf the first score in range would meet inf - inf.
+__device__ __forceinline__ float first_maximum(float z) { return fmaxf(z, -3.4e38f); }
+
 // A row's scores of a tile, in registers, and c times the largest (c < 0: smallest) of those that the
 // row sees; about -3.4e38 |c| for none.  What it does not see becomes that as well.
 template <Seen kSeen>

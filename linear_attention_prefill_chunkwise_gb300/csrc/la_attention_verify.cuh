@@ -383,7 +383,7 @@ __device__ __forceinline__ void verify_softmax(VerifyShared<D>& sm, const CacheP
           constexpr Seen kSeen = decltype(seen)::value;
           const float z = load_scores<kSeen>(t_s, s, c, keys);
           if (j == 0) {
-            m = z;
+            m = first_maximum(z);
           } else if (__any_sync(0xFFFFFFFFu, z > m + kSlack)) {
             // the scores were made ahead of the last product into O: it has to be done
             if (!warp_wait(&sm.pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1u, abort)) return false;
