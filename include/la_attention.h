@@ -9,7 +9,7 @@
  *
  * Scores, softmax statistics and outputs are held in FP32; the probabilities (and, in the
  * gradients, dS) are rounded to BF16 as operands of the products with v (dO, q and k).  A row that
- * sees no key gives o = 0 (lse = -inf).
+ * sees no key gives o = 0 (lse = -inf).  scale: finite, any sign, at most 2e38 in size.
  *
  * Layouts: q, o, dout, dq BF16 [tokens, H, D]; k, v, dk, dv BF16 [tokens, HK, D]; innermost
  * contiguous, each with a stride between tokens (ld*) and between heads (hs*) in elements, both

@@ -60,6 +60,7 @@ la_status launched(cudaError_t ce) {
 
 constexpr int kMostDrafts = 1 << 18;  // drafted tokens of a request: their tiles, of all query tiles, stay within int32
 constexpr int64_t kMostTokens = INT32_MAX - 1024;  // row numbers and tile ends stay within int32
+constexpr float kMostScale = 2.0e38f;  // the kernels multiply it by log2 e
 
 HeadsArg rows(const void* p, int64_t ld, int64_t hs, int64_t tokens, int heads, int D, const char* name) {
   return heads_arg(p, ld, hs, tokens, heads, D, 2, 16, name);
@@ -152,8 +153,9 @@ la_status check_prompt(const int32_t* cu_seqlens, int B, int T, int N, int H, in
 }
 
 la_status check_scale(float scale) {
-  // a scale of 0 is a plain mean; anything not finite has no meaning
-  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(LA_ERR_INVALID_ARGUMENT, "scale must be finite");
+  // a scale of 0 is a plain mean; anything not finite has no meaning, nor what is not once log2 e multiplies it
+  if (!(scale >= -kMostScale && scale <= kMostScale))
+    return fail(LA_ERR_INVALID_ARGUMENT, "scale must be finite and at most %g in size (got %g)", kMostScale, scale);
   return LA_OK;
 }
 
