@@ -298,12 +298,12 @@ la_status la_attn_prefill_fwd(const void* q, const void* k, const void* v, float
   la_host::DeviceState* ds = nullptr;
   if ((st = device(&ds)) != LA_OK) return st;
   laa::PrefillParams p{};
-  p.q = in(a[0]), p.k = in(a[1]), p.v = in(a[2]), p.o = out(a[3]);
+  p.v = in(a[2]), p.o = out(a[3]);
   p.lse = lse;
   p.cu_seqlens = cu_seqlens;
   p.dev_error = dev_error;
   p.scale = scale;
-  p.tokens = static_cast<int>(tokens), p.T = T, p.N = N, p.H = H, p.HK = HK, p.D = D;
+  p.tokens = static_cast<int>(tokens), p.T = T, p.N = N, p.H = H, p.HK = HK;
   laa::FwdMaps maps;
   if ((st = encode_heads(&maps.q, a[0], 1, laa::kTile)) != LA_OK || (st = encode_heads(&maps.k, a[1], 1, laa::kTile)) != LA_OK ||
       (st = encode_heads(&maps.v, a[2], 1, laa::kTile)) != LA_OK)
@@ -357,7 +357,7 @@ la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float
   la_host::DeviceState* ds = nullptr;
   if ((st = device(&ds)) != LA_OK) return st;
   laa::PrefillParams p{};
-  p.q = in(a[0]), p.k = in(a[1]), p.v = in(a[2]), p.o_in = in(a[3]), p.dout = in(a[4]);
+  p.o_in = in(a[3]), p.dout = in(a[4]);
   p.dq = out(a[5]), p.dk = out(a[6]), p.dv = out(a[7]);
   p.lse_in = lse;
   const BwdWorkspace w = bwd_workspace(tokens, N, H, HK, D);
@@ -370,7 +370,7 @@ la_status la_attn_prefill_bwd(const void* q, const void* k, const void* v, float
   p.cu_seqlens = cu_seqlens;
   p.dev_error = dev_error;
   p.scale = scale;
-  p.tokens = static_cast<int>(tokens), p.T = T, p.N = N, p.H = H, p.HK = HK, p.D = D;
+  p.tokens = static_cast<int>(tokens), p.T = T, p.N = N, p.H = H, p.HK = HK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   laa::BwdMaps maps;
   if ((st = encode_heads(&maps.q, a[0], 1, laa::kTile)) != LA_OK || (st = encode_heads(&maps.k, a[1], 1, laa::kTile)) != LA_OK ||
@@ -444,17 +444,14 @@ la_status la_attn_verify(const void* q, const void* k, const void* v, float scal
   la_host::DeviceState* ds = nullptr;
   if ((st = device(&ds)) != LA_OK) return st;
   laa::CacheParams p{};
-  p.q = in(a[0]), p.k = in(a[1]), p.v = in(a[2]), p.o = out(a[3]);
-  p.k_cache = static_cast<const bf16*>(k_cache);
-  p.v_cache = static_cast<const bf16*>(v_cache);
-  p.kp = kc.ps, p.kt = kc.ts, p.kh = kc.hs, p.vp = vc.ps, p.vt = vc.ts, p.vh = vc.hs;
+  p.v = in(a[2]), p.o = out(a[3]);
   p.ld_table = ld_table;
   p.cache_lens = cache_lens;
   p.page_table = page_table;
   p.mask = mask;
   p.dev_error = dev_error;
   p.scale = scale;
-  p.B = B, p.T = T, p.H = H, p.HK = HK, p.D = D, p.pages = pages, p.page_size = page_size, p.table_width = table_width;
+  p.B = B, p.T = T, p.HK = HK, p.pages = pages, p.page_size = page_size, p.table_width = table_width;
   p.part = workspace;
   const laa::VerifyShape shape = verify_shape(T, H, HK, mask != nullptr, page_size, page_table != nullptr);
   laa::VerifyMaps maps;
@@ -517,7 +514,7 @@ la_status la_attn_commit(const void* k, const void* v, void* k_cache, void* v_ca
   p.ld_table = ld_table;
   p.cache_lens = cache_lens, p.page_table = page_table, p.cu_seqlens = cu_seqlens, p.accepted_len = accepted_len, p.path = path;
   p.dev_error = dev_error;
-  p.B = B, p.T = T, p.H = HK, p.HK = HK, p.D = D, p.pages = pages, p.page_size = page_size, p.table_width = table_width;
+  p.B = B, p.T = T, p.HK = HK, p.D = D, p.pages = pages, p.page_size = page_size, p.table_width = table_width;
   // blocks of a request: its tokens (packed: their number is on the device, so at most what a batch
   // of one would take, and few enough that the empty ones cost little)
   const int64_t most = (T + laa::kCommitTokens - 1) / laa::kCommitTokens;

@@ -20,7 +20,7 @@ struct Heads {
 constexpr int kErrSeqlens = 1, kErrIndex = 2, kErrTimeout = 4;  // LA_DEV_ERR_*
 
 struct PrefillParams {
-  Heads<const bf16> q, k, v, o_in, dout;
+  Heads<const bf16> v, o_in, dout;  // (q and k come by tensor maps)
   Heads<bf16> o, dq, dk, dv;
   float* lse;           // [H, tokens]
   const float* lse_in;  // gradients
@@ -30,21 +30,20 @@ struct PrefillParams {
   const int32_t* cu_seqlens;
   int* dev_error;
   float scale;
-  int tokens, T, N, H, HK, D, splits;
+  int tokens, T, N, H, HK, splits;
 };
 
 struct CacheParams {
-  Heads<const bf16> q, k, v;
+  Heads<const bf16> k, v;  // la_attn_verify: q, k and the cache come by tensor maps
   Heads<bf16> o;
-  const bf16 *k_cache, *v_cache;
-  bf16 *k_out, *v_out;  // la_attn_commit
+  bf16 *k_out, *v_out;  // la_attn_commit, with the strides that follow
   int64_t kp, kt, kh, vp, vt, vh, ld_table;
   const int32_t *cache_lens, *page_table, *cu_seqlens, *accepted_len, *path;
   const int64_t* mask;
   void* part;  // workspace
   int* dev_error;
   float scale;
-  int B, T, H, HK, D, pages, page_size, table_width;
+  int B, T, HK, D, pages, page_size, table_width;
 };
 
 // Rows [lo, hi) of sequence n; an empty range (and the error bit) where its bounds do not fit.
