@@ -19,7 +19,10 @@
  * dev_error (nullable device int): LA_DEV_ERR_* bits as in la_prefill.h.
  * Outputs may share no element with an input or with each other (ranges between a token's first
  * and last head count whole): LA_ERR_INVALID_ARGUMENT.  Calls enqueue on `stream`, allocate
- * nothing, never synchronise and may be captured in a CUDA graph.  Results are bitwise repeatable.
+ * nothing, never synchronise and may be captured in a CUDA graph.  Results are bitwise repeatable: the
+ * same call gives the same bits.  Which parts of a sum la_attn_verify and the dk and dv of
+ * la_attn_prefill_bwd join depends on the whole batch's lengths, so there a request's bits may differ
+ * beside other requests; la_attn_prefill_fwd and dq give a sequence the same bits in any batch.
  * A workspace is written before it is read: its contents on entry do not matter, and calls that
  * may run at the same time need one each.
  */

@@ -2,9 +2,11 @@
 //
 // With p = 2^(c q.k - lse log2 e), c = scale log2 e, and delta_t = sum_d dO o:
 //     dS = p (dO.v - delta),   dv_j = sum_t p dO_t,   dk_j = scale sum_t dS q_t,   dq_t = scale sum_j dS k_j
+// p and dS are rounded to BF16 as operands of those products, 2^-8 of each term, as much as the gradients'
+// own rounding (0.0024 RMS from 64 bits, where FP32 ones give 0.0017); what is summed and subtracted is FP32.
 // Two kernels, so that every sum stays in tensor memory, in one order, without atomics or partial
-// sums in memory (a single pass would save two of the seven products and pay for it with FP32
-// additions of dq in memory, whose order changes):
+// sums in memory.  (A single pass would save two of the seven products and add dq in memory in FP32, in an
+// order that changes or in turns that blocks wait for; what the latter costs has not been measured.)
 //   dk, dv: a block owns 128 keys and walks over the rows that see them, of every head of the group.
 //     K Q^T and V dO^T give scores and dP transposed, keys along the lanes, so that p and dS, written
 //     back over them as BF16, are operands from tensor memory of p^T dO and dS^T Q.
@@ -19,8 +21,8 @@
 // Where a batch has few key/value heads and tiles for the SMs, a group's heads are shared out among
 // several items, whose FP32 sums a last kernel adds in order.
 //
-// Bound: the tensor cores at D = 128 (2 x 8192 tokens, 32 heads of 128 on 4: 2.48 ms in a row, the seven
-// products at 1.55 PFLOP/s under the power limit; 2.19 ms when cool); at D = 64 the warpgroups' way from
+// Bound: the tensor cores at D = 128 (2 x 8192 tokens, 32 heads of 128 on 4: 2.43 ms in a row, the seven
+// products at 1.58 PFLOP/s under the power limit; 2.19 ms when cool); at D = 64 the warpgroups' way from
 // scores to probabilities to dS (24 packed sequences of up to 2047 tokens, 16 heads: 0.45 ms; 2100 cycles
 // per tile of scores and SM for dk and dv, 1474 for dq, of which the products take 1152 and 768 and the
 // warps' instructions 800: what is left is the latency of barriers and tensor memory, which all warps meet

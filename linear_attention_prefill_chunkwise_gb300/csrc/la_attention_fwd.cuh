@@ -11,11 +11,14 @@
 // through a ring.  The two tiles share keys and values, which halves their traffic from L2.
 //
 // Bound: the tensor cores at D = 128 (2 x 8192 tokens, 64 heads of 128 on 8: 1.40 ms, 1.57 PFLOP/s, where
-// the power limit holds the clock; 1.28 ms when cool); at D = 64, where the products halve, the softmax
-// (1229 cycles per tile of scores and SM against 1524).  Measured against it on that case: two threads per
-// row, which meet to agree on a maximum, 1.57 ms; steps of 64 keys with two buffers of scores per tile,
-// whose products read the queries twice as often, 1.53 ms; half of p made before the new maximum is
-// known, 1.61 ms.
+// the power limit holds the clock; 1.28 ms when cool).  At D = 64, where the products halve, the latency of
+// handing scores and probabilities over: 1229 cycles per tile of scores and SM (1524 at D = 128) for 768 of
+// products and 512 of the special function unit.  The tensor pipe and that unit are busy 37 % of the time and
+// issue slots 42 %, as a tile's next S waits until its p v has read p from the same columns (8192 tokens,
+// 16 heads of 64: 138 us, 0.51 of the tensor cores' rate).
+// Measured against it on the first case: two threads per row, which meet to agree on a maximum, 1.57 ms; steps
+// of 64 keys with two buffers of scores per tile, whose products read the queries twice as often, 1.53 ms;
+// half of p made before the new maximum is known, 1.61 ms.
 #pragma once
 
 #include "la_attention_softmax.cuh"

@@ -2,9 +2,13 @@
 // running maximum and sum, as the forward kernels share it.
 //
 //     p = 2^(c S - m) with c = scale log2 e,  O += p v,  l += sum p;   o = O / l
-// The maximum m moves only when a row outgrows it by 2^kSlack, so that O is rarely rescaled.  p is
+// The running maximum and sum of a softmax in one pass (Milakov and Gimelshein, "Online normalizer
+// calculation for softmax", 2018), with a maximum m that moves only when a row outgrows it by
+// 2^kSlack, so that O is rarely rescaled: any m gives the same quotient as long as p stays in range.  p is
 // rounded to BF16 as an operand of the product with v: 2^-8 of each term, no more than the
-// output's own rounding; l sums the values before that rounding.
+// output's own rounding; l sums the values before that rounding.  (Outputs are 0.0020 RMS from 64 bits, where
+// FP32 probabilities give 0.0015 to 0.0017; a second BF16 operand for the rest of p would cost half as many
+// products again.)
 #pragma once
 
 #include "la_attention_tiles.cuh"

@@ -1,7 +1,7 @@
 // la_attention_verify.cuh -- drafted tokens (or one token) of many requests over a key/value cache
 // (include/la_attention.h) on the tensor cores.
 //
-// The work is bound by reading the cache once.  The rows that share a key/value head (a request's
+// Up to 128 rows per key/value head the work is bound by reading the cache once.  The rows that share a key/value head (a request's
 // tokens times the heads of a group, 128 at most at a time) are one tile of queries; its keys come
 // 128 at a time from the request's pages, and behind them the drafted tokens' own.  An MMA of 128
 // rows takes a fraction of the time that HBM takes for its keys and values, so that rows without a
@@ -17,9 +17,13 @@
 // unnormalised output, maximum and sum go to the workspace; a second kernel joins the parts of each
 // item in order.
 //
-// That case reads at 0.95 of the copy rate.  A load is a box of one page's rows: pages of 16 (2 KiB a
+// That case reads at 0.94 to 0.95 of the copy rate.  A load is a box of one page's rows: pages of 16 (2 KiB a
 // box) take 240 us where pages of 32 and more take 197 to 201 (16 requests of 16 tokens; four more warps
 // that copy 16 bytes a thread instead, three slots ahead, 268).
+//
+// More rows than that (drafted tokens times the heads of a group) take several query tiles, each of which reads
+// the cache again: 64 requests of 64 heads of 128 on 8, 1024 to 8192 cached, take 213 us for trees of 16 (one tile,
+// 0.85 of the copy rate), 402 and 453 of 17 and 32 (two), 675 of 64 (four; the products alone 263).
 //
 // Warps 0-3: softmax, a thread per row; two buffers of scores, so that the product for the next tile
 // runs during it.  Warp 4: products.  Warp 5: finds the pieces, looks up pages and loads.
