@@ -1,9 +1,9 @@
 // la_attention_verify.cuh -- drafted tokens (or one token) of many requests over a key/value cache
 // (include/la_attention.h) on the tensor cores.
 //
-// Up to 128 rows per key/value head the work is bound by reading the cache once.  The rows that share a key/value head (a request's
-// tokens times the heads of a group, 128 at most at a time) are one tile of queries; its keys come
-// 128 at a time from the request's pages, and behind them the drafted tokens' own.  An MMA of 128
+// Up to 128 rows per key/value head the work is bound by reading the cache once.  The rows that share a
+// key/value head (a request's tokens times the heads of a group, 128 at most at a time) are one tile of
+// queries; its keys come 128 at a time from the request's pages, and behind them the drafted tokens' own.  An MMA of 128
 // rows takes a fraction of the time that HBM takes for its keys and values, so that rows without a
 // token cost nothing that counts.  (A tile of D = 128 is 64 KiB: 1.5 us of an SM's share of HBM
 // against 0.55 us of products and about as long for the softmax, which overlaps them.)
@@ -21,9 +21,9 @@
 // box) take 240 us where pages of 32 and more take 197 to 201 (16 requests of 16 tokens; four more warps
 // that copy 16 bytes a thread instead, three slots ahead, 268).
 //
-// More rows than that (drafted tokens times the heads of a group) take several query tiles, each of which reads
-// the cache again: 64 requests of 64 heads of 128 on 8, 1024 to 8192 cached, take 213 us for trees of 16 (one tile,
-// 0.85 of the copy rate), 402 and 453 of 17 and 32 (two), 675 of 64 (four; the products alone 263).
+// More rows than 128 take several query tiles, each of which reads the cache again: 64 requests of 64 heads
+// of 128 on 8, 1024 to 8192 cached, take 213 us for trees of 16 (one tile, 0.85 of the copy rate), 402 and
+// 453 of 17 and 32 (two), 675 of 64 (four; the products alone 263).
 //
 // Warps 0-3: softmax, a thread per row; two buffers of scores, so that the product for the next tile
 // runs during it.  Warp 4: products.  Warp 5: finds the pieces, looks up pages and loads.

@@ -107,10 +107,11 @@ la_status device(la_host::DeviceState** ds) {
   });
 }
 
-// Whether the heads can be read and written 16 bytes at a time.  (With R a multiple of 16, FP32 8, so that no vector
-// is cut by the end of the rotated part or of its half.)  Otherwise elements go one at a time, 2 or 4 bytes an access and one
-// row ahead in registers: 16384 tokens of 32 + 4 heads of 128, BF16, all rotated, forward 54 us against 140 with rows 8 bytes
-// off, gradients 84 against 307; FP32 91 against 200 and 156 against 352.  (R = 90: the same, neighbours forward 182.)
+// Whether the heads can be read and written 16 bytes at a time.  (With R a multiple of 16, FP32 8, so that no
+// vector is cut by the end of the rotated part or of its half.)  Otherwise elements go one at a time, 2 or 4
+// bytes an access and one row ahead in registers: 16384 tokens of 32 + 4 heads of 128, BF16, all rotated,
+// forward 54 us against 140 with rows 8 bytes off, gradients 84 against 307; FP32 91 against 200 and 156
+// against 352.  (R = 90: the same, neighbours forward 182.)
 bool wide(const HeadsArg& h) {
   return !h.p || (reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.ld * h.element % 16 == 0 && h.hs * h.element % 16 == 0);
 }
